@@ -258,6 +258,168 @@ mhla_status mhla_backward(const void* q, const void* k, const void* v, const flo
                           const mhla_params* p, void* dq, void* dk, void* dv, float* dmc, void* workspace,
                           size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of a sequence model's layer around the attention: linear
+ * attention with a decay for each head (prompts, single tokens, backward),
+ * rotary positions and layer norm.  The conventions at the top of this file
+ * hold (device pointers, host-side checks before anything is enqueued,
+ * asynchronous on `stream`), except that tensors carry element strides
+ * instead of being contiguous and pointers need the alignment of their
+ * elements only; 16-byte aligned rows take the vector path.
+ * ------------------------------------------------------------------------ */
+
+/* Element strides of a tensor of rows [batch, head, token]; the row itself
+ * is contiguous.  Strides are >= 0; inputs may broadcast (stride 0), the
+ * rows of an output must not overlap. */
+typedef struct mhla_strides {
+  int64_t batch, head, token;
+} mhla_strides;
+
+/* Rotary positions: pair i of a row is rotated by position * f_i radians,
+ *   (a, b) -> m (a cos - b sin, a sin + b cos).
+ * HALF pairs entry i with entry i + rot_dim / 2; INTERLEAVED pairs 2i with
+ * 2i + 1.  Entries from rot_dim on are copied. */
+typedef enum mhla_rotary_style { MHLA_ROTARY_HALF = 0, MHLA_ROTARY_INTERLEAVED = 1 } mhla_rotary_style;
+
+/* f_i = base^(-2i / rot_dim) (NONE); LINEAR: f_i / factor (positions
+ * interpolated); BASE: base * factor^(rot_dim / (rot_dim - 2)) in place of
+ * base; PARTS: with r = original_length f_i / 2 pi turns over the original
+ * context and c = clamp((r - 1) / 31, 0, 1), f_i (c + (1 - c) / factor), and
+ * the amplitude m = 0.1 ln(factor) + 1 (1 otherwise) -- "YaRN: Efficient
+ * Context Window Extension of Large Language Models", section 3. */
+typedef enum mhla_rotary_scaling {
+  MHLA_ROTARY_SCALE_NONE = 0,
+  MHLA_ROTARY_SCALE_LINEAR = 1,
+  MHLA_ROTARY_SCALE_BASE = 2,
+  MHLA_ROTARY_SCALE_PARTS = 3
+} mhla_rotary_scaling;
+
+#define MHLA_ROTARY_MAX_PAIRS 128
+
+/* Host-side table of a rotation: turns[i] = f_i / 2 pi as a fraction of a
+ * turn times 2^64, so that position * turns[i] modulo 2^64 is the exact phase
+ * of that frequency at any position. */
+typedef struct mhla_rotary_table {
+  int pairs;        /* rot_dim / 2, 1 .. MHLA_ROTARY_MAX_PAIRS */
+  float amplitude;  /* m */
+  uint64_t turns[MHLA_ROTARY_MAX_PAIRS];
+} mhla_rotary_table;
+
+/* Fills *table.  rot_dim even, 2 .. 256; base > 0; factor > 0 (>= 1 for
+ * PARTS) and original_length > 0 (PARTS only), all finite. */
+mhla_status mhla_rotary_table_init(int rot_dim, double base, int scaling, double factor, double original_length,
+                                   mhla_rotary_table* table);
+
+typedef enum mhla_position_dtype { MHLA_POSITIONS_I32 = 0, MHLA_POSITIONS_I64 = 1 } mhla_position_dtype;
+
+typedef struct mhla_rotary_params {
+  int batch, tokens;         /* >= 0                                                     */
+  int heads, kv_heads;       /* >= 0: heads of q and of k                                */
+  int head_dim;              /* >= rot_dim of the table, <= 1024; even for INTERLEAVED   */
+  int dtype;                 /* mhla_dtype of q, k and the results                       */
+  int style;                 /* mhla_rotary_style                                        */
+  int transpose;             /* 0: rotate; 1: the transposed map, which takes gradients
+                              * of the results to gradients of q and k                   */
+  int position_dtype;        /* mhla_position_dtype of `positions`                       */
+  int64_t position_offset;   /* position of token t where positions is NULL: offset + t  */
+  int64_t position_batch_stride, position_token_stride; /* of `positions`, in elements   */
+  mhla_strides q, k, q_out, k_out;
+} mhla_rotary_params;
+
+/* Rotates q [batch, heads, tokens, head_dim] and, unless it is NULL, k
+ * [batch, kv_heads, tokens, head_dim] in one launch.  positions: device int32
+ * or int64 [batch, tokens] (any sign), or NULL.  Arithmetic in float32, the
+ * angle exact as above.  q_out may be q and k_out may be k (same strides);
+ * any other overlap is refused.  *table is read before the call returns. */
+mhla_status mhla_rotary(const void* q, const void* k, const void* positions, const mhla_rotary_table* table,
+                        const mhla_rotary_params* p, void* q_out, void* k_out, void* stream);
+
+/* Layer norm over the last axis of [rows, cols]:
+ *   y = (x - mean) rstd * weight + bias,  rstd = 1 / sqrt(var + eps),
+ * var the mean square deviation.  Statistics and arithmetic in float32. */
+typedef struct mhla_layernorm_params {
+  int64_t rows;          /* >= 0                                           */
+  int cols;              /* >= 1, <= 2^20                                  */
+  int dtype;             /* mhla_dtype of x, y, dy, dx                     */
+  int weight_dtype;      /* mhla_dtype of weight and bias                  */
+  float eps;             /* >= 0, finite                                   */
+  int64_t x_stride;      /* elements from row to row of x, >= cols         */
+  int64_t y_stride;      /* of y; of dx in the backward call, >= cols      */
+  int64_t dy_stride;     /* of dy, >= cols (backward only)                 */
+} mhla_layernorm_params;
+
+/* weight and bias: device [cols] or NULL (1 and 0).  mean and rstd: device
+ * float32 [rows], written unless NULL; the backward call reads them.  y may
+ * be x (same stride). */
+mhla_status mhla_layernorm_forward(const void* x, const void* weight, const void* bias,
+                                   const mhla_layernorm_params* p, void* y, float* mean, float* rstd, void* stream);
+
+/* Gradients: dx = rstd (w dy - mean(w dy) - xh mean(w dy xh)), dweight =
+ * sum dy xh, dbias = sum dy with xh = (x - mean) rstd.  dweight and dbias are
+ * float32 [cols], overwritten (zeros for no rows); either may be NULL and is
+ * then not computed.  dx may be dy or x (same stride).  Sums over the rows
+ * run in a fixed order: results do not change from call to call.  workspace:
+ * mhla_layernorm_backward_workspace_bytes bytes, 256-byte aligned, or NULL
+ * with 0 bytes (stream-ordered allocation). */
+mhla_status mhla_layernorm_backward_workspace_bytes(const mhla_layernorm_params* p, size_t* bytes);
+mhla_status mhla_layernorm_backward(const void* dy, const void* x, const void* weight, const float* mean,
+                                    const float* rstd, const mhla_layernorm_params* p, void* dx, float* dweight,
+                                    float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Linear attention with a decay for each head: with lambda = exp(log_decay[h])
+ *   S_t = lambda S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ * for t = 0 .. length - 1, S_{-1} = state_in (zeros where it is NULL) and
+ * state_out = S_{length-1}.  States are float32 [batch, heads, key_dim,
+ * value_dim], contiguous.  No feature map and no denominator: the caller
+ * applies the map it wants to q and k, and a norm over each head's output
+ * stands in for the normaliser.  log_decay is a constant of the head (it has
+ * no gradient): usually <= 0, -inf keeps only the token itself, > 0 grows.
+ * Causality holds for finite values; a NaN or infinity in k or v may reach
+ * the outputs of earlier tokens of its 128-token chunk. */
+typedef enum mhla_decay_variant {
+  MHLA_DECAY_AUTO = 0,   /* tensor cores for bf16, CUDA cores for float32        */
+  MHLA_DECAY_SIMT = 1,   /* float32 arithmetic on the CUDA cores, both dtypes    */
+  MHLA_DECAY_TENSOR = 2  /* tensor cores (bf16 only, else MHLA_ERR_UNSUPPORTED)  */
+} mhla_decay_variant;
+
+typedef struct mhla_decay_params {
+  int batch, heads, tokens;  /* >= 0                                                     */
+  int key_dim, value_dim;    /* each 16, 32, 64 or 128                                   */
+  int dtype;                 /* mhla_dtype of q, k, v, out and their gradients           */
+  int variant;               /* mhla_decay_variant                                       */
+  float scale;               /* finite                                                   */
+  mhla_strides q, k, v, out; /* out: forward only                                        */
+  mhla_strides dout, dq, dk, dv; /* backward only                                        */
+} mhla_decay_params;
+
+/* Prompts.  lengths: device int32 [batch] or NULL (all tokens); a sequence's
+ * length is clamped to 0 .. tokens, rows of out past it are written as zeros
+ * and their q, k, v are not used.  state_in may be NULL; state_out may be
+ * NULL (not wanted) or state_in (updated in place); tokens == 0 copies the
+ * state.  log_decay: device float32 [heads].  workspace as for
+ * mhla_forward, of mhla_decay_workspace_bytes bytes (which may be 0). */
+mhla_status mhla_decay_workspace_bytes(const mhla_decay_params* p, size_t* bytes);
+mhla_status mhla_decay_forward(const void* q, const void* k, const void* v, const float* log_decay,
+                               const int32_t* lengths, const float* state_in, const mhla_decay_params* p, void* out,
+                               float* state_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of L = sum(dout * out) + sum(dstate_out * state_out) with respect
+ * to q, k, v and state_in; nothing is kept from the forward call.
+ * dstate_out NULL: zeros; dstate_in NULL: not wanted, or dstate_out (in
+ * place).  Rows of dq, dk, dv past a sequence's length are written as zeros. */
+mhla_status mhla_decay_backward_workspace_bytes(const mhla_decay_params* p, size_t* bytes);
+mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, const float* log_decay,
+                                const int32_t* lengths, const float* state_in, const void* dout,
+                                const float* dstate_out, const mhla_decay_params* p, void* dq, void* dk, void* dv,
+                                float* dstate_in, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of every sequence (tokens == 1): S = lambda state_in + k v^T into
+ * state_out, which may be state_in, and o = scale S^T q.  One launch, no
+ * workspace. */
+mhla_status mhla_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
+                            const float* state_in, const mhla_decay_params* p, void* out, float* state_out,
+                            void* stream);
+
 /* Reads and clears the device error word of the current device.  Blocks the
  * host until the device is idle.  *code receives MHLA_OK or the first status
  * a kernel recorded (MHLA_ERR_DEVICE_TIMEOUT); *detail

@@ -12,6 +12,7 @@
 #include "mhla.h"
 #include "plan.h"
 #include "backward.h"
+#include "ops.h"
 #include "tc_bwd.h"
 #include "tc_causal.h"
 #include "tc_host.h"
@@ -24,9 +25,13 @@ std::atomic<unsigned int> g_debug_flow_stall{0};
 unsigned long long debug_flow_wait_ns() { return g_debug_flow_wait_ns.load(); }
 unsigned int debug_flow_stall() { return g_debug_flow_stall.load(); }
 
-namespace {
-
 thread_local std::string g_last_error;
+mhla_status record_cuda_error(cudaError_t e) {
+  g_last_error = cudaGetErrorString(e);
+  return MHLA_ERR_CUDA;
+}
+
+namespace {
 
 std::mutex g_events_mu;
 cudaEvent_t g_events[MHLA_NUM_PHASE_EVENTS];
@@ -52,10 +57,7 @@ constexpr size_t kFusedMaxRing = 16;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
-mhla_status cuda_fail(cudaError_t e) {
-  g_last_error = cudaGetErrorString(e);
-  return MHLA_ERR_CUDA;
-}
+mhla_status cuda_fail(cudaError_t e) { return record_cuda_error(e); }
 
 size_t elem_bytes(int dtype) { return dtype == MHLA_DTYPE_BF16 ? 2 : 4; }
 
