@@ -1,0 +1,274 @@
+// C entries of linear attention with a decay for each head (declared in
+// include/mhla.h): checks, the segment plan and the passes of decay.h.
+#include <cmath>
+
+#include "decay.h"
+#include "ops.h"
+
+namespace mhla {
+namespace {
+
+bool dim_ok(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
+
+mhla_status check_params(const mhla_decay_params* p) {
+  if (!p || p->batch < 0 || p->heads < 0 || p->tokens < 0) return MHLA_ERR_INVALID_ARG;
+  if (!dim_ok(p->key_dim) || !dim_ok(p->value_dim) || !ops_dtype_ok(p->dtype)) return MHLA_ERR_INVALID_ARG;
+  if (p->variant < MHLA_DECAY_AUTO || p->variant > MHLA_DECAY_TENSOR || !std::isfinite(p->scale))
+    return MHLA_ERR_INVALID_ARG;
+  if (p->variant == MHLA_DECAY_TENSOR) return MHLA_ERR_UNSUPPORTED;
+  if ((int64_t)p->batch * p->heads > (1 << 24) || p->tokens > (1 << 30)) return MHLA_ERR_UNSUPPORTED;
+  return MHLA_OK;
+}
+
+// Segments of a pass: enough CTAs (units x slices of 64 columns x segments)
+// for two on every SM, segments of at least 256 tokens (the state that starts
+// a segment costs about as much as that many tokens), at most 64 of them (a
+// segment sums all earlier states).
+constexpr int kSegQuantum = 128, kSegLeast = 256, kSegMost = 64;
+
+void plan_segments(int64_t units, int dz, int tokens, int* nseg, int* seg_len) {
+  const int64_t ctas = units * (dz > 64 ? dz / 64 : 1);
+  int64_t n = ctas > 0 ? 2 * kOpsSms / ctas : 1;
+  if (n > tokens / kSegLeast) n = tokens / kSegLeast;
+  if (n > kSegMost) n = kSegMost;
+  if (n < 1) n = 1;
+  int64_t len = (tokens + n - 1) / n;
+  len = (len + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
+  if (len < kSegQuantum) len = kSegQuantum;
+  *seg_len = (int)len;
+  *nseg = (int)((tokens + len - 1) / len);
+  if (*nseg < 1) *nseg = 1;
+}
+
+size_t pass_workspace(const mhla_decay_params* p, int dz) {
+  int nseg, seg_len;
+  const int64_t units = (int64_t)p->batch * p->heads;
+  plan_segments(units, dz, p->tokens, &nseg, &seg_len);
+  return nseg > 1 ? sizeof(float) * (size_t)units * nseg * p->key_dim * p->value_dim : 0;
+}
+
+RowTensor tensor(const mhla_decay_params* p, const void* ptr, const mhla_strides& s, int dim) {
+  return row_tensor(ptr, p->batch, p->heads, p->tokens, s, dim, ops_elem(p->dtype));
+}
+
+RowTensor state_tensor(const mhla_decay_params* p, const float* ptr) {
+  return flat_tensor(ptr, ptr ? (int64_t)p->batch * p->heads * p->key_dim * p->value_dim : 0, 4);
+}
+
+bool state_ok(const RowTensor& t) { return row_tensor_ok(t, false) && (uintptr_t)t.ptr % 16 == 0; }
+
+DecayPass pass_of(const mhla_decay_params* p, int dx, int dz) {
+  DecayPass a = {};
+  a.B = p->batch;
+  a.H = p->heads;
+  a.N = p->tokens;
+  a.DX = dx;
+  a.DZ = dz;
+  plan_segments((int64_t)p->batch * p->heads, dz, p->tokens, &a.nseg, &a.seg_len);
+  return a;
+}
+
+void set_rows(DecayPass& a, const RowTensor& x, const mhla_strides& sx, const RowTensor& y, const mhla_strides& sy,
+              const RowTensor& z, const mhla_strides& sz, const RowTensor& o, const mhla_strides& so) {
+  a.x = x.ptr;
+  a.y = y.ptr;
+  a.z = z.ptr;
+  a.o = const_cast<void*>(o.ptr);
+  a.sx = sx;
+  a.sy = sy;
+  a.sz = sz;
+  a.so = so;
+  a.vec = row_alignment(x, 16) == 16 && row_alignment(y, 16) == 16 && row_alignment(z, 16) == 16 &&
+          row_alignment(o, 16) == 16;
+}
+
+mhla_status copy_state(const mhla_decay_params* p, const float* from, float* to, cudaStream_t s) {
+  if (!to || to == from) return MHLA_OK;
+  const size_t n = sizeof(float) * (size_t)p->batch * p->heads * p->key_dim * p->value_dim;
+  const cudaError_t e =
+      from ? cudaMemcpyAsync(to, from, n, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(to, 0, n, s);
+  return e == cudaSuccess ? MHLA_OK : record_cuda_error(e);
+}
+
+cudaError_t launch_pass(const DecayPass& a, int dtype, int variant, cudaStream_t s) {
+  (void)variant;
+  return launch_decay_simt(a, dtype, s);
+}
+
+// Whether `out` shares memory with none of `in`.
+bool apart_from_all(const RowTensor& out, const RowTensor* in, int n) {
+  for (int i = 0; i < n; ++i)
+    if (!row_tensors_apart(out, in[i])) return false;
+  return true;
+}
+
+}  // namespace
+}  // namespace mhla
+
+extern "C" {
+
+mhla_status mhla_decay_workspace_bytes(const mhla_decay_params* p, size_t* bytes) {
+  using namespace mhla;
+  if (!bytes) return MHLA_ERR_INVALID_ARG;
+  const mhla_status st = check_params(p);
+  if (st != MHLA_OK) return st;
+  *bytes = pass_workspace(p, p->value_dim);
+  return MHLA_OK;
+}
+
+mhla_status mhla_decay_forward(const void* q, const void* k, const void* v, const float* log_decay,
+                               const int32_t* lengths, const float* state_in, const mhla_decay_params* p, void* out,
+                               float* state_out, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace mhla;
+  mhla_status st = check_params(p);
+  if (st != MHLA_OK) return st;
+  if ((int64_t)p->batch * p->heads == 0) return MHLA_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const RowTensor in[6] = {tensor(p, q, p->q, p->key_dim),         tensor(p, k, p->k, p->key_dim),
+                           tensor(p, v, p->v, p->value_dim),       flat_tensor(log_decay, p->heads, 4),
+                           flat_tensor(lengths, lengths ? p->batch : 0, 4), state_tensor(p, state_in)};
+  const RowTensor to = tensor(p, out, p->out, p->value_dim), ts = state_tensor(p, state_out);
+  for (const RowTensor& t : in)
+    if (!row_tensor_ok(t, false)) return MHLA_ERR_INVALID_ARG;
+  if (!row_tensor_ok(to, true) || !state_ok(in[5]) || !state_ok(ts)) return MHLA_ERR_INVALID_ARG;
+  if (!apart_from_all(to, in, 6) || !row_tensors_apart(to, ts) || !apart_from_all(ts, in, 5))
+    return MHLA_ERR_INVALID_ARG;
+  if (state_out != state_in && !row_tensors_apart(ts, in[5])) return MHLA_ERR_INVALID_ARG;
+  if (p->tokens == 0) return copy_state(p, state_in, state_out, s);
+  const size_t need = pass_workspace(p, p->value_dim);
+  const RowTensor tw = flat_tensor(workspace, workspace ? (int64_t)need : 0, 1);
+  if (!apart_from_all(tw, in, 6) || !row_tensors_apart(tw, to) || !row_tensors_apart(tw, ts))
+    return MHLA_ERR_INVALID_ARG;
+  Scratch scratch;
+  if ((st = scratch.take(workspace, workspace_bytes, need, s)) != MHLA_OK) return st;
+  DecayPass a = pass_of(p, p->key_dim, p->value_dim);
+  set_rows(a, in[0], p->q, in[1], p->k, in[2], p->v, to, p->out);
+  a.g = log_decay;
+  a.lengths = lengths;
+  a.s_in = state_in;
+  a.s_out = state_out;
+  a.s_ldx = p->value_dim;
+  a.s_ldz = 1;
+  a.seg = reinterpret_cast<float*>(scratch.ptr());
+  a.e = 1;
+  a.score = a.read = p->scale;
+  a.update = 1.f;
+  const cudaError_t e = launch_pass(a, p->dtype, p->variant, s);
+  return scratch.give_back(e == cudaSuccess ? MHLA_OK : record_cuda_error(e));
+}
+
+mhla_status mhla_decay_backward_workspace_bytes(const mhla_decay_params* p, size_t* bytes) {
+  using namespace mhla;
+  if (!bytes) return MHLA_ERR_INVALID_ARG;
+  const mhla_status st = check_params(p);
+  if (st != MHLA_OK) return st;
+  const size_t a = pass_workspace(p, p->key_dim), b = pass_workspace(p, p->value_dim);
+  *bytes = a > b ? a : b;
+  return MHLA_OK;
+}
+
+mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, const float* log_decay,
+                                const int32_t* lengths, const float* state_in, const void* dout,
+                                const float* dstate_out, const mhla_decay_params* p, void* dq, void* dk, void* dv,
+                                float* dstate_in, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace mhla;
+  mhla_status st = check_params(p);
+  if (st != MHLA_OK) return st;
+  if ((int64_t)p->batch * p->heads == 0) return MHLA_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const RowTensor in[8] = {tensor(p, q, p->q, p->key_dim),     tensor(p, k, p->k, p->key_dim),
+                           tensor(p, v, p->v, p->value_dim),   tensor(p, dout, p->dout, p->value_dim),
+                           flat_tensor(log_decay, p->heads, 4), flat_tensor(lengths, lengths ? p->batch : 0, 4),
+                           state_tensor(p, state_in),          state_tensor(p, dstate_out)};
+  const RowTensor out[3] = {tensor(p, dq, p->dq, p->key_dim), tensor(p, dk, p->dk, p->key_dim),
+                            tensor(p, dv, p->dv, p->value_dim)};
+  const RowTensor ts = state_tensor(p, dstate_in);
+  for (const RowTensor& t : in)
+    if (!row_tensor_ok(t, false)) return MHLA_ERR_INVALID_ARG;
+  if (!state_ok(in[6]) || !state_ok(in[7]) || !state_ok(ts)) return MHLA_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (!row_tensor_ok(out[i], true)) return MHLA_ERR_INVALID_ARG;
+    if (!apart_from_all(out[i], in, 8) || !row_tensors_apart(out[i], ts)) return MHLA_ERR_INVALID_ARG;
+    if (!apart_from_all(out[i], out, i)) return MHLA_ERR_INVALID_ARG;
+  }
+  if (!apart_from_all(ts, in, 7)) return MHLA_ERR_INVALID_ARG;
+  if (dstate_in != dstate_out && !row_tensors_apart(ts, in[7])) return MHLA_ERR_INVALID_ARG;
+  if (p->tokens == 0) return copy_state(p, dstate_out, dstate_in, s);
+  size_t need = 0;
+  if ((st = mhla_decay_backward_workspace_bytes(p, &need)) != MHLA_OK) return st;
+  const RowTensor tw = flat_tensor(workspace, workspace ? (int64_t)need : 0, 1);
+  if (!apart_from_all(tw, in, 8) || !apart_from_all(tw, out, 3) || !row_tensors_apart(tw, ts))
+    return MHLA_ERR_INVALID_ARG;
+  Scratch scratch;
+  if ((st = scratch.take(workspace, workspace_bytes, need, s)) != MHLA_OK) return st;
+  float* seg = reinterpret_cast<float*>(scratch.ptr());
+  const int dkey = p->key_dim, dval = p->value_dim;
+
+  DecayPass a = pass_of(p, dval, dkey);  // dq
+  set_rows(a, in[3], p->dout, in[2], p->v, in[1], p->k, out[0], p->dq);
+  a.g = log_decay;
+  a.lengths = lengths;
+  a.s_in = state_in;
+  a.s_ldx = 1;
+  a.s_ldz = dval;
+  a.seg = seg;
+  a.e = 1;
+  a.score = a.read = p->scale;
+  a.update = 1.f;
+  cudaError_t e = launch_pass(a, p->dtype, p->variant, s);
+
+  set_rows(a, in[2], p->v, in[3], p->dout, in[0], p->q, out[1], p->dk);
+  a.s_in = dstate_out;
+  a.reverse = 1;
+  a.e = 0;
+  a.read = 1.f;
+  a.update = p->scale;
+  if (e == cudaSuccess) e = launch_pass(a, p->dtype, p->variant, s);
+
+  DecayPass c = pass_of(p, dkey, dval);  // dv, and the gradient of the first state
+  set_rows(c, in[1], p->k, in[0], p->q, in[3], p->dout, out[2], p->dv);
+  c.g = log_decay;
+  c.lengths = lengths;
+  c.s_in = dstate_out;
+  c.s_out = dstate_in;
+  c.s_ldx = dval;
+  c.s_ldz = 1;
+  c.seg = seg;
+  c.reverse = 1;
+  c.e = 0;
+  c.score = p->scale;
+  c.read = 1.f;
+  c.update = p->scale;
+  if (e == cudaSuccess) e = launch_pass(c, p->dtype, p->variant, s);
+  return scratch.give_back(e == cudaSuccess ? MHLA_OK : record_cuda_error(e));
+}
+
+mhla_status mhla_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
+                            const float* state_in, const mhla_decay_params* p, void* out, float* state_out,
+                            void* stream) {
+  using namespace mhla;
+  mhla_status st = check_params(p);
+  if (st != MHLA_OK) return st;
+  if (p->tokens != 1) return MHLA_ERR_INVALID_ARG;
+  if ((int64_t)p->batch * p->heads == 0) return MHLA_OK;
+  const RowTensor in[5] = {tensor(p, q, p->q, p->key_dim), tensor(p, k, p->k, p->key_dim),
+                           tensor(p, v, p->v, p->value_dim), flat_tensor(log_decay, p->heads, 4),
+                           state_tensor(p, state_in)};
+  const RowTensor to = tensor(p, out, p->out, p->value_dim), ts = state_tensor(p, state_out);
+  for (const RowTensor& t : in)
+    if (!row_tensor_ok(t, false)) return MHLA_ERR_INVALID_ARG;
+  if (!row_tensor_ok(to, true) || !state_ok(in[4]) || !state_ok(ts)) return MHLA_ERR_INVALID_ARG;
+  if (!apart_from_all(to, in, 5) || !row_tensors_apart(to, ts) || !apart_from_all(ts, in, 4))
+    return MHLA_ERR_INVALID_ARG;
+  if (state_out != state_in && !row_tensors_apart(ts, in[4])) return MHLA_ERR_INVALID_ARG;
+  DecayPass a = pass_of(p, p->key_dim, p->value_dim);
+  set_rows(a, in[0], p->q, in[1], p->k, in[2], p->v, to, p->out);
+  a.g = log_decay;
+  a.s_in = state_in;
+  a.s_out = state_out;
+  a.read = p->scale;
+  const cudaError_t e = launch_decay_step(a, p->dtype, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? MHLA_OK : record_cuda_error(e);
+}
+
+}  // extern "C"
