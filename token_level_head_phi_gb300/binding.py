@@ -48,6 +48,10 @@ DTYPES = {"bf16": DTYPE_BF16, "f32": DTYPE_F32}
 LAYOUT_BHND = 0
 LAYOUT_BNHD = 1
 LAYOUTS = {"bhnd": LAYOUT_BHND, "bnhd": LAYOUT_BNHD}
+ROTARY_STYLES = {"half": 0, "interleaved": 1}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+ROTARY_MAX_PAIRS = 128
+DECAY_VARIANTS = {"auto": 0, "simt": 1, "tensor": 2}
 
 
 class MhlaError(RuntimeError):
@@ -77,7 +81,43 @@ class MhlaPlanInfo(ctypes.Structure):
     ]
 
 
+class MhlaStrides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("head", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
+class MhlaRotaryTable(ctypes.Structure):
+    _fields_ = [("pairs", ctypes.c_int), ("amplitude", ctypes.c_float), ("turns", ctypes.c_uint64 * ROTARY_MAX_PAIRS)]
+
+
+class MhlaRotaryParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("style", ctypes.c_int), ("transpose", ctypes.c_int),
+        ("position_dtype", ctypes.c_int), ("position_offset", ctypes.c_int64),
+        ("position_batch_stride", ctypes.c_int64), ("position_token_stride", ctypes.c_int64),
+        ("q", MhlaStrides), ("k", MhlaStrides), ("q_out", MhlaStrides), ("k_out", MhlaStrides),
+    ]
+
+
+class MhlaLayernormParams(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
+        ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+        ("dy_stride", ctypes.c_int64),
+    ]
+
+
+class MhlaDecayParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int), ("heads", ctypes.c_int), ("tokens", ctypes.c_int), ("key_dim", ctypes.c_int),
+        ("value_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("variant", ctypes.c_int), ("scale", ctypes.c_float),
+        ("q", MhlaStrides), ("k", MhlaStrides), ("v", MhlaStrides), ("out", MhlaStrides),
+        ("dout", MhlaStrides), ("dq", MhlaStrides), ("dk", MhlaStrides), ("dv", MhlaStrides),
+    ]
+
+
 _LIB = None
+_P = ctypes.c_void_p
 
 # (name, restype, argtypes) of every entry point in include/mhla.h
 SIGNATURES = [
@@ -102,6 +142,22 @@ SIGNATURES = [
     ("mhla_backward_workspace_bytes", ctypes.c_int, [ctypes.POINTER(MhlaParams), ctypes.POINTER(ctypes.c_size_t)]),
     ("mhla_backward", ctypes.c_int, [ctypes.c_void_p] * 5 + [ctypes.POINTER(MhlaParams)] + [ctypes.c_void_p] * 5
      + [ctypes.c_size_t, ctypes.c_void_p]),
+    ("mhla_rotary_table_init", ctypes.c_int, [ctypes.c_int, ctypes.c_double, ctypes.c_int, ctypes.c_double,
+                                              ctypes.c_double, ctypes.POINTER(MhlaRotaryTable)]),
+    ("mhla_rotary", ctypes.c_int, [_P, _P, _P, ctypes.POINTER(MhlaRotaryTable), ctypes.POINTER(MhlaRotaryParams),
+                                   _P, _P, _P]),
+    ("mhla_layernorm_forward", ctypes.c_int, [_P, _P, _P, ctypes.POINTER(MhlaLayernormParams), _P, _P, _P, _P]),
+    ("mhla_layernorm_backward_workspace_bytes", ctypes.c_int, [ctypes.POINTER(MhlaLayernormParams),
+                                                               ctypes.POINTER(ctypes.c_size_t)]),
+    ("mhla_layernorm_backward", ctypes.c_int, [_P] * 5 + [ctypes.POINTER(MhlaLayernormParams)] + [_P] * 4
+     + [ctypes.c_size_t, _P]),
+    ("mhla_decay_workspace_bytes", ctypes.c_int, [ctypes.POINTER(MhlaDecayParams), ctypes.POINTER(ctypes.c_size_t)]),
+    ("mhla_decay_forward", ctypes.c_int, [_P] * 6 + [ctypes.POINTER(MhlaDecayParams), _P, _P, _P, ctypes.c_size_t, _P]),
+    ("mhla_decay_backward_workspace_bytes", ctypes.c_int, [ctypes.POINTER(MhlaDecayParams),
+                                                           ctypes.POINTER(ctypes.c_size_t)]),
+    ("mhla_decay_backward", ctypes.c_int, [_P] * 8 + [ctypes.POINTER(MhlaDecayParams)] + [_P] * 5
+     + [ctypes.c_size_t, _P]),
+    ("mhla_decay_step", ctypes.c_int, [_P] * 5 + [ctypes.POINTER(MhlaDecayParams), _P, _P, _P]),
 ]
 
 
@@ -394,3 +450,396 @@ def mhla_set_debug(option: int, value: int) -> None:
 
 def mhla_abi_version() -> int:
     return load().mhla_abi_version()
+
+
+# --------------------------------------------------------------------------
+# Operators around the attention.  Tensors may have any strides as long as
+# the last axis is contiguous; nothing is copied to make them contiguous.
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_handle(stream, device) -> int:
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _axes(layout: str):
+    """Positions of the batch, head and token axes."""
+    if layout == "bhnd":
+        return 0, 1, 2
+    if layout == "bnhd":
+        return 0, 2, 1
+    raise ValueError(f"unknown layout {layout!r}; expected 'bhnd' or 'bnhd'")
+
+
+def _rows(name, t, like=None, dtype=None, shape=None):
+    """Checks one tensor of rows (last axis contiguous, on the GPU)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    return t
+
+
+def _flat(name, t, like, dtype, shape):
+    """Checks one contiguous side tensor."""
+    _rows(name, t, like, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _set_strides(field, t, axes) -> None:
+    st = t.stride()
+    field.batch, field.head, field.token = st[axes[0]], st[axes[1]], st[axes[2]]
+
+
+class RotaryPlan:
+    """The frequencies of a rotation, made once by :func:`mhla_rotary_plan`."""
+
+    def __init__(self, rot_dim: int, table: MhlaRotaryTable):
+        self.rot_dim = rot_dim
+        self.table = table
+        self._ref = ctypes.byref(table)
+
+    @property
+    def amplitude(self) -> float:
+        return self.table.amplitude
+
+
+def mhla_rotary_plan(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: float = 0.0) -> RotaryPlan:
+    """Frequencies for the first ``rot_dim`` entries of a head (see mhla_rotary_table_init in mhla.h).
+
+    ``scaling``: "none", "linear" (positions divided by ``factor``), "base"
+    (a larger base) or "parts" (slow frequencies interpolated, fast ones kept;
+    needs ``original_length``).
+    """
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r}; expected one of {sorted(ROTARY_SCALINGS)}")
+    table = MhlaRotaryTable()
+    _check(load().mhla_rotary_table_init(int(rot_dim), float(base), ROTARY_SCALINGS[scaling], float(factor),
+                                         float(original_length), ctypes.byref(table)), "mhla_rotary_table_init")
+    return RotaryPlan(int(rot_dim), table)
+
+
+def _rotary(q, k, plan, positions, offset, style, layout, q_out, k_out, stream, transpose, where):
+    import torch
+    axes = _axes(layout)
+    if style not in ROTARY_STYLES:
+        raise ValueError(f"unknown style {style!r}; expected one of {sorted(ROTARY_STYLES)}")
+    if q.dim() != 4:
+        raise ValueError("q and k must be [B, H, N, d] (layout 'bhnd') or [B, N, H, d] (layout 'bnhd')")
+    _rows("q", q)
+    p = MhlaRotaryParams()
+    shape = q.shape
+    p.batch, p.heads, p.tokens, p.head_dim = shape[0], shape[axes[1]], shape[axes[2]], shape[3]
+    p.dtype = DTYPES[_torch_dtype_name(q)]
+    p.style, p.transpose = ROTARY_STYLES[style], transpose
+    p.position_offset = int(offset)
+    q_out = torch.empty(shape, dtype=q.dtype, device=q.device) if q_out is None else _rows("q_out", q_out, q, q.dtype, shape)
+    _set_strides(p.q, q, axes)
+    _set_strides(p.q_out, q_out, axes)
+    if k is not None:
+        want = list(shape)
+        want[axes[1]] = k.shape[axes[1]] if k.dim() == 4 else -1
+        _rows("k", k, q, q.dtype, want)
+        p.kv_heads = k.shape[axes[1]]
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else _rows("k_out", k_out, q, q.dtype, k.shape)
+        _set_strides(p.k, k, axes)
+        _set_strides(p.k_out, k_out, axes)
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+        if not positions.is_cuda or positions.device != q.device:
+            raise ValueError(f"positions must be on {q.device}")
+        if positions.dim() == 1 and positions.shape[0] == p.tokens:
+            p.position_token_stride = positions.stride(0)
+        elif positions.dim() == 2 and tuple(positions.shape) in ((p.batch, p.tokens), (1, p.tokens)):
+            p.position_batch_stride = positions.stride(0) if positions.shape[0] > 1 else 0
+            p.position_token_stride = positions.stride(1)
+        else:
+            raise ValueError(f"positions must be [N] or [B, N], got {tuple(positions.shape)}")
+        p.position_dtype = 1 if positions.dtype == torch.int64 else 0
+    _check(load().mhla_rotary(q.data_ptr(), _ptr(k), _ptr(positions), plan._ref, ctypes.byref(p), q_out.data_ptr(),
+                              _ptr(k_out), _stream_handle(stream, q.device)), where)
+    return q_out, k_out
+
+
+def mhla_rotary_forward(q, k, plan: RotaryPlan, positions=None, offset: int = 0, style: str = "half",
+                        layout: str = "bhnd", q_out=None, k_out=None, stream=None):
+    """Rotary positions on queries and keys; returns ``(q_out, k_out)``.
+
+    ``k`` may be None and may have another number of heads than ``q``.
+    ``positions``: int32 or int64 [N] or [B, N] on the GPU; without it token t
+    has position ``offset + t``.  ``style``: "half" pairs entry i with
+    i + rot_dim / 2, "interleaved" 2i with 2i + 1.  ``q_out is q`` and
+    ``k_out is k`` rotate in place.
+    """
+    return _rotary(q, k, plan, positions, offset, style, layout, q_out, k_out, stream, 0, "mhla_rotary_forward")
+
+
+def mhla_rotary_backward(dq_out, dk_out, plan: RotaryPlan, positions=None, offset: int = 0, style: str = "half",
+                         layout: str = "bhnd", dq=None, dk=None, stream=None):
+    """Gradients of q and k from those of mhla_rotary_forward's results: ``(dq, dk)``."""
+    return _rotary(dq_out, dk_out, plan, positions, offset, style, layout, dq, dk, stream, 1, "mhla_rotary_backward")
+
+
+def _norm_rows(name, t, like=None):
+    """[rows, cols] of a tensor whose leading axes collapse into one stride: (rows, cols, stride)."""
+    _rows(name, t, like, like.dtype if like is not None else None, like.shape if like is not None else None)
+    if t.dim() < 1:
+        raise ValueError(f"{name} must have at least one axis")
+    cols = t.shape[-1]
+    rows, stride = 1, None
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * rows and t.numel():
+            raise ValueError(f"the leading axes of {name} must collapse into rows of one stride")
+        rows *= n
+    return rows, cols, cols if stride is None else stride
+
+
+def _norm_params(x, weight, bias, eps):
+    import torch
+    p = MhlaLayernormParams()
+    p.rows, p.cols, p.x_stride = _norm_rows("x", x)
+    if p.cols < 1:
+        raise ValueError("x must have at least one column")
+    p.dtype = DTYPES[_torch_dtype_name(x)]
+    p.weight_dtype = DTYPE_F32
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _flat(name, t, x, None, (p.cols,))
+            p.weight_dtype = DTYPES[_torch_dtype_name(t)]
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have the same dtype")
+    p.eps = eps
+    return p
+
+
+def mhla_layernorm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None, stream=None):
+    """Layer norm over the last axis; returns ``(y, mean, rstd)``.
+
+    ``weight`` and ``bias`` are [cols], bfloat16 or float32; ``mean`` and
+    ``rstd`` are float32 of x's leading shape, for the backward call.
+    ``out is x`` normalises in place.
+    """
+    import torch
+    p = _norm_params(x, weight, bias, eps)
+    lead = x.shape[:-1]
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
+    rows, _, p.y_stride = _norm_rows("out", out, x)
+    mean = torch.empty(lead, dtype=torch.float32, device=x.device) if mean is None else _flat("mean", mean, x, torch.float32, lead)
+    rstd = torch.empty(lead, dtype=torch.float32, device=x.device) if rstd is None else _flat("rstd", rstd, x, torch.float32, lead)
+    _check(load().mhla_layernorm_forward(x.data_ptr(), _ptr(weight), _ptr(bias), ctypes.byref(p), out.data_ptr(),
+                                         mean.data_ptr(), rstd.data_ptr(), _stream_handle(stream, x.device)),
+           "mhla_layernorm_forward")
+    return out, mean, rstd
+
+
+def mhla_layernorm_backward_workspace_bytes(p: MhlaLayernormParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().mhla_layernorm_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(n)),
+           "mhla_layernorm_backward_workspace_bytes")
+    return n.value
+
+
+def mhla_layernorm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, workspace=None,
+                            stream=None, params: bool = True):
+    """Gradients of mhla_layernorm_forward: ``(dx, dweight, dbias)``.
+
+    ``dweight`` and ``dbias`` are float32 [cols], summed over the rows in a
+    fixed order; ``params=False`` leaves them out (None).  ``dx is dy`` or
+    ``dx is x`` overwrites that input.
+    """
+    import torch
+    p = _norm_params(x, weight, None, 0.0)
+    _, _, p.dy_stride = _norm_rows("dy", dy, x)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
+    _, _, p.y_stride = _norm_rows("dx", dx, x)
+    lead = x.shape[:-1]
+    _flat("mean", mean, x, torch.float32, lead)
+    _flat("rstd", rstd, x, torch.float32, lead)
+    ws_bytes = 0
+    if params:
+        dweight = torch.empty(p.cols, dtype=torch.float32, device=x.device) if dweight is None else _flat("dweight", dweight, x, torch.float32, (p.cols,))
+        dbias = torch.empty(p.cols, dtype=torch.float32, device=x.device) if dbias is None else _flat("dbias", dbias, x, torch.float32, (p.cols,))
+        if workspace is None:
+            workspace = torch.empty(max(mhla_layernorm_backward_workspace_bytes(p), 1), dtype=torch.uint8, device=x.device)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    elif dweight is not None or dbias is not None:
+        raise ValueError("dweight and dbias need params=True")
+    _check(load().mhla_layernorm_backward(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
+                                          ctypes.byref(p), dx.data_ptr(), _ptr(dweight), _ptr(dbias),
+                                          _ptr(workspace) if params else None, ws_bytes,
+                                          _stream_handle(stream, x.device)), "mhla_layernorm_backward")
+    return dx, dweight, dbias
+
+
+def _decay_params(q, k, v, log_decay, scale, layout, variant):
+    """(params, axes) of q, k [B, H, N, dk] and v [B, H, N, dv] ('bhnd') or their token-major forms."""
+    import torch
+    axes = _axes(layout)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be [B, H, N, d] (layout 'bhnd') or [B, N, H, d] (layout 'bnhd')")
+    _rows("q", q)
+    _rows("k", k, q, q.dtype, q.shape)
+    _rows("v", v, q, q.dtype, tuple(q.shape[:3]) + (v.shape[3],))
+    p = MhlaDecayParams()
+    shape = q.shape
+    p.batch, p.heads, p.tokens = shape[0], shape[axes[1]], shape[axes[2]]
+    p.key_dim, p.value_dim = shape[3], v.shape[3]
+    p.dtype = DTYPES[_torch_dtype_name(q)]
+    if variant not in DECAY_VARIANTS:
+        raise ValueError(f"unknown variant {variant!r}; expected one of {sorted(DECAY_VARIANTS)}")
+    p.variant = DECAY_VARIANTS[variant]
+    p.scale = scale
+    _flat("log_decay", log_decay, q, torch.float32, (p.heads,))
+    _set_strides(p.q, q, axes)
+    _set_strides(p.k, k, axes)
+    _set_strides(p.v, v, axes)
+    return p, axes
+
+
+def _decay_state(name, t, p, like):
+    import torch
+    return _flat(name, t, like, torch.float32, (p.batch, p.heads, p.key_dim, p.value_dim))
+
+
+def _decay_lengths(lengths, p, like):
+    import torch
+    if lengths is not None:
+        _flat("lengths", lengths, like, torch.int32, (p.batch,))
+    return lengths
+
+
+def mhla_decay_workspace_bytes(p: MhlaDecayParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().mhla_decay_workspace_bytes(ctypes.byref(p), ctypes.byref(n)), "mhla_decay_workspace_bytes")
+    return n.value
+
+
+def mhla_decay_forward(q, k, v, log_decay, state=None, lengths=None, scale: float = 1.0, layout: str = "bhnd",
+                       variant: str = "auto", out=None, state_out=None, workspace=None, stream=None):
+    """Linear attention with a decay for each head over whole prompts: ``(out, state_out)``.
+
+    S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T and o_t = scale S_t^T q_t.
+    q, k: [B, H, N, dk], v: [B, H, N, dv] ('bhnd'; 'bnhd' is token-major), dk
+    and dv each 16, 32, 64 or 128, bfloat16 or float32.  ``log_decay``:
+    float32 [H].  ``state``: float32 [B, H, dk, dv] to start from (None:
+    zeros); ``state_out is state`` updates it in place.  ``lengths``: int32
+    [B] for sequences padded to N; rows past a length come out as zeros.
+    """
+    import torch
+    p, axes = _decay_params(q, k, v, log_decay, scale, layout, variant)
+    out = torch.empty(v.shape, dtype=v.dtype, device=v.device) if out is None else _rows("out", out, q, q.dtype, v.shape)
+    _set_strides(p.out, out, axes)
+    if state is not None:
+        _decay_state("state", state, p, q)
+    if state_out is None:
+        state_out = torch.empty((p.batch, p.heads, p.key_dim, p.value_dim), dtype=torch.float32, device=q.device)
+    else:
+        _decay_state("state_out", state_out, p, q)
+    _decay_lengths(lengths, p, q)
+    ws_bytes = 0
+    if workspace is None:
+        need = mhla_decay_workspace_bytes(p)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(load().mhla_decay_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths),
+                                     _ptr(state), ctypes.byref(p), out.data_ptr(), state_out.data_ptr(),
+                                     _ptr(workspace), ws_bytes, _stream_handle(stream, q.device)),
+           "mhla_decay_forward")
+    return out, state_out
+
+
+def mhla_decay_backward_workspace_bytes(p: MhlaDecayParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().mhla_decay_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(n)),
+           "mhla_decay_backward_workspace_bytes")
+    return n.value
+
+
+def mhla_decay_backward(q, k, v, log_decay, dout, state=None, dstate_out=None, lengths=None, scale: float = 1.0,
+                        layout: str = "bhnd", variant: str = "auto", dq=None, dk=None, dv=None, dstate=None,
+                        workspace=None, stream=None):
+    """Gradients of mhla_decay_forward: ``(dq, dk, dv, dstate)``.
+
+    ``dout`` is the gradient of out and ``dstate_out`` that of the final state
+    (None: zeros); ``dstate`` is the gradient of the starting state (float32
+    [B, H, dk, dv]).  Arguments as in the forward call.
+    """
+    import torch
+    p, axes = _decay_params(q, k, v, log_decay, scale, layout, variant)
+    _rows("dout", dout, q, q.dtype, v.shape)
+    _set_strides(p.dout, dout, axes)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else _rows("dq", dq, q, q.dtype, q.shape)
+    dk = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dk is None else _rows("dk", dk, q, q.dtype, q.shape)
+    dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else _rows("dv", dv, q, q.dtype, v.shape)
+    _set_strides(p.dq, dq, axes)
+    _set_strides(p.dk, dk, axes)
+    _set_strides(p.dv, dv, axes)
+    for name, t in (("state", state), ("dstate_out", dstate_out), ("dstate", dstate)):
+        if t is not None:
+            _decay_state(name, t, p, q)
+    if dstate is None:
+        dstate = torch.empty((p.batch, p.heads, p.key_dim, p.value_dim), dtype=torch.float32, device=q.device)
+    _decay_lengths(lengths, p, q)
+    ws_bytes = 0
+    if workspace is None:
+        need = mhla_decay_backward_workspace_bytes(p)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _check(load().mhla_decay_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths),
+                                      _ptr(state), dout.data_ptr(), _ptr(dstate_out), ctypes.byref(p), dq.data_ptr(),
+                                      dk.data_ptr(), dv.data_ptr(), dstate.data_ptr(), _ptr(workspace), ws_bytes,
+                                      _stream_handle(stream, q.device)), "mhla_decay_backward")
+    return dq, dk, dv, dstate
+
+
+def mhla_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, state_out=None, stream=None):
+    """One token of every sequence: returns ``out`` [B, H, dv].
+
+    q, k: [B, H, dk], v: [B, H, dv]; ``state`` float32 [B, H, dk, dv] is
+    updated in place unless ``state_out`` is given.
+    """
+    import torch
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, v must be [B, H, d]")
+    _rows("q", q)
+    _rows("k", k, q, q.dtype, q.shape)
+    _rows("v", v, q, q.dtype, tuple(q.shape[:2]) + (v.shape[2],))
+    p = MhlaDecayParams()
+    p.batch, p.heads, p.key_dim = q.shape
+    p.tokens, p.value_dim = 1, v.shape[2]
+    p.dtype = DTYPES[_torch_dtype_name(q)]
+    p.scale = scale
+    _flat("log_decay", log_decay, q, torch.float32, (p.heads,))
+    _decay_state("state", state, p, q)
+    state_out = state if state_out is None else _decay_state("state_out", state_out, p, q)
+    out = torch.empty(v.shape, dtype=v.dtype, device=v.device) if out is None else _rows("out", out, q, q.dtype, v.shape)
+    for field, t in ((p.q, q), (p.k, k), (p.v, v), (p.out, out)):
+        field.batch, field.head = t.stride(0), t.stride(1)
+    _check(load().mhla_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
+                                  ctypes.byref(p), out.data_ptr(), state_out.data_ptr(),
+                                  _stream_handle(stream, q.device)), "mhla_decay_step")
+    return out
