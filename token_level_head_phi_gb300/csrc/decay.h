@@ -78,6 +78,7 @@ __device__ __forceinline__ int decay_token(const DecayPass& p, int i, int length
 
 // Launches return a cudaError_t.
 cudaError_t launch_decay_simt(const DecayPass& p, int dtype, cudaStream_t s);
+cudaError_t launch_decay_mma(const DecayPass& p, cudaStream_t s);  // bf16
 cudaError_t launch_decay_step(const DecayPass& p, int dtype, cudaStream_t s);
 
 }  // namespace mhla

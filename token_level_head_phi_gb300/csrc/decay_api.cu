@@ -15,36 +15,41 @@ mhla_status check_params(const mhla_decay_params* p) {
   if (!dim_ok(p->key_dim) || !dim_ok(p->value_dim) || !ops_dtype_ok(p->dtype)) return MHLA_ERR_INVALID_ARG;
   if (p->variant < MHLA_DECAY_AUTO || p->variant > MHLA_DECAY_TENSOR || !std::isfinite(p->scale))
     return MHLA_ERR_INVALID_ARG;
-  if (p->variant == MHLA_DECAY_TENSOR) return MHLA_ERR_UNSUPPORTED;
+  if (p->variant == MHLA_DECAY_TENSOR && p->dtype != MHLA_DTYPE_BF16) return MHLA_ERR_UNSUPPORTED;
   if ((int64_t)p->batch * p->heads > (1 << 24) || p->tokens > (1 << 30)) return MHLA_ERR_UNSUPPORTED;
   return MHLA_OK;
 }
 
-// Segments of a pass: enough CTAs (units x slices of 64 columns x segments)
-// for two on every SM, segments of at least 256 tokens (the state that starts
-// a segment costs about as much as that many tokens), at most 64 of them (a
+bool on_tensor_cores(const mhla_decay_params* p) {
+  return p->dtype == MHLA_DTYPE_BF16 && p->variant != MHLA_DECAY_SIMT;
+}
+
+// Segments of a pass: as many as the CTAs (units x slices of 64 columns x
+// segments) that are resident at once (three on every SM, two with DX = 128
+// and on the CUDA cores), of at least 256 tokens (the state that starts a
+// segment costs about as much as that many tokens), and at most 64 of them (a
 // segment sums all earlier states).
 constexpr int kSegQuantum = 128, kSegLeast = 256, kSegMost = 64;
 
-void plan_segments(int64_t units, int dz, int tokens, int* nseg, int* seg_len) {
-  const int64_t ctas = units * (dz > 64 ? dz / 64 : 1);
-  int64_t n = ctas > 0 ? 2 * kOpsSms / ctas : 1;
-  if (n > tokens / kSegLeast) n = tokens / kSegLeast;
+void plan_segments(const mhla_decay_params* p, int dx, int dz, int* nseg, int* seg_len) {
+  const int64_t ctas = (int64_t)p->batch * p->heads * (dz > 64 ? dz / 64 : 1);
+  const int64_t slots = (on_tensor_cores(p) && dx < 128 ? 3 : 2) * kOpsSms;
+  int64_t n = ctas > 0 ? slots / ctas : 1;
+  if (n > p->tokens / kSegLeast) n = p->tokens / kSegLeast;
   if (n > kSegMost) n = kSegMost;
   if (n < 1) n = 1;
-  int64_t len = (tokens + n - 1) / n;
+  int64_t len = (p->tokens + n - 1) / n;
   len = (len + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
   if (len < kSegQuantum) len = kSegQuantum;
   *seg_len = (int)len;
-  *nseg = (int)((tokens + len - 1) / len);
+  *nseg = (int)((p->tokens + len - 1) / len);
   if (*nseg < 1) *nseg = 1;
 }
 
-size_t pass_workspace(const mhla_decay_params* p, int dz) {
+size_t pass_workspace(const mhla_decay_params* p, int dx, int dz) {
   int nseg, seg_len;
-  const int64_t units = (int64_t)p->batch * p->heads;
-  plan_segments(units, dz, p->tokens, &nseg, &seg_len);
-  return nseg > 1 ? sizeof(float) * (size_t)units * nseg * p->key_dim * p->value_dim : 0;
+  plan_segments(p, dx, dz, &nseg, &seg_len);
+  return nseg > 1 ? sizeof(float) * (size_t)p->batch * p->heads * nseg * dx * dz : 0;
 }
 
 RowTensor tensor(const mhla_decay_params* p, const void* ptr, const mhla_strides& s, int dim) {
@@ -64,7 +69,7 @@ DecayPass pass_of(const mhla_decay_params* p, int dx, int dz) {
   a.N = p->tokens;
   a.DX = dx;
   a.DZ = dz;
-  plan_segments((int64_t)p->batch * p->heads, dz, p->tokens, &a.nseg, &a.seg_len);
+  plan_segments(p, dx, dz, &a.nseg, &a.seg_len);
   return a;
 }
 
@@ -90,9 +95,8 @@ mhla_status copy_state(const mhla_decay_params* p, const float* from, float* to,
   return e == cudaSuccess ? MHLA_OK : record_cuda_error(e);
 }
 
-cudaError_t launch_pass(const DecayPass& a, int dtype, int variant, cudaStream_t s) {
-  (void)variant;
-  return launch_decay_simt(a, dtype, s);
+cudaError_t launch_pass(const DecayPass& a, const mhla_decay_params* p, cudaStream_t s) {
+  return on_tensor_cores(p) ? launch_decay_mma(a, s) : launch_decay_simt(a, p->dtype, s);
 }
 
 // Whether `out` shares memory with none of `in`.
@@ -112,7 +116,7 @@ mhla_status mhla_decay_workspace_bytes(const mhla_decay_params* p, size_t* bytes
   if (!bytes) return MHLA_ERR_INVALID_ARG;
   const mhla_status st = check_params(p);
   if (st != MHLA_OK) return st;
-  *bytes = pass_workspace(p, p->value_dim);
+  *bytes = pass_workspace(p, p->key_dim, p->value_dim);
   return MHLA_OK;
 }
 
@@ -135,7 +139,7 @@ mhla_status mhla_decay_forward(const void* q, const void* k, const void* v, cons
     return MHLA_ERR_INVALID_ARG;
   if (state_out != state_in && !row_tensors_apart(ts, in[5])) return MHLA_ERR_INVALID_ARG;
   if (p->tokens == 0) return copy_state(p, state_in, state_out, s);
-  const size_t need = pass_workspace(p, p->value_dim);
+  const size_t need = pass_workspace(p, p->key_dim, p->value_dim);
   const RowTensor tw = flat_tensor(workspace, workspace ? (int64_t)need : 0, 1);
   if (!apart_from_all(tw, in, 6) || !row_tensors_apart(tw, to) || !row_tensors_apart(tw, ts))
     return MHLA_ERR_INVALID_ARG;
@@ -153,7 +157,7 @@ mhla_status mhla_decay_forward(const void* q, const void* k, const void* v, cons
   a.e = 1;
   a.score = a.read = p->scale;
   a.update = 1.f;
-  const cudaError_t e = launch_pass(a, p->dtype, p->variant, s);
+  const cudaError_t e = launch_pass(a, p, s);
   return scratch.give_back(e == cudaSuccess ? MHLA_OK : record_cuda_error(e));
 }
 
@@ -162,7 +166,7 @@ mhla_status mhla_decay_backward_workspace_bytes(const mhla_decay_params* p, size
   if (!bytes) return MHLA_ERR_INVALID_ARG;
   const mhla_status st = check_params(p);
   if (st != MHLA_OK) return st;
-  const size_t a = pass_workspace(p, p->key_dim), b = pass_workspace(p, p->value_dim);
+  const size_t a = pass_workspace(p, p->value_dim, p->key_dim), b = pass_workspace(p, p->key_dim, p->value_dim);
   *bytes = a > b ? a : b;
   return MHLA_OK;
 }
@@ -215,7 +219,7 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
   a.e = 1;
   a.score = a.read = p->scale;
   a.update = 1.f;
-  cudaError_t e = launch_pass(a, p->dtype, p->variant, s);
+  cudaError_t e = launch_pass(a, p, s);
 
   set_rows(a, in[2], p->v, in[3], p->dout, in[0], p->q, out[1], p->dk);
   a.s_in = dstate_out;
@@ -223,7 +227,7 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
   a.e = 0;
   a.read = 1.f;
   a.update = p->scale;
-  if (e == cudaSuccess) e = launch_pass(a, p->dtype, p->variant, s);
+  if (e == cudaSuccess) e = launch_pass(a, p, s);
 
   DecayPass c = pass_of(p, dkey, dval);  // dv, and the gradient of the first state
   set_rows(c, in[1], p->k, in[0], p->q, in[3], p->dout, out[2], p->dv);
@@ -239,7 +243,7 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
   c.score = p->scale;
   c.read = 1.f;
   c.update = p->scale;
-  if (e == cudaSuccess) e = launch_pass(c, p->dtype, p->variant, s);
+  if (e == cudaSuccess) e = launch_pass(c, p, s);
   return scratch.give_back(e == cudaSuccess ? MHLA_OK : record_cuda_error(e));
 }
 

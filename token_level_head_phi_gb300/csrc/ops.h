@@ -72,25 +72,40 @@ inline bool row_tensor_ok(const RowTensor& t, bool output) {
   return true;
 }
 
+// The same memory with adjacent rows joined (the heads of a token-major
+// tensor) and axes that do not move (one entry, stride 0) dropped.
+inline RowTensor joined_rows(RowTensor t) {
+  for (int i = 0; i < 3; ++i)
+    if (t.n[i] <= 1 || t.stride[i] == 0) t.n[i] = 1, t.stride[i] = 0;
+  for (int pass = 0; pass < 3; ++pass)
+    for (int i = 0; i < 3; ++i)
+      if (t.n[i] > 1 && t.stride[i] == t.row) {
+        t.row *= t.n[i];
+        t.n[i] = 1;
+        t.stride[i] = 0;
+      }
+  return t;
+}
+
 // Whether two tensors certainly share no byte: their extents are apart, or
 // all their rows lie at residues of one common stride that are apart (slices
 // of one fused buffer, such as the q, k and v parts of a projection).
-inline bool row_tensors_apart(const RowTensor& a, const RowTensor& b) {
-  if (a.empty() || b.empty() || !a.ptr || !b.ptr) return true;
+inline bool row_tensors_apart(const RowTensor& first, const RowTensor& second) {
+  if (first.empty() || second.empty() || !first.ptr || !second.ptr) return true;
+  const RowTensor a = joined_rows(first), b = joined_rows(second);
   const uintptr_t pa = (uintptr_t)a.ptr, pb = (uintptr_t)b.ptr;
   if (pa + (uintptr_t)a.extent() <= pb || pb + (uintptr_t)b.extent() <= pa) return true;
-  int64_t g = 0;
+  int64_t g = 0;  // of all strides, in bytes
   const RowTensor* both[2] = {&a, &b};
   for (const RowTensor* t : both)
-    for (int i = 0; i < 3; ++i)
-      if (t->n[i] > 1) {
-        int64_t x = t->stride[i] * (int64_t)t->elem;
-        while (x) {
-          const int64_t r = g % x;
-          g = x;
-          x = r;
-        }
+    for (int i = 0; i < 3; ++i) {
+      int64_t x = t->stride[i] * (int64_t)t->elem;
+      while (x) {
+        const int64_t r = g % x;
+        g = x;
+        x = r;
       }
+    }
   if (g == 0) return false;
   const int64_t ra = a.row * (int64_t)a.elem, rb = b.row * (int64_t)b.elem;
   // where b's rows start, counted from a's, modulo g
