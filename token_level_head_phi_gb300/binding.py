@@ -455,6 +455,24 @@ def mhla_abi_version() -> int:
 # --------------------------------------------------------------------------
 # Operators around the attention.  Tensors may have any strides as long as
 # the last axis is contiguous; nothing is copied to make them contiguous.
+#
+# A call's checks and its parameter block depend only on the arguments' shapes,
+# strides, dtypes and devices, so they are made once for each such set and kept
+# (a decoding loop calls with the same ones for every token).
+
+_CALLS: dict = {}
+_MOST_CALLS = 4096
+
+
+def _sig(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.get_device())
+
+
+def _remember(key, call):
+    if len(_CALLS) >= _MOST_CALLS:
+        _CALLS.clear()
+    _CALLS[key] = call
+    return call
 
 
 def _ptr(t):
@@ -468,6 +486,12 @@ def _stream_handle(stream, device) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _fresh(t, contiguous):
+    """A contiguous tensor shaped and typed like t."""
+    import torch
+    return torch.empty_like(t) if contiguous else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _axes(layout: str):
     """Positions of the batch, head and token axes."""
     if layout == "bhnd":
@@ -475,6 +499,12 @@ def _axes(layout: str):
     if layout == "bnhd":
         return 0, 2, 1
     raise ValueError(f"unknown layout {layout!r}; expected 'bhnd' or 'bnhd'")
+
+
+def _choice(name, value, table):
+    if value not in table:
+        raise ValueError(f"unknown {name} {value!r}; expected one of {sorted(table)}")
+    return table[value]
 
 
 def _rows(name, t, like=None, dtype=None, shape=None):
@@ -489,20 +519,50 @@ def _rows(name, t, like=None, dtype=None, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
-    return t
 
 
 def _flat(name, t, like, dtype, shape):
-    """Checks one contiguous side tensor."""
+    """Checks one contiguous side tensor (None: not given)."""
+    if t is None:
+        return
     _rows(name, t, like, dtype, shape)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t
 
 
 def _set_strides(field, t, axes) -> None:
     st = t.stride()
     field.batch, field.head, field.token = st[axes[0]], st[axes[1]], st[axes[2]]
+
+
+def _set_output(field, name, t, like, shape, axes) -> None:
+    """Strides of an output: the given tensor's, or those of a new contiguous one."""
+    if t is not None:
+        _rows(name, t, like, like.dtype, shape)
+        _set_strides(field, t, axes)
+        return
+    st, step = [0, 0, 0], shape[3]
+    for a in (2, 1, 0):
+        st[a] = step
+        step *= max(shape[a], 1)
+    field.batch, field.head, field.token = st[axes[0]], st[axes[1]], st[axes[2]]
+
+
+class _Call:
+    """A parameter block with what the wrappers need beside it."""
+
+    def __init__(self, params, need=0, **kw):
+        self.params, self.ref, self.need = params, ctypes.byref(params), need
+        self.__dict__.update(kw)
+
+    def workspace(self, given, device):
+        """(tensor or None, bytes): the caller's workspace or a new one."""
+        if given is not None:
+            return given, given.numel() * given.element_size()
+        if not self.need:
+            return None, 0
+        import torch
+        return torch.empty(self.need, dtype=torch.uint8, device=device), self.need
 
 
 class RotaryPlan:
@@ -526,39 +586,33 @@ def mhla_rotary_plan(rot_dim: int, base: float = 10000.0, scaling: str = "none",
     (a larger base) or "parts" (slow frequencies interpolated, fast ones kept;
     needs ``original_length``).
     """
-    if scaling not in ROTARY_SCALINGS:
-        raise ValueError(f"unknown scaling {scaling!r}; expected one of {sorted(ROTARY_SCALINGS)}")
     table = MhlaRotaryTable()
-    _check(load().mhla_rotary_table_init(int(rot_dim), float(base), ROTARY_SCALINGS[scaling], float(factor),
-                                         float(original_length), ctypes.byref(table)), "mhla_rotary_table_init")
+    _check(load().mhla_rotary_table_init(int(rot_dim), float(base), _choice("scaling", scaling, ROTARY_SCALINGS),
+                                         float(factor), float(original_length), ctypes.byref(table)),
+           "mhla_rotary_table_init")
     return RotaryPlan(int(rot_dim), table)
 
 
-def _rotary(q, k, plan, positions, offset, style, layout, q_out, k_out, stream, transpose, where):
+def _rotary_call(q, k, positions, style, layout, q_out, k_out, transpose):
     import torch
     axes = _axes(layout)
-    if style not in ROTARY_STYLES:
-        raise ValueError(f"unknown style {style!r}; expected one of {sorted(ROTARY_STYLES)}")
+    p = MhlaRotaryParams()
+    p.style, p.transpose = _choice("style", style, ROTARY_STYLES), transpose
     if q.dim() != 4:
         raise ValueError("q and k must be [B, H, N, d] (layout 'bhnd') or [B, N, H, d] (layout 'bnhd')")
     _rows("q", q)
-    p = MhlaRotaryParams()
     shape = q.shape
     p.batch, p.heads, p.tokens, p.head_dim = shape[0], shape[axes[1]], shape[axes[2]], shape[3]
     p.dtype = DTYPES[_torch_dtype_name(q)]
-    p.style, p.transpose = ROTARY_STYLES[style], transpose
-    p.position_offset = int(offset)
-    q_out = torch.empty(shape, dtype=q.dtype, device=q.device) if q_out is None else _rows("q_out", q_out, q, q.dtype, shape)
     _set_strides(p.q, q, axes)
-    _set_strides(p.q_out, q_out, axes)
+    _set_output(p.q_out, "q_out", q_out, q, shape, axes)
     if k is not None:
         want = list(shape)
         want[axes[1]] = k.shape[axes[1]] if k.dim() == 4 else -1
         _rows("k", k, q, q.dtype, want)
         p.kv_heads = k.shape[axes[1]]
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else _rows("k_out", k_out, q, q.dtype, k.shape)
         _set_strides(p.k, k, axes)
-        _set_strides(p.k_out, k_out, axes)
+        _set_output(p.k_out, "k_out", k_out, q, k.shape, axes)
     elif k_out is not None:
         raise ValueError("k_out needs k")
     if positions is not None:
@@ -574,8 +628,23 @@ def _rotary(q, k, plan, positions, offset, style, layout, q_out, k_out, stream, 
         else:
             raise ValueError(f"positions must be [N] or [B, N], got {tuple(positions.shape)}")
         p.position_dtype = 1 if positions.dtype == torch.int64 else 0
-    _check(load().mhla_rotary(q.data_ptr(), _ptr(k), _ptr(positions), plan._ref, ctypes.byref(p), q_out.data_ptr(),
-                              _ptr(k_out), _stream_handle(stream, q.device)), where)
+    return _Call(p, q_dense=q.is_contiguous(), k_dense=k is not None and k.is_contiguous())
+
+
+def _rotary(q, k, plan, positions, offset, style, layout, q_out, k_out, stream, transpose, where):
+    key = ("rotary", transpose, style, layout, _sig(q), _sig(k), _sig(positions), _sig(q_out), _sig(k_out))
+    c = _CALLS.get(key) or _remember(key, _rotary_call(q, k, positions, style, layout, q_out, k_out, transpose))
+    if q_out is None:
+        q_out = _fresh(q, c.q_dense)
+    if k_out is None and k is not None:
+        k_out = _fresh(k, c.k_dense)
+    ref = c.ref
+    if offset:  # changes from token to token: in a block of its own
+        p = MhlaRotaryParams.from_buffer_copy(c.params)
+        p.position_offset = int(offset)
+        ref = ctypes.byref(p)
+    _check(load().mhla_rotary(q.data_ptr(), _ptr(k), _ptr(positions), plan._ref, ref, q_out.data_ptr(), _ptr(k_out),
+                              _stream_handle(stream, key[4][3])), where)
     return q_out, k_out
 
 
@@ -599,7 +668,7 @@ def mhla_rotary_backward(dq_out, dk_out, plan: RotaryPlan, positions=None, offse
 
 
 def _norm_rows(name, t, like=None):
-    """[rows, cols] of a tensor whose leading axes collapse into one stride: (rows, cols, stride)."""
+    """(rows, cols, stride) of a tensor whose leading axes collapse into rows of one stride."""
     _rows(name, t, like, like.dtype if like is not None else None, like.shape if like is not None else None)
     if t.dim() < 1:
         raise ValueError(f"{name} must have at least one axis")
@@ -617,9 +686,9 @@ def _norm_rows(name, t, like=None):
 
 
 def _norm_params(x, weight, bias, eps):
-    import torch
     p = MhlaLayernormParams()
     p.rows, p.cols, p.x_stride = _norm_rows("x", x)
+    p.y_stride = p.cols
     if p.cols < 1:
         raise ValueError("x must have at least one column")
     p.dtype = DTYPES[_torch_dtype_name(x)]
@@ -634,6 +703,16 @@ def _norm_params(x, weight, bias, eps):
     return p
 
 
+def _norm_forward_call(x, weight, bias, eps, out, mean, rstd):
+    import torch
+    p = _norm_params(x, weight, bias, eps)
+    if out is not None:
+        _, _, p.y_stride = _norm_rows("out", out, x)
+    _flat("mean", mean, x, torch.float32, x.shape[:-1])
+    _flat("rstd", rstd, x, torch.float32, x.shape[:-1])
+    return _Call(p, dense=x.is_contiguous(), lead=x.shape[:-1], device=x.device)
+
+
 def mhla_layernorm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None, stream=None):
     """Layer norm over the last axis; returns ``(y, mean, rstd)``.
 
@@ -642,14 +721,16 @@ def mhla_layernorm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=Non
     ``out is x`` normalises in place.
     """
     import torch
-    p = _norm_params(x, weight, bias, eps)
-    lead = x.shape[:-1]
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device) if out is None else out
-    rows, _, p.y_stride = _norm_rows("out", out, x)
-    mean = torch.empty(lead, dtype=torch.float32, device=x.device) if mean is None else _flat("mean", mean, x, torch.float32, lead)
-    rstd = torch.empty(lead, dtype=torch.float32, device=x.device) if rstd is None else _flat("rstd", rstd, x, torch.float32, lead)
-    _check(load().mhla_layernorm_forward(x.data_ptr(), _ptr(weight), _ptr(bias), ctypes.byref(p), out.data_ptr(),
-                                         mean.data_ptr(), rstd.data_ptr(), _stream_handle(stream, x.device)),
+    key = ("norm", eps, _sig(x), _sig(weight), _sig(bias), _sig(out), _sig(mean), _sig(rstd))
+    c = _CALLS.get(key) or _remember(key, _norm_forward_call(x, weight, bias, eps, out, mean, rstd))
+    if out is None:
+        out = _fresh(x, c.dense)
+    if mean is None:
+        mean = torch.empty(c.lead, dtype=torch.float32, device=c.device)
+    if rstd is None:
+        rstd = torch.empty(c.lead, dtype=torch.float32, device=c.device)
+    _check(load().mhla_layernorm_forward(x.data_ptr(), _ptr(weight), _ptr(bias), c.ref, out.data_ptr(),
+                                         mean.data_ptr(), rstd.data_ptr(), _stream_handle(stream, key[2][3])),
            "mhla_layernorm_forward")
     return out, mean, rstd
 
@@ -661,6 +742,22 @@ def mhla_layernorm_backward_workspace_bytes(p: MhlaLayernormParams) -> int:
     return n.value
 
 
+def _norm_backward_call(dy, x, mean, rstd, weight, dx, dweight, dbias, params):
+    import torch
+    p = _norm_params(x, weight, None, 0.0)
+    _, _, p.dy_stride = _norm_rows("dy", dy, x)
+    if dx is not None:
+        _, _, p.y_stride = _norm_rows("dx", dx, x)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _flat(name, t, x, torch.float32, x.shape[:-1])
+    for name, t in (("dweight", dweight), ("dbias", dbias)):
+        if t is not None and not params:
+            raise ValueError(f"{name} needs params=True")
+        _flat(name, t, x, torch.float32, (p.cols,))
+    return _Call(p, mhla_layernorm_backward_workspace_bytes(p) if params else 0, dense=x.is_contiguous(),
+                 cols=p.cols, device=x.device)
+
+
 def mhla_layernorm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, workspace=None,
                             stream=None, params: bool = True):
     """Gradients of mhla_layernorm_forward: ``(dx, dweight, dbias)``.
@@ -670,26 +767,22 @@ def mhla_layernorm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=Non
     ``dx is x`` overwrites that input.
     """
     import torch
-    p = _norm_params(x, weight, None, 0.0)
-    _, _, p.dy_stride = _norm_rows("dy", dy, x)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
-    _, _, p.y_stride = _norm_rows("dx", dx, x)
-    lead = x.shape[:-1]
-    _flat("mean", mean, x, torch.float32, lead)
-    _flat("rstd", rstd, x, torch.float32, lead)
+    key = ("norm backward", params, _sig(dy), _sig(x), _sig(mean), _sig(rstd), _sig(weight), _sig(dx), _sig(dweight),
+           _sig(dbias))
+    c = _CALLS.get(key) or _remember(key, _norm_backward_call(dy, x, mean, rstd, weight, dx, dweight, dbias, params))
+    if dx is None:
+        dx = _fresh(x, c.dense)
     ws_bytes = 0
     if params:
-        dweight = torch.empty(p.cols, dtype=torch.float32, device=x.device) if dweight is None else _flat("dweight", dweight, x, torch.float32, (p.cols,))
-        dbias = torch.empty(p.cols, dtype=torch.float32, device=x.device) if dbias is None else _flat("dbias", dbias, x, torch.float32, (p.cols,))
-        if workspace is None:
-            workspace = torch.empty(max(mhla_layernorm_backward_workspace_bytes(p), 1), dtype=torch.uint8, device=x.device)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    elif dweight is not None or dbias is not None:
-        raise ValueError("dweight and dbias need params=True")
+        if dweight is None:
+            dweight = torch.empty(c.cols, dtype=torch.float32, device=c.device)
+        if dbias is None:
+            dbias = torch.empty(c.cols, dtype=torch.float32, device=c.device)
+        workspace, ws_bytes = c.workspace(workspace, c.device)
     _check(load().mhla_layernorm_backward(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
-                                          ctypes.byref(p), dx.data_ptr(), _ptr(dweight), _ptr(dbias),
+                                          c.ref, dx.data_ptr(), _ptr(dweight), _ptr(dbias),
                                           _ptr(workspace) if params else None, ws_bytes,
-                                          _stream_handle(stream, x.device)), "mhla_layernorm_backward")
+                                          _stream_handle(stream, key[3][3])), "mhla_layernorm_backward")
     return dx, dweight, dbias
 
 
@@ -707,9 +800,7 @@ def _decay_params(q, k, v, log_decay, scale, layout, variant):
     p.batch, p.heads, p.tokens = shape[0], shape[axes[1]], shape[axes[2]]
     p.key_dim, p.value_dim = shape[3], v.shape[3]
     p.dtype = DTYPES[_torch_dtype_name(q)]
-    if variant not in DECAY_VARIANTS:
-        raise ValueError(f"unknown variant {variant!r}; expected one of {sorted(DECAY_VARIANTS)}")
-    p.variant = DECAY_VARIANTS[variant]
+    p.variant = _choice("variant", variant, DECAY_VARIANTS)
     p.scale = scale
     _flat("log_decay", log_decay, q, torch.float32, (p.heads,))
     _set_strides(p.q, q, axes)
@@ -718,22 +809,26 @@ def _decay_params(q, k, v, log_decay, scale, layout, variant):
     return p, axes
 
 
-def _decay_state(name, t, p, like):
+def _decay_side(p, like, lengths, **states):
     import torch
-    return _flat(name, t, like, torch.float32, (p.batch, p.heads, p.key_dim, p.value_dim))
-
-
-def _decay_lengths(lengths, p, like):
-    import torch
-    if lengths is not None:
-        _flat("lengths", lengths, like, torch.int32, (p.batch,))
-    return lengths
+    _flat("lengths", lengths, like, torch.int32, (p.batch,))
+    shape = (p.batch, p.heads, p.key_dim, p.value_dim)
+    for name, t in states.items():
+        _flat(name, t, like, torch.float32, shape)
+    return shape
 
 
 def mhla_decay_workspace_bytes(p: MhlaDecayParams) -> int:
     n = ctypes.c_size_t(0)
     _check(load().mhla_decay_workspace_bytes(ctypes.byref(p), ctypes.byref(n)), "mhla_decay_workspace_bytes")
     return n.value
+
+
+def _decay_forward_call(q, k, v, log_decay, state, lengths, scale, layout, variant, out, state_out):
+    p, axes = _decay_params(q, k, v, log_decay, scale, layout, variant)
+    _set_output(p.out, "out", out, q, v.shape, axes)
+    shape = _decay_side(p, q, lengths, state=state, state_out=state_out)
+    return _Call(p, mhla_decay_workspace_bytes(p), dense=v.is_contiguous(), shape=shape, device=q.device)
 
 
 def mhla_decay_forward(q, k, v, log_decay, state=None, lengths=None, scale: float = 1.0, layout: str = "bhnd",
@@ -748,26 +843,18 @@ def mhla_decay_forward(q, k, v, log_decay, state=None, lengths=None, scale: floa
     [B] for sequences padded to N; rows past a length come out as zeros.
     """
     import torch
-    p, axes = _decay_params(q, k, v, log_decay, scale, layout, variant)
-    out = torch.empty(v.shape, dtype=v.dtype, device=v.device) if out is None else _rows("out", out, q, q.dtype, v.shape)
-    _set_strides(p.out, out, axes)
-    if state is not None:
-        _decay_state("state", state, p, q)
+    key = ("decay", scale, layout, variant, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(state), _sig(lengths),
+           _sig(out), _sig(state_out))
+    c = _CALLS.get(key) or _remember(key, _decay_forward_call(q, k, v, log_decay, state, lengths, scale, layout,
+                                                              variant, out, state_out))
+    if out is None:
+        out = _fresh(v, c.dense)
     if state_out is None:
-        state_out = torch.empty((p.batch, p.heads, p.key_dim, p.value_dim), dtype=torch.float32, device=q.device)
-    else:
-        _decay_state("state_out", state_out, p, q)
-    _decay_lengths(lengths, p, q)
-    ws_bytes = 0
-    if workspace is None:
-        need = mhla_decay_workspace_bytes(p)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    if workspace is not None:
-        ws_bytes = workspace.numel() * workspace.element_size()
+        state_out = torch.empty(c.shape, dtype=torch.float32, device=c.device)
+    workspace, ws_bytes = c.workspace(workspace, c.device)
     _check(load().mhla_decay_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths),
-                                     _ptr(state), ctypes.byref(p), out.data_ptr(), state_out.data_ptr(),
-                                     _ptr(workspace), ws_bytes, _stream_handle(stream, q.device)),
-           "mhla_decay_forward")
+                                     _ptr(state), c.ref, out.data_ptr(), state_out.data_ptr(), _ptr(workspace),
+                                     ws_bytes, _stream_handle(stream, key[4][3])), "mhla_decay_forward")
     return out, state_out
 
 
@@ -776,6 +863,19 @@ def mhla_decay_backward_workspace_bytes(p: MhlaDecayParams) -> int:
     _check(load().mhla_decay_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(n)),
            "mhla_decay_backward_workspace_bytes")
     return n.value
+
+
+def _decay_backward_call(q, k, v, log_decay, dout, state, dstate_out, lengths, scale, layout, variant, dq, dk, dv,
+                         dstate):
+    p, axes = _decay_params(q, k, v, log_decay, scale, layout, variant)
+    _rows("dout", dout, q, q.dtype, v.shape)
+    _set_strides(p.dout, dout, axes)
+    _set_output(p.dq, "dq", dq, q, q.shape, axes)
+    _set_output(p.dk, "dk", dk, q, q.shape, axes)
+    _set_output(p.dv, "dv", dv, q, v.shape, axes)
+    shape = _decay_side(p, q, lengths, state=state, dstate_out=dstate_out, dstate=dstate)
+    return _Call(p, mhla_decay_backward_workspace_bytes(p), q_dense=q.is_contiguous(), k_dense=k.is_contiguous(),
+                 v_dense=v.is_contiguous(), shape=shape, device=q.device)
 
 
 def mhla_decay_backward(q, k, v, log_decay, dout, state=None, dstate_out=None, lengths=None, scale: float = 1.0,
@@ -788,40 +888,24 @@ def mhla_decay_backward(q, k, v, log_decay, dout, state=None, dstate_out=None, l
     [B, H, dk, dv]).  Arguments as in the forward call.
     """
     import torch
-    p, axes = _decay_params(q, k, v, log_decay, scale, layout, variant)
-    _rows("dout", dout, q, q.dtype, v.shape)
-    _set_strides(p.dout, dout, axes)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else _rows("dq", dq, q, q.dtype, q.shape)
-    dk = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dk is None else _rows("dk", dk, q, q.dtype, q.shape)
-    dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else _rows("dv", dv, q, q.dtype, v.shape)
-    _set_strides(p.dq, dq, axes)
-    _set_strides(p.dk, dk, axes)
-    _set_strides(p.dv, dv, axes)
-    for name, t in (("state", state), ("dstate_out", dstate_out), ("dstate", dstate)):
-        if t is not None:
-            _decay_state(name, t, p, q)
+    key = ("decay backward", scale, layout, variant, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(dout),
+           _sig(state), _sig(dstate_out), _sig(lengths), _sig(dq), _sig(dk), _sig(dv), _sig(dstate))
+    c = _CALLS.get(key) or _remember(key, _decay_backward_call(q, k, v, log_decay, dout, state, dstate_out, lengths,
+                                                               scale, layout, variant, dq, dk, dv, dstate))
+    dq = _fresh(q, c.q_dense) if dq is None else dq
+    dk = _fresh(k, c.k_dense) if dk is None else dk
+    dv = _fresh(v, c.v_dense) if dv is None else dv
     if dstate is None:
-        dstate = torch.empty((p.batch, p.heads, p.key_dim, p.value_dim), dtype=torch.float32, device=q.device)
-    _decay_lengths(lengths, p, q)
-    ws_bytes = 0
-    if workspace is None:
-        need = mhla_decay_backward_workspace_bytes(p)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    if workspace is not None:
-        ws_bytes = workspace.numel() * workspace.element_size()
+        dstate = torch.empty(c.shape, dtype=torch.float32, device=c.device)
+    workspace, ws_bytes = c.workspace(workspace, c.device)
     _check(load().mhla_decay_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths),
-                                      _ptr(state), dout.data_ptr(), _ptr(dstate_out), ctypes.byref(p), dq.data_ptr(),
+                                      _ptr(state), dout.data_ptr(), _ptr(dstate_out), c.ref, dq.data_ptr(),
                                       dk.data_ptr(), dv.data_ptr(), dstate.data_ptr(), _ptr(workspace), ws_bytes,
-                                      _stream_handle(stream, q.device)), "mhla_decay_backward")
+                                      _stream_handle(stream, key[4][3])), "mhla_decay_backward")
     return dq, dk, dv, dstate
 
 
-def mhla_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, state_out=None, stream=None):
-    """One token of every sequence: returns ``out`` [B, H, dv].
-
-    q, k: [B, H, dk], v: [B, H, dv]; ``state`` float32 [B, H, dk, dv] is
-    updated in place unless ``state_out`` is given.
-    """
+def _decay_step_call(q, k, v, log_decay, state, scale, out, state_out):
     import torch
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k, v must be [B, H, d]")
@@ -834,12 +918,31 @@ def mhla_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, sta
     p.dtype = DTYPES[_torch_dtype_name(q)]
     p.scale = scale
     _flat("log_decay", log_decay, q, torch.float32, (p.heads,))
-    _decay_state("state", state, p, q)
-    state_out = state if state_out is None else _decay_state("state_out", state_out, p, q)
-    out = torch.empty(v.shape, dtype=v.dtype, device=v.device) if out is None else _rows("out", out, q, q.dtype, v.shape)
-    for field, t in ((p.q, q), (p.k, k), (p.v, v), (p.out, out)):
+    if state is None:
+        raise ValueError("state must be given")
+    _decay_side(p, q, None, state=state, state_out=state_out)
+    for field, t in ((p.q, q), (p.k, k), (p.v, v)):
         field.batch, field.head = t.stride(0), t.stride(1)
-    _check(load().mhla_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(),
-                                  ctypes.byref(p), out.data_ptr(), state_out.data_ptr(),
-                                  _stream_handle(stream, q.device)), "mhla_decay_step")
+    if out is not None:
+        _rows("out", out, q, q.dtype, v.shape)
+        p.out.batch, p.out.head = out.stride(0), out.stride(1)
+    else:
+        p.out.batch, p.out.head = v.shape[1] * v.shape[2], v.shape[2]
+    return _Call(p, dense=v.is_contiguous())
+
+
+def mhla_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, state_out=None, stream=None):
+    """One token of every sequence: returns ``out`` [B, H, dv].
+
+    q, k: [B, H, dk], v: [B, H, dv]; ``state`` float32 [B, H, dk, dv] is
+    updated in place unless ``state_out`` is given.
+    """
+    key = ("decay step", scale, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(state), _sig(out), _sig(state_out))
+    c = _CALLS.get(key) or _remember(key, _decay_step_call(q, k, v, log_decay, state, scale, out, state_out))
+    if out is None:
+        out = _fresh(v, c.dense)
+    at = state.data_ptr()
+    _check(load().mhla_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), at, c.ref,
+                                  out.data_ptr(), at if state_out is None else state_out.data_ptr(),
+                                  _stream_handle(stream, key[2][3])), "mhla_decay_step")
     return out

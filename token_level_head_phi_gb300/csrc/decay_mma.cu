@@ -67,11 +67,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Two bf16 values times their weights, as a high + low pair of bf16.
-__device__ __forceinline__ void scale_split(uint32_t v, float w0, float w1, uint32_t& hi, uint32_t& lo) {
-  const float a = lo_f(v) * w0, b = hi_f(v) * w1;
+// Two bf16 values times their weights, as sums of three bf16 parts (24 bits).
+__device__ __forceinline__ void scale_split(uint32_t v, float w0, float w1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  float a = lo_f(v) * w0, b = hi_f(v) * w1;
   hi = pack2(a, b);
-  lo = pack2(a - lo_f(hi), b - hi_f(hi));
+  a -= lo_f(hi), b -= hi_f(hi);
+  mid = pack2(a, b);
+  lo = pack2(a - lo_f(mid), b - hi_f(mid));
 }
 
 template <int DX, int DZS, bool OUT>
@@ -227,6 +229,8 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
   };
   publish();
   const float2 carry = decay_power(g, C);
+  // a state that ends inside this CTA only feeds outputs rounded to bf16
+  const bool exact = !OUT || (last && p.s_out);
   __syncthreads();
 
   // Weights of a warp's 16 output rows: of the state (two rows a thread), of a
@@ -354,22 +358,36 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
           for (int r = 0; r < 4; ++r) u[m][r] = 0.f;
 #pragma unroll
         for (int k = 0; k < C / 16; ++k) {
-          uint32_t f[4], hi[4], lo[4];
+          uint32_t f[4], hi[4], mid[4], lo[4];
           // (w Y)^T: the transposed load gives rows of x against tokens
           ldsm4t(f, ya + tile_off<DX>(k * 16 + rb, 2 * (own_tile + i * kWarps) + cb));
           const float2 w0 = *reinterpret_cast<const float2*>(&sm.uw[k * 16 + gc]);
           const float2 w1 = *reinterpret_cast<const float2*>(&sm.uw[k * 16 + 8 + gc]);
-          scale_split(f[0], w0.x, w0.y, hi[0], lo[0]);
-          scale_split(f[1], w0.x, w0.y, hi[1], lo[1]);
-          scale_split(f[2], w1.x, w1.y, hi[2], lo[2]);
-          scale_split(f[3], w1.x, w1.y, hi[3], lo[3]);
+          scale_split(f[0], w0.x, w0.y, hi[0], mid[0], lo[0]);
+          scale_split(f[1], w0.x, w0.y, hi[1], mid[1], lo[1]);
+          scale_split(f[2], w1.x, w1.y, hi[2], mid[2], lo[2]);
+          scale_split(f[3], w1.x, w1.y, hi[3], mid[3], lo[3]);
+          // the parts in turn over all columns: consecutive MMAs never share an
+          // accumulator
+          uint32_t zf[kCols][4];
+#pragma unroll
+          for (int m = 0; m < kCols; ++m) ldsm4t(zf[m], za + tile_off<DZS>(k * 16 + ra, 2 * (own_col + m) + ca));
 #pragma unroll
           for (int m = 0; m < kCols; ++m) {
-            ldsm4t(f, za + tile_off<DZS>(k * 16 + ra, 2 * (own_col + m) + ca));
-            mma(u[2 * m], hi, f[0], f[1]);
-            mma(u[2 * m + 1], hi, f[2], f[3]);
-            mma(u[2 * m], lo, f[0], f[1]);
-            mma(u[2 * m + 1], lo, f[2], f[3]);
+            mma(u[2 * m], hi, zf[m][0], zf[m][1]);
+            mma(u[2 * m + 1], hi, zf[m][2], zf[m][3]);
+          }
+#pragma unroll
+          for (int m = 0; m < kCols; ++m) {
+            mma(u[2 * m], mid, zf[m][0], zf[m][1]);
+            mma(u[2 * m + 1], mid, zf[m][2], zf[m][3]);
+          }
+          if (exact) {
+#pragma unroll
+            for (int m = 0; m < kCols; ++m) {
+              mma(u[2 * m], lo, zf[m][0], zf[m][1]);
+              mma(u[2 * m + 1], lo, zf[m][2], zf[m][3]);
+            }
           }
         }
 #pragma unroll
