@@ -11,10 +11,13 @@
 //   U    = (w Y)^T Z            w_j = lambda^(n - j - e), w Y split into two bf16 parts
 //   S    = lambda^n S + U       float32 in registers, lambda^n as high + low parts
 // Roundings to bf16: P and the operand copy of S once each (relative error at
-// most 2^-9 a term, as large as the rounding of the output itself); the state
-// sees none: w Y keeps 16 bits as a high + low pair (rms 5e-7 of a term) and U
-// starts from zero in every chunk, so the tensor cores' truncating additions
-// never run over the long sum.
+// most 2^-8 a term, as large as the rounding of the output itself).  w Y is
+// held as three bf16 parts (24 bits) where a final state comes of it, so that
+// the state is as exact as float32 sums are, and as two (16 bits) where it
+// feeds rounded outputs only; U starts from zero in every chunk, so the tensor
+// cores' truncating additions never run over the long sum.
+#include <type_traits>
+
 #include "common.cuh"
 #include "decay.h"
 #include "ops.h"
@@ -60,6 +63,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The first product of a sum: nothing to add to.
+__device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -67,47 +77,101 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Two bf16 values times their weights, as sums of three bf16 parts (24 bits).
-__device__ __forceinline__ void scale_split(uint32_t v, float w0, float w1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+// Two bf16 values times their weights, as sums of PARTS bf16 parts (8 bits each).
+template <int PARTS>
+__device__ __forceinline__ void scale_split(uint32_t v, float w0, float w1, uint32_t (&o)[PARTS]) {
   float a = lo_f(v) * w0, b = hi_f(v) * w1;
-  hi = pack2(a, b);
-  a -= lo_f(hi), b -= hi_f(hi);
-  mid = pack2(a, b);
-  lo = pack2(a - lo_f(mid), b - hi_f(mid));
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    o[i] = pack2(a, b);
+    a -= lo_f(o[i]), b -= hi_f(o[i]);
+  }
+}
+
+__device__ __forceinline__ void stsm4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
+// Transposes the 4 x 4 words that four neighbouring lanes hold: lane c's word
+// i becomes lane i's word c.
+__device__ __forceinline__ void quad_transpose(uint32_t (&v)[4], int lane) {
+  const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const uint32_t t = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[i + 1], 1);
+    if (odd) v[i] = t;
+    else v[i + 1] = t;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t t = __shfl_xor_sync(0xffffffffu, high ? v[i] : v[i + 2], 2);
+    if (high) v[i] = t;
+    else v[i + 2] = t;
+  }
 }
 
 template <int DX, int DZS, bool OUT>
 struct alignas(16) MmaSmem {
-  __nv_bfloat16 x[OUT ? 2 : 1][OUT ? C * DX : 8];
+  __nv_bfloat16 x[OUT ? C * DX : 8];
   __nv_bfloat16 y[2][C * DX];
   __nv_bfloat16 z[2][C * DZS];
-  __nv_bfloat16 s[OUT ? DX * DZS : 8];
-  __nv_bfloat16 o[OUT && DX < DZS ? C * DZS : 8];
-  float uw[C];      // weights of the chunk's tokens in the state
+  __nv_bfloat16 s[2][OUT ? DX * DZS : 8];
+  float4 wt[OUT ? 4 : 1][OUT ? 32 : 1];  // a lane's weights of a 16 x 16 score tile: off (2), on (2) the diagonal
+  float uw[2][C];   // weights of the chunk's tokens in the state: full chunks, the last one
   float pw[C + 1];  // lambda^n
 };
 
-// A chunk's rows of one tensor into a tile; rows from n on are zeros.
-template <int D>
-__device__ __forceinline__ void load_tile(__nv_bfloat16* tile, const __nv_bfloat16* first, int64_t step, int n,
-                                          bool vec) {
-  constexpr int kPieces = D / 8;
-  const uint32_t base = smem_addr(tile);
-#pragma unroll
-  for (int i = threadIdx.x; i < C * kPieces; i += kThreads) {
-    const int r = i / kPieces, piece = i % kPieces;
-    const __nv_bfloat16* src = first + (r < n ? r * step : 0) + piece * 8;
-    const uint32_t dst = base + tile_off<D>(r, piece);
-    if (vec) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(r < n ? 16 : 0) : "memory");
-    } else {
-      alignas(16) __nv_bfloat16 v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = r < n ? src[j] : __float2bfloat16_rn(0.f);
-      *reinterpret_cast<uint4*>(reinterpret_cast<char*>(tile) + tile_off<D>(r, piece)) = *reinterpret_cast<uint4*>(v);
-    }
+// Copies ROWS rows of chunk after chunk of one tensor into tiles, by THREADS
+// threads; rows from n on are zeros.  A thread takes the same 16-byte piece of
+// every STEP-th row.
+template <int D, int ROWS, int THREADS>
+struct RowLoader {
+  static constexpr int kPieces = D / 8;
+  static constexpr int kStep = THREADS / kPieces;  // rows taken at a time
+  static constexpr int kTurns = ROWS / kStep;
+  static_assert(THREADS % kPieces == 0 && ROWS % kStep == 0, "");
+  const __nv_bfloat16* src;  // this thread's piece of its first row
+  int64_t step;              // elements from token to token of the pass
+  int row, piece;
+
+  __device__ __forceinline__ void init(const __nv_bfloat16* first, int64_t token_step, int r0, int thread) {
+    row = r0 + thread / kPieces;
+    piece = thread % kPieces;
+    step = token_step;
+    src = first + row * token_step + piece * 8;
   }
-}
+  __device__ __forceinline__ void load(__nv_bfloat16* tile, int n, bool vec) {
+    const __nv_bfloat16* at = src;
+    if (vec && n == C) {
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        const uint32_t dst = smem_addr(tile) + tile_off<D>(row + i * kStep, piece);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(at) : "memory");
+        at += kStep * step;
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kTurns; ++i) {
+        const int r = row + i * kStep;
+        const bool live = r < n;
+        alignas(16) __nv_bfloat16 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __float2bfloat16_rn(0.f);
+        if (live && vec) {
+          *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(at);
+        } else if (live) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = at[j];
+        }
+        *reinterpret_cast<uint4*>(reinterpret_cast<char*>(tile) + tile_off<D>(r, piece)) = *reinterpret_cast<uint4*>(v);
+        at += kStep * step;
+      }
+    }
+    src += C * step;
+  }
+};
 
 // OUT: the pass itself; otherwise only the segment's own final state.
 template <int DX, int DZS, bool OUT>
@@ -143,26 +207,38 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
   float* segs = p.seg + (p.nseg > 1 ? (int64_t)unit * p.nseg * one : 0);
   const bool vec = p.vec != 0;
 
+  RowLoader<DX, C, kThreads> ly;
+  RowLoader<DZS, C, kThreads> lz;
+  ly.init(y, sign * p.sy.token, 0, tid);
+  lz.init(z, sign * p.sz.token, 0, tid);
   auto fetch = [&](int c0) {
     const int st = (c0 / C) & 1, n = min(C, valid - c0);
-    if (OUT) load_tile<DX>(sm.x[OUT ? st : 0], x + sign * c0 * p.sx.token, sign * p.sx.token, n, vec);
-    load_tile<DX>(sm.y[st], y + sign * c0 * p.sy.token, sign * p.sy.token, n, vec);
-    load_tile<DZS>(sm.z[st], z + sign * c0 * p.sz.token, sign * p.sz.token, n, vec);
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    ly.load(sm.y[st], n, vec);
+    lz.load(sm.z[st], n, vec);
   };
-  if (valid > 0) fetch(0);
+  // x has one buffer: the warp that has read a row tile refills it
+  auto fetch_x = [&](int c0, int tile) {
+    RowLoader<DX, 16, 32> lx;
+    lx.init(x + sign * c0 * p.sx.token, sign * p.sx.token, tile * 16, lane);
+    lx.load(sm.x, min(C, valid - c0), vec);
+  };
+  if (valid > 0) {
+    fetch(0);
+    if (OUT) fetch_x(0, warp);
+  }
 
   if (tid <= C) {
     const float2 w = decay_power(g, tid);
     sm.pw[tid] = w.x + w.y;
   }
-  auto token_weights = [&](int n) {  // of a chunk of n tokens
-    if (tid < C) {
-      const float2 w = decay_power(g, max(0, n - tid - p.e));
-      sm.uw[tid] = (w.x + w.y) * p.update;
+  if (tid < C) {
+    const int ends[2] = {C, valid % C};  // tokens of a full chunk and of a part of one
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 w = decay_power(g, max(0, ends[i] - tid - p.e));
+      sm.uw[i][tid] = (w.x + w.y) * p.update;
     }
-  };
-  token_weights(min(C, valid));
+  }
 
   // the state before the segment.  s_in may be overwritten by the last
   // segment's CTA, so with several segments the second launch reads the copy
@@ -214,70 +290,77 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
           }
     }
   }
-  auto publish = [&]() {  // the operand copy of the state
+  // addresses inside a 16 x 16 block for ldmatrix / stmatrix: rows are the
+  // first 8 / last 8 in lanes 0-7, 16-23 / 8-15, 24-31 for A (and for
+  // transposed B and accumulators), columns the other way round for B
+  const int ra = (lane & 7) + ((lane >> 3) & 1) * 8, ca = lane >> 4;
+  const int rb = (lane & 7) + (lane >> 4) * 8, cb = (lane >> 3) & 1;
+  auto publish = [&](int at) {  // an operand copy of the state
     if (!OUT || !owner) return;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
 #pragma unroll
-      for (int n8 = 0; n8 < 2 * kCols; ++n8)
-#pragma unroll
-        for (int r = 0; r < 4; r += 2) {
-          const int2 at = entry(i, n8, r);
-          const uint32_t off = tile_off<DZS>(at.x, at.y / 8) + (at.y % 8) * 2;
-          *reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(sm.s) + off) = pack2(s[i][n8][r], s[i][n8][r + 1]);
-        }
+      for (int m = 0; m < kCols; ++m) {
+        const float(&a)[4] = s[i][2 * m];
+        const float(&c)[4] = s[i][2 * m + 1];
+        stsm4(smem_addr(sm.s[at]) + tile_off<DZS>((own_tile + i * kWarps) * 16 + ra, 2 * (own_col + m) + ca),
+              pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(c[0], c[1]), pack2(c[2], c[3]));
+      }
   };
-  publish();
+  publish(0);
   const float2 carry = decay_power(g, C);
-  // a state that ends inside this CTA only feeds outputs rounded to bf16
-  const bool exact = !OUT || (last && p.s_out);
+  // Where no final state comes of it, a state feeds outputs rounded to bf16
+  // only: two parts (16 bits) are plenty.  A final state takes three.
+  const bool exact = p.s_out && (!OUT || last);
   __syncthreads();
 
-  // Weights of a warp's 16 output rows: of the state (two rows a thread), of a
-  // tile on the diagonal (0 above it) and, for the others, lambda^(16 + t - j)
-  // to be multiplied by lambda^(16 (tiles in between)).
-  float read0 = 0.f, read1 = 0.f, on[8], off[8];
+  // Weights of a score tile's entries, the same for every warp: on the diagonal
+  // (0 above it), and lambda^(16 + t - j) for the others, to be multiplied by
+  // lambda^(16 (tiles in between)).
   if (OUT) {
-    read0 = sm.pw[warp * 16 + gr + p.e] * p.read;
-    read1 = sm.pw[warp * 16 + gr + 8 + p.e] * p.read;
+    float w[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      // entry k: n8 tile k / 4, row half (k / 2) % 2, column k % 2
-      const int d = gr + ((k >> 1) & 1) * 8 - ((k >> 2) * 8 + gc + (k & 1));
-      on[k] = d >= 0 ? sm.pw[d] * p.score : 0.f;
-      off[k] = sm.pw[16 + d] * p.score;
+    for (int k = 0; k < 4; ++k) {  // warp: off, off, on, on; n8 tile warp & 1, row half k / 2, column k & 1
+      const int d = gr + (k >> 1) * 8 - ((warp & 1) * 8 + gc + (k & 1));
+      w[k] = warp < 2 ? sm.pw[16 + d] * p.score : d >= 0 ? sm.pw[d] * p.score : 0.f;
     }
+    sm.wt[OUT ? warp : 0][OUT ? lane : 0] = make_float4(w[0], w[1], w[2], w[3]);
+    static_assert(kWarps == 4, "");
   }
-  // addresses inside a 16 x 16 block for ldmatrix: rows are the first 8 / last
-  // 8 in lanes 0-7, 16-23 / 8-15, 24-31 for A (and for transposed B), columns
-  // the other way round for B
-  const int ra = (lane & 7) + ((lane >> 3) & 1) * 8, ca = lane >> 4;
-  const int rb = (lane & 7) + (lane >> 4) * 8, cb = (lane >> 3) & 1;
 
   for (int c0 = 0; c0 < valid; c0 += C) {
     const int n = min(C, valid - c0), st = (c0 / C) & 1;
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    __syncthreads();  // the chunk's rows and the state's copy are there
+    // The one barrier of a chunk: its rows and the state's copy are there, and
+    // the buffers of the chunk before are free.
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    // Row tile t has t + 1 score tiles; each warp takes another one in every
+    // chunk, so that the four schedulers of an SM get the same work.
+    const int rt = (warp + (c0 / C)) % kWarps;
     if (c0 + C < valid) fetch(c0 + C);
     const uint32_t ya = smem_addr(sm.y[st]), za = smem_addr(sm.z[st]);
     if (OUT) {
-      const uint32_t xa = smem_addr(sm.x[OUT ? st : 0]), sa = smem_addr(sm.s);
+      const uint32_t xa = smem_addr(sm.x), sa = smem_addr(sm.s[st]);
       uint32_t xf[kTiles][4];
 #pragma unroll
-      for (int k = 0; k < kTiles; ++k) ldsm4(xf[k], xa + tile_off<DX>(warp * 16 + ra, 2 * k + ca));
+      for (int k = 0; k < kTiles; ++k) ldsm4(xf[k], xa + tile_off<DX>(rt * 16 + ra, 2 * k + ca));
+      __syncwarp();
+      if (c0 + C < valid) fetch_x(c0 + C, rt);
+      const float read0 = sm.pw[rt * 16 + gr + p.e] * p.read, read1 = sm.pw[rt * 16 + gr + 8 + p.e] * p.read;
       float acc[2 * kZ16][4];
-#pragma unroll
-      for (int i = 0; i < 2 * kZ16; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][r] = 0.f;
 #pragma unroll
       for (int k = 0; k < kTiles; ++k)
 #pragma unroll
         for (int m = 0; m < kZ16; ++m) {
           uint32_t f[4];
           ldsm4t(f, sa + tile_off<DZS>(k * 16 + ra, 2 * m + ca));
-          mma(acc[2 * m], xf[k], f[0], f[1]);
-          mma(acc[2 * m + 1], xf[k], f[2], f[3]);
+          if (k == 0) {
+            mma0(acc[2 * m], xf[k], f[0], f[1]);
+            mma0(acc[2 * m + 1], xf[k], f[2], f[3]);
+          } else {
+            mma(acc[2 * m], xf[k], f[0], f[1]);
+            mma(acc[2 * m + 1], xf[k], f[2], f[3]);
+          }
         }
 #pragma unroll
       for (int i = 0; i < 2 * kZ16; ++i) {
@@ -286,27 +369,36 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
         acc[i][2] *= read1;
         acc[i][3] *= read1;
       }
-      for (int jt = 0; jt <= warp; ++jt) {
-        float d[2][4] = {};
+      #pragma unroll 2
+      for (int jt = 0; jt <= rt; ++jt) {
+        float d[2][4];
 #pragma unroll
         for (int k = 0; k < kTiles; ++k) {
           uint32_t f[4];
           ldsm4(f, ya + tile_off<DX>(jt * 16 + rb, 2 * k + cb));
-          mma(d[0], xf[k], f[0], f[1]);
-          mma(d[1], xf[k], f[2], f[3]);
+          if (k == 0) {
+            mma0(d[0], xf[k], f[0], f[1]);
+            mma0(d[1], xf[k], f[2], f[3]);
+          } else {
+            mma(d[0], xf[k], f[0], f[1]);
+            mma(d[1], xf[k], f[2], f[3]);
+          }
         }
         uint32_t pf[4];
-        if (jt == warp) {
+        const int table = jt == rt ? 2 : 0;
+        const float4 wa = sm.wt[OUT ? table : 0][OUT ? lane : 0], wb = sm.wt[OUT ? table + 1 : 0][OUT ? lane : 0];
+        const float wk[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+        if (jt == rt) {
           // masked entries are dropped by selection: their scores may be infinite
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int dist = gr + ((k >> 1) & 1) * 8 - ((k >> 2) * 8 + gc + (k & 1));
-            d[k >> 2][k & 3] = dist >= 0 ? d[k >> 2][k & 3] * on[k] : 0.f;
+            d[k >> 2][k & 3] = dist >= 0 ? d[k >> 2][k & 3] * wk[k] : 0.f;
           }
         } else {
-          const float f = sm.pw[16 * (warp - jt - 1)];
+          const float f = sm.pw[16 * (rt - jt - 1)];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) d[k >> 2][k & 3] *= off[k] * f;
+          for (int k = 0; k < 8; ++k) d[k >> 2][k & 3] *= wk[k] * f;
         }
         pf[0] = pack2(d[0][0], d[0][1]);
         pf[1] = pack2(d[0][2], d[0][3]);
@@ -320,73 +412,73 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
           mma(acc[2 * m + 1], pf, f[2], f[3]);
         }
       }
-      // rows to memory through this warp's own rows of a shared tile
-      __syncwarp();
-      constexpr bool kOwnTile = DX < DZS;
-      char* os = reinterpret_cast<char*>(kOwnTile ? sm.o : sm.x[OUT ? st : 0]) + (kOwnTile ? 0 : warp * 16 * (DX - DZS) * 2);
+      // Rows to memory: four lanes hold two columns each of every 8-column
+      // piece of a row; a 4 x 4 exchange gives each lane a whole piece.
 #pragma unroll
-      for (int i = 0; i < 2 * kZ16; ++i) {
-        *reinterpret_cast<uint32_t*>(os + tile_off<DZS>(warp * 16 + gr, i) + gc * 2) = pack2(acc[i][0], acc[i][1]);
-        *reinterpret_cast<uint32_t*>(os + tile_off<DZS>(warp * 16 + gr + 8, i) + gc * 2) = pack2(acc[i][2], acc[i][3]);
-      }
-      __syncwarp();
-      constexpr int kPieces = DZS / 8;
+      for (int half = 0; half < 2; ++half) {
+        const int r = rt * 16 + gr + half * 8;
+        T* row = o + decay_token(p, begin + c0 + r, length) * p.so.token;
 #pragma unroll
-      for (int i = lane; i < 16 * kPieces; i += 32) {
-        const int r = warp * 16 + i / kPieces, piece = i % kPieces;
-        if (r >= n) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(os + tile_off<DZS>(r, piece));
-        T* dst = o + decay_token(p, begin + c0 + r, length) * p.so.token + piece * 8;
-        if (vec) {
-          __stcs(reinterpret_cast<uint4*>(dst), v);
-        } else {
-          const T* e = reinterpret_cast<const T*>(&v);
+        for (int q = 0; q < (2 * kZ16 + 3) / 4; ++q) {
+          uint32_t v[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dst[j] = e[j];
+          for (int i = 0; i < 4; ++i)
+            v[i] = 4 * q + i < 2 * kZ16 ? pack2(acc[(4 * q + i) % (2 * kZ16)][2 * half], acc[(4 * q + i) % (2 * kZ16)][2 * half + 1]) : 0;
+          quad_transpose(v, lane);
+          const int piece = 4 * q + (lane & 3);
+          if (r >= n || piece >= 2 * kZ16) continue;
+          if (vec) {
+            __stcs(reinterpret_cast<uint4*>(row + piece * 8), make_uint4(v[0], v[1], v[2], v[3]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              row[piece * 8 + 2 * j] = __float2bfloat16_rn(lo_f(v[j]));
+              row[piece * 8 + 2 * j + 1] = __float2bfloat16_rn(hi_f(v[j]));
+            }
+          }
         }
       }
     }
     // U of each row tile, then the state
     const float2 w = n == C ? carry : decay_power(g, n);
-    if (owner) {
+    auto update = [&](auto parts) {
+      constexpr int kParts = decltype(parts)::value;
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
         float u[2 * kCols][4];
 #pragma unroll
-        for (int m = 0; m < 2 * kCols; ++m)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) u[m][r] = 0.f;
-#pragma unroll
         for (int k = 0; k < C / 16; ++k) {
-          uint32_t f[4], hi[4], mid[4], lo[4];
+          uint32_t f[4], wy[4][kParts];
           // (w Y)^T: the transposed load gives rows of x against tokens
           ldsm4t(f, ya + tile_off<DX>(k * 16 + rb, 2 * (own_tile + i * kWarps) + cb));
-          const float2 w0 = *reinterpret_cast<const float2*>(&sm.uw[k * 16 + gc]);
-          const float2 w1 = *reinterpret_cast<const float2*>(&sm.uw[k * 16 + 8 + gc]);
-          scale_split(f[0], w0.x, w0.y, hi[0], mid[0], lo[0]);
-          scale_split(f[1], w0.x, w0.y, hi[1], mid[1], lo[1]);
-          scale_split(f[2], w1.x, w1.y, hi[2], mid[2], lo[2]);
-          scale_split(f[3], w1.x, w1.y, hi[3], mid[3], lo[3]);
-          // the parts in turn over all columns: consecutive MMAs never share an
-          // accumulator
-          uint32_t zf[kCols][4];
+          const float2 w0 = *reinterpret_cast<const float2*>(&sm.uw[n < C][k * 16 + gc]);
+          const float2 w1 = *reinterpret_cast<const float2*>(&sm.uw[n < C][k * 16 + 8 + gc]);
+          scale_split<kParts>(f[0], w0.x, w0.y, wy[0]);
+          scale_split<kParts>(f[1], w0.x, w0.y, wy[1]);
+          scale_split<kParts>(f[2], w1.x, w1.y, wy[2]);
+          scale_split<kParts>(f[3], w1.x, w1.y, wy[3]);
+          // 32 columns at a time, the parts in turn over all of them, so that
+          // consecutive MMAs do not share an accumulator
+          constexpr int kHalf = kCols > 2 ? 2 : kCols;
 #pragma unroll
-          for (int m = 0; m < kCols; ++m) ldsm4t(zf[m], za + tile_off<DZS>(k * 16 + ra, 2 * (own_col + m) + ca));
+          for (int m0 = 0; m0 < kCols; m0 += kHalf) {
+            uint32_t zf[kHalf][4];
 #pragma unroll
-          for (int m = 0; m < kCols; ++m) {
-            mma(u[2 * m], hi, zf[m][0], zf[m][1]);
-            mma(u[2 * m + 1], hi, zf[m][2], zf[m][3]);
-          }
+            for (int m = 0; m < kHalf; ++m)
+              ldsm4t(zf[m], za + tile_off<DZS>(k * 16 + ra, 2 * (own_col + m0 + m) + ca));
 #pragma unroll
-          for (int m = 0; m < kCols; ++m) {
-            mma(u[2 * m], mid, zf[m][0], zf[m][1]);
-            mma(u[2 * m + 1], mid, zf[m][2], zf[m][3]);
-          }
-          if (exact) {
+            for (int q = 0; q < kParts; ++q) {
+              const uint32_t part[4] = {wy[0][q], wy[1][q], wy[2][q], wy[3][q]};
 #pragma unroll
-            for (int m = 0; m < kCols; ++m) {
-              mma(u[2 * m], lo, zf[m][0], zf[m][1]);
-              mma(u[2 * m + 1], lo, zf[m][2], zf[m][3]);
+              for (int m = 0; m < kHalf; ++m) {
+                if (k == 0 && q == 0) {
+                  mma0(u[2 * (m0 + m)], part, zf[m][0], zf[m][1]);
+                  mma0(u[2 * (m0 + m) + 1], part, zf[m][2], zf[m][3]);
+                } else {
+                  mma(u[2 * (m0 + m)], part, zf[m][0], zf[m][1]);
+                  mma(u[2 * (m0 + m) + 1], part, zf[m][2], zf[m][3]);
+                }
+              }
             }
           }
         }
@@ -395,11 +487,14 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
 #pragma unroll
           for (int r = 0; r < 4; ++r) s[i][m][r] = fmaf(s[i][m][r], w.x, fmaf(s[i][m][r], w.y, u[m][r]));
       }
+    };
+    if (owner) {
+      if (exact)
+        update(std::integral_constant<int, 3>());
+      else
+        update(std::integral_constant<int, 2>());
     }
-    __syncthreads();  // every warp has read the chunk and the state's copy
-    publish();
-    const int rest = valid - c0 - C;
-    if (rest > 0 && rest < C) token_weights(rest);
+    publish(st ^ 1);
   }
 
   if (OUT) {
