@@ -34,10 +34,11 @@ struct DecayPass {
   const int32_t* lengths;
   const float* s_in;  // [units][DX][DZ], or its transpose (s_ldx, s_ldz); may be null
   float* s_out;       // same layout; may be null, may be s_in
-  float* seg;         // [units][nseg][DX][DZ] segment states (nseg > 1)
-  int s_ldx, s_ldz;   // element strides of a state's x and z axes
+  float* seg;         // [units][nseg][DX * DZ] segment states (nseg > 1)
+  int s_ldx, s_ldz;   // element strides of a state's x and z axes, in s_in, s_out and seg
   int B, H, N, DX, DZ;
   int nseg, seg_len;
+  int launches;  // 1: the segments' own states, 2: the pass itself, 3: both
   int reverse;  // 1: token i of the pass is the sequence's token length - 1 - i
   int e;
   float score, read, update;

@@ -70,6 +70,7 @@ DecayPass pass_of(const mhla_decay_params* p, int dx, int dz) {
   a.DX = dx;
   a.DZ = dz;
   plan_segments(p, dx, dz, &a.nseg, &a.seg_len);
+  a.launches = 3;
   return a;
 }
 
@@ -221,14 +222,8 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
   a.update = 1.f;
   cudaError_t e = launch_pass(a, p, s);
 
-  set_rows(a, in[2], p->v, in[3], p->dout, in[0], p->q, out[1], p->dk);
-  a.s_in = dstate_out;
-  a.reverse = 1;
-  a.e = 0;
-  a.read = 1.f;
-  a.update = p->scale;
-  if (e == cudaSuccess) e = launch_pass(a, p, s);
-
+  // dk and dv carry the same states, transposed: the segments' own are formed
+  // once, in dv's orientation.
   DecayPass c = pass_of(p, dkey, dval);  // dv, and the gradient of the first state
   set_rows(c, in[1], p->k, in[0], p->q, in[3], p->dout, out[2], p->dv);
   c.g = log_decay;
@@ -243,6 +238,18 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
   c.score = p->scale;
   c.read = 1.f;
   c.update = p->scale;
+  DecayPass b = c;  // dk
+  b.DX = dval;
+  b.DZ = dkey;
+  set_rows(b, in[2], p->v, in[3], p->dout, in[0], p->q, out[1], p->dk);
+  b.s_out = nullptr;
+  b.s_ldx = 1;
+  b.s_ldz = dval;
+  b.launches = 2;
+  c.launches = 1;
+  if (e == cudaSuccess) e = launch_pass(c, p, s);
+  if (e == cudaSuccess) e = launch_pass(b, p, s);
+  c.launches = 2;
   if (e == cudaSuccess) e = launch_pass(c, p, s);
   return scratch.give_back(e == cudaSuccess ? MHLA_OK : record_cuda_error(e));
 }

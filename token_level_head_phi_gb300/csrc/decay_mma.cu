@@ -264,11 +264,12 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int2 at = entry(i, n8, r);
-          const int64_t slot = (p.nseg - 1) * one + (int64_t)at.x * p.DZ + z0 + at.y;
+          const int64_t in = (int64_t)at.x * p.s_ldx + (int64_t)(z0 + at.y) * p.s_ldz;
+          const int64_t slot = (p.nseg - 1) * one + in;
           if (OUT && p.nseg > 1) {
             s[i][n8][r] = segs[slot];
           } else {
-            s[i][n8][r] = p.s_in[state + (int64_t)at.x * p.s_ldx + (int64_t)(z0 + at.y) * p.s_ldz];
+            s[i][n8][r] = p.s_in[state + in];
             if (!OUT) segs[slot] = s[i][n8][r];
           }
         }
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
   if (OUT && owner && valid > 0) {
     for (int q = 0; q < seg; ++q) {
       const float2 w = decay_power(g, (seg - 1 - q) * p.seg_len);
-      const float* u = segs + q * one + z0;
+      const float* u = segs + q * one;
 #pragma unroll
       for (int i = 0; i < kOwn; ++i)
 #pragma unroll
@@ -284,7 +285,8 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
 #pragma unroll
           for (int r = 0; r < 4; r += 2) {
             const int2 at = entry(i, n8, r);
-            const float2 v = *reinterpret_cast<const float2*>(u + (int64_t)at.x * p.DZ + at.y);
+            const float* f = u + (int64_t)at.x * p.s_ldx + (int64_t)(z0 + at.y) * p.s_ldz;
+            const float2 v = p.s_ldz == 1 ? *reinterpret_cast<const float2*>(f) : make_float2(f[0], f[p.s_ldz]);
             s[i][n8][r] = fmaf(v.x, w.x, fmaf(v.x, w.y, s[i][n8][r]));
             s[i][n8][r + 1] = fmaf(v.y, w.x, fmaf(v.y, w.y, s[i][n8][r + 1]));
           }
@@ -512,10 +514,11 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int2 at = entry(i, n8, r);
+        const int64_t in = (int64_t)at.x * p.s_ldx + (int64_t)(z0 + at.y) * p.s_ldz;
         if (OUT)
-          p.s_out[state + (int64_t)at.x * p.s_ldx + (int64_t)(z0 + at.y) * p.s_ldz] = s[i][n8][r];
+          p.s_out[state + in] = s[i][n8][r];
         else
-          segs[seg * one + (int64_t)at.x * p.DZ + z0 + at.y] = s[i][n8][r];
+          segs[seg * one + in] = s[i][n8][r];
       }
 }
 
@@ -523,7 +526,7 @@ template <int DX, int DZS>
 cudaError_t run(const DecayPass& p, cudaStream_t s) {
   const unsigned units = (unsigned)(p.B * p.H), slices = (unsigned)(p.DZ / DZS);
   cudaError_t e;
-  if (p.nseg > 1) {
+  if (p.nseg > 1 && (p.launches & 1)) {
     constexpr int smem = (int)sizeof(MmaSmem<DX, DZS, false>);
     auto* k = decay_mma_kernel<DX, DZS, false>;
     if (smem > 48 * 1024 &&
@@ -532,6 +535,7 @@ cudaError_t run(const DecayPass& p, cudaStream_t s) {
     k<<<dim3(units, (unsigned)(p.nseg - 1), slices), kThreads, smem, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
+  if (!(p.launches & 2)) return cudaSuccess;
   constexpr int smem = (int)sizeof(MmaSmem<DX, DZS, true>);
   auto* k = decay_mma_kernel<DX, DZS, true>;
   if (smem > 48 * 1024 &&

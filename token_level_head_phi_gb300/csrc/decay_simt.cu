@@ -67,10 +67,10 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const DecayPass p)
   const bool copied = OUT && p.nseg > 1;
   for (int i = tid; i < DX * DZS; i += kThreads) {
     const int a = i / DZS, c = i % DZS;
-    const int64_t at = (int64_t)a * p.DZ + z0 + c;
+    const int64_t at = (int64_t)a * p.s_ldx + (int64_t)(z0 + c) * p.s_ldz;
     float s = 0.f;
     if (seg == 0 && p.s_in) {
-      s = copied ? segs[(p.nseg - 1) * one + at] : p.s_in[state + (int64_t)a * p.s_ldx + (int64_t)(z0 + c) * p.s_ldz];
+      s = copied ? segs[(p.nseg - 1) * one + at] : p.s_in[state + at];
       if (!OUT) segs[(p.nseg - 1) * one + at] = s;
     }
     if (OUT && valid > 0)
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const DecayPass p)
   } else if (valid > 0) {
     for (int i = tid; i < DX * DZS; i += kThreads) {
       const int a = i / DZS, c = i % DZS;
-      segs[seg * one + (int64_t)a * p.DZ + z0 + c] = sm.s[a][c];
+      segs[seg * one + (int64_t)a * p.s_ldx + (int64_t)(z0 + c) * p.s_ldz] = sm.s[a][c];
     }
   }
 }
@@ -188,7 +188,7 @@ cudaError_t run(const DecayPass& p, cudaStream_t s) {
   constexpr int smem = (int)sizeof(SimtSmem<DX, DZS>);
   const unsigned units = (unsigned)(p.B * p.H), slices = (unsigned)(p.DZ / DZS);
   cudaError_t e;
-  if (p.nseg > 1) {
+  if (p.nseg > 1 && (p.launches & 1)) {
     auto* k = decay_simt_kernel<T, DX, DZS, false>;
     if (smem > 48 * 1024 &&
         (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
@@ -196,6 +196,7 @@ cudaError_t run(const DecayPass& p, cudaStream_t s) {
     k<<<dim3(units, (unsigned)(p.nseg - 1), slices), kThreads, smem, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
+  if (!(p.launches & 2)) return cudaSuccess;
   auto* k = decay_simt_kernel<T, DX, DZS, true>;
   if (smem > 48 * 1024 &&
       (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)

@@ -1,9 +1,9 @@
 // One token of linear attention with a decay for each head:
 //   S = lambda S_in + k v^T,  o = scale S^T q.
 // Bound: reading and writing the float32 state, 8 key_dim value_dim bytes a
-// head.  One CTA per (batch, head); a thread takes four columns of a share of
-// the rows, all its loads in flight at once, and the column sums meet through
-// shuffles and one exchange in shared memory.
+// head.  One small CTA per (batch, head) and 32 columns: a thread takes four
+// columns of a share of the rows, all its loads in flight at once, and the
+// column sums meet through shuffles and one exchange in shared memory.
 #include "common.cuh"
 #include "decay.h"
 #include "ops.h"
@@ -11,27 +11,30 @@
 namespace mhla {
 namespace {
 
+template <int DV>
+constexpr int step_slice = DV < 32 ? DV : 32;  // columns of a CTA
 template <int DK, int DV>
-constexpr int step_threads = DK * DV / 4 < 256 ? DK * DV / 4 : 256;
+constexpr int step_threads = DK * step_slice<DV> / 4 < 128 ? DK * step_slice<DV> / 4 : 128;
 
 template <typename T, int DK, int DV>
 __global__ void __launch_bounds__(step_threads<DK, DV>) decay_step_kernel(const DecayPass p) {
+  constexpr int kSlice = step_slice<DV>;
   constexpr int kThreads = step_threads<DK, DV>;
-  constexpr int kCols = DV / 4;             // threads across a row
-  constexpr int kRows = kThreads / kCols;   // rows taken at a time
-  constexpr int kPer = DK / kRows;          // rows of a thread
+  constexpr int kCols = kSlice / 4;        // threads across a row
+  constexpr int kRows = kThreads / kCols;  // rows taken at a time
+  constexpr int kPer = DK / kRows;         // rows of a thread
   constexpr int kWarps = kThreads / 32;
-  __shared__ float sums[kWarps][DV];
-  const int unit = blockIdx.x, b = unit / p.H, h = unit % p.H;
+  __shared__ float sums[kWarps][kSlice];
+  const int unit = blockIdx.x, b = unit / p.H, h = unit % p.H, c0 = blockIdx.y * kSlice;
   const int col = threadIdx.x % kCols, row = threadIdx.x / kCols;
-  const float4* s_in = reinterpret_cast<const float4*>(p.s_in + (int64_t)unit * DK * DV) + threadIdx.x;
-  float4* s_out = reinterpret_cast<float4*>(p.s_out + (int64_t)unit * DK * DV) + threadIdx.x;
+  const int64_t first = (int64_t)unit * DK * DV + row * DV + c0 + 4 * col;
   float4 s[kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) s[i] = p.s_in ? s_in[i * kThreads] : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < kPer; ++i) 
+    s[i] = p.s_in ? *reinterpret_cast<const float4*>(p.s_in + first + i * kRows * DV) : make_float4(0.f, 0.f, 0.f, 0.f);
   const T* q = static_cast<const T*>(p.x) + b * p.sx.batch + h * p.sx.head;
   const T* k = static_cast<const T*>(p.y) + b * p.sy.batch + h * p.sy.head;
-  const T* v = static_cast<const T*>(p.z) + b * p.sz.batch + h * p.sz.head + 4 * col;
+  const T* v = static_cast<const T*>(p.z) + b * p.sz.batch + h * p.sz.head + c0 + 4 * col;
   const float v0 = to_f32(v[0]), v1 = to_f32(v[1]), v2 = to_f32(v[2]), v3 = to_f32(v[3]);
   const float2 w = decay_power(p.g[h], 1);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -43,7 +46,7 @@ __global__ void __launch_bounds__(step_threads<DK, DV>) decay_step_kernel(const 
     t.y = fmaf(t.y, w.x, fmaf(t.y, w.y, kk * v1));
     t.z = fmaf(t.z, w.x, fmaf(t.z, w.y, kk * v2));
     t.w = fmaf(t.w, w.x, fmaf(t.w, w.y, kk * v3));
-    if (p.s_out) s_out[i * kThreads] = t;
+    if (p.s_out) *reinterpret_cast<float4*>(p.s_out + first + i * kRows * DV) = t;
     o.x = fmaf(qq, t.x, o.x);
     o.y = fmaf(qq, t.y, o.y);
     o.z = fmaf(qq, t.z, o.z);
@@ -58,21 +61,25 @@ __global__ void __launch_bounds__(step_threads<DK, DV>) decay_step_kernel(const 
   }
   if ((threadIdx.x & 31) < kCols) *reinterpret_cast<float4*>(&sums[threadIdx.x >> 5][4 * col]) = o;
   __syncthreads();
-  if (threadIdx.x < DV) {
+  if (threadIdx.x < kSlice) {
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) t += sums[i][threadIdx.x];
-    static_cast<T*>(p.o)[b * p.so.batch + h * p.so.head + threadIdx.x] = from_f32<T>(t * p.read);
+    static_cast<T*>(p.o)[b * p.so.batch + h * p.so.head + c0 + threadIdx.x] = from_f32<T>(t * p.read);
   }
+}
+
+template <typename T, int DK, int DV>
+void run(const DecayPass& p, cudaStream_t s) {
+  decay_step_kernel<T, DK, DV><<<dim3((unsigned)(p.B * p.H), DV / step_slice<DV>), step_threads<DK, DV>, 0, s>>>(p);
 }
 
 template <typename T, int DK>
 void run_v(const DecayPass& p, cudaStream_t s) {
-  const unsigned units = (unsigned)(p.B * p.H);
-  if (p.DZ == 16) decay_step_kernel<T, DK, 16><<<units, step_threads<DK, 16>, 0, s>>>(p);
-  else if (p.DZ == 32) decay_step_kernel<T, DK, 32><<<units, step_threads<DK, 32>, 0, s>>>(p);
-  else if (p.DZ == 64) decay_step_kernel<T, DK, 64><<<units, step_threads<DK, 64>, 0, s>>>(p);
-  else decay_step_kernel<T, DK, 128><<<units, step_threads<DK, 128>, 0, s>>>(p);
+  if (p.DZ == 16) run<T, DK, 16>(p, s);
+  else if (p.DZ == 32) run<T, DK, 32>(p, s);
+  else if (p.DZ == 64) run<T, DK, 64>(p, s);
+  else run<T, DK, 128>(p, s);
 }
 
 template <typename T>

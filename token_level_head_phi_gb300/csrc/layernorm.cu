@@ -88,27 +88,34 @@ __device__ __forceinline__ void load_param(const void* p, int is_f32, int c, flo
   }
 }
 
-// Sum over the G threads of a row (every thread gets it).  G > 32: the whole
-// CTA, through `sh`, which the caller alternates between uses.
-template <int G>
-__device__ __forceinline__ float2 row_sum2(float2 v, float2* sh) {
+// Sums of R rows' pairs over the G threads of a row (every thread gets them).
+// G > 32: the whole CTA, behind one barrier through `sh`, which the caller
+// alternates between uses.
+template <int G, int R>
+__device__ __forceinline__ void row_sums2(float2 (&v)[R], float2 (*sh)[32]) {
 #pragma unroll
-  for (int o = (G < 32 ? G : 32) / 2; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int o = (G < 32 ? G : 32) / 2; o > 0; o >>= 1) {
+      v[r].x += __shfl_xor_sync(0xffffffffu, v[r].x, o);
+      v[r].y += __shfl_xor_sync(0xffffffffu, v[r].y, o);
+    }
   if constexpr (G > 32) {
     constexpr int W = G / 32;
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = sh[(threadIdx.x & 31) & (W - 1)];
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    for (int r = 0; r < R; ++r)
+      if ((threadIdx.x & 31) == 0) sh[r][threadIdx.x >> 5] = v[r];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      v[r] = sh[r][(threadIdx.x & 31) & (W - 1)];
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1) {
+        v[r].x += __shfl_xor_sync(0xffffffffu, v[r].x, o);
+        v[r].y += __shfl_xor_sync(0xffffffffu, v[r].y, o);
+      }
     }
   }
-  return v;
 }
 
 template <int G>
@@ -260,7 +267,7 @@ template <typename T, int VEC, int G, int E, int R>
 __global__ void __launch_bounds__(norm_bwd_threads<G>) norm_bwd_kernel(const NormArgs a) {
   constexpr int kThreads = norm_bwd_threads<G>;
   constexpr int kGroups = kThreads / G;
-  __shared__ float2 sh[2][32];
+  __shared__ float2 sh[2][R][32];
   extern __shared__ float acc[];  // [2][cols], only for partial sums of several groups
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
   const int nv = a.cols / VEC;
@@ -270,70 +277,80 @@ __global__ void __launch_bounds__(norm_bwd_threads<G>) norm_bwd_kernel(const Nor
 #pragma unroll
     for (int j = 0; j < VEC; ++j) dw[e][j] = db[e][j] = 0.f;
 
-  int turn = 0;  // alternates the exchange slots, so one barrier per row is enough
-  // every thread of the CTA makes the same number of turns
-  for (int64_t base = (int64_t)blockIdx.x * (kGroups * R); base < a.rows; base += (int64_t)gridDim.x * (kGroups * R)) {
-    Raw<T, VEC> rx[R][E], rg[R][E];
-    float mean[R], rstd[R];
+  float w[E][VEC];  // of this thread's columns
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) w[e][j] = 1.f;
+    if (a.w && lane + e * G < nv) load_param<VEC>(a.w, a.w_f32, (lane + e * G) * VEC, w[e]);
+  }
+
+  // The next rows are on their way while the current ones are reduced and
+  // written: their raw registers are free once xh and g are formed.
+  Raw<T, VEC> rx[R][E], rg[R][E];
+  float mean[R], rstd[R];
+  auto fetch = [&](int64_t base) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int64_t row = base + group + r * kGroups;
       const bool live = row < a.rows;
       mean[r] = live ? a.mean[row] : 0.f;
       rstd[r] = live ? a.rstd[row] : 0.f;
+      const T* x = static_cast<const T*>(a.x) + row * a.sx + lane * VEC;
+      const T* dy = static_cast<const T*>(a.dy) + row * a.sdy + lane * VEC;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int i = lane + e * G;
-        if (live && i < nv) {
-          rx[r][e].load_once(static_cast<const T*>(a.x) + row * a.sx + (int64_t)i * VEC);
-          rg[r][e].load_once(static_cast<const T*>(a.dy) + row * a.sdy + (int64_t)i * VEC);
-        } else {
+        if (live && lane + e * G < nv) {
+          rx[r][e].load_once(x + e * G * VEC);
+          rg[r][e].load_once(dy + e * G * VEC);
+        } else {  // adds nothing to any sum
           rx[r][e].zero();
           rg[r][e].zero();
         }
       }
     }
+  };
+  int turn = 0;  // alternates the exchange slots, so one barrier per turn is enough
+  const int64_t stride = (int64_t)gridDim.x * (kGroups * R);
+  int64_t base = (int64_t)blockIdx.x * (kGroups * R);
+  if (base < a.rows) fetch(base);
+  // every thread of the CTA makes the same number of turns
+  for (; base < a.rows; base += stride) {
+    float xh[R][E][VEC], g[R][E][VEC], scale[R];
+    float2 sum[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      sum[r] = make_float2(0.f, 0.f);
+      scale[r] = rstd[r];
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const float d = to_f32(rg[r][e].v[j]), z = (to_f32(rx[r][e].v[j]) - mean[r]) * rstd[r];
+          dw[e][j] = fmaf(d, z, dw[e][j]);
+          db[e][j] += d;
+          xh[r][e][j] = z;
+          g[r][e][j] = d * w[e][j];
+          sum[r].x += g[r][e][j];
+          sum[r].y = fmaf(g[r][e][j], z, sum[r].y);
+        }
+    }
+    if (base + stride < a.rows) fetch(base + stride);
+    row_sums2<G, R>(sum, sh[turn]);
+    turn ^= 1;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int64_t row = base + group + r * kGroups;
-      const bool live = row < a.rows;
-      float2 s = make_float2(0.f, 0.f);
+      if (row >= a.rows) continue;
+      const float c1 = sum[r].x * a.inv_cols * scale[r], c2 = sum[r].y * a.inv_cols * scale[r];
+      T* dx = static_cast<T*>(a.y) + row * a.sy + lane * VEC;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int i = lane + e * G;
-        if (!live || i >= nv) continue;
-        float w[VEC];
-        if (a.w) load_param<VEC>(a.w, a.w_f32, i * VEC, w);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (to_f32(rx[r][e].v[j]) - mean[r]) * rstd[r];
-          const float g0 = to_f32(rg[r][e].v[j]);
-          const float g = a.w ? g0 * w[j] : g0;
-          s.x += g;
-          s.y = fmaf(g, xh, s.y);
-          dw[e][j] = fmaf(g0, xh, dw[e][j]);
-          db[e][j] += g0;
-        }
-      }
-      s = row_sum2<G>(s, sh[turn]);
-      turn ^= 1;
-      if (!live) continue;
-      const float c1 = s.x * a.inv_cols, c2 = s.y * a.inv_cols;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int i = lane + e * G;
-        if (i >= nv) continue;
-        float w[VEC];
-        if (a.w) load_param<VEC>(a.w, a.w_f32, i * VEC, w);
+        if (lane + e * G >= nv) continue;
         Raw<T, VEC> o;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (to_f32(rx[r][e].v[j]) - mean[r]) * rstd[r];
-          float g = to_f32(rg[r][e].v[j]);
-          if (a.w) g *= w[j];
-          o.v[j] = from_f32<T>(rstd[r] * (g - c1 - xh * c2));
-        }
-        o.store(static_cast<T*>(a.y) + row * a.sy + (int64_t)i * VEC);
+        for (int j = 0; j < VEC; ++j) o.v[j] = from_f32<T>(fmaf(g[r][e][j], scale[r], -fmaf(xh[r][e][j], c2, c1)));
+        o.store(dx + e * G * VEC);
       }
     }
   }
@@ -389,13 +406,14 @@ __global__ void __launch_bounds__(norm_bwd_threads<G>) norm_bwd_kernel(const Nor
 // Rows longer than a CTA's registers: dx with one CTA per row.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const NormArgs a) {
-  __shared__ float2 sh[32];
+  __shared__ float2 sh[1][32];
   const int nv = a.cols / VEC;
   const T* x = static_cast<const T*>(a.x) + blockIdx.x * a.sx;
   const T* dy = static_cast<const T*>(a.dy) + blockIdx.x * a.sdy;
   T* dx = static_cast<T*>(a.y) + blockIdx.x * a.sy;
   const float mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
-  float2 s = make_float2(0.f, 0.f);
+  float2 sum[1] = {make_float2(0.f, 0.f)};
+  float2& s = sum[0];
   Raw<T, VEC> rx, rg;
   float w[VEC];
   for (int i = threadIdx.x; i < nv; i += 1024) {
@@ -411,7 +429,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const NormArgs a) {
       s.y = fmaf(g, xh, s.y);
     }
   }
-  s = row_sum2<1024>(s, sh);
+  row_sums2<1024, 1>(sum, sh);
   const float c1 = s.x * a.inv_cols, c2 = s.y * a.inv_cols;
   for (int i = threadIdx.x; i < nv; i += 1024) {
     rx.load(x + (int64_t)i * VEC);
@@ -454,6 +472,7 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* partial,
   const int c = blockIdx.x * 32 + tx;  // over [2][cols]
   float s = 0.f;
   if (c < 2 * cols)
+#pragma unroll 8
     for (int p = ty; p < parts; p += 32) s += partial[(int64_t)p * 2 * cols + c];
   sh[ty][tx] = s;
   __syncthreads();
@@ -505,24 +524,24 @@ mhla_status with_bwd_shape(int cols, bool vec, F&& f) {
   constexpr int W = 16 / sizeof(T);
   if (vec) {
     const int nv = cols / W;
-    if (nv <= 2) return f.template go<W, 2, 1, 4>();
-    if (nv <= 4) return f.template go<W, 4, 1, 4>();
-    if (nv <= 8) return f.template go<W, 8, 1, 4>();
-    if (nv <= 16) return f.template go<W, 16, 1, 4>();
-    if (nv <= 32) return f.template go<W, 32, 1, 4>();
-    if (nv <= 64) return f.template go<W, 32, 2, 2>();
-    if (nv <= 128) return f.template go<W, 32, 4, 1>();
-    if (nv <= 256) return f.template go<W, 128, 2, 1>();
-    if (nv <= 512) return f.template go<W, 128, 4, 1>();
-    if (nv <= 1024) return f.template go<W, 256, 4, 1>();
-    if (nv <= 2048) return f.template go<W, 1024, 2, 1>();
+    if (nv <= 2) return f.template go<W, 2, 1, 2>();
+    if (nv <= 4) return f.template go<W, 4, 1, 2>();
+    if (nv <= 8) return f.template go<W, 8, 1, 2>();
+    if (nv <= 16) return f.template go<W, 16, 1, 2>();
+    if (nv <= 32) return f.template go<W, 32, 1, 2>();
+    if (nv <= 64) return f.template go<W, 64, 1, 2>();
+    if (nv <= 128) return f.template go<W, 128, 1, 2>();
+    if (nv <= 256) return f.template go<W, 256, 1, 2>();
+    if (nv <= 512) return f.template go<W, 512, 1, 1>();
+    if (nv <= 1024) return f.template go<W, 512, 2, 1>();
+    if (nv <= 2048) return f.template go<W, 512, 4, 1>();
     return f.template go_long<W>();
   }
-  if (cols <= 8) return f.template go<1, 8, 1, 4>();
-  if (cols <= 32) return f.template go<1, 32, 1, 4>();
-  if (cols <= 128) return f.template go<1, 32, 4, 1>();
-  if (cols <= 512) return f.template go<1, 32, 16, 1>();
-  if (cols <= 2048) return f.template go<1, 128, 16, 1>();
+  if (cols <= 8) return f.template go<1, 8, 1, 2>();
+  if (cols <= 32) return f.template go<1, 32, 1, 2>();
+  if (cols <= 128) return f.template go<1, 32, 4, 2>();
+  if (cols <= 512) return f.template go<1, 128, 4, 2>();
+  if (cols <= 2048) return f.template go<1, 256, 8, 1>();
   if (cols <= 8192) return f.template go<1, 512, 16, 1>();
   return f.template go_long<1>();
 }
@@ -546,7 +565,8 @@ struct Forward {
 };
 
 // Partial rows of dw and db that the backward pass of these sizes writes:
-// a few CTAs of the register kernels on every SM, or 64 shares of the rows.
+// one for each of the CTAs that are resident at once (512 to 640 threads on
+// every SM), or 64 shares of the rows.
 constexpr int kLongShares = 64;
 struct Parts {
   const NormArgs& a;
@@ -554,7 +574,7 @@ struct Parts {
   template <int VEC, int G, int E, int R>
   mhla_status go() {
     constexpr int rows = norm_bwd_threads<G> / G * R;
-    constexpr int64_t per_sm = norm_bwd_threads<G> <= 128 ? 4 : norm_bwd_threads<G> <= 256 ? 2 : 1;
+    constexpr int64_t per_sm = (norm_bwd_threads<G> <= 128 ? 640 : 512) / norm_bwd_threads<G>;  // registers allow it
     n = (a.rows + rows - 1) / rows;
     if (n > per_sm * kOpsSms) n = per_sm * kOpsSms;
     return MHLA_OK;
