@@ -188,7 +188,14 @@ def test_backward(b, h, n, dk, dv, layout, with_state, dtype, variant):
     state = make((b, h, dk, dv), "f32", 4, 3.0) if with_state else None
     ds = make((b, h, dk, dv), "f32", 6) if with_state else None
     scale = dk ** -0.5
-    got = mb.mhla_decay_backward(q, k, v, g, do, state=state, dstate_out=ds, scale=scale, layout=layout, variant=variant)
+    into = None if with_state else torch.empty(b, h, dk, dv, device="cuda")  # asked for although there is no state
+    got = mb.mhla_decay_backward(q, k, v, g, do, state=state, dstate_out=ds, scale=scale, layout=layout, variant=variant,
+                                 dstate=into)
+    if not with_state:
+        fewer = mb.mhla_decay_backward(q, k, v, g, do, scale=scale, layout=layout, variant=variant)
+        assert fewer[3] is None
+        for x, y in zip(fewer[:3], got[:3]):  # states of 16 bits where none is asked for
+            torch.testing.assert_close(x, y, rtol=2.0 ** -6, atol=2.0 ** -8 * y.abs().max().item())
     scale = float(np.float32(scale))
     for i in range(b):
         for j in range(h):
@@ -291,7 +298,7 @@ def test_strides_and_alignment(offset, dtype):
     grads = torch.full_like(fused, 7)
     gpart = lambda i: grads[:, :, offset + i * h * d: offset + (i + 1) * h * d].unflatten(2, (h, d))  # noqa: E731
     got = mb.mhla_decay_backward(q, k, v, g, do, layout="bnhd", dq=gpart(0), dk=gpart(1), dv=gpart(2))
-    for x, y in zip(got, want):
+    for x, y in zip(got[:3], want[:3]):
         assert torch.equal(x, y)
     assert (grads[:, :, :offset] == 7).all() and (grads[:, :, offset + 3 * h * d:] == 7).all()
     one = k[:, :, :1].expand(b, n, h, d)  # one key head for all
@@ -327,7 +334,7 @@ def test_empty_problems():
     assert out.shape == q.shape and torch.equal(s, state)
     _, s = mb.mhla_decay_forward(q, q, q, g)
     assert not s.any()
-    _, _, _, ds = mb.mhla_decay_backward(q, q, q, g, q, dstate_out=state)
+    _, _, _, ds = mb.mhla_decay_backward(q, q, q, g, q, state=state, dstate_out=state)
     assert torch.equal(ds, state)
     q = torch.empty(0, 2, 5, 32, device="cuda")
     out, s = mb.mhla_decay_forward(q, q, q, g)

@@ -885,7 +885,8 @@ def mhla_decay_backward(q, k, v, log_decay, dout, state=None, dstate_out=None, l
 
     ``dout`` is the gradient of out and ``dstate_out`` that of the final state
     (None: zeros); ``dstate`` is the gradient of the starting state (float32
-    [B, H, dk, dv]).  Arguments as in the forward call.
+    [B, H, dk, dv]; None without one, unless a tensor is given for it).
+    Arguments as in the forward call.
     """
     import torch
     key = ("decay backward", scale, layout, variant, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(dout),
@@ -895,12 +896,12 @@ def mhla_decay_backward(q, k, v, log_decay, dout, state=None, dstate_out=None, l
     dq = _fresh(q, c.q_dense) if dq is None else dq
     dk = _fresh(k, c.k_dense) if dk is None else dk
     dv = _fresh(v, c.v_dense) if dv is None else dv
-    if dstate is None:
+    if dstate is None and state is not None:
         dstate = torch.empty(c.shape, dtype=torch.float32, device=c.device)
     workspace, ws_bytes = c.workspace(workspace, c.device)
     _check(load().mhla_decay_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths),
                                       _ptr(state), dout.data_ptr(), _ptr(dstate_out), c.ref, dq.data_ptr(),
-                                      dk.data_ptr(), dv.data_ptr(), dstate.data_ptr(), _ptr(workspace), ws_bytes,
+                                      dk.data_ptr(), dv.data_ptr(), _ptr(dstate), _ptr(workspace), ws_bytes,
                                       _stream_handle(stream, key[4][3])), "mhla_decay_backward")
     return dq, dk, dv, dstate
 

@@ -1,10 +1,12 @@
 // Linear attention with a decay for each head on the CUDA cores: float32
 // arithmetic for both dtypes (see decay.h for the pass).
 //
-// One CTA per (unit, segment, slice of at most 64 columns of z) walks its
-// segment in 32-token tiles with the state in shared memory.  Per tile: the
-// masked, decayed scores (2 x 2 register tiles), the output rows
-// (2 tokens x DZ/16 columns) and the state (DX/16 x DZ/16 entries a thread).
+// One CTA of 256 threads per (unit, segment, slice of at most 64 columns of z)
+// walks its segment in 64-token tiles with the state in shared memory.  A
+// thread keeps 4 x 4 entries of the scores, 4 tokens x DZ/16 columns of the
+// output and DX/16 x DZ/16 entries of the state in registers, and reads its
+// operands as 16-byte vectors along the contraction: bound by the float32
+// units, not by shared memory (64 products for 8 vector reads).
 #include "common.cuh"
 #include "decay.h"
 #include "ops.h"
@@ -12,22 +14,57 @@
 namespace mhla {
 namespace {
 
-constexpr int C = 32;  // tokens of a tile
+constexpr int C = 64;  // tokens of a tile
 constexpr int kThreads = 256;
 
+// Rows of x and y are 4 floats longer than they need be: eight neighbouring
+// rows start in eight different groups of four banks.
 template <int DX, int DZS>
-struct SimtSmem {
-  float x[C][DX + 1];
-  float y[C][DX + 1];
+struct alignas(16) SimtSmem {
+  float x[C][DX + 4];
+  float y[C][DX + 4];
   float z[C][DZS];
   float s[DX][DZS];
-  float w[C][C + 1];
-  float pw[C + 1];  // lambda^n
+  float w[C][C + 4];
+  float pw[C + 4];  // lambda^n
 };
+
+// N consecutive floats of shared memory.
+template <int N>
+__device__ __forceinline__ void read_n(const float* p, float (&v)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 t = reinterpret_cast<const float4*>(p)[i];
+      v[4 * i] = t.x, v[4 * i + 1] = t.y, v[4 * i + 2] = t.z, v[4 * i + 3] = t.w;
+    }
+  } else if constexpr (N == 2) {
+    const float2 t = *reinterpret_cast<const float2*>(p);
+    v[0] = t.x, v[1] = t.y;
+  } else {
+    v[0] = p[0];
+  }
+}
 
 template <typename T, int D>
 __device__ __forceinline__ void load_rows(float* dst, int ld, const T* src, int64_t token_stride, const DecayPass& p,
                                           int first, int n, int length) {
+  if (p.vec) {
+    constexpr int V = 16 / sizeof(T), kPieces = D / V;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < C * kPieces; i += kThreads) {
+      const int r = i / kPieces, c = i % kPieces * V;
+      alignas(16) T v[V];
+      if (r < n) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(src + decay_token(p, first + r, length) * token_stride + c);
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < n) f = make_float4(to_f32(v[j]), to_f32(v[j + 1]), to_f32(v[j + 2]), to_f32(v[j + 3]));
+        *reinterpret_cast<float4*>(dst + r * ld + c + j) = f;
+      }
+    }
+    return;
+  }
   for (int i = threadIdx.x; i < C * D; i += kThreads) {
     const int r = i / D, c = i % D;
     dst[r * ld + c] = r < n ? to_f32(src[decay_token(p, first + r, length) * token_stride + c]) : 0.f;
@@ -85,84 +122,111 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const DecayPass p)
   for (int c0 = 0; c0 < valid; c0 += C) {
     const int n = min(C, valid - c0), first = begin + c0;
     __syncthreads();
-    if (OUT) load_rows<T, DX>(&sm.x[0][0], DX + 1, x, p.sx.token, p, first, n, length);
-    load_rows<T, DX>(&sm.y[0][0], DX + 1, y, p.sy.token, p, first, n, length);
+    if (OUT) load_rows<T, DX>(&sm.x[0][0], DX + 4, x, p.sx.token, p, first, n, length);
+    load_rows<T, DX>(&sm.y[0][0], DX + 4, y, p.sy.token, p, first, n, length);
     load_rows<T, DZS>(&sm.z[0][0], DZS, z, p.sz.token, p, first, n, length);
     __syncthreads();
     if (OUT) {
-      float d[2][2] = {};
-      for (int a = 0; a < DX; ++a) {
-        const float x0 = sm.x[2 * tr][a], x1 = sm.x[2 * tr + 1][a];
-        const float y0 = sm.y[tc][a], y1 = sm.y[tc + 16][a];
-        d[0][0] = fmaf(x0, y0, d[0][0]);
-        d[0][1] = fmaf(x0, y1, d[0][1]);
-        d[1][0] = fmaf(x1, y0, d[1][0]);
-        d[1][1] = fmaf(x1, y1, d[1][1]);
+      // scores of tokens 4 tr .. 4 tr + 3 against tokens tc, tc + 16, ...
+      float d[4][4] = {};
+      const int groups = min(4, tr / 4 + 1);  // later groups of 16 lie above the diagonal
+#pragma unroll 2
+      for (int a = 0; a < DX; a += 4) {
+        float xv[4][4], yv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) read_n<4>(&sm.x[4 * tr + i][a], xv[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j >= groups) break;
+          read_n<4>(&sm.y[tc + 16 * j][a], yv);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[i][j] = fmaf(xv[i][q], yv[q], d[i][j]);
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int t = 2 * tr + i, u = tc + 16 * j;
+        for (int j = 0; j < 4; ++j) {
+          const int t = 4 * tr + i, u = tc + 16 * j;
           sm.w[t][u] = t >= u ? d[i][j] * (sm.pw[t - u] * p.score) : 0.f;
         }
       // the earlier tokens through the state
-      float acc[2][KC] = {};
-      for (int a = 0; a < DX; ++a) {
-        const float x0 = sm.x[2 * tr][a], x1 = sm.x[2 * tr + 1][a];
+      float acc[4][KC] = {};
+#pragma unroll 2
+      for (int a = 0; a < DX; a += 4) {
+        float xv[4][4];
 #pragma unroll
-        for (int k = 0; k < KC; ++k) {
-          const float s = sm.s[a][tc + 16 * k];
-          acc[0][k] = fmaf(x0, s, acc[0][k]);
-          acc[1][k] = fmaf(x1, s, acc[1][k]);
-        }
-      }
-      const float r0 = sm.pw[2 * tr + p.e] * p.read, r1 = sm.pw[2 * tr + 1 + p.e] * p.read;
+        for (int i = 0; i < 4; ++i) read_n<4>(&sm.x[4 * tr + i][a], xv[i]);
 #pragma unroll
-      for (int k = 0; k < KC; ++k) {
-        acc[0][k] *= r0;
-        acc[1][k] *= r1;
-      }
-      __syncthreads();
-      for (int j = 0; j <= 2 * tr + 1; ++j) {
-        const float w0 = sm.w[2 * tr][j], w1 = sm.w[2 * tr + 1][j];
+        for (int q = 0; q < 4; ++q) {
+          float sv[KC];
+          read_n<KC>(&sm.s[a + q][KC * tc], sv);
 #pragma unroll
-        for (int k = 0; k < KC; ++k) {
-          const float v = sm.z[j][tc + 16 * k];
-          acc[0][k] = fmaf(w0, v, acc[0][k]);
-          acc[1][k] = fmaf(w1, v, acc[1][k]);
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < KC; ++k) acc[i][k] = fmaf(xv[i][q], sv[k], acc[i][k]);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = 2 * tr + i;
+      for (int i = 0; i < 4; ++i) {
+        const float r = sm.pw[4 * tr + i + p.e] * p.read;
+#pragma unroll
+        for (int k = 0; k < KC; ++k) acc[i][k] *= r;
+      }
+      __syncthreads();  // the scores are there, and every output row has read the state
+      for (int j = 0; j < 4 * tr + 4; j += 4) {
+        float wv[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) read_n<4>(&sm.w[4 * tr + i][j], wv[i]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float zv[KC];
+          read_n<KC>(&sm.z[j + q][KC * tc], zv);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < KC; ++k) acc[i][k] = fmaf(wv[i][q], zv[k], acc[i][k]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 4 * tr + i;
         if (t >= n) continue;
-        T* row = o + decay_token(p, first + t, length) * p.so.token;
+        T* row = o + decay_token(p, first + t, length) * p.so.token + KC * tc;
+        if (sizeof(T) * KC == 16 && p.vec) {
+          alignas(16) T v[KC];
 #pragma unroll
-        for (int k = 0; k < KC; ++k) row[tc + 16 * k] = from_f32<T>(acc[i][k]);
+          for (int k = 0; k < KC; ++k) v[k] = from_f32<T>(acc[i][k]);
+          if constexpr (sizeof(T) * KC == 16) *reinterpret_cast<uint4*>(row) = *reinterpret_cast<uint4*>(v);
+        } else {
+#pragma unroll
+          for (int k = 0; k < KC; ++k) row[k] = from_f32<T>(acc[i][k]);
+        }
       }
     }
-    // the state behind the tile
+    // the state behind the tile: rows KA tr .. and columns KC tc ..
     float u[KA][KC] = {};
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
       const float w = sm.pw[n - j - p.e] * p.update;
-      float zz[KC];
+      float yv[KA], zv[KC];
+      read_n<KA>(&sm.y[j][KA * tr], yv);
+      read_n<KC>(&sm.z[j][KC * tc], zv);
 #pragma unroll
-      for (int k = 0; k < KC; ++k) zz[k] = sm.z[j][tc + 16 * k];
+      for (int k = 0; k < KC; ++k) zv[k] *= w;
 #pragma unroll
-      for (int i = 0; i < KA; ++i) {
-        const float yy = sm.y[j][tr + 16 * i] * w;
+      for (int i = 0; i < KA; ++i)
 #pragma unroll
-        for (int k = 0; k < KC; ++k) u[i][k] = fmaf(yy, zz[k], u[i][k]);
-      }
+        for (int k = 0; k < KC; ++k) u[i][k] = fmaf(yv[i], zv[k], u[i][k]);
     }
-    if (OUT) __syncthreads();  // every output row has read the state
     const float2 w = decay_power(g, n);
 #pragma unroll
     for (int i = 0; i < KA; ++i)
 #pragma unroll
       for (int k = 0; k < KC; ++k) {
-        float& s = sm.s[tr + 16 * i][tc + 16 * k];
+        float& s = sm.s[KA * tr + i][KC * tc + k];
         s = fmaf(s, w.x, fmaf(s, w.y, u[i][k]));
       }
   }
