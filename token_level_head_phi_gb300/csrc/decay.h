@@ -14,9 +14,11 @@
 // Only powers with exponents >= 0 are ever formed, so any decay is safe.
 //
 // Long sequences are cut into `nseg` segments of seg_len tokens: a first
-// launch forms each segment's own final state, the second one starts every
-// segment from the sum of the earlier segments' states, each under its power
-// of lambda, formed directly and not step by step.
+// launch forms each segment's own final state, a small second one turns them
+// into the states before each segment, and the third runs all segments at
+// once.  The second and third are launched with programmatic stream
+// serialization: they set up and start their loads while their predecessor
+// drains, and call decay_wait before they read what it wrote.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -34,11 +36,11 @@ struct DecayPass {
   const int32_t* lengths;
   const float* s_in;  // [units][DX][DZ], or its transpose (s_ldx, s_ldz); may be null
   float* s_out;       // same layout; may be null, may be s_in
-  float* seg;         // [units][nseg][DX * DZ] segment states (nseg > 1)
+  float* seg;         // [units][nseg][DX * DZ] (nseg > 1): slot i the state before segment i
   int s_ldx, s_ldz;   // element strides of a state's x and z axes, in s_in, s_out and seg
   int B, H, N, DX, DZ;
   int nseg, seg_len;
-  int launches;  // 1: the segments' own states, 2: the pass itself, 3: both
+  int launches;  // 1: the states before the segments, 2: the pass itself, 3: both
   int reverse;  // 1: token i of the pass is the sequence's token length - 1 - i
   int e;
   float score, read, update;
@@ -46,6 +48,9 @@ struct DecayPass {
 };
 
 #ifdef __CUDACC__
+__device__ __forceinline__ void decay_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void decay_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // lambda^n = exp(n g) as high + low parts, so that a state that is multiplied
 // by it thousands of times does not drift by the rounding of one float32
 // factor.  Slow decays go through exp(x) = 1 + expm1(x), whose float32 value
@@ -78,6 +83,7 @@ __device__ __forceinline__ int decay_token(const DecayPass& p, int i, int length
 #endif
 
 // Launches return a cudaError_t.
+cudaError_t launch_decay_scan(const DecayPass& p, cudaStream_t s);
 cudaError_t launch_decay_simt(const DecayPass& p, int dtype, cudaStream_t s);
 cudaError_t launch_decay_mma(const DecayPass& p, cudaStream_t s);  // bf16
 cudaError_t launch_decay_step(const DecayPass& p, int dtype, cudaStream_t s);

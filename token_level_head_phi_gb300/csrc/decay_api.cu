@@ -24,26 +24,35 @@ bool on_tensor_cores(const mhla_decay_params* p) {
   return p->dtype == MHLA_DTYPE_BF16 && p->variant != MHLA_DECAY_SIMT;
 }
 
-// Segments of a pass: as many as the CTAs (units x slices of 64 columns x
-// segments) that are resident at once (three on every SM, two with DX = 128
-// and on the CUDA cores), of at least 256 tokens (the state that starts a
-// segment costs about as much as that many tokens), and at most 64 of them (a
-// segment sums all earlier states).
-constexpr int kSegQuantum = 128, kSegLeast = 256, kSegMost = 64;
+// Segments of a pass.  CTAs (units x slices of 64 columns x segments) run in
+// waves of those that are resident at once: three on every SM, two with DX =
+// 128 and on the CUDA cores.  A segment costs its tokens and about a hundred
+// more for its start, and more than one segment costs the launch that forms
+// their states, measured at 0.6 of the pass itself.  The count with the
+// smallest product wins; segments are of at least 128 tokens and at most 64.
+// (32k tokens x 64 heads: 7 segments, one wave; 2k tokens x 60 heads of 128:
+// 5 segments, two waves, 92 against 105 us with 2 segments in one.)
+constexpr int kSegQuantum = 128, kSegMost = 64, kSegStart = 100;
 
 void plan_segments(const mhla_decay_params* p, int dx, int dz, int* nseg, int* seg_len) {
   const int64_t ctas = (int64_t)p->batch * p->heads * (dz > 64 ? dz / 64 : 1);
   const int64_t slots = (on_tensor_cores(p) && dx < 128 ? 3 : 2) * kOpsSms;
-  int64_t n = ctas > 0 ? slots / ctas : 1;
-  if (n > p->tokens / kSegLeast) n = p->tokens / kSegLeast;
-  if (n > kSegMost) n = kSegMost;
-  if (n < 1) n = 1;
-  int64_t len = (p->tokens + n - 1) / n;
-  len = (len + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
-  if (len < kSegQuantum) len = kSegQuantum;
-  *seg_len = (int)len;
-  *nseg = (int)((p->tokens + len - 1) / len);
-  if (*nseg < 1) *nseg = 1;
+  *nseg = 1;
+  *seg_len = (p->tokens + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
+  double best = (double)((ctas + slots - 1) / slots) * (*seg_len + kSegStart);
+  for (int n = 2; n <= kSegMost; ++n) {
+    int len = (p->tokens + n - 1) / n;
+    len = (len + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
+    const int count = (p->tokens + len - 1) / len;
+    if (count != n) continue;
+    const double cost = 1.6 * (double)((ctas * n + slots - 1) / slots) * (len + kSegStart);
+    if (cost < best) {
+      best = cost;
+      *nseg = n;
+      *seg_len = len;
+    }
+  }
+  if (*seg_len < kSegQuantum) *seg_len = kSegQuantum;
 }
 
 size_t pass_workspace(const mhla_decay_params* p, int dx, int dz) {

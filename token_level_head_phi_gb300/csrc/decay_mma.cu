@@ -21,6 +21,7 @@
 #include "common.cuh"
 #include "decay.h"
 #include "ops.h"
+#include "tc_host.h"
 
 namespace mhla {
 namespace {
@@ -240,9 +241,6 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
     }
   }
 
-  // the state before the segment.  s_in may be overwritten by the last
-  // segment's CTA, so with several segments the second launch reads the copy
-  // that the first one left in the last slot
   const int own_tile = warp % (kTiles < kWarps ? kTiles : kWarps);
   const int own_col = kSplit > 1 ? (warp / kTiles) * kCols : 0;
   const bool owner = own_col < kZ16;
@@ -256,41 +254,23 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
     for (int n8 = 0; n8 < 2 * kCols; ++n8)
 #pragma unroll
       for (int r = 0; r < 4; ++r) s[i][n8][r] = 0.f;
-  if (owner && seg == 0 && p.s_in) {
+  if (!OUT) decay_dependents();
+  // the state before the segment: the first launch starts every one from zero
+  if (OUT && p.nseg > 1) decay_wait();
+  const float* before = !OUT ? nullptr : p.nseg > 1 ? segs + seg * one : p.s_in ? p.s_in + state : nullptr;
+  if (owner && before) {
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
 #pragma unroll
       for (int n8 = 0; n8 < 2 * kCols; ++n8)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < 4; r += 2) {
           const int2 at = entry(i, n8, r);
-          const int64_t in = (int64_t)at.x * p.s_ldx + (int64_t)(z0 + at.y) * p.s_ldz;
-          const int64_t slot = (p.nseg - 1) * one + in;
-          if (OUT && p.nseg > 1) {
-            s[i][n8][r] = segs[slot];
-          } else {
-            s[i][n8][r] = p.s_in[state + in];
-            if (!OUT) segs[slot] = s[i][n8][r];
-          }
+          const float* f = before + (int64_t)at.x * p.s_ldx + (int64_t)(z0 + at.y) * p.s_ldz;
+          const float2 v = p.s_ldz == 1 ? *reinterpret_cast<const float2*>(f) : make_float2(f[0], f[p.s_ldz]);
+          s[i][n8][r] = v.x;
+          s[i][n8][r + 1] = v.y;
         }
-  }
-  if (OUT && owner && valid > 0) {
-    for (int q = 0; q < seg; ++q) {
-      const float2 w = decay_power(g, (seg - 1 - q) * p.seg_len);
-      const float* u = segs + q * one;
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i)
-#pragma unroll
-        for (int n8 = 0; n8 < 2 * kCols; ++n8)
-#pragma unroll
-          for (int r = 0; r < 4; r += 2) {
-            const int2 at = entry(i, n8, r);
-            const float* f = u + (int64_t)at.x * p.s_ldx + (int64_t)(z0 + at.y) * p.s_ldz;
-            const float2 v = p.s_ldz == 1 ? *reinterpret_cast<const float2*>(f) : make_float2(f[0], f[p.s_ldz]);
-            s[i][n8][r] = fmaf(v.x, w.x, fmaf(v.x, w.y, s[i][n8][r]));
-            s[i][n8][r + 1] = fmaf(v.y, w.x, fmaf(v.y, w.y, s[i][n8][r + 1]));
-          }
-    }
   }
   // addresses inside a 16 x 16 block for ldmatrix / stmatrix: rows are the
   // first 8 / last 8 in lanes 0-7, 16-23 / 8-15, 24-31 for A (and for
@@ -518,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
         if (OUT)
           p.s_out[state + in] = s[i][n8][r];
         else
-          segs[seg * one + in] = s[i][n8][r];
+          segs[(seg + 1) * one + in] = s[i][n8][r];
       }
 }
 
@@ -534,6 +514,7 @@ cudaError_t run(const DecayPass& p, cudaStream_t s) {
       return e;
     k<<<dim3(units, (unsigned)(p.nseg - 1), slices), kThreads, smem, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_decay_scan(p, s)) != cudaSuccess) return e;
   }
   if (!(p.launches & 2)) return cudaSuccess;
   constexpr int smem = (int)sizeof(MmaSmem<DX, DZS, true>);
@@ -541,7 +522,8 @@ cudaError_t run(const DecayPass& p, cudaStream_t s) {
   if (smem > 48 * 1024 &&
       (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
     return e;
-  k<<<dim3(units, (unsigned)p.nseg, slices), kThreads, smem, s>>>(p);
+  if (p.nseg > 1) return (cudaError_t)launch_pdl(k, dim3(units, (unsigned)p.nseg, slices), dim3(kThreads), smem, s, p);
+  k<<<dim3(units, 1, slices), kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 

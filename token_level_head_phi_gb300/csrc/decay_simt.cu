@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "decay.h"
 #include "ops.h"
+#include "tc_host.h"
 
 namespace mhla {
 namespace {
@@ -98,25 +99,13 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const DecayPass p)
     const float2 w = decay_power(g, tid);
     sm.pw[tid] = w.x + w.y;
   }
-  // the state before the segment; s_in may be overwritten by the last
-  // segment's CTA, so with several segments the second launch reads the copy
-  // that the first one left in the last slot
-  const bool copied = OUT && p.nseg > 1;
+  if (!OUT) decay_dependents();
+  // the state before the segment: the first launch starts every one from zero
+  if (OUT && p.nseg > 1) decay_wait();
+  const float* before = !OUT ? nullptr : p.nseg > 1 ? segs + seg * one : p.s_in ? p.s_in + state : nullptr;
   for (int i = tid; i < DX * DZS; i += kThreads) {
     const int a = i / DZS, c = i % DZS;
-    const int64_t at = (int64_t)a * p.s_ldx + (int64_t)(z0 + c) * p.s_ldz;
-    float s = 0.f;
-    if (seg == 0 && p.s_in) {
-      s = copied ? segs[(p.nseg - 1) * one + at] : p.s_in[state + at];
-      if (!OUT) segs[(p.nseg - 1) * one + at] = s;
-    }
-    if (OUT && valid > 0)
-      for (int r = 0; r < seg; ++r) {
-        const float2 w = decay_power(g, (seg - 1 - r) * p.seg_len);
-        const float u = segs[r * one + at];
-        s = fmaf(u, w.x, fmaf(u, w.y, s));
-      }
-    sm.s[a][c] = s;
+    sm.s[a][c] = before ? before[(int64_t)a * p.s_ldx + (int64_t)(z0 + c) * p.s_ldz] : 0.f;
   }
 
   for (int c0 = 0; c0 < valid; c0 += C) {
@@ -242,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const DecayPass p)
   } else if (valid > 0) {
     for (int i = tid; i < DX * DZS; i += kThreads) {
       const int a = i / DZS, c = i % DZS;
-      segs[seg * one + (int64_t)a * p.s_ldx + (int64_t)(z0 + c) * p.s_ldz] = sm.s[a][c];
+      segs[(seg + 1) * one + (int64_t)a * p.s_ldx + (int64_t)(z0 + c) * p.s_ldz] = sm.s[a][c];
     }
   }
 }
@@ -259,13 +248,15 @@ cudaError_t run(const DecayPass& p, cudaStream_t s) {
       return e;
     k<<<dim3(units, (unsigned)(p.nseg - 1), slices), kThreads, smem, s>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_decay_scan(p, s)) != cudaSuccess) return e;
   }
   if (!(p.launches & 2)) return cudaSuccess;
   auto* k = decay_simt_kernel<T, DX, DZS, true>;
   if (smem > 48 * 1024 &&
       (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
     return e;
-  k<<<dim3(units, (unsigned)p.nseg, slices), kThreads, smem, s>>>(p);
+  if (p.nseg > 1) return (cudaError_t)launch_pdl(k, dim3(units, (unsigned)p.nseg, slices), dim3(kThreads), smem, s, p);
+  k<<<dim3(units, 1, slices), kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
