@@ -479,17 +479,9 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_handle(stream, device) -> int:
-    if stream is None:
-        import torch
-        return torch.cuda.current_stream(device).cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _fresh(t, contiguous):
-    """A contiguous tensor shaped and typed like t."""
+def _contiguous_like(t):
     import torch
-    return torch.empty_like(t) if contiguous else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _axes(layout: str):
@@ -549,20 +541,35 @@ def _set_output(field, name, t, like, shape, axes) -> None:
 
 
 class _Call:
-    """A parameter block with what the wrappers need beside it."""
+    """An entry point with its parameter block and what its wrapper needs beside them."""
 
-    def __init__(self, params, need=0, **kw):
+    def __init__(self, entry, like, params, need=0, **kw):
+        import torch
+        self.entry, self.call = entry, getattr(load(), entry)
         self.params, self.ref, self.need = params, ctypes.byref(params), need
+        self.device, self.index = like.device, like.get_device()
+        self.empty, self.f32, self.u8 = torch.empty, torch.float32, torch.uint8
+        self.current = torch.cuda.current_stream
         self.__dict__.update(kw)
 
-    def workspace(self, given, device):
+    def stream(self, given) -> int:
+        if given is None:
+            return self.current(self.index).cuda_stream
+        return given.cuda_stream if hasattr(given, "cuda_stream") else int(given)
+
+    def workspace(self, given):
         """(tensor or None, bytes): the caller's workspace or a new one."""
         if given is not None:
             return given, given.numel() * given.element_size()
         if not self.need:
             return None, 0
-        import torch
-        return torch.empty(self.need, dtype=torch.uint8, device=device), self.need
+        return self.empty(self.need, dtype=self.u8, device=self.device), self.need
+
+
+def _fresh(t):
+    """What makes a contiguous tensor shaped and typed like t."""
+    import torch
+    return torch.empty_like if t.is_contiguous() else _contiguous_like
 
 
 class RotaryPlan:
@@ -628,23 +635,26 @@ def _rotary_call(q, k, positions, style, layout, q_out, k_out, transpose):
         else:
             raise ValueError(f"positions must be [N] or [B, N], got {tuple(positions.shape)}")
         p.position_dtype = 1 if positions.dtype == torch.int64 else 0
-    return _Call(p, q_dense=q.is_contiguous(), k_dense=k is not None and k.is_contiguous())
+    return _Call("mhla_rotary", q, p, new_q=_fresh(q), new_k=None if k is None else _fresh(k))
 
 
 def _rotary(q, k, plan, positions, offset, style, layout, q_out, k_out, stream, transpose, where):
     key = ("rotary", transpose, style, layout, _sig(q), _sig(k), _sig(positions), _sig(q_out), _sig(k_out))
     c = _CALLS.get(key) or _remember(key, _rotary_call(q, k, positions, style, layout, q_out, k_out, transpose))
     if q_out is None:
-        q_out = _fresh(q, c.q_dense)
+        q_out = c.new_q(q)
     if k_out is None and k is not None:
-        k_out = _fresh(k, c.k_dense)
+        k_out = c.new_k(k)
     ref = c.ref
     if offset:  # changes from token to token: in a block of its own
         p = MhlaRotaryParams.from_buffer_copy(c.params)
         p.position_offset = int(offset)
         ref = ctypes.byref(p)
-    _check(load().mhla_rotary(q.data_ptr(), _ptr(k), _ptr(positions), plan._ref, ref, q_out.data_ptr(), _ptr(k_out),
-                              _stream_handle(stream, key[4][3])), where)
+    status = c.call(q.data_ptr(), None if k is None else k.data_ptr(),
+                    None if positions is None else positions.data_ptr(), plan._ref, ref, q_out.data_ptr(),
+                    None if k is None else k_out.data_ptr(), c.stream(stream))
+    if status:
+        raise MhlaError(status, where)
     return q_out, k_out
 
 
@@ -710,7 +720,7 @@ def _norm_forward_call(x, weight, bias, eps, out, mean, rstd):
         _, _, p.y_stride = _norm_rows("out", out, x)
     _flat("mean", mean, x, torch.float32, x.shape[:-1])
     _flat("rstd", rstd, x, torch.float32, x.shape[:-1])
-    return _Call(p, dense=x.is_contiguous(), lead=x.shape[:-1], device=x.device)
+    return _Call("mhla_layernorm_forward", x, p, new=_fresh(x), lead=x.shape[:-1])
 
 
 def mhla_layernorm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None, stream=None):
@@ -720,18 +730,18 @@ def mhla_layernorm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=Non
     ``rstd`` are float32 of x's leading shape, for the backward call.
     ``out is x`` normalises in place.
     """
-    import torch
     key = ("norm", eps, _sig(x), _sig(weight), _sig(bias), _sig(out), _sig(mean), _sig(rstd))
     c = _CALLS.get(key) or _remember(key, _norm_forward_call(x, weight, bias, eps, out, mean, rstd))
     if out is None:
-        out = _fresh(x, c.dense)
+        out = c.new(x)
     if mean is None:
-        mean = torch.empty(c.lead, dtype=torch.float32, device=c.device)
+        mean = c.empty(c.lead, dtype=c.f32, device=c.device)
     if rstd is None:
-        rstd = torch.empty(c.lead, dtype=torch.float32, device=c.device)
-    _check(load().mhla_layernorm_forward(x.data_ptr(), _ptr(weight), _ptr(bias), c.ref, out.data_ptr(),
-                                         mean.data_ptr(), rstd.data_ptr(), _stream_handle(stream, key[2][3])),
-           "mhla_layernorm_forward")
+        rstd = c.empty(c.lead, dtype=c.f32, device=c.device)
+    status = c.call(x.data_ptr(), _ptr(weight), _ptr(bias), c.ref, out.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                    c.stream(stream))
+    if status:
+        raise MhlaError(status, "mhla_layernorm_forward")
     return out, mean, rstd
 
 
@@ -754,8 +764,8 @@ def _norm_backward_call(dy, x, mean, rstd, weight, dx, dweight, dbias, params):
         if t is not None and not params:
             raise ValueError(f"{name} needs params=True")
         _flat(name, t, x, torch.float32, (p.cols,))
-    return _Call(p, mhla_layernorm_backward_workspace_bytes(p) if params else 0, dense=x.is_contiguous(),
-                 cols=p.cols, device=x.device)
+    return _Call("mhla_layernorm_backward", x, p, mhla_layernorm_backward_workspace_bytes(p) if params else 0,
+                 new=_fresh(x), cols=p.cols)
 
 
 def mhla_layernorm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None, workspace=None,
@@ -766,23 +776,22 @@ def mhla_layernorm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=Non
     fixed order; ``params=False`` leaves them out (None).  ``dx is dy`` or
     ``dx is x`` overwrites that input.
     """
-    import torch
     key = ("norm backward", params, _sig(dy), _sig(x), _sig(mean), _sig(rstd), _sig(weight), _sig(dx), _sig(dweight),
            _sig(dbias))
     c = _CALLS.get(key) or _remember(key, _norm_backward_call(dy, x, mean, rstd, weight, dx, dweight, dbias, params))
     if dx is None:
-        dx = _fresh(x, c.dense)
+        dx = c.new(x)
     ws_bytes = 0
     if params:
         if dweight is None:
-            dweight = torch.empty(c.cols, dtype=torch.float32, device=c.device)
+            dweight = c.empty(c.cols, dtype=c.f32, device=c.device)
         if dbias is None:
-            dbias = torch.empty(c.cols, dtype=torch.float32, device=c.device)
-        workspace, ws_bytes = c.workspace(workspace, c.device)
-    _check(load().mhla_layernorm_backward(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(),
-                                          c.ref, dx.data_ptr(), _ptr(dweight), _ptr(dbias),
-                                          _ptr(workspace) if params else None, ws_bytes,
-                                          _stream_handle(stream, key[3][3])), "mhla_layernorm_backward")
+            dbias = c.empty(c.cols, dtype=c.f32, device=c.device)
+        workspace, ws_bytes = c.workspace(workspace)
+    status = c.call(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(), c.ref, dx.data_ptr(),
+                    _ptr(dweight), _ptr(dbias), _ptr(workspace) if params else None, ws_bytes, c.stream(stream))
+    if status:
+        raise MhlaError(status, "mhla_layernorm_backward")
     return dx, dweight, dbias
 
 
@@ -828,7 +837,7 @@ def _decay_forward_call(q, k, v, log_decay, state, lengths, scale, layout, varia
     p, axes = _decay_params(q, k, v, log_decay, scale, layout, variant)
     _set_output(p.out, "out", out, q, v.shape, axes)
     shape = _decay_side(p, q, lengths, state=state, state_out=state_out)
-    return _Call(p, mhla_decay_workspace_bytes(p), dense=v.is_contiguous(), shape=shape, device=q.device)
+    return _Call("mhla_decay_forward", q, p, mhla_decay_workspace_bytes(p), new=_fresh(v), shape=shape)
 
 
 def mhla_decay_forward(q, k, v, log_decay, state=None, lengths=None, scale: float = 1.0, layout: str = "bhnd",
@@ -842,19 +851,19 @@ def mhla_decay_forward(q, k, v, log_decay, state=None, lengths=None, scale: floa
     zeros); ``state_out is state`` updates it in place.  ``lengths``: int32
     [B] for sequences padded to N; rows past a length come out as zeros.
     """
-    import torch
     key = ("decay", scale, layout, variant, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(state), _sig(lengths),
            _sig(out), _sig(state_out))
     c = _CALLS.get(key) or _remember(key, _decay_forward_call(q, k, v, log_decay, state, lengths, scale, layout,
                                                               variant, out, state_out))
     if out is None:
-        out = _fresh(v, c.dense)
+        out = c.new(v)
     if state_out is None:
-        state_out = torch.empty(c.shape, dtype=torch.float32, device=c.device)
-    workspace, ws_bytes = c.workspace(workspace, c.device)
-    _check(load().mhla_decay_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths),
-                                     _ptr(state), c.ref, out.data_ptr(), state_out.data_ptr(), _ptr(workspace),
-                                     ws_bytes, _stream_handle(stream, key[4][3])), "mhla_decay_forward")
+        state_out = c.empty(c.shape, dtype=c.f32, device=c.device)
+    workspace, ws_bytes = c.workspace(workspace)
+    status = c.call(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths), _ptr(state), c.ref,
+                    out.data_ptr(), state_out.data_ptr(), _ptr(workspace), ws_bytes, c.stream(stream))
+    if status:
+        raise MhlaError(status, "mhla_decay_forward")
     return out, state_out
 
 
@@ -874,8 +883,8 @@ def _decay_backward_call(q, k, v, log_decay, dout, state, dstate_out, lengths, s
     _set_output(p.dk, "dk", dk, q, q.shape, axes)
     _set_output(p.dv, "dv", dv, q, v.shape, axes)
     shape = _decay_side(p, q, lengths, state=state, dstate_out=dstate_out, dstate=dstate)
-    return _Call(p, mhla_decay_backward_workspace_bytes(p), q_dense=q.is_contiguous(), k_dense=k.is_contiguous(),
-                 v_dense=v.is_contiguous(), shape=shape, device=q.device)
+    return _Call("mhla_decay_backward", q, p, mhla_decay_backward_workspace_bytes(p), new_q=_fresh(q), new_k=_fresh(k),
+                 new_v=_fresh(v), shape=shape)
 
 
 def mhla_decay_backward(q, k, v, log_decay, dout, state=None, dstate_out=None, lengths=None, scale: float = 1.0,
@@ -888,21 +897,21 @@ def mhla_decay_backward(q, k, v, log_decay, dout, state=None, dstate_out=None, l
     [B, H, dk, dv]; None without one, unless a tensor is given for it).
     Arguments as in the forward call.
     """
-    import torch
     key = ("decay backward", scale, layout, variant, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(dout),
            _sig(state), _sig(dstate_out), _sig(lengths), _sig(dq), _sig(dk), _sig(dv), _sig(dstate))
     c = _CALLS.get(key) or _remember(key, _decay_backward_call(q, k, v, log_decay, dout, state, dstate_out, lengths,
                                                                scale, layout, variant, dq, dk, dv, dstate))
-    dq = _fresh(q, c.q_dense) if dq is None else dq
-    dk = _fresh(k, c.k_dense) if dk is None else dk
-    dv = _fresh(v, c.v_dense) if dv is None else dv
+    dq = c.new_q(q) if dq is None else dq
+    dk = c.new_k(k) if dk is None else dk
+    dv = c.new_v(v) if dv is None else dv
     if dstate is None and state is not None:
-        dstate = torch.empty(c.shape, dtype=torch.float32, device=c.device)
-    workspace, ws_bytes = c.workspace(workspace, c.device)
-    _check(load().mhla_decay_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths),
-                                      _ptr(state), dout.data_ptr(), _ptr(dstate_out), c.ref, dq.data_ptr(),
-                                      dk.data_ptr(), dv.data_ptr(), _ptr(dstate), _ptr(workspace), ws_bytes,
-                                      _stream_handle(stream, key[4][3])), "mhla_decay_backward")
+        dstate = c.empty(c.shape, dtype=c.f32, device=c.device)
+    workspace, ws_bytes = c.workspace(workspace)
+    status = c.call(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths), _ptr(state),
+                    dout.data_ptr(), _ptr(dstate_out), c.ref, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dstate),
+                    _ptr(workspace), ws_bytes, c.stream(stream))
+    if status:
+        raise MhlaError(status, "mhla_decay_backward")
     return dq, dk, dv, dstate
 
 
@@ -929,7 +938,7 @@ def _decay_step_call(q, k, v, log_decay, state, scale, out, state_out):
         p.out.batch, p.out.head = out.stride(0), out.stride(1)
     else:
         p.out.batch, p.out.head = v.shape[1] * v.shape[2], v.shape[2]
-    return _Call(p, dense=v.is_contiguous())
+    return _Call("mhla_decay_step", q, p, new=_fresh(v))
 
 
 def mhla_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, state_out=None, stream=None):
@@ -941,9 +950,10 @@ def mhla_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, sta
     key = ("decay step", scale, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(state), _sig(out), _sig(state_out))
     c = _CALLS.get(key) or _remember(key, _decay_step_call(q, k, v, log_decay, state, scale, out, state_out))
     if out is None:
-        out = _fresh(v, c.dense)
+        out = c.new(v)
     at = state.data_ptr()
-    _check(load().mhla_decay_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), at, c.ref,
-                                  out.data_ptr(), at if state_out is None else state_out.data_ptr(),
-                                  _stream_handle(stream, key[2][3])), "mhla_decay_step")
+    status = c.call(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), at, c.ref, out.data_ptr(),
+                    at if state_out is None else state_out.data_ptr(), c.stream(stream))
+    if status:
+        raise MhlaError(status, "mhla_decay_step")
     return out
