@@ -24,6 +24,9 @@ bool on_tensor_cores(const mhla_decay_params* p) {
   return p->dtype == MHLA_DTYPE_BF16 && p->variant != MHLA_DECAY_SIMT;
 }
 
+// The tcgen05 kernel takes 128-token chunks of 64-entry rows.
+bool big_tiles(int dx, int dz, int tokens) { return dx == 64 && dz % 64 == 0 && tokens >= 256; }
+
 // Segments of a pass.  CTAs (units x slices of 64 columns x segments) run in
 // waves of those that are resident at once: three on every SM, two with DX =
 // 128 and on the CUDA cores.  A segment costs its tokens and about a hundred
@@ -36,7 +39,7 @@ constexpr int kSegQuantum = 128, kSegMost = 64, kSegStart = 100;
 
 void plan_segments(const mhla_decay_params* p, int dx, int dz, int* nseg, int* seg_len) {
   const int64_t ctas = (int64_t)p->batch * p->heads * (dz > 64 ? dz / 64 : 1);
-  const int64_t slots = (on_tensor_cores(p) && dx < 128 ? 3 : 2) * kOpsSms;
+  const int64_t slots = (on_tensor_cores(p) && dx < 128 && !big_tiles(dx, dz, p->tokens) ? 3 : 2) * kOpsSms;
   *nseg = 1;
   *seg_len = (p->tokens + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
   double best = (double)((ctas + slots - 1) / slots) * (*seg_len + kSegStart);
@@ -71,7 +74,7 @@ RowTensor state_tensor(const mhla_decay_params* p, const float* ptr) {
 
 bool state_ok(const RowTensor& t) { return row_tensor_ok(t, false) && (uintptr_t)t.ptr % 16 == 0; }
 
-DecayPass pass_of(const mhla_decay_params* p, int dx, int dz) {
+DecayPass pass_of(const mhla_decay_params* p, int dx, int dz, unsigned int* err) {
   DecayPass a = {};
   a.B = p->batch;
   a.H = p->heads;
@@ -80,6 +83,7 @@ DecayPass pass_of(const mhla_decay_params* p, int dx, int dz) {
   a.DZ = dz;
   plan_segments(p, dx, dz, &a.nseg, &a.seg_len);
   a.launches = 3;
+  a.err = err;
   return a;
 }
 
@@ -106,7 +110,8 @@ mhla_status copy_state(const mhla_decay_params* p, const float* from, float* to,
 }
 
 cudaError_t launch_pass(const DecayPass& a, const mhla_decay_params* p, cudaStream_t s) {
-  return on_tensor_cores(p) ? launch_decay_mma(a, s) : launch_decay_simt(a, p->dtype, s);
+  if (!on_tensor_cores(p)) return launch_decay_simt(a, p->dtype, s);
+  return big_tiles(a.DX, a.DZ, a.N) && a.vec ? launch_decay_tc(a, s) : launch_decay_mma(a, s);
 }
 
 // Whether `out` shares memory with none of `in`.
@@ -155,7 +160,9 @@ mhla_status mhla_decay_forward(const void* q, const void* k, const void* v, cons
     return MHLA_ERR_INVALID_ARG;
   Scratch scratch;
   if ((st = scratch.take(workspace, workspace_bytes, need, s)) != MHLA_OK) return st;
-  DecayPass a = pass_of(p, p->key_dim, p->value_dim);
+  unsigned int* err = nullptr;
+  if ((st = ops_error_ptr(&err)) != MHLA_OK) return scratch.give_back(st);
+  DecayPass a = pass_of(p, p->key_dim, p->value_dim, err);
   set_rows(a, in[0], p->q, in[1], p->k, in[2], p->v, to, p->out);
   a.g = log_decay;
   a.lengths = lengths;
@@ -218,7 +225,9 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
   float* seg = reinterpret_cast<float*>(scratch.ptr());
   const int dkey = p->key_dim, dval = p->value_dim;
 
-  DecayPass a = pass_of(p, dval, dkey);  // dq
+  unsigned int* err = nullptr;
+  if ((st = ops_error_ptr(&err)) != MHLA_OK) return scratch.give_back(st);
+  DecayPass a = pass_of(p, dval, dkey, err);  // dq
   set_rows(a, in[3], p->dout, in[2], p->v, in[1], p->k, out[0], p->dq);
   a.g = log_decay;
   a.lengths = lengths;
@@ -233,7 +242,7 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
 
   // dk and dv carry the same states, transposed: the segments' own are formed
   // once, in dv's orientation.
-  DecayPass c = pass_of(p, dkey, dval);  // dv, and the gradient of the first state
+  DecayPass c = pass_of(p, dkey, dval, err);  // dv, and the gradient of the first state
   set_rows(c, in[1], p->k, in[0], p->q, in[3], p->dout, out[2], p->dv);
   c.g = log_decay;
   c.lengths = lengths;
@@ -281,7 +290,7 @@ mhla_status mhla_decay_step(const void* q, const void* k, const void* v, const f
   if (!apart_from_all(to, in, 5) || !row_tensors_apart(to, ts) || !apart_from_all(ts, in, 4))
     return MHLA_ERR_INVALID_ARG;
   if (state_out != state_in && !row_tensors_apart(ts, in[4])) return MHLA_ERR_INVALID_ARG;
-  DecayPass a = pass_of(p, p->key_dim, p->value_dim);
+  DecayPass a = pass_of(p, p->key_dim, p->value_dim, nullptr);
   set_rows(a, in[0], p->q, in[1], p->k, in[2], p->v, to, p->out);
   a.g = log_decay;
   a.s_in = state_in;

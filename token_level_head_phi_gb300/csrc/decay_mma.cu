@@ -20,6 +20,7 @@
 
 #include "common.cuh"
 #include "decay.h"
+#include "decay_tile.cuh"
 #include "ops.h"
 #include "tc_host.h"
 
@@ -29,22 +30,6 @@ namespace {
 constexpr int C = 64;  // tokens of a chunk
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-// Byte offset of 16-byte piece `piece` of row `row` in a tile of D-entry bf16
-// rows: pieces are permuted so that eight rows' pieces of one column fall into
-// different banks.
-template <int D>
-__device__ __forceinline__ uint32_t tile_off(int row, int piece) {
-  constexpr int kPieces = D / 8;
-  if constexpr (kPieces >= 8)
-    return (uint32_t)(row * (D * 2) + ((piece ^ (row & 7)) << 4));
-  else
-    return (uint32_t)(row * (D * 2) + ((piece ^ ((row / (8 / kPieces)) & (kPieces - 1))) << 4));
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -71,24 +56,6 @@ __device__ __forceinline__ void mma0(float (&d)[4], const uint32_t (&a)[4], uint
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// Two bf16 values times their weights, as sums of PARTS bf16 parts (8 bits each).
-template <int PARTS>
-__device__ __forceinline__ void scale_split(uint32_t v, float w0, float w1, uint32_t (&o)[PARTS]) {
-  float a = lo_f(v) * w0, b = hi_f(v) * w1;
-#pragma unroll
-  for (int i = 0; i < PARTS; ++i) {
-    o[i] = pack2(a, b);
-    a -= lo_f(o[i]), b -= hi_f(o[i]);
-  }
-}
-
 __device__ __forceinline__ void stsm4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
@@ -122,56 +89,6 @@ struct alignas(16) MmaSmem {
   float4 wt[OUT ? 4 : 1][OUT ? 32 : 1];  // a lane's weights of a 16 x 16 score tile: off (2), on (2) the diagonal
   float uw[2][C];   // weights of the chunk's tokens in the state: full chunks, the last one
   float pw[C + 1];  // lambda^n
-};
-
-// Copies ROWS rows of chunk after chunk of one tensor into tiles, by THREADS
-// threads; rows from n on are zeros.  A thread takes the same 16-byte piece of
-// every STEP-th row.
-template <int D, int ROWS, int THREADS>
-struct RowLoader {
-  static constexpr int kPieces = D / 8;
-  static constexpr int kStep = THREADS / kPieces;  // rows taken at a time
-  static constexpr int kTurns = ROWS / kStep;
-  static_assert(THREADS % kPieces == 0 && ROWS % kStep == 0, "");
-  const __nv_bfloat16* src;  // this thread's piece of its first row
-  int64_t step;              // elements from token to token of the pass
-  int row, piece;
-
-  __device__ __forceinline__ void init(const __nv_bfloat16* first, int64_t token_step, int r0, int thread) {
-    row = r0 + thread / kPieces;
-    piece = thread % kPieces;
-    step = token_step;
-    src = first + row * token_step + piece * 8;
-  }
-  __device__ __forceinline__ void load(__nv_bfloat16* tile, int n, bool vec) {
-    const __nv_bfloat16* at = src;
-    if (vec && n == C) {
-#pragma unroll
-      for (int i = 0; i < kTurns; ++i) {
-        const uint32_t dst = smem_addr(tile) + tile_off<D>(row + i * kStep, piece);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(at) : "memory");
-        at += kStep * step;
-      }
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < kTurns; ++i) {
-        const int r = row + i * kStep;
-        const bool live = r < n;
-        alignas(16) __nv_bfloat16 v[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __float2bfloat16_rn(0.f);
-        if (live && vec) {
-          *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(at);
-        } else if (live) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = at[j];
-        }
-        *reinterpret_cast<uint4*>(reinterpret_cast<char*>(tile) + tile_off<D>(r, piece)) = *reinterpret_cast<uint4*>(v);
-        at += kStep * step;
-      }
-    }
-    src += C * step;
-  }
 };
 
 // OUT: the pass itself; otherwise only the segment's own final state.
@@ -208,8 +125,8 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
   float* segs = p.seg + (p.nseg > 1 ? (int64_t)unit * p.nseg * one : 0);
   const bool vec = p.vec != 0;
 
-  RowLoader<DX, C, kThreads> ly;
-  RowLoader<DZS, C, kThreads> lz;
+  RowLoader<DX, C, C, kThreads> ly;
+  RowLoader<DZS, C, C, kThreads> lz;
   ly.init(y, sign * p.sy.token, 0, tid);
   lz.init(z, sign * p.sz.token, 0, tid);
   auto fetch = [&](int c0) {
@@ -219,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(
   };
   // x has one buffer: the warp that has read a row tile refills it
   auto fetch_x = [&](int c0, int tile) {
-    RowLoader<DX, 16, 32> lx;
+    RowLoader<DX, C, 16, 32> lx;
     lx.init(x + sign * c0 * p.sx.token, sign * p.sx.token, tile * 16, lane);
     lx.load(sm.x, min(C, valid - c0), vec);
   };

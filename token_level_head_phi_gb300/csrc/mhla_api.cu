@@ -77,6 +77,12 @@ mhla_status device_error_ptr(unsigned int** out) {
   return MHLA_OK;
 }
 
+}  // namespace
+
+mhla_status ops_error_ptr(unsigned int** out) { return device_error_ptr(out); }
+
+namespace {
+
 // Shape and option checks; fills the plan without touching the device.
 // split_units: the number of (batch, head) units the split of long blocks is
 // sized for (0: this problem's own); a group of a larger problem passes the

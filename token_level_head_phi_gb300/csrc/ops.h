@@ -13,6 +13,9 @@ namespace mhla {
 // Keeps the text of a CUDA error for mhla_last_error_string.
 mhla_status record_cuda_error(cudaError_t e);
 
+// The device error word that kernels with bounded waits write.
+mhla_status ops_error_ptr(unsigned int** out);
+
 constexpr int kOpsSms = 152;  // SMs of a GB300: grids are sized in multiples of it
 
 inline size_t ops_elem(int dtype) { return dtype == MHLA_DTYPE_BF16 ? 2 : 4; }
