@@ -23,6 +23,8 @@
 // Columns of tensor memory (256 of 512 a CTA): D 0-127, overlaid by U once P
 // is formed; P 128-191; O 192-255.  The first launch (OUT = false) forms the
 // states alone: U 0-127.
+#include <type_traits>
+
 #include "decay.h"
 #include "decay_tile.cuh"
 #include "ops.h"
@@ -52,7 +54,7 @@ struct Layout {
   static constexpr uint32_t tail = OUT ? 6 * kTile + kTile / 2 : 6 * kTile;
   static constexpr uint32_t bytes = tail + 1024;
 };
-struct Tail {
+struct alignas(16) Tail {
   float tab[64];     // lambda^d of the diagonal block at 31 + d, 0 for d < 0
   float cw[32];      // lambda^(32 - j)
   float p32[4];      // lambda^(32 m)
@@ -110,16 +112,17 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
     tmem_relinquish();
   }
 
-  RowLoader<D, C, C, kWork> lx, ly, lz;
-  if (tid < kWork) {
+  // the ninth warp loads the chunks and issues the products
+  RowLoader<D, C, C, 32> lx, ly, lz;
+  if (warp == kWork / 32) {
     if (OUT)
-      lx.init(static_cast<const T*>(p.x) + b * p.sx.batch + h * p.sx.head + t0 * p.sx.token, sign * p.sx.token, 0, tid);
-    ly.init(static_cast<const T*>(p.y) + b * p.sy.batch + h * p.sy.head + t0 * p.sy.token, sign * p.sy.token, 0, tid);
-    lz.init(static_cast<const T*>(p.z) + b * p.sz.batch + h * p.sz.head + t0 * p.sz.token + z0, sign * p.sz.token, 0, tid);
+      lx.init(static_cast<const T*>(p.x) + b * p.sx.batch + h * p.sx.head + t0 * p.sx.token, sign * p.sx.token, 0, lane);
+    ly.init(static_cast<const T*>(p.y) + b * p.sy.batch + h * p.sy.head + t0 * p.sy.token, sign * p.sy.token, 0, lane);
+    lz.init(static_cast<const T*>(p.z) + b * p.sz.batch + h * p.sz.head + t0 * p.sz.token + z0, sign * p.sz.token, 0, lane);
     if (valid > 0) {
       ly.load(reinterpret_cast<T*>(mem + L::y), min(C, valid), true);
-      lz.load(reinterpret_cast<T*>(mem + L::z), min(C, valid), true);
       if (OUT) lx.load(reinterpret_cast<T*>(mem + L::x), min(C, valid), true);
+      lz.load(reinterpret_cast<T*>(mem + L::z), min(C, valid), true);
     }
   }
   if (tid < 64) {
@@ -157,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
   const int row = 32 * q + lane;
   const float2 w_read = decay_power(g, row + p.e);
   const float read = (w_read.x + w_read.y) * p.read;
+  const uint64_t read2 = pair(read, read);
   const float2 w_lane = decay_power(g, lane);
   const float lane_score = (w_lane.x + w_lane.y) * p.score;
   const int j_row = tid & (C - 1);
@@ -185,7 +189,11 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
     for (int c0 = 0; c0 < valid; c0 += C) {
       const uint32_t st = (uint32_t)(c0 / C) & 1u;
       const uint32_t ya = base + L::y + st * kTile, za = base + L::z + st * kTile;
-      if (__syncthreads_or(0)) break;
+      const bool more = c0 + C < valid;
+      const int n_next = min(C, valid - c0 - C);
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async();
+      if (__syncthreads_or(!ok)) break;
       if (OUT && lane == 0) {
         tc_fence_after();
         const uint64_t xd = sdesc_sw128(base + L::x, 0u, 1024u), yd = sdesc_sw128(ya, 0u, 1024u);
@@ -197,7 +205,15 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
         umma_commit(bar_a);
       }
       __syncwarp();
-      if (__syncthreads_or(0)) break;
+      if (more) {
+        ly.load(reinterpret_cast<T*>(mem + L::y + (st ^ 1u) * kTile), n_next, true);
+        lz.load(reinterpret_cast<T*>(mem + L::z + (st ^ 1u) * kTile), n_next, true);
+        if (OUT && !exact) {
+          ok = mbar_wait(bar_a, st, p.err, 0xd03, abort_flag);
+          lx.load(reinterpret_cast<T*>(mem + L::x), n_next, true);
+        }
+      }
+      if (__syncthreads_or(!ok)) break;
       if (lane == 0) {
         tc_fence_after();
         const uint64_t zd = sdesc_sw128(za, 0u, 1024u);
@@ -216,81 +232,99 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
         umma_commit(bar_b);
       }
       __syncwarp();
+      if (OUT && more && exact) {  // x has held the third part of w Y
+        ok = mbar_wait(bar_b, st, p.err, 0xd04, abort_flag);
+        lx.load(reinterpret_cast<T*>(mem + L::x), n_next, true);
+      }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     for (int c0 = 0; c0 < valid; c0 += C) {
       const int n = min(C, valid - c0);
       const uint32_t st = (uint32_t)(c0 / C) & 1u;
-      const bool more = c0 + C < valid;
-      const int n_next = min(C, valid - c0 - C);
       uint8_t* yt = mem + L::y + st * kTile;
-      asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async();
       if (__syncthreads_or(!ok)) break;  // the chunk and the state's copy are there
-      if (more) {
-        ly.load(reinterpret_cast<T*>(mem + L::y + (st ^ 1u) * kTile), n_next, true);
-        lz.load(reinterpret_cast<T*>(mem + L::z + (st ^ 1u) * kTile), n_next, true);
-      }
       // half a row of w Y; a tile's pieces are read and written by one thread
       float wj = (w_full.x + w_full.y) * p.update;
       if (n < C) {
         const float2 w = decay_power(g, max(n - j_row - p.e, 0));
         wj = (w.x + w.y) * p.update;
       }
-      uint4 hi[4];
-      uint32_t lo[16];
+      const uint64_t wj2 = pair(wj, wj);
       const int piece0 = 4 * (tid >> 7);
+      // pieces i of the row as PARTS parts; the first part takes the row's place
+      auto split = [&](auto parts, auto&& first) {
+        constexpr int kParts = decltype(parts)::value;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t off = tile_off<D>(j_row, piece0 + i);
-        const uint4 v = *reinterpret_cast<const uint4*>(yt + off);
-        uint32_t a[3], c[3], d[3], e[3];
-        scale_split<3>(v.x, wj, wj, a);
-        scale_split<3>(v.y, wj, wj, c);
-        scale_split<3>(v.z, wj, wj, d);
-        scale_split<3>(v.w, wj, wj, e);
-        hi[i] = make_uint4(a[0], c[0], d[0], e[0]);
-        *reinterpret_cast<uint4*>(mem + L::mid + off) = make_uint4(a[1], c[1], d[1], e[1]);
-        lo[4 * i] = a[2], lo[4 * i + 1] = c[2], lo[4 * i + 2] = d[2], lo[4 * i + 3] = e[2];
-      }
-      if (OUT) {
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t off = tile_off<D>(j_row, piece0 + i);
+          const uint4 v = *reinterpret_cast<const uint4*>(yt + off);
+          uint32_t a[kParts], c[kParts], d[kParts], e[kParts];
+          scale_split2<kParts>(v.x, wj2, a);
+          scale_split2<kParts>(v.y, wj2, c);
+          scale_split2<kParts>(v.z, wj2, d);
+          scale_split2<kParts>(v.w, wj2, e);
+          first(i, off, make_uint4(a[0], c[0], d[0], e[0]));
+          *reinterpret_cast<uint4*>(mem + L::mid + off) = make_uint4(a[1], c[1], d[1], e[1]);
+          if constexpr (kParts == 3)
+            *reinterpret_cast<uint4*>(mem + L::lo + off) = make_uint4(a[2], c[2], d[2], e[2]);
+        }
+      };
+      using Two = std::integral_constant<int, 2>;
+      using Three = std::integral_constant<int, 3>;
+      auto in_place = [&](int, uint32_t off, uint4 v) { *reinterpret_cast<uint4*>(yt + off) = v; };
+      if (OUT && !exact) {  // while the first products still read the rows
+        uint4 hi[4];
+        split(Two(), [&](int i, uint32_t, uint4 v) { hi[i] = v; });
         ok = mbar_wait(bar_a, st, p.err, 0xd01, abort_flag);
         tc_fence_after();
-      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t off = tile_off<D>(j_row, piece0 + i);
-        *reinterpret_cast<uint4*>(yt + off) = hi[i];
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(yt + tile_off<D>(j_row, piece0 + i)) = hi[i];
+      } else {
+        if (OUT) {
+          ok = mbar_wait(bar_a, st, p.err, 0xd01, abort_flag);
+          tc_fence_after();
+        }
         if (exact)
-          *reinterpret_cast<uint4*>(mem + L::lo + off) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+          split(Three(), in_place);
+        else
+          split(Two(), in_place);
       }
       if (OUT) {
-        if (more && !exact) lx.load(reinterpret_cast<T*>(mem + L::x), n_next, true);
         float v[32];
         tmem_ld32(tmq + kColO + 32 * half, v);
         tmem_wait_ld();
         uint32_t r[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i] * read);
+        for (int i = 0; i < 16; ++i) {
+          const float2 f = unpair(mul2(pair(v[2 * i], v[2 * i + 1]), read2));
+          r[2 * i] = __float_as_uint(f.x), r[2 * i + 1] = __float_as_uint(f.y);
+        }
         tmem_st32(tmq + kColO + 32 * half, r);
         // P in blocks of 32 columns up to the diagonal, shared out over the
         // two warps of a row
-        const int blocks = q + 1, split = (blocks + 1) / 2;
-        for (int k = half ? split : 0; k < (half ? blocks : split); ++k) {
+        const int blocks = q + 1, middle = (blocks + 1) / 2;
+        for (int k = half ? middle : 0; k < (half ? blocks : middle); ++k) {
           tmem_ld32(tmq + 32 * k, v);
           tmem_wait_ld();
+          uint32_t pk[16];
           if (k == q) {
             // masked entries are dropped by selection: their scores may be infinite
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = lane >= i ? v[i] * tail.tab[31 + lane - i] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = pack2(v[2 * i], v[2 * i + 1]);
           } else {
             const float f = lane_score * tail.p32[q - k - 1];
+            const uint64_t f2 = pair(f, f);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = v[i] * f * tail.cw[i];
+            for (int i = 0; i < 8; ++i) {
+              const float4 c = reinterpret_cast<const float4*>(tail.cw)[i];
+              pk[2 * i] = pack2(mul2(mul2(pair(v[4 * i], v[4 * i + 1]), f2), pair(c.x, c.y)));
+              pk[2 * i + 1] = pack2(mul2(mul2(pair(v[4 * i + 2], v[4 * i + 3]), f2), pair(c.z, c.w)));
+            }
           }
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) pk[i] = pack2(v[2 * i], v[2 * i + 1]);
           tmem_st16(tmq + kColP + 16 * k, pk);
         }
         tmem_wait_st();
@@ -300,14 +334,18 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
       if (__syncthreads_or(!ok)) break;  // P, O and the parts of w Y are there
       ok = mbar_wait(bar_b, st, p.err, 0xd02, abort_flag);
       tc_fence_after();
-      if (OUT && more && exact) lx.load(reinterpret_cast<T*>(mem + L::x), n_next, true);
       const float2 w = n == C ? carry : decay_power(g, n);
       float u0[16], u1[16];
       tmem_ld16(tmq + dx0, u0);
       tmem_ld16(tmq + 64 + dx0, u1);
       tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], w.x, fmaf(s[i], w.y, u0[i] + u1[i]));
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t old = pair(s[2 * i], s[2 * i + 1]);
+        const uint64_t u = add2(pair(u0[2 * i], u0[2 * i + 1]), pair(u1[2 * i], u1[2 * i + 1]));
+        const float2 f = unpair(fma2(old, pair(w.x, w.x), fma2(old, pair(w.y, w.y), u)));
+        s[2 * i] = f.x, s[2 * i + 1] = f.y;
+      }
       if (OUT) {
         publish();
         float v[32];
@@ -332,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
       }
       tc_fence_before();
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 
   __syncthreads();

@@ -31,6 +31,49 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// Pairs of float32 in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  const float2 f = unpair(v);
+  return pack2(f.x, f.y);
+}
+
+// Two bf16 values times their common weight, as sums of PARTS bf16 parts.
+template <int PARTS>
+__device__ __forceinline__ void scale_split2(uint32_t v, uint64_t w, uint32_t (&o)[PARTS]) {
+  const uint64_t minus = pair(-1.f, -1.f);
+  uint64_t a = mul2(pair(lo_f(v), hi_f(v)), w);
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    o[i] = pack2(a);
+    if (i + 1 < PARTS) a = fma2(pair(lo_f(o[i]), hi_f(o[i])), minus, a);
+  }
+}
+
 // Two bf16 values times their weights, as sums of PARTS bf16 parts (8 bits each).
 template <int PARTS>
 __device__ __forceinline__ void scale_split(uint32_t v, float w0, float w1, uint32_t (&o)[PARTS]) {
