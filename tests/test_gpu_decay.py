@@ -119,9 +119,10 @@ def test_forward(b, h, n, dk, dv, layout, with_state, dtype, variant):
 
 
 @pytest.mark.parametrize("dtype,variant", VARIANTS)
+@pytest.mark.parametrize("dim", [32, 64])
 @pytest.mark.parametrize("n,lengths", [(130, [0, 1, 64, 65, 130, 999, -3]), (1300, [0, 1, 255, 256, 257, 1299, 1300])])
-def test_forward_lengths(n, lengths, dtype, variant):
-    b, h, dk, dv = len(lengths), 1, 32, 32
+def test_forward_lengths(n, lengths, dim, dtype, variant):
+    b, h, dk, dv = len(lengths), 1, dim, dim
     q, k, v = (make((b, h, n, dk), dtype, i) for i in (1, 2, 3))
     state = make((b, h, dk, dv), "f32", 4)
     g = decays(h, -0.01)
@@ -141,9 +142,10 @@ def test_forward_lengths(n, lengths, dtype, variant):
 
 
 @pytest.mark.parametrize("dtype,variant", VARIANTS)
+@pytest.mark.parametrize("d", [32, 64])
 @pytest.mark.parametrize("g", [0.0, -math.inf, -40.0, -1e-7, 0.01])
-def test_forward_extreme_decays(g, dtype, variant):
-    n, d = 600, 32
+def test_forward_extreme_decays(g, d, dtype, variant):
+    n = 600
     q, k, v = (make((1, 1, n, d), dtype, i) for i in (1, 2, 3))
     state = make((1, 1, d, d), "f32", 4, 1e4)
     out, state_out = mb.mhla_decay_forward(q, k, v, decays(1, g), state=state, variant=variant)
@@ -205,9 +207,10 @@ def test_backward(b, h, n, dk, dv, layout, with_state, dtype, variant):
                            scale, dtype, variant == "tensor")
 
 
+@pytest.mark.parametrize("d", [32, 64])
 @pytest.mark.parametrize("dtype,variant", VARIANTS)
-def test_backward_lengths(dtype, variant):
-    n, d, lengths = 600, 32, [0, 1, 63, 300, 600]
+def test_backward_lengths(d, dtype, variant):
+    n, lengths = 600, [0, 1, 63, 300, 600]
     b = len(lengths)
     q, k, v, do = (make((b, 1, n, d), dtype, i) for i in (1, 2, 3, 4))
     state, ds = make((b, 1, d, d), "f32", 5), make((b, 1, d, d), "f32", 6)
@@ -277,11 +280,11 @@ def test_later_tokens_leave_earlier_outputs(variant, dtype):
     assert torch.equal(a[:, :, :cut], b[:, :, :cut]) and not torch.equal(a[:, :, cut:], b[:, :, cut:])
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dtype,d", [("bf16", 32), ("f32", 32)])
 @pytest.mark.parametrize("offset", [0, 1, 3])
-def test_strides_and_alignment(offset, dtype):
+def test_strides_and_alignment(offset, dtype, d):
     """q, k, v, out as slices of one fused buffer, aligned or not; a broadcast k."""
-    b, n, h, d = 2, 150, 3, 32
+    b, n, h = 2, 150, 3
     width = 4 * h * d + 5 + (3 if offset == 0 else 0)  # rows 16-byte aligned only for offset 0
     fused = make((b, n, width), dtype, 1)
     part = lambda i: fused[:, :, offset + i * h * d: offset + (i + 1) * h * d].unflatten(2, (h, d))  # noqa: E731
@@ -314,6 +317,7 @@ def test_strides_and_alignment(offset, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n", [100, 1500])
 def test_state_in_place_and_repeatable(n, dtype):
+    """Also the 64-entry rows' own kernel; long enough for several segments in the second case."""
     q, k, v, do = (make((1, 2, n, 64), dtype, i) for i in (1, 2, 3, 4))
     g = decays(2)
     state, ds = make((1, 2, 64, 64), "f32", 5), make((1, 2, 64, 64), "f32", 6)
@@ -358,3 +362,21 @@ def test_other_stream_and_graph():
     graph.replay()
     mb.mhla_decay_step(q[:, :, 0], k[:, :, 0], v[:, :, 0], g, state)
     assert torch.equal(out, want) and torch.equal(st, state)
+
+
+@pytest.mark.parametrize("n", [70, 1000])
+def test_unaligned_rows_of_64(n):
+    """Rows that are not 16-byte aligned take another kernel, with another order of sums and the same bounds."""
+    h, d = 2, 64
+    fused = make((1, n, 4 * h * d + 1), "bf16", 1)
+    q, k, v, out = (fused[:, :, 1 + i * h * d: 1 + (i + 1) * h * d].unflatten(2, (h, d)) for i in range(4))
+    g = decays(h)
+    got, state = mb.mhla_decay_forward(q, k, v, g, layout="bnhd", scale=0.125, out=out)
+    for j in range(h):
+        check_forward(head(q, "bnhd", 0, j), head(k, "bnhd", 0, j), head(v, "bnhd", 0, j), float(g[j]),
+                      head(got, "bnhd", 0, j), f64(state)[0, j], None, None, 0.125, "bf16", True)
+
+
+def test_no_device_error_was_reported():
+    """None of the kernels' bounded waits ran out above."""
+    assert mb.mhla_device_status() == (0, 0)

@@ -24,22 +24,25 @@ bool on_tensor_cores(const mhla_decay_params* p) {
   return p->dtype == MHLA_DTYPE_BF16 && p->variant != MHLA_DECAY_SIMT;
 }
 
-// The tcgen05 kernel takes 128-token chunks of 64-entry rows.
-bool big_tiles(int dx, int dz, int tokens) { return dx == 64 && dz % 64 == 0 && tokens >= 256; }
+// The tcgen05 kernel takes rows of 64 entries (and 16-byte alignment).  It is
+// ahead of the mma.sync kernel at every length there: 128 tokens x 64 heads
+// 6.7 against 7.2 us, 2k tokens 33 against 40, 32k tokens 336 against 405.
+bool big_tiles(int dx, int dz) { return dx == 64 && dz % 64 == 0; }
 
-// Segments of a pass.  CTAs (units x slices of 64 columns x segments) run in
-// waves of those that are resident at once: three on every SM, two with DX =
-// 128 and on the CUDA cores.  A segment costs its tokens and about a hundred
+// Segments of a pass.  CTAs (units x slices of 64 columns x segments; 32
+// columns with mma.sync and DX = 128) run in waves of those that are resident
+// at once: three on every SM with mma.sync, two otherwise.  A segment costs its tokens and about a hundred
 // more for its start, and more than one segment costs the launch that forms
 // their states, measured at 0.6 of the pass itself.  The count with the
 // smallest product wins; segments are of at least 128 tokens and at most 64.
 // (32k tokens x 64 heads: 7 segments, one wave; 2k tokens x 60 heads of 128:
-// 5 segments, two waves, 92 against 105 us with 2 segments in one.)
+// 5 segments, two waves, 92 against 105 us with 2 segments in one wave.)
 constexpr int kSegQuantum = 128, kSegMost = 64, kSegStart = 100;
 
 void plan_segments(const mhla_decay_params* p, int dx, int dz, int* nseg, int* seg_len) {
-  const int64_t ctas = (int64_t)p->batch * p->heads * (dz > 64 ? dz / 64 : 1);
-  const int64_t slots = (on_tensor_cores(p) && dx < 128 && !big_tiles(dx, dz, p->tokens) ? 3 : 2) * kOpsSms;
+  const int slice = on_tensor_cores(p) && dx == 128 ? 32 : 64;
+  const int64_t ctas = (int64_t)p->batch * p->heads * (dz > slice ? dz / slice : 1);
+  const int64_t slots = (on_tensor_cores(p) && !big_tiles(dx, dz) ? 3 : 2) * kOpsSms;
   *nseg = 1;
   *seg_len = (p->tokens + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
   double best = (double)((ctas + slots - 1) / slots) * (*seg_len + kSegStart);
@@ -111,7 +114,7 @@ mhla_status copy_state(const mhla_decay_params* p, const float* from, float* to,
 
 cudaError_t launch_pass(const DecayPass& a, const mhla_decay_params* p, cudaStream_t s) {
   if (!on_tensor_cores(p)) return launch_decay_simt(a, p->dtype, s);
-  return big_tiles(a.DX, a.DZ, a.N) && a.vec ? launch_decay_tc(a, s) : launch_decay_mma(a, s);
+  return big_tiles(a.DX, a.DZ) && a.vec ? launch_decay_tc(a, s) : launch_decay_mma(a, s);
 }
 
 // Whether `out` shares memory with none of `in`.

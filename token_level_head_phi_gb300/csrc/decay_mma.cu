@@ -1,8 +1,8 @@
 // Linear attention with a decay for each head on the tensor cores (bf16; see
 // decay.h for the pass).
 //
-// One CTA of four warps per (unit, segment, slice of at most 64 columns of z)
-// walks its segment in 64-token chunks; the next chunk's rows arrive by
+// One CTA of four warps per (unit, segment, slice of at most 64 columns of z;
+// 32 with 128-entry rows) walks its segment in 64-token chunks; the next chunk's rows arrive by
 // asynchronous copies while the current one is worked on.  Per chunk, with
 // float32 accumulators throughout:
 //   o    = X S                  S in shared memory as bf16, rows scaled by lambda^(i + e)
@@ -93,7 +93,7 @@ struct alignas(16) MmaSmem {
 
 // OUT: the pass itself; otherwise only the segment's own final state.
 template <int DX, int DZS, bool OUT>
-__global__ void __launch_bounds__(kThreads, DX == 128 ? 2 : 3) decay_mma_kernel(const DecayPass p) {
+__global__ void __launch_bounds__(kThreads, 3) decay_mma_kernel(const DecayPass p) {
   extern __shared__ char raw[];
   MmaSmem<DX, DZS, OUT>& sm = *reinterpret_cast<MmaSmem<DX, DZS, OUT>*>(raw);
   // the state's 16-row tiles over the warps; with fewer tiles than warps the
@@ -448,7 +448,11 @@ template <int DX>
 cudaError_t run_z(const DecayPass& p, cudaStream_t s) {
   if (p.DZ == 16) return run<DX, 16>(p, s);
   if (p.DZ == 32) return run<DX, 32>(p, s);
-  return run<DX, 64>(p, s);
+  // rows of 128: with 64 columns a warp holds 128 registers of state, two CTAs
+  // fit an SM, and 2k tokens x 60 ragged heads take 105 us; with 32 columns the
+  // scores are formed twice as often, three CTAs fit, and it is 88 us
+  if constexpr (DX == 128) return run<DX, 32>(p, s);
+  else return run<DX, 64>(p, s);
 }
 
 }  // namespace
