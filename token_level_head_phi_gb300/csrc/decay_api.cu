@@ -24,8 +24,8 @@ bool on_tensor_cores(const mhla_decay_params* p) {
   return p->dtype == MHLA_DTYPE_BF16 && p->variant != MHLA_DECAY_SIMT;
 }
 
-// The tcgen05 kernel takes rows of 64 entries (and 16-byte alignment).  It is
-// ahead of the mma.sync kernel at every length there: 128 tokens x 64 heads
+// The tcgen05 kernel takes rows of 64 entries (and 16-byte alignment, and at
+// least one chunk of 128 tokens).  It is ahead of the mma.sync kernel there: 128 tokens x 64 heads
 // 6.7 against 7.2 us, 2k tokens 33 against 40, 32k tokens 336 against 405.
 bool big_tiles(int dx, int dz) { return dx == 64 && dz % 64 == 0; }
 
@@ -114,7 +114,12 @@ mhla_status copy_state(const mhla_decay_params* p, const float* from, float* to,
 
 cudaError_t launch_pass(const DecayPass& a, const mhla_decay_params* p, cudaStream_t s) {
   if (!on_tensor_cores(p)) return launch_decay_simt(a, p->dtype, s);
-  return big_tiles(a.DX, a.DZ) && a.vec ? launch_decay_tc(a, s) : launch_decay_mma(a, s);
+  if (big_tiles(a.DX, a.DZ) && a.vec && a.N >= 128) {
+    // not supported: strides that a tensor map cannot hold, such as a broadcast axis
+    const cudaError_t e = launch_decay_tc(a, s);
+    if (e != cudaErrorNotSupported) return e;
+  }
+  return launch_decay_mma(a, s);
 }
 
 // Whether `out` shares memory with none of `in`.

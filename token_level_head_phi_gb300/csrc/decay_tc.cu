@@ -8,8 +8,8 @@
 // the products, operands stay in shared and tensor memory, and two CTAs share
 // an SM, each a plain sequence of steps that the other one's steps fill.
 //
-// A CTA of eight working warps and one that issues takes (unit, segment, 64
-// columns of z) in 128-token chunks; row t of a chunk is lane t of tensor
+// A CTA of eight working warps and one that loads (TMA) and issues takes (unit,
+// segment, 64 columns of z) in 128-token chunks; row t of a chunk is lane t of tensor
 // memory and belongs to two threads (a half of the columns each):
 //   D = X Y^T and O = X S                               -> barrier A
 //   w Y in bf16 parts: the high one over Y, the next beside it
@@ -19,6 +19,11 @@
 // U has 64 rows; its operand Z repeats (leading offset 0), so that lanes 64 to
 // 127 hold the same rows again and all eight warps share the state update.
 // Roundings: as in the mma.sync kernel.
+//
+// A pass from the last token to the first (REV) takes its chunks from the end
+// and keeps the tokens of a chunk in their order in memory: row r is place 127
+// - r of the pass, and the triangle of P is mirrored.  The first tokens' chunk
+// then starts before the sequence, where loads give zeros.
 //
 // Columns of tensor memory (256 of 512 a CTA): D 0-127, overlaid by U once P
 // is formed; P 128-191; O 192-255.  The first launch (OUT = false) forms the
@@ -56,9 +61,9 @@ struct Layout {
 };
 struct alignas(16) Tail {
   float tab[64];     // lambda^d of the diagonal block at 31 + d, 0 for d < 0
-  float cw[32];      // lambda^(32 - j)
+  float cw[32];      // lambda^(32 - j), reversed for REV
   float p32[4];      // lambda^(32 m)
-  uint64_t bar[2];
+  uint64_t bar[2], full[2], full_x;
   uint32_t tmem;
   int abort;
 };
@@ -73,8 +78,36 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-template <bool OUT>
-__global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p) {
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+               : "memory");
+}
+
+// A map of rows and the places of its token, head and batch axes (1 to 3,
+// ordered by stride).
+struct RowMap {
+  CUtensorMap map;
+  int token, head, batch;
+};
+struct TcArgs {
+  RowMap x, y, z, o;
+  DecayPass p;
+};
+
+__device__ __forceinline__ int coordinate(const RowMap& m, int axis, int token, int head, int batch) {
+  return m.token == axis ? token : m.head == axis ? head : batch;
+}
+__device__ __forceinline__ void load_rows(uint32_t dst, const RowMap& m, uint32_t bar, int col, int token, int head,
+                                          int batch) {
+  tma_load_4d(dst, &m.map, bar, col, coordinate(m, 1, token, head, batch), coordinate(m, 2, token, head, batch),
+              coordinate(m, 3, token, head, batch), policy_evict_first());
+}
+
+template <bool OUT, bool REV>
+__global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_constant__ TcArgs a) {
+  const DecayPass& p = a.p;
   using L = Layout<OUT>;
   using T = __nv_bfloat16;
   extern __shared__ uint8_t raw[];
@@ -94,43 +127,52 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
   const int valid = max(0, min(end, length) - begin);
   const bool last = seg == (length > 0 ? (length - 1) / p.seg_len : 0);
   const bool exact = p.s_out && (!OUT || last);  // three parts where a final state comes of it
-  const int t0 = valid > 0 ? decay_token(p, begin, length) : 0;
-  const int64_t sign = p.reverse ? -1 : 1;
+  auto first_token = [&](int c0) { return REV ? length - begin - c0 - C : begin + c0; };  // of row 0
   T* o = static_cast<T*>(p.o) + b * p.so.batch + h * p.so.head + z0;
   const int64_t one = (int64_t)D * p.DZ, state = unit * one;
   float* segs = p.seg + (p.nseg > 1 ? (int64_t)unit * p.nseg * one : 0);
 
   const uint32_t bar_a = smem_u32(&tail.bar[0]), bar_b = smem_u32(&tail.bar[1]);
-  if (tid == 0) {
+  const uint32_t full[2] = {smem_u32(&tail.full[0]), smem_u32(&tail.full[1])}, full_x = smem_u32(&tail.full_x);
+  // the ninth warp's first lane loads the chunks and issues the products
+  const bool issuer = tid == kWork;
+  int loaded = 0, loaded_x = 0, seen = 0, seen_x = 0;  // chunks asked for, and waited for
+  auto fetch = [&](int c0) {
+    const uint32_t st = (uint32_t)(c0 / C) & 1u;
+    mbar_arrive_expect_tx(full[st], 2 * kTile);
+    load_rows(base + L::y + st * kTile, a.y, full[st], 0, first_token(c0), h, b);
+    load_rows(base + L::z + st * kTile, a.z, full[st], z0, first_token(c0), h, b);
+    ++loaded;
+  };
+  auto fetch_x = [&](int c0) {
+    mbar_arrive_expect_tx(full_x, kTile);
+    load_rows(base + L::x, a.x, full_x, 0, first_token(c0), h, b);
+    ++loaded_x;
+  };
+  if (issuer) {
     mbar_init(bar_a, 1);
     mbar_init(bar_b, 1);
+    mbar_init(full[0], 1);
+    mbar_init(full[1], 1);
+    mbar_init(full_x, 1);
     tail.abort = 0;
     fence_barrier_init();
+    if (valid > 0) {
+      fetch(0);
+      if (OUT) fetch_x(0);
+    }
   }
   if (warp == kWork / 32) {
+    __syncwarp();
     tmem_alloc(smem_u32(&tail.tmem), kCols);
     tmem_relinquish();
-  }
-
-  // the ninth warp loads the chunks and issues the products
-  RowLoader<D, C, C, 32> lx, ly, lz;
-  if (warp == kWork / 32) {
-    if (OUT)
-      lx.init(static_cast<const T*>(p.x) + b * p.sx.batch + h * p.sx.head + t0 * p.sx.token, sign * p.sx.token, 0, lane);
-    ly.init(static_cast<const T*>(p.y) + b * p.sy.batch + h * p.sy.head + t0 * p.sy.token, sign * p.sy.token, 0, lane);
-    lz.init(static_cast<const T*>(p.z) + b * p.sz.batch + h * p.sz.head + t0 * p.sz.token + z0, sign * p.sz.token, 0, lane);
-    if (valid > 0) {
-      ly.load(reinterpret_cast<T*>(mem + L::y), min(C, valid), true);
-      if (OUT) lx.load(reinterpret_cast<T*>(mem + L::x), min(C, valid), true);
-      lz.load(reinterpret_cast<T*>(mem + L::z), min(C, valid), true);
-    }
   }
   if (tid < 64) {
     const float2 w = decay_power(g, max(tid - 31, 0));
     tail.tab[tid] = tid >= 31 ? (w.x + w.y) * p.score : 0.f;
   } else if (tid < 96) {
     const float2 w = decay_power(g, 32 - lane);
-    tail.cw[lane] = w.x + w.y;
+    tail.cw[REV ? 31 - lane : lane] = w.x + w.y;
   } else if (tid < 100) {
     const float2 w = decay_power(g, 32 * (tid - 96));
     tail.p32[tid - 96] = w.x + w.y;
@@ -156,15 +198,17 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
   };
   if (OUT && tid < kWork) publish();
 
-  // weights of this thread's rows: row t of the outputs, row j of w Y
-  const int row = 32 * q + lane;
-  const float2 w_read = decay_power(g, row + p.e);
+  // weights of this thread's rows, by their places in the pass: row t of the
+  // outputs, row j of w Y
+  const int row = 32 * q + lane, place = REV ? C - 1 - row : row;
+  const int qp = REV ? 3 - q : q, lp = REV ? 31 - lane : lane;  // its block and its place in the block
+  const float2 w_read = decay_power(g, place + p.e);
   const float read = (w_read.x + w_read.y) * p.read;
   const uint64_t read2 = pair(read, read);
-  const float2 w_lane = decay_power(g, lane);
+  const float2 w_lane = decay_power(g, lp);
   const float lane_score = (w_lane.x + w_lane.y) * p.score;
-  const int j_row = tid & (C - 1);
-  const float2 w_full = decay_power(g, C - j_row - p.e);
+  const int j_row = tid & (C - 1), j_place = REV ? C - 1 - j_row : j_row;
+  const float2 w_full = decay_power(g, C - j_place - p.e);
   const float2 carry = decay_power(g, C);
 
   tc_fence_before();
@@ -180,6 +224,8 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
   }
 
   volatile int* abort_flag = &tail.abort;
+  // a chunk with rows past a sequence's length: they hold whatever the padding holds
+  auto dirty = [&](int c0) { return !REV && valid - c0 < C && begin + valid < p.N; };
   bool ok = true;
   if (warp == kWork / 32) {
     // ------------------------------------------------ issues the products
@@ -190,10 +236,13 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
       const uint32_t st = (uint32_t)(c0 / C) & 1u;
       const uint32_t ya = base + L::y + st * kTile, za = base + L::z + st * kTile;
       const bool more = c0 + C < valid;
-      const int n_next = min(C, valid - c0 - C);
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async();
+      if (lane == 0) {
+        ok = mbar_wait(full[st], (uint32_t)(c0 / C >> 1) & 1u, p.err, 0xd06, abort_flag);
+        if (OUT) ok = mbar_wait(full_x, st, p.err, 0xd07, abort_flag) && ok;
+        if (ok) ++seen, seen_x += OUT;
+      }
       if (__syncthreads_or(!ok)) break;
+      if (dirty(c0)) __syncthreads();
       if (OUT && lane == 0) {
         tc_fence_after();
         const uint64_t xd = sdesc_sw128(base + L::x, 0u, 1024u), yd = sdesc_sw128(ya, 0u, 1024u);
@@ -205,14 +254,14 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
         umma_commit(bar_a);
       }
       __syncwarp();
-      if (more) {
-        ly.load(reinterpret_cast<T*>(mem + L::y + (st ^ 1u) * kTile), n_next, true);
-        lz.load(reinterpret_cast<T*>(mem + L::z + (st ^ 1u) * kTile), n_next, true);
+      if (more && lane == 0) {
+        fetch(c0 + C);
         if (OUT && !exact) {
           ok = mbar_wait(bar_a, st, p.err, 0xd03, abort_flag);
-          lx.load(reinterpret_cast<T*>(mem + L::x), n_next, true);
+          fetch_x(c0 + C);
         }
       }
+      __syncwarp();
       if (__syncthreads_or(!ok)) break;
       if (lane == 0) {
         tc_fence_after();
@@ -232,12 +281,17 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
         umma_commit(bar_b);
       }
       __syncwarp();
-      if (OUT && more && exact) {  // x has held the third part of w Y
+      if (OUT && more && exact && lane == 0) {  // x has held the third part of w Y
         ok = mbar_wait(bar_b, st, p.err, 0xd04, abort_flag);
-        lx.load(reinterpret_cast<T*>(mem + L::x), n_next, true);
+        fetch_x(c0 + C);
       }
+      __syncwarp();
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (lane == 0) {  // after an early end: no copy may land once the CTA is gone
+      for (; seen < loaded; ++seen) mbar_wait(full[seen & 1], (uint32_t)(seen >> 1) & 1u, p.err, 0xd08);
+      for (; seen_x < loaded_x; ++seen_x) mbar_wait(full_x, (uint32_t)seen_x & 1u, p.err, 0xd09);
+    }
+    __syncwarp();
   } else {
     for (int c0 = 0; c0 < valid; c0 += C) {
       const int n = min(C, valid - c0);
@@ -245,10 +299,20 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
       uint8_t* yt = mem + L::y + st * kTile;
       fence_proxy_async();
       if (__syncthreads_or(!ok)) break;  // the chunk and the state's copy are there
+      if (dirty(c0)) {
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = n * 8 + tid; i < C * 8; i += kWork) {
+          *reinterpret_cast<uint4*>(yt + 16 * i) = zero;
+          *reinterpret_cast<uint4*>(mem + L::z + st * kTile + 16 * i) = zero;
+          if (OUT) *reinterpret_cast<uint4*>(mem + L::x + 16 * i) = zero;
+        }
+        fence_proxy_async();
+        __syncthreads();
+      }
       // half a row of w Y; a tile's pieces are read and written by one thread
       float wj = (w_full.x + w_full.y) * p.update;
       if (n < C) {
-        const float2 w = decay_power(g, max(n - j_row - p.e, 0));
+        const float2 w = decay_power(g, max(n - j_place - p.e, 0));
         wj = (w.x + w.y) * p.update;
       }
       const uint64_t wj2 = pair(wj, wj);
@@ -304,19 +368,23 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
         tmem_st32(tmq + kColO + 32 * half, r);
         // P in blocks of 32 columns up to the diagonal, shared out over the
         // two warps of a row
-        const int blocks = q + 1, middle = (blocks + 1) / 2;
+        const int blocks = qp + 1, middle = (blocks + 1) / 2;
         for (int k = half ? middle : 0; k < (half ? blocks : middle); ++k) {
-          tmem_ld32(tmq + 32 * k, v);
+          const int kc = REV ? 3 - k : k;  // its place among the columns
+          tmem_ld32(tmq + 32 * kc, v);
           tmem_wait_ld();
           uint32_t pk[16];
-          if (k == q) {
+          if (k == qp) {
             // masked entries are dropped by selection: their scores may be infinite
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = lane >= i ? v[i] * tail.tab[31 + lane - i] : 0.f;
+            for (int i = 0; i < 32; ++i) {
+              const int d = REV ? i - lane : lane - i;
+              v[i] = d >= 0 ? v[i] * tail.tab[31 + d] : 0.f;
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) pk[i] = pack2(v[2 * i], v[2 * i + 1]);
           } else {
-            const float f = lane_score * tail.p32[q - k - 1];
+            const float f = lane_score * tail.p32[qp - k - 1];
             const uint64_t f2 = pair(f, f);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -325,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
               pk[2 * i + 1] = pack2(mul2(mul2(pair(v[4 * i + 2], v[4 * i + 3]), f2), pair(c.z, c.w)));
             }
           }
-          tmem_st16(tmq + kColP + 16 * k, pk);
+          tmem_st16(tmq + kColP + 16 * kc, pk);
         }
         tmem_wait_st();
       }
@@ -351,25 +419,42 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
         float v[32];
         tmem_ld32(tmq + kColO + 32 * half, v);
         tmem_wait_ld();
-        // rows to memory through the warp's own part of a tile, so that eight
-        // rows' 64-byte halves leave together
-        uint8_t* stage = mem + L::mid;
+        // A warp's 32 rows x 64 bytes leave as one TMA store (64-byte swizzle);
+        // a part of a chunk row by row, since a store may not start before the
+        // sequence or run past its length.
+        uint8_t* stage = mem + L::mid + 2048 * warp;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(stage + tile_off<D>(row, 4 * half + i)) =
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) =
               make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
                          pack2(v[8 * i + 4], v[8 * i + 5]), pack2(v[8 * i + 6], v[8 * i + 7]));
-        __syncwarp();
+        const int token = first_token(c0) + 32 * q;
+        if (n == C) {
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_4d(&a.o.map, smem_u32(stage), z0 + 32 * half, coordinate(a.o, 1, token, h, b),
+                         coordinate(a.o, 2, token, h, b), coordinate(a.o, 3, token, h, b));
+            bulk_commit();
+            bulk_wait_read<0>();
+          }
+        } else {
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 32 * q + 8 * i + lane / 4, piece = 4 * half + lane % 4;
-          const uint4 t = *reinterpret_cast<const uint4*>(stage + tile_off<D>(r, piece));
-          if (r < n)
-            __stcs(reinterpret_cast<uint4*>(o + decay_token(p, begin + c0 + r, length) * p.so.token + piece * 8), t);
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + lane / 4, piece = lane % 4;
+            const uint4 t = *reinterpret_cast<const uint4*>(stage + r * 64 + ((piece ^ (r >> 1 & 3)) << 4));
+            const int at = 32 * q + r;
+            if ((REV ? C - 1 - at : at) < n)
+              *reinterpret_cast<uint4*>(o + (int64_t)(token + r) * p.so.token + 32 * half + piece * 8) = t;
+          }
         }
+        __syncwarp();
       }
       tc_fence_before();
     }
+    if (OUT && lane == 0) bulk_wait<0>();
+    __syncwarp();
   }
 
   __syncthreads();
@@ -389,30 +474,69 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const DecayPass p
   for (int i = 0; i < 16; ++i) to[(int64_t)(dx0 + i) * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz] = s[i];
 }
 
-template <bool OUT>
-cudaError_t prepare() {
-  return cudaFuncSetAttribute(decay_tc_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)(Layout<OUT>::bytes + 1024));
+// Axes ordered by stride, as nested as they are in memory.
+bool make_map(RowMap* m, const void* base, const mhla_strides& st, int64_t cols, const DecayPass& p, int box_cols,
+              int box_rows, int swizzle) {
+  struct Axis {
+    int64_t n, stride;
+    int* place;
+    uint32_t box;
+  } ax[3] = {{p.N, st.token, &m->token, (uint32_t)box_rows}, {p.H, st.head, &m->head, 1u}, {p.B, st.batch, &m->batch, 1u}};
+  for (Axis& x : ax) {
+    if (x.n > 1 && x.stride <= 0) return false;  // a broadcast axis
+    if (x.n <= 1) x.stride = (int64_t)1 << 34;   // never stepped along
+  }
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (ax[j].stride < ax[i].stride) {
+        const Axis t = ax[i];
+        ax[i] = ax[j];
+        ax[j] = t;
+      }
+  uint64_t dims[4] = {(uint64_t)cols}, strides[3];
+  uint32_t box[4] = {(uint32_t)box_cols};
+  for (int i = 0; i < 3; ++i) {
+    *ax[i].place = i + 1;
+    dims[i + 1] = (uint64_t)ax[i].n;
+    strides[i] = 2ull * (uint64_t)ax[i].stride;
+    if (strides[i] >= (1ull << 40)) return false;
+    box[i + 1] = ax[i].box;
+  }
+  return encode_tmap_rows(&m->map, base, dims, strides, box, swizzle);
+}
+
+template <bool REV>
+cudaError_t run(const TcArgs& a, cudaStream_t s) {
+  const DecayPass& p = a.p;
+  const unsigned units = (unsigned)(p.B * p.H), slices = (unsigned)(p.DZ / D);
+  cudaError_t e;
+  if (p.nseg > 1 && (p.launches & 1)) {
+    constexpr size_t smem = Layout<false>::bytes + 1024;
+    auto* k = decay_tc_kernel<false, REV>;
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+    k<<<dim3(units, (unsigned)(p.nseg - 1), slices), kThreads, smem, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_decay_scan(p, s)) != cudaSuccess) return e;
+  }
+  if (!(p.launches & 2)) return cudaSuccess;
+  constexpr size_t smem = Layout<true>::bytes + 1024;
+  auto* k = decay_tc_kernel<true, REV>;
+  if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+  const dim3 grid(units, (unsigned)p.nseg, slices);
+  if (p.nseg > 1) return (cudaError_t)launch_pdl(k, grid, dim3(kThreads), smem, s, a);
+  k<<<grid, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_decay_tc(const DecayPass& p, cudaStream_t s) {
-  const unsigned units = (unsigned)(p.B * p.H), slices = (unsigned)(p.DZ / D);
-  cudaError_t e;
-  if (p.nseg > 1 && (p.launches & 1)) {
-    if ((e = prepare<false>()) != cudaSuccess) return e;
-    decay_tc_kernel<false><<<dim3(units, (unsigned)(p.nseg - 1), slices), kThreads, Layout<false>::bytes + 1024, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_decay_scan(p, s)) != cudaSuccess) return e;
-  }
-  if (!(p.launches & 2)) return cudaSuccess;
-  if ((e = prepare<true>()) != cudaSuccess) return e;
-  const dim3 grid(units, (unsigned)p.nseg, slices);
-  constexpr size_t smem = Layout<true>::bytes + 1024;
-  if (p.nseg > 1) return (cudaError_t)launch_pdl(decay_tc_kernel<true>, grid, dim3(kThreads), smem, s, p);
-  decay_tc_kernel<true><<<grid, kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  TcArgs a;
+  a.p = p;
+  if (!make_map(&a.x, p.x, p.sx, p.DX, p, D, C, 128) || !make_map(&a.y, p.y, p.sy, p.DX, p, D, C, 128) ||
+      !make_map(&a.z, p.z, p.sz, p.DZ, p, D, C, 128) || !make_map(&a.o, p.o, p.so, p.DZ, p, 32, 32, 64))
+    return cudaErrorNotSupported;
+  return p.reverse ? run<true>(a, s) : run<false>(a, s);
 }
 
 }  // namespace mhla

@@ -28,6 +28,10 @@ int encode_tmap(CUtensorMap* map, const void* base, int rank, const uint64_t* di
 // Same without swizzle (row-major boxes in shared memory), bf16.
 int encode_tmap_plain(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                       const uint64_t* strides_bytes, const uint32_t* box);
+// A four-dimensional map of bf16 rows (dims[0] entries), 128- or 64-byte
+// swizzle, encoded anew in every call; false where the driver refuses it.
+bool encode_tmap_rows(CUtensorMap* map, const void* base, const uint64_t* dims, const uint64_t* strides_bytes,
+                      const uint32_t* box, int swizzle_bytes);
 inline int encode_tmap_bf16(CUtensorMap* map, const void* base, int rank, const uint64_t* dims,
                             const uint64_t* strides_bytes, const uint32_t* box) {
   return encode_tmap(map, base, rank, dims, strides_bytes, box, false);

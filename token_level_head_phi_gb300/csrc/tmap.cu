@@ -66,8 +66,7 @@ int encode_tmap_plain(CUtensorMap* map, const void* base, int rank, const uint64
 }
 
 namespace {
-int encode_impl(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
-                const uint32_t* box, bool f16, bool swizzle) {
+bool load_encoder() {
   std::call_once(g_enc_once, [] {
     cudaDriverEntryPointQueryResult q;
     void* fn = nullptr;
@@ -76,7 +75,12 @@ int encode_impl(CUtensorMap* map, const void* base, int rank, const uint64_t* di
         q == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
-  if (!g_encode) return (int)cudaErrorNotSupported;
+  return g_encode != nullptr;
+}
+
+int encode_impl(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes,
+                const uint32_t* box, bool f16, bool swizzle) {
+  if (!load_encoder()) return (int)cudaErrorNotSupported;
   MapKey key;
   std::memset(&key, 0, sizeof(key));  // padding bytes take part in the hash and the comparison
   key.base = base;
@@ -118,6 +122,18 @@ int encode_impl(CUtensorMap* map, const void* base, int rank, const uint64_t* di
   return 0;
 }
 }  // namespace
+
+bool encode_tmap_rows(CUtensorMap* map, const void* base, const uint64_t* dims, const uint64_t* strides_bytes,
+                      const uint32_t* box, int swizzle_bytes) {
+  if (!load_encoder()) return false;
+  const cuuint64_t gdim[4] = {dims[0], dims[1], dims[2], dims[3]};
+  const cuuint64_t gstride[3] = {strides_bytes[0], strides_bytes[1], strides_bytes[2]};
+  const cuuint32_t bdim[4] = {box[0], box[1], box[2], box[3]}, estride[4] = {1, 1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gdim, gstride, bdim, estride,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 int encode_token_map(CUtensorMap* map, const Plan& p, const void* base, const ChunkShape& c) {
   const uint32_t box[5] = {64, (uint32_t)c.cw, (uint32_t)c.ch, (uint32_t)c.ct, 1};
