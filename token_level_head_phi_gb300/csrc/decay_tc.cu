@@ -14,8 +14,9 @@
 //   D = X Y^T and O = X S                               -> barrier A
 //   w Y in bf16 parts: the high one over Y, the next beside it
 //   O *= lambda^(t + e), P = D decayed and masked, as bf16 in tensor memory
-//   O += P Z and U = Z^T [parts of w Y]                 -> barrier B
-//   S = lambda^n S + sum of U's parts; O to memory
+//   U = Z^T [parts of w Y]                              -> barrier U
+//   O += P Z                                            -> barrier B
+//   S = lambda^n S + sum of U's parts, then O to memory
 // U has 64 rows; its operand Z repeats (leading offset 0), so that lanes 64 to
 // 127 hold the same rows again and all eight warps share the state update.
 // Roundings: as in the mma.sync kernel.
@@ -63,7 +64,7 @@ struct alignas(16) Tail {
   float tab[64];     // lambda^d of the diagonal block at 31 + d, 0 for d < 0
   float cw[32];      // lambda^(32 - j), reversed for REV
   float p32[4];      // lambda^(32 m)
-  uint64_t bar[2], full[2], full_x;
+  uint64_t bar[4], full[2], full_x;
   uint32_t tmem;
   int abort;
 };
@@ -132,7 +133,8 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
   const int64_t one = (int64_t)D * p.DZ, state = unit * one;
   float* segs = p.seg + (p.nseg > 1 ? (int64_t)unit * p.nseg * one : 0);
 
-  const uint32_t bar_a = smem_u32(&tail.bar[0]), bar_b = smem_u32(&tail.bar[1]);
+  const uint32_t bar_a = smem_u32(&tail.bar[0]), bar_b = smem_u32(&tail.bar[1]), bar_u = smem_u32(&tail.bar[2]);
+  const uint32_t bar_r = smem_u32(&tail.bar[3]);  // the outputs before have been read out of shared memory (8 warps)
   const uint32_t full[2] = {smem_u32(&tail.full[0]), smem_u32(&tail.full[1])}, full_x = smem_u32(&tail.full_x);
   // the ninth warp's first lane loads the chunks and issues the products
   const bool issuer = tid == kWork;
@@ -152,6 +154,8 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
   if (issuer) {
     mbar_init(bar_a, 1);
     mbar_init(bar_b, 1);
+    mbar_init(bar_u, 1);
+    mbar_init(bar_r, kWork / 32);
     mbar_init(full[0], 1);
     mbar_init(full[1], 1);
     mbar_init(full_x, 1);
@@ -255,9 +259,11 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
       }
       __syncwarp();
       if (more && lane == 0) {
+        // the outputs of the chunk before leave through its y
+        if (OUT) ok = mbar_wait(bar_r, st, p.err, 0xd0b, abort_flag);
         fetch(c0 + C);
         if (OUT && !exact) {
-          ok = mbar_wait(bar_a, st, p.err, 0xd03, abort_flag);
+          ok = mbar_wait(bar_a, st, p.err, 0xd03, abort_flag) && ok;
           fetch_x(c0 + C);
         }
       }
@@ -266,10 +272,6 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
       if (lane == 0) {
         tc_fence_after();
         const uint64_t zd = sdesc_sw128(za, 0u, 1024u);
-        if (OUT) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) umma_tmem_a(tm + kColO, tm + kColP + 8u * k, zd + 128 * k, id_p, 1u);
-        }
         const uint64_t wd = sdesc_sw128(ya, base + L::mid - ya, 1024u);
 #pragma unroll
         for (int k = 0; k < 8; ++k) umma_bf16(tm, zd + 128 * k, wd + 128 * k, id_u, k > 0);
@@ -278,11 +280,16 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
 #pragma unroll
           for (int k = 0; k < 8; ++k) umma_bf16(tm + 64u, zd + 128 * k, ld + 128 * k, id_l, 1u);
         }
-        umma_commit(bar_b);
+        umma_commit(bar_u);
+        if (OUT) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) umma_tmem_a(tm + kColO, tm + kColP + 8u * k, zd + 128 * k, id_p, 1u);
+          umma_commit(bar_b);
+        }
       }
       __syncwarp();
       if (OUT && more && exact && lane == 0) {  // x has held the third part of w Y
-        ok = mbar_wait(bar_b, st, p.err, 0xd04, abort_flag);
+        ok = mbar_wait(bar_u, st, p.err, 0xd04, abort_flag);
         fetch_x(c0 + C);
       }
       __syncwarp();
@@ -338,15 +345,24 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
       using Two = std::integral_constant<int, 2>;
       using Three = std::integral_constant<int, 3>;
       auto in_place = [&](int, uint32_t off, uint4 v) { *reinterpret_cast<uint4*>(yt + off) = v; };
+      auto outputs_read = [&]() {
+        if (lane == 0) {
+          bulk_wait_read<0>();
+          mbar_arrive(bar_r);
+        }
+        __syncwarp();
+      };
       if (OUT && !exact) {  // while the first products still read the rows
         uint4 hi[4];
         split(Two(), [&](int i, uint32_t, uint4 v) { hi[i] = v; });
+        outputs_read();
         ok = mbar_wait(bar_a, st, p.err, 0xd01, abort_flag);
         tc_fence_after();
 #pragma unroll
         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(yt + tile_off<D>(j_row, piece0 + i)) = hi[i];
       } else {
         if (OUT) {
+          outputs_read();
           ok = mbar_wait(bar_a, st, p.err, 0xd01, abort_flag);
           tc_fence_after();
         }
@@ -400,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
       tc_fence_before();
       fence_proxy_async();
       if (__syncthreads_or(!ok)) break;  // P, O and the parts of w Y are there
-      ok = mbar_wait(bar_b, st, p.err, 0xd02, abort_flag);
+      ok = mbar_wait(bar_u, st, p.err, 0xd02, abort_flag);
       tc_fence_after();
       const float2 w = n == C ? carry : decay_power(g, n);
       float u0[16], u1[16];
@@ -416,13 +432,15 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
       }
       if (OUT) {
         publish();
+        ok = mbar_wait(bar_b, st, p.err, 0xd0a, abort_flag) && ok;
+        tc_fence_after();
         float v[32];
         tmem_ld32(tmq + kColO + 32 * half, v);
         tmem_wait_ld();
         // A warp's 32 rows x 64 bytes leave as one TMA store (64-byte swizzle);
         // a part of a chunk row by row, since a store may not start before the
         // sequence or run past its length.
-        uint8_t* stage = mem + L::mid + 2048 * warp;
+        uint8_t* stage = yt + 2048 * warp;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) =
@@ -436,7 +454,6 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
             tma_store_4d(&a.o.map, smem_u32(stage), z0 + 32 * half, coordinate(a.o, 1, token, h, b),
                          coordinate(a.o, 2, token, h, b), coordinate(a.o, 3, token, h, b));
             bulk_commit();
-            bulk_wait_read<0>();
           }
         } else {
           __syncwarp();
