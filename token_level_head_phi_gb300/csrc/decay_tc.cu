@@ -27,8 +27,14 @@
 // then starts before the sequence, where loads give zeros.
 //
 // Columns of tensor memory (256 of 512 a CTA): D 0-127, overlaid by U once P
-// is formed; P 128-191; O 192-255.  The first launch (OUT = false) forms the
-// states alone: U 0-127.
+// is formed; P 128-191; O 192-255.
+//
+// The first launch forms the segments' states alone.  A chunk there is a chain
+// of waits (load, split, products, update) that other CTAs' chains fill: where
+// there are CTAs enough for four on every SM, a kernel of its own takes
+// 64-token chunks with four working warps (32k tokens x 64 heads: 293 against
+// 313 us in all); with fewer, this one (OUT = false, U in columns 0-127) is
+// ahead (8k tokens x 32 heads, backward: 138 against 149 us).
 #include <type_traits>
 
 #include "decay.h"
@@ -94,6 +100,7 @@ struct RowMap {
 };
 struct TcArgs {
   RowMap x, y, z, o;
+  RowMap y64, z64;  // in boxes of 64 rows
   DecayPass p;
 };
 
@@ -491,6 +498,188 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
   for (int i = 0; i < 16; ++i) to[(int64_t)(dx0 + i) * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz] = s[i];
 }
 
+// ------------------- the segments' own states, many at once: 64-token chunks
+
+constexpr int kStateChunk = 64;
+constexpr int kStateWork = 128;
+constexpr int kStateThreads = kStateWork + 32;
+constexpr uint32_t kStateTile = kStateChunk * D * 2;
+struct StateLayout {
+  static constexpr uint32_t y = 0, z = 2 * kStateTile, mid = 4 * kStateTile, lo = 5 * kStateTile;
+  static constexpr uint32_t tail = 6 * kStateTile;
+  static constexpr uint32_t bytes = tail + 64;
+};
+struct StateTail {
+  uint64_t bar, full[2];
+  uint32_t tmem;
+  int abort;
+};
+
+// U's first part in columns 0-63, the others in 64-127.
+template <bool REV>
+__global__ void __launch_bounds__(kStateThreads, 4) decay_tc_state_kernel(const __grid_constant__ TcArgs a) {
+  const DecayPass& p = a.p;
+  using L = StateLayout;
+  constexpr int N = kStateChunk;
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
+  uint8_t* mem = raw + (base - smem_u32(raw));
+  StateTail& tail = *reinterpret_cast<StateTail*>(mem + L::tail);
+
+  const int unit = blockIdx.x, seg = blockIdx.y, z0 = blockIdx.z * D;
+  const int b = unit / p.H, h = unit % p.H;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const float g = p.g[h];
+  const int length = decay_length(p, b);
+  const int begin = seg * p.seg_len;
+  const int valid = max(0, min(min(begin + p.seg_len, p.N), length) - begin);
+  const bool exact = p.s_out != nullptr;  // three parts where a final state comes of it
+  const uint32_t bar = smem_u32(&tail.bar), full[2] = {smem_u32(&tail.full[0]), smem_u32(&tail.full[1])};
+  int loaded = 0, seen = 0;
+  auto fetch = [&](int c0) {
+    const uint32_t st = (uint32_t)(c0 / N) & 1u;
+    const int token = REV ? length - begin - c0 - N : begin + c0;
+    mbar_arrive_expect_tx(full[st], 2 * kStateTile);
+    load_rows(base + L::y + st * kStateTile, a.y64, full[st], 0, token, h, b);
+    load_rows(base + L::z + st * kStateTile, a.z64, full[st], z0, token, h, b);
+    ++loaded;
+  };
+  if (tid == kStateWork) {
+    mbar_init(bar, 1);
+    mbar_init(full[0], 1);
+    mbar_init(full[1], 1);
+    tail.abort = 0;
+    fence_barrier_init();
+    if (valid > 0) fetch(0);
+  }
+  if (warp == kStateWork / 32) {
+    __syncwarp();
+    tmem_alloc(smem_u32(&tail.tmem), 128);
+    tmem_relinquish();
+  }
+  decay_dependents();
+  const int row = tid & (N - 1), place = REV ? N - 1 - row : row;
+  const float2 w_full = decay_power(g, N - place - p.e);
+  const float2 carry = decay_power(g, N);
+  const int dz = 32 * (warp & 1) + lane, dx0 = 32 * ((warp >> 1) & 1);
+  float s[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s[i] = 0.f;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = tail.tmem, tmq = tm + ((uint32_t)(32 * (warp & 3)) << 16);
+  volatile int* abort_flag = &tail.abort;
+  bool ok = true;
+  auto dirty = [&](int c0) { return !REV && valid - c0 < N && begin + valid < p.N; };
+
+  if (warp == kStateWork / 32) {
+    constexpr uint32_t id_u = idesc_bf16_f32(128, 128, true, true), id_l = idesc_bf16_f32(128, 64, true, true);
+    for (int c0 = 0; c0 < valid; c0 += N) {
+      const uint32_t st = (uint32_t)(c0 / N) & 1u;
+      const uint32_t ya = base + L::y + st * kStateTile, za = base + L::z + st * kStateTile;
+      if (lane == 0) {
+        ok = mbar_wait(full[st], (uint32_t)(c0 / N >> 1) & 1u, p.err, 0xd0c, abort_flag);
+        if (ok) ++seen;
+      }
+      if (__syncthreads_or(!ok)) break;
+      if (dirty(c0)) __syncthreads();
+      if (lane == 0 && c0 + N < valid) fetch(c0 + N);
+      __syncwarp();
+      if (__syncthreads_or(0)) break;
+      if (lane == 0) {
+        tc_fence_after();
+        const uint64_t zd = sdesc_sw128(za, 0u, 1024u), wd = sdesc_sw128(ya, base + L::mid - ya, 1024u);
+#pragma unroll
+        for (int k = 0; k < N / 16; ++k) umma_bf16(tm, zd + 128 * k, wd + 128 * k, id_u, k > 0);
+        if (exact) {  // the third part adds to the second
+          const uint64_t ld = sdesc_sw128(base + L::lo, 0u, 1024u);
+#pragma unroll
+          for (int k = 0; k < N / 16; ++k) umma_bf16(tm + 64u, zd + 128 * k, ld + 128 * k, id_l, 1u);
+        }
+        umma_commit(bar);
+      }
+      __syncwarp();
+    }
+    if (lane == 0)
+      for (; seen < loaded; ++seen) mbar_wait(full[seen & 1], (uint32_t)(seen >> 1) & 1u, p.err, 0xd0d);
+    __syncwarp();
+  } else {
+    for (int c0 = 0; c0 < valid; c0 += N) {
+      const int n = min(N, valid - c0);
+      const uint32_t st = (uint32_t)(c0 / N) & 1u;
+      uint8_t* yt = mem + L::y + st * kStateTile;
+      if (__syncthreads_or(!ok)) break;  // the chunk is there
+      if (dirty(c0)) {
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = n * 8 + tid; i < N * 8; i += kStateWork) {
+          *reinterpret_cast<uint4*>(yt + 16 * i) = zero;
+          *reinterpret_cast<uint4*>(mem + L::z + st * kStateTile + 16 * i) = zero;
+        }
+        fence_proxy_async();
+        __syncthreads();
+      }
+      float wj = (w_full.x + w_full.y) * p.update;
+      if (n < N) {
+        const float2 w = decay_power(g, max(n - place - p.e, 0));
+        wj = (w.x + w.y) * p.update;
+      }
+      const uint64_t wj2 = pair(wj, wj);
+      auto split = [&](auto parts) {  // half a row; the first part takes the row's place
+        constexpr int kParts = decltype(parts)::value;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t off = tile_off<D>(row, 4 * (tid / N) + i);
+          const uint4 v = *reinterpret_cast<const uint4*>(yt + off);
+          uint32_t a[kParts], c[kParts], d[kParts], e[kParts];
+          scale_split2<kParts>(v.x, wj2, a);
+          scale_split2<kParts>(v.y, wj2, c);
+          scale_split2<kParts>(v.z, wj2, d);
+          scale_split2<kParts>(v.w, wj2, e);
+          *reinterpret_cast<uint4*>(yt + off) = make_uint4(a[0], c[0], d[0], e[0]);
+          *reinterpret_cast<uint4*>(mem + L::mid + off) = make_uint4(a[1], c[1], d[1], e[1]);
+          if constexpr (kParts == 3)
+            *reinterpret_cast<uint4*>(mem + L::lo + off) = make_uint4(a[2], c[2], d[2], e[2]);
+        }
+      };
+      if (exact)
+        split(std::integral_constant<int, 3>());
+      else
+        split(std::integral_constant<int, 2>());
+      fence_proxy_async();
+      if (__syncthreads_or(0)) break;  // the parts of w Y are there
+      const float2 w = n == N ? carry : decay_power(g, n);
+      ok = mbar_wait(bar, st, p.err, 0xd05, abort_flag);
+      tc_fence_after();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float u0[16], u1[16];
+        tmem_ld16(tmq + dx0 + 16 * k, u0);
+        tmem_ld16(tmq + 64 + dx0 + 16 * k, u1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float& s0 = s[16 * k + 2 * i];
+          float& s1 = s[16 * k + 2 * i + 1];
+          const uint64_t u = add2(pair(u0[2 * i], u0[2 * i + 1]), pair(u1[2 * i], u1[2 * i + 1]));
+          const float2 f = unpair(fma2(pair(s0, s1), pair(w.x, w.x), fma2(pair(s0, s1), pair(w.y, w.y), u)));
+          s0 = f.x, s1 = f.y;
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (warp == kStateWork / 32) {
+    tmem_dealloc(tm, 128);
+    return;
+  }
+  if (valid == 0) return;
+  float* to = p.seg + ((int64_t)unit * p.nseg + seg + 1) * D * p.DZ;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) to[(int64_t)(dx0 + i) * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz] = s[i];
+}
+
 // Axes ordered by stride, as nested as they are in memory.
 bool make_map(RowMap* m, const void* base, const mhla_strides& st, int64_t cols, const DecayPass& p, int box_cols,
               int box_rows, int swizzle) {
@@ -528,10 +717,18 @@ cudaError_t run(const TcArgs& a, cudaStream_t s) {
   const unsigned units = (unsigned)(p.B * p.H), slices = (unsigned)(p.DZ / D);
   cudaError_t e;
   if (p.nseg > 1 && (p.launches & 1)) {
-    constexpr size_t smem = Layout<false>::bytes + 1024;
-    auto* k = decay_tc_kernel<false, REV>;
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
-    k<<<dim3(units, (unsigned)(p.nseg - 1), slices), kThreads, smem, s>>>(a);
+    const dim3 grid(units, (unsigned)(p.nseg - 1), slices);
+    if ((int64_t)units * (p.nseg - 1) * slices >= 4 * kOpsSms) {
+      constexpr size_t smem = StateLayout::bytes + 1024;
+      auto* k = decay_tc_state_kernel<REV>;
+      if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+      k<<<grid, kStateThreads, smem, s>>>(a);
+    } else {
+      constexpr size_t smem = Layout<false>::bytes + 1024;
+      auto* k = decay_tc_kernel<false, REV>;
+      if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+      k<<<grid, kThreads, smem, s>>>(a);
+    }
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_decay_scan(p, s)) != cudaSuccess) return e;
   }
@@ -551,7 +748,9 @@ cudaError_t launch_decay_tc(const DecayPass& p, cudaStream_t s) {
   TcArgs a;
   a.p = p;
   if (!make_map(&a.x, p.x, p.sx, p.DX, p, D, C, 128) || !make_map(&a.y, p.y, p.sy, p.DX, p, D, C, 128) ||
-      !make_map(&a.z, p.z, p.sz, p.DZ, p, D, C, 128) || !make_map(&a.o, p.o, p.so, p.DZ, p, 32, 32, 64))
+      !make_map(&a.z, p.z, p.sz, p.DZ, p, D, C, 128) || !make_map(&a.o, p.o, p.so, p.DZ, p, 32, 32, 64) ||
+      !make_map(&a.y64, p.y, p.sy, p.DX, p, D, kStateChunk, 128) ||
+      !make_map(&a.z64, p.z, p.sz, p.DZ, p, D, kStateChunk, 128))
     return cudaErrorNotSupported;
   return p.reverse ? run<true>(a, s) : run<false>(a, s);
 }
