@@ -11,7 +11,8 @@
 //   U    = (w Y)^T Z            w_j = lambda^(n - j - e), w Y split into two bf16 parts
 //   S    = lambda^n S + U       float32 in registers, lambda^n as high + low parts
 // Roundings to bf16: P and the operand copy of S once each (relative error at
-// most 2^-8 a term, as large as the rounding of the output itself).  w Y is
+// most 2^-8 a term, as large as the rounding of the output itself; 2^-16 for
+// prompts shorter than 128 tokens).  w Y is
 // held as three bf16 parts (24 bits) where a final state comes of it, so that
 // the state is as exact as float32 sums are, and as two (16 bits) where it
 // feeds rounded outputs only; U starts from zero in every chunk, so the tensor
@@ -80,22 +81,25 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&v)[4], int lane) {
   }
 }
 
-template <int DX, int DZS, bool OUT>
+template <int DX, int DZS, bool OUT, bool FINE>
 struct alignas(16) MmaSmem {
   __nv_bfloat16 x[OUT ? C * DX : 8];
   __nv_bfloat16 y[2][C * DX];
   __nv_bfloat16 z[2][C * DZS];
   __nv_bfloat16 s[2][OUT ? DX * DZS : 8];
+  __nv_bfloat16 s_lo[2][OUT && FINE ? DX * DZS : 8];
   float4 wt[OUT ? 4 : 1][OUT ? 32 : 1];  // a lane's weights of a 16 x 16 score tile: off (2), on (2) the diagonal
   float uw[2][C];   // weights of the chunk's tokens in the state: full chunks, the last one
   float pw[C + 1];  // lambda^n
 };
 
-// OUT: the pass itself; otherwise only the segment's own final state.
-template <int DX, int DZS, bool OUT>
+// OUT: the pass itself; otherwise only the segment's own final state.  FINE:
+// P and the operand copy of S keep 16 bits too, as high + low parts.
+template <int DX, int DZS, bool OUT, bool FINE>
 __global__ void __launch_bounds__(kThreads, 3) decay_mma_kernel(const DecayPass p) {
   extern __shared__ char raw[];
-  MmaSmem<DX, DZS, OUT>& sm = *reinterpret_cast<MmaSmem<DX, DZS, OUT>*>(raw);
+  using Smem = MmaSmem<DX, DZS, OUT, FINE>;
+  Smem& sm = *reinterpret_cast<Smem*>(raw);
   // the state's 16-row tiles over the warps; with fewer tiles than warps the
   // columns are shared out too
   constexpr int kTiles = DX / 16;
@@ -202,8 +206,13 @@ __global__ void __launch_bounds__(kThreads, 3) decay_mma_kernel(const DecayPass 
       for (int m = 0; m < kCols; ++m) {
         const float(&a)[4] = s[i][2 * m];
         const float(&c)[4] = s[i][2 * m + 1];
-        stsm4(smem_addr(sm.s[at]) + tile_off<DZS>((own_tile + i * kWarps) * 16 + ra, 2 * (own_col + m) + ca),
-              pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(c[0], c[1]), pack2(c[2], c[3]));
+        const uint32_t off = tile_off<DZS>((own_tile + i * kWarps) * 16 + ra, 2 * (own_col + m) + ca);
+        const uint32_t h[4] = {pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(c[0], c[1]), pack2(c[2], c[3])};
+        stsm4(smem_addr(sm.s[at]) + off, h[0], h[1], h[2], h[3]);
+        if constexpr (FINE)
+          stsm4(smem_addr(sm.s_lo[at]) + off, pack2(a[0] - lo_f(h[0]), a[1] - hi_f(h[0])),
+                pack2(a[2] - lo_f(h[1]), a[3] - hi_f(h[1])), pack2(c[0] - lo_f(h[2]), c[1] - hi_f(h[2])),
+                pack2(c[2] - lo_f(h[3]), c[3] - hi_f(h[3])));
       }
   };
   publish(0);
@@ -260,6 +269,11 @@ __global__ void __launch_bounds__(kThreads, 3) decay_mma_kernel(const DecayPass 
             mma(acc[2 * m], xf[k], f[0], f[1]);
             mma(acc[2 * m + 1], xf[k], f[2], f[3]);
           }
+          if constexpr (FINE) {
+            ldsm4t(f, smem_addr(sm.s_lo[st]) + tile_off<DZS>(k * 16 + ra, 2 * m + ca));
+            mma(acc[2 * m], xf[k], f[0], f[1]);
+            mma(acc[2 * m + 1], xf[k], f[2], f[3]);
+          }
         }
 #pragma unroll
       for (int i = 0; i < 2 * kZ16; ++i) {
@@ -303,12 +317,23 @@ __global__ void __launch_bounds__(kThreads, 3) decay_mma_kernel(const DecayPass 
         pf[1] = pack2(d[0][2], d[0][3]);
         pf[2] = pack2(d[1][0], d[1][1]);
         pf[3] = pack2(d[1][2], d[1][3]);
+        uint32_t pl[4];
+        if constexpr (FINE) {
+          pl[0] = pack2(d[0][0] - lo_f(pf[0]), d[0][1] - hi_f(pf[0]));
+          pl[1] = pack2(d[0][2] - lo_f(pf[1]), d[0][3] - hi_f(pf[1]));
+          pl[2] = pack2(d[1][0] - lo_f(pf[2]), d[1][1] - hi_f(pf[2]));
+          pl[3] = pack2(d[1][2] - lo_f(pf[3]), d[1][3] - hi_f(pf[3]));
+        }
 #pragma unroll
         for (int m = 0; m < kZ16; ++m) {
           uint32_t f[4];
           ldsm4t(f, za + tile_off<DZS>(jt * 16 + ra, 2 * m + ca));
           mma(acc[2 * m], pf, f[0], f[1]);
           mma(acc[2 * m + 1], pf, f[2], f[3]);
+          if constexpr (FINE) {
+            mma(acc[2 * m], pl, f[0], f[1]);
+            mma(acc[2 * m + 1], pl, f[2], f[3]);
+          }
         }
       }
       // Rows to memory: four lanes hold two columns each of every 8-column
@@ -419,29 +444,33 @@ __global__ void __launch_bounds__(kThreads, 3) decay_mma_kernel(const DecayPass 
       }
 }
 
+template <int DX, int DZS, bool OUT, bool FINE>
+cudaError_t launch(const DecayPass& p, int segments, bool dependent, cudaStream_t s) {
+  constexpr int smem = (int)sizeof(MmaSmem<DX, DZS, OUT, FINE>);
+  auto* k = decay_mma_kernel<DX, DZS, OUT, FINE>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  const dim3 grid((unsigned)(p.B * p.H), (unsigned)segments, (unsigned)(p.DZ / DZS));
+  if (dependent) return (cudaError_t)launch_pdl(k, grid, dim3(kThreads), smem, s, p);
+  k<<<grid, kThreads, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <int DX, int DZS>
 cudaError_t run(const DecayPass& p, cudaStream_t s) {
-  const unsigned units = (unsigned)(p.B * p.H), slices = (unsigned)(p.DZ / DZS);
   cudaError_t e;
   if (p.nseg > 1 && (p.launches & 1)) {
-    constexpr int smem = (int)sizeof(MmaSmem<DX, DZS, false>);
-    auto* k = decay_mma_kernel<DX, DZS, false>;
-    if (smem > 48 * 1024 &&
-        (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
-      return e;
-    k<<<dim3(units, (unsigned)(p.nseg - 1), slices), kThreads, smem, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch<DX, DZS, false, false>(p, p.nseg - 1, false, s)) != cudaSuccess) return e;
     if ((e = launch_decay_scan(p, s)) != cudaSuccess) return e;
   }
   if (!(p.launches & 2)) return cudaSuccess;
-  constexpr int smem = (int)sizeof(MmaSmem<DX, DZS, true>);
-  auto* k = decay_mma_kernel<DX, DZS, true>;
-  if (smem > 48 * 1024 &&
-      (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
-    return e;
-  if (p.nseg > 1) return (cudaError_t)launch_pdl(k, dim3(units, (unsigned)p.nseg, slices), dim3(kThreads), smem, s, p);
-  k<<<dim3(units, 1, slices), kThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  // Two roundings as large as the output's own make its error 1.4 times one
+  // rounding, on average; over the few outputs of a short prompt the average
+  // says little, and the 16-bit operands cost nothing that shows there.
+  if (p.N < 128) return launch<DX, DZS, true, true>(p, p.nseg, p.nseg > 1, s);
+  return launch<DX, DZS, true, false>(p, p.nseg, p.nseg > 1, s);
 }
 
 template <int DX>
