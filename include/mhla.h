@@ -370,7 +370,7 @@ mhla_status mhla_layernorm_backward(const void* dy, const void* x, const void* w
  *   S_t = lambda S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
  * for t = 0 .. length - 1, S_{-1} = state_in (zeros where it is NULL) and
  * state_out = S_{length-1}.  States are float32 [batch, heads, key_dim,
- * value_dim], contiguous.  No feature map and no denominator: the caller
+ * value_dim], contiguous and 16-byte aligned.  No feature map and no denominator: the caller
  * applies the map it wants to q and k, and a norm over each head's output
  * stands in for the normaliser.  log_decay is a constant of the head (it has
  * no gradient): usually <= 0, -inf keeps only the token itself, > 0 grows.
