@@ -94,6 +94,8 @@ SHAPES = [  # batch, heads, tokens, dk, dv, layout
     (1, 2, 333, 64, 32, "bnhd"),
     (1, 1, 700, 64, 64, "bhnd"),    # two segments
     (1, 2, 1111, 128, 64, "bnhd"),  # four segments, a short last chunk
+    (1, 1, 128, 128, 128, "bhnd"),
+    (2, 3, 1111, 128, 128, "bnhd"),
     (1, 1, 900, 32, 128, "bhnd"),
     (1, 1, 1025, 16, 64, "bhnd"),   # a last segment of one token
 ]
@@ -119,7 +121,7 @@ def test_forward(b, h, n, dk, dv, layout, with_state, dtype, variant):
 
 
 @pytest.mark.parametrize("dtype,variant", VARIANTS)
-@pytest.mark.parametrize("dim", [32, 64])
+@pytest.mark.parametrize("dim", [32, 64, 128])
 @pytest.mark.parametrize("n,lengths", [(130, [0, 1, 64, 65, 130, 999, -3]), (1300, [0, 1, 255, 256, 257, 1299, 1300])])
 def test_forward_lengths(n, lengths, dim, dtype, variant):
     b, h, dk, dv = len(lengths), 1, dim, dim
@@ -142,7 +144,7 @@ def test_forward_lengths(n, lengths, dim, dtype, variant):
 
 
 @pytest.mark.parametrize("dtype,variant", VARIANTS)
-@pytest.mark.parametrize("d", [32, 64])
+@pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("g", [0.0, -math.inf, -40.0, -1e-7, 0.01])
 def test_forward_extreme_decays(g, d, dtype, variant):
     n = 600
@@ -207,7 +209,7 @@ def test_backward(b, h, n, dk, dv, layout, with_state, dtype, variant):
                            scale, dtype, variant == "tensor")
 
 
-@pytest.mark.parametrize("d", [32, 64])
+@pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("dtype,variant", VARIANTS)
 def test_backward_lengths(d, dtype, variant):
     n, lengths = 600, [0, 1, 63, 300, 600]
@@ -364,10 +366,11 @@ def test_other_stream_and_graph():
     assert torch.equal(out, want) and torch.equal(st, state)
 
 
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("n", [70, 1000])
-def test_unaligned_rows_of_64(n):
+def test_unaligned_rows(n, d):
     """Rows that are not 16-byte aligned take another kernel, with another order of sums and the same bounds."""
-    h, d = 2, 64
+    h = 2
     fused = make((1, n, 4 * h * d + 1), "bf16", 1)
     q, k, v, out = (fused[:, :, 1 + i * h * d: 1 + (i + 1) * h * d].unflatten(2, (h, d)) for i in range(4))
     g = decays(h)
