@@ -95,6 +95,7 @@ SHAPES = [  # batch, heads, tokens, dk, dv, layout
     (1, 1, 700, 64, 64, "bhnd"),    # two segments
     (1, 2, 1111, 128, 64, "bnhd"),  # four segments, a short last chunk
     (1, 1, 128, 128, 128, "bhnd"),
+    (1, 2, 300, 128, 64, "bhnd"),
     (2, 3, 1111, 128, 128, "bnhd"),
     (1, 1, 900, 32, 128, "bhnd"),
     (1, 1, 1025, 16, 64, "bhnd"),   # a last segment of one token

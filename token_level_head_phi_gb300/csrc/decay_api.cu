@@ -27,7 +27,7 @@ bool on_tensor_cores(const mhla_decay_params* p) {
 // The tcgen05 kernel takes rows of 64 entries (and 16-byte alignment, and at
 // least one chunk of 128 tokens).  It is ahead of the mma.sync kernel there: 128 tokens x 64 heads
 // 6.7 against 7.2 us, 2k tokens 33 against 40, 32k tokens 336 against 405.
-bool big_tiles(int dx, int dz) { return (dx == 64 && dz % 64 == 0) || (dx == 128 && dz == 128); }
+bool big_tiles(int dx, int dz) { return dx >= 64 && dz % 64 == 0; }
 
 // Segments of a pass.  CTAs (units x slices of 64 columns x segments; 32
 // columns with mma.sync and DX = 128) run in waves of those that are resident
@@ -41,9 +41,9 @@ constexpr int kSegQuantum = 128, kSegMost = 64, kSegStart = 100;
 
 void plan_segments(const mhla_decay_params* p, int dx, int dz, int* nseg, int* seg_len) {
   const bool wide = on_tensor_cores(p) && dx == 128;
-  const int slice = !wide ? 64 : big_tiles(dx, dz) ? 128 : 32;
+  const int slice = !wide ? 64 : big_tiles(dx, dz) ? dz : 32;
   const int64_t ctas = (int64_t)p->batch * p->heads * (dz > slice ? dz / slice : 1);
-  const int64_t slots = (wide && slice == 128 ? 1 : on_tensor_cores(p) && !big_tiles(dx, dz) ? 3 : 2) * kOpsSms;
+  const int64_t slots = (wide && slice >= 64 ? 1 : on_tensor_cores(p) && !big_tiles(dx, dz) ? 3 : 2) * kOpsSms;
   *nseg = 1;
   *seg_len = (p->tokens + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
   double best = (double)((ctas + slots - 1) / slots) * (*seg_len + kSegStart);

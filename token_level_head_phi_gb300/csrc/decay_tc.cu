@@ -37,33 +37,29 @@
 // ahead (8k tokens x 32 heads, backward: 138 against 149 us).
 #include <type_traits>
 
-#include "decay.h"
+#include "decay_tc.cuh"
 #include "decay_tile.cuh"
 #include "ops.h"
-#include "tc_common.cuh"
-#include "tc_host.h"
 
 namespace mhla {
 namespace {
 
-using namespace tc;
-
 constexpr int C = 128;       // tokens of a chunk
-constexpr int D = 64;        // entries of a block: rows and slices are W blocks wide
-constexpr uint32_t kBlock = C * D * 2;
-template <int W>
-constexpr int kWorkThreads = 256 * W;
+constexpr int D = 64;        // entries of a row, columns of a slice
+constexpr int kWork = 256;   // working threads
+constexpr int kThreads = kWork + 32;
+constexpr uint32_t kTile = C * D * 2;
+constexpr uint32_t kColP = 128, kColO = 192;
 
 // Shared memory, from a 1024-byte boundary: y, y, z, z, mid, then x and s (OUT)
 // or lo, then the rest.
-template <bool OUT, int W>
+template <bool OUT>
 struct Layout {
-  static constexpr uint32_t kTile = W * kBlock;
   static constexpr uint32_t y = 0, z = 2 * kTile, mid = 4 * kTile;
   static constexpr uint32_t x = 5 * kTile;   // OUT; its last use in a chunk over, the third part of w Y
   static constexpr uint32_t lo = 5 * kTile;
   static constexpr uint32_t s = 6 * kTile;   // OUT
-  static constexpr uint32_t tail = OUT ? 6 * kTile + W * W * D * D * 2 : 6 * kTile;
+  static constexpr uint32_t tail = OUT ? 6 * kTile + kTile / 2 : 6 * kTile;
   static constexpr uint32_t bytes = tail + 1024;
 };
 struct alignas(16) Tail {
@@ -76,63 +72,21 @@ struct alignas(16) Tail {
 };
 static_assert(sizeof(Tail) <= 1024, "");
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2, int c3) {
-  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-               : "memory");
-}
-
-// A map of rows and the places of its token, head and batch axes (1 to 3,
-// ordered by stride).
-struct RowMap {
-  CUtensorMap map;
-  int token, head, batch;
-};
-struct TcArgs {
-  RowMap x, y, z, o;
-  RowMap y64, z64;  // in boxes of 64 rows
-  DecayPass p;
-};
-
-__device__ __forceinline__ int coordinate(const RowMap& m, int axis, int token, int head, int batch) {
-  return m.token == axis ? token : m.head == axis ? head : batch;
-}
-__device__ __forceinline__ void load_rows(uint32_t dst, const RowMap& m, uint32_t bar, int col, int token, int head,
-                                          int batch) {
-  tma_load_4d(dst, &m.map, bar, col, coordinate(m, 1, token, head, batch), coordinate(m, 2, token, head, batch),
-              coordinate(m, 3, token, head, batch), policy_evict_first());
-}
-
-template <bool OUT, bool REV, int W>
-__global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
-    decay_tc_kernel(const __grid_constant__ TcArgs a) {
-  static_assert(W == 1 || (W == 2 && OUT), "");
+template <bool OUT, bool REV>
+__global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_constant__ TcArgs a) {
   const DecayPass& p = a.p;
-  using L = Layout<OUT, W>;
-  constexpr int kWork = kWorkThreads<W>, DW = W * D;
-  constexpr uint32_t kTile = L::kTile;
+  using L = Layout<OUT>;
   using T = __nv_bfloat16;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* mem = raw + (base - smem_u32(raw));
   Tail& tail = *reinterpret_cast<Tail*>(mem + L::tail);
-  constexpr uint32_t kCols = W == 2 ? 512 : OUT ? 256 : 128;
-  constexpr uint32_t kColP = 128 * W, kColO = kColP + 64;  // columns of tensor memory behind D and U
+  constexpr uint32_t kCols = OUT ? 256 : 128;
 
-  const int unit = blockIdx.x, seg = blockIdx.y, z0 = blockIdx.z * DW;
+  const int unit = blockIdx.x, seg = blockIdx.y, z0 = blockIdx.z * D;
   const int b = unit / p.H, h = unit % p.H;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int q = warp & 3, part = (warp >> 2) & (2 * W - 1);  // lanes 32 q .. of tensor memory, 32 columns
+  const int q = warp & 3, half = (warp >> 2) & 1;  // lanes 32 q .. of tensor memory, half of the columns
   const float g = p.g[h];
   const int length = decay_length(p, b);
   const int begin = seg * p.seg_len;
@@ -142,7 +96,7 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
   const bool exact = p.s_out && (!OUT || last);  // three parts where a final state comes of it
   auto first_token = [&](int c0) { return REV ? length - begin - c0 - C : begin + c0; };  // of row 0
   T* o = static_cast<T*>(p.o) + b * p.so.batch + h * p.so.head + z0;
-  const int64_t one = (int64_t)DW * p.DZ, state = unit * one;
+  const int64_t one = (int64_t)D * p.DZ, state = unit * one;
   float* segs = p.seg + (p.nseg > 1 ? (int64_t)unit * p.nseg * one : 0);
 
   const uint32_t bar_a = smem_u32(&tail.bar[0]), bar_b = smem_u32(&tail.bar[1]), bar_u = smem_u32(&tail.bar[2]);
@@ -154,17 +108,13 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
   auto fetch = [&](int c0) {
     const uint32_t st = (uint32_t)(c0 / C) & 1u;
     mbar_arrive_expect_tx(full[st], 2 * kTile);
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      load_rows(base + L::y + st * kTile + k * kBlock, a.y, full[st], k * D, first_token(c0), h, b);
-      load_rows(base + L::z + st * kTile + k * kBlock, a.z, full[st], z0 + k * D, first_token(c0), h, b);
-    }
+    load_rows(base + L::y + st * kTile, a.y, full[st], 0, first_token(c0), h, b);
+    load_rows(base + L::z + st * kTile, a.z, full[st], z0, first_token(c0), h, b);
     ++loaded;
   };
   auto fetch_x = [&](int c0) {
     mbar_arrive_expect_tx(full_x, kTile);
-#pragma unroll
-    for (int k = 0; k < W; ++k) load_rows(base + L::x + k * kBlock, a.x, full_x, k * D, first_token(c0), h, b);
+    load_rows(base + L::x, a.x, full_x, 0, first_token(c0), h, b);
     ++loaded_x;
   };
   if (issuer) {
@@ -200,22 +150,21 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
   if (!OUT) decay_dependents();
   if (OUT && p.nseg > 1) decay_wait();
 
-  // This thread's part of the state: column dz of z, entries dx0 .. dx0 + E - 1.
-  constexpr int E = 16 * W;
-  const int dz = W == 1 ? 32 * (q & 1) + lane : 32 * q + lane;
-  const int dx0 = W == 1 ? E * ((q >> 1) * 2 + part) : E * part;
-  float s[E];
+  // This thread's part of the state: column dz of z, entries dx0 .. dx0 + 15.
+  const int dz = 32 * (q & 1) + lane, dx0 = 16 * ((q >> 1) * 2 + half);
+  float s[16];
   const float* before = !OUT ? nullptr : p.nseg > 1 ? segs + seg * one : p.s_in ? p.s_in + state : nullptr;
 #pragma unroll
-  for (int i = 0; i < E; ++i)
+  for (int i = 0; i < 16; ++i)
     s[i] = before && tid < kWork ? before[(int64_t)(dx0 + i) * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz] : 0.f;
   auto publish = [&]() {  // S as the second operand of X S: row dz, its entries along the row
-    uint8_t* to = mem + L::s + (dx0 / D) * (DW * D * 2);
+    uint32_t v[8];
 #pragma unroll
-    for (int i = 0; i < E / 8; ++i)
-      *reinterpret_cast<uint4*>(to + tile_off<D>(dz, dx0 % D / 8 + i)) =
-          make_uint4(pack2(s[8 * i], s[8 * i + 1]), pack2(s[8 * i + 2], s[8 * i + 3]),
-                     pack2(s[8 * i + 4], s[8 * i + 5]), pack2(s[8 * i + 6], s[8 * i + 7]));
+    for (int i = 0; i < 8; ++i) v[i] = pack2(s[2 * i], s[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<uint4*>(mem + L::s + tile_off<D>(dz, dx0 / 8 + i)) =
+          make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   };
   if (OUT && tid < kWork) publish();
 
@@ -237,11 +186,10 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
   tc_fence_after();
   const uint32_t tm = tail.tmem, tmq = tm + ((uint32_t)(32 * q) << 16);
   if (OUT && tid < kWork) {  // blocks of P above the diagonal stay zero
-    uint32_t zero[16];
+    uint32_t zero[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) zero[i] = 0u;
-#pragma unroll
-    for (int i = 0; i < 2 / W; ++i) tmem_st16(tmq + kColP + 16 * (2 / W * part + i), zero);
+    for (int i = 0; i < 32; ++i) zero[i] = 0u;
+    tmem_st32(tmq + kColP + 32 * half, zero);
     tmem_wait_st();
   }
 
@@ -251,11 +199,9 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
   bool ok = true;
   if (warp == kWork / 32) {
     // ------------------------------------------------ issues the products
-    constexpr uint32_t id_d = idesc_bf16_f32(128, 128, false, false), id_o = idesc_bf16_f32(128, DW, false, false);
-    constexpr uint32_t id_p = idesc_bf16_f32(128, DW, false, true);
-    constexpr uint32_t id_u = idesc_bf16_f32(128, 128, true, true), id_l = idesc_bf16_f32(128, DW, true, true);
-    // from one block of 64 columns of z to the next; one block repeats
-    constexpr uint32_t kZStep = W == 1 ? 0u : kBlock;
+    constexpr uint32_t id_d = idesc_bf16_f32(128, 128, false, false), id_o = idesc_bf16_f32(128, 64, false, false);
+    constexpr uint32_t id_p = idesc_bf16_f32(128, 64, false, true);
+    constexpr uint32_t id_u = idesc_bf16_f32(128, 128, true, true), id_l = idesc_bf16_f32(128, 64, true, true);
     for (int c0 = 0; c0 < valid; c0 += C) {
       const uint32_t st = (uint32_t)(c0 / C) & 1u;
       const uint32_t ya = base + L::y + st * kTile, za = base + L::z + st * kTile;
@@ -272,14 +218,9 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
         const uint64_t xd = sdesc_sw128(base + L::x, 0u, 1024u), yd = sdesc_sw128(ya, 0u, 1024u);
         const uint64_t sd = sdesc_sw128(base + L::s, 0u, 1024u);
 #pragma unroll
-        for (int k = 0; k < 4 * W; ++k) {
-          const uint32_t at = (k / 4) * (kBlock / 16) + 2 * (k % 4);
-          umma_bf16(tm, xd + at, yd + at, id_d, k > 0);
-        }
+        for (int k = 0; k < 4; ++k) umma_bf16(tm, xd + 2 * k, yd + 2 * k, id_d, k > 0);
 #pragma unroll
-        for (int k = 0; k < 4 * W; ++k)
-          umma_bf16(tm + kColO, xd + (k / 4) * (kBlock / 16) + 2 * (k % 4),
-                    sd + (k / 4) * (DW * D * 2 / 16) + 2 * (k % 4), id_o, k > 0);
+        for (int k = 0; k < 4; ++k) umma_bf16(tm + kColO, xd + 2 * k, sd + 2 * k, id_o, k > 0);
         umma_commit(bar_a);
       }
       __syncwarp();
@@ -296,19 +237,14 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
       if (__syncthreads_or(!ok)) break;
       if (lane == 0) {
         tc_fence_after();
-        const uint64_t zd = sdesc_sw128(za, kZStep, 1024u);
-        const uint64_t wd = sdesc_sw128(ya, W == 1 ? base + L::mid - ya : kBlock, 1024u);
+        const uint64_t zd = sdesc_sw128(za, 0u, 1024u);
+        const uint64_t wd = sdesc_sw128(ya, base + L::mid - ya, 1024u);
 #pragma unroll
         for (int k = 0; k < 8; ++k) umma_bf16(tm, zd + 128 * k, wd + 128 * k, id_u, k > 0);
-        if (W == 2) {
-          const uint64_t md = sdesc_sw128(base + L::mid, kBlock, 1024u);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) umma_bf16(tm + 128u, zd + 128 * k, md + 128 * k, id_u, k > 0);
-        }
         if (exact) {  // the third part adds to the second
-          const uint64_t ld = sdesc_sw128(base + L::lo, kZStep, 1024u);
+          const uint64_t ld = sdesc_sw128(base + L::lo, 0u, 1024u);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) umma_bf16(tm + DW, zd + 128 * k, ld + 128 * k, id_l, 1u);
+          for (int k = 0; k < 8; ++k) umma_bf16(tm + 64u, zd + 128 * k, ld + 128 * k, id_l, 1u);
         }
         umma_commit(bar_u);
         if (OUT) {
@@ -339,32 +275,27 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
       if (dirty(c0)) {
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         for (int i = n * 8 + tid; i < C * 8; i += kWork) {
-#pragma unroll
-          for (int k = 0; k < W; ++k) {
-            const uint32_t off = k * kBlock + 16 * i;
-            *reinterpret_cast<uint4*>(yt + off) = zero;
-            *reinterpret_cast<uint4*>(mem + L::z + st * kTile + off) = zero;
-            if (OUT) *reinterpret_cast<uint4*>(mem + L::x + off) = zero;
-          }
+          *reinterpret_cast<uint4*>(yt + 16 * i) = zero;
+          *reinterpret_cast<uint4*>(mem + L::z + st * kTile + 16 * i) = zero;
+          if (OUT) *reinterpret_cast<uint4*>(mem + L::x + 16 * i) = zero;
         }
         fence_proxy_async();
         __syncthreads();
       }
-      // 32 entries of a row of w Y; a tile's pieces are read and written by one thread
+      // half a row of w Y; a tile's pieces are read and written by one thread
       float wj = (w_full.x + w_full.y) * p.update;
       if (n < C) {
         const float2 w = decay_power(g, max(n - j_place - p.e, 0));
         wj = (w.x + w.y) * p.update;
       }
       const uint64_t wj2 = pair(wj, wj);
-      const uint32_t block0 = (tid >> 8) * kBlock;
-      const int piece0 = 4 * (tid >> 7 & 1);
+      const int piece0 = 4 * (tid >> 7);
       // pieces i of the row as PARTS parts; the first part takes the row's place
       auto split = [&](auto parts, auto&& first) {
         constexpr int kParts = decltype(parts)::value;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t off = block0 + tile_off<D>(j_row, piece0 + i);
+          const uint32_t off = tile_off<D>(j_row, piece0 + i);
           const uint4 v = *reinterpret_cast<const uint4*>(yt + off);
           uint32_t a[kParts], c[kParts], d[kParts], e[kParts];
           scale_split2<kParts>(v.x, wj2, a);
@@ -394,7 +325,7 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
         ok = mbar_wait(bar_a, st, p.err, 0xd01, abort_flag);
         tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(yt + block0 + tile_off<D>(j_row, piece0 + i)) = hi[i];
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(yt + tile_off<D>(j_row, piece0 + i)) = hi[i];
       } else {
         if (OUT) {
           outputs_read();
@@ -408,7 +339,7 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
       }
       if (OUT) {
         float v[32];
-        tmem_ld32(tmq + kColO + 32 * part, v);
+        tmem_ld32(tmq + kColO + 32 * half, v);
         tmem_wait_ld();
         uint32_t r[32];
 #pragma unroll
@@ -416,13 +347,11 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
           const float2 f = unpair(mul2(pair(v[2 * i], v[2 * i + 1]), read2));
           r[2 * i] = __float_as_uint(f.x), r[2 * i + 1] = __float_as_uint(f.y);
         }
-        tmem_st32(tmq + kColO + 32 * part, r);
+        tmem_st32(tmq + kColO + 32 * half, r);
         // P in blocks of 32 columns up to the diagonal, shared out over the
-        // warps of a row
+        // two warps of a row
         const int blocks = qp + 1, middle = (blocks + 1) / 2;
-        const int k0 = W == 2 ? part : part ? middle : 0;
-        const int k1 = W == 2 ? min(part + 1, blocks) : part ? blocks : middle;
-        for (int k = k0; k < k1; ++k) {
+        for (int k = half ? middle : 0; k < (half ? blocks : middle); ++k) {
           const int kc = REV ? 3 - k : k;  // its place among the columns
           tmem_ld32(tmq + 32 * kc, v);
           tmem_wait_ld();
@@ -456,27 +385,23 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
       ok = mbar_wait(bar_u, st, p.err, 0xd02, abort_flag);
       tc_fence_after();
       const float2 w = n == C ? carry : decay_power(g, n);
+      float u0[16], u1[16];
+      tmem_ld16(tmq + dx0, u0);
+      tmem_ld16(tmq + 64 + dx0, u1);
+      tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < W; ++k) {
-        float u0[16], u1[16];
-        tmem_ld16(tmq + dx0 + 16 * k, u0);
-        tmem_ld16(tmq + DW + dx0 + 16 * k, u1);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float& s0 = s[16 * k + 2 * i];
-          float& s1 = s[16 * k + 2 * i + 1];
-          const uint64_t u = add2(pair(u0[2 * i], u0[2 * i + 1]), pair(u1[2 * i], u1[2 * i + 1]));
-          const float2 f = unpair(fma2(pair(s0, s1), pair(w.x, w.x), fma2(pair(s0, s1), pair(w.y, w.y), u)));
-          s0 = f.x, s1 = f.y;
-        }
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t old = pair(s[2 * i], s[2 * i + 1]);
+        const uint64_t u = add2(pair(u0[2 * i], u0[2 * i + 1]), pair(u1[2 * i], u1[2 * i + 1]));
+        const float2 f = unpair(fma2(old, pair(w.x, w.x), fma2(old, pair(w.y, w.y), u)));
+        s[2 * i] = f.x, s[2 * i + 1] = f.y;
       }
       if (OUT) {
         publish();
         ok = mbar_wait(bar_b, st, p.err, 0xd0a, abort_flag) && ok;
         tc_fence_after();
         float v[32];
-        tmem_ld32(tmq + kColO + 32 * part, v);
+        tmem_ld32(tmq + kColO + 32 * half, v);
         tmem_wait_ld();
         // A warp's 32 rows x 64 bytes leave as one TMA store (64-byte swizzle);
         // a part of a chunk row by row, since a store may not start before the
@@ -492,7 +417,7 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
-            tma_store_4d(&a.o.map, smem_u32(stage), z0 + 32 * part, coordinate(a.o, 1, token, h, b),
+            tma_store_4d(&a.o.map, smem_u32(stage), z0 + 32 * half, coordinate(a.o, 1, token, h, b),
                          coordinate(a.o, 2, token, h, b), coordinate(a.o, 3, token, h, b));
             bulk_commit();
           }
@@ -504,7 +429,7 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
             const uint4 t = *reinterpret_cast<const uint4*>(stage + r * 64 + ((piece ^ (r >> 1 & 3)) << 4));
             const int at = 32 * q + r;
             if ((REV ? C - 1 - at : at) < n)
-              *reinterpret_cast<uint4*>(o + (int64_t)(token + r) * p.so.token + 32 * part + piece * 8) = t;
+              *reinterpret_cast<uint4*>(o + (int64_t)(token + r) * p.so.token + 32 * half + piece * 8) = t;
           }
         }
         __syncwarp();
@@ -521,28 +446,28 @@ __global__ void __launch_bounds__(kWorkThreads<W> + 32, W == 1 ? 2 : 1)
     return;
   }
   if (OUT) {
-    for (int i = tid; i < (end - begin - valid) * DW; i += kWork)
-      o[(int64_t)(begin + valid + i / DW) * p.so.token + i % DW] = __float2bfloat16_rn(0.f);
+    for (int i = tid; i < (end - begin - valid) * D; i += kWork)
+      o[(int64_t)(begin + valid + i / D) * p.so.token + i % D] = __float2bfloat16_rn(0.f);
     if (!last || !p.s_out) return;
   } else if (valid == 0) {
     return;
   }
   float* to = OUT ? p.s_out + state : segs + (seg + 1) * one;
 #pragma unroll
-  for (int i = 0; i < E; ++i) to[(int64_t)(dx0 + i) * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz] = s[i];
+  for (int i = 0; i < 16; ++i) to[(int64_t)(dx0 + i) * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz] = s[i];
 }
 
 // ------------------- the segments' own states, many at once: 64-token chunks
 
 constexpr int kStateChunk = 64;
-template <int W>
-constexpr int kStateThreads = 128 * W;
+template <int XB>
+constexpr int kStateThreads = 128 * XB;
 constexpr uint32_t kStateBlock = kStateChunk * D * 2;
-template <int W>
+template <int XB, int ZB>  // blocks of 64 entries of a row and of 64 columns of z
 struct StateLayout {
-  static constexpr uint32_t kStateTile = W * kStateBlock;
-  static constexpr uint32_t y = 0, z = 2 * kStateTile, mid = 4 * kStateTile, lo = 5 * kStateTile;
-  static constexpr uint32_t tail = 6 * kStateTile;
+  static constexpr uint32_t kY = XB * kStateBlock, kZ = ZB * kStateBlock;
+  static constexpr uint32_t y = 0, z = 2 * kY, mid = z + 2 * kZ, lo = mid + kY;
+  static constexpr uint32_t tail = lo + kY;
   static constexpr uint32_t bytes = tail + 64;
 };
 struct StateTail {
@@ -551,21 +476,23 @@ struct StateTail {
   int abort;
 };
 
-// U's first part in columns 0 to 64 W - 1, the others behind it.
-template <bool REV, int W>
-__global__ void __launch_bounds__(kStateThreads<W> + 32, W == 1 ? 4 : 2)
+// One block of z repeats, so that all 128 lanes of U hold rows.  With 64-entry
+// rows U's first part is in columns 0-63 and the others in 64-127, two of them
+// in one product; with 128 all parts add to one sum, the small ones first.
+template <bool REV, int XB, int ZB>
+__global__ void __launch_bounds__(kStateThreads<XB> + 32, XB == 1 ? 4 : 2)
     decay_tc_state_kernel(const __grid_constant__ TcArgs a) {
+  static_assert(ZB <= XB, "");
   const DecayPass& p = a.p;
-  using L = StateLayout<W>;
-  constexpr int kStateWork = kStateThreads<W>, DW = W * D;
-  constexpr uint32_t kStateTile = L::kStateTile, kCols = 128 * W;
+  using L = StateLayout<XB, ZB>;
+  constexpr int kStateWork = kStateThreads<XB>;
   constexpr int N = kStateChunk;
   extern __shared__ uint8_t raw[];
   const uint32_t base = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* mem = raw + (base - smem_u32(raw));
   StateTail& tail = *reinterpret_cast<StateTail*>(mem + L::tail);
 
-  const int unit = blockIdx.x, seg = blockIdx.y, z0 = blockIdx.z * DW;
+  const int unit = blockIdx.x, seg = blockIdx.y, z0 = blockIdx.z * (ZB * D);
   const int b = unit / p.H, h = unit % p.H;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const float g = p.g[h];
@@ -578,12 +505,12 @@ __global__ void __launch_bounds__(kStateThreads<W> + 32, W == 1 ? 4 : 2)
   auto fetch = [&](int c0) {
     const uint32_t st = (uint32_t)(c0 / N) & 1u;
     const int token = REV ? length - begin - c0 - N : begin + c0;
-    mbar_arrive_expect_tx(full[st], 2 * kStateTile);
+    mbar_arrive_expect_tx(full[st], L::kY + L::kZ);
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-      load_rows(base + L::y + st * kStateTile + k * kStateBlock, a.y64, full[st], k * D, token, h, b);
-      load_rows(base + L::z + st * kStateTile + k * kStateBlock, a.z64, full[st], z0 + k * D, token, h, b);
-    }
+    for (int k = 0; k < XB; ++k) load_rows(base + L::y + st * L::kY + k * kStateBlock, a.y64, full[st], k * D, token, h, b);
+#pragma unroll
+    for (int k = 0; k < ZB; ++k)
+      load_rows(base + L::z + st * L::kZ + k * kStateBlock, a.z64, full[st], z0 + k * D, token, h, b);
     ++loaded;
   };
   if (tid == kStateWork) {
@@ -596,7 +523,7 @@ __global__ void __launch_bounds__(kStateThreads<W> + 32, W == 1 ? 4 : 2)
   }
   if (warp == kStateWork / 32) {
     __syncwarp();
-    tmem_alloc(smem_u32(&tail.tmem), kCols);
+    tmem_alloc(smem_u32(&tail.tmem), 128);
     tmem_relinquish();
   }
   decay_dependents();
@@ -604,9 +531,8 @@ __global__ void __launch_bounds__(kStateThreads<W> + 32, W == 1 ? 4 : 2)
   const float2 w_full = decay_power(g, N - place - p.e);
   const float2 carry = decay_power(g, N);
   // This thread's part of the state: column dz of z, entries dx0 .. dx0 + E - 1.
-  constexpr int E = 32 * W;
-  const int dz = W == 1 ? 32 * (warp & 1) + lane : 32 * (warp & 3) + lane;
-  const int dx0 = W == 1 ? E * ((warp >> 1) & 1) : E * (warp >> 2);
+  constexpr int E = 32 * ZB;
+  const int dz = 32 * (warp & (2 * ZB - 1)) + lane, dx0 = E * (ZB == 1 ? warp >> 1 : warp >> 2);
   float s[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) s[i] = 0.f;
@@ -619,11 +545,11 @@ __global__ void __launch_bounds__(kStateThreads<W> + 32, W == 1 ? 4 : 2)
   auto dirty = [&](int c0) { return !REV && valid - c0 < N && begin + valid < p.N; };
 
   if (warp == kStateWork / 32) {
-    constexpr uint32_t id_u = idesc_bf16_f32(128, 128, true, true), id_l = idesc_bf16_f32(128, DW, true, true);
-    constexpr uint32_t kZStep = W == 1 ? 0u : kStateBlock;
+    constexpr uint32_t id_u = idesc_bf16_f32(128, 128, true, true), id_l = idesc_bf16_f32(128, XB * D, true, true);
+    constexpr uint32_t kZStep = ZB == 1 ? 0u : kStateBlock;
     for (int c0 = 0; c0 < valid; c0 += N) {
       const uint32_t st = (uint32_t)(c0 / N) & 1u;
-      const uint32_t ya = base + L::y + st * kStateTile, za = base + L::z + st * kStateTile;
+      const uint32_t ya = base + L::y + st * L::kY, za = base + L::z + st * L::kZ;
       if (lane == 0) {
         ok = mbar_wait(full[st], (uint32_t)(c0 / N >> 1) & 1u, p.err, 0xd0c, abort_flag);
         if (ok) ++seen;
@@ -635,19 +561,25 @@ __global__ void __launch_bounds__(kStateThreads<W> + 32, W == 1 ? 4 : 2)
       if (__syncthreads_or(0)) break;
       if (lane == 0) {
         tc_fence_after();
-        const uint64_t zd = sdesc_sw128(za, kZStep, 1024u);
-        const uint64_t wd = sdesc_sw128(ya, W == 1 ? base + L::mid - ya : kStateBlock, 1024u);
+        const uint64_t zd = sdesc_sw128(za, kZStep, 1024u), ld = sdesc_sw128(base + L::lo, kStateBlock, 1024u);
+        if constexpr (XB == 1) {
+          const uint64_t wd = sdesc_sw128(ya, base + L::mid - ya, 1024u);
 #pragma unroll
-        for (int k = 0; k < N / 16; ++k) umma_bf16(tm, zd + 128 * k, wd + 128 * k, id_u, k > 0);
-        if (W == 2) {
-          const uint64_t md = sdesc_sw128(base + L::mid, kStateBlock, 1024u);
+          for (int k = 0; k < N / 16; ++k) umma_bf16(tm, zd + 128 * k, wd + 128 * k, id_u, k > 0);
+          if (exact) {  // the third part adds to the second
 #pragma unroll
-          for (int k = 0; k < N / 16; ++k) umma_bf16(tm + 128u, zd + 128 * k, md + 128 * k, id_u, k > 0);
-        }
-        if (exact) {  // the third part adds to the second
-          const uint64_t ld = sdesc_sw128(base + L::lo, kZStep, 1024u);
+            for (int k = 0; k < N / 16; ++k) umma_bf16(tm + 64u, zd + 128 * k, ld + 128 * k, id_l, 1u);
+          }
+        } else {
+          if (exact) {
 #pragma unroll
-          for (int k = 0; k < N / 16; ++k) umma_bf16(tm + DW, zd + 128 * k, ld + 128 * k, id_l, 1u);
+            for (int k = 0; k < N / 16; ++k) umma_bf16(tm, zd + 128 * k, ld + 128 * k, id_l, k > 0);
+          }
+          const uint64_t md = sdesc_sw128(base + L::mid, kStateBlock, 1024u), hd = sdesc_sw128(ya, kStateBlock, 1024u);
+#pragma unroll
+          for (int k = 0; k < N / 16; ++k) umma_bf16(tm, zd + 128 * k, md + 128 * k, id_l, k > 0 || exact);
+#pragma unroll
+          for (int k = 0; k < N / 16; ++k) umma_bf16(tm, zd + 128 * k, hd + 128 * k, id_l, 1u);
         }
         umma_commit(bar);
       }
@@ -660,16 +592,16 @@ __global__ void __launch_bounds__(kStateThreads<W> + 32, W == 1 ? 4 : 2)
     for (int c0 = 0; c0 < valid; c0 += N) {
       const int n = min(N, valid - c0);
       const uint32_t st = (uint32_t)(c0 / N) & 1u;
-      uint8_t* yt = mem + L::y + st * kStateTile;
+      uint8_t* yt = mem + L::y + st * L::kY;
       if (__syncthreads_or(!ok)) break;  // the chunk is there
       if (dirty(c0)) {
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         for (int i = n * 8 + tid; i < N * 8; i += kStateWork) {
 #pragma unroll
-          for (int k = 0; k < W; ++k) {
-            *reinterpret_cast<uint4*>(yt + k * kStateBlock + 16 * i) = zero;
-            *reinterpret_cast<uint4*>(mem + L::z + st * kStateTile + k * kStateBlock + 16 * i) = zero;
-          }
+          for (int k = 0; k < XB; ++k) *reinterpret_cast<uint4*>(yt + k * kStateBlock + 16 * i) = zero;
+#pragma unroll
+          for (int k = 0; k < ZB; ++k)
+            *reinterpret_cast<uint4*>(mem + L::z + st * L::kZ + k * kStateBlock + 16 * i) = zero;
         }
         fence_proxy_async();
         __syncthreads();
@@ -707,16 +639,17 @@ __global__ void __launch_bounds__(kStateThreads<W> + 32, W == 1 ? 4 : 2)
       ok = mbar_wait(bar, st, p.err, 0xd05, abort_flag);
       tc_fence_after();
 #pragma unroll
-      for (int k = 0; k < 2 * W; ++k) {
+      for (int k = 0; k < E / 16; ++k) {
         float u0[16], u1[16];
         tmem_ld16(tmq + dx0 + 16 * k, u0);
-        tmem_ld16(tmq + DW + dx0 + 16 * k, u1);
+        if (XB == 1) tmem_ld16(tmq + 64 + dx0 + 16 * k, u1);
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float& s0 = s[16 * k + 2 * i];
           float& s1 = s[16 * k + 2 * i + 1];
-          const uint64_t u = add2(pair(u0[2 * i], u0[2 * i + 1]), pair(u1[2 * i], u1[2 * i + 1]));
+          uint64_t u = pair(u0[2 * i], u0[2 * i + 1]);
+          if (XB == 1) u = add2(u, pair(u1[2 * i], u1[2 * i + 1]));
           const float2 f = unpair(fma2(pair(s0, s1), pair(w.x, w.x), fma2(pair(s0, s1), pair(w.y, w.y), u)));
           s0 = f.x, s1 = f.y;
         }
@@ -726,85 +659,51 @@ __global__ void __launch_bounds__(kStateThreads<W> + 32, W == 1 ? 4 : 2)
   }
   __syncthreads();
   if (warp == kStateWork / 32) {
-    tmem_dealloc(tm, kCols);
+    tmem_dealloc(tm, 128);
     return;
   }
   if (valid == 0) return;
-  float* to = p.seg + ((int64_t)unit * p.nseg + seg + 1) * DW * p.DZ;
+  float* to = p.seg + ((int64_t)unit * p.nseg + seg + 1) * (XB * D) * p.DZ;
 #pragma unroll
   for (int i = 0; i < E; ++i) to[(int64_t)(dx0 + i) * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz] = s[i];
 }
 
-// Axes ordered by stride, as nested as they are in memory.
-bool make_map(RowMap* m, const void* base, const mhla_strides& st, int64_t cols, const DecayPass& p, int box_cols,
-              int box_rows, int swizzle) {
-  struct Axis {
-    int64_t n, stride;
-    int* place;
-    uint32_t box;
-  } ax[3] = {{p.N, st.token, &m->token, (uint32_t)box_rows}, {p.H, st.head, &m->head, 1u}, {p.B, st.batch, &m->batch, 1u}};
-  for (Axis& x : ax) {
-    if (x.n > 1 && x.stride <= 0) return false;  // a broadcast axis
-    if (x.n <= 1) x.stride = (int64_t)1 << 34;   // never stepped along
-  }
-  for (int i = 0; i < 3; ++i)
-    for (int j = i + 1; j < 3; ++j)
-      if (ax[j].stride < ax[i].stride) {
-        const Axis t = ax[i];
-        ax[i] = ax[j];
-        ax[j] = t;
-      }
-  uint64_t dims[4] = {(uint64_t)cols}, strides[3];
-  uint32_t box[4] = {(uint32_t)box_cols};
-  for (int i = 0; i < 3; ++i) {
-    *ax[i].place = i + 1;
-    dims[i + 1] = (uint64_t)ax[i].n;
-    strides[i] = 2ull * (uint64_t)ax[i].stride;
-    if (strides[i] >= (1ull << 40)) return false;
-    box[i + 1] = ax[i].box;
-  }
-  return encode_tmap_rows(&m->map, base, dims, strides, box, swizzle);
-}
-
-template <class K>
-cudaError_t room(K* kernel, size_t smem) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-}
-
-template <bool REV, int W>
-cudaError_t run(const TcArgs& a, cudaStream_t s) {
+template <bool REV, int XB, int ZB>
+cudaError_t states(const TcArgs& a, cudaStream_t s) {
   const DecayPass& p = a.p;
-  const unsigned units = (unsigned)(p.B * p.H), slices = (unsigned)(p.DZ / (W * D));
-  constexpr int threads = kWorkThreads<W> + 32;
+  const unsigned units = (unsigned)(p.B * p.H), slices = (unsigned)(p.DZ / (ZB * D));
+  const dim3 grid(units, (unsigned)(p.nseg - 1), slices);
   cudaError_t e;
-  if (p.nseg > 1 && (p.launches & 1)) {
-    const dim3 grid(units, (unsigned)(p.nseg - 1), slices);
-    auto small_chunks = [&]() {
-      constexpr size_t smem = StateLayout<W>::bytes + 1024;
-      auto* k = decay_tc_state_kernel<REV, W>;
-      if ((e = room(k, smem)) == cudaSuccess) k<<<grid, kStateThreads<W> + 32, smem, s>>>(a);
-    };
-    if constexpr (W == 1) {
-      if ((int64_t)units * (p.nseg - 1) * slices >= 4 * kOpsSms) {
-        small_chunks();
-      } else {
-        constexpr size_t smem = Layout<false, W>::bytes + 1024;
-        auto* k = decay_tc_kernel<false, REV, W>;
-        if ((e = room(k, smem)) == cudaSuccess) k<<<grid, threads, smem, s>>>(a);
-      }
-    } else {
+  auto small_chunks = [&]() {
+    constexpr size_t smem = StateLayout<XB, ZB>::bytes + 1024;
+    auto* k = decay_tc_state_kernel<REV, XB, ZB>;
+    if ((e = room(k, smem)) == cudaSuccess) k<<<grid, kStateThreads<XB> + 32, smem, s>>>(a);
+  };
+  if constexpr (XB == 1) {
+    if ((int64_t)units * (p.nseg - 1) * slices >= 4 * kOpsSms) {
       small_chunks();
+    } else {
+      constexpr size_t smem = Layout<false>::bytes + 1024;
+      auto* k = decay_tc_kernel<false, REV>;
+      if ((e = room(k, smem)) == cudaSuccess) k<<<grid, kThreads, smem, s>>>(a);
     }
-    if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_decay_scan(p, s)) != cudaSuccess) return e;
+  } else {
+    small_chunks();
   }
-  if (!(p.launches & 2)) return cudaSuccess;
-  constexpr size_t smem = Layout<true, W>::bytes + 1024;
-  auto* k = decay_tc_kernel<true, REV, W>;
-  if ((e = room(k, smem)) != cudaSuccess) return e;
-  const dim3 grid(units, (unsigned)p.nseg, slices);
-  if (p.nseg > 1) return (cudaError_t)launch_pdl(k, grid, dim3(threads), smem, s, a);
-  k<<<grid, threads, smem, s>>>(a);
+  if (e != cudaSuccess || (e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_decay_scan(p, s);
+}
+
+template <bool REV>
+cudaError_t pass(const TcArgs& a, cudaStream_t s) {
+  const DecayPass& p = a.p;
+  constexpr size_t smem = Layout<true>::bytes + 1024;
+  auto* k = decay_tc_kernel<true, REV>;
+  const cudaError_t e = room(k, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(p.B * p.H), (unsigned)p.nseg, (unsigned)(p.DZ / D));
+  if (p.nseg > 1) return (cudaError_t)launch_pdl(k, grid, dim3(kThreads), smem, s, a);
+  k<<<grid, kThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -818,8 +717,16 @@ cudaError_t launch_decay_tc(const DecayPass& p, cudaStream_t s) {
       !make_map(&a.y64, p.y, p.sy, p.DX, p, D, kStateChunk, 128) ||
       !make_map(&a.z64, p.z, p.sz, p.DZ, p, D, kStateChunk, 128))
     return cudaErrorNotSupported;
-  if (p.DX == 2 * D) return p.reverse ? run<true, 2>(a, s) : run<false, 2>(a, s);
-  return p.reverse ? run<true, 1>(a, s) : run<false, 1>(a, s);
+  const bool wide = p.DX == 2 * D;
+  if (p.nseg > 1 && (p.launches & 1)) {
+    const cudaError_t e = !wide            ? (p.reverse ? states<true, 1, 1>(a, s) : states<false, 1, 1>(a, s))
+                          : p.DZ == 2 * D ? (p.reverse ? states<true, 2, 2>(a, s) : states<false, 2, 2>(a, s))
+                                          : (p.reverse ? states<true, 2, 1>(a, s) : states<false, 2, 1>(a, s));
+    if (e != cudaSuccess) return e;
+  }
+  if (!(p.launches & 2)) return cudaSuccess;
+  if (wide) return launch_decay_tc_wide(a, s);
+  return p.reverse ? pass<true>(a, s) : pass<false>(a, s);
 }
 
 }  // namespace mhla
