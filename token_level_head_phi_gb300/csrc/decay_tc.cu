@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
 
   const int unit = blockIdx.x, seg = blockIdx.y, z0 = blockIdx.z * D;
   const int b = unit / p.H, h = unit % p.H;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid / 32, 0), lane = tid % 32;
   const int q = warp & 3, half = (warp >> 2) & 1;  // lanes 32 q .. of tensor memory, half of the columns
   const float g = p.g[h];
   const int length = decay_length(p, b);
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
   const uint32_t bar_r = smem_u32(&tail.bar[3]);  // the outputs before have been read out of shared memory (8 warps)
   const uint32_t full[2] = {smem_u32(&tail.full[0]), smem_u32(&tail.full[1])}, full_x = smem_u32(&tail.full_x);
   // the ninth warp's first lane loads the chunks and issues the products
-  const bool issuer = tid == kWork;
+  const bool issuer = warp == kWork / 32 && elect_one();
   int loaded = 0, loaded_x = 0, seen = 0, seen_x = 0;  // chunks asked for, and waited for
   auto fetch = [&](int c0) {
     const uint32_t st = (uint32_t)(c0 / C) & 1u;
@@ -202,18 +202,19 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
     constexpr uint32_t id_d = idesc_bf16_f32(128, 128, false, false), id_o = idesc_bf16_f32(128, 64, false, false);
     constexpr uint32_t id_p = idesc_bf16_f32(128, 64, false, true);
     constexpr uint32_t id_u = idesc_bf16_f32(128, 128, true, true), id_l = idesc_bf16_f32(128, 64, true, true);
+    const bool leader = elect_one();
     for (int c0 = 0; c0 < valid; c0 += C) {
       const uint32_t st = (uint32_t)(c0 / C) & 1u;
       const uint32_t ya = base + L::y + st * kTile, za = base + L::z + st * kTile;
       const bool more = c0 + C < valid;
-      if (lane == 0) {
+      if (leader) {
         ok = mbar_wait(full[st], (uint32_t)(c0 / C >> 1) & 1u, p.err, 0xd06, abort_flag);
         if (OUT) ok = mbar_wait(full_x, st, p.err, 0xd07, abort_flag) && ok;
         if (ok) ++seen, seen_x += OUT;
       }
       if (__syncthreads_or(!ok)) break;
       if (dirty(c0)) __syncthreads();
-      if (OUT && lane == 0) {
+      if (OUT && leader) {
         tc_fence_after();
         const uint64_t xd = sdesc_sw128(base + L::x, 0u, 1024u), yd = sdesc_sw128(ya, 0u, 1024u);
         const uint64_t sd = sdesc_sw128(base + L::s, 0u, 1024u);
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
         umma_commit(bar_a);
       }
       __syncwarp();
-      if (more && lane == 0) {
+      if (more && leader) {
         // the outputs of the chunk before leave through its y
         if (OUT) ok = mbar_wait(bar_r, st, p.err, 0xd0b, abort_flag);
         fetch(c0 + C);
@@ -235,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
       }
       __syncwarp();
       if (__syncthreads_or(!ok)) break;
-      if (lane == 0) {
+      if (leader) {
         tc_fence_after();
         const uint64_t zd = sdesc_sw128(za, 0u, 1024u);
         const uint64_t wd = sdesc_sw128(ya, base + L::mid - ya, 1024u);
@@ -254,13 +255,13 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
         }
       }
       __syncwarp();
-      if (OUT && more && exact && lane == 0) {  // x has held the third part of w Y
+      if (OUT && more && exact && leader) {  // x has held the third part of w Y
         ok = mbar_wait(bar_u, st, p.err, 0xd04, abort_flag);
         fetch_x(c0 + C);
       }
       __syncwarp();
     }
-    if (lane == 0) {  // after an early end: no copy may land once the CTA is gone
+    if (leader) {  // after an early end: no copy may land once the CTA is gone
       for (; seen < loaded; ++seen) mbar_wait(full[seen & 1], (uint32_t)(seen >> 1) & 1u, p.err, 0xd08);
       for (; seen_x < loaded_x; ++seen_x) mbar_wait(full_x, (uint32_t)seen_x & 1u, p.err, 0xd09);
     }
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kStateThreads<XB> + 32, XB == 1 ? 4 : 2)
 
   const int unit = blockIdx.x, seg = blockIdx.y, z0 = blockIdx.z * (ZB * D);
   const int b = unit / p.H, h = unit % p.H;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid / 32, 0), lane = tid % 32;
   const float g = p.g[h];
   const int length = decay_length(p, b);
   const int begin = seg * p.seg_len;
@@ -513,7 +514,7 @@ __global__ void __launch_bounds__(kStateThreads<XB> + 32, XB == 1 ? 4 : 2)
       load_rows(base + L::z + st * L::kZ + k * kStateBlock, a.z64, full[st], z0 + k * D, token, h, b);
     ++loaded;
   };
-  if (tid == kStateWork) {
+  if (warp == kStateWork / 32 && elect_one()) {
     mbar_init(bar, 1);
     mbar_init(full[0], 1);
     mbar_init(full[1], 1);
@@ -547,19 +548,20 @@ __global__ void __launch_bounds__(kStateThreads<XB> + 32, XB == 1 ? 4 : 2)
   if (warp == kStateWork / 32) {
     constexpr uint32_t id_u = idesc_bf16_f32(128, 128, true, true), id_l = idesc_bf16_f32(128, XB * D, true, true);
     constexpr uint32_t kZStep = ZB == 1 ? 0u : kStateBlock;
+    const bool leader = elect_one();
     for (int c0 = 0; c0 < valid; c0 += N) {
       const uint32_t st = (uint32_t)(c0 / N) & 1u;
       const uint32_t ya = base + L::y + st * L::kY, za = base + L::z + st * L::kZ;
-      if (lane == 0) {
+      if (leader) {
         ok = mbar_wait(full[st], (uint32_t)(c0 / N >> 1) & 1u, p.err, 0xd0c, abort_flag);
         if (ok) ++seen;
       }
       if (__syncthreads_or(!ok)) break;
       if (dirty(c0)) __syncthreads();
-      if (lane == 0 && c0 + N < valid) fetch(c0 + N);
+      if (leader && c0 + N < valid) fetch(c0 + N);
       __syncwarp();
       if (__syncthreads_or(0)) break;
-      if (lane == 0) {
+      if (leader) {
         tc_fence_after();
         const uint64_t zd = sdesc_sw128(za, kZStep, 1024u), ld = sdesc_sw128(base + L::lo, kStateBlock, 1024u);
         if constexpr (XB == 1) {
@@ -585,7 +587,7 @@ __global__ void __launch_bounds__(kStateThreads<XB> + 32, XB == 1 ? 4 : 2)
       }
       __syncwarp();
     }
-    if (lane == 0)
+    if (leader)
       for (; seen < loaded; ++seen) mbar_wait(full[seen & 1], (uint32_t)(seen >> 1) & 1u, p.err, 0xd0d);
     __syncwarp();
   } else {

@@ -26,6 +26,20 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t sr
                : "memory");
 }
 
+// True in one lane of a converged warp.  Work under this predicate, in a warp
+// whose index comes from a shuffle, keeps its addresses and descriptors in
+// uniform registers: a product issues in 40 cycles instead of 100 under
+// `lane == 0`.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0u;
+}
+
 // A map of rows and the places of its token, head and batch axes (1 to 3,
 // ordered by stride).
 struct RowMap {

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_wide_kernel(const __grid
 
   const int unit = blockIdx.x, seg = blockIdx.y, z0 = blockIdx.z * DZ;
   const int b = unit / p.H, h = unit % p.H;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid / 32, 0), lane = tid % 32;
   const int q = warp & 3, half = (warp >> 2) & 1;  // lanes 32 q .. of tensor memory, half of the columns
   const bool outputs = warp < kGroup / 32, issues = warp == kWork / 32;
   const float g = p.g[h];
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_wide_kernel(const __grid
     for (int k = 0; k < 2; ++k) load_rows(base + L::x + k * kBlock, a.x, bar(kX), k * D, first_token(c0), h, b);
     ++loaded_x;
   };
-  if (tid == kWork) {
+  if (issues && elect_one()) {
     for (int i = 0; i < kBars; ++i)
       mbar_init(bar(i), i == kP || i == kO || i == kW || i == kS || i == kR ? kGroup / 32 : 1);
     tail.abort = 0;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_wide_kernel(const __grid
     // from one block of 64 columns of z to the next; a single one repeats, so
     // that all lanes of U hold rows
     constexpr uint32_t kZStep = ZB == 1 ? 0u : kBlock;
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t xd = sdesc_sw128(base + L::x, 0u, 1024u), sd = sdesc_sw128(base + L::s, 0u, 1024u);
       auto scores = [&](int c0) {
         const int i = c0 / C;
