@@ -40,6 +40,7 @@ struct DecayPass {
   int s_ldx, s_ldz;   // element strides of a state's x and z axes, in s_in, s_out and seg
   int B, H, N, DX, DZ;
   int nseg, seg_len;
+  int slice;     // columns of z that a CTA of the 128-entry tcgen05 pass takes
   int launches;  // 1: the states before the segments, 2: the pass itself, 3: both
   int reverse;  // 1: token i of the pass is the sequence's token length - 1 - i
   int e;

@@ -38,33 +38,39 @@ bool big_tiles(int dx, int dz) { return dx >= 64 && dz % 64 == 0; }
 // (32k tokens x 64 heads: 7 segments, one wave; 2k tokens x 60 heads of 128:
 // 5 segments, two waves, 92 against 105 us with 2 segments in one wave.)
 constexpr int kSegQuantum = 128, kSegMost = 64, kSegStart = 100;
+constexpr double kNarrow = 0.8;
 
-void plan_segments(const mhla_decay_params* p, int dx, int dz, int* nseg, int* seg_len) {
-  const bool wide = on_tensor_cores(p) && dx == 128;
-  const int slice = !wide ? 64 : big_tiles(dx, dz) ? dz : 32;
-  const int64_t ctas = (int64_t)p->batch * p->heads * (dz > slice ? dz / slice : 1);
-  const int64_t slots = (wide && slice >= 64 ? 1 : on_tensor_cores(p) && !big_tiles(dx, dz) ? 3 : 2) * kOpsSms;
-  *nseg = 1;
-  *seg_len = (p->tokens + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
-  double best = (double)((ctas + slots - 1) / slots) * (*seg_len + kSegStart);
-  for (int n = 2; n <= kSegMost; ++n) {
-    int len = (p->tokens + n - 1) / n;
-    len = (len + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
-    const int count = (p->tokens + len - 1) / len;
-    if (count != n) continue;
-    const double cost = 1.6 * (double)((ctas * n + slots - 1) / slots) * (len + kSegStart);
-    if (cost < best) {
-      best = cost;
-      *nseg = n;
-      *seg_len = len;
+struct Plan {
+  int nseg, seg_len;
+  int slice;  // columns of z that a CTA takes
+};
+
+Plan plan_segments(const mhla_decay_params* p, int dx, int dz) {
+  const bool tc = on_tensor_cores(p) && big_tiles(dx, dz), wide = on_tensor_cores(p) && dx == 128;
+  const int64_t slots = (tc && wide ? 1 : on_tensor_cores(p) && !tc ? 3 : 2) * kOpsSms;
+  const int most = wide && !tc ? 32 : tc && wide ? 128 : 64;
+  const int tokens = (p->tokens + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
+  Plan best = {};
+  double least = 0.;
+  for (int slice = dz < most ? dz : most; slice >= (tc ? 64 : dz < most ? dz : most); slice /= 2) {
+    const int64_t ctas = (int64_t)p->batch * p->heads * (dz / slice);
+    const double weight = tc && wide && slice == 64 ? kNarrow : 1.;
+    for (int n = 1; n <= kSegMost; ++n) {
+      int len = (tokens / kSegQuantum + n - 1) / n * kSegQuantum;
+      if (len < kSegQuantum) len = kSegQuantum;
+      if (n > 1 && (p->tokens + len - 1) / len != n) continue;
+      const double cost = (n > 1 ? 1.6 : 1.) * weight * (double)((ctas * n + slots - 1) / slots) * (len + kSegStart);
+      if (best.nseg == 0 || cost < least) {
+        least = cost;
+        best = {n, len, slice};
+      }
     }
   }
-  if (*seg_len < kSegQuantum) *seg_len = kSegQuantum;
+  return best;
 }
 
 size_t pass_workspace(const mhla_decay_params* p, int dx, int dz) {
-  int nseg, seg_len;
-  plan_segments(p, dx, dz, &nseg, &seg_len);
+  const int nseg = plan_segments(p, dx, dz).nseg;
   return nseg > 1 ? sizeof(float) * (size_t)p->batch * p->heads * nseg * dx * dz : 0;
 }
 
@@ -85,7 +91,10 @@ DecayPass pass_of(const mhla_decay_params* p, int dx, int dz, unsigned int* err)
   a.N = p->tokens;
   a.DX = dx;
   a.DZ = dz;
-  plan_segments(p, dx, dz, &a.nseg, &a.seg_len);
+  const Plan plan = plan_segments(p, dx, dz);
+  a.nseg = plan.nseg;
+  a.seg_len = plan.seg_len;
+  a.slice = plan.slice;
   a.launches = 3;
   a.err = err;
   return a;

@@ -468,7 +468,7 @@ cudaError_t run(const TcArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_decay_tc_wide(const TcArgs& a, cudaStream_t s) {
-  if (a.p.DZ == 2 * D) return a.p.reverse ? run<true, 2>(a, s) : run<false, 2>(a, s);
+  if (a.p.slice == 2 * D) return a.p.reverse ? run<true, 2>(a, s) : run<false, 2>(a, s);
   return a.p.reverse ? run<true, 1>(a, s) : run<false, 1>(a, s);
 }
 
