@@ -367,6 +367,59 @@ def test_other_stream_and_graph():
     assert torch.equal(out, want) and torch.equal(st, state)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,d", [(60, 64), (256, 64), (900, 64), (1400, 128)])
+def test_backward_in_place_streams_and_graph(n, d, dtype):
+    """The gradients' passes run side by side: same bits in place, on another stream, and from a graph."""
+    q, k, v, do = (make((2, 3, n, d), dtype, i) for i in (1, 2, 3, 4))
+    g, state, ds = decays(3), make((2, 3, d, d), "f32", 5), make((2, 3, d, d), "f32", 6)
+    want = mb.mhla_decay_backward(q, k, v, g, do, state=state, dstate_out=ds)
+    inplace = ds.clone()
+    for x, y in zip(mb.mhla_decay_backward(q, k, v, g, do, state=state, dstate_out=inplace, dstate=inplace), want):
+        assert torch.equal(x, y)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = mb.mhla_decay_backward(q, k, v, g, do, state=state, dstate_out=ds, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    first, second = ([torch.zeros_like(x) for x in want] for _ in range(2))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for into in (first, second):  # the side streams join one capture twice
+            mb.mhla_decay_backward(q, k, v, g, do, state=state, dstate_out=ds, dq=into[0], dk=into[1], dv=into[2],
+                                   dstate=into[3])
+    for _ in range(2):
+        graph.replay()
+    for into in (first, second):
+        for x, y in zip(into, want):
+            assert torch.equal(x, y)
+
+
+def test_backward_beside_a_capture():
+    """A call on a stream of its own while the same thread captures another one stays out of the capture."""
+    n, d = 100, 64  # one segment: no workspace
+    q, k, v, do = (make((1, 2, n, d), "bf16", i) for i in (1, 2, 3, 4))
+    g = decays(2)
+    want = mb.mhla_decay_backward(q, k, v, g, do)
+    into, beside = ([torch.zeros_like(x) for x in want[:3]] for _ in range(2))
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mb.mhla_decay_backward(q, k, v, g, do, dq=into[0], dk=into[1], dv=into[2])
+        mb.mhla_decay_backward(q, k, v, g, do, dq=beside[0], dk=beside[1], dv=beside[2], stream=other)
+    torch.cuda.synchronize()
+    for x, y in zip(beside, want):
+        assert torch.equal(x, y)
+    for x in into:
+        assert not x.any()
+    graph.replay()
+    for x, y in zip(into, want):
+        assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("n", [70, 1000])
 def test_unaligned_rows(n, d):

@@ -1,6 +1,8 @@
 // C entries of linear attention with a decay for each head (declared in
 // include/mhla.h): checks, the segment plan and the passes of decay.h.
+#include <algorithm>
 #include <cmath>
+#include <map>
 
 #include "decay.h"
 #include "ops.h"
@@ -38,14 +40,14 @@ bool big_tiles(int dx, int dz) { return dx >= 64 && dz % 64 == 0; }
 // (32k tokens x 64 heads: 7 segments, one wave; 2k tokens x 60 heads of 128:
 // 5 segments, two waves, 92 against 105 us with 2 segments in one wave.)
 constexpr int kSegQuantum = 128, kSegMost = 64, kSegStart = 100;
-constexpr double kNarrow = 0.8;
+constexpr double kNarrow = 0.8, kWaveSlack = 0.1;
 
 struct Plan {
   int nseg, seg_len;
   int slice;  // columns of z that a CTA takes
 };
 
-Plan plan_segments(const mhla_decay_params* p, int dx, int dz) {
+Plan plan_segments(const mhla_decay_params* p, int dx, int dz, int passes) {
   const bool tc = on_tensor_cores(p) && big_tiles(dx, dz), wide = on_tensor_cores(p) && dx == 128;
   const int64_t slots = (tc && wide ? 1 : on_tensor_cores(p) && !tc ? 3 : 2) * kOpsSms;
   const int most = wide && !tc ? 32 : tc && wide ? 128 : 64;
@@ -53,13 +55,14 @@ Plan plan_segments(const mhla_decay_params* p, int dx, int dz) {
   Plan best = {};
   double least = 0.;
   for (int slice = dz < most ? dz : most; slice >= (tc ? 64 : dz < most ? dz : most); slice /= 2) {
-    const int64_t ctas = (int64_t)p->batch * p->heads * (dz / slice);
+    const int64_t ctas = (int64_t)p->batch * p->heads * (dz / slice) * passes;
     const double weight = tc && wide && slice == 64 ? kNarrow : 1.;
     for (int n = 1; n <= kSegMost; ++n) {
       int len = (tokens / kSegQuantum + n - 1) / n * kSegQuantum;
       if (len < kSegQuantum) len = kSegQuantum;
       if (n > 1 && (p->tokens + len - 1) / len != n) continue;
-      const double cost = (n > 1 ? 1.6 : 1.) * weight * (double)((ctas * n + slots - 1) / slots) * (len + kSegStart);
+      const double waves = std::max(1., std::ceil((double)(ctas * n) / (double)slots - kWaveSlack));
+      const double cost = (n > 1 ? 1.6 : 1.) * weight * waves * (len + kSegStart);
       if (best.nseg == 0 || cost < least) {
         least = cost;
         best = {n, len, slice};
@@ -69,9 +72,10 @@ Plan plan_segments(const mhla_decay_params* p, int dx, int dz) {
   return best;
 }
 
-size_t pass_workspace(const mhla_decay_params* p, int dx, int dz) {
-  const int nseg = plan_segments(p, dx, dz).nseg;
-  return nseg > 1 ? sizeof(float) * (size_t)p->batch * p->heads * nseg * dx * dz : 0;
+size_t pass_workspace(const mhla_decay_params* p, int dx, int dz, int passes) {
+  const int nseg = plan_segments(p, dx, dz, passes).nseg;
+  const size_t bytes = nseg > 1 ? sizeof(float) * (size_t)p->batch * p->heads * nseg * dx * dz : 0;
+  return (bytes + 255) / 256 * 256;
 }
 
 RowTensor tensor(const mhla_decay_params* p, const void* ptr, const mhla_strides& s, int dim) {
@@ -84,14 +88,14 @@ RowTensor state_tensor(const mhla_decay_params* p, const float* ptr) {
 
 bool state_ok(const RowTensor& t) { return row_tensor_ok(t, false) && (uintptr_t)t.ptr % 16 == 0; }
 
-DecayPass pass_of(const mhla_decay_params* p, int dx, int dz, unsigned int* err) {
+DecayPass pass_of(const mhla_decay_params* p, int dx, int dz, int passes, unsigned int* err) {
   DecayPass a = {};
   a.B = p->batch;
   a.H = p->heads;
   a.N = p->tokens;
   a.DX = dx;
   a.DZ = dz;
-  const Plan plan = plan_segments(p, dx, dz);
+  const Plan plan = plan_segments(p, dx, dz, passes);
   a.nseg = plan.nseg;
   a.seg_len = plan.seg_len;
   a.slice = plan.slice;
@@ -132,6 +136,82 @@ cudaError_t launch_pass(const DecayPass& a, const mhla_decay_params* p, cudaStre
   return launch_decay_mma(a, s);
 }
 
+// Side streams of the calling thread and the current device.  The passes of
+// the three gradients run side by side on them: alone, each of them leaves SMs
+// idle at its start and end and wherever its segments do not fill a wave (2 x
+// 8k tokens x 16 heads of 64: 134 us one after another, 111 side by side; 3 x
+// 777 tokens x 5 heads, float32: 93 and 47).  A capture of the caller's stream
+// takes the side streams along, as branches of its graph.
+constexpr int kGradients = 3;
+
+class Branches {
+ public:
+  ~Branches() {
+    for (int i = 0; i < 2; ++i) {
+      if (stream_[i]) cudaStreamDestroy(stream_[i]);
+      if (done_[i]) cudaEventDestroy(done_[i]);
+    }
+    if (ready_) cudaEventDestroy(ready_);
+  }
+  // Whether the side streams can follow s: they exist and are in no capture
+  // but that of s.
+  bool open(cudaStream_t s) {
+    if (!made_) made_ = make() ? 1 : -1;
+    used_ = 0;
+    unsigned long long id[3] = {};
+    bool same = made_ == 1 && capture(s, &id[2]);
+    for (int i = 0; i < 2; ++i) same = same && capture(stream_[i], &id[i]) && id[i] == (id[i] ? id[2] : 0);
+    if (!same) cudaGetLastError();
+    return same;
+  }
+  // Side stream i, behind what s holds now; s itself if that fails.
+  cudaStream_t fork(int i, cudaStream_t s) {
+    if (cudaEventRecord(ready_, s) != cudaSuccess || cudaStreamWaitEvent(stream_[i], ready_, 0) != cudaSuccess) {
+      cudaGetLastError();
+      return s;
+    }
+    used_ |= 1 << i;
+    return stream_[i];
+  }
+  // s waits for the side streams.
+  cudaError_t join(cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < 2; ++i) {
+      if (!(used_ >> i & 1)) continue;
+      cudaError_t j = cudaEventRecord(done_[i], stream_[i]);
+      if (j == cudaSuccess) j = cudaStreamWaitEvent(s, done_[i], 0);
+      if (e == cudaSuccess) e = j;
+    }
+    return e;
+  }
+
+ private:
+  static bool capture(cudaStream_t s, unsigned long long* id) {  // its id, 0 outside one
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    if (cudaStreamGetCaptureInfo(s, &status, id) != cudaSuccess || status == cudaStreamCaptureStatusInvalidated)
+      return false;
+    if (status == cudaStreamCaptureStatusNone) *id = 0;
+    return true;
+  }
+  bool make() {
+    bool ok = cudaEventCreateWithFlags(&ready_, cudaEventDisableTiming) == cudaSuccess;
+    for (int i = 0; i < 2; ++i)
+      ok = ok && cudaStreamCreateWithFlags(&stream_[i], cudaStreamNonBlocking) == cudaSuccess &&
+           cudaEventCreateWithFlags(&done_[i], cudaEventDisableTiming) == cudaSuccess;
+    return ok;
+  }
+  int made_ = 0, used_ = 0;
+  cudaStream_t stream_[2] = {};
+  cudaEvent_t ready_ = nullptr, done_[2] = {};
+};
+
+Branches& branches() {
+  thread_local std::map<int, Branches> of_device;
+  int device = 0;
+  cudaGetDevice(&device);
+  return of_device[device];
+}
+
 // Whether `out` shares memory with none of `in`.
 bool apart_from_all(const RowTensor& out, const RowTensor* in, int n) {
   for (int i = 0; i < n; ++i)
@@ -149,7 +229,7 @@ mhla_status mhla_decay_workspace_bytes(const mhla_decay_params* p, size_t* bytes
   if (!bytes) return MHLA_ERR_INVALID_ARG;
   const mhla_status st = check_params(p);
   if (st != MHLA_OK) return st;
-  *bytes = pass_workspace(p, p->key_dim, p->value_dim);
+  *bytes = pass_workspace(p, p->key_dim, p->value_dim, 1);
   return MHLA_OK;
 }
 
@@ -172,7 +252,7 @@ mhla_status mhla_decay_forward(const void* q, const void* k, const void* v, cons
     return MHLA_ERR_INVALID_ARG;
   if (state_out != state_in && !row_tensors_apart(ts, in[5])) return MHLA_ERR_INVALID_ARG;
   if (p->tokens == 0) return copy_state(p, state_in, state_out, s);
-  const size_t need = pass_workspace(p, p->key_dim, p->value_dim);
+  const size_t need = pass_workspace(p, p->key_dim, p->value_dim, 1);
   const RowTensor tw = flat_tensor(workspace, workspace ? (int64_t)need : 0, 1);
   if (!apart_from_all(tw, in, 6) || !row_tensors_apart(tw, to) || !row_tensors_apart(tw, ts))
     return MHLA_ERR_INVALID_ARG;
@@ -180,7 +260,7 @@ mhla_status mhla_decay_forward(const void* q, const void* k, const void* v, cons
   if ((st = scratch.take(workspace, workspace_bytes, need, s)) != MHLA_OK) return st;
   unsigned int* err = nullptr;
   if ((st = ops_error_ptr(&err)) != MHLA_OK) return scratch.give_back(st);
-  DecayPass a = pass_of(p, p->key_dim, p->value_dim, err);
+  DecayPass a = pass_of(p, p->key_dim, p->value_dim, 1, err);
   set_rows(a, in[0], p->q, in[1], p->k, in[2], p->v, to, p->out);
   a.g = log_decay;
   a.lengths = lengths;
@@ -201,8 +281,8 @@ mhla_status mhla_decay_backward_workspace_bytes(const mhla_decay_params* p, size
   if (!bytes) return MHLA_ERR_INVALID_ARG;
   const mhla_status st = check_params(p);
   if (st != MHLA_OK) return st;
-  const size_t a = pass_workspace(p, p->value_dim, p->key_dim), b = pass_workspace(p, p->key_dim, p->value_dim);
-  *bytes = a > b ? a : b;
+  *bytes = pass_workspace(p, p->value_dim, p->key_dim, kGradients) +
+           pass_workspace(p, p->key_dim, p->value_dim, kGradients);
   return MHLA_OK;
 }
 
@@ -245,7 +325,7 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
 
   unsigned int* err = nullptr;
   if ((st = ops_error_ptr(&err)) != MHLA_OK) return scratch.give_back(st);
-  DecayPass a = pass_of(p, dval, dkey, err);  // dq
+  DecayPass a = pass_of(p, dval, dkey, kGradients, err);  // dq
   set_rows(a, in[3], p->dout, in[2], p->v, in[1], p->k, out[0], p->dq);
   a.g = log_decay;
   a.lengths = lengths;
@@ -256,11 +336,10 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
   a.e = 1;
   a.score = a.read = p->scale;
   a.update = 1.f;
-  cudaError_t e = launch_pass(a, p, s);
 
   // dk and dv carry the same states, transposed: the segments' own are formed
   // once, in dv's orientation.
-  DecayPass c = pass_of(p, dkey, dval, err);  // dv, and the gradient of the first state
+  DecayPass c = pass_of(p, dkey, dval, kGradients, err);  // dv, and the gradient of the first state
   set_rows(c, in[1], p->k, in[0], p->q, in[3], p->dout, out[2], p->dv);
   c.g = log_decay;
   c.lengths = lengths;
@@ -268,7 +347,7 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
   c.s_out = dstate_in;
   c.s_ldx = dval;
   c.s_ldz = 1;
-  c.seg = seg;
+  c.seg = seg + pass_workspace(p, dval, dkey, kGradients) / sizeof(float);
   c.reverse = 1;
   c.e = 0;
   c.score = p->scale;
@@ -283,10 +362,20 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
   b.s_ldz = dval;
   b.launches = 2;
   c.launches = 1;
+  Branches& side = branches();
+  const bool apart = side.open(s);
+  const cudaStream_t sa = apart ? side.fork(0, s) : s;
+  cudaError_t e = launch_pass(a, p, sa);
   if (e == cudaSuccess) e = launch_pass(c, p, s);
-  if (e == cudaSuccess) e = launch_pass(b, p, s);
+  // with one segment dk reads dstate_out while dv's pass writes dstate_in
+  const cudaStream_t sb = apart && (c.nseg > 1 || !dstate_in || dstate_in != dstate_out) ? side.fork(1, s) : s;
+  if (e == cudaSuccess) e = launch_pass(b, p, sb);
   c.launches = 2;
   if (e == cudaSuccess) e = launch_pass(c, p, s);
+  if (apart) {
+    const cudaError_t j = side.join(s);
+    if (e == cudaSuccess) e = j;
+  }
   return scratch.give_back(e == cudaSuccess ? MHLA_OK : record_cuda_error(e));
 }
 
@@ -308,7 +397,7 @@ mhla_status mhla_decay_step(const void* q, const void* k, const void* v, const f
   if (!apart_from_all(to, in, 5) || !row_tensors_apart(to, ts) || !apart_from_all(ts, in, 4))
     return MHLA_ERR_INVALID_ARG;
   if (state_out != state_in && !row_tensors_apart(ts, in[4])) return MHLA_ERR_INVALID_ARG;
-  DecayPass a = pass_of(p, p->key_dim, p->value_dim, nullptr);
+  DecayPass a = pass_of(p, p->key_dim, p->value_dim, 1, nullptr);
   set_rows(a, in[0], p->q, in[1], p->k, in[2], p->v, to, p->out);
   a.g = log_decay;
   a.s_in = state_in;
