@@ -26,21 +26,31 @@ bool on_tensor_cores(const mhla_decay_params* p) {
   return p->dtype == MHLA_DTYPE_BF16 && p->variant != MHLA_DECAY_SIMT;
 }
 
-// The tcgen05 kernel takes rows of 64 entries (and 16-byte alignment, and at
-// least one chunk of 128 tokens).  It is ahead of the mma.sync kernel there: 128 tokens x 64 heads
-// 6.7 against 7.2 us, 2k tokens 33 against 40, 32k tokens 336 against 405.
+// The tcgen05 kernels take rows of 64 and 128 entries and slices of 64 columns
+// (and 16-byte alignment, and at least one chunk of 128 tokens).  They are
+// ahead of the mma.sync kernel there: 64 heads of 64 entries, 128 tokens 6.7
+// against 7.2 us, 2k tokens 33 against 40, 32k tokens 287 against 405; of 128
+// entries, 60 heads of 2k tokens 54 against 111, 64 of 32k 621 against 1692.
 bool big_tiles(int dx, int dz) { return dx >= 64 && dz % 64 == 0; }
 
-// Segments of a pass.  CTAs (units x slices of 64 columns x segments; 32
-// columns with mma.sync and DX = 128) run in waves of those that are resident
-// at once: three on every SM with mma.sync, two otherwise.  A segment costs its tokens and about a hundred
-// more for its start, and more than one segment costs the launch that forms
-// their states, measured at 0.6 of the pass itself.  The count with the
-// smallest product wins; segments are of at least 128 tokens and at most 64.
-// (32k tokens x 64 heads: 7 segments, one wave; 2k tokens x 60 heads of 128:
-// 5 segments, two waves, 92 against 105 us with 2 segments in one wave.)
+// Segments of a pass, and with them the slices of z.  CTAs (units x slices x
+// segments) run in waves of those that are resident at once.  A segment costs
+// its tokens and about a hundred more for its start, and more than one segment
+// costs the launch that forms their states, measured at 0.6 of the pass itself.
+// The count with the smallest product wins; segments are of at least 128 tokens
+// and at most 64.  (mma.sync, 2k tokens x 60 heads of 128: 5 segments in two
+// waves 92 us, 2 in one wave 105.)
+//
+// The tcgen05 kernel for 128-entry rows also has a choice of slice: 64 columns
+// take 0.8 of the time of 128, and where that fills the SMs with one segment,
+// no states are needed (60 heads of 2k tokens: 54 us, 128 columns in one
+// segment 66, in two 70; 64 heads of 4k: 99, 119 and 123).
+//
+// `passes` run side by side (the gradients) and share the SMs: 2 x 8k tokens x
+// 16 heads of 64, 3 segments 111 us, 8 as for one pass 113; 4 x 2k tokens, one
+// segment 55, 4 as for one pass 72.
 constexpr int kSegQuantum = 128, kSegMost = 64, kSegStart = 100;
-constexpr double kNarrow = 0.8, kWaveSlack = 0.1;
+constexpr double kNarrow = 0.8;
 
 struct Plan {
   int nseg, seg_len;
@@ -48,21 +58,23 @@ struct Plan {
 };
 
 Plan plan_segments(const mhla_decay_params* p, int dx, int dz, int passes) {
-  const bool tc = on_tensor_cores(p) && big_tiles(dx, dz), wide = on_tensor_cores(p) && dx == 128;
-  const int64_t slots = (tc && wide ? 1 : on_tensor_cores(p) && !tc ? 3 : 2) * kOpsSms;
-  const int most = wide && !tc ? 32 : tc && wide ? 128 : 64;
-  const int tokens = (p->tokens + kSegQuantum - 1) / kSegQuantum * kSegQuantum;
+  const bool tc = on_tensor_cores(p) && big_tiles(dx, dz), mma = on_tensor_cores(p) && !tc;
+  const bool wide = tc && dx == 128;
+  const int widest = std::min(dz, wide ? 128 : mma && dx == 128 ? 32 : 64);
+  const int narrowest = wide ? 64 : widest;
+  // resident CTAs of an SM: by shared memory; the float32 kernel's with small states are smaller
+  const int resident = wide ? 1 : mma || (!tc && dx * widest <= 2048) ? 3 : 2;
+  const int64_t slots = resident * kOpsSms;
+  const int tokens = std::max(1, (p->tokens + kSegQuantum - 1) / kSegQuantum) * kSegQuantum;
   Plan best = {};
   double least = 0.;
-  for (int slice = dz < most ? dz : most; slice >= (tc ? 64 : dz < most ? dz : most); slice /= 2) {
+  for (int slice = widest; slice >= narrowest; slice /= 2) {
     const int64_t ctas = (int64_t)p->batch * p->heads * (dz / slice) * passes;
-    const double weight = tc && wide && slice == 64 ? kNarrow : 1.;
     for (int n = 1; n <= kSegMost; ++n) {
-      int len = (tokens / kSegQuantum + n - 1) / n * kSegQuantum;
-      if (len < kSegQuantum) len = kSegQuantum;
+      const int len = (tokens / kSegQuantum + n - 1) / n * kSegQuantum;
       if (n > 1 && (p->tokens + len - 1) / len != n) continue;
-      const double waves = std::max(1., std::ceil((double)(ctas * n) / (double)slots - kWaveSlack));
-      const double cost = (n > 1 ? 1.6 : 1.) * weight * waves * (len + kSegStart);
+      const double waves = (double)((ctas * n + slots - 1) / slots);
+      const double cost = (n > 1 ? 1.6 : 1.) * (wide && slice == 64 ? kNarrow : 1.) * waves * (len + kSegStart);
       if (best.nseg == 0 || cost < least) {
         least = cost;
         best = {n, len, slice};
