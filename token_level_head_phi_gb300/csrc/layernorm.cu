@@ -15,6 +15,7 @@
 
 #include "common.cuh"
 #include "ops.h"
+#include "tc_host.h"
 
 namespace mhla {
 namespace {
@@ -355,6 +356,7 @@ __global__ void __launch_bounds__(norm_bwd_threads<G>) norm_bwd_kernel(const Nor
     }
   }
   if (!a.partial) return;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // norm_reduce_kernel, which waits for all of this
 
   // groups that share a warp hold the same columns in lanes G apart
   if constexpr (G < 32) {
@@ -471,8 +473,9 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* partial,
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;  // over [2][cols]
   float s = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c < 2 * cols)
-#pragma unroll 8
+#pragma unroll 12
     for (int p = ty; p < parts; p += 32) s += partial[(int64_t)p * 2 * cols + c];
   sh[ty][tx] = s;
   __syncthreads();
@@ -766,9 +769,10 @@ mhla_status mhla_layernorm_backward(const void* dy, const void* x, const void* w
     st = with_bwd_shape<float>(p->cols, vec, Backward<float>{a, s, parts.n});
   }
   if (st == MHLA_OK && sums) {
-    norm_reduce_kernel<<<(unsigned)((2 * p->cols + 31) / 32), 1024, 0, s>>>(a.partial, (int)parts.n, p->cols, dweight,
-                                                                           dbias);
-    st = launch_status();
+    const cudaError_t e =
+        (cudaError_t)launch_pdl(norm_reduce_kernel, dim3((unsigned)((2 * p->cols + 31) / 32)), dim3(1024), 0, s,
+                                (const float*)a.partial, (int)parts.n, (int)p->cols, dweight, dbias);
+    if (e != cudaSuccess) st = record_cuda_error(e);
   }
   return scratch.give_back(st);
 }
