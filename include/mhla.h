@@ -406,7 +406,10 @@ mhla_status mhla_decay_forward(const void* q, const void* k, const void* v, cons
 /* Gradients of L = sum(dout * out) + sum(dstate_out * state_out) with respect
  * to q, k, v and state_in; nothing is kept from the forward call.
  * dstate_out NULL: zeros; dstate_in NULL: not wanted, or dstate_out (in
- * place).  Rows of dq, dk, dv past a sequence's length are written as zeros. */
+ * place).  Rows of dq, dk, dv past a sequence's length are written as zeros.
+ * The passes of the three gradients run side by side on `stream` and two
+ * streams of the calling thread, which `stream` has joined when the call
+ * returns; a capture of `stream` takes them along. */
 mhla_status mhla_decay_backward_workspace_bytes(const mhla_decay_params* p, size_t* bytes);
 mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, const float* log_decay,
                                 const int32_t* lengths, const float* state_in, const void* dout,

@@ -88,7 +88,7 @@ __device__ __forceinline__ int decay_token(const DecayPass& p, int i, int length
 cudaError_t launch_decay_scan(const DecayPass& p, cudaStream_t s);
 cudaError_t launch_decay_simt(const DecayPass& p, int dtype, cudaStream_t s);
 cudaError_t launch_decay_mma(const DecayPass& p, cudaStream_t s);  // bf16
-cudaError_t launch_decay_tc(const DecayPass& p, cudaStream_t s);   // bf16, DX = 64, DZ a multiple of 64, vec
+cudaError_t launch_decay_tc(const DecayPass& p, cudaStream_t s);   // bf16, DX = 64 or 128, DZ a multiple of 64, vec
 cudaError_t launch_decay_step(const DecayPass& p, int dtype, cudaStream_t s);
 
 }  // namespace mhla

@@ -28,9 +28,10 @@ bool on_tensor_cores(const mhla_decay_params* p) {
 
 // The tcgen05 kernels take rows of 64 and 128 entries and slices of 64 columns
 // (and 16-byte alignment, and at least one chunk of 128 tokens).  They are
-// ahead of the mma.sync kernel there: 64 heads of 64 entries, 128 tokens 6.7
-// against 7.2 us, 2k tokens 33 against 40, 32k tokens 287 against 405; of 128
-// entries, 60 heads of 2k tokens 54 against 111, 64 of 32k 621 against 1692.
+// ahead of the mma.sync kernel there: 64 heads of 64 entries, 128 tokens 10.8
+// against 12.8 us, 2k tokens 39 against 56, 32k tokens 287 against 414; of 128
+// entries, 128 tokens 12.8 against 14.8, 60 heads of 2k tokens 54 against 111,
+// 64 of 32k 621 against 1690 (graph launches, cold L2).
 bool big_tiles(int dx, int dz) { return dx >= 64 && dz % 64 == 0; }
 
 // Segments of a pass, and with them the slices of z.  CTAs (units x slices x
@@ -151,8 +152,9 @@ cudaError_t launch_pass(const DecayPass& a, const mhla_decay_params* p, cudaStre
 // Side streams of the calling thread and the current device.  The passes of
 // the three gradients run side by side on them: alone, each of them leaves SMs
 // idle at its start and end and wherever its segments do not fill a wave (2 x
-// 8k tokens x 16 heads of 64: 134 us one after another, 111 side by side; 3 x
-// 777 tokens x 5 heads, float32: 93 and 47).  A capture of the caller's stream
+// 8k tokens x 16 heads of 64: 134 us one after another, 111 side by side; 4 x
+// 2k tokens: 91 and 55; 3 x 777 tokens x 5 heads, float32: 93 and 66; 16 tokens
+// of one head: 27 and 14).  A capture of the caller's stream
 // takes the side streams along, as branches of its graph.
 constexpr int kGradients = 3;
 

@@ -2,9 +2,9 @@
 // decay.h for the pass).
 //
 // One CTA of four warps per (unit, segment, slice of at most 64 columns of z;
-// 32 with 128-entry rows) walks its segment in 64-token chunks; the next chunk's rows arrive by
-// asynchronous copies while the current one is worked on.  Per chunk, with
-// float32 accumulators throughout:
+// 32 with 128-entry rows) walks its segment in 64-token chunks; the next
+// chunk's rows arrive by asynchronous copies while the current one is worked
+// on.  Per chunk, with float32 accumulators throughout:
 //   o    = X S                  S in shared memory as bf16, rows scaled by lambda^(i + e)
 //   P    = X Y^T                16 x 16 tiles up to the diagonal, decayed and masked in registers
 //   o   += P Z                  P goes from accumulator to operand registers
@@ -17,6 +17,9 @@
 // the state is as exact as float32 sums are, and as two (16 bits) where it
 // feeds rounded outputs only; U starts from zero in every chunk, so the tensor
 // cores' truncating additions never run over the long sum.
+// Bound by issue slots: products and the arithmetic around them share them.
+// Measured: 32k tokens x 64 heads of 32 / 64 entries 283 us, of 64 414 us, of
+// 128 1690 us (the last two run here where rows are not 16-byte aligned).
 #include <type_traits>
 
 #include "common.cuh"

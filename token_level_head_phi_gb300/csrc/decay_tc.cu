@@ -32,9 +32,15 @@
 // The first launch forms the segments' states alone.  A chunk there is a chain
 // of waits (load, split, products, update) that other CTAs' chains fill: where
 // there are CTAs enough for four on every SM, a kernel of its own takes
-// 64-token chunks with four working warps (32k tokens x 64 heads: 293 against
-// 313 us in all); with fewer, this one (OUT = false, U in columns 0-127) is
-// ahead (8k tokens x 32 heads, backward: 138 against 149 us).
+// 64-token chunks with four working warps (32k tokens x 64 heads: 287 against
+// 300 us in all); with fewer, this one (OUT = false, U in columns 0-127) is
+// ahead (8k tokens x 64 heads: 105 against 113 us; backward on 8k x 32 heads:
+// 109 against 122 us).  For rows of 128 entries the 64-token kernel forms the
+// states and decay_tc_wide.cu has the pass.
+//
+// Measured, 16k tokens x 64 heads alone: states 55 us, pass 96 us = 5.3 TB/s.
+// Bound by the chains of a chunk, with shared memory (loads, parts, operands of
+// the products, outputs) busy for two thirds of the time.
 #include <type_traits>
 
 #include "decay_tc.cuh"

@@ -14,6 +14,12 @@
 //
 // Columns of tensor memory: D and P 0-127, U 128-255, O of X S from 256, O of
 // P Z behind it.  U adds the parts of w Y to one sum, the small ones first.
+//
+// Measured: 32k tokens x 64 heads of 128 621 us (pass, states and scan; the
+// chain of one group of warps 764, products issued by `lane == 0` 678), 60
+// heads of 2k tokens 54 us in slices of 64 columns.  A 128-token chunk of 128
+// columns takes 6000 cycles, its transfers through shared memory about 4600:
+// that bounds it, then the hand-overs between the groups.
 #include <type_traits>
 
 #include "decay_tc.cuh"
