@@ -35,12 +35,16 @@ bool on_tensor_cores(const mhla_decay_params* p) {
 bool big_tiles(int dx, int dz) { return dx >= 64 && dz % 64 == 0; }
 
 // Segments of a pass, and with them the slices of z.  CTAs (units x slices x
-// segments) run in waves of those that are resident at once.  A segment costs
-// its tokens and about a hundred more for its start, and more than one segment
-// costs the launch that forms their states, measured at 0.6 of the pass itself.
-// The count with the smallest product wins; segments are of at least 128 tokens
-// and at most 64.  (mma.sync, 2k tokens x 60 heads of 128: 5 segments in two
-// waves 92 us, 2 in one wave 105.)
+// segments) run in waves of those that are resident at once.  In each wave a
+// segment costs its tokens and about a hundred more for its start, and all
+// segments but the last cost half of that in the launch that forms their states
+// (0.9 for 128-entry rows, with two CTAs an SM; two such launches serve the
+// three gradients).  The launches themselves cost about 6 us = 250 tokens.  The
+// cheapest count wins; segments are of at least 128 tokens (64 on the CUDA
+// cores) and at most 64.  (32k tokens x 64 heads of 64: 19 segments 287 us, 9 to
+// 16 306 to 336, 4 371; of 128: 14 617, 4 695, 1 713; backward on 3 x 200 tokens
+// x 5 heads of 64: 1 14, 2 24; CUDA cores, 777 tokens x 15 heads of 64: 13
+// segments 37 us, 7 48; 400 tokens x 8 heads: 29 with 64-token segments, 44.)
 //
 // The tcgen05 kernel for 128-entry rows also has a choice of slice: 64 columns
 // take 0.8 of the time of 128, and where that fills the SMs with one segment,
@@ -50,8 +54,8 @@ bool big_tiles(int dx, int dz) { return dx >= 64 && dz % 64 == 0; }
 // `passes` run side by side (the gradients) and share the SMs: 2 x 8k tokens x
 // 16 heads of 64, 3 segments 111 us, 8 as for one pass 113; 4 x 2k tokens, one
 // segment 55, 4 as for one pass 72.
-constexpr int kSegQuantum = 128, kSegMost = 64, kSegStart = 100;
-constexpr double kNarrow = 0.8;
+constexpr int kSegMost = 64, kSegStart = 100, kSegLaunches = 250;
+constexpr double kNarrow = 0.8, kStates = 0.5, kStatesWide = 0.9;
 
 struct Plan {
   int nseg, seg_len;
@@ -65,19 +69,24 @@ Plan plan_segments(const mhla_decay_params* p, int dx, int dz, int passes) {
   const int narrowest = wide ? 64 : widest;
   // resident CTAs of an SM: by shared memory; the float32 kernel's with small states are smaller
   const int resident = wide ? 1 : mma || (!tc && dx * widest <= 2048) ? 3 : 2;
-  const int64_t slots = resident * kOpsSms;
-  const int tokens = std::max(1, (p->tokens + kSegQuantum - 1) / kSegQuantum) * kSegQuantum;
+  const int64_t slots = resident * kOpsSms, state_slots = (wide ? 2 : resident) * kOpsSms;
+  const int quantum = on_tensor_cores(p) ? 128 : 64;  // a chunk, or the larger of two kernels' chunks
+  const int tokens = std::max(1, (p->tokens + quantum - 1) / quantum) * quantum;
   Plan best = {};
   double least = 0.;
   for (int slice = widest; slice >= narrowest; slice /= 2) {
     const int64_t ctas = (int64_t)p->batch * p->heads * (dz / slice) * passes;
     for (int n = 1; n <= kSegMost; ++n) {
-      const int len = (tokens / kSegQuantum + n - 1) / n * kSegQuantum;
+      const int len = (tokens / quantum + n - 1) / n * quantum;
       if (n > 1 && (p->tokens + len - 1) / len != n) continue;
-      const double waves = (double)((ctas * n + slots - 1) / slots);
-      const double cost = (n > 1 ? 1.6 : 1.) * (wide && slice == 64 ? kNarrow : 1.) * waves * (len + kSegStart);
-      if (best.nseg == 0 || cost < least) {
-        least = cost;
+      const double weight = wide && slice == 64 ? kNarrow : 1.;
+      const double pass = weight * (double)((ctas * n + slots - 1) / slots) * (len + kSegStart);
+      const int64_t parts = ctas / passes * std::min(passes, 2) * (n - 1);
+      double states = (wide ? kStatesWide : kStates) * weight *
+                      (double)((parts + state_slots - 1) / state_slots) * (len + kSegStart);
+      if (n > 1) states += kSegLaunches;
+      if (best.nseg == 0 || pass + states < least) {
+        least = pass + states;
         best = {n, len, slice};
       }
     }
@@ -86,8 +95,8 @@ Plan plan_segments(const mhla_decay_params* p, int dx, int dz, int passes) {
 }
 
 size_t pass_workspace(const mhla_decay_params* p, int dx, int dz, int passes) {
-  const int nseg = plan_segments(p, dx, dz, passes).nseg;
-  const size_t bytes = nseg > 1 ? sizeof(float) * (size_t)p->batch * p->heads * nseg * dx * dz : 0;
+  const Plan plan = plan_segments(p, dx, dz, passes);
+  const size_t bytes = plan.nseg > 1 ? sizeof(float) * (size_t)p->batch * p->heads * plan.nseg * dx * dz : 0;
   return (bytes + 255) / 256 * 256;
 }
 
