@@ -158,11 +158,10 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
 
   // This thread's part of the state: column dz of z, entries dx0 .. dx0 + 15.
   const int dz = 32 * (q & 1) + lane, dx0 = 16 * ((q >> 1) * 2 + half);
-  float s[16];
+  const int64_t at = (int64_t)dx0 * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz;
+  float s[16] = {};
   const float* before = !OUT ? nullptr : p.nseg > 1 ? segs + seg * one : p.s_in ? p.s_in + state : nullptr;
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    s[i] = before && tid < kWork ? before[(int64_t)(dx0 + i) * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz] : 0.f;
+  if (before && tid < kWork) read_state(s, before + at, p.s_ldx);
   auto publish = [&]() {  // S as the second operand of X S: row dz, its entries along the row
     uint32_t v[8];
 #pragma unroll
@@ -459,9 +458,7 @@ __global__ void __launch_bounds__(kThreads, 2) decay_tc_kernel(const __grid_cons
   } else if (valid == 0) {
     return;
   }
-  float* to = OUT ? p.s_out + state : segs + (seg + 1) * one;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) to[(int64_t)(dx0 + i) * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz] = s[i];
+  write_state(s, (OUT ? p.s_out + state : segs + (seg + 1) * one) + at, p.s_ldx);
 }
 
 // ------------------- the segments' own states, many at once: 64-token chunks
@@ -672,8 +669,7 @@ __global__ void __launch_bounds__(kStateThreads<XB> + 32, XB == 1 ? 4 : 2)
   }
   if (valid == 0) return;
   float* to = p.seg + ((int64_t)unit * p.nseg + seg + 1) * (XB * D) * p.DZ;
-#pragma unroll
-  for (int i = 0; i < E; ++i) to[(int64_t)(dx0 + i) * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz] = s[i];
+  write_state(s, to + (int64_t)dx0 * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz, p.s_ldx);
 }
 
 template <bool REV, int XB, int ZB>

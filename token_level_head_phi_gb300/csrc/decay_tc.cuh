@@ -61,6 +61,32 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const RowMap& m, uint32_
               coordinate(m, 3, token, head, batch), policy_evict_first());
 }
 
+// E entries of a state along x, ldx apart, from a 16-byte boundary.
+template <int E>
+__device__ __forceinline__ void read_state(float (&s)[E], const float* from, int ldx) {
+  if (ldx == 1) {
+#pragma unroll
+    for (int i = 0; i < E; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(from + i);
+      s[i] = v.x, s[i + 1] = v.y, s[i + 2] = v.z, s[i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) s[i] = from[(int64_t)i * ldx];
+  }
+}
+template <int E>
+__device__ __forceinline__ void write_state(const float (&s)[E], float* to, int ldx) {
+  if (ldx == 1) {
+#pragma unroll
+    for (int i = 0; i < E; i += 4)
+      *reinterpret_cast<float4*>(to + i) = make_float4(s[i], s[i + 1], s[i + 2], s[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < E; ++i) to[(int64_t)i * ldx] = s[i];
+  }
+}
+
 // Axes ordered by stride, as nested as they are in memory.
 inline bool make_map(RowMap* m, const void* base, const mhla_strides& st, int64_t cols, const DecayPass& p, int box_cols,
               int box_rows, int swizzle) {

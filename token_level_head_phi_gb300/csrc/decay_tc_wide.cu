@@ -354,10 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_wide_kernel(const __grid
     const int dz = ZB == 1 ? 32 * (q & 1) + lane : 32 * q + lane;
     const int dx0 = ZB == 1 ? E * ((q >> 1) * 2 + half) : E * half;
     const int64_t at = (int64_t)dx0 * p.s_ldx + (int64_t)(z0 + dz) * p.s_ldz;
-    float s[E];
+    float s[E] = {};
     const float* before = p.nseg > 1 ? segs : p.s_in ? p.s_in + unit * one : nullptr;
-#pragma unroll
-    for (int i = 0; i < E; ++i) s[i] = before ? before[at + (int64_t)i * p.s_ldx] : 0.f;
+    if (before) read_state(s, before + at, p.s_ldx);
     auto publish = [&]() {  // S as the second operand of X S: row dz, its entries along the row
       uint8_t* to = mem + L::s + (dx0 / D) * (L::kS / 2);
 #pragma unroll
@@ -439,11 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) decay_tc_wide_kernel(const __grid
       }
       if (c0 + C < valid) publish();
     }
-    if (last && p.s_out) {
-      float* to = p.s_out + unit * one + at;
-#pragma unroll
-      for (int i = 0; i < E; ++i) to[(int64_t)i * p.s_ldx] = s[i];
-    }
+    if (last && p.s_out) write_state(s, p.s_out + unit * one + at, p.s_ldx);
     tc_fence_before();
   }
 
