@@ -1,0 +1,67 @@
+"""Calls of the sequence operators on streams of their own, several at a time."""
+
+import pytest
+import torch
+
+from token_level_head_phi_gb300 import binding as mb
+
+pytestmark = pytest.mark.gpu
+
+
+def make(shape, seed, dtype=torch.bfloat16):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=gen).to(dtype).cuda()
+
+
+def decay_forward(seed):
+    q, k, v = (make((1, 4, 2500, 64), seed + i) for i in range(3))
+    g = torch.full((4,), -0.01, device="cuda")
+    return lambda **kw: mb.mhla_decay_forward(q, k, v, g, **kw)
+
+
+def decay_backward(seed):
+    q, k, v, do = (make((1, 4, 2500, 64), seed + i) for i in range(4))
+    g, s = torch.full((4,), -0.01, device="cuda"), make((1, 4, 64, 64), seed, torch.float32)
+    return lambda **kw: mb.mhla_decay_backward(q, k, v, g, do, state=s, **kw)
+
+
+def norm_backward(seed):
+    x, dy = make((3000, 512), seed), make((3000, 512), seed + 1)
+    _, mean, rstd = mb.mhla_layernorm_forward(x)
+    return lambda **kw: mb.mhla_layernorm_backward(dy, x, mean, rstd, **kw)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("kind", [decay_forward, decay_backward, norm_backward])
+def test_calls_on_two_streams_at_once(kind, raw):
+    """Each has a workspace of its own, although neither waits for the other, and nor does the current stream."""
+    problems = [kind(10), kind(20)]
+    want = [p() for p in problems]
+    streams = [torch.cuda.Stream() for _ in problems]
+    torch.cuda.synchronize()
+    got, filled = [], []
+    for _ in range(10):
+        for p, s in zip(problems, streams):
+            got.append(p(stream=s.cuda_stream if raw else s))
+        filled.append(torch.full((1 << 20,), 7.0, device="cuda"))  # on the current stream
+    torch.cuda.synchronize()
+    for i, results in enumerate(got):
+        for x, y in zip(results, want[i % 2]):
+            assert torch.equal(x, y)
+    assert all((t == 7.0).all() for t in filled)
+
+
+def test_results_may_be_dropped_on_the_current_stream():
+    problem = norm_backward(30)
+    want, side = problem(), torch.cuda.Stream()
+    for _ in range(20):
+        side.wait_stream(torch.cuda.current_stream())
+        got = problem(stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+        del got, x
+
+
+def test_no_device_error_was_reported():
+    assert mb.mhla_device_status() == (0, 0)

@@ -459,6 +459,9 @@ def mhla_abi_version() -> int:
 # A call's checks and its parameter block depend only on the arguments' shapes,
 # strides, dtypes and devices, so they are made once for each such set and kept
 # (a decoding loop calls with the same ones for every token).
+#
+# Everything runs on torch's current stream, or on ``stream`` as it would under
+# ``torch.cuda.stream(stream)``: what a call allocates belongs to that stream.
 
 _CALLS: dict = {}
 _MOST_CALLS = 4096
@@ -545,6 +548,31 @@ def _current_stream(index) -> int:
     return torch.cuda.current_stream(index).cuda_stream
 
 
+def _on_stream(stream, like, outputs, call):
+    """call() with ``stream`` (a torch stream or a raw handle) as torch's current one.
+
+    So the workspace and the results come from that stream's memory, and no
+    other stream gets the workspace's block while the kernels still use it.
+    The results (all but the caller's own ``outputs``) may be read on the stream
+    that was current, behind a wait, and dropped there.
+    """
+    import torch
+    if not like.is_cuda:
+        raise ValueError("stream needs CUDA tensors")
+    index = like.get_device()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=index)
+    elif stream.device.index != index:
+        raise ValueError(f"stream must be on {like.device}")
+    before = torch.cuda.current_stream(index)
+    with torch.cuda.stream(stream):
+        results = call()
+    for t in results if isinstance(results, tuple) else (results,):
+        if t is not None and not any(t is o for o in outputs):
+            t.record_stream(before)
+    return results
+
+
 class _Call:
     """An entry point with its parameter block and what its wrapper needs beside them."""
 
@@ -558,10 +586,8 @@ class _Call:
         self.current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _current_stream
         self.__dict__.update(kw)
 
-    def stream(self, given) -> int:
-        if given is None:
-            return self.current(self.index)
-        return given.cuda_stream if hasattr(given, "cuda_stream") else int(given)
+    def stream(self) -> int:
+        return self.current(self.index)
 
     def workspace(self, given):
         """(tensor or None, bytes): the caller's workspace or a new one."""
@@ -645,6 +671,9 @@ def _rotary_call(q, k, positions, style, layout, q_out, k_out, transpose):
 
 
 def _rotary(q, k, plan, positions, offset, style, layout, q_out, k_out, stream, transpose, where):
+    if stream is not None:
+        return _on_stream(stream, q, (q_out, k_out), lambda: _rotary(
+            q, k, plan, positions, offset, style, layout, q_out, k_out, None, transpose, where))
     key = ("rotary", transpose, style, layout, _sig(q), _sig(k), _sig(positions), _sig(q_out), _sig(k_out))
     c = _CALLS.get(key) or _remember(key, _rotary_call(q, k, positions, style, layout, q_out, k_out, transpose))
     if q_out is None:
@@ -658,7 +687,7 @@ def _rotary(q, k, plan, positions, offset, style, layout, q_out, k_out, stream, 
         ref = ctypes.byref(p)
     status = c.call(q.data_ptr(), None if k is None else k.data_ptr(),
                     None if positions is None else positions.data_ptr(), plan._ref, ref, q_out.data_ptr(),
-                    None if k is None else k_out.data_ptr(), c.stream(stream))
+                    None if k is None else k_out.data_ptr(), c.stream())
     if status:
         raise MhlaError(status, where)
     return q_out, k_out
@@ -736,6 +765,9 @@ def mhla_layernorm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=Non
     ``rstd`` are float32 of x's leading shape, for the backward call.
     ``out is x`` normalises in place.
     """
+    if stream is not None:
+        return _on_stream(stream, x, (out, mean, rstd), lambda: mhla_layernorm_forward(
+            x, weight, bias, eps, out, mean, rstd))
     key = ("norm", eps, _sig(x), _sig(weight), _sig(bias), _sig(out), _sig(mean), _sig(rstd))
     c = _CALLS.get(key) or _remember(key, _norm_forward_call(x, weight, bias, eps, out, mean, rstd))
     if out is None:
@@ -745,7 +777,7 @@ def mhla_layernorm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=Non
     if rstd is None:
         rstd = c.empty(c.lead, dtype=c.f32, device=c.device)
     status = c.call(x.data_ptr(), _ptr(weight), _ptr(bias), c.ref, out.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                    c.stream(stream))
+                    c.stream())
     if status:
         raise MhlaError(status, "mhla_layernorm_forward")
     return out, mean, rstd
@@ -782,6 +814,9 @@ def mhla_layernorm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=Non
     fixed order; ``params=False`` leaves them out (None).  ``dx is dy`` or
     ``dx is x`` overwrites that input.
     """
+    if stream is not None:
+        return _on_stream(stream, x, (dx, dweight, dbias), lambda: mhla_layernorm_backward(
+            dy, x, mean, rstd, weight, dx, dweight, dbias, workspace, params=params))
     key = ("norm backward", params, _sig(dy), _sig(x), _sig(mean), _sig(rstd), _sig(weight), _sig(dx), _sig(dweight),
            _sig(dbias))
     c = _CALLS.get(key) or _remember(key, _norm_backward_call(dy, x, mean, rstd, weight, dx, dweight, dbias, params))
@@ -795,7 +830,7 @@ def mhla_layernorm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=Non
             dbias = c.empty(c.cols, dtype=c.f32, device=c.device)
         workspace, ws_bytes = c.workspace(workspace)
     status = c.call(dy.data_ptr(), x.data_ptr(), _ptr(weight), mean.data_ptr(), rstd.data_ptr(), c.ref, dx.data_ptr(),
-                    _ptr(dweight), _ptr(dbias), _ptr(workspace) if params else None, ws_bytes, c.stream(stream))
+                    _ptr(dweight), _ptr(dbias), _ptr(workspace) if params else None, ws_bytes, c.stream())
     if status:
         raise MhlaError(status, "mhla_layernorm_backward")
     return dx, dweight, dbias
@@ -857,6 +892,9 @@ def mhla_decay_forward(q, k, v, log_decay, state=None, lengths=None, scale: floa
     zeros); ``state_out is state`` updates it in place.  ``lengths``: int32
     [B] for sequences padded to N; rows past a length come out as zeros.
     """
+    if stream is not None:
+        return _on_stream(stream, q, (out, state_out), lambda: mhla_decay_forward(
+            q, k, v, log_decay, state, lengths, scale, layout, variant, out, state_out, workspace))
     key = ("decay", scale, layout, variant, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(state), _sig(lengths),
            _sig(out), _sig(state_out))
     c = _CALLS.get(key) or _remember(key, _decay_forward_call(q, k, v, log_decay, state, lengths, scale, layout,
@@ -867,7 +905,7 @@ def mhla_decay_forward(q, k, v, log_decay, state=None, lengths=None, scale: floa
         state_out = c.empty(c.shape, dtype=c.f32, device=c.device)
     workspace, ws_bytes = c.workspace(workspace)
     status = c.call(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths), _ptr(state), c.ref,
-                    out.data_ptr(), state_out.data_ptr(), _ptr(workspace), ws_bytes, c.stream(stream))
+                    out.data_ptr(), state_out.data_ptr(), _ptr(workspace), ws_bytes, c.stream())
     if status:
         raise MhlaError(status, "mhla_decay_forward")
     return out, state_out
@@ -903,6 +941,9 @@ def mhla_decay_backward(q, k, v, log_decay, dout, state=None, dstate_out=None, l
     [B, H, dk, dv]; None without one, unless a tensor is given for it).
     Arguments as in the forward call.
     """
+    if stream is not None:
+        return _on_stream(stream, q, (dq, dk, dv, dstate), lambda: mhla_decay_backward(
+            q, k, v, log_decay, dout, state, dstate_out, lengths, scale, layout, variant, dq, dk, dv, dstate, workspace))
     key = ("decay backward", scale, layout, variant, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(dout),
            _sig(state), _sig(dstate_out), _sig(lengths), _sig(dq), _sig(dk), _sig(dv), _sig(dstate))
     c = _CALLS.get(key) or _remember(key, _decay_backward_call(q, k, v, log_decay, dout, state, dstate_out, lengths,
@@ -915,7 +956,7 @@ def mhla_decay_backward(q, k, v, log_decay, dout, state=None, dstate_out=None, l
     workspace, ws_bytes = c.workspace(workspace)
     status = c.call(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(lengths), _ptr(state),
                     dout.data_ptr(), _ptr(dstate_out), c.ref, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dstate),
-                    _ptr(workspace), ws_bytes, c.stream(stream))
+                    _ptr(workspace), ws_bytes, c.stream())
     if status:
         raise MhlaError(status, "mhla_decay_backward")
     return dq, dk, dv, dstate
@@ -953,13 +994,16 @@ def mhla_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, sta
     q, k: [B, H, dk], v: [B, H, dv]; ``state`` float32 [B, H, dk, dv] is
     updated in place unless ``state_out`` is given.
     """
+    if stream is not None:
+        return _on_stream(stream, q, (out,), lambda: mhla_decay_step(
+            q, k, v, log_decay, state, scale, out, state_out))
     key = ("decay step", scale, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(state), _sig(out), _sig(state_out))
     c = _CALLS.get(key) or _remember(key, _decay_step_call(q, k, v, log_decay, state, scale, out, state_out))
     if out is None:
         out = c.new(v)
     at = state.data_ptr()
     status = c.call(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), at, c.ref, out.data_ptr(),
-                    at if state_out is None else state_out.data_ptr(), c.stream(stream))
+                    at if state_out is None else state_out.data_ptr(), c.stream())
     if status:
         raise MhlaError(status, "mhla_decay_step")
     return out
