@@ -1,4 +1,4 @@
-"""Calls of the sequence operators on streams of their own, several at a time."""
+"""Calls on streams of their own, several at a time."""
 
 import pytest
 import torch
@@ -31,8 +31,15 @@ def norm_backward(seed):
     return lambda **kw: mb.mhla_layernorm_backward(dy, x, mean, rstd, **kw)
 
 
+def block_attention(seed):
+    q, k, v, do = (make((1, 4, 1024, 64), seed + i) for i in range(4))
+    mc = torch.softmax(make((16, 16), seed, torch.float32), 1)
+    args = ((1, 32, 32), (1, 8, 8))
+    return lambda **kw: (mb.mhla_forward(q, k, v, mc, *args, **kw),) + mb.mhla_backward(q, k, v, mc, do, *args, **kw)
+
+
 @pytest.mark.parametrize("raw", [False, True])
-@pytest.mark.parametrize("kind", [decay_forward, decay_backward, norm_backward])
+@pytest.mark.parametrize("kind", [decay_forward, decay_backward, norm_backward, block_attention])
 def test_calls_on_two_streams_at_once(kind, raw):
     """Each has a workspace of its own, although neither waits for the other, and nor does the current stream."""
     problems = [kind(10), kind(20)]
@@ -61,6 +68,14 @@ def test_results_may_be_dropped_on_the_current_stream():
         for x, y in zip(got, want):
             assert torch.equal(x, y)
         del got, x
+
+
+def test_the_default_stream_by_handle():
+    problem = norm_backward(40)
+    want = problem()
+    for handle in (0, 1):
+        for x, y in zip(problem(stream=handle), want):
+            assert torch.equal(x, y)
 
 
 def test_no_device_error_was_reported():

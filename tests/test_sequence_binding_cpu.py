@@ -1,6 +1,6 @@
-"""Streams, memory and scalars of the binding's wrappers around the rotary,
-layer-norm and decayed-attention entries, on the CPU: tensors that pass for
-CUDA tensors, entries that record how they were called, no kernel."""
+"""Streams, memory and scalars of the binding's wrappers, on the CPU: tensors
+that pass for CUDA tensors, entries that record how they were called, no
+kernel."""
 
 import contextlib
 import types
@@ -13,7 +13,8 @@ from token_level_head_phi_gb300 import build as mbuild
 
 RAW = 0x7700  # a stream's handle
 ENTRIES = ("mhla_rotary", "mhla_layernorm_forward", "mhla_layernorm_backward", "mhla_decay_forward",
-           "mhla_decay_backward", "mhla_decay_step")
+           "mhla_decay_backward", "mhla_decay_step", "mhla_forward", "mhla_backward", "mhla_forward_noalloc",
+           "mhla_forward_host")
 
 
 class Card(torch.Tensor):
@@ -124,6 +125,33 @@ def test_own_results_are_left_alone(gpu):
     out, state = card(1, 2, 8, 64), card(1, 2, 64, 64, dtype=torch.float32)
     mb.mhla_decay_forward(q, q, q, g, out=out, state_out=state, stream=RAW)
     assert not hasattr(out, "recorded") and not hasattr(state, "recorded") and not gpu.allocated
+
+
+GRID, BLOCK = (1, 8, 8), (1, 4, 4)
+
+
+@pytest.mark.parametrize("name", ["mhla_forward", "mhla_backward", "mhla_forward_noalloc"])
+@pytest.mark.parametrize("stream", [None, RAW])
+def test_block_attention_memory_comes_from_the_stream_of_the_call(gpu, name, stream):
+    q, mc = card(1, 2, 64, 64), card(4, 4, dtype=torch.float32)
+    gpu.now = 0x4400
+    args = (q, q, q, mc) + ((q,) if name == "mhla_backward" else ())
+    results = getattr(mb, name)(*args, GRID, BLOCK, stream=stream)
+    want = stream or 0x4400
+    assert gpu.calls[-1].name == name and gpu.calls[-1].stream == want
+    assert len(gpu.allocated) == {"mhla_forward": 2, "mhla_backward": 5, "mhla_forward_noalloc": 1}[name]
+    assert all(at == want for at, _ in gpu.allocated)
+    for t in results if isinstance(results, tuple) else (results,):
+        assert not stream or t.recorded.cuda_stream == 0x4400
+
+
+def test_host_call_buffer_comes_from_the_stream_of_the_call(gpu, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    q, mc = torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16), torch.zeros(4, 4)
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
+    mb.mhla_forward_host(q, q, q, mc, GRID, BLOCK, out=torch.zeros_like(q), stream=RAW)
+    assert gpu.calls[-1].stream == RAW and [at for at, _ in gpu.allocated] == [RAW]
 
 
 def test_stream_needs_cuda_tensors():

@@ -256,6 +256,39 @@ def _params_for(q, grid, block, feature_map, norm, variant, causal=False, layout
     return make_params(B, H, d, grid, block, _torch_dtype_name(q), feature_map, norm, variant, causal, layout)
 
 
+def _torch_stream(stream, index):
+    """A torch stream or a raw handle as a torch stream of device ``index``."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        # 1 is another name of the default stream, which torch knows as 0
+        return torch.cuda.default_stream(index) if handle < 2 else torch.cuda.ExternalStream(handle, device=index)
+    if stream.device.index != index:
+        raise ValueError(f"stream must be on cuda:{index}")
+    return stream
+
+
+def _on_stream(stream, like, outputs, call):
+    """call() with ``stream`` (a torch stream or a raw handle) as torch's current one.
+
+    So the workspace and the results come from that stream's memory, and no
+    other stream gets the workspace's block while the kernels still use it.
+    The results (all but the caller's own ``outputs``) may be read on the stream
+    that was current, behind a wait, and dropped there.
+    """
+    import torch
+    if not like.is_cuda:
+        raise ValueError("stream needs CUDA tensors")
+    index = like.get_device()
+    before = torch.cuda.current_stream(index)
+    with torch.cuda.stream(_torch_stream(stream, index)):
+        results = call()
+    for t in results if isinstance(results, tuple) else (results,):
+        if t is not None and not any(t is o for o in outputs):
+            t.record_stream(before)
+    return results
+
+
 def mhla_forward(q, k, v, mc, grid, block, norm: str = "divisive", feature_map: str = "elu1",
                  variant: str = "auto", out=None, workspace=None, stream=None, causal: bool = False,
                  layout: str = "bhnd"):
@@ -266,6 +299,9 @@ def mhla_forward(q, k, v, mc, grid, block, norm: str = "divisive", feature_map: 
     (default: torch's current stream) and does not synchronise.
     """
     import torch
+    if stream is not None:
+        return _on_stream(stream, q, (out,), lambda: mhla_forward(
+            q, k, v, mc, grid, block, norm, feature_map, variant, out, workspace, None, causal, layout))
     p = _params_for(q, grid, block, feature_map, norm, variant, causal, layout)
     for name, t in (("q", q), ("k", k), ("v", v)):
         if not t.is_cuda or not t.is_contiguous() or t.shape != q.shape or t.dtype != q.dtype:
@@ -281,9 +317,7 @@ def mhla_forward(q, k, v, mc, grid, block, norm: str = "divisive", feature_map: 
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
     ws_bytes = workspace.numel() * workspace.element_size()
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    handle = torch.cuda.current_stream(q.device).cuda_stream
     status = load().mhla_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), mc.data_ptr(), ctypes.byref(p),
                                  out.data_ptr(), workspace.data_ptr(), ws_bytes, handle)
     _check(status, "mhla_forward")
@@ -309,6 +343,10 @@ def mhla_backward(q, k, v, mc, dout, grid, block, norm: str = "divisive", featur
     causal form (float32 CUDA cores).
     """
     import torch
+    if stream is not None:
+        return _on_stream(stream, q, (dq, dk, dv, dmc), lambda: mhla_backward(
+            q, k, v, mc, dout, grid, block, norm, feature_map, dq, dk, dv, dmc, workspace, None, variant, layout,
+            causal))
     p = _params_for(q, grid, block, feature_map, norm, variant, causal, layout)
     for name, t in (("q", q), ("k", k), ("v", v), ("dout", dout)):
         if not t.is_cuda or not t.is_contiguous() or t.shape != q.shape or t.dtype != q.dtype:
@@ -330,9 +368,7 @@ def mhla_backward(q, k, v, mc, dout, grid, block, norm: str = "divisive", featur
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
     ws_bytes = workspace.numel() * workspace.element_size()
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    handle = torch.cuda.current_stream(q.device).cuda_stream
     status = load().mhla_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), mc.data_ptr(), dout.data_ptr(),
                                   ctypes.byref(p), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dmc.data_ptr(),
                                   workspace.data_ptr(), ws_bytes, handle)
@@ -354,13 +390,14 @@ def mhla_forward_noalloc(q, k, v, mc, grid, block, norm: str = "divisive", featu
     cannot allocate at call time; ``out`` must be given by such callers (when
     it is None this wrapper allocates it with torch, for convenience)."""
     import torch
+    if stream is not None:
+        return _on_stream(stream, q, (out,), lambda: mhla_forward_noalloc(
+            q, k, v, mc, grid, block, norm, feature_map, variant, out, None, layout))
     p = _params_for(q, grid, block, feature_map, norm, variant, False, layout)
     p.mc_per_head = _mc_per_head(mc, p)
     if out is None:
         out = torch.empty_like(q)
-    if stream is None:
-        stream = torch.cuda.current_stream(q.device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    handle = torch.cuda.current_stream(q.device).cuda_stream
     status = load().mhla_forward_noalloc(q.data_ptr(), k.data_ptr(), v.data_ptr(), mc.data_ptr(), ctypes.byref(p),
                                          out.data_ptr(), handle)
     _check(status, "mhla_forward_noalloc")
@@ -377,6 +414,11 @@ def mhla_forward_host(q, k, v, mc, grid, block, norm: str = "divisive", feature_
     result back into ``out``; returns when ``out`` is complete.
     """
     import torch
+    if stream is not None:  # a new dev_buffer comes from that stream's memory
+        index = torch.cuda.current_device() if dev_buffer is None else dev_buffer.get_device()
+        with torch.cuda.stream(_torch_stream(stream, index)):
+            return mhla_forward_host(q, k, v, mc, grid, block, norm, feature_map, variant, out, dev_buffer, None, causal,
+                                     layout)
     p = _params_for(q, grid, block, feature_map, norm, variant, causal, layout)
     p.mc_per_head = _mc_per_head(mc, p)
     for name, t in (("q", q), ("k", k), ("v", v), ("mc", mc)):
@@ -387,9 +429,7 @@ def mhla_forward_host(q, k, v, mc, grid, block, norm: str = "divisive", feature_
     need = mhla_host_buffer_bytes(p)
     if dev_buffer is None:
         dev_buffer = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev_buffer.device)
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    handle = torch.cuda.current_stream(dev_buffer.device).cuda_stream
     status = load().mhla_forward_host(q.data_ptr(), k.data_ptr(), v.data_ptr(), mc.data_ptr(), ctypes.byref(p),
                                       out.data_ptr(), dev_buffer.data_ptr(),
                                       dev_buffer.numel() * dev_buffer.element_size(), handle)
@@ -546,31 +586,6 @@ def _set_output(field, name, t, like, shape, axes) -> None:
 def _current_stream(index) -> int:
     import torch
     return torch.cuda.current_stream(index).cuda_stream
-
-
-def _on_stream(stream, like, outputs, call):
-    """call() with ``stream`` (a torch stream or a raw handle) as torch's current one.
-
-    So the workspace and the results come from that stream's memory, and no
-    other stream gets the workspace's block while the kernels still use it.
-    The results (all but the caller's own ``outputs``) may be read on the stream
-    that was current, behind a wait, and dropped there.
-    """
-    import torch
-    if not like.is_cuda:
-        raise ValueError("stream needs CUDA tensors")
-    index = like.get_device()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), device=index)
-    elif stream.device.index != index:
-        raise ValueError(f"stream must be on {like.device}")
-    before = torch.cuda.current_stream(index)
-    with torch.cuda.stream(stream):
-        results = call()
-    for t in results if isinstance(results, tuple) else (results,):
-        if t is not None and not any(t is o for o in outputs):
-            t.record_stream(before)
-    return results
 
 
 class _Call:
