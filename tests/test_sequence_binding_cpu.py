@@ -145,6 +145,33 @@ def test_block_attention_memory_comes_from_the_stream_of_the_call(gpu, name, str
         assert not stream or t.recorded.cuda_stream == 0x4400
 
 
+def given_workspace(name, ws):
+    q, mc = card(1, 2, 64, 64), card(4, 4, dtype=torch.float32)
+    if name == "mhla_forward":
+        return mb.mhla_forward(q, q, q, mc, GRID, BLOCK, workspace=ws)
+    if name == "mhla_backward":
+        return mb.mhla_backward(q, q, q, mc, q, GRID, BLOCK, workspace=ws)
+    if name == "mhla_forward_host":
+        c = lambda t: t.as_subclass(torch.Tensor)  # noqa: E731
+        return mb.mhla_forward_host(c(q), c(q), c(q), c(mc), GRID, BLOCK, out=torch.zeros(1, 2, 64, 64), dev_buffer=ws)
+    return calls()[name](workspace=ws)
+
+
+@pytest.mark.parametrize("name", ["norm backward", "decay", "decay backward", "mhla_forward", "mhla_backward",
+                                  "mhla_forward_host"])
+def test_workspace_of_the_caller(gpu, name):
+    """The kernels write its first bytes: it has to be on the GPU and without gaps."""
+    ws = card(1 << 16, dtype=torch.uint8)
+    given_workspace(name, ws)
+    args = gpu.calls[-1].args
+    assert ws.data_ptr() in args and ws.numel() in args
+    for bad in (torch.zeros(1 << 16, dtype=torch.uint8), card(2, 1 << 16, dtype=torch.uint8)[:, ::2],
+                card(1, dtype=torch.uint8).expand(1 << 16)):
+        with pytest.raises(ValueError, match="contiguous CUDA tensor"):
+            given_workspace(name, bad)
+    assert len(gpu.calls) == 1
+
+
 def test_host_call_buffer_comes_from_the_stream_of_the_call(gpu, monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     q, mc = torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16), torch.zeros(4, 4)

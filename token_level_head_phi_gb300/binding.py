@@ -256,6 +256,13 @@ def _params_for(q, grid, block, feature_map, norm, variant, causal=False, layout
     return make_params(B, H, d, grid, block, _torch_dtype_name(q), feature_map, norm, variant, causal, layout)
 
 
+def _buffer_bytes(name, t, device) -> int:
+    """Bytes of a caller's scratch buffer, which the kernels write from its first element on."""
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
+    return t.numel() * t.element_size()
+
+
 def _torch_stream(stream, index):
     """A torch stream or a raw handle as a torch stream of device ``index``."""
     import torch
@@ -316,7 +323,7 @@ def mhla_forward(q, k, v, mc, grid, block, norm: str = "divisive", feature_map: 
     need = mhla_workspace_bytes(p)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = _buffer_bytes("workspace", workspace, q.device)
     handle = torch.cuda.current_stream(q.device).cuda_stream
     status = load().mhla_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), mc.data_ptr(), ctypes.byref(p),
                                  out.data_ptr(), workspace.data_ptr(), ws_bytes, handle)
@@ -367,7 +374,7 @@ def mhla_backward(q, k, v, mc, dout, grid, block, norm: str = "divisive", featur
     need = mhla_backward_workspace_bytes(p)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws_bytes = _buffer_bytes("workspace", workspace, q.device)
     handle = torch.cuda.current_stream(q.device).cuda_stream
     status = load().mhla_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), mc.data_ptr(), dout.data_ptr(),
                                   ctypes.byref(p), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dmc.data_ptr(),
@@ -429,10 +436,10 @@ def mhla_forward_host(q, k, v, mc, grid, block, norm: str = "divisive", feature_
     need = mhla_host_buffer_bytes(p)
     if dev_buffer is None:
         dev_buffer = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    buffer_bytes = _buffer_bytes("dev_buffer", dev_buffer, dev_buffer.device)
     handle = torch.cuda.current_stream(dev_buffer.device).cuda_stream
     status = load().mhla_forward_host(q.data_ptr(), k.data_ptr(), v.data_ptr(), mc.data_ptr(), ctypes.byref(p),
-                                      out.data_ptr(), dev_buffer.data_ptr(),
-                                      dev_buffer.numel() * dev_buffer.element_size(), handle)
+                                      out.data_ptr(), dev_buffer.data_ptr(), buffer_bytes, handle)
     _check(status, "mhla_forward_host")
     return out
 
@@ -607,7 +614,7 @@ class _Call:
     def workspace(self, given):
         """(tensor or None, bytes): the caller's workspace or a new one."""
         if given is not None:
-            return given, given.numel() * given.element_size()
+            return given, _buffer_bytes("workspace", given, self.device)
         if not self.need:
             return None, 0
         return self.empty(self.need, dtype=self.u8, device=self.device), self.need
