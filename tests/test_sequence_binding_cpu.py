@@ -41,7 +41,7 @@ class Gpu:
 
     def entry(self, name):
         def call(*args):
-            params = [a._obj for a in args if type(a).__name__ == "CArgObject"]
+            params = [type(a._obj).from_buffer_copy(a._obj) for a in args if type(a).__name__ == "CArgObject"]
             self.calls.append(types.SimpleNamespace(name=name, args=args, params=params[-1], stream=args[-1]))
             return 0
         return call
@@ -125,6 +125,20 @@ def test_own_results_are_left_alone(gpu):
     out, state = card(1, 2, 8, 64), card(1, 2, 64, 64, dtype=torch.float32)
     mb.mhla_decay_forward(q, q, q, g, out=out, state_out=state, stream=RAW)
     assert not hasattr(out, "recorded") and not hasattr(state, "recorded") and not gpu.allocated
+
+
+@pytest.mark.parametrize("name,field", [("norm", "eps"), ("decay", "scale"), ("decay backward", "scale"),
+                                        ("step", "scale")])
+def test_scalars_are_taken_by_value(gpu, name, field):
+    """A zero-dimensional tensor hashes by identity: its value may change between two calls."""
+    value = torch.tensor(0.5)
+    call = calls(**{field: value})[name]
+    call()
+    value.mul_(2)
+    call()
+    value.mul_(0.5)
+    call()
+    assert [getattr(c.params, field) for c in gpu.calls] == [0.5, 1.0, 0.5]
 
 
 GRID, BLOCK = (1, 8, 8), (1, 4, 4)

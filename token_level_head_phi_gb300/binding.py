@@ -505,7 +505,8 @@ def mhla_abi_version() -> int:
 #
 # A call's checks and its parameter block depend only on the arguments' shapes,
 # strides, dtypes and devices, so they are made once for each such set and kept
-# (a decoding loop calls with the same ones for every token).
+# (a decoding loop calls with the same ones for every token).  Scalars among
+# the arguments are taken by value before they become part of that key.
 #
 # Everything runs on torch's current stream, or on ``stream`` as it would under
 # ``torch.cuda.stream(stream)``: what a call allocates belongs to that stream.
@@ -790,6 +791,7 @@ def mhla_layernorm_forward(x, weight=None, bias=None, eps: float = 1e-5, out=Non
     if stream is not None:
         return _on_stream(stream, x, (out, mean, rstd), lambda: mhla_layernorm_forward(
             x, weight, bias, eps, out, mean, rstd))
+    eps = float(eps)
     key = ("norm", eps, _sig(x), _sig(weight), _sig(bias), _sig(out), _sig(mean), _sig(rstd))
     c = _CALLS.get(key) or _remember(key, _norm_forward_call(x, weight, bias, eps, out, mean, rstd))
     if out is None:
@@ -839,6 +841,7 @@ def mhla_layernorm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=Non
     if stream is not None:
         return _on_stream(stream, x, (dx, dweight, dbias), lambda: mhla_layernorm_backward(
             dy, x, mean, rstd, weight, dx, dweight, dbias, workspace, params=params))
+    params = bool(params)
     key = ("norm backward", params, _sig(dy), _sig(x), _sig(mean), _sig(rstd), _sig(weight), _sig(dx), _sig(dweight),
            _sig(dbias))
     c = _CALLS.get(key) or _remember(key, _norm_backward_call(dy, x, mean, rstd, weight, dx, dweight, dbias, params))
@@ -917,6 +920,7 @@ def mhla_decay_forward(q, k, v, log_decay, state=None, lengths=None, scale: floa
     if stream is not None:
         return _on_stream(stream, q, (out, state_out), lambda: mhla_decay_forward(
             q, k, v, log_decay, state, lengths, scale, layout, variant, out, state_out, workspace))
+    scale = float(scale)
     key = ("decay", scale, layout, variant, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(state), _sig(lengths),
            _sig(out), _sig(state_out))
     c = _CALLS.get(key) or _remember(key, _decay_forward_call(q, k, v, log_decay, state, lengths, scale, layout,
@@ -966,6 +970,7 @@ def mhla_decay_backward(q, k, v, log_decay, dout, state=None, dstate_out=None, l
     if stream is not None:
         return _on_stream(stream, q, (dq, dk, dv, dstate), lambda: mhla_decay_backward(
             q, k, v, log_decay, dout, state, dstate_out, lengths, scale, layout, variant, dq, dk, dv, dstate, workspace))
+    scale = float(scale)
     key = ("decay backward", scale, layout, variant, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(dout),
            _sig(state), _sig(dstate_out), _sig(lengths), _sig(dq), _sig(dk), _sig(dv), _sig(dstate))
     c = _CALLS.get(key) or _remember(key, _decay_backward_call(q, k, v, log_decay, dout, state, dstate_out, lengths,
@@ -1019,6 +1024,7 @@ def mhla_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, sta
     if stream is not None:
         return _on_stream(stream, q, (out,), lambda: mhla_decay_step(
             q, k, v, log_decay, state, scale, out, state_out))
+    scale = float(scale)
     key = ("decay step", scale, _sig(q), _sig(k), _sig(v), _sig(log_decay), _sig(state), _sig(out), _sig(state_out))
     c = _CALLS.get(key) or _remember(key, _decay_step_call(q, k, v, log_decay, state, scale, out, state_out))
     if out is None:
