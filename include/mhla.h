@@ -36,6 +36,8 @@
  *   - The stream argument is a cudaStream_t (NULL = legacy default stream).
  *     Work is enqueued asynchronously; no call synchronises the host unless
  *     its comment says so.
+ *   - Kernels launch on the current device, which has to be the pointers' and
+ *     the stream's.
  *   - Every argument is checked on the host before anything is enqueued.  An
  *     invalid argument returns an error status and enqueues nothing.  No
  *     kernel traps.  A kernel whose bounded wait on the device expires stops

@@ -37,7 +37,7 @@ class Gpu:
     """torch's streams and allocations, and the entries' calls."""
 
     def __init__(self):
-        self.now, self.allocated, self.calls = 0, [], []
+        self.now, self.device, self.allocated, self.calls = 0, 0, [], []
 
     def entry(self, name):
         def call(*args):
@@ -76,6 +76,8 @@ def gpu(monkeypatch):
     monkeypatch.setattr(torch.cuda, "ExternalStream",
                         lambda h, device=None: types.SimpleNamespace(cuda_stream=h))
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: g.now, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: g.device, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: g.device)
     return g
 
 
@@ -159,6 +161,22 @@ def test_block_attention_memory_comes_from_the_stream_of_the_call(gpu, name, str
         assert not stream or t.recorded.cuda_stream == 0x4400
 
 
+@pytest.mark.parametrize("name", NAMES + ["mhla_forward", "mhla_backward"])
+def test_tensors_of_another_device_than_the_current_one(gpu, name):
+    """The entries launch on the current device, where other devices' pointers would fault."""
+    if name.startswith("mhla"):
+        call = lambda: given_workspace(name, None)  # noqa: E731
+    else:
+        call = calls()[name]
+    call()  # also once the checks of these shapes are behind
+    gpu.device = 1
+    with pytest.raises(ValueError, match="current device"):
+        call()
+    gpu.device = 0
+    call()
+    assert len(gpu.calls) == 2
+
+
 def given_workspace(name, ws):
     q, mc = card(1, 2, 64, 64), card(4, 4, dtype=torch.float32)
     if name == "mhla_forward":
@@ -187,7 +205,6 @@ def test_workspace_of_the_caller(gpu, name):
 
 
 def test_host_call_buffer_comes_from_the_stream_of_the_call(gpu, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     q, mc = torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16), torch.zeros(4, 4)
     empty = torch.empty
     monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))

@@ -263,6 +263,20 @@ def _buffer_bytes(name, t, device) -> int:
     return t.numel() * t.element_size()
 
 
+def _not_current(index):
+    """The entries launch on the current device, whatever the pointers' device."""
+    return ValueError(f"the tensors are on cuda:{index}, which is not the current device")
+
+
+def _stream_handle(like) -> int:
+    """Handle of torch's current stream on the device of ``like``."""
+    import torch
+    index = like.get_device()
+    if torch.cuda.current_device() != index:
+        raise _not_current(index)
+    return torch.cuda.current_stream(index).cuda_stream
+
+
 def _torch_stream(stream, index):
     """A torch stream or a raw handle as a torch stream of device ``index``."""
     import torch
@@ -324,7 +338,7 @@ def mhla_forward(q, k, v, mc, grid, block, norm: str = "divisive", feature_map: 
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
     ws_bytes = _buffer_bytes("workspace", workspace, q.device)
-    handle = torch.cuda.current_stream(q.device).cuda_stream
+    handle = _stream_handle(q)
     status = load().mhla_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), mc.data_ptr(), ctypes.byref(p),
                                  out.data_ptr(), workspace.data_ptr(), ws_bytes, handle)
     _check(status, "mhla_forward")
@@ -375,7 +389,7 @@ def mhla_backward(q, k, v, mc, dout, grid, block, norm: str = "divisive", featur
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
     ws_bytes = _buffer_bytes("workspace", workspace, q.device)
-    handle = torch.cuda.current_stream(q.device).cuda_stream
+    handle = _stream_handle(q)
     status = load().mhla_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), mc.data_ptr(), dout.data_ptr(),
                                   ctypes.byref(p), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dmc.data_ptr(),
                                   workspace.data_ptr(), ws_bytes, handle)
@@ -404,7 +418,7 @@ def mhla_forward_noalloc(q, k, v, mc, grid, block, norm: str = "divisive", featu
     p.mc_per_head = _mc_per_head(mc, p)
     if out is None:
         out = torch.empty_like(q)
-    handle = torch.cuda.current_stream(q.device).cuda_stream
+    handle = _stream_handle(q)
     status = load().mhla_forward_noalloc(q.data_ptr(), k.data_ptr(), v.data_ptr(), mc.data_ptr(), ctypes.byref(p),
                                          out.data_ptr(), handle)
     _check(status, "mhla_forward_noalloc")
@@ -437,7 +451,7 @@ def mhla_forward_host(q, k, v, mc, grid, block, norm: str = "divisive", feature_
     if dev_buffer is None:
         dev_buffer = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
     buffer_bytes = _buffer_bytes("dev_buffer", dev_buffer, dev_buffer.device)
-    handle = torch.cuda.current_stream(dev_buffer.device).cuda_stream
+    handle = _stream_handle(dev_buffer)
     status = load().mhla_forward_host(q.data_ptr(), k.data_ptr(), v.data_ptr(), mc.data_ptr(), ctypes.byref(p),
                                       out.data_ptr(), dev_buffer.data_ptr(), buffer_bytes, handle)
     _check(status, "mhla_forward_host")
@@ -607,9 +621,12 @@ class _Call:
         self.empty, self.f32, self.u8 = torch.empty, torch.float32, torch.uint8
         # the current stream's handle without a Stream object (0.1 us against 1.1)
         self.current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or _current_stream
+        self.current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         self.__dict__.update(kw)
 
     def stream(self) -> int:
+        if self.current_device() != self.index:
+            raise _not_current(self.index)
         return self.current(self.index)
 
     def workspace(self, given):
