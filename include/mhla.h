@@ -410,8 +410,9 @@ mhla_status mhla_decay_forward(const void* q, const void* k, const void* v, cons
  * dstate_out NULL: zeros; dstate_in NULL: not wanted, or dstate_out (in
  * place).  Rows of dq, dk, dv past a sequence's length are written as zeros.
  * The passes of the three gradients run side by side on `stream` and two
- * streams of the calling thread, which `stream` has joined when the call
- * returns; a capture of `stream` takes them along. */
+ * streams that the calling thread keeps for it, which `stream` has joined when
+ * the call returns; a capture of `stream` takes them along.  A thread keeps
+ * them for 16 streams; on further ones the passes run one after another. */
 mhla_status mhla_decay_backward_workspace_bytes(const mhla_decay_params* p, size_t* bytes);
 mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, const float* log_decay,
                                 const int32_t* lengths, const float* state_in, const void* dout,

@@ -70,6 +70,70 @@ def test_results_may_be_dropped_on_the_current_stream():
         del got, x
 
 
+def test_gradients_on_one_stream_do_not_wait_for_another():
+    """A stream that is held up holds up none of the others, whichever share its hardware queue."""
+    problem = decay_backward(50)
+    want, held = problem(), torch.cuda.Stream()
+    others = [torch.cuda.Stream() for _ in range(6)]
+    for s in [held] + others:
+        problem(stream=s)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(held):
+        torch.cuda._sleep(2_000_000_000)  # about a second
+    first = problem(stream=held)
+    done = torch.cuda.Event()
+    done.record(held)
+    got, ends = [], []
+    for s in others:
+        got.append(problem(stream=s))
+        ends.append(torch.cuda.Event())
+        ends[-1].record(s)
+    early = False
+    while not early and not done.query():
+        early = any(e.query() for e in ends)
+        early = early and not done.query()
+    torch.cuda.synchronize()
+    assert early
+    for results in got + [first]:
+        for x, y in zip(results, want):
+            assert torch.equal(x, y)
+
+
+def test_gradients_on_more_streams_than_have_side_streams():
+    problem = decay_backward(60)
+    want = problem()
+    streams = [torch.cuda.Stream() for _ in range(24)]
+    assert len({s.cuda_stream for s in streams}) > 16
+    torch.cuda.synchronize()
+    for _ in range(2):
+        got = [problem(stream=s) for s in streams]
+        torch.cuda.synchronize()
+        for results in got:
+            for x, y in zip(results, want):
+                assert torch.equal(x, y)
+
+
+def test_gradients_captured_on_two_streams_in_turn():
+    problems = [decay_backward(70), decay_backward(80)]
+    want = [p() for p in problems]
+    streams = [torch.cuda.Stream() for _ in problems]
+    into = [tuple(torch.zeros_like(x) for x in w) for w in want]
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in problems]
+    for p, s, g, t in zip(problems, streams, graphs, into):
+        with torch.cuda.graph(g, stream=s):
+            p(dq=t[0], dk=t[1], dv=t[2], dstate=t[3])
+    for g in graphs:
+        g.replay()
+    for p, s, w in zip(problems, streams, want):  # the side streams are free again
+        for x, y in zip(p(stream=s), w):
+            torch.cuda.current_stream().wait_stream(s)
+            assert torch.equal(x, y)
+    for t, w in zip(into, want):
+        for x, y in zip(t, w):
+            assert torch.equal(x, y)
+
+
 def test_the_default_stream_by_handle():
     problem = norm_backward(40)
     want = problem()

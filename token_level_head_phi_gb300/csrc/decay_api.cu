@@ -2,7 +2,6 @@
 // include/mhla.h): checks, the segment plan and the passes of decay.h.
 #include <algorithm>
 #include <cmath>
-#include <map>
 
 #include "decay.h"
 #include "ops.h"
@@ -158,14 +157,18 @@ cudaError_t launch_pass(const DecayPass& a, const mhla_decay_params* p, cudaStre
   return launch_decay_mma(a, s);
 }
 
-// Side streams of the calling thread and the current device.  The passes of
-// the three gradients run side by side on them: alone, each of them leaves SMs
-// idle at its start and end and wherever its segments do not fill a wave (2 x
-// 8k tokens x 16 heads of 64: 134 us one after another, 111 side by side; 4 x
-// 2k tokens: 91 and 55; 3 x 777 tokens x 5 heads, float32: 93 and 66; 16 tokens
-// of one head: 27 and 14).  A capture of the caller's stream
-// takes the side streams along, as branches of its graph.
+// Two side streams of one caller's stream, in the calling thread and on the
+// current device.  The passes of the three gradients run side by side on them:
+// alone, each of them leaves SMs idle at its start and end and wherever its
+// segments do not fill a wave (2 x 8k tokens x 16 heads of 64: 134 us one after
+// another, 111 side by side; 4 x 2k tokens: 91 and 55; 3 x 777 tokens x 5 heads,
+// float32: 93 and 66; 16 tokens of one head: 27 and 14).  A capture of the
+// caller's stream takes the side streams along, as branches of its graph.  Side
+// streams that several callers' streams shared would order those streams' work
+// behind one another; a thread keeps pairs for its first kPairs streams, and on
+// further ones the passes run one after another.
 constexpr int kGradients = 3;
+constexpr int kPairs = 16;
 
 class Branches {
  public:
@@ -176,10 +179,13 @@ class Branches {
     }
     if (ready_) cudaEventDestroy(ready_);
   }
+  bool serves(int device, cudaStream_t s) const { return made_ && device_ == device && caller_ == s; }
   // Whether the side streams can follow s: they exist and are in no capture
   // but that of s.
-  bool open(cudaStream_t s) {
-    if (!made_) made_ = make() ? 1 : -1;
+  bool open(int device, cudaStream_t s) {
+    if (!made_) made_ = make(s) ? 1 : -1;
+    device_ = device;
+    caller_ = s;
     used_ = 0;
     unsigned long long id[3] = {};
     bool same = made_ == 1 && capture(s, &id[2]);
@@ -216,23 +222,36 @@ class Branches {
     if (status == cudaStreamCaptureStatusNone) *id = 0;
     return true;
   }
-  bool make() {
+  bool make(cudaStream_t s) {
+    // nothing here is part of a capture that may be under way
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool relaxed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
+    int priority = 0;
+    if (cudaStreamGetPriority(s, &priority) != cudaSuccess) priority = 0;
     bool ok = cudaEventCreateWithFlags(&ready_, cudaEventDisableTiming) == cudaSuccess;
     for (int i = 0; i < 2; ++i)
-      ok = ok && cudaStreamCreateWithFlags(&stream_[i], cudaStreamNonBlocking) == cudaSuccess &&
+      ok = ok && cudaStreamCreateWithPriority(&stream_[i], cudaStreamNonBlocking, priority) == cudaSuccess &&
            cudaEventCreateWithFlags(&done_[i], cudaEventDisableTiming) == cudaSuccess;
+    if (relaxed) cudaThreadExchangeStreamCaptureMode(&mode);
     return ok;
   }
-  int made_ = 0, used_ = 0;
+  int made_ = 0, used_ = 0, device_ = 0;
+  cudaStream_t caller_ = nullptr;
   cudaStream_t stream_[2] = {};
   cudaEvent_t ready_ = nullptr, done_[2] = {};
 };
 
-Branches& branches() {
-  thread_local std::map<int, Branches> of_device;
+// The side streams of s, ready to follow it, or null.
+Branches* branches(cudaStream_t s) {
+  thread_local Branches pairs[kPairs];
+  thread_local int used = 0;
   int device = 0;
-  cudaGetDevice(&device);
-  return of_device[device];
+  if (cudaGetDevice(&device) != cudaSuccess) return nullptr;
+  int i = 0;
+  while (i < used && !pairs[i].serves(device, s)) ++i;
+  if (i == kPairs) return nullptr;
+  if (i == used) ++used;
+  return pairs[i].open(device, s) ? &pairs[i] : nullptr;
 }
 
 // Whether `out` shares memory with none of `in`.
@@ -385,18 +404,17 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
   b.s_ldz = dval;
   b.launches = 2;
   c.launches = 1;
-  Branches& side = branches();
-  const bool apart = side.open(s);
-  const cudaStream_t sa = apart ? side.fork(0, s) : s;
+  Branches* side = branches(s);
+  const cudaStream_t sa = side ? side->fork(0, s) : s;
   cudaError_t e = launch_pass(a, p, sa);
   if (e == cudaSuccess) e = launch_pass(c, p, s);
   // with one segment dk reads dstate_out while dv's pass writes dstate_in
-  const cudaStream_t sb = apart && (c.nseg > 1 || !dstate_in || dstate_in != dstate_out) ? side.fork(1, s) : s;
+  const cudaStream_t sb = side && (c.nseg > 1 || !dstate_in || dstate_in != dstate_out) ? side->fork(1, s) : s;
   if (e == cudaSuccess) e = launch_pass(b, p, sb);
   c.launches = 2;
   if (e == cudaSuccess) e = launch_pass(c, p, s);
-  if (apart) {
-    const cudaError_t j = side.join(s);
+  if (side) {
+    const cudaError_t j = side->join(s);
     if (e == cudaSuccess) e = j;
   }
   return scratch.give_back(e == cudaSuccess ? MHLA_OK : record_cuda_error(e));
