@@ -84,6 +84,14 @@ __device__ __forceinline__ int decay_token(const DecayPass& p, int i, int length
 }
 #endif
 
+// Resident CTAs of an SM of the CUDA-core kernel's pass: one where its tiles
+// take 131 KB of shared memory; three with short rows and 64-column slices (64
+// registers a thread); two elsewhere (up to 128 registers, or more than a third
+// of the shared memory).
+constexpr int decay_simt_resident(int dx, int slice) {
+  return dx == 128 && slice == 64 ? 1 : dx <= 32 && slice == 64 ? 3 : 2;
+}
+
 // Launches return a cudaError_t.
 cudaError_t launch_decay_scan(const DecayPass& p, cudaStream_t s);
 cudaError_t launch_decay_simt(const DecayPass& p, int dtype, cudaStream_t s);

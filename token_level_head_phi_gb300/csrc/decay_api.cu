@@ -43,7 +43,9 @@ bool big_tiles(int dx, int dz) { return dx >= 64 && dz % 64 == 0; }
 // cores) and at most 64.  (32k tokens x 64 heads of 64: 19 segments 287 us, 9 to
 // 16 306 to 336, 4 371; of 128: 14 617, 4 695, 1 713; backward on 3 x 200 tokens
 // x 5 heads of 64: 1 14, 2 24; CUDA cores, 777 tokens x 15 heads of 64: 13
-// segments 37 us, 7 48; 400 tokens x 8 heads: 29 with 64-token segments, 44.)
+// segments 37 us, 7 48; 400 tokens x 8 heads: 29 with 64-token segments, 44; rows
+// of 128, where one CTA fits an SM: 60 heads of 2k tokens 581 us in one segment,
+// 714 in five, as for two CTAs.)
 //
 // The tcgen05 kernel for 128-entry rows also has a choice of slice: 64 columns
 // take 0.8 of the time of 128, and where that fills the SMs with one segment,
@@ -52,7 +54,9 @@ bool big_tiles(int dx, int dz) { return dx >= 64 && dz % 64 == 0; }
 //
 // `passes` run side by side (the gradients) and share the SMs: 2 x 8k tokens x
 // 16 heads of 64, 3 segments 111 us, 8 as for one pass 113; 4 x 2k tokens, one
-// segment 55, 4 as for one pass 72.
+// segment 55, 4 as for one pass 72.  On the CUDA cores: 2 x 500 tokens x 4 heads
+// of 128, counted as two CTAs an SM 100 us, as one 148; 2 x 2k x 16 heads of 64 / 32,
+// as three 178, as two 264.
 constexpr int kSegMost = 64, kSegStart = 100, kSegLaunches = 250;
 constexpr double kNarrow = 0.8, kStates = 0.5, kStatesWide = 0.9;
 
@@ -66,8 +70,13 @@ Plan plan_segments(const mhla_decay_params* p, int dx, int dz, int passes) {
   const bool wide = tc && dx == 128;
   const int widest = std::min(dz, wide ? 128 : mma && dx == 128 ? 32 : 64);
   const int narrowest = wide ? 64 : widest;
-  // resident CTAs of an SM: by shared memory; the float32 kernel's with small states are smaller
-  const int resident = wide ? 1 : mma || (!tc && dx * widest <= 2048) ? 3 : 2;
+  // CTAs of an SM.  Three passes on the CUDA cores never run all at once (the
+  // states come first), and counting more of them than fit is ahead.
+  const int resident = wide          ? 1
+                       : tc          ? 2
+                       : mma         ? 3
+                       : passes == 1 ? decay_simt_resident(dx, widest)
+                                     : (dx * widest <= 2048 ? 3 : 2);
   const int64_t slots = resident * kOpsSms, state_slots = (wide ? 2 : resident) * kOpsSms;
   const int quantum = on_tensor_cores(p) ? 128 : 64;  // a chunk, or the larger of two kernels' chunks
   const int tokens = std::max(1, (p->tokens + quantum - 1) / quantum) * quantum;

