@@ -299,8 +299,9 @@ typedef enum mhla_rotary_scaling {
 #define MHLA_ROTARY_MAX_PAIRS 128
 
 /* Host-side table of a rotation: turns[i] = f_i / 2 pi as a fraction of a
- * turn times 2^64, so that position * turns[i] modulo 2^64 is the exact phase
- * of that frequency at any position. */
+ * turn times 2^64; position * turns[i] modulo 2^64 is the phase.  The entries
+ * come of doubles: for f_i <= 1 the phase is off by less than |position| 2^-51
+ * turns (2^-53 without a scaling). */
 typedef struct mhla_rotary_table {
   int pairs;        /* rot_dim / 2, 1 .. MHLA_ROTARY_MAX_PAIRS */
   float amplitude;  /* m */
@@ -331,8 +332,9 @@ typedef struct mhla_rotary_params {
 /* Rotates q [batch, heads, tokens, head_dim] and, unless it is NULL, k
  * [batch, kv_heads, tokens, head_dim] in one launch.  positions: device int32
  * or int64 [batch, tokens] (any sign), or NULL.  Arithmetic in float32, the
- * angle exact as above.  q_out may be q and k_out may be k (same strides);
- * any other overlap is refused.  *table is read before the call returns. */
+ * phase as above, rounded to float32 within its turn (2^-26 turns).  q_out may
+ * be q and k_out may be k (same strides); any other overlap is refused.  *table
+ * is read before the call returns. */
 mhla_status mhla_rotary(const void* q, const void* k, const void* positions, const mhla_rotary_table* table,
                         const mhla_rotary_params* p, void* q_out, void* k_out, void* stream);
 

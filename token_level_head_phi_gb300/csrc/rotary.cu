@@ -2,11 +2,13 @@
 // m (a cos x - b sin x, a sin x + b cos x) with x = position * f_i ("RoFormer:
 // Enhanced Transformer with Rotary Position Embedding", section 3.2.2).
 //
-// The angle is formed without a rounding that grows with the position: f_i is
-// kept as a 64-bit fraction of a turn, so position * f_i modulo 2^64 is the
-// phase exactly (integer wrap-around drops whole turns), and its top 32 bits
-// feed sincospif.  The phase is off by at most position * 2^-65 turns, where
-// a float32 angle at position 2^20 is off by up to 0.03 radians.
+// f_i is kept as a 64-bit fraction of a turn, so that position * f_i modulo 2^64
+// takes the phase of that fraction without a rounding (integer wrap-around
+// drops whole turns), and its top 32 bits feed sincospif.  The fraction comes
+// of doubles: it is off by less than 2^-51 of a turn for f_i <= 1 (2^-53 without
+// a scaling), so the phase by less than position * 2^-51 turns, and by another
+// 2^-26 from its float32 value.  At position 2^20 that is 1e-7 radians, where a
+// float32 angle is off by up to 0.03.
 //
 // Bound: memory.  A thread takes one vector of pairs of one token, forms its
 // sines once and walks over the heads of q and k with four heads' loads in
