@@ -379,7 +379,18 @@ mhla_status mhla_layernorm_backward(const void* dy, const void* x, const void* w
  * stands in for the normaliser.  log_decay is a constant of the head (it has
  * no gradient): usually <= 0, -inf keeps only the token itself, > 0 grows.
  * Causality holds for finite values; a NaN or infinity in k or v may reach
- * the outputs of earlier tokens of its 128-token chunk. */
+ * the outputs of earlier tokens of its 128-token chunk.
+ *
+ * Roundings: float32 sums throughout; a bf16 result is rounded once.  On the
+ * tensor cores the decayed scores and the copy of the carried state that
+ * multiplies x are operands in bf16: each adds up to 2^-8 of the magnitudes it
+ * multiplies (|scores| |v|, |q| |S|) to the outputs' and gradients' error.  Calls
+ * of fewer than 128 tokens keep 16 bits of both (2^-16).  `tokens` counts here,
+ * not `lengths`: the outputs of a short sequence, on a large state that cancels
+ * in S^T q above all, are rounded more coarsely in a batch that is padded to
+ * 128 tokens or more.  MHLA_DECAY_SIMT and mhla_decay_step round the result
+ * only, at every length.  Final states keep the accuracy of float32 sums in
+ * every variant. */
 typedef enum mhla_decay_variant {
   MHLA_DECAY_AUTO = 0,   /* tensor cores for bf16, CUDA cores for float32        */
   MHLA_DECAY_SIMT = 1,   /* float32 arithmetic on the CUDA cores, both dtypes    */

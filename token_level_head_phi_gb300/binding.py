@@ -933,6 +933,9 @@ def mhla_decay_forward(q, k, v, log_decay, state=None, lengths=None, scale: floa
     float32 [H].  ``state``: float32 [B, H, dk, dv] to start from (None:
     zeros); ``state_out is state`` updates it in place.  ``lengths``: int32
     [B] for sequences padded to N; rows past a length come out as zeros.
+    bfloat16 runs on the tensor cores with operands rounded to bfloat16 from
+    N = 128 on, padding included (see mhla.h); ``variant="simt"`` rounds the
+    results only.
     """
     if stream is not None:
         return _on_stream(stream, q, (out, state_out), lambda: mhla_decay_forward(

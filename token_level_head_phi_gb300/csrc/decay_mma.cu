@@ -471,7 +471,10 @@ cudaError_t run(const DecayPass& p, cudaStream_t s) {
   if (!(p.launches & 2)) return cudaSuccess;
   // Two roundings as large as the output's own make its error 1.4 times one
   // rounding, on average; over the few outputs of a short prompt the average
-  // says little, and the 16-bit operands cost nothing that shows there.
+  // says little, and the 16-bit operands cost nothing that shows there.  The
+  // tokens of the call decide, padding included: a sequence's own length is on
+  // the device, and the tcgen05 kernels have no room for the low parts (shared
+  // memory holds two CTAs an SM to the last KB, tensor memory is full).
   if (p.N < 128) return launch<DX, DZS, true, true>(p, p.nseg, p.nseg > 1, s);
   return launch<DX, DZS, true, false>(p, p.nseg, p.nseg > 1, s);
 }
