@@ -473,8 +473,8 @@ cudaError_t run(const DecayPass& p, cudaStream_t s) {
   // rounding, on average; over the few outputs of a short prompt the average
   // says little, and the 16-bit operands cost nothing that shows there.  The
   // tokens of the call decide, padding included: a sequence's own length is on
-  // the device, and the tcgen05 kernels have no room for the low parts (shared
-  // memory holds two CTAs an SM to the last KB, tensor memory is full).
+  // the device, and the tcgen05 kernels, as laid out, have no place for the low
+  // parts (tensor memory is full; the 128-entry rows fill shared memory too).
   if (p.N < 128) return launch<DX, DZS, true, true>(p, p.nseg, p.nseg > 1, s);
   return launch<DX, DZS, true, false>(p, p.nseg, p.nseg > 1, s);
 }
