@@ -263,7 +263,9 @@ mhla_status mhla_backward(const void* q, const void* k, const void* v, const flo
 /* ------------------------------------------------------------------------
  * Operators of a sequence model's layer around the attention: linear
  * attention with a decay for each head (prompts, single tokens, backward),
- * rotary positions and layer norm.  The conventions at the top of this file
+ * rotary positions, layer norm, the norm of queries and keys with their
+ * rotation, and a recurrent layer's gated recurrence and short convolution
+ * (prompts, single tokens, backward).  The conventions at the top of this file
  * hold (device pointers, host-side checks before anything is enqueued,
  * asynchronous on `stream`), except that tensors carry element strides
  * instead of being contiguous and pointers need the alignment of their
@@ -438,6 +440,153 @@ mhla_status mhla_decay_backward(const void* q, const void* k, const void* v, con
 mhla_status mhla_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
                             const float* state_in, const mhla_decay_params* p, void* out, float* state_out,
                             void* stream);
+
+/* Norm of queries and keys over each head and their rotary positions in one
+ * pass: with rstd = 1 / sqrt(mean(x^2) + eps) over a row,
+ *   y = R(position) (x rstd * weight),
+ * R the map of mhla_rotary (its styles, tables and positions).  Squares and
+ * sums in float32: rows whose squares leave its range (entries beyond 1e19)
+ * come out as zeros, as their rstd is 0. */
+typedef struct mhla_qknorm_params {
+  int batch, tokens;         /* >= 0                                                     */
+  int heads, kv_heads;       /* >= 0, <= 32768: heads of q and of k                      */
+  int head_dim;              /* >= rot_dim of the table, 1 .. 256; even for INTERLEAVED  */
+  int dtype;                 /* mhla_dtype of q, k, their gradients and the results      */
+  int weight_dtype;          /* mhla_dtype of q_weight and k_weight                      */
+  int style;                 /* mhla_rotary_style                                        */
+  int position_dtype;        /* mhla_position_dtype of `positions`                       */
+  float eps;                 /* >= 0, finite                                             */
+  int64_t position_offset;   /* position of token t where positions is NULL: offset + t  */
+  int64_t position_batch_stride, position_token_stride; /* of `positions`, in elements   */
+  mhla_strides q, k;
+  mhla_strides q_out, k_out; /* forward: results; backward: dq, dk                       */
+  mhla_strides dq_out, dk_out; /* backward only: the gradients of the results            */
+} mhla_qknorm_params;
+
+/* q_weight, k_weight: device [head_dim], the same for every head, or NULL
+ * (1).  table NULL: no rotation.  k may be NULL.  q_out may be q and k_out may
+ * be k (same strides); any other overlap is refused. */
+mhla_status mhla_qknorm_forward(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                                const void* positions, const mhla_rotary_table* table, const mhla_qknorm_params* p,
+                                void* q_out, void* k_out, void* stream);
+
+/* Gradients from those of the results: with t = R^T dy and g = weight t,
+ *   dx = rstd (g - xh mean(g xh)),  dweight = sum t xh,  xh = x rstd;
+ * nothing is kept from the forward call.  dq_weight, dk_weight: float32
+ * [head_dim], overwritten (zeros for no rows), or NULL (not wanted); their
+ * sums run in a fixed order.  dq may be dq_out or q, dk may be dk_out or k
+ * (same strides).  workspace as for mhla_layernorm_backward. */
+mhla_status mhla_qknorm_backward_workspace_bytes(const mhla_qknorm_params* p, size_t* bytes);
+mhla_status mhla_qknorm_backward(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                                 const void* q_weight, const void* k_weight, const void* positions,
+                                 const mhla_rotary_table* table, const mhla_qknorm_params* p, void* dq, void* dk,
+                                 float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* Linear recurrence with gates of each token and channel:
+ *   h_t = a_t h_{t-1} + c_t u_t,   u_t = x_t sigma(input_gate_t)
+ * for t = 0 .. length - 1, h_{-1} = state_in (zeros where it is NULL), out_t =
+ * h_t and state_out = h_{length-1}; sigma is the logistic function, u_t = x_t
+ * without an input gate.  States are float32 [batch, width], contiguous.
+ * DECAY: a = exp(log_decay sigma(gate)) with log_decay float32 [width], finite
+ * and <= 0; SIGMOID: a = sigma(gate), without log_decay.
+ * NORM: c = sqrt(max(1 - a^2, 0)) (inputs and states of one size), MEAN:
+ * c = 1 - a (a running mean), NONE: c = 1.
+ * All arithmetic in float32, a result is rounded once. */
+typedef enum mhla_gated_kind { MHLA_GATED_DECAY = 0, MHLA_GATED_SIGMOID = 1 } mhla_gated_kind;
+typedef enum mhla_gated_scale {
+  MHLA_GATED_SCALE_NORM = 0,
+  MHLA_GATED_SCALE_MEAN = 1,
+  MHLA_GATED_SCALE_NONE = 2
+} mhla_gated_scale;
+
+#define MHLA_GATED_MARK 64 /* tokens between two marks */
+
+typedef struct mhla_gated_params {
+  int batch, tokens, width;  /* >= 0                                                     */
+  int dtype;                 /* mhla_dtype of x, the gates, out and their gradients      */
+  int kind;                  /* mhla_gated_kind                                          */
+  int scale;                 /* mhla_gated_scale                                         */
+  int marks;                 /* backward: 1 where the call is given marks, else 0        */
+  /* of tensors [batch, tokens, width]; `head` is not used */
+  mhla_strides x, gate, input_gate, out;          /* out: forward and step only          */
+  mhla_strides dout, dx, dgate, dinput_gate;      /* backward only                       */
+} mhla_gated_params;
+
+/* Prompts.  lengths as for mhla_decay_forward: rows of out past a length are
+ * written as zeros, their inputs are not used.  state_out may be NULL (not
+ * wanted) or state_in (updated in place).  marks: float32 [batch,
+ * ceil(tokens / MHLA_GATED_MARK), width] or NULL; entry j receives the state
+ * before token MHLA_GATED_MARK j (the final one past a length), which the
+ * backward call takes.  No other result may share memory with an input. */
+mhla_status mhla_gated_forward(const void* x, const void* gate, const void* input_gate, const float* log_decay,
+                               const int32_t* lengths, const float* state_in, const mhla_gated_params* p, void* out,
+                               float* state_out, float* marks, void* stream);
+
+/* Gradients of L = sum(dout * out) + sum(dstate_out * state_out) with respect
+ * to x, the gates, log_decay and state_in.  marks: those of the forward call
+ * with the same inputs; with NULL (and p->marks 0) the call forms them first,
+ * from state_in, which is not read otherwise.  dinput_gate goes with
+ * input_gate; dlog_decay float32 [width] (DECAY only) may be NULL, its sums run
+ * in a fixed order; dstate_in may be NULL or dstate_out; dstate_out NULL: zeros.
+ * Where c = 0 its derivative is taken as 0.  Rows past a length are written as
+ * zeros.  workspace as for mhla_layernorm_backward. */
+mhla_status mhla_gated_backward_workspace_bytes(const mhla_gated_params* p, size_t* bytes);
+mhla_status mhla_gated_backward(const void* x, const void* gate, const void* input_gate, const float* log_decay,
+                                const int32_t* lengths, const float* state_in, const float* marks, const void* dout,
+                                const float* dstate_out, const mhla_gated_params* p, void* dx, void* dgate,
+                                void* dinput_gate, float* dlog_decay, float* dstate_in, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* One token of every sequence (tokens == 1).  state_out may be state_in. */
+mhla_status mhla_gated_step(const void* x, const void* gate, const void* input_gate, const float* log_decay,
+                            const float* state_in, const mhla_gated_params* p, void* out, float* state_out,
+                            void* stream);
+
+/* Short causal convolution of each channel:
+ *   y_t = f(sum_j weight[d][j] x_{t - taps + 1 + j} + bias[d]),  f(z) = z or
+ *   z sigma(z) (SILU),
+ * where the rows before the first token come from state_in (zeros where it is
+ * NULL).  A state holds the last taps - 1 rows of x: [batch, taps - 1, width] of
+ * x's dtype, contiguous, so it is exact.  Sums in float32, a result is rounded
+ * once. */
+typedef enum mhla_activation { MHLA_ACTIVATION_NONE = 0, MHLA_ACTIVATION_SILU = 1 } mhla_activation;
+
+typedef struct mhla_shortconv_params {
+  int batch, tokens, width;  /* >= 0                                                     */
+  int taps;                  /* 2 .. 4                                                   */
+  int dtype;                 /* mhla_dtype of x, out, the states and their gradients     */
+  int weight_dtype;          /* mhla_dtype of weight and bias                            */
+  int activation;            /* mhla_activation                                          */
+  /* of tensors [batch, tokens, width]; `head` is not used */
+  mhla_strides x, out;       /* out: forward and step only                               */
+  mhla_strides dout, dx;     /* backward only                                            */
+} mhla_shortconv_params;
+
+/* Prompts.  weight: device [width, taps]; bias: device [width] or NULL.
+ * lengths as for mhla_decay_forward: rows of out past a length are written as
+ * zeros; state_out, NULL (not wanted) or state_in (in place), receives the last
+ * taps - 1 rows before the length. */
+mhla_status mhla_shortconv_forward(const void* x, const void* weight, const void* bias, const int32_t* lengths,
+                                   const void* state_in, const mhla_shortconv_params* p, void* out, void* state_out,
+                                   void* stream);
+
+/* Gradients of L = sum(dout * out) + sum(dstate_out * state_out); nothing is
+ * kept from the forward call.  dweight float32 [width, taps] and dbias float32
+ * [width] (without a bias too), overwritten, or NULL; their sums run in a
+ * fixed order.  dstate_in may be NULL, dstate_out NULL: zeros.  No result may
+ * share memory with an input.  Rows of dx past a length are written as zeros.
+ * workspace as for mhla_layernorm_backward. */
+mhla_status mhla_shortconv_backward_workspace_bytes(const mhla_shortconv_params* p, size_t* bytes);
+mhla_status mhla_shortconv_backward(const void* x, const void* weight, const void* bias, const int32_t* lengths,
+                                    const void* state_in, const void* dout, const void* dstate_out,
+                                    const mhla_shortconv_params* p, void* dx, float* dweight, float* dbias,
+                                    void* dstate_in, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token of every sequence (tokens == 1): the state, given and moved on by
+ * one row into state_out, which may be state_in. */
+mhla_status mhla_shortconv_step(const void* x, const void* weight, const void* bias, const void* state_in,
+                                const mhla_shortconv_params* p, void* out, void* state_out, void* stream);
 
 /* Reads and clears the device error word of the current device.  Blocks the
  * host until the device is idle.  *code receives MHLA_OK or the first status

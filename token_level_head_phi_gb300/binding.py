@@ -52,6 +52,10 @@ ROTARY_STYLES = {"half": 0, "interleaved": 1}
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 ROTARY_MAX_PAIRS = 128
 DECAY_VARIANTS = {"auto": 0, "simt": 1, "tensor": 2}
+GATED_DECAY, GATED_SIGMOID = 0, 1
+GATED_SCALES = {"norm": 0, "mean": 1, "none": 2}
+GATED_MARK = 64
+ACTIVATIONS = {"none": 0, "silu": 1}
 
 
 class MhlaError(RuntimeError):
@@ -116,6 +120,34 @@ class MhlaDecayParams(ctypes.Structure):
     ]
 
 
+class MhlaQknormParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("style", ctypes.c_int),
+        ("position_dtype", ctypes.c_int), ("eps", ctypes.c_float), ("position_offset", ctypes.c_int64),
+        ("position_batch_stride", ctypes.c_int64), ("position_token_stride", ctypes.c_int64),
+        ("q", MhlaStrides), ("k", MhlaStrides), ("q_out", MhlaStrides), ("k_out", MhlaStrides),
+        ("dq_out", MhlaStrides), ("dk_out", MhlaStrides),
+    ]
+
+
+class MhlaGatedParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("width", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("kind", ctypes.c_int), ("scale", ctypes.c_int), ("marks", ctypes.c_int),
+        ("x", MhlaStrides), ("gate", MhlaStrides), ("input_gate", MhlaStrides), ("out", MhlaStrides),
+        ("dout", MhlaStrides), ("dx", MhlaStrides), ("dgate", MhlaStrides), ("dinput_gate", MhlaStrides),
+    ]
+
+
+class MhlaShortconvParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("width", ctypes.c_int), ("taps", ctypes.c_int),
+        ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("activation", ctypes.c_int),
+        ("x", MhlaStrides), ("out", MhlaStrides), ("dout", MhlaStrides), ("dx", MhlaStrides),
+    ]
+
+
 _LIB = None
 _P = ctypes.c_void_p
 
@@ -158,6 +190,25 @@ SIGNATURES = [
     ("mhla_decay_backward", ctypes.c_int, [_P] * 8 + [ctypes.POINTER(MhlaDecayParams)] + [_P] * 5
      + [ctypes.c_size_t, _P]),
     ("mhla_decay_step", ctypes.c_int, [_P] * 5 + [ctypes.POINTER(MhlaDecayParams), _P, _P, _P]),
+    ("mhla_qknorm_forward", ctypes.c_int, [_P] * 5 + [ctypes.POINTER(MhlaRotaryTable), ctypes.POINTER(MhlaQknormParams),
+                                                      _P, _P, _P]),
+    ("mhla_qknorm_backward_workspace_bytes", ctypes.c_int, [ctypes.POINTER(MhlaQknormParams),
+                                                            ctypes.POINTER(ctypes.c_size_t)]),
+    ("mhla_qknorm_backward", ctypes.c_int, [_P] * 7 + [ctypes.POINTER(MhlaRotaryTable),
+                                                       ctypes.POINTER(MhlaQknormParams)] + [_P] * 5
+     + [ctypes.c_size_t, _P]),
+    ("mhla_gated_forward", ctypes.c_int, [_P] * 6 + [ctypes.POINTER(MhlaGatedParams), _P, _P, _P, _P]),
+    ("mhla_gated_backward_workspace_bytes", ctypes.c_int, [ctypes.POINTER(MhlaGatedParams),
+                                                           ctypes.POINTER(ctypes.c_size_t)]),
+    ("mhla_gated_backward", ctypes.c_int, [_P] * 9 + [ctypes.POINTER(MhlaGatedParams)] + [_P] * 6
+     + [ctypes.c_size_t, _P]),
+    ("mhla_gated_step", ctypes.c_int, [_P] * 5 + [ctypes.POINTER(MhlaGatedParams), _P, _P, _P]),
+    ("mhla_shortconv_forward", ctypes.c_int, [_P] * 5 + [ctypes.POINTER(MhlaShortconvParams), _P, _P, _P]),
+    ("mhla_shortconv_backward_workspace_bytes", ctypes.c_int, [ctypes.POINTER(MhlaShortconvParams),
+                                                               ctypes.POINTER(ctypes.c_size_t)]),
+    ("mhla_shortconv_backward", ctypes.c_int, [_P] * 7 + [ctypes.POINTER(MhlaShortconvParams)] + [_P] * 5
+     + [ctypes.c_size_t, _P]),
+    ("mhla_shortconv_step", ctypes.c_int, [_P] * 4 + [ctypes.POINTER(MhlaShortconvParams), _P, _P, _P]),
 ]
 
 
@@ -672,8 +723,25 @@ def mhla_rotary_plan(rot_dim: int, base: float = 10000.0, scaling: str = "none",
     return RotaryPlan(int(rot_dim), table)
 
 
-def _rotary_call(q, k, positions, style, layout, q_out, k_out, transpose):
+def _set_positions(p, positions, q) -> None:
+    """Strides and dtype of positions [N], [1, N] or [B, N] (None: not given)."""
     import torch
+    if positions is not None:
+        if positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
+        if not positions.is_cuda or positions.device != q.device:
+            raise ValueError(f"positions must be on {q.device}")
+        if positions.dim() == 1 and positions.shape[0] == p.tokens:
+            p.position_token_stride = positions.stride(0)
+        elif positions.dim() == 2 and tuple(positions.shape) in ((p.batch, p.tokens), (1, p.tokens)):
+            p.position_batch_stride = positions.stride(0) if positions.shape[0] > 1 else 0
+            p.position_token_stride = positions.stride(1)
+        else:
+            raise ValueError(f"positions must be [N] or [B, N], got {tuple(positions.shape)}")
+        p.position_dtype = 1 if positions.dtype == torch.int64 else 0
+
+
+def _rotary_call(q, k, positions, style, layout, q_out, k_out, transpose):
     axes = _axes(layout)
     p = MhlaRotaryParams()
     p.style, p.transpose = _choice("style", style, ROTARY_STYLES), transpose
@@ -694,19 +762,7 @@ def _rotary_call(q, k, positions, style, layout, q_out, k_out, transpose):
         _set_output(p.k_out, "k_out", k_out, q, k.shape, axes)
     elif k_out is not None:
         raise ValueError("k_out needs k")
-    if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64):
-            raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-        if not positions.is_cuda or positions.device != q.device:
-            raise ValueError(f"positions must be on {q.device}")
-        if positions.dim() == 1 and positions.shape[0] == p.tokens:
-            p.position_token_stride = positions.stride(0)
-        elif positions.dim() == 2 and tuple(positions.shape) in ((p.batch, p.tokens), (1, p.tokens)):
-            p.position_batch_stride = positions.stride(0) if positions.shape[0] > 1 else 0
-            p.position_token_stride = positions.stride(1)
-        else:
-            raise ValueError(f"positions must be [N] or [B, N], got {tuple(positions.shape)}")
-        p.position_dtype = 1 if positions.dtype == torch.int64 else 0
+    _set_positions(p, positions, q)
     return _Call("mhla_rotary", q, p, new_q=_fresh(q), new_k=None if k is None else _fresh(k))
 
 
@@ -1054,4 +1110,522 @@ def mhla_decay_step(q, k, v, log_decay, state, scale: float = 1.0, out=None, sta
                     at if state_out is None else state_out.data_ptr(), c.stream())
     if status:
         raise MhlaError(status, "mhla_decay_step")
+    return out
+
+
+# --------------------------------------------------------------------------
+# Norm of queries and keys with their rotation
+
+
+def _qknorm_params(q, k, plan, q_weight, k_weight, eps, positions, style, layout):
+    axes = _axes(layout)
+    p = MhlaQknormParams()
+    p.style = _choice("style", style, ROTARY_STYLES)
+    if q.dim() != 4:
+        raise ValueError("q and k must be [B, H, N, d] (layout 'bhnd') or [B, N, H, d] (layout 'bnhd')")
+    _rows("q", q)
+    shape = q.shape
+    p.batch, p.heads, p.tokens, p.head_dim = shape[0], shape[axes[1]], shape[axes[2]], shape[3]
+    p.dtype = DTYPES[_torch_dtype_name(q)]
+    p.eps = eps
+    _set_strides(p.q, q, axes)
+    if k is not None:
+        want = list(shape)
+        want[axes[1]] = k.shape[axes[1]] if k.dim() == 4 else -1
+        _rows("k", k, q, q.dtype, want)
+        p.kv_heads = k.shape[axes[1]]
+        _set_strides(p.k, k, axes)
+    elif k_weight is not None:
+        raise ValueError("k_weight needs k")
+    p.weight_dtype = DTYPE_F32
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            _flat(name, t, q, None, (p.head_dim,))
+            p.weight_dtype = DTYPES[_torch_dtype_name(t)]
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TypeError("q_weight and k_weight must have the same dtype")
+    if plan is not None and plan.rot_dim > p.head_dim:
+        raise ValueError(f"the plan rotates {plan.rot_dim} entries of heads of {p.head_dim}")
+    _set_positions(p, positions, q)
+    return p, axes
+
+
+def _with_offset(c, offset):
+    """The call's parameter block, or one with this offset, which changes from token to token."""
+    if not offset:
+        return c.ref
+    p = type(c.params).from_buffer_copy(c.params)
+    p.position_offset = int(offset)
+    return ctypes.byref(p)
+
+
+def _qknorm_forward_call(q, k, plan, q_weight, k_weight, eps, positions, style, layout, q_out, k_out):
+    p, axes = _qknorm_params(q, k, plan, q_weight, k_weight, eps, positions, style, layout)
+    _set_output(p.q_out, "q_out", q_out, q, q.shape, axes)
+    if k is not None:
+        _set_output(p.k_out, "k_out", k_out, q, k.shape, axes)
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    return _Call("mhla_qknorm_forward", q, p, new_q=_fresh(q), new_k=None if k is None else _fresh(k))
+
+
+def mhla_qknorm_forward(q, k, plan: Optional[RotaryPlan], q_weight=None, k_weight=None, eps: float = 1e-6,
+                        positions=None, offset: int = 0, style: str = "half", layout: str = "bhnd", q_out=None,
+                        k_out=None, stream=None):
+    """Root-mean-square norm of queries and keys over each head, then their rotary positions: ``(q_out, k_out)``.
+
+    y = R(position) (x weight / sqrt(mean(x^2) + eps)) in one pass.  ``k`` may
+    be None and may have another number of heads.  ``q_weight`` and
+    ``k_weight``: [d], the same for every head, bfloat16 or float32 (None: 1).
+    ``plan`` None leaves the rotation out; ``positions``, ``offset``,
+    ``style`` and ``layout`` as for mhla_rotary_forward.  ``q_out is q`` and
+    ``k_out is k`` work in place.  Heads have at most 256 entries.
+    """
+    if stream is not None:
+        return _on_stream(stream, q, (q_out, k_out), lambda: mhla_qknorm_forward(
+            q, k, plan, q_weight, k_weight, eps, positions, offset, style, layout, q_out, k_out))
+    eps = float(eps)
+    key = ("qknorm", plan and plan.rot_dim, eps, style, layout, _sig(q), _sig(k), _sig(q_weight), _sig(k_weight),
+           _sig(positions), _sig(q_out), _sig(k_out))
+    c = _CALLS.get(key) or _remember(key, _qknorm_forward_call(q, k, plan, q_weight, k_weight, eps, positions, style,
+                                                               layout, q_out, k_out))
+    if q_out is None:
+        q_out = c.new_q(q)
+    if k_out is None and k is not None:
+        k_out = c.new_k(k)
+    status = c.call(q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+                    None if plan is None else plan._ref, _with_offset(c, offset), q_out.data_ptr(), _ptr(k_out),
+                    c.stream())
+    if status:
+        raise MhlaError(status, "mhla_qknorm_forward")
+    return q_out, k_out
+
+
+def mhla_qknorm_backward_workspace_bytes(p: MhlaQknormParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().mhla_qknorm_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(n)),
+           "mhla_qknorm_backward_workspace_bytes")
+    return n.value
+
+
+def _qknorm_backward_call(dq_out, dk_out, q, k, plan, q_weight, k_weight, eps, positions, style, layout, dq, dk,
+                          dq_weight, dk_weight, params):
+    import torch
+    p, axes = _qknorm_params(q, k, plan, q_weight, k_weight, eps, positions, style, layout)
+    _rows("dq_out", dq_out, q, q.dtype, q.shape)
+    _set_strides(p.dq_out, dq_out, axes)
+    _set_output(p.q_out, "dq", dq, q, q.shape, axes)
+    if k is not None:
+        if dk_out is None:
+            raise ValueError("k needs dk_out")
+        _rows("dk_out", dk_out, q, q.dtype, k.shape)
+        _set_strides(p.dk_out, dk_out, axes)
+        _set_output(p.k_out, "dk", dk, q, k.shape, axes)
+    for name, t in (("dk_out", dk_out), ("dk", dk), ("dk_weight", dk_weight)):
+        if t is not None and k is None:
+            raise ValueError(f"{name} needs k")
+    for name, t in (("dq_weight", dq_weight), ("dk_weight", dk_weight)):
+        if t is not None and not params:
+            raise ValueError(f"{name} needs params=True")
+        _flat(name, t, q, torch.float32, (p.head_dim,))
+    return _Call("mhla_qknorm_backward", q, p, mhla_qknorm_backward_workspace_bytes(p) if params else 0,
+                 new_q=_fresh(q), new_k=None if k is None else _fresh(k), dim=p.head_dim)
+
+
+def mhla_qknorm_backward(dq_out, dk_out, q, k, plan: Optional[RotaryPlan], q_weight=None, k_weight=None,
+                         eps: float = 1e-6, positions=None, offset: int = 0, style: str = "half",
+                         layout: str = "bhnd", dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None,
+                         stream=None, params: bool = True):
+    """Gradients of mhla_qknorm_forward: ``(dq, dk, dq_weight, dk_weight)``.
+
+    ``q`` and ``k`` are the forward call's inputs.  ``dq_weight`` and
+    ``dk_weight`` are float32 [d], summed over all rows in a fixed order;
+    ``params=False`` leaves them out (None).  ``dq`` may be ``dq_out`` or
+    ``q``, ``dk`` may be ``dk_out`` or ``k``.
+    """
+    if stream is not None:
+        return _on_stream(stream, q, (dq, dk, dq_weight, dk_weight), lambda: mhla_qknorm_backward(
+            dq_out, dk_out, q, k, plan, q_weight, k_weight, eps, positions, offset, style, layout, dq, dk, dq_weight,
+            dk_weight, workspace, params=params))
+    eps, params = float(eps), bool(params)
+    key = ("qknorm backward", plan and plan.rot_dim, params, eps, style, layout, _sig(dq_out), _sig(dk_out), _sig(q),
+           _sig(k), _sig(q_weight), _sig(k_weight), _sig(positions), _sig(dq), _sig(dk), _sig(dq_weight),
+           _sig(dk_weight))
+    c = _CALLS.get(key) or _remember(key, _qknorm_backward_call(
+        dq_out, dk_out, q, k, plan, q_weight, k_weight, eps, positions, style, layout, dq, dk, dq_weight, dk_weight,
+        params))
+    if dq is None:
+        dq = c.new_q(q)
+    if dk is None and k is not None:
+        dk = c.new_k(k)
+    ws_bytes = 0
+    if params:
+        if dq_weight is None:
+            dq_weight = c.empty(c.dim, dtype=c.f32, device=c.device)
+        if dk_weight is None and k is not None:
+            dk_weight = c.empty(c.dim, dtype=c.f32, device=c.device)
+        workspace, ws_bytes = c.workspace(workspace)
+    status = c.call(dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+                    _ptr(positions), None if plan is None else plan._ref, _with_offset(c, offset), dq.data_ptr(),
+                    _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), _ptr(workspace) if params else None, ws_bytes,
+                    c.stream())
+    if status:
+        raise MhlaError(status, "mhla_qknorm_backward")
+    return dq, dk, dq_weight, dk_weight
+
+
+# --------------------------------------------------------------------------
+# A recurrent layer: gated recurrence and short convolution.  Tensors are
+# [B, N, D] (single tokens: [B, D]).
+
+
+def _set_tokens(field, t) -> None:
+    """Strides of a tensor [B, N, D] or [B, D]."""
+    field.batch = t.stride(0)
+    field.token = t.stride(1) if t.dim() == 3 else 0
+
+
+def _set_result(field, name, t, like) -> None:
+    """Strides of a result: the given tensor's, or those of a new contiguous one."""
+    if t is not None:
+        _rows(name, t, like, like.dtype, like.shape)
+        _set_tokens(field, t)
+        return
+    step = max(like.shape[-1], 1)
+    field.token = step
+    field.batch = step * max(like.shape[1], 1) if like.dim() == 3 else step
+
+
+def _gated_params(x, gate, log_decay, input_gate, scale, dims):
+    import torch
+    if x.dim() != dims:
+        raise ValueError("x must be [B, N, D]" if dims == 3 else "x must be [B, D]")
+    _rows("x", x)
+    _rows("gate", gate, x, x.dtype, x.shape)
+    p = MhlaGatedParams()
+    p.batch, p.width = x.shape[0], x.shape[-1]
+    p.tokens = x.shape[1] if dims == 3 else 1
+    p.dtype = DTYPES[_torch_dtype_name(x)]
+    p.kind = GATED_SIGMOID if log_decay is None else GATED_DECAY
+    p.scale = _choice("scale", scale, GATED_SCALES)
+    _flat("log_decay", log_decay, x, torch.float32, (p.width,))
+    _set_tokens(p.x, x)
+    _set_tokens(p.gate, gate)
+    if input_gate is not None:
+        _rows("input_gate", input_gate, x, x.dtype, x.shape)
+        _set_tokens(p.input_gate, input_gate)
+    return p
+
+
+def _gated_side(p, like, lengths, **states):
+    import torch
+    _flat("lengths", lengths, like, torch.int32, (p.batch,))
+    for name, t in states.items():
+        _flat(name, t, like, torch.float32, (p.batch, p.width))
+    return (p.batch, p.width)
+
+
+def _marks_shape(p):
+    return p.batch, -(-p.tokens // GATED_MARK), p.width
+
+
+def _gated_forward_call(x, gate, log_decay, input_gate, state, lengths, scale, out, state_out, marks):
+    import torch
+    p = _gated_params(x, gate, log_decay, input_gate, scale, 3)
+    _set_result(p.out, "out", out, x)
+    shape = _gated_side(p, x, lengths, state=state, state_out=state_out)
+    _flat("marks", marks, x, torch.float32, _marks_shape(p))
+    return _Call("mhla_gated_forward", x, p, new=_fresh(x), shape=shape, marks=_marks_shape(p))
+
+
+def mhla_gated_forward(x, gate, log_decay=None, input_gate=None, state=None, lengths=None, scale: str = "norm",
+                       out=None, state_out=None, marks=None, stream=None, keep: bool = False):
+    """Gated linear recurrence over whole prompts: ``(out, state_out, marks)``.
+
+    h_t = a_t h_{t-1} + c_t u_t with u = x sigmoid(input_gate) (x without one)
+    and a = exp(log_decay sigmoid(gate)), or sigmoid(gate) where ``log_decay``
+    is None.  x, gate, input_gate: [B, N, D], bfloat16 or float32;
+    ``log_decay``: float32 [D], finite and <= 0.  ``scale``: c = sqrt(1 - a^2)
+    ("norm"), 1 - a ("mean") or 1 ("none").  ``state``: float32 [B, D] to start
+    from (None: zeros); ``state_out is state`` updates it in place.
+    ``lengths``: int32 [B] for sequences padded to N; rows past a length come
+    out as zeros.  ``keep=True`` also returns the states that the backward call
+    starts from (float32 [B, ceil(N / 64), D], into ``marks`` where given),
+    None otherwise.
+    """
+    if stream is not None:
+        return _on_stream(stream, x, (out, state_out, marks), lambda: mhla_gated_forward(
+            x, gate, log_decay, input_gate, state, lengths, scale, out, state_out, marks, keep=keep))
+    key = ("gated", scale, _sig(x), _sig(gate), _sig(log_decay), _sig(input_gate), _sig(state), _sig(lengths),
+           _sig(out), _sig(state_out), _sig(marks))
+    c = _CALLS.get(key) or _remember(key, _gated_forward_call(x, gate, log_decay, input_gate, state, lengths, scale,
+                                                              out, state_out, marks))
+    if out is None:
+        out = c.new(x)
+    if state_out is None:
+        state_out = c.empty(c.shape, dtype=c.f32, device=c.device)
+    if keep and marks is None:
+        marks = c.empty(c.marks, dtype=c.f32, device=c.device)
+    status = c.call(x.data_ptr(), gate.data_ptr(), _ptr(input_gate), _ptr(log_decay), _ptr(lengths), _ptr(state), c.ref,
+                    out.data_ptr(), state_out.data_ptr(), _ptr(marks), c.stream())
+    if status:
+        raise MhlaError(status, "mhla_gated_forward")
+    return out, state_out, marks
+
+
+def mhla_gated_backward_workspace_bytes(p: MhlaGatedParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().mhla_gated_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(n)),
+           "mhla_gated_backward_workspace_bytes")
+    return n.value
+
+
+def _gated_backward_call(x, gate, dout, log_decay, input_gate, state, dstate_out, marks, lengths, scale, dx, dgate,
+                         dinput_gate, dlog_decay, dstate, params):
+    import torch
+    p = _gated_params(x, gate, log_decay, input_gate, scale, 3)
+    _rows("dout", dout, x, x.dtype, x.shape)
+    _set_tokens(p.dout, dout)
+    _set_result(p.dx, "dx", dx, x)
+    _set_result(p.dgate, "dgate", dgate, x)
+    if input_gate is not None:
+        _set_result(p.dinput_gate, "dinput_gate", dinput_gate, x)
+    elif dinput_gate is not None:
+        raise ValueError("dinput_gate needs input_gate")
+    if dlog_decay is not None and (log_decay is None or not params):
+        raise ValueError("dlog_decay needs log_decay and params=True")
+    _flat("dlog_decay", dlog_decay, x, torch.float32, (p.width,))
+    shape = _gated_side(p, x, lengths, state=state, dstate_out=dstate_out, dstate=dstate)
+    _flat("marks", marks, x, torch.float32, _marks_shape(p))
+    p.marks = int(marks is not None)
+    return _Call("mhla_gated_backward", x, p, mhla_gated_backward_workspace_bytes(p), new_x=_fresh(x), new_r=_fresh(gate),
+                 new_i=None if input_gate is None else _fresh(input_gate), shape=shape, width=p.width)
+
+
+def mhla_gated_backward(x, gate, dout, log_decay=None, input_gate=None, state=None, dstate_out=None, marks=None,
+                        lengths=None, scale: str = "norm", dx=None, dgate=None, dinput_gate=None, dlog_decay=None,
+                        dstate=None, workspace=None, stream=None, params: bool = True):
+    """Gradients of mhla_gated_forward: ``(dx, dgate, dinput_gate, dlog_decay, dstate)``.
+
+    ``dout`` is the gradient of out and ``dstate_out`` that of the final state
+    (None: zeros).  ``marks`` are those that the forward call kept; without
+    them the states are formed again from ``state``.  ``dinput_gate`` is None
+    without an input gate, ``dlog_decay`` (float32 [D], summed in a fixed order)
+    without log_decay or with ``params=False``, and ``dstate`` (float32 [B, D])
+    without ``state``, unless a tensor is given for it.
+    """
+    if stream is not None:
+        return _on_stream(stream, x, (dx, dgate, dinput_gate, dlog_decay, dstate), lambda: mhla_gated_backward(
+            x, gate, dout, log_decay, input_gate, state, dstate_out, marks, lengths, scale, dx, dgate, dinput_gate,
+            dlog_decay, dstate, workspace, params=params))
+    params = bool(params)
+    key = ("gated backward", params, scale, _sig(x), _sig(gate), _sig(dout), _sig(log_decay), _sig(input_gate),
+           _sig(state), _sig(dstate_out), _sig(marks), _sig(lengths), _sig(dx), _sig(dgate), _sig(dinput_gate),
+           _sig(dlog_decay), _sig(dstate))
+    c = _CALLS.get(key) or _remember(key, _gated_backward_call(
+        x, gate, dout, log_decay, input_gate, state, dstate_out, marks, lengths, scale, dx, dgate, dinput_gate,
+        dlog_decay, dstate, params))
+    dx = c.new_x(x) if dx is None else dx
+    dgate = c.new_r(gate) if dgate is None else dgate
+    if dinput_gate is None and input_gate is not None:
+        dinput_gate = c.new_i(input_gate)
+    if dlog_decay is None and log_decay is not None and params:
+        dlog_decay = c.empty(c.width, dtype=c.f32, device=c.device)
+    if dstate is None and state is not None:
+        dstate = c.empty(c.shape, dtype=c.f32, device=c.device)
+    workspace, ws_bytes = c.workspace(workspace)
+    status = c.call(x.data_ptr(), gate.data_ptr(), _ptr(input_gate), _ptr(log_decay), _ptr(lengths), _ptr(state),
+                    _ptr(marks), dout.data_ptr(), _ptr(dstate_out), c.ref, dx.data_ptr(), dgate.data_ptr(),
+                    _ptr(dinput_gate), _ptr(dlog_decay), _ptr(dstate), _ptr(workspace), ws_bytes, c.stream())
+    if status:
+        raise MhlaError(status, "mhla_gated_backward")
+    return dx, dgate, dinput_gate, dlog_decay, dstate
+
+
+def _gated_step_call(x, gate, state, log_decay, input_gate, scale, out, state_out):
+    p = _gated_params(x, gate, log_decay, input_gate, scale, 2)
+    if state is None:
+        raise ValueError("state must be given")
+    _gated_side(p, x, None, state=state, state_out=state_out)
+    _set_result(p.out, "out", out, x)
+    return _Call("mhla_gated_step", x, p, new=_fresh(x))
+
+
+def mhla_gated_step(x, gate, state, log_decay=None, input_gate=None, scale: str = "norm", out=None, state_out=None,
+                    stream=None):
+    """One token of every sequence: returns ``out`` [B, D].
+
+    x, gate, input_gate: [B, D]; ``state`` float32 [B, D] is updated in place
+    unless ``state_out`` is given.
+    """
+    if stream is not None:
+        return _on_stream(stream, x, (out,), lambda: mhla_gated_step(
+            x, gate, state, log_decay, input_gate, scale, out, state_out))
+    key = ("gated step", scale, _sig(x), _sig(gate), _sig(state), _sig(log_decay), _sig(input_gate), _sig(out),
+           _sig(state_out))
+    c = _CALLS.get(key) or _remember(key, _gated_step_call(x, gate, state, log_decay, input_gate, scale, out,
+                                                           state_out))
+    if out is None:
+        out = c.new(x)
+    at = state.data_ptr()
+    status = c.call(x.data_ptr(), gate.data_ptr(), _ptr(input_gate), _ptr(log_decay), at, c.ref, out.data_ptr(),
+                    at if state_out is None else state_out.data_ptr(), c.stream())
+    if status:
+        raise MhlaError(status, "mhla_gated_step")
+    return out
+
+
+def _conv_params(x, weight, bias, activation, dims):
+    if x.dim() != dims:
+        raise ValueError("x must be [B, N, D]" if dims == 3 else "x must be [B, D]")
+    _rows("x", x)
+    p = MhlaShortconvParams()
+    p.batch, p.width = x.shape[0], x.shape[-1]
+    p.tokens = x.shape[1] if dims == 3 else 1
+    p.dtype = DTYPES[_torch_dtype_name(x)]
+    if weight.dim() != 2:
+        raise ValueError("weight must be [D, taps]")
+    p.taps = weight.shape[1]
+    _flat("weight", weight, x, None, (p.width, p.taps))
+    p.weight_dtype = DTYPES[_torch_dtype_name(weight)]
+    _flat("bias", bias, x, weight.dtype, (p.width,))
+    p.activation = _choice("activation", activation, ACTIVATIONS)
+    _set_tokens(p.x, x)
+    return p
+
+
+def _conv_side(p, like, lengths, **states):
+    import torch
+    _flat("lengths", lengths, like, torch.int32, (p.batch,))
+    shape = (p.batch, max(p.taps - 1, 0), p.width)
+    for name, t in states.items():
+        _flat(name, t, like, like.dtype, shape)
+    return shape
+
+
+def _conv_forward_call(x, weight, bias, state, lengths, activation, out, state_out):
+    p = _conv_params(x, weight, bias, activation, 3)
+    _set_result(p.out, "out", out, x)
+    shape = _conv_side(p, x, lengths, state=state, state_out=state_out)
+    return _Call("mhla_shortconv_forward", x, p, new=_fresh(x), shape=shape, dtype=x.dtype)
+
+
+def mhla_shortconv_forward(x, weight, bias=None, state=None, lengths=None, activation: str = "none", out=None,
+                           state_out=None, stream=None):
+    """Short causal convolution of each channel over whole prompts: ``(out, state_out)``.
+
+    out_t = f(sum_j weight[d, j] x_{t - taps + 1 + j} + bias[d]), f the identity
+    or ("silu") z sigmoid(z).  x: [B, N, D], bfloat16 or float32; ``weight``:
+    [D, taps] with 2 to 4 taps and ``bias`` [D], bfloat16 or float32.
+    ``state``: the taps - 1 rows before the first token, [B, taps - 1, D] of
+    x's dtype (None: zeros); ``state_out`` receives the last ones and may be
+    ``state``.  ``lengths``: int32 [B] for sequences padded to N; rows past a
+    length come out as zeros.
+    """
+    if stream is not None:
+        return _on_stream(stream, x, (out, state_out), lambda: mhla_shortconv_forward(
+            x, weight, bias, state, lengths, activation, out, state_out))
+    key = ("conv", activation, _sig(x), _sig(weight), _sig(bias), _sig(state), _sig(lengths), _sig(out),
+           _sig(state_out))
+    c = _CALLS.get(key) or _remember(key, _conv_forward_call(x, weight, bias, state, lengths, activation, out,
+                                                             state_out))
+    if out is None:
+        out = c.new(x)
+    if state_out is None:
+        state_out = c.empty(c.shape, dtype=c.dtype, device=c.device)
+    status = c.call(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(lengths), _ptr(state), c.ref, out.data_ptr(),
+                    state_out.data_ptr(), c.stream())
+    if status:
+        raise MhlaError(status, "mhla_shortconv_forward")
+    return out, state_out
+
+
+def mhla_shortconv_backward_workspace_bytes(p: MhlaShortconvParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().mhla_shortconv_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(n)),
+           "mhla_shortconv_backward_workspace_bytes")
+    return n.value
+
+
+def _conv_backward_call(x, weight, dout, bias, state, dstate_out, lengths, activation, dx, dweight, dbias, dstate,
+                        params):
+    import torch
+    p = _conv_params(x, weight, bias, activation, 3)
+    _rows("dout", dout, x, x.dtype, x.shape)
+    _set_tokens(p.dout, dout)
+    _set_result(p.dx, "dx", dx, x)
+    for name, t, shape in (("dweight", dweight, (p.width, p.taps)), ("dbias", dbias, (p.width,))):
+        if t is not None and not params:
+            raise ValueError(f"{name} needs params=True")
+        _flat(name, t, x, torch.float32, shape)
+    shape = _conv_side(p, x, lengths, state=state, dstate_out=dstate_out, dstate=dstate)
+    return _Call("mhla_shortconv_backward", x, p, mhla_shortconv_backward_workspace_bytes(p) if params else 0,
+                 new=_fresh(x), shape=shape, dtype=x.dtype, wshape=(p.width, p.taps), width=p.width)
+
+
+def mhla_shortconv_backward(x, weight, dout, bias=None, state=None, dstate_out=None, lengths=None,
+                            activation: str = "none", dx=None, dweight=None, dbias=None, dstate=None, workspace=None,
+                            stream=None, params: bool = True):
+    """Gradients of mhla_shortconv_forward: ``(dx, dweight, dbias, dstate)``.
+
+    ``dweight`` (float32 [D, taps]) and ``dbias`` (float32 [D], None without a
+    bias unless a tensor is given for it) are summed in a fixed order;
+    ``params=False`` leaves them out.  ``dstate`` is the gradient of ``state``
+    (x's dtype; None without one, unless a tensor is given for it).
+    """
+    if stream is not None:
+        return _on_stream(stream, x, (dx, dweight, dbias, dstate), lambda: mhla_shortconv_backward(
+            x, weight, dout, bias, state, dstate_out, lengths, activation, dx, dweight, dbias, dstate, workspace,
+            params=params))
+    params = bool(params)
+    key = ("conv backward", params, activation, _sig(x), _sig(weight), _sig(dout), _sig(bias), _sig(state),
+           _sig(dstate_out), _sig(lengths), _sig(dx), _sig(dweight), _sig(dbias), _sig(dstate))
+    c = _CALLS.get(key) or _remember(key, _conv_backward_call(x, weight, dout, bias, state, dstate_out, lengths,
+                                                              activation, dx, dweight, dbias, dstate, params))
+    if dx is None:
+        dx = c.new(x)
+    ws_bytes = 0
+    if params:
+        if dweight is None:
+            dweight = c.empty(c.wshape, dtype=c.f32, device=c.device)
+        if dbias is None and bias is not None:
+            dbias = c.empty(c.width, dtype=c.f32, device=c.device)
+        workspace, ws_bytes = c.workspace(workspace)
+    if dstate is None and state is not None:
+        dstate = c.empty(c.shape, dtype=c.dtype, device=c.device)
+    status = c.call(x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(lengths), _ptr(state), dout.data_ptr(),
+                    _ptr(dstate_out), c.ref, dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(dstate),
+                    _ptr(workspace) if params else None, ws_bytes, c.stream())
+    if status:
+        raise MhlaError(status, "mhla_shortconv_backward")
+    return dx, dweight, dbias, dstate
+
+
+def _conv_step_call(x, weight, state, bias, activation, out, state_out):
+    p = _conv_params(x, weight, bias, activation, 2)
+    if state is None:
+        raise ValueError("state must be given")
+    _conv_side(p, x, None, state=state, state_out=state_out)
+    _set_result(p.out, "out", out, x)
+    return _Call("mhla_shortconv_step", x, p, new=_fresh(x))
+
+
+def mhla_shortconv_step(x, weight, state, bias=None, activation: str = "none", out=None, state_out=None, stream=None):
+    """One token of every sequence: returns ``out`` [B, D].
+
+    x: [B, D]; ``state`` [B, taps - 1, D] moves on by one row, in place unless
+    ``state_out`` is given.
+    """
+    if stream is not None:
+        return _on_stream(stream, x, (out,), lambda: mhla_shortconv_step(
+            x, weight, state, bias, activation, out, state_out))
+    key = ("conv step", activation, _sig(x), _sig(weight), _sig(state), _sig(bias), _sig(out), _sig(state_out))
+    c = _CALLS.get(key) or _remember(key, _conv_step_call(x, weight, state, bias, activation, out, state_out))
+    if out is None:
+        out = c.new(x)
+    at = state.data_ptr()
+    status = c.call(x.data_ptr(), weight.data_ptr(), _ptr(bias), at, c.ref, out.data_ptr(),
+                    at if state_out is None else state_out.data_ptr(), c.stream())
+    if status:
+        raise MhlaError(status, "mhla_shortconv_step")
     return out

@@ -1,0 +1,75 @@
+// Short vectors of a row and the approximate functions of the streaming
+// operators (gated recurrence, normalised queries and keys, short convolution).
+#pragma once
+
+#include "common.cuh"
+
+namespace mhla {
+
+// N consecutive elements, at most 16 bytes; `whole`
+// takes them in one access, otherwise the first `n` one by one.
+template <typename T, int N>
+struct Pack {
+  static_assert(sizeof(T) * N <= 16, "one access");
+  alignas(sizeof(T) * N) T v[N];
+  __device__ __forceinline__ float f(int i) const { return to_f32(v[i]); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = from_f32<T>(0.f);
+  }
+  __device__ __forceinline__ void load(const T* p, bool whole, int n = N) {
+    if (whole) {
+      if constexpr (sizeof(T) * N == 16)
+        *reinterpret_cast<uint4*>(v) = __ldcs(reinterpret_cast<const uint4*>(p));
+      else if constexpr (sizeof(T) * N == 8)
+        *reinterpret_cast<uint2*>(v) = __ldcs(reinterpret_cast<const uint2*>(p));
+      else if constexpr (sizeof(T) * N == 4)
+        *reinterpret_cast<unsigned int*>(v) = __ldcs(reinterpret_cast<const unsigned int*>(p));
+      else
+        v[0] = p[0];
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = i < n ? p[i] : from_f32<T>(0.f);
+  }
+  __device__ __forceinline__ void store(T* p, bool whole, int n = N) const {
+    if (whole) {
+      if constexpr (sizeof(T) * N == 16)
+        __stcs(reinterpret_cast<uint4*>(p), *reinterpret_cast<const uint4*>(v));
+      else if constexpr (sizeof(T) * N == 8)
+        __stcs(reinterpret_cast<uint2*>(p), *reinterpret_cast<const uint2*>(v));
+      else if constexpr (sizeof(T) * N == 4)
+        __stcs(reinterpret_cast<unsigned int*>(p), *reinterpret_cast<const unsigned int*>(v));
+      else
+        p[0] = v[0];
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) p[i] = v[i];
+  }
+};
+
+// Entry i of a parameter vector that is bf16 or float32.
+__device__ __forceinline__ float param_at(const void* p, int is_f32, int64_t i) {
+  return is_f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rsq(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+}  // namespace mhla

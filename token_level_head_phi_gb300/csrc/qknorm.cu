@@ -1,0 +1,614 @@
+// Norm of queries and keys over each head and their rotation, in one pass:
+//   y = R(position) (x rstd w),  rstd = 1 / sqrt(mean(x^2) + eps),
+// and the gradients: with t = R^T dy and g = w t,
+//   dx = rstd (g - xh mean(g xh)),  dw = sum t xh,  xh = x rstd.
+//
+// A row is held by a group of G threads, so that both entries of a rotated
+// pair are one thread's, and is read once; its sums meet through shuffles.  A
+// group forms the sines of its token once and walks over the heads.  Phases
+// are the 64-bit fractions of a turn of mhla_rotary_table.
+// Bound: memory (each row read once and written once; the backward pass reads
+// two rows and writes one).
+#include <cmath>
+
+#include "common.cuh"
+#include "ops.h"
+#include "pack.cuh"
+
+namespace mhla {
+namespace {
+
+constexpr int kMaxDim = 256;
+
+struct QkArgs {
+  const void* x[2];
+  const void* dy[2];  // backward
+  void* y[2];         // results; dq and dk in the backward pass
+  mhla_strides sx[2], sdy[2], sy[2];
+  const void* w[2];
+  int w_f32;
+  const void* positions;
+  int64_t pos_offset, pos_sb, pos_st;
+  int pos64;
+  int heads[2];
+  int batch, tokens, dim;
+  int half;      // rotated pairs
+  int adjacent;  // pairs (2i, 2i + 1) taken apart into two single entries
+  int slots;     // of a row, two vectors each
+  int group, lanes_shift;  // threads of a row, a power of two, and its logarithm
+  int heads_per_thread;
+  int ctas[2];     // backward: CTAs that take q's and k's rows
+  float eps, inv_dim, amp;
+  float* partial;  // backward: [CTAs][dim]
+  mhla_rotary_table table;
+};
+
+// Columns of a slot's two vectors.  ACROSS pairs entry i of the first with
+// entry i of the second; otherwise neighbours inside a vector are paired.
+template <int VEC, bool ACROSS>
+__device__ __forceinline__ void columns(const QkArgs& a, int slot, int* lo, int* hi) {
+  if (ACROSS && !a.adjacent) {
+    const int rot = a.half / VEC;
+    if (slot < rot) {
+      *lo = slot * VEC;
+      *hi = a.half + slot * VEC;
+      return;
+    }
+    slot -= rot;
+    *lo = 2 * a.half + slot * 2 * VEC;
+  } else {
+    *lo = slot * 2 * VEC;
+  }
+  *hi = *lo + VEC;
+}
+
+// Cosines and sines of a slot's pairs; 1 and 0 for entries that are not
+// rotated.
+template <int VEC, bool ACROSS>
+__device__ __forceinline__ void turns_of(const QkArgs& a, const uint64_t* turns, int64_t pos, int lo, float sign,
+                                         float (&cs)[VEC], float (&sn)[VEC]) {
+  const int first = ACROSS && !a.adjacent ? lo : lo / 2;  // pair of the first entry
+  const bool rotated = ACROSS && !a.adjacent ? lo < a.half : true;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    cs[i] = 1.f;
+    sn[i] = 0.f;
+    if (rotated && first + i < a.half) {
+      const uint64_t phase = (uint64_t)pos * turns[first + i];
+      sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &sn[i], &cs[i]);
+      cs[i] *= a.amp;
+      sn[i] *= a.amp * sign;
+    }
+  }
+}
+
+// Rotates a slot's values in place.
+template <int VEC, bool ACROSS>
+__device__ __forceinline__ void turn(float (&v)[2][VEC], const float (&cs)[VEC], const float (&sn)[VEC]) {
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) {
+    float& p = ACROSS ? v[0][i] : v[2 * i / VEC][2 * i % VEC];
+    float& q = ACROSS ? v[1][i] : v[(2 * i + 1) / VEC][(2 * i + 1) % VEC];
+    const float x = p, y = q;
+    p = x * cs[i] - y * sn[i];
+    q = x * sn[i] + y * cs[i];
+  }
+}
+
+__device__ __forceinline__ int64_t position_of(const QkArgs& a, int64_t b, int t) {
+  if (!a.positions) return a.pos_offset + t;
+  const int64_t at = b * a.pos_sb + t * a.pos_st;
+  return a.pos64 ? static_cast<const int64_t*>(a.positions)[at] : static_cast<const int32_t*>(a.positions)[at];
+}
+
+template <typename T, int VEC, bool ACROSS, int E>
+__global__ void __launch_bounds__(256) qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int R = E > 1 ? 2 : 4;  // rows in flight
+  __shared__ uint64_t turns[MHLA_ROTARY_MAX_PAIRS];
+  for (int i = threadIdx.x; i < a.half; i += blockDim.x) turns[i] = a.table.turns[i];
+  __syncthreads();
+  const int lane = threadIdx.x & (a.group - 1);
+  const int64_t token = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> a.lanes_shift;
+  const bool live = token < (int64_t)a.batch * a.tokens;
+  const int64_t b = live ? token / a.tokens : 0;
+  const int t = live ? (int)(token - b * a.tokens) : 0;
+  const int64_t pos = position_of(a, b, t);
+  int col[E][2];
+  bool in[E][2];
+  float cs[E][VEC], sn[E][VEC];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int slot = lane + e * a.group;
+    columns<VEC, ACROSS>(a, slot, &col[e][0], &col[e][1]);
+    turns_of<VEC, ACROSS>(a, turns, pos, col[e][0], 1.f, cs[e], sn[e]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) in[e][k] = live && slot < a.slots && col[e][k] < a.dim;
+  }
+  const int first = blockIdx.y * a.heads_per_thread, last = min(first + a.heads_per_thread, a.heads[0] + a.heads[1]);
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    int h = max(first - (which ? a.heads[0] : 0), 0);
+    const int end = which ? last - a.heads[0] : min(last, a.heads[0]);
+    if (h >= end) continue;  // the same for the whole grid row
+    float w[E][2][VEC];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+          w[e][k][i] = a.w[which] && in[e][k] ? param_at(a.w[which], a.w_f32, col[e][k] + i) : 1.f;
+    const T* src = static_cast<const T*>(a.x[which]) + b * a.sx[which].batch + t * a.sx[which].token;
+    T* dst = static_cast<T*>(a.y[which]) + b * a.sy[which].batch + t * a.sy[which].token;
+    for (; h < end; h += R) {
+      Pack<T, VEC> raw[R][E][2];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (in[e][k] && h + r < end)
+              raw[r][e][k].load(src + (h + r) * a.sx[which].head + col[e][k], true);
+            else
+              raw[r][e][k].zero();
+      float sum[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        sum[r] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) sum[r] = fmaf(raw[r][e][k].f(i), raw[r][e][k].f(i), sum[r]);
+      }
+      for (int o = a.group / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float rstd = rsqrtf(fmaf(sum[r], a.inv_dim, a.eps));
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          float v[2][VEC];
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[k][i] = raw[r][e][k].f(i) * rstd * w[e][k][i];
+          turn<VEC, ACROSS>(v, cs[e], sn[e]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (in[e][k] && h + r < end) {
+              Pack<T, VEC> o;
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) o.v[i] = from_f32<T>(v[k][i]);
+              o.store(dst + (h + r) * a.sy[which].head + col[e][k], true);
+            }
+        }
+      }
+    }
+  }
+}
+
+// CTAs take the tokens in turn, those below ctas[0] q's rows and the others
+// k's, and keep the sums of dw of their columns in registers.
+template <typename T, int VEC, bool ACROSS, int E>
+__global__ void __launch_bounds__(256) qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int R = E > 1 ? 1 : 2;
+  __shared__ uint64_t turns[MHLA_ROTARY_MAX_PAIRS];
+  __shared__ float sums[8][kMaxDim];
+  for (int i = threadIdx.x; i < a.half; i += blockDim.x) turns[i] = a.table.turns[i];
+  __syncthreads();
+  const int which = (int)blockIdx.x >= a.ctas[0];
+  const int cta = blockIdx.x - (which ? a.ctas[0] : 0), ctas = a.ctas[which], heads = a.heads[which];
+  const int lane = threadIdx.x & (a.group - 1), per = blockDim.x >> a.lanes_shift;
+  int col[E][2];
+  bool in[E][2];
+  float w[E][2][VEC], dw[E][2][VEC];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int slot = lane + e * a.group;
+    columns<VEC, ACROSS>(a, slot, &col[e][0], &col[e][1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      in[e][k] = slot < a.slots && col[e][k] < a.dim;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        w[e][k][i] = a.w[which] && in[e][k] ? param_at(a.w[which], a.w_f32, col[e][k] + i) : 1.f;
+        dw[e][k][i] = 0.f;
+      }
+    }
+  }
+  const int64_t all = (int64_t)a.batch * a.tokens;
+  // every thread of the CTA makes the same number of turns
+  for (int64_t base = (int64_t)cta * per; base < all; base += (int64_t)ctas * per) {
+    const int64_t token = base + (threadIdx.x >> a.lanes_shift);
+    const bool live = token < all;
+    const int64_t b = live ? token / a.tokens : 0;
+    const int t = live ? (int)(token - b * a.tokens) : 0;
+    const int64_t pos = position_of(a, b, t);
+    float cs[E][VEC], sn[E][VEC];
+#pragma unroll
+    for (int e = 0; e < E; ++e) turns_of<VEC, ACROSS>(a, turns, pos, col[e][0], -1.f, cs[e], sn[e]);
+    const T* x = static_cast<const T*>(a.x[which]) + b * a.sx[which].batch + t * a.sx[which].token;
+    const T* dy = static_cast<const T*>(a.dy[which]) + b * a.sdy[which].batch + t * a.sdy[which].token;
+    T* dx = static_cast<T*>(a.y[which]) + b * a.sy[which].batch + t * a.sy[which].token;
+    for (int h = 0; h < heads; h += R) {
+      Pack<T, VEC> rx[R][E][2], rd[R][E][2];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (in[e][k] && live && h + r < heads) {
+              rx[r][e][k].load(x + (h + r) * a.sx[which].head + col[e][k], true);
+              rd[r][e][k].load(dy + (h + r) * a.sdy[which].head + col[e][k], true);
+            } else {
+              rx[r][e][k].zero();
+              rd[r][e][k].zero();
+            }
+      float v[R][E][2][VEC], sum[R], along[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        sum[r] = along[r] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[r][e][k][i] = rd[r][e][k].f(i);
+          turn<VEC, ACROSS>(v[r][e], cs[e], sn[e]);  // t
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              const float xv = rx[r][e][k].f(i);
+              sum[r] = fmaf(xv, xv, sum[r]);
+              along[r] = fmaf(v[r][e][k][i] * w[e][k][i], xv, along[r]);
+            }
+        }
+      }
+      for (int o = a.group / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
+          along[r] += __shfl_xor_sync(0xffffffffu, along[r], o);
+        }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bool row = live && h + r < heads;
+        // a row that is not there adds nothing, although its rstd may be infinite
+        const float rstd = row ? rsqrtf(fmaf(sum[r], a.inv_dim, a.eps)) : 0.f;
+        const float mean = along[r] * rstd * a.inv_dim;  // of g xh
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            Pack<T, VEC> o;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+              const float xh = rx[r][e][k].f(i) * rstd, tv = v[r][e][k][i];
+              dw[e][k][i] = fmaf(tv, xh, dw[e][k][i]);
+              o.v[i] = from_f32<T>(rstd * fmaf(tv, w[e][k][i], -xh * mean));
+            }
+            if (in[e][k] && row) o.store(dx + (h + r) * a.sy[which].head + col[e][k], true);
+          }
+      }
+    }
+  }
+  if (!a.partial) return;
+  // groups of a warp hold the same columns; then the warps in order
+  for (int o = a.group; o < 32; o <<= 1)
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) dw[e][k][i] += __shfl_xor_sync(0xffffffffu, dw[e][k][i], o);
+  if ((threadIdx.x & 31) < a.group)
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (in[e][k])
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) sums[threadIdx.x >> 5][col[e][k] + i] = dw[e][k][i];
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.dim; c += blockDim.x) {
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < 8; ++v) s += sums[v][c];
+    a.partial[(int64_t)blockIdx.x * a.dim + c] = s;
+  }
+}
+
+// Adds the CTAs' rows: a CTA takes 32 columns of q's or k's, 32 threads a column.
+__global__ void __launch_bounds__(1024) qknorm_reduce_kernel(const float* partial, int ctas_q, int ctas_k, int dim,
+                                                             float* dq_weight, float* dk_weight) {
+  __shared__ float sh[32][33];
+  const int which = blockIdx.y, tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
+  const int first = which ? ctas_q : 0, last = which ? ctas_q + ctas_k : ctas_q;
+  float s = 0.f;
+  if (c < dim)
+    for (int p = first + ty; p < last; p += 32) s += partial[(int64_t)p * dim + c];
+  sh[ty][tx] = s;
+  __syncthreads();
+  float* out = which ? dk_weight : dq_weight;
+  if (ty == 0 && c < dim && out) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += sh[i][tx];
+    out[c] = t;
+  }
+}
+
+// ---------------------------------------------------------------- dispatch
+
+constexpr int kBwdResident = 3;  // CTAs of the backward kernel that an SM holds
+
+// CTAs of the backward pass: those that are resident at once, shared out by
+// the number of heads, none for nothing.
+void share_ctas(QkArgs* a) {
+  const int64_t per = 256 / a->group, all = (int64_t)a->batch * a->tokens;
+  const int64_t most = (all + per - 1) / per;  // one turn each
+  const int total = a->heads[0] + a->heads[1];
+  for (int i = 0; i < 2; ++i) {
+    int64_t n = total ? (int64_t)kBwdResident * kOpsSms * a->heads[i] / total : 0;
+    if (n < 1) n = 1;
+    if (n > most) n = most;
+    a->ctas[i] = a->heads[i] && all ? (int)n : 0;
+  }
+}
+
+template <typename T, int VEC, bool ACROSS, int E>
+mhla_status launch(QkArgs& a, bool backward, cudaStream_t s) {
+  if (backward) {
+    qknorm_bwd_kernel<T, VEC, ACROSS, E><<<a.ctas[0] + a.ctas[1], 256, 0, s>>>(a);
+    return launch_status();
+  }
+  // Heads are shared out over threads only where there are too few tokens to
+  // fill the GPU, as each share forms the sines again.
+  const int64_t items = (int64_t)a.batch * a.tokens * a.group, want = (int64_t)kOpsSms * 2048;
+  const int total = a.heads[0] + a.heads[1];
+  int64_t parts = (want + items - 1) / items;
+  if (parts > total) parts = total;
+  a.heads_per_thread = (int)((total + parts - 1) / parts);
+  parts = (total + a.heads_per_thread - 1) / a.heads_per_thread;
+  const int threads = items * parts < want ? 64 : 256;
+  const int64_t blocks = (items + threads - 1) / threads;
+  if (blocks > 0x7fffffff || parts > 65535) return MHLA_ERR_UNSUPPORTED;
+  qknorm_fwd_kernel<T, VEC, ACROSS, E><<<dim3((unsigned)blocks, (unsigned)parts), threads, 0, s>>>(a);
+  return launch_status();
+}
+
+// Elements of the widest vector that divides the rotated part (each half of it
+// for HALF), the row and every row start.
+int vector_of(int dim, int pairs, int style, int elem, int align) {
+  const int unit = style == MHLA_ROTARY_HALF ? pairs : 2 * pairs;
+  for (int v = 16 / elem; v > 1; v /= 2)
+    if (unit % v == 0 && dim % v == 0 && align >= v * elem && 2 * v * elem >= 16) return v;
+  return 1;
+}
+
+// Slots and the threads of a row for vectors of `vec` elements.
+void shape_rows(QkArgs* a, int vec, int style) {
+  a->adjacent = vec == 1 && style == MHLA_ROTARY_INTERLEAVED;
+  a->slots = style == MHLA_ROTARY_HALF ? a->half / vec + (a->dim - 2 * a->half + 2 * vec - 1) / (2 * vec)
+                                       : (a->dim + 2 * vec - 1) / (2 * vec);
+  a->group = 1;
+  a->lanes_shift = 0;
+  while (a->group < 32 && a->group < a->slots) {
+    a->group *= 2;
+    ++a->lanes_shift;
+  }
+}
+
+template <typename T>
+mhla_status dispatch(QkArgs& a, int style, int vec, bool backward, cudaStream_t s) {
+  constexpr int W = 16 / sizeof(T);
+  const bool half = style == MHLA_ROTARY_HALF;
+  if (vec == W)  // at most 32 slots
+    return half ? launch<T, W, true, 1>(a, backward, s) : launch<T, W, false, 1>(a, backward, s);
+  if (vec == W / 2) {
+    if (a.slots <= 32)
+      return half ? launch<T, W / 2, true, 1>(a, backward, s) : launch<T, W / 2, false, 1>(a, backward, s);
+    return half ? launch<T, W / 2, true, 2>(a, backward, s) : launch<T, W / 2, false, 2>(a, backward, s);
+  }
+  if (a.slots <= 32) return launch<T, 1, true, 1>(a, backward, s);
+  if (a.slots <= 64) return launch<T, 1, true, 2>(a, backward, s);
+  return launch<T, 1, true, 4>(a, backward, s);
+}
+
+mhla_status check_params(const mhla_qknorm_params* p, const mhla_rotary_table* table) {
+  if (!p || p->batch < 0 || p->tokens < 0 || p->heads < 0 || p->kv_heads < 0) return MHLA_ERR_INVALID_ARG;
+  if (!ops_dtype_ok(p->dtype) || !ops_dtype_ok(p->weight_dtype)) return MHLA_ERR_INVALID_ARG;
+  if (p->style != MHLA_ROTARY_HALF && p->style != MHLA_ROTARY_INTERLEAVED) return MHLA_ERR_INVALID_ARG;
+  if (p->position_dtype != MHLA_POSITIONS_I32 && p->position_dtype != MHLA_POSITIONS_I64) return MHLA_ERR_INVALID_ARG;
+  if (!std::isfinite(p->eps) || p->eps < 0.f || p->head_dim < 1) return MHLA_ERR_INVALID_ARG;
+  if (p->style == MHLA_ROTARY_INTERLEAVED && p->head_dim % 2 != 0) return MHLA_ERR_INVALID_ARG;
+  if (table && (table->pairs < 1 || table->pairs > MHLA_ROTARY_MAX_PAIRS || p->head_dim < 2 * table->pairs))
+    return MHLA_ERR_INVALID_ARG;
+  if (p->head_dim > kMaxDim || p->heads > 32768 || p->kv_heads > 32768) return MHLA_ERR_UNSUPPORTED;
+  return MHLA_OK;
+}
+
+QkArgs args_of(const mhla_qknorm_params* p, const mhla_rotary_table* table, bool k, const void* positions) {
+  QkArgs a = {};
+  a.heads[0] = p->heads;
+  a.heads[1] = k ? p->kv_heads : 0;
+  a.batch = p->batch;
+  a.tokens = p->tokens;
+  a.dim = p->head_dim;
+  a.inv_dim = 1.f / (float)p->head_dim;
+  a.eps = p->eps;
+  a.w_f32 = p->weight_dtype == MHLA_DTYPE_F32;
+  a.sx[0] = p->q;
+  a.sx[1] = p->k;
+  a.sdy[0] = p->dq_out;
+  a.sdy[1] = p->dk_out;
+  a.sy[0] = p->q_out;
+  a.sy[1] = p->k_out;
+  a.positions = positions;
+  a.pos_offset = p->position_offset;
+  a.pos_sb = p->position_batch_stride;
+  a.pos_st = p->position_token_stride;
+  a.pos64 = p->position_dtype == MHLA_POSITIONS_I64;
+  a.amp = 1.f;
+  if (table) {
+    a.half = table->pairs;
+    a.amp = table->amplitude;
+    a.table = *table;
+  }
+  return a;
+}
+
+RowTensor rows(const void* ptr, const mhla_qknorm_params* p, int heads, const mhla_strides& s) {
+  return row_tensor(ptr, p->batch, heads, p->tokens, s, p->head_dim, ops_elem(p->dtype));
+}
+
+// Tensors without rows may have no address.
+bool any_rows(const mhla_qknorm_params* p, int heads) { return p->batch > 0 && p->tokens > 0 && heads > 0; }
+
+RowTensor positions_of(const void* ptr, const mhla_qknorm_params* p) {
+  const mhla_strides s = {p->position_batch_stride, 0, p->position_token_stride};
+  return row_tensor(ptr, ptr ? p->batch : 0, 1, p->tokens, s, 1, p->position_dtype == MHLA_POSITIONS_I64 ? 8 : 4);
+}
+
+int least_alignment(const RowTensor* t, int n) {
+  int align = 16;
+  for (int i = 0; i < n; ++i)
+    if (!t[i].empty()) {
+      const int x = row_alignment(t[i], 16);
+      align = x < align ? x : align;
+    }
+  return align;
+}
+
+// At least the CTAs of the backward pass, whatever the table, the pointers'
+// alignment and the presence of k: rows by 32 threads take the most turns, and
+// rounding up the smaller share adds one.
+int64_t most_ctas(const mhla_qknorm_params* p) {
+  const int64_t all = (int64_t)p->batch * p->tokens, turns = 2 * ((all + 7) / 8);
+  const int64_t most = kBwdResident * kOpsSms + 1;
+  return turns < most ? turns : most;
+}
+
+}  // namespace
+}  // namespace mhla
+
+extern "C" {
+
+mhla_status mhla_qknorm_forward(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                                const void* positions, const mhla_rotary_table* table, const mhla_qknorm_params* p,
+                                void* q_out, void* k_out, void* stream) {
+  using namespace mhla;
+  const mhla_status st = check_params(p, table);
+  if (st != MHLA_OK) return st;
+  if (!k && any_rows(p, p->kv_heads) && (k_out || k_weight)) return MHLA_ERR_INVALID_ARG;
+  const int kv = k ? p->kv_heads : 0;
+  const RowTensor t[4] = {rows(q, p, p->heads, p->q), rows(k, p, kv, p->k), rows(q_out, p, p->heads, p->q_out),
+                          rows(k_out, p, kv, p->k_out)};
+  const size_t we = ops_elem(p->weight_dtype);
+  const RowTensor side[3] = {flat_tensor(q_weight, q_weight ? p->head_dim : 0, we),
+                             flat_tensor(k_weight, k_weight ? p->head_dim : 0, we), positions_of(positions, p)};
+  for (int i = 0; i < 4; ++i)
+    if (!row_tensor_ok(t[i], i >= 2)) return MHLA_ERR_INVALID_ARG;
+  for (const RowTensor& x : side)
+    if (!row_tensor_ok(x, false) || !row_tensors_apart(x, t[2]) || !row_tensors_apart(x, t[3]))
+      return MHLA_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i) {
+    if (!row_tensors_same(t[i], t[2 + i]) && !row_tensors_apart(t[i], t[2 + i])) return MHLA_ERR_INVALID_ARG;
+    if (!row_tensors_apart(t[1 - i], t[2 + i])) return MHLA_ERR_INVALID_ARG;
+  }
+  if (!row_tensors_apart(t[2], t[3])) return MHLA_ERR_INVALID_ARG;
+  if (p->batch == 0 || p->tokens == 0 || p->heads + kv == 0) return MHLA_OK;
+  QkArgs a = args_of(p, table, k != nullptr, positions);
+  a.x[0] = q;
+  a.x[1] = k;
+  a.y[0] = q_out;
+  a.y[1] = k_out;
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
+  const int vec = vector_of(a.dim, a.half, p->style, (int)ops_elem(p->dtype), least_alignment(t, 4));
+  shape_rows(&a, vec, p->style);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return p->dtype == MHLA_DTYPE_BF16 ? dispatch<__nv_bfloat16>(a, p->style, vec, false, s)
+                                     : dispatch<float>(a, p->style, vec, false, s);
+}
+
+mhla_status mhla_qknorm_backward_workspace_bytes(const mhla_qknorm_params* p, size_t* bytes) {
+  using namespace mhla;
+  if (!bytes) return MHLA_ERR_INVALID_ARG;
+  const mhla_status st = check_params(p, nullptr);
+  if (st != MHLA_OK) return st;
+  *bytes = sizeof(float) * (size_t)most_ctas(p) * (size_t)p->head_dim;
+  return MHLA_OK;
+}
+
+mhla_status mhla_qknorm_backward(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                                 const void* q_weight, const void* k_weight, const void* positions,
+                                 const mhla_rotary_table* table, const mhla_qknorm_params* p, void* dq, void* dk,
+                                 float* dq_weight, float* dk_weight, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  using namespace mhla;
+  mhla_status st = check_params(p, table);
+  if (st != MHLA_OK) return st;
+  if (!k && any_rows(p, p->kv_heads) && (dk_out || dk || k_weight || dk_weight)) return MHLA_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int kv = k ? p->kv_heads : 0;
+  const RowTensor x[2] = {rows(q, p, p->heads, p->q), rows(k, p, kv, p->k)};
+  const RowTensor dy[2] = {rows(dq_out, p, p->heads, p->dq_out), rows(dk_out, p, kv, p->dk_out)};
+  const RowTensor dx[2] = {rows(dq, p, p->heads, p->q_out), rows(dk, p, kv, p->k_out)};
+  const bool sums = dq_weight || dk_weight;
+  size_t need = 0;
+  if (sums && (st = mhla_qknorm_backward_workspace_bytes(p, &need)) != MHLA_OK) return st;
+  const size_t we = ops_elem(p->weight_dtype);
+  const RowTensor side[3] = {flat_tensor(q_weight, q_weight ? p->head_dim : 0, we),
+                             flat_tensor(k_weight, k_weight ? p->head_dim : 0, we), positions_of(positions, p)};
+  const RowTensor more[3] = {flat_tensor(dq_weight, dq_weight ? p->head_dim : 0, 4),
+                             flat_tensor(dk_weight, dk_weight ? p->head_dim : 0, 4),
+                             flat_tensor(workspace, workspace ? (int64_t)need : 0, 1)};
+  const RowTensor* inputs[7] = {&x[0], &x[1], &dy[0], &dy[1], &side[0], &side[1], &side[2]};
+  const RowTensor* results[5] = {&dx[0], &dx[1], &more[0], &more[1], &more[2]};
+  for (const RowTensor* i : inputs)
+    if (!row_tensor_ok(*i, false)) return MHLA_ERR_INVALID_ARG;
+  for (int o = 0; o < 5; ++o) {
+    if (!row_tensor_ok(*results[o], true)) return MHLA_ERR_INVALID_ARG;
+    for (int i = 0; i < 7; ++i) {
+      const bool own = o < 2 && i < 4 && i % 2 == o;  // dq over dq_out or q
+      if (own && row_tensors_same(*inputs[i], *results[o])) continue;
+      if (!row_tensors_apart(*inputs[i], *results[o])) return MHLA_ERR_INVALID_ARG;
+    }
+    for (int i = o + 1; i < 5; ++i)
+      if (!row_tensors_apart(*results[i], *results[o])) return MHLA_ERR_INVALID_ARG;
+  }
+  QkArgs a = args_of(p, table, k != nullptr, positions);
+  const RowTensor all[6] = {x[0], x[1], dy[0], dy[1], dx[0], dx[1]};
+  const int vec = vector_of(a.dim, a.half, p->style, (int)ops_elem(p->dtype), least_alignment(all, 6));
+  shape_rows(&a, vec, p->style);
+  share_ctas(&a);
+  Scratch scratch;
+  if (sums && (st = scratch.take(workspace, workspace_bytes, need, s)) != MHLA_OK) return st;
+  a.x[0] = q;
+  a.x[1] = k;
+  a.dy[0] = dq_out;
+  a.dy[1] = dk_out;
+  a.y[0] = dq;
+  a.y[1] = dk;
+  a.w[0] = q_weight;
+  a.w[1] = k_weight;
+  a.partial = sums ? reinterpret_cast<float*>(scratch.ptr()) : nullptr;
+  if (a.ctas[0] + a.ctas[1] > 0)
+    st = p->dtype == MHLA_DTYPE_BF16 ? dispatch<__nv_bfloat16>(a, p->style, vec, true, s)
+                                     : dispatch<float>(a, p->style, vec, true, s);
+  if (st == MHLA_OK && sums) {
+    qknorm_reduce_kernel<<<dim3((unsigned)((a.dim + 31) / 32), 2), 1024, 0, s>>>(a.partial, a.ctas[0], a.ctas[1],
+                                                                                 a.dim, dq_weight, dk_weight);
+    st = launch_status();
+  }
+  return scratch.give_back(st);
+}
+
+}  // extern "C"

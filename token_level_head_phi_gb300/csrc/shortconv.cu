@@ -1,0 +1,502 @@
+// Short causal convolution of each channel, y_t = f(sum_j w_j x_{t-K+1+j} + b),
+// and its gradients: with dz_t = dout_t f'(z_t),
+//   dx_s = sum_j w_j dz_{s+K-1-j},  dw_j = sum_t dz_t x_{t-K+1+j},  db = sum_t dz_t.
+//
+// A thread takes a few neighbouring channels and walks over a segment of the
+// tokens with the last K rows in registers; the K - 1 rows before a segment
+// (and, backwards, behind it) are read again by its neighbour.  Bound: memory.
+#include "common.cuh"
+#include "ops.h"
+#include "pack.cuh"
+
+namespace mhla {
+namespace {
+
+constexpr int kVec = 4;       // channels of a thread
+constexpr int kThreads = 256;
+
+struct ConvArgs {
+  const void *x, *dout, *w, *bias, *state_in, *dstate_out;
+  void *out, *state_out, *dx, *dstate_in;
+  mhla_strides sx, so, sdo, sdx;
+  const int32_t* lengths;
+  float* partial;  // [rows][K + 1][D]
+  int B, N, D;
+  int w_f32, silu;
+  int vecs;            // of a row
+  int across, down;    // of a CTA: vectors and segments, powers of two
+  int across_shift;
+  int segments, seg;   // segments of a sequence, tokens of one
+  int whole;           // vectors in one access
+};
+
+__device__ __forceinline__ int length_of(const ConvArgs& p, int b) {
+  if (!p.lengths) return p.N;
+  const int n = p.lengths[b];
+  return n < 0 ? 0 : n > p.N ? p.N : n;
+}
+
+// A thread's channels, sequence and segment.
+struct Place {
+  int ch, n, b, first;
+  bool live;
+  __device__ __forceinline__ Place(const ConvArgs& p) {
+    const int vec = blockIdx.x * p.across + (threadIdx.x & (p.across - 1));
+    const int64_t at = (int64_t)blockIdx.y * p.down + (threadIdx.x >> p.across_shift);
+    b = (int)(at / p.segments);
+    first = (int)(at - (int64_t)b * p.segments) * p.seg;
+    ch = vec * kVec;
+    n = min(kVec, p.D - ch);
+    live = vec < p.vecs && b < p.B;
+  }
+};
+
+template <int K>
+__device__ __forceinline__ void load_weights(const ConvArgs& p, const Place& at, float (&w)[K][kVec],
+                                             float (&bias)[kVec]) {
+#pragma unroll
+  for (int c = 0; c < kVec; ++c) {
+    const bool in = at.live && c < at.n;
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[j][c] = in ? param_at(p.w, p.w_f32, (int64_t)(at.ch + c) * K + j) : 0.f;
+    bias[c] = in && p.bias ? param_at(p.bias, p.w_f32, at.ch + c) : 0.f;
+  }
+}
+
+// Row t of x, rows before the first token from the incoming state, zeros past
+// the length.
+template <typename T, int K>
+__device__ __forceinline__ void load_row(const ConvArgs& p, const Place& at, int t, int len, Pack<T, kVec>* r) {
+  if (t >= len || !at.live) {
+    r->zero();
+  } else if (t >= 0) {
+    r->load(static_cast<const T*>(p.x) + at.b * p.sx.batch + t * p.sx.token + at.ch, p.whole && at.n == kVec, at.n);
+  } else if (p.state_in) {
+    r->load(static_cast<const T*>(p.state_in) + ((int64_t)at.b * (K - 1) + t + K - 1) * p.D + at.ch, false, at.n);
+  } else {
+    r->zero();
+  }
+}
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const __grid_constant__ ConvArgs p) {
+  constexpr int U = 4;  // rows in flight
+  const Place at(p);
+  if (!at.live) return;
+  const int len = length_of(p, at.b), last = min(at.first + p.seg, p.N);
+  float w[K][kVec], bias[kVec];
+  load_weights<K>(p, at, w, bias);
+  float win[K - 1][kVec];  // rows t - K + 1 .. t - 1
+  Pack<T, kVec> r;
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) {
+    load_row<T, K>(p, at, at.first - (K - 1) + j, len, &r);
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) win[j][c] = r.f(c);
+  }
+  T* out = static_cast<T*>(p.out) + at.b * p.so.batch + at.ch;
+  const bool whole = p.whole && at.n == kVec;
+  for (int t0 = at.first; t0 < last; t0 += U) {
+    Pack<T, kVec> row[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_row<T, K>(p, at, t0 + u, len, &row[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = t0 + u;
+      Pack<T, kVec> o;
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) {
+        const float x = row[u].f(c);
+        float z = fmaf(w[K - 1][c], x, bias[c]);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
+#pragma unroll
+        for (int j = 0; j + 1 < K - 1; ++j) win[j][c] = win[j + 1][c];
+        win[K - 2][c] = x;
+        if (p.silu) z = z * rcp(1.f + ex2(-z * kLog2e));
+        o.v[c] = from_f32<T>(t < len ? z : 0.f);
+      }
+      if (t < last) o.store(out + t * p.so.token, whole, at.n);
+    }
+  }
+  if (p.state_out && at.first == 0) {
+    // the same thread that read state_in, which this may be
+    Pack<T, kVec> keep[K - 1];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) load_row<T, K>(p, at, len - (K - 1) + j, len, &keep[j]);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+      keep[j].store(static_cast<T*>(p.state_out) + ((int64_t)at.b * (K - 1) + j) * p.D + at.ch, false, at.n);
+  }
+}
+
+template <typename T, int K>
+__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const __grid_constant__ ConvArgs p) {
+  constexpr int U = 4;  // rows in flight
+  extern __shared__ float sums[];  // [down][(K + 1) * kVec][across]
+  const Place at(p);
+  float dw[K + 1][kVec];
+#pragma unroll
+  for (int j = 0; j <= K; ++j)
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) dw[j][c] = 0.f;
+  if (at.live) {
+    const int len = length_of(p, at.b), last = min(at.first + p.seg, p.N);
+    float w[K][kVec], bias[kVec];
+    load_weights<K>(p, at, w, bias);
+    float win[K - 1][kVec], dz[K - 1][kVec];  // rows t - K + 1 .. t - 1 of x and of dL/dz
+    Pack<T, kVec> r;
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) {
+      load_row<T, K>(p, at, at.first - (K - 1) + j, len, &r);
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) {
+        win[j][c] = r.f(c);
+        dz[j][c] = 0.f;
+      }
+    }
+    const bool whole = p.whole && at.n == kVec;
+    const T* dout = static_cast<const T*>(p.dout) + at.b * p.sdo.batch + at.ch;
+    T* dx = static_cast<T*>(p.dx) + at.b * p.sdx.batch + at.ch;
+    // Rows s < first belong to the segment before, but the first one's are the
+    // incoming state's.
+    for (int t0 = at.first; t0 < last + K - 1; t0 += U) {
+      Pack<T, kVec> row[U], rd[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        load_row<T, K>(p, at, t0 + u, t0 + u < last + K - 1 ? len : 0, &row[u]);
+        if (t0 + u < len && t0 + u < last + K - 1)
+          rd[u].load(dout + (t0 + u) * p.sdo.token, whole, at.n);
+        else
+          rd[u].zero();
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int t = t0 + u, s = t - (K - 1), extra = s - (len - (K - 1));
+        float d[kVec], o[kVec];
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) {
+          const float x = row[u].f(c);
+          d[c] = rd[u].f(c);
+          if (p.silu) {
+            float z = fmaf(w[K - 1][c], x, bias[c]);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
+            const float q = rcp(1.f + ex2(-z * kLog2e));
+            const float slope = q * fmaf(z, 1.f - q, 1.f);
+            d[c] = t < len ? d[c] * slope : 0.f;
+          }
+          if (t < last) {
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) dw[j][c] = fmaf(d[c], win[j][c], dw[j][c]);
+            dw[K - 1][c] = fmaf(d[c], x, dw[K - 1][c]);
+            dw[K][c] += d[c];
+          }
+          // dz_{s + i} meets w_{K - 1 - i}; d is dz_{s + K - 1}
+          o[c] = w[0][c] * d[c];
+#pragma unroll
+          for (int i = 0; i < K - 1; ++i) o[c] = fmaf(w[K - 1 - i][c], dz[i][c], o[c]);
+#pragma unroll
+          for (int j = 0; j + 1 < K - 1; ++j) {
+            win[j][c] = win[j + 1][c];
+            dz[j][c] = dz[j + 1][c];
+          }
+          win[K - 2][c] = x;
+          dz[K - 2][c] = d[c];
+        }
+        if (t >= last + K - 1 || s < at.first - (at.first == 0 ? K - 1 : 0)) continue;
+        if (p.dstate_out && extra >= 0 && extra < K - 1) {  // the row went into the outgoing state
+          r.load(static_cast<const T*>(p.dstate_out) + ((int64_t)at.b * (K - 1) + extra) * p.D + at.ch, false, at.n);
+#pragma unroll
+          for (int c = 0; c < kVec; ++c) o[c] += r.f(c);
+        }
+#pragma unroll
+        for (int c = 0; c < kVec; ++c) r.v[c] = from_f32<T>(s < len ? o[c] : 0.f);
+        if (s >= 0)
+          r.store(dx + s * p.sdx.token, whole, at.n);
+        else if (p.dstate_in)
+          r.store(static_cast<T*>(p.dstate_in) + ((int64_t)at.b * (K - 1) + s + K - 1) * p.D + at.ch, false, at.n);
+      }
+    }
+  }
+  if (!p.partial) return;
+  const int a = threadIdx.x & (p.across - 1), d = threadIdx.x >> p.across_shift;
+  constexpr int kSums = (K + 1) * kVec;
+#pragma unroll
+  for (int j = 0; j <= K; ++j)
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) sums[(d * kSums + j * kVec + c) * p.across + a] = dw[j][c];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kSums * p.across; i += kThreads) {
+    const int vec = blockIdx.x * p.across + i % p.across, j = i / p.across / kVec, c = i / p.across % kVec;
+    if (vec * kVec + c >= p.D) continue;
+    float s = 0.f;
+    for (int v = 0; v < p.down; ++v) s += sums[v * kSums * p.across + i];
+    p.partial[((int64_t)blockIdx.y * (K + 1) + j) * p.D + vec * kVec + c] = s;
+  }
+}
+
+// Adds the partial rows in order: 32 channels per CTA, 32 threads to one.
+__global__ void __launch_bounds__(1024) conv_reduce_kernel(const float* partial, int rows, int K, int D, float* dweight,
+                                                           float* dbias) {
+  __shared__ float sh[32][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx, j = blockIdx.y;
+  float s = 0.f;
+  if (c < D)
+    for (int r = ty; r < rows; r += 32) s += partial[((int64_t)r * (K + 1) + j) * D + c];
+  sh[ty][tx] = s;
+  __syncthreads();
+  if (ty == 0 && c < D) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += sh[i][tx];
+    if (j < K) {
+      if (dweight) dweight[(int64_t)c * K + j] = t;
+    } else if (dbias) {
+      dbias[c] = t;
+    }
+  }
+}
+
+// One token of every sequence.
+template <typename T, int K>
+__global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ ConvArgs p) {
+  const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+  if (i >= (int64_t)p.B * p.D) return;
+  const int64_t b = i / p.D;
+  const int ch = (int)(i - b * p.D);
+  const T x = static_cast<const T*>(p.x)[b * p.sx.batch + ch];
+  T row[K];
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j)
+    row[j] = p.state_in ? static_cast<const T*>(p.state_in)[(b * (K - 1) + j) * p.D + ch] : from_f32<T>(0.f);
+  row[K - 1] = x;
+  // the forward kernel's order, so that tokens give the same bits either way
+  float z = fmaf(param_at(p.w, p.w_f32, (int64_t)ch * K + K - 1), to_f32(x), p.bias ? param_at(p.bias, p.w_f32, ch) : 0.f);
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) z = fmaf(param_at(p.w, p.w_f32, (int64_t)ch * K + j), to_f32(row[j]), z);
+  if (p.silu) z = z * rcp(1.f + ex2(-z * kLog2e));
+  static_cast<T*>(p.out)[b * p.so.batch + ch] = from_f32<T>(z);
+  if (p.state_out)
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j) static_cast<T*>(p.state_out)[(b * (K - 1) + j) * p.D + ch] = row[j + 1];
+}
+
+// ---------------------------------------------------------------- dispatch
+
+enum { kForward, kBackward, kStep };
+
+// Threads of a CTA across the channels and down the tokens, and the tokens of
+// a segment: as long as possible (its neighbours read its borders again), but
+// with enough segments to fill the GPU.
+void shape(ConvArgs* p, int what) {
+  p->vecs = (p->D + kVec - 1) / kVec;
+  p->across = 1;
+  p->across_shift = 0;
+  while (p->across < 32 && p->across < p->vecs) {
+    p->across *= 2;
+    ++p->across_shift;
+  }
+  p->down = kThreads / p->across;
+  const int64_t lines = (int64_t)p->B * p->vecs, want = (int64_t)kOpsSms * (what == kForward ? 2048 : 1024);
+  int seg = 64;
+  while (seg > 8 && lines * ((p->N + seg - 1) / seg) < want) seg /= 2;
+  p->seg = seg;
+  p->segments = p->N > 0 ? (p->N + seg - 1) / seg : 1;
+}
+
+int64_t grid_down(const ConvArgs& p) { return ((int64_t)p.B * p.segments + p.down - 1) / p.down; }
+
+template <typename T, int K>
+mhla_status launch(const ConvArgs& a, int what, cudaStream_t s) {
+  if (what == kStep) {
+    const int64_t blocks = ((int64_t)a.B * a.D + 127) / 128;
+    if (blocks > 0x7fffffff) return MHLA_ERR_UNSUPPORTED;
+    conv_step_kernel<T, K><<<(unsigned)blocks, 128, 0, s>>>(a);
+    return launch_status();
+  }
+  const dim3 grid((unsigned)((a.vecs + a.across - 1) / a.across), (unsigned)grid_down(a));
+  if (what == kForward) {
+    conv_fwd_kernel<T, K><<<grid, kThreads, 0, s>>>(a);
+  } else {
+    const size_t smem = a.partial ? sizeof(float) * (K + 1) * kVec * kThreads : 0;
+    conv_bwd_kernel<T, K><<<grid, kThreads, smem, s>>>(a);
+  }
+  return launch_status();
+}
+
+template <typename T>
+mhla_status with_taps(const ConvArgs& a, int taps, int what, cudaStream_t s) {
+  if (taps == 2) return launch<T, 2>(a, what, s);
+  if (taps == 3) return launch<T, 3>(a, what, s);
+  return launch<T, 4>(a, what, s);
+}
+
+mhla_status dispatch(const ConvArgs& a, const mhla_shortconv_params* p, int what, cudaStream_t s) {
+  if (what != kStep && grid_down(a) > 65535) return MHLA_ERR_UNSUPPORTED;
+  return p->dtype == MHLA_DTYPE_BF16 ? with_taps<__nv_bfloat16>(a, p->taps, what, s)
+                                     : with_taps<float>(a, p->taps, what, s);
+}
+
+mhla_status check_params(const mhla_shortconv_params* p) {
+  if (!p || p->batch < 0 || p->tokens < 0 || p->width < 0 || !ops_dtype_ok(p->dtype) || !ops_dtype_ok(p->weight_dtype))
+    return MHLA_ERR_INVALID_ARG;
+  if (p->activation != MHLA_ACTIVATION_NONE && p->activation != MHLA_ACTIVATION_SILU) return MHLA_ERR_INVALID_ARG;
+  if (p->taps < 1) return MHLA_ERR_INVALID_ARG;
+  if (p->taps < 2 || p->taps > 4 || p->tokens > 0x7fffff00 || p->width > 0x7fffff00) return MHLA_ERR_UNSUPPORTED;
+  return MHLA_OK;
+}
+
+RowTensor rows(const void* ptr, const mhla_shortconv_params* p, const mhla_strides& s) {
+  return row_tensor(ptr, p->batch, 1, p->tokens, s, p->width, ops_elem(p->dtype));
+}
+// a state, contiguous, or NULL
+RowTensor state_of(const void* ptr, const mhla_shortconv_params* p) {
+  return flat_tensor(ptr, ptr ? (int64_t)p->batch * (p->taps - 1) * p->width : 0, ops_elem(p->dtype));
+}
+RowTensor param_of(const void* ptr, int64_t n, int dtype) { return flat_tensor(ptr, ptr ? n : 0, ops_elem(dtype)); }
+
+// Inputs may share memory, results nothing with one another or with an input
+// but out[same_out] with in[same_in].
+bool apart(const RowTensor* in, int n_in, const RowTensor* out, int n_out, int same_in, int same_out) {
+  for (int i = 0; i < n_in; ++i)
+    if (!row_tensor_ok(in[i], false)) return false;
+  for (int o = 0; o < n_out; ++o) {
+    if (!row_tensor_ok(out[o], true)) return false;
+    for (int i = 0; i < n_in; ++i) {
+      if (i == same_in && o == same_out && row_tensors_same(in[i], out[o])) continue;
+      if (!row_tensors_apart(in[i], out[o])) return false;
+    }
+    for (int q = o + 1; q < n_out; ++q)
+      if (!row_tensors_apart(out[o], out[q])) return false;
+  }
+  return true;
+}
+
+int whole_vectors(const RowTensor* t, int n) {
+  for (int i = 0; i < n; ++i)
+    if (!t[i].empty() && row_alignment(t[i], 16) < kVec * (int)t[i].elem) return 0;
+  return 1;
+}
+
+ConvArgs args_of(const mhla_shortconv_params* p, const void* x, const void* weight, const void* bias,
+                 const int32_t* lengths, const void* state_in) {
+  ConvArgs a = {};
+  a.x = x;
+  a.w = weight;
+  a.bias = bias;
+  a.lengths = lengths;
+  a.state_in = state_in;
+  a.sx = p->x;
+  a.B = p->batch;
+  a.N = p->tokens;
+  a.D = p->width;
+  a.w_f32 = p->weight_dtype == MHLA_DTYPE_F32;
+  a.silu = p->activation == MHLA_ACTIVATION_SILU;
+  return a;
+}
+
+}  // namespace
+}  // namespace mhla
+
+extern "C" {
+
+mhla_status mhla_shortconv_forward(const void* x, const void* weight, const void* bias, const int32_t* lengths,
+                                   const void* state_in, const mhla_shortconv_params* p, void* out, void* state_out,
+                                   void* stream) {
+  using namespace mhla;
+  const mhla_status st = check_params(p);
+  if (st != MHLA_OK) return st;
+  if (!weight && p->width) return MHLA_ERR_INVALID_ARG;
+  const RowTensor in[5] = {rows(x, p, p->x), param_of(weight, (int64_t)p->width * p->taps, p->weight_dtype),
+                           param_of(bias, p->width, p->weight_dtype), flat_tensor(lengths, lengths ? p->batch : 0, 4),
+                           state_of(state_in, p)};
+  const RowTensor res[2] = {rows(out, p, p->out), state_of(state_out, p)};
+  if (!apart(in, 5, res, 2, 4, 1)) return MHLA_ERR_INVALID_ARG;
+  if (p->batch == 0 || p->width == 0) return MHLA_OK;
+  ConvArgs a = args_of(p, x, weight, bias, lengths, state_in);
+  a.out = out;
+  a.so = p->out;
+  a.state_out = state_out;
+  a.whole = whole_vectors(in, 1) && whole_vectors(res, 1);
+  shape(&a, kForward);
+  return dispatch(a, p, kForward, static_cast<cudaStream_t>(stream));
+}
+
+mhla_status mhla_shortconv_backward_workspace_bytes(const mhla_shortconv_params* p, size_t* bytes) {
+  using namespace mhla;
+  if (!bytes) return MHLA_ERR_INVALID_ARG;
+  const mhla_status st = check_params(p);
+  if (st != MHLA_OK) return st;
+  ConvArgs a = args_of(p, nullptr, nullptr, nullptr, nullptr, nullptr);
+  shape(&a, kBackward);
+  *bytes = p->batch && p->width ? sizeof(float) * (size_t)grid_down(a) * (p->taps + 1) * (size_t)p->width : 0;
+  return MHLA_OK;
+}
+
+mhla_status mhla_shortconv_backward(const void* x, const void* weight, const void* bias, const int32_t* lengths,
+                                    const void* state_in, const void* dout, const void* dstate_out,
+                                    const mhla_shortconv_params* p, void* dx, float* dweight, float* dbias,
+                                    void* dstate_in, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace mhla;
+  mhla_status st = check_params(p);
+  if (st != MHLA_OK) return st;
+  if (!weight && p->width) return MHLA_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool sums = dweight || dbias;
+  size_t need = 0;
+  if (sums && (st = mhla_shortconv_backward_workspace_bytes(p, &need)) != MHLA_OK) return st;
+  const RowTensor in[7] = {rows(x, p, p->x), rows(dout, p, p->dout),
+                           param_of(weight, (int64_t)p->width * p->taps, p->weight_dtype),
+                           param_of(bias, p->width, p->weight_dtype), flat_tensor(lengths, lengths ? p->batch : 0, 4),
+                           state_of(state_in, p), state_of(dstate_out, p)};
+  const RowTensor res[5] = {rows(dx, p, p->dx), param_of(dweight, (int64_t)p->width * p->taps, MHLA_DTYPE_F32),
+                            param_of(dbias, p->width, MHLA_DTYPE_F32), state_of(dstate_in, p),
+                            flat_tensor(workspace, workspace ? (int64_t)need : 0, 1)};
+  if (!apart(in, 7, res, 5, -1, -1)) return MHLA_ERR_INVALID_ARG;
+  if (p->batch == 0 || p->width == 0) {  // empty sums
+    cudaError_t e = cudaSuccess;
+    if (dweight && p->width) e = cudaMemsetAsync(dweight, 0, sizeof(float) * (size_t)p->width * p->taps, s);
+    if (e == cudaSuccess && dbias && p->width) e = cudaMemsetAsync(dbias, 0, sizeof(float) * (size_t)p->width, s);
+    return e == cudaSuccess ? MHLA_OK : record_cuda_error(e);
+  }
+  Scratch scratch;
+  if (sums && (st = scratch.take(workspace, workspace_bytes, need, s)) != MHLA_OK) return st;
+  ConvArgs a = args_of(p, x, weight, bias, lengths, state_in);
+  a.dout = dout;
+  a.sdo = p->dout;
+  a.dstate_out = dstate_out;
+  a.dx = dx;
+  a.sdx = p->dx;
+  a.dstate_in = dstate_in;
+  a.partial = sums ? reinterpret_cast<float*>(scratch.ptr()) : nullptr;
+  a.whole = whole_vectors(in, 2) && whole_vectors(res, 1);
+  shape(&a, kBackward);
+  st = dispatch(a, p, kBackward, s);
+  if (st == MHLA_OK && sums) {
+    conv_reduce_kernel<<<dim3((unsigned)((p->width + 31) / 32), (unsigned)(p->taps + 1)), 1024, 0, s>>>(
+        a.partial, (int)grid_down(a), p->taps, p->width, dweight, dbias);
+    st = launch_status();
+  }
+  return scratch.give_back(st);
+}
+
+mhla_status mhla_shortconv_step(const void* x, const void* weight, const void* bias, const void* state_in,
+                                const mhla_shortconv_params* p, void* out, void* state_out, void* stream) {
+  using namespace mhla;
+  const mhla_status st = check_params(p);
+  if (st != MHLA_OK) return st;
+  if (p->tokens != 1 || (!weight && p->width)) return MHLA_ERR_INVALID_ARG;
+  const RowTensor in[4] = {rows(x, p, p->x), param_of(weight, (int64_t)p->width * p->taps, p->weight_dtype),
+                           param_of(bias, p->width, p->weight_dtype), state_of(state_in, p)};
+  const RowTensor res[2] = {rows(out, p, p->out), state_of(state_out, p)};
+  if (!apart(in, 4, res, 2, 3, 1)) return MHLA_ERR_INVALID_ARG;
+  if (p->batch == 0 || p->width == 0) return MHLA_OK;
+  ConvArgs a = args_of(p, x, weight, bias, nullptr, state_in);
+  a.out = out;
+  a.so = p->out;
+  a.state_out = state_out;
+  return dispatch(a, p, kStep, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
