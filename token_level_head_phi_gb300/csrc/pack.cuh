@@ -111,4 +111,26 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 }
 __device__ __forceinline__ uint64_t splat(float a) { return pair(a, a); }
 
+// Elements 2 i and 2 i + 1 of a pack.
+template <int N>
+__device__ __forceinline__ uint64_t pair_of(const Pack<__nv_bfloat16, N>& x, int i) {
+  const uint32_t v = reinterpret_cast<const uint32_t*>(x.v)[i];
+  return pair(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+template <int N>
+__device__ __forceinline__ uint64_t pair_of(const Pack<float, N>& x, int i) {
+  return pair(x.v[2 * i], x.v[2 * i + 1]);
+}
+template <int N>
+__device__ __forceinline__ void put_pair(Pack<__nv_bfloat16, N>* x, int i, uint64_t v) {
+  const float2 f = unpair(v);
+  reinterpret_cast<__nv_bfloat162*>(x->v)[i] = __floats2bfloat162_rn(f.x, f.y);
+}
+template <int N>
+__device__ __forceinline__ void put_pair(Pack<float, N>* x, int i, uint64_t v) {
+  const float2 f = unpair(v);
+  x->v[2 * i] = f.x;
+  x->v[2 * i + 1] = f.y;
+}
+
 }  // namespace mhla

@@ -62,37 +62,160 @@ __device__ __forceinline__ void columns(const QkArgs& a, int slot, int* lo, int*
   *hi = *lo + VEC;
 }
 
-// Cosines and sines of a slot's pairs; 1 and 0 for entries that are not
-// rotated.
+// A slot's 2 VEC values, as pairs of neighbours where there are any.
 template <int VEC, bool ACROSS>
-__device__ __forceinline__ void turns_of(const QkArgs& a, const uint64_t* turns, int64_t pos, int lo, float sign,
-                                         float (&cs)[VEC], float (&sn)[VEC]) {
-  const int first = ACROSS && !a.adjacent ? lo : lo / 2;  // pair of the first entry
-  const bool rotated = ACROSS && !a.adjacent ? lo < a.half : true;
+struct Values {
+  static constexpr bool kPairs = ACROSS && VEC > 1;
+  uint64_t p[kPairs ? VEC : 1];    // the first vector's pairs, then the second's
+  float f[kPairs ? 1 : 2 * VEC];
+
+  template <typename T>
+  __device__ __forceinline__ void read(const Pack<T, VEC> (&x)[2]) {
+    if constexpr (kPairs) {
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-    if (rotated && first + i < a.half) {
-      const uint64_t phase = (uint64_t)pos * turns[first + i];
-      sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &sn[i], &cs[i]);
-      cs[i] *= a.amp;
-      sn[i] *= a.amp * sign;
+      for (int i = 0; i < VEC; ++i) p[i] = pair_of(x[i >= VEC / 2], i % (VEC / 2));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * VEC; ++i) f[i] = x[i / VEC].f(i % VEC);
     }
   }
-}
+  template <typename T>
+  __device__ __forceinline__ void write(Pack<T, VEC> (&x)[2]) const {
+    if constexpr (kPairs) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) put_pair(&x[i >= VEC / 2], i % (VEC / 2), p[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * VEC; ++i) x[i / VEC].v[i % VEC] = from_f32<T>(f[i]);
+    }
+  }
+  // entries of the first, then of the second vector
+  __device__ __forceinline__ void set(const float (&v)[2 * VEC]) {
+    if constexpr (kPairs) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) p[i] = pair(v[2 * i], v[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * VEC; ++i) f[i] = v[i];
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[2 * VEC]) const {
+#pragma unroll
+    for (int i = 0; i < 2 * VEC; ++i) {
+      if constexpr (kPairs)
+        v[i] = i % 2 ? unpair(p[i / 2]).y : unpair(p[i / 2]).x;
+      else
+        v[i] = f[i];
+    }
+  }
+  __device__ __forceinline__ void fill(float v) {
+    if constexpr (kPairs) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) p[i] = splat(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * VEC; ++i) f[i] = v;
+    }
+  }
+  // this = x y, x y + this, this s
+  __device__ __forceinline__ void product(const Values& x, const Values& y) {
+    if constexpr (kPairs) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) p[i] = mul2(x.p[i], y.p[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * VEC; ++i) f[i] = x.f[i] * y.f[i];
+    }
+  }
+  __device__ __forceinline__ void add_product(const Values& x, const Values& y) {
+    if constexpr (kPairs) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) p[i] = fma2(x.p[i], y.p[i], p[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * VEC; ++i) f[i] = fmaf(x.f[i], y.f[i], f[i]);
+    }
+  }
+  __device__ __forceinline__ void scale(float s) {
+    if constexpr (kPairs) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) p[i] = mul2(p[i], splat(s));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * VEC; ++i) f[i] *= s;
+    }
+  }
+  // this = a this + b x
+  __device__ __forceinline__ void combine(float a, float b, const Values& x) {
+    if constexpr (kPairs) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) p[i] = fma2(x.p[i], splat(b), mul2(p[i], splat(a)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * VEC; ++i) f[i] = fmaf(x.f[i], b, f[i] * a);
+    }
+  }
+  __device__ __forceinline__ float dot(const Values& x) const {
+    if constexpr (kPairs) {
+      uint64_t s = mul2(p[0], x.p[0]);
+#pragma unroll
+      for (int i = 1; i < VEC; ++i) s = fma2(p[i], x.p[i], s);
+      const float2 t = unpair(s);
+      return t.x + t.y;
+    } else {
+      float s = f[0] * x.f[0];
+#pragma unroll
+      for (int i = 1; i < 2 * VEC; ++i) s = fmaf(f[i], x.f[i], s);
+      return s;
+    }
+  }
+  // Rotates the pairs: (a, b) -> (c_a a + s_b b, s_a a + c_b b), `c` and `s` laid
+  // out as the values that they multiply.
+  __device__ __forceinline__ void turn(const Values& c, const Values& s) {
+    if constexpr (kPairs) {
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) {
+        const uint64_t a = p[i], b = p[i + VEC / 2];
+        p[i] = fma2(a, c.p[i], mul2(b, s.p[i + VEC / 2]));
+        p[i + VEC / 2] = fma2(b, c.p[i + VEC / 2], mul2(a, s.p[i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const int j = ACROSS ? i : 2 * i, k = ACROSS ? i + VEC : 2 * i + 1;
+        const float a = f[j], b = f[k];
+        f[j] = fmaf(a, c.f[j], b * s.f[k]);
+        f[k] = fmaf(b, c.f[k], a * s.f[j]);
+      }
+    }
+  }
+};
 
-// Rotates a slot's values in place.
+// What a slot's values are multiplied with by Values::turn: cosines (in `c`) and
+// sines (in `s`, the second one's with the sign turned, so that turn adds them)
+// times the values' weights; 1 and 0 where nothing is rotated.
 template <int VEC, bool ACROSS>
-__device__ __forceinline__ void turn(float (&v)[2][VEC], const float (&cs)[VEC], const float (&sn)[VEC]) {
+__device__ __forceinline__ void turns_of(const QkArgs& a, const uint64_t* turns, int64_t pos, int lo, float sign,
+                                         Values<VEC, ACROSS>* c, Values<VEC, ACROSS>* s) {
+  const int first = ACROSS && !a.adjacent ? lo : lo / 2;  // pair of the first entry
+  const bool rotated = ACROSS && !a.adjacent ? lo < a.half : true;
+  float fc[2 * VEC], fs[2 * VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
-    float& p = ACROSS ? v[0][i] : v[2 * i / VEC][2 * i % VEC];
-    float& q = ACROSS ? v[1][i] : v[(2 * i + 1) / VEC][(2 * i + 1) % VEC];
-    const float x = p, y = q;
-    p = x * cs[i] - y * sn[i];
-    q = x * sn[i] + y * cs[i];
+    float cs = 1.f, sn = 0.f;
+    if (rotated && first + i < a.half) {
+      const uint64_t phase = (uint64_t)pos * turns[first + i];
+      sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &sn, &cs);
+      cs *= a.amp;
+      sn *= a.amp * sign;
+    }
+    const int j = ACROSS ? i : 2 * i, k = ACROSS ? i + VEC : 2 * i + 1;
+    fc[j] = fc[k] = cs;
+    fs[j] = sn;
+    fs[k] = -sn;
   }
+  c->set(fc);
+  s->set(fs);
 }
 
 __device__ __forceinline__ int64_t position_of(const QkArgs& a, int64_t b, int t) {
@@ -101,9 +224,23 @@ __device__ __forceinline__ int64_t position_of(const QkArgs& a, int64_t b, int t
   return a.pos64 ? static_cast<const int64_t*>(a.positions)[at] : static_cast<const int32_t*>(a.positions)[at];
 }
 
+template <int VEC, bool ACROSS>
+__device__ __forceinline__ void weights_of(const QkArgs& a, int which, const int (&col)[2], const bool (&in)[2],
+                                           Values<VEC, ACROSS>* w) {
+  float f[2 * VEC];
+#pragma unroll
+  for (int i = 0; i < 2 * VEC; ++i)
+    f[i] = a.w[which] && in[i / VEC] ? param_at(a.w[which], a.w_f32, col[i / VEC] + i % VEC) : 1.f;
+  w->set(f);
+}
+
+// CTAs that an SM holds.
+constexpr int kFwdResident = 2, kBwdResident = 2;
+
 template <typename T, int VEC, bool ACROSS, int E>
-__global__ void __launch_bounds__(256) qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
+__global__ void __launch_bounds__(256, kFwdResident) qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
   constexpr int R = E > 1 ? 2 : 4;  // rows in flight
+  using V = Values<VEC, ACROSS>;
   __shared__ uint64_t turns[MHLA_ROTARY_MAX_PAIRS];
   for (int i = threadIdx.x; i < a.half; i += blockDim.x) turns[i] = a.table.turns[i];
   __syncthreads();
@@ -115,32 +252,33 @@ __global__ void __launch_bounds__(256) qknorm_fwd_kernel(const __grid_constant__
   const int64_t pos = position_of(a, b, t);
   int col[E][2];
   bool in[E][2];
-  float cs[E][VEC], sn[E][VEC];
+  V cs[E], sn[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int slot = lane + e * a.group;
     columns<VEC, ACROSS>(a, slot, &col[e][0], &col[e][1]);
-    turns_of<VEC, ACROSS>(a, turns, pos, col[e][0], 1.f, cs[e], sn[e]);
+    turns_of<VEC, ACROSS>(a, turns, pos, col[e][0], 1.f, &cs[e], &sn[e]);
 #pragma unroll
     for (int k = 0; k < 2; ++k) in[e][k] = live && slot < a.slots && col[e][k] < a.dim;
   }
   const int first = blockIdx.y * a.heads_per_thread, last = min(first + a.heads_per_thread, a.heads[0] + a.heads[1]);
-#pragma unroll
+#pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     int h = max(first - (which ? a.heads[0] : 0), 0);
     const int end = which ? last - a.heads[0] : min(last, a.heads[0]);
     if (h >= end) continue;  // the same for the whole grid row
-    float w[E][2][VEC];
+    V c[E], s[E];  // with the weights
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          w[e][k][i] = a.w[which] && in[e][k] ? param_at(a.w[which], a.w_f32, col[e][k] + i) : 1.f;
-    const T* src = static_cast<const T*>(a.x[which]) + b * a.sx[which].batch + t * a.sx[which].token;
-    T* dst = static_cast<T*>(a.y[which]) + b * a.sy[which].batch + t * a.sy[which].token;
-    for (; h < end; h += R) {
+    for (int e = 0; e < E; ++e) {
+      V w;
+      weights_of(a, which, col[e], in[e], &w);
+      c[e].product(cs[e], w);
+      s[e].product(sn[e], w);
+    }
+    const int64_t xh = a.sx[which].head, yh = a.sy[which].head;
+    const T* src = static_cast<const T*>(a.x[which]) + b * a.sx[which].batch + t * a.sx[which].token + h * xh;
+    T* dst = static_cast<T*>(a.y[which]) + b * a.sy[which].batch + t * a.sy[which].token + h * yh;
+    for (; h < end; h += R, src += R * xh, dst += R * yh) {
       Pack<T, VEC> raw[R][E][2];
 #pragma unroll
       for (int r = 0; r < R; ++r)
@@ -149,7 +287,7 @@ __global__ void __launch_bounds__(256) qknorm_fwd_kernel(const __grid_constant__
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if (in[e][k] && h + r < end)
-              raw[r][e][k].load(src + (h + r) * a.sx[which].head + col[e][k], true);
+              raw[r][e][k].load(src + r * xh + col[e][k], true);
             else
               raw[r][e][k].zero();
       float sum[R];
@@ -157,34 +295,30 @@ __global__ void __launch_bounds__(256) qknorm_fwd_kernel(const __grid_constant__
       for (int r = 0; r < R; ++r) {
         sum[r] = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) sum[r] = fmaf(raw[r][e][k].f(i), raw[r][e][k].f(i), sum[r]);
+        for (int e = 0; e < E; ++e) {
+          V v;
+          v.read(raw[r][e]);
+          sum[r] += v.dot(v);
+        }
       }
       for (int o = a.group / 2; o > 0; o >>= 1)
 #pragma unroll
         for (int r = 0; r < R; ++r) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
+        if (h + r >= end) break;  // the same for all lanes
         const float rstd = rsqrtf(fmaf(sum[r], a.inv_dim, a.eps));
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          float v[2][VEC];
+          V v;
+          v.read(raw[r][e]);
+          v.scale(rstd);
+          v.turn(c[e], s[e]);
+          Pack<T, VEC> o[2];
+          v.write(o);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[k][i] = raw[r][e][k].f(i) * rstd * w[e][k][i];
-          turn<VEC, ACROSS>(v, cs[e], sn[e]);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (in[e][k] && h + r < end) {
-              Pack<T, VEC> o;
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) o.v[i] = from_f32<T>(v[k][i]);
-              o.store(dst + (h + r) * a.sy[which].head + col[e][k], true);
-            }
+            if (in[e][k]) o[k].store(dst + r * yh + col[e][k], true);
         }
       }
     }
@@ -194,8 +328,9 @@ __global__ void __launch_bounds__(256) qknorm_fwd_kernel(const __grid_constant__
 // CTAs take the tokens in turn, those below ctas[0] q's rows and the others
 // k's, and keep the sums of dw of their columns in registers.
 template <typename T, int VEC, bool ACROSS, int E>
-__global__ void __launch_bounds__(256) qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
-  constexpr int R = E > 1 ? 1 : 2;
+__global__ void __launch_bounds__(256, kBwdResident) qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int R = E * VEC > 4 ? 1 : 2;  // rows of a step; the next step's are on their way
+  using V = Values<VEC, ACROSS>;
   __shared__ uint64_t turns[MHLA_ROTARY_MAX_PAIRS];
   __shared__ float sums[8][kMaxDim];
   for (int i = threadIdx.x; i < a.half; i += blockDim.x) turns[i] = a.table.turns[i];
@@ -205,37 +340,28 @@ __global__ void __launch_bounds__(256) qknorm_bwd_kernel(const __grid_constant__
   const int lane = threadIdx.x & (a.group - 1), per = blockDim.x >> a.lanes_shift;
   int col[E][2];
   bool in[E][2];
-  float w[E][2][VEC], dw[E][2][VEC];
+  V w[E], dw[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int slot = lane + e * a.group;
     columns<VEC, ACROSS>(a, slot, &col[e][0], &col[e][1]);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      in[e][k] = slot < a.slots && col[e][k] < a.dim;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        w[e][k][i] = a.w[which] && in[e][k] ? param_at(a.w[which], a.w_f32, col[e][k] + i) : 1.f;
-        dw[e][k][i] = 0.f;
-      }
-    }
+    for (int k = 0; k < 2; ++k) in[e][k] = slot < a.slots && col[e][k] < a.dim;
+    weights_of(a, which, col[e], in[e], &w[e]);
+    dw[e].fill(0.f);
   }
-  const int64_t all = (int64_t)a.batch * a.tokens;
+  const int64_t all = (int64_t)a.batch * a.tokens, xh = a.sx[which].head, dyh = a.sdy[which].head, dxh = a.sy[which].head;
   // every thread of the CTA makes the same number of turns
   for (int64_t base = (int64_t)cta * per; base < all; base += (int64_t)ctas * per) {
     const int64_t token = base + (threadIdx.x >> a.lanes_shift);
     const bool live = token < all;
     const int64_t b = live ? token / a.tokens : 0;
     const int t = live ? (int)(token - b * a.tokens) : 0;
-    const int64_t pos = position_of(a, b, t);
-    float cs[E][VEC], sn[E][VEC];
-#pragma unroll
-    for (int e = 0; e < E; ++e) turns_of<VEC, ACROSS>(a, turns, pos, col[e][0], -1.f, cs[e], sn[e]);
     const T* x = static_cast<const T*>(a.x[which]) + b * a.sx[which].batch + t * a.sx[which].token;
     const T* dy = static_cast<const T*>(a.dy[which]) + b * a.sdy[which].batch + t * a.sdy[which].token;
     T* dx = static_cast<T*>(a.y[which]) + b * a.sy[which].batch + t * a.sy[which].token;
-    for (int h = 0; h < heads; h += R) {
-      Pack<T, VEC> rx[R][E][2], rd[R][E][2];
+    Pack<T, VEC> nx[R][E][2], nd[R][E][2];
+    auto fetch = [&](int h) {
 #pragma unroll
       for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -243,33 +369,39 @@ __global__ void __launch_bounds__(256) qknorm_bwd_kernel(const __grid_constant__
 #pragma unroll
           for (int k = 0; k < 2; ++k)
             if (in[e][k] && live && h + r < heads) {
-              rx[r][e][k].load(x + (h + r) * a.sx[which].head + col[e][k], true);
-              rd[r][e][k].load(dy + (h + r) * a.sdy[which].head + col[e][k], true);
+              nx[r][e][k].load(x + (h + r) * xh + col[e][k], true);
+              nd[r][e][k].load(dy + (h + r) * dyh + col[e][k], true);
             } else {
-              rx[r][e][k].zero();
-              rd[r][e][k].zero();
+              nx[r][e][k].zero();
+              nd[r][e][k].zero();
             }
-      float v[R][E][2][VEC], sum[R], along[R];
+    };
+    fetch(0);
+    const int64_t pos = position_of(a, b, t);
+    V cs[E], sn[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) turns_of<VEC, ACROSS>(a, turns, pos, col[e][0], -1.f, &cs[e], &sn[e]);
+    for (int h = 0; h < heads; h += R) {
+      V v[R][E];
+      Pack<T, VEC> rx[R][E][2];
+      float sum[R], along[R];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         sum[r] = along[r] = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
+          v[r][e].read(nd[r][e]);
+          v[r][e].turn(cs[e], sn[e]);  // t
+          V xv, g;
+          xv.read(nx[r][e]);
+          g.product(v[r][e], w[e]);
+          sum[r] += xv.dot(xv);
+          along[r] += g.dot(xv);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[r][e][k][i] = rd[r][e][k].f(i);
-          turn<VEC, ACROSS>(v[r][e], cs[e], sn[e]);  // t
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              const float xv = rx[r][e][k].f(i);
-              sum[r] = fmaf(xv, xv, sum[r]);
-              along[r] = fmaf(v[r][e][k][i] * w[e][k][i], xv, along[r]);
-            }
+          for (int k = 0; k < 2; ++k) rx[r][e][k] = nx[r][e][k];
         }
       }
+      if (h + R < heads) fetch(h + R);
       for (int o = a.group / 2; o > 0; o >>= 1)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -283,38 +415,36 @@ __global__ void __launch_bounds__(256) qknorm_bwd_kernel(const __grid_constant__
         const float rstd = row ? rsqrtf(fmaf(sum[r], a.inv_dim, a.eps)) : 0.f;
         const float mean = along[r] * rstd * a.inv_dim;  // of g xh
 #pragma unroll
-        for (int e = 0; e < E; ++e)
+        for (int e = 0; e < E; ++e) {
+          V xv;
+          xv.read(rx[r][e]);
+          xv.scale(rstd);  // xh
+          dw[e].add_product(v[r][e], xv);
+          v[r][e].product(v[r][e], w[e]);
+          v[r][e].combine(rstd, -mean * rstd, xv);
+          Pack<T, VEC> o[2];
+          v[r][e].write(o);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            Pack<T, VEC> o;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-              const float xh = rx[r][e][k].f(i) * rstd, tv = v[r][e][k][i];
-              dw[e][k][i] = fmaf(tv, xh, dw[e][k][i]);
-              o.v[i] = from_f32<T>(rstd * fmaf(tv, w[e][k][i], -xh * mean));
-            }
-            if (in[e][k] && row) o.store(dx + (h + r) * a.sy[which].head + col[e][k], true);
-          }
+          for (int k = 0; k < 2; ++k)
+            if (in[e][k] && row) o[k].store(dx + (h + r) * dxh + col[e][k], true);
+        }
       }
     }
   }
   if (!a.partial) return;
   // groups of a warp hold the same columns; then the warps in order
-  for (int o = a.group; o < 32; o <<= 1)
 #pragma unroll
-    for (int e = 0; e < E; ++e)
+  for (int e = 0; e < E; ++e) {
+    float f[2 * VEC];
+    dw[e].get(f);
+    for (int o = a.group; o < 32; o <<= 1)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int i = 0; i < 2 * VEC; ++i) f[i] += __shfl_xor_sync(0xffffffffu, f[i], o);
+    if ((threadIdx.x & 31) < a.group)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) dw[e][k][i] += __shfl_xor_sync(0xffffffffu, dw[e][k][i], o);
-  if ((threadIdx.x & 31) < a.group)
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (in[e][k])
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) sums[threadIdx.x >> 5][col[e][k] + i] = dw[e][k][i];
+      for (int i = 0; i < 2 * VEC; ++i)
+        if (in[e][i / VEC]) sums[threadIdx.x >> 5][col[e][i / VEC] + i % VEC] = f[i];
+  }
   __syncthreads();
   for (int c = threadIdx.x; c < a.dim; c += blockDim.x) {
     float s = 0.f;
@@ -346,8 +476,6 @@ __global__ void __launch_bounds__(1024) qknorm_reduce_kernel(const float* partia
 
 // ---------------------------------------------------------------- dispatch
 
-constexpr int kBwdResident = 3;  // CTAs of the backward kernel that an SM holds
-
 // CTAs of the backward pass: those that are resident at once, shared out by
 // the number of heads, none for nothing.
 void share_ctas(QkArgs* a) {
@@ -370,7 +498,7 @@ mhla_status launch(QkArgs& a, bool backward, cudaStream_t s) {
   }
   // Heads are shared out over threads only where there are too few tokens to
   // fill the GPU, as each share forms the sines again.
-  const int64_t items = (int64_t)a.batch * a.tokens * a.group, want = (int64_t)kOpsSms * 2048;
+  const int64_t items = (int64_t)a.batch * a.tokens * a.group, want = (int64_t)kOpsSms * kFwdResident * 256;
   const int total = a.heads[0] + a.heads[1];
   int64_t parts = (want + items - 1) / items;
   if (parts > total) parts = total;

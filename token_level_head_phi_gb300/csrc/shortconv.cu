@@ -14,6 +14,12 @@ namespace {
 
 constexpr int kVec = 4;       // channels of a thread
 constexpr int kThreads = 256;
+constexpr int kRows = 4;      // rows of a step; the next step's are on their way
+
+enum { kForward, kBackward, kStep };
+
+// CTAs that an SM holds.
+constexpr int resident(int what) { return what == kForward ? 3 : 2; }
 
 struct ConvArgs {
   const void *x, *dout, *w, *bias, *state_in, *dstate_out;
@@ -51,16 +57,43 @@ struct Place {
   }
 };
 
-template <int K>
-__device__ __forceinline__ void load_weights(const ConvArgs& p, const Place& at, float (&w)[K][kVec],
-                                             float (&bias)[kVec]) {
+// Channel pairs of a thread's weights and bias.
+template <typename W, int K>
+__device__ __forceinline__ void load_weights_as(const ConvArgs& p, const Place& at, float (&w)[kVec][K], float (&bias)[kVec]) {
+  const W *pw = static_cast<const W*>(p.w) + (int64_t)at.ch * K, *pb = static_cast<const W*>(p.bias) + at.ch;
+  if (at.n == kVec) {
 #pragma unroll
-  for (int c = 0; c < kVec; ++c) {
-    const bool in = at.live && c < at.n;
+    for (int i = 0; i < kVec * K; ++i) w[i / K][i % K] = to_f32(pw[i]);
 #pragma unroll
-    for (int j = 0; j < K; ++j) w[j][c] = in ? param_at(p.w, p.w_f32, (int64_t)(at.ch + c) * K + j) : 0.f;
-    bias[c] = in && p.bias ? param_at(p.bias, p.w_f32, at.ch + c) : 0.f;
+    for (int c = 0; c < kVec; ++c) bias[c] = p.bias ? to_f32(pb[c]) : 0.f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec * K; ++i) w[i / K][i % K] = i < at.n * K ? to_f32(pw[i]) : 0.f;
+#pragma unroll
+    for (int c = 0; c < kVec; ++c) bias[c] = p.bias && c < at.n ? to_f32(pb[c]) : 0.f;
   }
+}
+template <int K>
+__device__ __forceinline__ void load_weights(const ConvArgs& p, const Place& at, uint64_t (&w)[K][kVec / 2],
+                                             uint64_t (&bias)[kVec / 2]) {
+  float f[kVec][K], g[kVec];
+  if (p.w_f32)
+    load_weights_as<float, K>(p, at, f, g);
+  else
+    load_weights_as<__nv_bfloat16, K>(p, at, f, g);
+#pragma unroll
+  for (int c = 0; c < kVec / 2; ++c) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) w[j][c] = pair(f[2 * c][j], f[2 * c + 1][j]);
+    bias[c] = pair(g[2 * c], g[2 * c + 1]);
+  }
+}
+
+// 1 / (1 + e^-z)
+__device__ __forceinline__ uint64_t logistic(uint64_t z) {
+  const float2 y = unpair(mul2(z, splat(-kLog2e)));
+  const float2 d = unpair(add2(pair(ex2(y.x), ex2(y.y)), splat(1.f)));
+  return pair(rcp(d.x), rcp(d.y));
 }
 
 // Row t of x, rows before the first token from the incoming state, zeros past
@@ -79,45 +112,63 @@ __device__ __forceinline__ void load_row(const ConvArgs& p, const Place& at, int
 }
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const __grid_constant__ ConvArgs p) {
-  constexpr int U = 4;  // rows in flight
+__global__ void __launch_bounds__(kThreads, resident(kForward)) conv_fwd_kernel(const __grid_constant__ ConvArgs p) {
+  constexpr int H = kVec / 2;
   const Place at(p);
   if (!at.live) return;
   const int len = length_of(p, at.b), last = min(at.first + p.seg, p.N);
-  float w[K][kVec], bias[kVec];
+  uint64_t w[K][H], bias[H];
   load_weights<K>(p, at, w, bias);
-  float win[K - 1][kVec];  // rows t - K + 1 .. t - 1
+  uint64_t win[K - 1][H];  // rows t - K + 1 .. t - 1
   Pack<T, kVec> r;
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
     load_row<T, K>(p, at, at.first - (K - 1) + j, len, &r);
 #pragma unroll
-    for (int c = 0; c < kVec; ++c) win[j][c] = r.f(c);
+    for (int c = 0; c < H; ++c) win[j][c] = pair_of(r, c);
   }
+  const T* x = static_cast<const T*>(p.x) + at.b * p.sx.batch + at.ch;
   T* out = static_cast<T*>(p.out) + at.b * p.so.batch + at.ch;
   const bool whole = p.whole && at.n == kVec;
-  for (int t0 = at.first; t0 < last; t0 += U) {
-    Pack<T, kVec> row[U];
+  const int inside = whole ? min(last, len) : at.first;  // steps up to here need no checks
+  Pack<T, kVec> row[kRows], next[kRows];
+  auto fetch = [&](Pack<T, kVec>(&to)[kRows], int t0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) load_row<T, K>(p, at, t0 + u, len, &row[u]);
+    for (int u = 0; u < kRows; ++u) {
+      if (t0 + kRows <= inside)
+        to[u].load(x + (t0 + u) * p.sx.token, true);
+      else if (t0 < last)
+        load_row<T, K>(p, at, t0 + u, len, &to[u]);
+    }
+  };
+  fetch(row, at.first);
+  for (int t0 = at.first; t0 < last; t0 += kRows) {
+    fetch(next, t0 + kRows);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kRows; ++u) {
       const int t = t0 + u;
       Pack<T, kVec> o;
 #pragma unroll
-      for (int c = 0; c < kVec; ++c) {
-        const float x = row[u].f(c);
-        float z = fmaf(w[K - 1][c], x, bias[c]);
+      for (int c = 0; c < H; ++c) {
+        const uint64_t xv = pair_of(row[u], c);
+        uint64_t z = fma2(w[K - 1][c], xv, bias[c]);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
+        for (int j = 0; j < K - 1; ++j) z = fma2(w[j][c], win[j][c], z);
 #pragma unroll
         for (int j = 0; j + 1 < K - 1; ++j) win[j][c] = win[j + 1][c];
-        win[K - 2][c] = x;
-        if (p.silu) z = z * rcp(1.f + ex2(-z * kLog2e));
-        o.v[c] = from_f32<T>(t < len ? z : 0.f);
+        win[K - 2][c] = xv;
+        if (p.silu) z = mul2(z, logistic(z));
+        put_pair(&o, c, z);
       }
-      if (t < last) o.store(out + t * p.so.token, whole, at.n);
+      if (t0 + kRows <= inside) {
+        o.store(out + t * p.so.token, true);
+      } else if (t < last) {
+        if (t >= len) o.zero();
+        o.store(out + t * p.so.token, whole, at.n);
+      }
     }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) row[u] = next[u];
   }
   if (p.state_out && at.first == 0) {
     // the same thread that read state_in, which this may be
@@ -131,91 +182,121 @@ __global__ void __launch_bounds__(kThreads) conv_fwd_kernel(const __grid_constan
 }
 
 template <typename T, int K>
-__global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const __grid_constant__ ConvArgs p) {
-  constexpr int U = 4;  // rows in flight
+__global__ void __launch_bounds__(kThreads, resident(kBackward)) conv_bwd_kernel(const __grid_constant__ ConvArgs p) {
+  constexpr int H = kVec / 2;
   extern __shared__ float sums[];  // [down][(K + 1) * kVec][across]
   const Place at(p);
-  float dw[K + 1][kVec];
+  uint64_t dw[K + 1][H];
 #pragma unroll
   for (int j = 0; j <= K; ++j)
 #pragma unroll
-    for (int c = 0; c < kVec; ++c) dw[j][c] = 0.f;
+    for (int c = 0; c < H; ++c) dw[j][c] = splat(0.f);
   if (at.live) {
-    const int len = length_of(p, at.b), last = min(at.first + p.seg, p.N);
-    float w[K][kVec], bias[kVec];
+    const int len = length_of(p, at.b), last = min(at.first + p.seg, p.N), end = last + K - 1;
+    uint64_t w[K][H], bias[H];
     load_weights<K>(p, at, w, bias);
-    float win[K - 1][kVec], dz[K - 1][kVec];  // rows t - K + 1 .. t - 1 of x and of dL/dz
+    uint64_t win[K - 1][H], dz[K - 1][H];  // rows t - K + 1 .. t - 1 of x and of dL/dz
     Pack<T, kVec> r;
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
       load_row<T, K>(p, at, at.first - (K - 1) + j, len, &r);
 #pragma unroll
-      for (int c = 0; c < kVec; ++c) {
-        win[j][c] = r.f(c);
-        dz[j][c] = 0.f;
+      for (int c = 0; c < H; ++c) {
+        win[j][c] = pair_of(r, c);
+        dz[j][c] = splat(0.f);
       }
     }
     const bool whole = p.whole && at.n == kVec;
+    const T* x = static_cast<const T*>(p.x) + at.b * p.sx.batch + at.ch;
     const T* dout = static_cast<const T*>(p.dout) + at.b * p.sdo.batch + at.ch;
     T* dx = static_cast<T*>(p.dx) + at.b * p.sdx.batch + at.ch;
+    // Steps inside need no checks: their rows are before the length and the
+    // segment's end, and the rows s = t - (K - 1) of dx not before its start.
+    auto inside = [&](int t0) { return whole && t0 >= at.first + K - 1 && t0 + kRows <= min(last, len); };
+    Pack<T, kVec> row[kRows], rd[kRows], next[kRows], nextd[kRows];
+    auto fetch = [&](Pack<T, kVec>(&to)[kRows], Pack<T, kVec>(&tod)[kRows], int t0) {
+      if (whole && t0 + kRows <= min(end, len)) {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          to[u].load(x + (t0 + u) * p.sx.token, true);
+          tod[u].load(dout + (t0 + u) * p.sdo.token, true);
+        }
+      } else if (t0 < end) {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          const bool in = t0 + u < end;
+          load_row<T, K>(p, at, t0 + u, in ? len : 0, &to[u]);
+          if (in && t0 + u < len)
+            tod[u].load(dout + (t0 + u) * p.sdo.token, whole, at.n);
+          else
+            tod[u].zero();
+        }
+      }
+    };
+    fetch(row, rd, at.first);
     // Rows s < first belong to the segment before, but the first one's are the
     // incoming state's.
-    for (int t0 = at.first; t0 < last + K - 1; t0 += U) {
-      Pack<T, kVec> row[U], rd[U];
+    for (int t0 = at.first; t0 < end; t0 += kRows) {
+      fetch(next, nextd, t0 + kRows);
+      const bool fast = inside(t0);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        load_row<T, K>(p, at, t0 + u, t0 + u < last + K - 1 ? len : 0, &row[u]);
-        if (t0 + u < len && t0 + u < last + K - 1)
-          rd[u].load(dout + (t0 + u) * p.sdo.token, whole, at.n);
-        else
-          rd[u].zero();
-      }
+      for (int u = 0; u < kRows; ++u) {
+        const int t = t0 + u, s = t - (K - 1);
+        uint64_t o[H];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int t = t0 + u, s = t - (K - 1), extra = s - (len - (K - 1));
-        float d[kVec], o[kVec];
-#pragma unroll
-        for (int c = 0; c < kVec; ++c) {
-          const float x = row[u].f(c);
-          d[c] = rd[u].f(c);
+        for (int c = 0; c < H; ++c) {
+          const uint64_t xv = pair_of(row[u], c);
+          uint64_t d = pair_of(rd[u], c);
           if (p.silu) {
-            float z = fmaf(w[K - 1][c], x, bias[c]);
+            uint64_t z = fma2(w[K - 1][c], xv, bias[c]);
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j) z = fmaf(w[j][c], win[j][c], z);
-            const float q = rcp(1.f + ex2(-z * kLog2e));
-            const float slope = q * fmaf(z, 1.f - q, 1.f);
-            d[c] = t < len ? d[c] * slope : 0.f;
+            for (int j = 0; j < K - 1; ++j) z = fma2(w[j][c], win[j][c], z);
+            // q (1 + z (1 - q))
+            const uint64_t q = logistic(z), zq = mul2(z, q);
+            d = mul2(d, fma2(zq, fma2(q, splat(-1.f), splat(1.f)), q));
           }
-          if (t < last) {
+          if (!fast && t >= len) d = splat(0.f);
+          const uint64_t own = fast || t < last ? d : splat(0.f);
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j) dw[j][c] = fmaf(d[c], win[j][c], dw[j][c]);
-            dw[K - 1][c] = fmaf(d[c], x, dw[K - 1][c]);
-            dw[K][c] += d[c];
-          }
+          for (int j = 0; j < K - 1; ++j) dw[j][c] = fma2(own, win[j][c], dw[j][c]);
+          dw[K - 1][c] = fma2(own, xv, dw[K - 1][c]);
+          dw[K][c] = add2(dw[K][c], own);
           // dz_{s + i} meets w_{K - 1 - i}; d is dz_{s + K - 1}
-          o[c] = w[0][c] * d[c];
+          o[c] = mul2(w[0][c], d);
 #pragma unroll
-          for (int i = 0; i < K - 1; ++i) o[c] = fmaf(w[K - 1 - i][c], dz[i][c], o[c]);
+          for (int i = 0; i < K - 1; ++i) o[c] = fma2(w[K - 1 - i][c], dz[i][c], o[c]);
 #pragma unroll
           for (int j = 0; j + 1 < K - 1; ++j) {
             win[j][c] = win[j + 1][c];
             dz[j][c] = dz[j + 1][c];
           }
-          win[K - 2][c] = x;
-          dz[K - 2][c] = d[c];
+          win[K - 2][c] = xv;
+          dz[K - 2][c] = d;
         }
-        if (t >= last + K - 1 || s < at.first - (at.first == 0 ? K - 1 : 0)) continue;
+        if (fast) {
+#pragma unroll
+          for (int c = 0; c < H; ++c) put_pair(&r, c, o[c]);
+          r.store(dx + s * p.sdx.token, true);
+          continue;
+        }
+        const int extra = s - (len - (K - 1));
+        if (t >= end || s < at.first - (at.first == 0 ? K - 1 : 0)) continue;
         if (p.dstate_out && extra >= 0 && extra < K - 1) {  // the row went into the outgoing state
           r.load(static_cast<const T*>(p.dstate_out) + ((int64_t)at.b * (K - 1) + extra) * p.D + at.ch, false, at.n);
 #pragma unroll
-          for (int c = 0; c < kVec; ++c) o[c] += r.f(c);
+          for (int c = 0; c < H; ++c) o[c] = add2(o[c], pair_of(r, c));
         }
 #pragma unroll
-        for (int c = 0; c < kVec; ++c) r.v[c] = from_f32<T>(s < len ? o[c] : 0.f);
+        for (int c = 0; c < H; ++c) put_pair(&r, c, s < len ? o[c] : splat(0.f));
         if (s >= 0)
           r.store(dx + s * p.sdx.token, whole, at.n);
         else if (p.dstate_in)
           r.store(static_cast<T*>(p.dstate_in) + ((int64_t)at.b * (K - 1) + s + K - 1) * p.D + at.ch, false, at.n);
+      }
+#pragma unroll
+      for (int u = 0; u < kRows; ++u) {
+        row[u] = next[u];
+        rd[u] = nextd[u];
       }
     }
   }
@@ -225,7 +306,8 @@ __global__ void __launch_bounds__(kThreads) conv_bwd_kernel(const __grid_constan
 #pragma unroll
   for (int j = 0; j <= K; ++j)
 #pragma unroll
-    for (int c = 0; c < kVec; ++c) sums[(d * kSums + j * kVec + c) * p.across + a] = dw[j][c];
+    for (int c = 0; c < kVec; ++c)
+      sums[(d * kSums + j * kVec + c) * p.across + a] = c % 2 ? unpair(dw[j][c / 2]).y : unpair(dw[j][c / 2]).x;
   __syncthreads();
   for (int i = threadIdx.x; i < kSums * p.across; i += kThreads) {
     const int vec = blockIdx.x * p.across + i % p.across, j = i / p.across / kVec, c = i / p.across % kVec;
@@ -284,11 +366,10 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 
 // ---------------------------------------------------------------- dispatch
 
-enum { kForward, kBackward, kStep };
-
 // Threads of a CTA across the channels and down the tokens, and the tokens of
-// a segment: as long as possible (its neighbours read its borders again), but
-// with enough segments to fill the GPU.
+// a segment: those with the least time, counted in rows that one thread takes
+// after another -- a segment's own and about 16 for its weights and borders --
+// over the waves of CTAs that the GPU holds at once.
 void shape(ConvArgs* p, int what) {
   p->vecs = (p->D + kVec - 1) / kVec;
   p->across = 1;
@@ -298,11 +379,18 @@ void shape(ConvArgs* p, int what) {
     ++p->across_shift;
   }
   p->down = kThreads / p->across;
-  const int64_t lines = (int64_t)p->B * p->vecs, want = (int64_t)kOpsSms * (what == kForward ? 2048 : 1024);
-  int seg = 64;
-  while (seg > 8 && lines * ((p->N + seg - 1) / seg) < want) seg /= 2;
-  p->seg = seg;
-  p->segments = p->N > 0 ? (p->N + seg - 1) / seg : 1;
+  const int64_t columns = (p->vecs + p->across - 1) / p->across, slots = (int64_t)kOpsSms * resident(what);
+  int64_t best = 0;
+  for (int seg = 8; seg <= 256; seg += 4) {
+    const int64_t segments = p->N > 0 ? ((int64_t)p->N + seg - 1) / seg : 1;
+    const int64_t ctas = columns * (((int64_t)p->B * segments + p->down - 1) / p->down);
+    const int64_t cost = (ctas + slots - 1) / slots * (seg + 16);
+    if (seg == 8 || cost < best) {
+      best = cost;
+      p->seg = seg;
+      p->segments = (int)segments;
+    }
+  }
 }
 
 int64_t grid_down(const ConvArgs& p) { return ((int64_t)p.B * p.segments + p.down - 1) / p.down; }
