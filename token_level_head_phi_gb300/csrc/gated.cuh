@@ -21,15 +21,17 @@
 
 namespace mhla {
 
-constexpr int kGatedTok = 8;        // tokens of a warp
-constexpr int kGatedWarps = 8;      // warps of a CTA
-constexpr int kGatedTile = kGatedTok * kGatedWarps;
-constexpr int kGatedSlab = 64;      // channels of a CTA
-constexpr int kGatedCluster = 8;    // most CTAs of a cluster
-static_assert(kGatedTile == MHLA_GATED_MARK, "a tile starts at a mark");
+constexpr int kGatedWarps = 8;    // warps of a CTA
+constexpr int kGatedSlab = 64;    // channels of a CTA
+constexpr int kGatedCluster = 8;  // most CTAs of a cluster
+// tokens of a warp and of a CTA's tile
+template <bool F32, bool BACKWARD>
+constexpr int kGatedTok = BACKWARD || F32 ? 8 : 16;
+inline int gated_tile(bool f32, bool backward) { return kGatedWarps * (backward || f32 ? 8 : 16); }
+static_assert(kGatedWarps * 8 == MHLA_GATED_MARK, "a backward tile starts at a mark");
 // CTAs that an SM holds: their registers, and the shared memory of float32's
 // backward pass.
-constexpr int gated_resident(bool f32, bool backward) { return backward ? (f32 ? 1 : 2) : (f32 ? 2 : 3); }
+constexpr int gated_resident(bool f32, bool backward) { return f32 ? 1 : 2; }
 
 struct GatedArgs {
   const void *x, *r, *i, *dout;
@@ -43,7 +45,7 @@ struct GatedArgs {
   float* partial;  // [B][cluster][D], sums for log_decay's gradient
   int B, N, D, n_marks, slabs;
   int scale;
-  int vec;  // both channels of a lane in one access
+  int vec;  // rows start at multiples of 16 bytes (2), of a pair of elements (1) or of one (0)
 };
 
 // Launches return a status.
@@ -55,58 +57,56 @@ mhla_status launch_gated_step(const GatedArgs& a, int dtype, int kind, cudaStrea
 
 // What the gates of two channels make, as pairs of float32.
 struct Gates {
-  uint64_t gap;   // 1 - a
-  uint64_t s;     // sigma(r)
-  uint64_t less;  // 1 - sigma(r)
-  uint64_t q;     // sigma(i); 1 without an input gate
+  float2 m;     // a - 1
+  float2 s;     // sigma(r)
+  float2 less;  // 1 - sigma(r)
+  float2 q;     // sigma(i); not set without an input gate
 };
 
-// sigma(r) = 1 / (1 + 2^-(r log2 e)), one reciprocal for both gates; the
-// powers stay below 2^62, so their product does not overflow and sigma not
-// below 2^-62.
+// sigma(r) = 1 / (1 + 2^-(r log2 e)), one reciprocal for both gates.  r is taken
+// as at least -43 (least_gate), so the powers' product does not overflow, and
+// sigma as at least 2e-19.
 //
 // a is formed as 1 + expm1(log a): its rounding (2^-25 next to 1) is multiplied
 // with itself over all the tokens that a slow channel remembers, so a float32
 // exponential's last bit, which errs to one side, would show (the final state
 // of 32k tokens 4.5e-6 off instead of 3e-7).  expm1 is its Taylor series above
-// -1/4 (the first term left out is x^7 / 5040, 5e-8 of the sum) and 2^(x log2
-// e) - 1 below.  `g`: log_decay, at most 0.
+// -1/8 (the first term left out is x^6 / 720, 4e-8 of the sum) and 2^(x log2
+// e) - 1 below.  `g`: log_decay, at most 0; `g2`: g log2 e.
 template <int KIND, bool IN>
-__device__ __forceinline__ Gates gates_of(uint64_t r, uint64_t i, uint64_t g) {
-  const uint64_t one = splat(1.f), minus = splat(-1.f);
+__device__ __forceinline__ Gates gates_of(float2 r, float2 i, float2 g, float2 g2) {
   Gates o;
-  const float2 f = unpair(mul2(r, splat(-kLog2e)));
-  const uint64_t e = pair(ex2(least(f.x, 62.f)), ex2(least(f.y, 62.f))), e1 = add2(e, one);
+  const float2 f = (mulc(r, kLog2e));
+  const float2 e = make_float2(ex2(-f.x), ex2(-f.y)), e1 = addc(e, 1.f);
   if constexpr (IN) {
-    const float2 h = unpair(mul2(i, splat(-kLog2e)));
-    const uint64_t k1 = add2(pair(ex2(least(h.x, 62.f)), ex2(least(h.y, 62.f))), one);
-    const float2 d = unpair(mul2(e1, k1));
-    const uint64_t inv = pair(rcp(d.x), rcp(d.y));
+    const float2 h = (mulc(i, kLog2e));
+    const float2 k1 = addc(make_float2(ex2(-h.x), ex2(-h.y)), 1.f);
+    const float2 d = (mul2(e1, k1));
+    const float2 inv = make_float2(rcp(d.x), rcp(d.y));
     o.s = mul2(inv, k1);
     o.q = mul2(inv, e1);
   } else {
-    const float2 d = unpair(e1);
-    o.s = pair(rcp(d.x), rcp(d.y));
-    o.q = one;
+    const float2 d = (e1);
+    o.s = make_float2(rcp(d.x), rcp(d.y));
   }
   o.less = mul2(e, o.s);
   if constexpr (KIND == MHLA_GATED_DECAY) {
-    const uint64_t x = mul2(g, o.s);
-    uint64_t t = fma2(x, splat(-1.f / 720.f), splat(-1.f / 120.f));
-    t = fma2(x, t, splat(-1.f / 24.f));
-    t = fma2(x, t, splat(-1.f / 6.f));
-    t = fma2(x, t, splat(-0.5f));
-    t = fma2(x, t, minus);
-    const float2 near = unpair(mul2(x, t)), at = unpair(x), y = unpair(mul2(x, splat(kLog2e)));
-    const float2 far = unpair(fma2(pair(ex2(y.x), ex2(y.y)), minus, one));
-    o.gap = pair(at.x > -0.25f ? near.x : far.x, at.y > -0.25f ? near.y : far.y);
+    const float2 x = mul2(g, o.s);
+    float2 t = fma2(x, splat(1.f / 120.f), splat(1.f / 24.f));
+    t = fmac(x, t, 1.f / 6.f);
+    t = fmac(x, t, 0.5f);
+    t = fmac(x, t, 1.f);
+    const float2 near = (mul2(x, t)), at = (x), y = (mul2(o.s, g2));
+    o.m = make_float2(at.x > -0.125f ? near.x : ex2(y.x) - 1.f, at.y > -0.125f ? near.y : ex2(y.y) - 1.f);
   } else {
-    o.gap = o.less;
+    const float2 v = (o.less);
+    o.m = make_float2(-v.x, -v.y);
   }
   return o;
 }
 
-__device__ __forceinline__ uint64_t decay_of(uint64_t gap) { return fma2(gap, splat(-1.f), splat(1.f)); }
+// 1 - a^2 with its sign turned.
+__device__ __forceinline__ float2 minus_v(float2 m) { return mul2(m, addc(m, 2.f)); }
 
 __device__ __forceinline__ int gated_length(const GatedArgs& p, int b) {
   if (!p.lengths) return p.N;
@@ -117,24 +117,35 @@ __device__ __forceinline__ int gated_length(const GatedArgs& p, int b) {
 // Two neighbouring channels of a row.
 template <typename T>
 using Two = Pack<T, 2>;
-__device__ __forceinline__ uint64_t wide(const Two<__nv_bfloat16>& x) {
+__device__ __forceinline__ float2 wide(const Two<__nv_bfloat16>& x) {
   const uint32_t w = *reinterpret_cast<const uint32_t*>(x.v);
-  return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-__device__ __forceinline__ uint64_t wide(const Two<float>& x) { return pair(x.v[0], x.v[1]); }
-__device__ __forceinline__ Two<__nv_bfloat16> narrow(uint64_t x, __nv_bfloat16) {
-  const float2 f = unpair(x);
+__device__ __forceinline__ float2 wide(const Two<float>& x) { return make_float2(x.v[0], x.v[1]); }
+__device__ __forceinline__ Two<__nv_bfloat16> narrow(float2 x, __nv_bfloat16) {
+  const float2 f = (x);
   const __nv_bfloat162 y = __floats2bfloat162_rn(f.x, f.y);
   Two<__nv_bfloat16> o;
   *reinterpret_cast<uint32_t*>(o.v) = *reinterpret_cast<const uint32_t*>(&y);
   return o;
 }
-__device__ __forceinline__ Two<float> narrow(uint64_t x, float) {
-  const float2 f = unpair(x);
+__device__ __forceinline__ Two<float> narrow(float2 x, float) {
+  const float2 f = (x);
   Two<float> o;
   o.v[0] = f.x;
   o.v[1] = f.y;
   return o;
+}
+
+// A gate's value, NaN kept, not below where sigma is taken to end.
+__device__ __forceinline__ float2 least_gate(const Two<__nv_bfloat16>& x) {
+  const __nv_bfloat162 end = __float2bfloat162_rn(-43.f);
+  const __nv_bfloat162 y = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(x.v), end);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&y);
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 least_gate(const Two<float>& x) {
+  return make_float2(most(x.v[0], -43.f), most(x.v[1], -43.f));
 }
 
 // A lane's two channels.
@@ -145,13 +156,113 @@ struct Lane {
     n = min(max(D - ch, 0), 2);
   }
   // entries of a float32 vector; zeros where it is NULL and outside
-  __device__ __forceinline__ uint64_t get(const float* p) const {
-    return pair(p && n > 0 ? p[ch] : 0.f, p && n > 1 ? p[ch + 1] : 0.f);
+  __device__ __forceinline__ float2 get(const float* p) const {
+    return make_float2(p && n > 0 ? p[ch] : 0.f, p && n > 1 ? p[ch + 1] : 0.f);
   }
-  __device__ __forceinline__ void put(float* p, uint64_t v) const {
-    const float2 f = unpair(v);
+  __device__ __forceinline__ void put(float* p, float2 v) const {
+    const float2 f = (v);
     if (n > 0) p[ch] = f.x;
     if (n > 1) p[ch + 1] = f.y;
+  }
+};
+
+// ------------------------------------------------- a warp's shared memory
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from, int bytes) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(BYTES), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// TOK rows of a slab, of one warp.
+template <typename T, int TOK>
+struct Rows {
+  Two<T> v[TOK][32];
+  static constexpr int kPiece = 16 / sizeof(T), kPieces = kGatedSlab / kPiece;  // of a row
+  static constexpr int kAtOnce = 32 / kPieces;                                  // rows of one access of the warp
+};
+
+// A lane's way through the rows of a slab in global memory.
+template <typename T, typename P>
+struct Walk {
+  P* at;  // of the lane: its piece of one of the first rows, or its two channels of the first
+  int64_t stride;
+  using R1 = Rows<T, 1>;
+
+  __device__ __forceinline__ Walk(P* slab, int64_t stride, int vec) : stride(stride) {
+    const int l = threadIdx.x & 31;
+    at = slab + (vec == 2 ? l / R1::kPieces * stride + l % R1::kPieces * R1::kPiece : 2 * l);
+  }
+
+  // Starts copies of the rows from `t0` on; zeros where they have no `rows` or
+  // the row ends (`cols` entries).  `fast`: there are TOK whole ones, vec is 2.
+  template <int TOK>
+  __device__ __forceinline__ void fetch(Rows<T, TOK>& to, int t0, bool fast, int rows, int cols, int vec) const {
+    const int l = threadIdx.x & 31;
+    const T* from = at + t0 * stride;
+    if (fast) {
+      Two<T>* place = &to.v[l / R1::kPieces][l % R1::kPieces * (R1::kPiece / 2)];
+#pragma unroll
+      for (int i = 0; i < TOK / R1::kAtOnce; ++i, from += R1::kAtOnce * stride)
+        copy_async<16>(place + i * R1::kAtOnce * 32, from, 16);
+    } else if (vec == 2) {
+      const int row = l / R1::kPieces, col = l % R1::kPieces * R1::kPiece;
+      const int left = min(max(cols - col, 0), R1::kPiece) * (int)sizeof(T);
+      for (int i = 0; i < TOK / R1::kAtOnce; ++i, from += R1::kAtOnce * stride) {
+        Two<T>* place = &to.v[row + i * R1::kAtOnce][col / 2];
+        if (row + i * R1::kAtOnce < rows && left)
+          copy_async<16>(place, from, left);
+        else
+          *reinterpret_cast<uint4*>(place) = make_uint4(0, 0, 0, 0);
+      }
+    } else {
+      for (int i = 0; i < TOK; ++i, from += stride) {
+        Two<T>& place = to.v[i][l];
+        if (vec == 1 && i < rows && 2 * l + 1 < cols) {
+          copy_async<2 * sizeof(T)>(&place, from, 2 * (int)sizeof(T));
+        } else {
+          Two<T> v;
+          v.zero();
+          if (i < rows) v.load(from, false, cols - 2 * l);
+          place = v;
+        }
+      }
+    }
+  }
+
+  // Writes the rows from `t0` on, as far as there are `rows` and columns.
+  template <int TOK>
+  __device__ __forceinline__ void write(const Rows<T, TOK>& from, int t0, bool fast, int rows, int cols, int vec) const {
+    const int l = threadIdx.x & 31;
+    P* to = at + t0 * stride;
+    if (vec == 2) {
+      __syncwarp();
+      const int row = l / R1::kPieces, col = l % R1::kPieces * R1::kPiece;
+      const Two<T>* place = &from.v[row][col / 2];
+      if (fast) {
+#pragma unroll
+        for (int i = 0; i < TOK / R1::kAtOnce; ++i, to += R1::kAtOnce * stride)
+          __stcs(reinterpret_cast<uint4*>(to), *reinterpret_cast<const uint4*>(place + i * R1::kAtOnce * 32));
+      } else {
+        for (int i = 0; i < TOK / R1::kAtOnce; ++i, to += R1::kAtOnce * stride) {
+          Pack<T, R1::kPiece> o;
+          *reinterpret_cast<uint4*>(o.v) = *reinterpret_cast<const uint4*>(place + i * R1::kAtOnce * 32);
+          if (row + i * R1::kAtOnce < rows) o.store(to, col + R1::kPiece <= cols, cols - col);
+        }
+      }
+      __syncwarp();  // before the next copies arrive here
+    } else {
+      for (int i = 0; i < TOK && i < rows; ++i, to += stride)
+        from.v[i][l].store(to, vec == 1 && 2 * l + 1 < cols, cols - 2 * l);
+    }
   }
 };
 
@@ -172,63 +283,70 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // The map h -> A h + H of two channels.
 struct __align__(16) Map {
-  uint64_t A, H;
+  float2 A, H;
 };
 __device__ __forceinline__ Map same() { return Map{splat(1.f), splat(0.f)}; }
 __device__ __forceinline__ Map then(Map first, Map next) {
   return Map{mul2(next.A, first.A), fma2(next.A, first.H, next.H)};
 }
-__device__ __forceinline__ uint64_t through(Map m, uint64_t h) { return fma2(m.A, h, m.H); }
+__device__ __forceinline__ float2 through(Map m, float2 h) { return fma2(m.A, h, m.H); }
 __device__ __forceinline__ Map load_map(const Map* p) {
-  const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
-  return Map{v.x, v.y};
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  return Map{make_float2(v.x, v.y), make_float2(v.z, v.w)};
 }
-__device__ __forceinline__ void store_map(Map* p, Map m) { *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(m.A, m.H); }
+__device__ __forceinline__ void store_map(Map* p, Map m) { *reinterpret_cast<float4*>(p) = make_float4(m.A.x, m.A.y, m.H.x, m.H.y); }
 
 // Stores m to the same place of CTA `rank`'s shared memory.
 __device__ __forceinline__ void send(Map* place, int rank, Map m) {
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(place);
   uint32_t there;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(mine), "r"(rank));
-  asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(there), "l"(m.A), "l"(m.H) : "memory");
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(there), "f"(m.A.x), "f"(m.A.y), "f"(m.H.x),
+               "f"(m.H.y)
+               : "memory");
 }
+
+// Barrier `id` (1 .. 15) between two warps of a CTA: one has written, the other
+// reads.
+__device__ __forceinline__ void hand_over(int id) { asm volatile("barrier.cta.arrive.aligned %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void take_over(int id) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory"); }
 
 // What a warp of CTA `rank` (of `ranks`) starts its tokens with, and what all
 // the cluster's tiles make of `carry`.  REVERSE: the last warp of the last CTA
-// comes first.  `turn` alternates, so one barrier a call is enough.
+// comes first.  The last warp of the order adds up the tile and sends it to all
+// CTAs of the cluster, its own among them; every warp follows the tiles by
+// itself.  `turn` alternates, so that a barrier for the warps' maps and one for
+// the tiles' are enough.
 template <bool REVERSE>
 struct Scan {
   Map maps[2][kGatedWarps][32];
   Map tiles[2][kGatedCluster][32];
 
-  __device__ __forceinline__ uint64_t run(int turn, int rank, int ranks, Map map, uint64_t* carry) {
-    const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-    store_map(&maps[turn][w][l], map);
+  __device__ __forceinline__ float2 run(int turn, int rank, int ranks, Map map, float2* carry) {
+    const int l = threadIdx.x & 31, w = threadIdx.x >> 5, order = REVERSE ? kGatedWarps - 1 - w : w;
+    store_map(&maps[turn][order][l], map);
     __syncthreads();
-    Map before = same(), all = before;
+    Map before = same();
 #pragma unroll
-    for (int i = 0; i < kGatedWarps; ++i) {
-      const int v = REVERSE ? kGatedWarps - 1 - i : i;
-      if (v == w) before = all;
-      all = then(all, load_map(&maps[turn][v][l]));
-    }
-    uint64_t start = *carry;
-    if (ranks == 1) {
-      *carry = through(all, start);
-      return through(before, start);
-    }
-    if (w < ranks) send(&tiles[turn][rank][l], w, all);
-    cluster_arrive();
-    cluster_wait();
+    for (int v = 0; v < kGatedWarps - 1; ++v)
+      if (v < order) before = then(before, load_map(&maps[turn][v][l]));
     const int place = REVERSE ? ranks - 1 - rank : rank;  // of this CTA in the order
-    uint64_t h = start;
-#pragma unroll
-    for (int i = 0; i < kGatedCluster; ++i) {
-      if (i == place) start = h;
-      if (i < ranks) h = through(load_map(&tiles[turn][REVERSE ? ranks - 1 - i : i][l]), h);
+    if (order == kGatedWarps - 1) {
+      const Map all = then(before, map);
+      for (int r = 0; r < ranks; ++r) send(&tiles[turn][place][l], r, all);
     }
+    if (ranks > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+    float2 h = *carry;
+    for (int i = 0; i < place; ++i) h = through(load_map(&tiles[turn][i][l]), h);
+    const float2 start = through(before, h);
+    for (int i = place; i < ranks; ++i) h = through(load_map(&tiles[turn][i][l]), h);
     *carry = h;
-    return through(before, start);
+    return start;
   }
 };
 
@@ -236,8 +354,9 @@ struct Scan {
 
 // CTAs of a cluster: the power of two with the fewest rounds of tiles, counted
 // over the waves of CTAs that the GPU holds at once; of equal ones the smallest.
-inline int gated_cluster(int64_t units, int tokens, int resident) {
-  const int64_t slots = (int64_t)kOpsSms * resident, tiles = ((int64_t)tokens + kGatedTile - 1) / kGatedTile;
+inline int gated_cluster(int64_t units, int tokens, bool f32, bool backward) {
+  const int tile = gated_tile(f32, backward);
+  const int64_t slots = (int64_t)kOpsSms * gated_resident(f32, backward), tiles = ((int64_t)tokens + tile - 1) / tile;
   int64_t best = 0;
   int c = 1;
   for (int n = 1; n <= kGatedCluster; n *= 2) {
@@ -252,9 +371,11 @@ inline int gated_cluster(int64_t units, int tokens, int resident) {
 
 #ifdef __CUDACC__
 template <typename K>
-mhla_status launch_gated_clusters(K kernel, const GatedArgs& a, int resident, size_t smem, cudaStream_t s) {
+mhla_status launch_gated_clusters(K kernel, const GatedArgs& a, bool f32, bool backward, size_t smem, cudaStream_t s) {
   const int64_t units = (int64_t)a.B * a.slabs;
-  const int cluster = gated_cluster(units, a.N, resident);
+  const int cluster = gated_cluster(units, a.N, f32, backward);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return record_cuda_error(e);
   if (units * cluster > 0x7fffffff) return MHLA_ERR_UNSUPPORTED;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cluster));
@@ -267,7 +388,7 @@ mhla_status launch_gated_clusters(K kernel, const GatedArgs& a, int resident, si
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  e = cudaLaunchKernelEx(&cfg, kernel, a);
   return e == cudaSuccess ? launch_status() : record_cuda_error(e);
 }
 

@@ -1,4 +1,6 @@
 // C entries of the gated recurrence: checks, scratch, launches.
+#include <algorithm>
+
 #include "gated.cuh"
 
 namespace mhla {
@@ -72,14 +74,19 @@ GatedArgs args_of(const mhla_gated_params* p, const void* x, const void* gate, c
 // Rows of the sums for log_decay's gradient.
 int64_t partial_rows(const mhla_gated_params* p) {
   const int64_t units = (int64_t)p->batch * ((p->width + kGatedSlab - 1) / kGatedSlab);
-  return (int64_t)p->batch * gated_cluster(units, p->tokens, gated_resident(p->dtype == MHLA_DTYPE_F32, true));
+  return (int64_t)p->batch * gated_cluster(units, p->tokens, p->dtype == MHLA_DTYPE_F32, true);
 }
 
-// Whether the two channels of a lane can be one access in all of these.
-int pairs_aligned(const RowTensor* t, int n) {
-  for (int i = 0; i < n; ++i)
-    if (!t[i].empty() && row_alignment(t[i], 2 * (int)t[i].elem) < 2 * (int)t[i].elem) return 0;
-  return 1;
+// 2, 1 or 0: rows of all of these start at multiples of 16 bytes, of a pair of
+// elements, or of one.
+int alignment_of(const RowTensor* t, int n) {
+  int level = 2;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].empty()) continue;
+    const int a = row_alignment(t[i], 16), mine = a == 16 ? 2 : a >= 2 * (int)t[i].elem ? 1 : 0;
+    level = mine < level ? mine : level;
+  }
+  return level;
 }
 
 }  // namespace
@@ -107,7 +114,7 @@ mhla_status mhla_gated_forward(const void* x, const void* gate, const void* inpu
   a.so = p->out;
   a.state_out = state_out;
   a.marks = marks;
-  a.vec = pairs_aligned(in, 3) && pairs_aligned(res, 1);
+  a.vec = std::min(alignment_of(in, 3), alignment_of(res, 1));
   return launch_gated_fwd(a, p->dtype, p->kind, static_cast<cudaStream_t>(stream));
 }
 
@@ -165,7 +172,7 @@ mhla_status mhla_gated_backward(const void* x, const void* gate, const void* inp
     at += partial_rows(p) * p->width;
   }
   a.state_in = state_in;
-  a.vec = pairs_aligned(in, 4) && pairs_aligned(res, 3);
+  a.vec = std::min(alignment_of(in, 4), alignment_of(res, 3));
   a.marks = const_cast<float*>(marks);
   if (!marks && a.n_marks > 0) {
     a.marks = at;
@@ -209,7 +216,7 @@ mhla_status mhla_gated_step(const void* x, const void* gate, const void* input_g
   a.out = out;
   a.so = p->out;
   a.state_out = state_out;
-  a.vec = pairs_aligned(in, 3) && pairs_aligned(res, 1);
+  a.vec = std::min(alignment_of(in, 3), alignment_of(res, 1));
   return launch_gated_step(a, p->dtype, p->kind, static_cast<cudaStream_t>(stream));
 }
 

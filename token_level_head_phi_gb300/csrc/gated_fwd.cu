@@ -4,103 +4,151 @@
 namespace mhla {
 namespace {
 
-// c of two channels: sqrt(1 - a^2) = sqrt(gap (1 + a)), or k1 gap + k0.
+// c of two channels: sqrt(1 - a^2), or k0 + k1 m: 1 or 1 - a.
 template <bool NORM>
-__device__ __forceinline__ uint64_t factor(uint64_t gap, uint64_t a, uint64_t k1, uint64_t k0) {
-  if constexpr (!NORM) return fma2(gap, k1, k0);
-  const float2 v = unpair(mul2(gap, add2(a, splat(1.f))));
-  return pair(root(v.x), root(v.y));
+__device__ __forceinline__ float2 factor(float2 m, float2 k1, float2 k0) {
+  if constexpr (!NORM) return fma2(m, k1, k0);
+  const float2 v = (minus_v(m));
+  return make_float2(root(-v.x), root(-v.y));
 }
 
+// A warp's inputs of two rounds; the results take x's place.
+template <typename T, bool IN>
+struct Stage {
+  static constexpr int kTok = kGatedTok<sizeof(T) == 4, false>;
+  Rows<T, kTok> x[2], r[2], i[IN ? 2 : 0];
+};
+
+// The warps of a CTA hand their states (alone) or the maps of their tokens (in a
+// cluster) from one to the next, without a barrier for all of them.
 template <typename T, int KIND, bool IN, bool NORM>
 __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 4, false))
     gated_fwd_kernel(const __grid_constant__ GatedArgs p) {
-  __shared__ Scan<false> scan;
+  constexpr int kTok = kGatedTok<sizeof(T) == 4, false>, kTile = kGatedWarps * kTok;
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  __shared__ Map mail[kGatedWarps][32];
+  __shared__ Map tiles[2][kGatedCluster][32];
   const int rank = cluster_rank(), ranks = cluster_size(), unit = blockIdx.x / ranks;
-  const int b = unit / p.slabs, w = threadIdx.x >> 5;
-  const Lane ln(unit - b * p.slabs, p.D);
-  const int len = gated_length(p, b), round = kGatedTile * ranks;  // tokens that the cluster takes at once
-  const float2 lg = unpair(ln.get(KIND == MHLA_GATED_DECAY ? p.g : nullptr));
-  const uint64_t g = pair(least(lg.x, 0.f), least(lg.y, 0.f));
-  const uint64_t k1 = splat(p.scale == MHLA_GATED_SCALE_MEAN ? 1.f : 0.f), k0 = splat(p.scale == MHLA_GATED_SCALE_MEAN ? 0.f : 1.f);
-  uint64_t carry = ln.get(p.state_in ? p.state_in + (int64_t)b * p.D : nullptr);
-  const T* x = static_cast<const T*>(p.x) + b * p.sx.batch + ln.ch;
-  const T* r = static_cast<const T*>(p.r) + b * p.sr.batch + ln.ch;
-  const T* i = static_cast<const T*>(p.i) + b * p.si.batch + ln.ch;
-  T* out = static_cast<T*>(p.out) + b * p.so.batch + ln.ch;
-  // whole slabs of aligned pairs: no checks inside rounds that end before the length
-  const bool vec = p.vec && ln.n == 2, whole = p.vec && (unit - b * p.slabs + 1) * kGatedSlab <= p.D;
+  const int w = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), l = threadIdx.x & 31;
+  const int b = unit / p.slabs, slab = unit - b * p.slabs, first = slab * kGatedSlab, cols = p.D - first;
+  Stage<T, IN>& my = reinterpret_cast<Stage<T, IN>*>(dynamic)[w];
+  const Lane ln(slab, p.D);
+  const int len = gated_length(p, b), round = kTile * ranks;  // tokens that the cluster takes at once
+  const float2 lg = ln.get(KIND == MHLA_GATED_DECAY ? p.g : nullptr);
+  const float2 g = make_float2(least(lg.x, 0.f), least(lg.y, 0.f)), g2 = mulc(g, kLog2e);
+  const float2 k1 = splat(p.scale == MHLA_GATED_SCALE_MEAN ? -1.f : 0.f), k0 = splat(p.scale == MHLA_GATED_SCALE_MEAN ? 0.f : 1.f);
+  float2 carry = ln.get(p.state_in ? p.state_in + (int64_t)b * p.D : nullptr);
+  using In = Walk<T, const T>;
+  const In x(static_cast<const T*>(p.x) + b * p.sx.batch + first, p.sx.token, p.vec);
+  const In r(static_cast<const T*>(p.r) + b * p.sr.batch + first, p.sr.token, p.vec);
+  const In i(static_cast<const T*>(p.i) + b * p.si.batch + first, p.si.token, p.vec);
+  const Walk<T, T> out(static_cast<T*>(p.out) + b * p.so.batch + first, p.so.token, p.vec);
+  const bool whole = p.vec == 2 && cols >= kGatedSlab;
 
-  Two<T> rx[kGatedTok], rr[kGatedTok], ri[kGatedTok];
-  auto fetch = [&](int t0, bool fast) {
-    const T *px = x + t0 * p.sx.token, *pr = r + t0 * p.sr.token, *pi = i + t0 * p.si.token;
-    if (fast) {
-#pragma unroll
-      for (int j = 0; j < kGatedTok; ++j, px += p.sx.token, pr += p.sr.token, pi += p.si.token) {
-        rx[j].load(px, true);
-        rr[j].load(pr, true);
-        if constexpr (IN) ri[j].load(pi, true);
-      }
-      return;
+  auto fetch = [&](int slot, int t0) {
+    if (t0 < len) {
+      const bool fast = whole && t0 + kTok <= len;
+      x.fetch(my.x[slot], t0, fast, len - t0, cols, p.vec);
+      r.fetch(my.r[slot], t0, fast, len - t0, cols, p.vec);
+      if constexpr (IN) i.fetch(my.i[slot], t0, fast, len - t0, cols, p.vec);
     }
-#pragma unroll
-    for (int j = 0; j < kGatedTok; ++j, px += p.sx.token, pr += p.sr.token, pi += p.si.token) {
-      rx[j].zero();
-      rr[j].zero();
-      ri[j].zero();
-      if (ln.n == 0 || t0 + j >= len) continue;
-      rx[j].load(px, vec, ln.n);
-      rr[j].load(pr, vec, ln.n);
-      if constexpr (IN) ri[j].load(pi, vec, ln.n);
-    }
+    copies_commit();
   };
-  int t0 = rank * kGatedTile + w * kGatedTok, turn = 0;
+  auto write = [&](int slot, int t0) {
+    if (p.out && t0 < p.N) out.write(my.x[slot], t0, whole && t0 + kTok <= p.N, p.N - t0, cols, p.vec);
+  };
+  auto mark = [&](int t0, float2 h) {
+    if (p.marks && t0 % MHLA_GATED_MARK == 0 && t0 < p.N)
+      ln.put(p.marks + ((int64_t)b * p.n_marks + t0 / MHLA_GATED_MARK) * p.D, h);
+  };
+  const int mine = rank * kTile + w * kTok;
+  int t0 = mine, turn = 0;
   if (ranks > 1) cluster_arrive();  // nobody sends before all have begun
-  if (len > 0) fetch(t0, whole && round <= len);
+  fetch(0, t0);
   if (ranks > 1) cluster_wait();
   for (int base = 0; base < len; base += round, t0 += round, turn ^= 1) {  // the same turns in all of the cluster
-    const bool fast = whole && base + round <= len;
-    uint64_t a[kGatedTok], add[kGatedTok];
+    fetch(turn ^ 1, t0 + round);
+    copies_wait<1>();
+    __syncwarp();
+    float2 a[kTok], add[kTok];
     Map map = same();
+    if (t0 < len) {
 #pragma unroll
-    for (int j = 0; j < kGatedTok; ++j) {
-      const Gates t = gates_of<KIND, IN>(wide(rr[j]), IN ? wide(ri[j]) : 0, g);
-      const uint64_t u = IN ? mul2(wide(rx[j]), t.q) : wide(rx[j]);
-      a[j] = decay_of(t.gap);
-      add[j] = mul2(factor<NORM>(t.gap, a[j], k1, k0), u);
-    }
-    if (!fast)
-#pragma unroll
-      for (int j = 0; j < kGatedTok; ++j)
-        if (t0 + j >= len) {  // keeps the state
-          a[j] = splat(1.f);
-          add[j] = splat(0.f);
-        }
-#pragma unroll
-    for (int j = 0; j < kGatedTok; ++j) map = then(map, Map{a[j], add[j]});
-    if (base + round < len) fetch(t0 + round, whole && base + 2 * round <= len);
-    uint64_t h = scan.run(turn, rank, ranks, map, &carry);
-    if (p.marks && w == 0 && t0 < p.N) ln.put(p.marks + ((int64_t)b * p.n_marks + t0 / MHLA_GATED_MARK) * p.D, h);
-    T* po = out + t0 * p.so.token;
-    if (p.out && fast) {
-#pragma unroll
-      for (int j = 0; j < kGatedTok; ++j, po += p.so.token) {
-        h = fma2(a[j], h, add[j]);
-        narrow(h, T()).store(po, true);
+      for (int j = 0; j < kTok; ++j) {
+        const Gates t = gates_of<KIND, IN>(least_gate(my.r[turn].v[j][l]), IN ? least_gate(my.i[turn].v[j][l]) : splat(0.f), g, g2);
+        const float2 xv = wide(my.x[turn].v[j][l]), u = IN ? mul2(xv, t.q) : xv;
+        a[j] = addc(t.m, 1.f);
+        add[j] = mul2(factor<NORM>(t.m, k1, k0), u);
       }
-    } else if (p.out && ln.n) {
+      if (t0 + kTok > len)
 #pragma unroll
-      for (int j = 0; j < kGatedTok; ++j, po += p.so.token) {
-        h = fma2(a[j], h, add[j]);
-        if (t0 + j < p.N) narrow(t0 + j < len ? h : splat(0.f), T()).store(po, vec, ln.n);
-      }
+        for (int j = 0; j < kTok; ++j)
+          if (t0 + j >= len) a[j] = splat(1.f), add[j] = splat(0.f);  // keeps the state
+      map = Map{a[0], add[0]};
+#pragma unroll
+      for (int j = 1; j < kTok; ++j) map = then(map, Map{a[j], add[j]});
     }
+    float2 h;
+    if (ranks == 1) {
+      h = carry;
+      if (w > 0 || base > 0) {
+        take_over(1 + w);
+        h = mail[w][l].H;
+      }
+      carry = through(map, h);
+      if (w < kGatedWarps - 1 || base + round < len) {
+        const int to = (w + 1) % kGatedWarps;
+        mail[to][l].H = carry;
+        hand_over(1 + to);
+      }
+    } else {
+      Map before = same();
+      if (w > 0) {
+        take_over(1 + w);
+        before = load_map(&mail[w][l]);
+      }
+      const Map all = then(before, map);
+      if (w < kGatedWarps - 1) {
+        store_map(&mail[w + 1][l], all);
+        hand_over(2 + w);
+      } else {
+        for (int v = 0; v < ranks; ++v) send(&tiles[turn][rank][l], v, all);
+      }
+      cluster_arrive();
+      cluster_wait();
+      h = carry;
+      for (int v = 0; v < rank; ++v) h = through(load_map(&tiles[turn][v][l]), h);
+      carry = h;
+      for (int v = rank; v < ranks; ++v) carry = through(load_map(&tiles[turn][v][l]), carry);
+      h = through(before, h);
+    }
+    mark(t0, h);
+    if (t0 < len)
+#pragma unroll
+      for (int j = 0; j < kTok; ++j) {
+        h = fma2(a[j], h, add[j]);
+        my.x[turn].v[j][l] = narrow(h, T());
+      }
+    if (t0 + kTok > len)
+#pragma unroll
+      for (int j = 0; j < kTok; ++j)
+        if (t0 + j >= len) my.x[turn].v[j][l].zero();
+    write(turn, t0);
   }
-  if (p.state_out && rank == 0 && w == 0) ln.put(p.state_out + (int64_t)b * p.D, carry);
+  // alone, the last warp has the final state, and marks past the length need it
+  if (ranks == 1 && len > 0 && p.marks) {
+    __syncthreads();
+    if (w == kGatedWarps - 1) mail[0][l].H = carry;
+    __syncthreads();
+    carry = mail[0][l].H;
+  }
+  if (p.state_out && rank == 0 && w == kGatedWarps - 1) ln.put(p.state_out + (int64_t)b * p.D, carry);
+  if (t0 >= p.N) return;
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) my.x[0].v[j][l].zero();
   for (; t0 < p.N; t0 += round) {  // padding
-    if (p.marks && w == 0) ln.put(p.marks + ((int64_t)b * p.n_marks + t0 / MHLA_GATED_MARK) * p.D, carry);
-    if (!p.out || !ln.n) continue;
-    for (int t = t0; t < t0 + kGatedTok && t < p.N; ++t) narrow(splat(0.f), T()).store(out + t * p.so.token, vec, ln.n);
+    mark(t0, carry);
+    write(0, t0);
   }
 }
 
@@ -114,17 +162,18 @@ __global__ void __launch_bounds__(128) gated_step_kernel(const __grid_constant__
   Lane ln(0, 0);
   ln.ch = 2 * (int)(at - b * pairs);
   ln.n = min(p.D - ln.ch, 2);
-  const bool vec = p.vec && ln.n == 2;
+  const bool vec = p.vec > 0 && ln.n == 2;
   Two<T> x, r, i;
   x.load(static_cast<const T*>(p.x) + b * p.sx.batch + ln.ch, vec, ln.n);
   r.load(static_cast<const T*>(p.r) + b * p.sr.batch + ln.ch, vec, ln.n);
   if constexpr (IN) i.load(static_cast<const T*>(p.i) + b * p.si.batch + ln.ch, vec, ln.n);
-  const float2 lg = unpair(ln.get(KIND == MHLA_GATED_DECAY ? p.g : nullptr));
-  uint64_t h = ln.get(p.state_in ? p.state_in + b * p.D : nullptr);
-  const Gates t = gates_of<KIND, IN>(wide(r), IN ? wide(i) : 0, pair(least(lg.x, 0.f), least(lg.y, 0.f)));
-  const uint64_t a = decay_of(t.gap), u = IN ? mul2(wide(x), t.q) : wide(x);
+  const float2 lg = (ln.get(KIND == MHLA_GATED_DECAY ? p.g : nullptr));
+  float2 h = ln.get(p.state_in ? p.state_in + b * p.D : nullptr);
+  const float2 g = make_float2(least(lg.x, 0.f), least(lg.y, 0.f));
+  const Gates t = gates_of<KIND, IN>(least_gate(r), IN ? least_gate(i) : splat(0.f), g, mulc(g, kLog2e));
+  const float2 u = IN ? mul2(wide(x), t.q) : wide(x);
   const float k = p.scale == MHLA_GATED_SCALE_MEAN ? 1.f : 0.f;
-  h = fma2(a, h, mul2(factor<NORM>(t.gap, a, splat(k), splat(1.f - k)), u));
+  h = fma2(addc(t.m, 1.f), h, mul2(factor<NORM>(t.m, splat(-k), splat(1.f - k)), u));
   narrow(h, T()).store(static_cast<T*>(p.out) + b * p.so.batch + ln.ch, vec, ln.n);
   if (p.state_out) ln.put(p.state_out + b * p.D, h);
 }
@@ -134,9 +183,9 @@ struct Forward {
   cudaStream_t s;
   template <typename T, int KIND, bool IN>
   mhla_status go() {
-    if (a.scale == MHLA_GATED_SCALE_NORM)
-      return launch_gated_clusters(gated_fwd_kernel<T, KIND, IN, true>, a, gated_resident(sizeof(T) == 4, false), 0, s);
-    return launch_gated_clusters(gated_fwd_kernel<T, KIND, IN, false>, a, gated_resident(sizeof(T) == 4, false), 0, s);
+    auto kernel = a.scale == MHLA_GATED_SCALE_NORM ? gated_fwd_kernel<T, KIND, IN, true>
+                                                   : gated_fwd_kernel<T, KIND, IN, false>;
+    return launch_gated_clusters(kernel, a, sizeof(T) == 4, false, kGatedWarps * sizeof(Stage<T, IN>), s);
   }
 };
 

@@ -81,54 +81,42 @@ __device__ __forceinline__ float least(float x, float y) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
   return z;
 }
+// The larger one, a NaN if either is.
+__device__ __forceinline__ float most(float x, float y) {
+  float z;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(z) : "f"(x), "f"(y));
+  return z;
+}
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Pairs of float32 in one instruction.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t splat(float a) { return pair(a, a); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 splat(float a) { return make_float2(a, a); }
+// With a constant.
+__device__ __forceinline__ float2 addc(float2 a, float c) { return add2(a, splat(c)); }
+__device__ __forceinline__ float2 mulc(float2 a, float c) { return mul2(a, splat(c)); }
+__device__ __forceinline__ float2 fmac(float2 a, float2 b, float c) { return fma2(a, b, splat(c)); }
 
 // Elements 2 i and 2 i + 1 of a pack.
 template <int N>
-__device__ __forceinline__ uint64_t pair_of(const Pack<__nv_bfloat16, N>& x, int i) {
+__device__ __forceinline__ float2 pair_of(const Pack<__nv_bfloat16, N>& x, int i) {
   const uint32_t v = reinterpret_cast<const uint32_t*>(x.v)[i];
-  return pair(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 template <int N>
-__device__ __forceinline__ uint64_t pair_of(const Pack<float, N>& x, int i) {
-  return pair(x.v[2 * i], x.v[2 * i + 1]);
+__device__ __forceinline__ float2 pair_of(const Pack<float, N>& x, int i) {
+  return make_float2(x.v[2 * i], x.v[2 * i + 1]);
 }
 template <int N>
-__device__ __forceinline__ void put_pair(Pack<__nv_bfloat16, N>* x, int i, uint64_t v) {
-  const float2 f = unpair(v);
+__device__ __forceinline__ void put_pair(Pack<__nv_bfloat16, N>* x, int i, float2 v) {
+  const float2 f = (v);
   reinterpret_cast<__nv_bfloat162*>(x->v)[i] = __floats2bfloat162_rn(f.x, f.y);
 }
 template <int N>
-__device__ __forceinline__ void put_pair(Pack<float, N>* x, int i, uint64_t v) {
-  const float2 f = unpair(v);
+__device__ __forceinline__ void put_pair(Pack<float, N>* x, int i, float2 v) {
+  const float2 f = (v);
   x->v[2 * i] = f.x;
   x->v[2 * i + 1] = f.y;
 }

@@ -66,7 +66,7 @@ __device__ __forceinline__ void columns(const QkArgs& a, int slot, int* lo, int*
 template <int VEC, bool ACROSS>
 struct Values {
   static constexpr bool kPairs = ACROSS && VEC > 1;
-  uint64_t p[kPairs ? VEC : 1];    // the first vector's pairs, then the second's
+  float2 p[kPairs ? VEC : 1];    // the first vector's pairs, then the second's
   float f[kPairs ? 1 : 2 * VEC];
 
   template <typename T>
@@ -93,7 +93,7 @@ struct Values {
   __device__ __forceinline__ void set(const float (&v)[2 * VEC]) {
     if constexpr (kPairs) {
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) p[i] = pair(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < VEC; ++i) p[i] = make_float2(v[2 * i], v[2 * i + 1]);
     } else {
 #pragma unroll
       for (int i = 0; i < 2 * VEC; ++i) f[i] = v[i];
@@ -103,7 +103,7 @@ struct Values {
 #pragma unroll
     for (int i = 0; i < 2 * VEC; ++i) {
       if constexpr (kPairs)
-        v[i] = i % 2 ? unpair(p[i / 2]).y : unpair(p[i / 2]).x;
+        v[i] = i % 2 ? (p[i / 2]).y : (p[i / 2]).x;
       else
         v[i] = f[i];
     }
@@ -157,10 +157,10 @@ struct Values {
   }
   __device__ __forceinline__ float dot(const Values& x) const {
     if constexpr (kPairs) {
-      uint64_t s = mul2(p[0], x.p[0]);
+      float2 s = mul2(p[0], x.p[0]);
 #pragma unroll
       for (int i = 1; i < VEC; ++i) s = fma2(p[i], x.p[i], s);
-      const float2 t = unpair(s);
+      const float2 t = (s);
       return t.x + t.y;
     } else {
       float s = f[0] * x.f[0];
@@ -175,7 +175,7 @@ struct Values {
     if constexpr (kPairs) {
 #pragma unroll
       for (int i = 0; i < VEC / 2; ++i) {
-        const uint64_t a = p[i], b = p[i + VEC / 2];
+        const float2 a = p[i], b = p[i + VEC / 2];
         p[i] = fma2(a, c.p[i], mul2(b, s.p[i + VEC / 2]));
         p[i + VEC / 2] = fma2(b, c.p[i + VEC / 2], mul2(a, s.p[i]));
       }

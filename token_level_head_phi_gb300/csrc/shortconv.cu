@@ -74,8 +74,8 @@ __device__ __forceinline__ void load_weights_as(const ConvArgs& p, const Place& 
   }
 }
 template <int K>
-__device__ __forceinline__ void load_weights(const ConvArgs& p, const Place& at, uint64_t (&w)[K][kVec / 2],
-                                             uint64_t (&bias)[kVec / 2]) {
+__device__ __forceinline__ void load_weights(const ConvArgs& p, const Place& at, float2 (&w)[K][kVec / 2],
+                                             float2 (&bias)[kVec / 2]) {
   float f[kVec][K], g[kVec];
   if (p.w_f32)
     load_weights_as<float, K>(p, at, f, g);
@@ -84,16 +84,16 @@ __device__ __forceinline__ void load_weights(const ConvArgs& p, const Place& at,
 #pragma unroll
   for (int c = 0; c < kVec / 2; ++c) {
 #pragma unroll
-    for (int j = 0; j < K; ++j) w[j][c] = pair(f[2 * c][j], f[2 * c + 1][j]);
-    bias[c] = pair(g[2 * c], g[2 * c + 1]);
+    for (int j = 0; j < K; ++j) w[j][c] = make_float2(f[2 * c][j], f[2 * c + 1][j]);
+    bias[c] = make_float2(g[2 * c], g[2 * c + 1]);
   }
 }
 
 // 1 / (1 + e^-z)
-__device__ __forceinline__ uint64_t logistic(uint64_t z) {
-  const float2 y = unpair(mul2(z, splat(-kLog2e)));
-  const float2 d = unpair(add2(pair(ex2(y.x), ex2(y.y)), splat(1.f)));
-  return pair(rcp(d.x), rcp(d.y));
+__device__ __forceinline__ float2 logistic(float2 z) {
+  const float2 y = (mul2(z, splat(-kLog2e)));
+  const float2 d = (add2(make_float2(ex2(y.x), ex2(y.y)), splat(1.f)));
+  return make_float2(rcp(d.x), rcp(d.y));
 }
 
 // Row t of x, rows before the first token from the incoming state, zeros past
@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(kThreads, resident(kForward)) conv_fwd_kernel(
   const Place at(p);
   if (!at.live) return;
   const int len = length_of(p, at.b), last = min(at.first + p.seg, p.N);
-  uint64_t w[K][H], bias[H];
+  float2 w[K][H], bias[H];
   load_weights<K>(p, at, w, bias);
-  uint64_t win[K - 1][H];  // rows t - K + 1 .. t - 1
+  float2 win[K - 1][H];  // rows t - K + 1 .. t - 1
   Pack<T, kVec> r;
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kThreads, resident(kForward)) conv_fwd_kernel(
       Pack<T, kVec> o;
 #pragma unroll
       for (int c = 0; c < H; ++c) {
-        const uint64_t xv = pair_of(row[u], c);
-        uint64_t z = fma2(w[K - 1][c], xv, bias[c]);
+        const float2 xv = pair_of(row[u], c);
+        float2 z = fma2(w[K - 1][c], xv, bias[c]);
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) z = fma2(w[j][c], win[j][c], z);
 #pragma unroll
@@ -186,16 +186,16 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward)) conv_bwd_kernel
   constexpr int H = kVec / 2;
   extern __shared__ float sums[];  // [down][(K + 1) * kVec][across]
   const Place at(p);
-  uint64_t dw[K + 1][H];
+  float2 dw[K + 1][H];
 #pragma unroll
   for (int j = 0; j <= K; ++j)
 #pragma unroll
     for (int c = 0; c < H; ++c) dw[j][c] = splat(0.f);
   if (at.live) {
     const int len = length_of(p, at.b), last = min(at.first + p.seg, p.N), end = last + K - 1;
-    uint64_t w[K][H], bias[H];
+    float2 w[K][H], bias[H];
     load_weights<K>(p, at, w, bias);
-    uint64_t win[K - 1][H], dz[K - 1][H];  // rows t - K + 1 .. t - 1 of x and of dL/dz
+    float2 win[K - 1][H], dz[K - 1][H];  // rows t - K + 1 .. t - 1 of x and of dL/dz
     Pack<T, kVec> r;
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
@@ -242,21 +242,21 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward)) conv_bwd_kernel
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
         const int t = t0 + u, s = t - (K - 1);
-        uint64_t o[H];
+        float2 o[H];
 #pragma unroll
         for (int c = 0; c < H; ++c) {
-          const uint64_t xv = pair_of(row[u], c);
-          uint64_t d = pair_of(rd[u], c);
+          const float2 xv = pair_of(row[u], c);
+          float2 d = pair_of(rd[u], c);
           if (p.silu) {
-            uint64_t z = fma2(w[K - 1][c], xv, bias[c]);
+            float2 z = fma2(w[K - 1][c], xv, bias[c]);
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) z = fma2(w[j][c], win[j][c], z);
             // q (1 + z (1 - q))
-            const uint64_t q = logistic(z), zq = mul2(z, q);
+            const float2 q = logistic(z), zq = mul2(z, q);
             d = mul2(d, fma2(zq, fma2(q, splat(-1.f), splat(1.f)), q));
           }
           if (!fast && t >= len) d = splat(0.f);
-          const uint64_t own = fast || t < last ? d : splat(0.f);
+          const float2 own = fast || t < last ? d : splat(0.f);
 #pragma unroll
           for (int j = 0; j < K - 1; ++j) dw[j][c] = fma2(own, win[j][c], dw[j][c]);
           dw[K - 1][c] = fma2(own, xv, dw[K - 1][c]);
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward)) conv_bwd_kernel
   for (int j = 0; j <= K; ++j)
 #pragma unroll
     for (int c = 0; c < kVec; ++c)
-      sums[(d * kSums + j * kVec + c) * p.across + a] = c % 2 ? unpair(dw[j][c / 2]).y : unpair(dw[j][c / 2]).x;
+      sums[(d * kSums + j * kVec + c) * p.across + a] = c % 2 ? (dw[j][c / 2]).y : (dw[j][c / 2]).x;
   __syncthreads();
   for (int i = threadIdx.x; i < kSums * p.across; i += kThreads) {
     const int vec = blockIdx.x * p.across + i % p.across, j = i / p.across / kVec, c = i / p.across % kVec;
