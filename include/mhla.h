@@ -500,7 +500,7 @@ typedef enum mhla_gated_scale {
   MHLA_GATED_SCALE_NONE = 2
 } mhla_gated_scale;
 
-#define MHLA_GATED_MARK 64 /* tokens between two marks */
+#define MHLA_GATED_MARK 16 /* tokens between two marks */
 
 typedef struct mhla_gated_params {
   int batch, tokens, width;  /* >= 0                                                     */

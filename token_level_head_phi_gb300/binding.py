@@ -54,7 +54,7 @@ ROTARY_MAX_PAIRS = 128
 DECAY_VARIANTS = {"auto": 0, "simt": 1, "tensor": 2}
 GATED_DECAY, GATED_SIGMOID = 0, 1
 GATED_SCALES = {"norm": 0, "mean": 1, "none": 2}
-GATED_MARK = 64
+GATED_MARK = 16
 ACTIVATIONS = {"none": 0, "silu": 1}
 
 
@@ -1350,7 +1350,7 @@ def mhla_gated_forward(x, gate, log_decay=None, input_gate=None, state=None, len
     from (None: zeros); ``state_out is state`` updates it in place.
     ``lengths``: int32 [B] for sequences padded to N; rows past a length come
     out as zeros.  ``keep=True`` also returns the states that the backward call
-    starts from (float32 [B, ceil(N / 64), D], into ``marks`` where given),
+    starts from (float32 [B, ceil(N / 16), D], into ``marks`` where given),
     None otherwise.
     """
     if stream is not None:

@@ -5,14 +5,16 @@
 //   dlog a_t = G_t (a_t h_{t-1} + u_t dc_t / dlog a_t),   du_t = G_t c_t.
 // Both recurrences are scans of the maps h -> A h + H, which compose.
 //
-// A CTA takes 64 channels of one sequence, in tiles of 64 tokens: a warp 8
-// tokens, a lane two channels, whose values are one register pair and one
-// instruction.  Each warp forms the map of its 8 tokens in registers, the maps
-// meet in shared memory behind one barrier, and a second walk over the same
-// tokens writes the results from the state that the warp starts with.  Every
-// input is read once.  Where sequences and channels are few, a cluster of CTAs
-// takes successive tiles of the same channels at once and exchanges the tiles'
-// maps through distributed shared memory.
+// A CTA takes 64 channels of one sequence, tile by tile: a warp 16 tokens (8 in
+// the backward pass and of float32), a lane two channels, whose values are one
+// register pair and one instruction.  Each warp forms the map of its tokens,
+// takes the state from the warp before it, hands its own on and then walks over
+// the same tokens again for the results: the warps of a CTA run after one
+// another without a barrier for all of them.  Every input is read once, by
+// asynchronous copies into shared memory of the warp's own, a round ahead.
+// Where sequences and channels are few, a cluster of CTAs takes successive tiles
+// of the same channels at once and exchanges the tiles' maps through distributed
+// shared memory.
 #pragma once
 
 #include "common.cuh"
@@ -28,7 +30,6 @@ constexpr int kGatedCluster = 8;  // most CTAs of a cluster
 template <bool F32, bool BACKWARD>
 constexpr int kGatedTok = BACKWARD || F32 ? 8 : 16;
 inline int gated_tile(bool f32, bool backward) { return kGatedWarps * (backward || f32 ? 8 : 16); }
-static_assert(kGatedWarps * 8 == MHLA_GATED_MARK, "a backward tile starts at a mark");
 // CTAs that an SM holds: their registers, and the shared memory of float32's
 // backward pass.
 constexpr int gated_resident(bool f32, bool backward) { return f32 ? 1 : 2; }
@@ -311,56 +312,21 @@ __device__ __forceinline__ void send(Map* place, int rank, Map m) {
 __device__ __forceinline__ void hand_over(int id) { asm volatile("barrier.cta.arrive.aligned %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void take_over(int id) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory"); }
 
-// What a warp of CTA `rank` (of `ranks`) starts its tokens with, and what all
-// the cluster's tiles make of `carry`.  REVERSE: the last warp of the last CTA
-// comes first.  The last warp of the order adds up the tile and sends it to all
-// CTAs of the cluster, its own among them; every warp follows the tiles by
-// itself.  `turn` alternates, so that a barrier for the warps' maps and one for
-// the tiles' are enough.
-template <bool REVERSE>
-struct Scan {
-  Map maps[2][kGatedWarps][32];
-  Map tiles[2][kGatedCluster][32];
-
-  __device__ __forceinline__ float2 run(int turn, int rank, int ranks, Map map, float2* carry) {
-    const int l = threadIdx.x & 31, w = threadIdx.x >> 5, order = REVERSE ? kGatedWarps - 1 - w : w;
-    store_map(&maps[turn][order][l], map);
-    __syncthreads();
-    Map before = same();
-#pragma unroll
-    for (int v = 0; v < kGatedWarps - 1; ++v)
-      if (v < order) before = then(before, load_map(&maps[turn][v][l]));
-    const int place = REVERSE ? ranks - 1 - rank : rank;  // of this CTA in the order
-    if (order == kGatedWarps - 1) {
-      const Map all = then(before, map);
-      for (int r = 0; r < ranks; ++r) send(&tiles[turn][place][l], r, all);
-    }
-    if (ranks > 1) {
-      cluster_arrive();
-      cluster_wait();
-    } else {
-      __syncthreads();
-    }
-    float2 h = *carry;
-    for (int i = 0; i < place; ++i) h = through(load_map(&tiles[turn][i][l]), h);
-    const float2 start = through(before, h);
-    for (int i = place; i < ranks; ++i) h = through(load_map(&tiles[turn][i][l]), h);
-    *carry = h;
-    return start;
-  }
-};
-
 #endif
 
-// CTAs of a cluster: the power of two with the fewest rounds of tiles, counted
-// over the waves of CTAs that the GPU holds at once; of equal ones the smallest.
+// CTAs of a cluster: the power of two with the least time, counted in rounds of
+// tiles over the waves of CTAs that the GPU holds at once; of equal ones the
+// smallest.  A round of a cluster, whose warps all wait for the other CTAs,
+// counts twice that of a CTA alone (1.5 times in the longer backward rounds):
+// 64 x 512 tokens of 4096 channels forward take 186 us alone and 257 us in
+// pairs, 2 x 32k of 1024 channels 470 us alone and 139 us in clusters of 8.
 inline int gated_cluster(int64_t units, int tokens, bool f32, bool backward) {
   const int tile = gated_tile(f32, backward);
   const int64_t slots = (int64_t)kOpsSms * gated_resident(f32, backward), tiles = ((int64_t)tokens + tile - 1) / tile;
   int64_t best = 0;
   int c = 1;
   for (int n = 1; n <= kGatedCluster; n *= 2) {
-    const int64_t cost = (units * n + slots - 1) / slots * ((tiles + n - 1) / n);
+    const int64_t cost = (units * n + slots - 1) / slots * ((tiles + n - 1) / n) * (n == 1 ? 2 : backward ? 3 : 4);
     if (n == 1 || cost < best) {
       best = cost;
       c = n;
