@@ -169,20 +169,6 @@ struct Lane {
 
 // ------------------------------------------------- a warp's shared memory
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* to, const void* from, int bytes) {
-  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(BYTES), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int PENDING>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
-}
-
 // TOK rows of a slab, of one warp.
 template <typename T, int TOK>
 struct Rows {

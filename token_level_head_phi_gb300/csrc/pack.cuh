@@ -50,6 +50,22 @@ struct Pack {
   }
 };
 
+// Asynchronous copies into shared memory: `bytes` of BYTES (4, 8 or 16), zeros
+// behind them.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from, int bytes) {
+  const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(BYTES), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
 // Entry i of a parameter vector that is bf16 or float32.
 __device__ __forceinline__ float param_at(const void* p, int is_f32, int64_t i) {
   return is_f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);

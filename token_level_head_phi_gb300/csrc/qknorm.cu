@@ -44,22 +44,24 @@ struct QkArgs {
 };
 
 // Columns of a slot's two vectors.  ACROSS pairs entry i of the first with
-// entry i of the second; otherwise neighbours inside a vector are paired.
+// entry i of the second; otherwise neighbours inside a vector are paired.  Only
+// single entries of adjacent pairs are next to one another: neighbouring threads
+// read neighbouring vectors.
 template <int VEC, bool ACROSS>
 __device__ __forceinline__ void columns(const QkArgs& a, int slot, int* lo, int* hi) {
-  if (ACROSS && !a.adjacent) {
-    const int rot = a.half / VEC;
-    if (slot < rot) {
-      *lo = slot * VEC;
-      *hi = a.half + slot * VEC;
-      return;
-    }
-    slot -= rot;
-    *lo = 2 * a.half + slot * 2 * VEC;
-  } else {
-    *lo = slot * 2 * VEC;
+  if (ACROSS && a.adjacent) {
+    *lo = 2 * slot;
+    *hi = 2 * slot + 1;
+    return;
   }
-  *hi = *lo + VEC;
+  const int rot = ACROSS ? a.half / VEC : 0;  // slots that are rotated across
+  if (slot < rot) {
+    *lo = slot * VEC;
+    *hi = a.half + slot * VEC;
+  } else {
+    *lo = 2 * rot * VEC + (slot - rot) * VEC;
+    *hi = *lo + (a.slots - rot) * VEC;
+  }
 }
 
 // A slot's 2 VEC values, as pairs of neighbours where there are any.
@@ -194,22 +196,29 @@ struct Values {
 // What a slot's values are multiplied with by Values::turn: cosines (in `c`) and
 // sines (in `s`, the second one's with the sign turned, so that turn adds them)
 // times the values' weights; 1 and 0 where nothing is rotated.
-template <int VEC, bool ACROSS>
-__device__ __forceinline__ void turns_of(const QkArgs& a, const uint64_t* turns, int64_t pos, int lo, float sign,
+//
+// Rows of bf16 take the approximate sine and cosine, off by 2^-21 at most within
+// half a turn (5e-7 of a pair, whose entries are rounded to 2^-9 of themselves).
+template <typename T, int VEC, bool ACROSS>
+__device__ __forceinline__ void turns_of(const QkArgs& a, const uint64_t* turns, int64_t pos, const int (&col)[2], float sign,
                                          Values<VEC, ACROSS>* c, Values<VEC, ACROSS>* s) {
-  const int first = ACROSS && !a.adjacent ? lo : lo / 2;  // pair of the first entry
-  const bool rotated = ACROSS && !a.adjacent ? lo < a.half : true;
   float fc[2 * VEC], fs[2 * VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
     float cs = 1.f, sn = 0.f;
-    if (rotated && first + i < a.half) {
-      const uint64_t phase = (uint64_t)pos * turns[first + i];
-      sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &sn, &cs);
+    const int j = ACROSS ? i : 2 * i, k = ACROSS ? i + VEC : 2 * i + 1;  // the pair's entries
+    const int entry = j < VEC ? col[0] + j : col[1] + j - VEC;           // the first one's column
+    const int pair = ACROSS && !a.adjacent ? entry : entry / 2;
+    if (pair < a.half && (!ACROSS || a.adjacent || col[0] < a.half)) {
+      const uint64_t phase = (uint64_t)pos * turns[pair];
+      const float half_turns = (float)(int32_t)(phase >> 32) * 4.656612873077393e-10f;  // in [-1, 1)
+      if constexpr (sizeof(T) == 2)
+        __sincosf(half_turns * 3.14159265f, &sn, &cs);
+      else
+        sincospif(half_turns, &sn, &cs);
       cs *= a.amp;
       sn *= a.amp * sign;
     }
-    const int j = ACROSS ? i : 2 * i, k = ACROSS ? i + VEC : 2 * i + 1;
     fc[j] = fc[k] = cs;
     fs[j] = sn;
     fs[k] = -sn;
@@ -235,108 +244,211 @@ __device__ __forceinline__ void weights_of(const QkArgs& a, int which, const int
 }
 
 // CTAs that an SM holds.
-constexpr int kFwdResident = 2, kBwdResident = 2;
+constexpr int kResident = 2;
+
+// A thread's vectors of the next rows: asynchronous copies into places of its own
+// in shared memory, STEPS - 1 steps of ROWS rows ahead; elements of 2 bytes, which
+// cannot be copied so, are read a row ahead into registers.
+template <typename T, int VEC, int E, int ROWS, int STEPS>
+struct Ring {
+  static constexpr int kBytes = VEC * (int)sizeof(T);
+  static constexpr bool kAsync = kBytes >= 4;
+  static constexpr size_t kSmem = kAsync ? (size_t)STEPS * ROWS * E * 2 * kBytes * 256 : 0;
+  static_assert(kSmem <= 100 * 1024, "two CTAs on an SM");
+  unsigned char* base;
+
+  __device__ __forceinline__ explicit Ring(unsigned char* smem) : base(smem) {}
+  __device__ __forceinline__ unsigned char* place(int step, int row, int i) const {
+    return base + ((((step * ROWS + row) * 2 * E) + i) * 256 + threadIdx.x) * kBytes;
+  }
+  // Starts vector i of a row; zeros where it does not exist.
+  __device__ __forceinline__ void start(int step, int row, int i, const T* from, bool exists, const T* any) {
+    if constexpr (kAsync)
+      copy_async<kBytes>(place(step, row, i), exists ? from : any, exists ? kBytes : 0);
+  }
+  __device__ __forceinline__ void take(int step, int row, int i, Pack<T, VEC>* to) const {
+    if constexpr (kBytes == 16)
+      *reinterpret_cast<uint4*>(to->v) = *reinterpret_cast<const uint4*>(place(step, row, i));
+    else if constexpr (kBytes == 8)
+      *reinterpret_cast<uint2*>(to->v) = *reinterpret_cast<const uint2*>(place(step, row, i));
+    else
+      *reinterpret_cast<uint32_t*>(to->v) = *reinterpret_cast<const uint32_t*>(place(step, row, i));
+  }
+};
+
+constexpr int kFwdRows = 4, kFwdSteps = 2, kBwdSteps = 3;
+template <typename T, int VEC, int E>
+using FwdRing = Ring<T, VEC, E, kFwdRows, kFwdSteps>;
 
 template <typename T, int VEC, bool ACROSS, int E>
-__global__ void __launch_bounds__(256, kFwdResident) qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
-  constexpr int R = E > 1 ? 2 : 4;  // rows in flight
+__global__ void __launch_bounds__(256, kResident) qknorm_fwd_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int R = kFwdRows, kSteps = kFwdSteps;
   using V = Values<VEC, ACROSS>;
+  using Rows = FwdRing<T, VEC, E>;
+  extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ uint64_t turns[MHLA_ROTARY_MAX_PAIRS];
   for (int i = threadIdx.x; i < a.half; i += blockDim.x) turns[i] = a.table.turns[i];
   __syncthreads();
-  const int lane = threadIdx.x & (a.group - 1);
-  const int64_t token = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> a.lanes_shift;
-  const bool live = token < (int64_t)a.batch * a.tokens;
-  const int64_t b = live ? token / a.tokens : 0;
-  const int t = live ? (int)(token - b * a.tokens) : 0;
-  const int64_t pos = position_of(a, b, t);
+  Rows ring(dynamic);
+  const int lane = threadIdx.x & (a.group - 1), per = blockDim.x >> a.lanes_shift;
   int col[E][2];
   bool in[E][2];
-  V cs[E], sn[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int slot = lane + e * a.group;
     columns<VEC, ACROSS>(a, slot, &col[e][0], &col[e][1]);
-    turns_of<VEC, ACROSS>(a, turns, pos, col[e][0], 1.f, &cs[e], &sn[e]);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) in[e][k] = live && slot < a.slots && col[e][k] < a.dim;
+    for (int k = 0; k < 2; ++k) in[e][k] = slot < a.slots && col[e][k] < a.dim;
   }
-  const int first = blockIdx.y * a.heads_per_thread, last = min(first + a.heads_per_thread, a.heads[0] + a.heads[1]);
+  const int64_t all = (int64_t)a.batch * a.tokens, stride = (int64_t)gridDim.x * per;
+  const int total = a.heads[0] + a.heads[1];
+  const int first = blockIdx.y * a.heads_per_thread, last = min(first + a.heads_per_thread, total);
+  // q's heads, then k's, in steps that do not mix them
+  const int split = min(max(a.heads[0], first), last);
+  auto next = [&](int h) { return h < split ? min(h + R, split) : h + R; };
+
+  // a token's rows: those that are computed, and those that are fetched ahead
+  struct Place {
+    int64_t base, b;
+    int t, h;
+    bool live;
+  };
+  auto locate = [&](Place& p, int64_t base) {
+    const int64_t token = base + (threadIdx.x >> a.lanes_shift);
+    p.base = base;
+    p.h = first;
+    p.live = token < all;
+    p.b = p.live ? token / a.tokens : 0;
+    p.t = p.live ? (int)(token - p.b * a.tokens) : 0;
+  };
+  auto row_of = [&](const Place& p, int h) {
+    const int which = h >= a.heads[0];
+    return static_cast<const T*>(a.x[which]) + p.b * a.sx[which].batch + p.t * a.sx[which].token +
+           (h - (which ? a.heads[0] : 0)) * a.sx[which].head;
+  };
+  Place ahead, now;
+  locate(ahead, (int64_t)blockIdx.x * per);
+  int put = 0, got = 0;
+  auto fetch = [&] {
+    if (Rows::kAsync && ahead.base < all) {
+      const int end = next(ahead.h);
+      const T* any = row_of(ahead, ahead.h);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bool exists = ahead.live && ahead.h + r < end;
+        const T* from = row_of(ahead, exists ? ahead.h + r : ahead.h);
+#pragma unroll
+        for (int i = 0; i < 2 * E; ++i) ring.start(put, r, i, from + col[i / 2][i % 2], exists && in[i / 2][i % 2], any);
+      }
+      ahead.h = end;
+      if (end >= last) locate(ahead, ahead.base + stride);
+    }
+    copies_commit();
+    put = put + 1 < kSteps ? put + 1 : 0;
+  };
+  if (Rows::kAsync)
+    for (int i = 0; i < kSteps - 1; ++i) fetch();
+
+  locate(now, (int64_t)blockIdx.x * per);
+  int64_t pos = position_of(a, now.b, now.t);
+  for (int64_t base = (int64_t)blockIdx.x * per; base < all; base += stride) {
+    V cs[E], sn[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) turns_of<T, VEC, ACROSS>(a, turns, pos, col[e], 1.f, &cs[e], &sn[e]);
+    Place then;
+    locate(then, base + stride);
+    pos = position_of(a, then.b, then.t);  // a token ahead
 #pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    int h = max(first - (which ? a.heads[0] : 0), 0);
-    const int end = which ? last - a.heads[0] : min(last, a.heads[0]);
-    if (h >= end) continue;  // the same for the whole grid row
-    V c[E], s[E];  // with the weights
+    for (int which = 0; which < 2; ++which) {
+      const int end = which ? last : split;
+      int h = which ? split : first;
+      if (h >= end) continue;  // the same for the whole grid row
+      V c[E], s[E];  // with the weights
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      V w;
-      weights_of(a, which, col[e], in[e], &w);
-      c[e].product(cs[e], w);
-      s[e].product(sn[e], w);
-    }
-    const int64_t xh = a.sx[which].head, yh = a.sy[which].head;
-    const T* src = static_cast<const T*>(a.x[which]) + b * a.sx[which].batch + t * a.sx[which].token + h * xh;
-    T* dst = static_cast<T*>(a.y[which]) + b * a.sy[which].batch + t * a.sy[which].token + h * yh;
-    for (; h < end; h += R, src += R * xh, dst += R * yh) {
-      Pack<T, VEC> raw[R][E][2];
+      for (int e = 0; e < E; ++e) {
+        V w;
+        weights_of(a, which, col[e], in[e], &w);
+        c[e].product(cs[e], w);
+        s[e].product(sn[e], w);
+      }
+      const int64_t yh = a.sy[which].head;
+      T* dst = static_cast<T*>(a.y[which]) + now.b * a.sy[which].batch + now.t * a.sy[which].token +
+               (h - (which ? a.heads[0] : 0)) * yh;
+      for (; h < end; h += R, dst += R * yh) {
+        Pack<T, VEC> raw[R][E][2];
+        if constexpr (Rows::kAsync) {
+          fetch();
+          copies_wait<kSteps - 1>();
 #pragma unroll
-      for (int r = 0; r < R; ++r)
+          for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int e = 0; e < E; ++e)
+            for (int i = 0; i < 2 * E; ++i) ring.take(got, r, i, &raw[r][i / 2][i % 2]);
+          got = got + 1 < kSteps ? got + 1 : 0;
+        } else {
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (in[e][k] && h + r < end)
-              raw[r][e][k].load(src + r * xh + col[e][k], true);
-            else
-              raw[r][e][k].zero();
-      float sum[R];
+          for (int r = 0; r < R; ++r)
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        sum[r] = 0.f;
+            for (int i = 0; i < 2 * E; ++i) {
+              raw[r][i / 2][i % 2].zero();
+              if (in[i / 2][i % 2] && now.live && h + r < end)
+                raw[r][i / 2][i % 2].load(row_of(now, h + r) + col[i / 2][i % 2], true);
+            }
+        }
+        float sum[R];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          V v;
-          v.read(raw[r][e]);
-          sum[r] += v.dot(v);
+        for (int r = 0; r < R; ++r) {
+          sum[r] = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            V v;
+            v.read(raw[r][e]);
+            sum[r] += v.dot(v);
+          }
+        }
+        for (int o = a.group / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int r = 0; r < R; ++r) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (h + r >= end) break;  // the same for all lanes
+          const float rstd = rsqrtf(fmaf(sum[r], a.inv_dim, a.eps));
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            V v;
+            v.read(raw[r][e]);
+            v.scale(rstd);
+            v.turn(c[e], s[e]);
+            Pack<T, VEC> o[2];
+            v.write(o);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (in[e][k] && now.live) o[k].store(dst + r * yh + col[e][k], true);
+          }
         }
       }
-      for (int o = a.group / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int r = 0; r < R; ++r) sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (h + r >= end) break;  // the same for all lanes
-        const float rstd = rsqrtf(fmaf(sum[r], a.inv_dim, a.eps));
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          V v;
-          v.read(raw[r][e]);
-          v.scale(rstd);
-          v.turn(c[e], s[e]);
-          Pack<T, VEC> o[2];
-          v.write(o);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (in[e][k]) o[k].store(dst + r * yh + col[e][k], true);
-        }
-      }
     }
+    now = then;
   }
 }
 
 // CTAs take the tokens in turn, those below ctas[0] q's rows and the others
 // k's, and keep the sums of dw of their columns in registers.
+template <typename T, int VEC, int E>
+using BwdRing = Ring<T, VEC, 2 * E, 1, kBwdSteps>;  // x's vectors, then dy's
+
 template <typename T, int VEC, bool ACROSS, int E>
-__global__ void __launch_bounds__(256, kBwdResident) qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
-  constexpr int R = E * VEC > 4 ? 1 : 2;  // rows of a step; the next step's are on their way
+__global__ void __launch_bounds__(256, kResident) qknorm_bwd_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int kSteps = kBwdSteps;
   using V = Values<VEC, ACROSS>;
+  using Rows = BwdRing<T, VEC, E>;
+  extern __shared__ __align__(16) unsigned char dynamic[];
   __shared__ uint64_t turns[MHLA_ROTARY_MAX_PAIRS];
   __shared__ float sums[8][kMaxDim];
   for (int i = threadIdx.x; i < a.half; i += blockDim.x) turns[i] = a.table.turns[i];
   __syncthreads();
+  Rows ring(dynamic);
   const int which = (int)blockIdx.x >= a.ctas[0];
-  const int cta = blockIdx.x - (which ? a.ctas[0] : 0), ctas = a.ctas[which], heads = a.heads[which];
+  const int cta = blockIdx.x - (which ? a.ctas[0] : 0), heads = a.heads[which];
   const int lane = threadIdx.x & (a.group - 1), per = blockDim.x >> a.lanes_shift;
   int col[E][2];
   bool in[E][2];
@@ -350,84 +462,123 @@ __global__ void __launch_bounds__(256, kBwdResident) qknorm_bwd_kernel(const __g
     weights_of(a, which, col[e], in[e], &w[e]);
     dw[e].fill(0.f);
   }
-  const int64_t all = (int64_t)a.batch * a.tokens, xh = a.sx[which].head, dyh = a.sdy[which].head, dxh = a.sy[which].head;
-  // every thread of the CTA makes the same number of turns
-  for (int64_t base = (int64_t)cta * per; base < all; base += (int64_t)ctas * per) {
+  const int64_t all = (int64_t)a.batch * a.tokens, stride = (int64_t)a.ctas[which] * per, start = (int64_t)cta * per;
+  const int64_t xh = a.sx[which].head, dyh = a.sdy[which].head, dxh = a.sy[which].head;
+
+  // the token whose rows are fetched ahead
+  int64_t ahead = start;
+  const T *ax = nullptr, *ady = nullptr;
+  bool alive = false;
+  int ah = 0, put = 0, got = 0;
+  auto point = [&](int64_t base, const T** x, const T** dy) {
     const int64_t token = base + (threadIdx.x >> a.lanes_shift);
     const bool live = token < all;
-    const int64_t b = live ? token / a.tokens : 0;
-    const int t = live ? (int)(token - b * a.tokens) : 0;
-    const T* x = static_cast<const T*>(a.x[which]) + b * a.sx[which].batch + t * a.sx[which].token;
-    const T* dy = static_cast<const T*>(a.dy[which]) + b * a.sdy[which].batch + t * a.sdy[which].token;
+    const int64_t b = live ? token / a.tokens : 0, t = live ? token - b * a.tokens : 0;
+    *x = static_cast<const T*>(a.x[which]) + b * a.sx[which].batch + t * a.sx[which].token;
+    *dy = static_cast<const T*>(a.dy[which]) + b * a.sdy[which].batch + t * a.sdy[which].token;
+    return live;
+  };
+  auto fetch = [&] {
+    if (Rows::kAsync && ahead < all) {
+      if (ah == 0) alive = point(ahead, &ax, &ady);
+#pragma unroll
+      for (int i = 0; i < 2 * E; ++i) {
+        const bool exists = alive && in[i / 2][i % 2];
+        ring.start(put, 0, i, ax + col[i / 2][i % 2], exists, ax);
+        ring.start(put, 0, 2 * E + i, ady + col[i / 2][i % 2], exists, ady);
+      }
+      ax += xh;
+      ady += dyh;
+      if (++ah == heads) {
+        ah = 0;
+        ahead += stride;
+      }
+    }
+    copies_commit();
+    put = put + 1 < kSteps ? put + 1 : 0;
+  };
+  if (Rows::kAsync)
+    for (int i = 0; i < kSteps - 1; ++i) fetch();
+
+  // every thread of the CTA makes the same number of turns
+  for (int64_t base = start; base < all; base += stride) {
+    const T *x, *dy;
+    const bool live = point(base, &x, &dy);
+    const int64_t token = live ? base + (threadIdx.x >> a.lanes_shift) : 0, b = token / a.tokens, t = token - b * a.tokens;
     T* dx = static_cast<T*>(a.y[which]) + b * a.sy[which].batch + t * a.sy[which].token;
-    Pack<T, VEC> nx[R][E][2], nd[R][E][2];
-    auto fetch = [&](int h) {
-#pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (in[e][k] && live && h + r < heads) {
-              nx[r][e][k].load(x + (h + r) * xh + col[e][k], true);
-              nd[r][e][k].load(dy + (h + r) * dyh + col[e][k], true);
-            } else {
-              nx[r][e][k].zero();
-              nd[r][e][k].zero();
-            }
-    };
-    fetch(0);
-    const int64_t pos = position_of(a, b, t);
+    const int64_t pos = position_of(a, b, (int)t);
     V cs[E], sn[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) turns_of<VEC, ACROSS>(a, turns, pos, col[e][0], -1.f, &cs[e], &sn[e]);
-    for (int h = 0; h < heads; h += R) {
-      V v[R][E];
-      Pack<T, VEC> rx[R][E][2];
-      float sum[R], along[R];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        sum[r] = along[r] = 0.f;
+    for (int e = 0; e < E; ++e) turns_of<T, VEC, ACROSS>(a, turns, pos, col[e], -1.f, &cs[e], &sn[e]);
+    Pack<T, VEC> nx[Rows::kAsync ? 1 : E][2], nd[Rows::kAsync ? 1 : E][2];
+    auto read = [&](int h) {
+      if constexpr (!Rows::kAsync) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          v[r][e].read(nd[r][e]);
-          v[r][e].turn(cs[e], sn[e]);  // t
-          V xv, g;
-          xv.read(nx[r][e]);
-          g.product(v[r][e], w[e]);
-          sum[r] += xv.dot(xv);
-          along[r] += g.dot(xv);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) rx[r][e][k] = nx[r][e][k];
+          for (int k = 0; k < 2; ++k) {
+            nx[e][k].zero();
+            nd[e][k].zero();
+            if (in[e][k] && live && h < heads) {
+              nx[e][k].load(x + h * xh + col[e][k], true);
+              nd[e][k].load(dy + h * dyh + col[e][k], true);
+            }
+          }
         }
       }
-      if (h + R < heads) fetch(h + R);
-      for (int o = a.group / 2; o > 0; o >>= 1)
+    };
+    read(0);
+    for (int h = 0; h < heads; ++h, dx += dxh) {
+      Pack<T, VEC> rx[E][2];
+      V v[E];
+      float sum = 0.f, along = 0.f;
+      if constexpr (Rows::kAsync) {
+        fetch();
+        copies_wait<kSteps - 1>();
+      }
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], o);
-          along[r] += __shfl_xor_sync(0xffffffffu, along[r], o);
+      for (int e = 0; e < E; ++e) {
+        Pack<T, VEC> rd[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if constexpr (Rows::kAsync) {
+            ring.take(got, 0, 2 * e + k, &rx[e][k]);
+            ring.take(got, 0, 2 * E + 2 * e + k, &rd[k]);
+          } else {
+            rx[e][k] = nx[e][k];
+            rd[k] = nd[e][k];
+          }
         }
+        v[e].read(rd);
+        v[e].turn(cs[e], sn[e]);  // t
+        V xv, g;
+        xv.read(rx[e]);
+        g.product(v[e], w[e]);
+        sum += xv.dot(xv);
+        along += g.dot(xv);
+      }
+      got = got + 1 < kSteps ? got + 1 : 0;
+      read(h + 1);
+      for (int o = a.group / 2; o > 0; o >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        along += __shfl_xor_sync(0xffffffffu, along, o);
+      }
+      // a row that is not there adds nothing, although its rstd may be infinite
+      const float rstd = live ? rsqrtf(fmaf(sum, a.inv_dim, a.eps)) : 0.f;
+      const float mean = along * rstd * a.inv_dim;  // of g xh
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const bool row = live && h + r < heads;
-        // a row that is not there adds nothing, although its rstd may be infinite
-        const float rstd = row ? rsqrtf(fmaf(sum[r], a.inv_dim, a.eps)) : 0.f;
-        const float mean = along[r] * rstd * a.inv_dim;  // of g xh
+      for (int e = 0; e < E; ++e) {
+        V xv;
+        xv.read(rx[e]);
+        xv.scale(rstd);  // xh
+        dw[e].add_product(v[e], xv);
+        v[e].product(v[e], w[e]);
+        v[e].combine(rstd, -mean * rstd, xv);
+        Pack<T, VEC> o[2];
+        v[e].write(o);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          V xv;
-          xv.read(rx[r][e]);
-          xv.scale(rstd);  // xh
-          dw[e].add_product(v[r][e], xv);
-          v[r][e].product(v[r][e], w[e]);
-          v[r][e].combine(rstd, -mean * rstd, xv);
-          Pack<T, VEC> o[2];
-          v[r][e].write(o);
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (in[e][k] && row) o[k].store(dx + (h + r) * dxh + col[e][k], true);
-        }
+        for (int k = 0; k < 2; ++k)
+          if (in[e][k] && live) o[k].store(dx + col[e][k], true);
       }
     }
   }
@@ -483,7 +634,9 @@ void share_ctas(QkArgs* a) {
   const int64_t most = (all + per - 1) / per;  // one turn each
   const int total = a->heads[0] + a->heads[1];
   for (int i = 0; i < 2; ++i) {
-    int64_t n = total ? (int64_t)kBwdResident * kOpsSms * a->heads[i] / total : 0;
+    // a token's sines and positions count about two rows
+    const int64_t weight[2] = {a->heads[0] ? a->heads[0] + 2 : 0, a->heads[1] ? a->heads[1] + 2 : 0};
+    int64_t n = total ? (int64_t)kResident * kOpsSms * weight[i] / (weight[0] + weight[1]) : 0;
     if (n < 1) n = 1;
     if (n > most) n = most;
     a->ctas[i] = a->heads[i] && all ? (int)n : 0;
@@ -493,21 +646,28 @@ void share_ctas(QkArgs* a) {
 template <typename T, int VEC, bool ACROSS, int E>
 mhla_status launch(QkArgs& a, bool backward, cudaStream_t s) {
   if (backward) {
-    qknorm_bwd_kernel<T, VEC, ACROSS, E><<<a.ctas[0] + a.ctas[1], 256, 0, s>>>(a);
+    auto kernel = qknorm_bwd_kernel<T, VEC, ACROSS, E>;
+    constexpr size_t smem = BwdRing<T, VEC, E>::kSmem;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return record_cuda_error(e);
+    kernel<<<a.ctas[0] + a.ctas[1], 256, smem, s>>>(a);
     return launch_status();
   }
   // Heads are shared out over threads only where there are too few tokens to
   // fill the GPU, as each share forms the sines again.
-  const int64_t items = (int64_t)a.batch * a.tokens * a.group, want = (int64_t)kOpsSms * kFwdResident * 256;
+  auto kernel = qknorm_fwd_kernel<T, VEC, ACROSS, E>;
+  constexpr size_t smem = FwdRing<T, VEC, E>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  const int64_t slots = (int64_t)kOpsSms * kResident, per = 256 / a.group;
+  int64_t blocks = ((int64_t)a.batch * a.tokens + per - 1) / per;
   const int total = a.heads[0] + a.heads[1];
-  int64_t parts = (want + items - 1) / items;
-  if (parts > total) parts = total;
+  int64_t parts = slots / blocks;
+  parts = parts < 1 ? 1 : parts > total ? total : parts;
   a.heads_per_thread = (int)((total + parts - 1) / parts);
   parts = (total + a.heads_per_thread - 1) / a.heads_per_thread;
-  const int threads = items * parts < want ? 64 : 256;
-  const int64_t blocks = (items + threads - 1) / threads;
-  if (blocks > 0x7fffffff || parts > 65535) return MHLA_ERR_UNSUPPORTED;
-  qknorm_fwd_kernel<T, VEC, ACROSS, E><<<dim3((unsigned)blocks, (unsigned)parts), threads, 0, s>>>(a);
+  if (blocks > slots) blocks = slots;
+  kernel<<<dim3((unsigned)blocks, (unsigned)parts), 256, smem, s>>>(a);
   return launch_status();
 }
 
@@ -516,7 +676,7 @@ mhla_status launch(QkArgs& a, bool backward, cudaStream_t s) {
 int vector_of(int dim, int pairs, int style, int elem, int align) {
   const int unit = style == MHLA_ROTARY_HALF ? pairs : 2 * pairs;
   for (int v = 16 / elem; v > 1; v /= 2)
-    if (unit % v == 0 && dim % v == 0 && align >= v * elem && 2 * v * elem >= 16) return v;
+    if (unit % v == 0 && dim % v == 0 && align >= v * elem) return v;
   return 1;
 }
 
@@ -533,20 +693,28 @@ void shape_rows(QkArgs* a, int vec, int style) {
   }
 }
 
+template <typename T, int VEC>
+mhla_status with_style(QkArgs& a, int style, bool backward, cudaStream_t s) {
+  const bool half = style == MHLA_ROTARY_HALF;
+  if constexpr (VEC >= 4) {  // at most 32 slots
+    return half ? launch<T, VEC, true, 1>(a, backward, s) : launch<T, VEC, false, 1>(a, backward, s);
+  } else if constexpr (VEC == 2) {
+    if (a.slots <= 32) return half ? launch<T, 2, true, 1>(a, backward, s) : launch<T, 2, false, 1>(a, backward, s);
+    return half ? launch<T, 2, true, 2>(a, backward, s) : launch<T, 2, false, 2>(a, backward, s);
+  } else {
+    if (a.slots <= 32) return launch<T, 1, true, 1>(a, backward, s);
+    if (a.slots <= 64) return launch<T, 1, true, 2>(a, backward, s);
+    return launch<T, 1, true, 4>(a, backward, s);
+  }
+}
+
 template <typename T>
 mhla_status dispatch(QkArgs& a, int style, int vec, bool backward, cudaStream_t s) {
-  constexpr int W = 16 / sizeof(T);
-  const bool half = style == MHLA_ROTARY_HALF;
-  if (vec == W)  // at most 32 slots
-    return half ? launch<T, W, true, 1>(a, backward, s) : launch<T, W, false, 1>(a, backward, s);
-  if (vec == W / 2) {
-    if (a.slots <= 32)
-      return half ? launch<T, W / 2, true, 1>(a, backward, s) : launch<T, W / 2, false, 1>(a, backward, s);
-    return half ? launch<T, W / 2, true, 2>(a, backward, s) : launch<T, W / 2, false, 2>(a, backward, s);
-  }
-  if (a.slots <= 32) return launch<T, 1, true, 1>(a, backward, s);
-  if (a.slots <= 64) return launch<T, 1, true, 2>(a, backward, s);
-  return launch<T, 1, true, 4>(a, backward, s);
+  if constexpr (sizeof(T) == 2)
+    if (vec == 8) return with_style<T, 8>(a, style, backward, s);
+  if (vec == 4) return with_style<T, 4>(a, style, backward, s);
+  if (vec == 2) return with_style<T, 2>(a, style, backward, s);
+  return with_style<T, 1>(a, style, backward, s);
 }
 
 mhla_status check_params(const mhla_qknorm_params* p, const mhla_rotary_table* table) {
@@ -618,8 +786,8 @@ int least_alignment(const RowTensor* t, int n) {
 // alignment and the presence of k: rows by 32 threads take the most turns, and
 // rounding up the smaller share adds one.
 int64_t most_ctas(const mhla_qknorm_params* p) {
-  const int64_t all = (int64_t)p->batch * p->tokens, turns = 2 * ((all + 7) / 8);
-  const int64_t most = kBwdResident * kOpsSms + 1;
+  const int64_t all = (int64_t)p->batch * p->tokens, turns = 2 * ((all + 8 - 1) / (8));
+  const int64_t most = kResident * kOpsSms + 1;
   return turns < most ? turns : most;
 }
 

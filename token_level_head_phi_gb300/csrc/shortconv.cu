@@ -12,14 +12,14 @@
 namespace mhla {
 namespace {
 
-constexpr int kVec = 4;       // channels of a thread
+
 constexpr int kThreads = 256;
 constexpr int kRows = 4;      // rows of a step; the next step's are on their way
 
 enum { kForward, kBackward, kStep };
 
-// CTAs that an SM holds.
-constexpr int resident(int what) { return what == kForward ? 3 : 2; }
+// CTAs that an SM holds: their registers.
+constexpr int resident(int what, int elem) { return what == kForward && elem == 2 ? 3 : 2; }
 
 struct ConvArgs {
   const void *x, *dout, *w, *bias, *state_in, *dstate_out;
@@ -29,6 +29,7 @@ struct ConvArgs {
   float* partial;  // [rows][K + 1][D]
   int B, N, D;
   int w_f32, silu;
+  int width;           // channels of a thread
   int vecs;            // of a row
   int across, down;    // of a CTA: vectors and segments, powers of two
   int across_shift;
@@ -51,38 +52,38 @@ struct Place {
     const int64_t at = (int64_t)blockIdx.y * p.down + (threadIdx.x >> p.across_shift);
     b = (int)(at / p.segments);
     first = (int)(at - (int64_t)b * p.segments) * p.seg;
-    ch = vec * kVec;
-    n = min(kVec, p.D - ch);
+    ch = vec * p.width;
+    n = min(p.width, p.D - ch);
     live = vec < p.vecs && b < p.B;
   }
 };
 
 // Channel pairs of a thread's weights and bias.
-template <typename W, int K>
-__device__ __forceinline__ void load_weights_as(const ConvArgs& p, const Place& at, float (&w)[kVec][K], float (&bias)[kVec]) {
+template <int V, typename W, int K>
+__device__ __forceinline__ void load_weights_as(const ConvArgs& p, const Place& at, float (&w)[V][K], float (&bias)[V]) {
   const W *pw = static_cast<const W*>(p.w) + (int64_t)at.ch * K, *pb = static_cast<const W*>(p.bias) + at.ch;
-  if (at.n == kVec) {
+  if (at.n == V) {
 #pragma unroll
-    for (int i = 0; i < kVec * K; ++i) w[i / K][i % K] = to_f32(pw[i]);
+    for (int i = 0; i < V * K; ++i) w[i / K][i % K] = to_f32(pw[i]);
 #pragma unroll
-    for (int c = 0; c < kVec; ++c) bias[c] = p.bias ? to_f32(pb[c]) : 0.f;
+    for (int c = 0; c < V; ++c) bias[c] = p.bias ? to_f32(pb[c]) : 0.f;
   } else {
 #pragma unroll
-    for (int i = 0; i < kVec * K; ++i) w[i / K][i % K] = i < at.n * K ? to_f32(pw[i]) : 0.f;
+    for (int i = 0; i < V * K; ++i) w[i / K][i % K] = i < at.n * K ? to_f32(pw[i]) : 0.f;
 #pragma unroll
-    for (int c = 0; c < kVec; ++c) bias[c] = p.bias && c < at.n ? to_f32(pb[c]) : 0.f;
+    for (int c = 0; c < V; ++c) bias[c] = p.bias && c < at.n ? to_f32(pb[c]) : 0.f;
   }
 }
-template <int K>
-__device__ __forceinline__ void load_weights(const ConvArgs& p, const Place& at, float2 (&w)[K][kVec / 2],
-                                             float2 (&bias)[kVec / 2]) {
-  float f[kVec][K], g[kVec];
+template <int V, int K>
+__device__ __forceinline__ void load_weights(const ConvArgs& p, const Place& at, float2 (&w)[K][V / 2],
+                                             float2 (&bias)[V / 2]) {
+  float f[V][K], g[V];
   if (p.w_f32)
-    load_weights_as<float, K>(p, at, f, g);
+    load_weights_as<V, float, K>(p, at, f, g);
   else
-    load_weights_as<__nv_bfloat16, K>(p, at, f, g);
+    load_weights_as<V, __nv_bfloat16, K>(p, at, f, g);
 #pragma unroll
-  for (int c = 0; c < kVec / 2; ++c) {
+  for (int c = 0; c < V / 2; ++c) {
 #pragma unroll
     for (int j = 0; j < K; ++j) w[j][c] = make_float2(f[2 * c][j], f[2 * c + 1][j]);
     bias[c] = make_float2(g[2 * c], g[2 * c + 1]);
@@ -98,12 +99,12 @@ __device__ __forceinline__ float2 logistic(float2 z) {
 
 // Row t of x, rows before the first token from the incoming state, zeros past
 // the length.
-template <typename T, int K>
-__device__ __forceinline__ void load_row(const ConvArgs& p, const Place& at, int t, int len, Pack<T, kVec>* r) {
+template <int V, typename T, int K>
+__device__ __forceinline__ void load_row(const ConvArgs& p, const Place& at, int t, int len, Pack<T, V>* r) {
   if (t >= len || !at.live) {
     r->zero();
   } else if (t >= 0) {
-    r->load(static_cast<const T*>(p.x) + at.b * p.sx.batch + t * p.sx.token + at.ch, p.whole && at.n == kVec, at.n);
+    r->load(static_cast<const T*>(p.x) + at.b * p.sx.batch + t * p.sx.token + at.ch, p.whole && at.n == V, at.n);
   } else if (p.state_in) {
     r->load(static_cast<const T*>(p.state_in) + ((int64_t)at.b * (K - 1) + t + K - 1) * p.D + at.ch, false, at.n);
   } else {
@@ -111,43 +112,48 @@ __device__ __forceinline__ void load_row(const ConvArgs& p, const Place& at, int
   }
 }
 
-template <typename T, int K>
-__global__ void __launch_bounds__(kThreads, resident(kForward)) conv_fwd_kernel(const __grid_constant__ ConvArgs p) {
-  constexpr int H = kVec / 2;
+template <typename T, int K, int V>
+__global__ void __launch_bounds__(kThreads, resident(kForward, sizeof(T))) conv_fwd_kernel(const __grid_constant__ ConvArgs p) {
+  constexpr int H = V / 2;
   const Place at(p);
   if (!at.live) return;
   const int len = length_of(p, at.b), last = min(at.first + p.seg, p.N);
   float2 w[K][H], bias[H];
-  load_weights<K>(p, at, w, bias);
+  load_weights<V, K>(p, at, w, bias);
   float2 win[K - 1][H];  // rows t - K + 1 .. t - 1
-  Pack<T, kVec> r;
+  Pack<T, V> r;
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) {
-    load_row<T, K>(p, at, at.first - (K - 1) + j, len, &r);
+    load_row<V, T, K>(p, at, at.first - (K - 1) + j, len, &r);
 #pragma unroll
     for (int c = 0; c < H; ++c) win[j][c] = pair_of(r, c);
   }
   const T* x = static_cast<const T*>(p.x) + at.b * p.sx.batch + at.ch;
   T* out = static_cast<T*>(p.out) + at.b * p.so.batch + at.ch;
-  const bool whole = p.whole && at.n == kVec;
+  const bool whole = p.whole && at.n == V;
   const int inside = whole ? min(last, len) : at.first;  // steps up to here need no checks
-  Pack<T, kVec> row[kRows], next[kRows];
-  auto fetch = [&](Pack<T, kVec>(&to)[kRows], int t0) {
+  Pack<T, V> row[kRows], next[kRows];
+  auto fetch = [&](Pack<T, V>(&to)[kRows], int t0) {
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       if (t0 + kRows <= inside)
         to[u].load(x + (t0 + u) * p.sx.token, true);
       else if (t0 < last)
-        load_row<T, K>(p, at, t0 + u, len, &to[u]);
+        load_row<V, T, K>(p, at, t0 + u, len, &to[u]);
     }
   };
   fetch(row, at.first);
   for (int t0 = at.first; t0 < last; t0 += kRows) {
+    if (t0 >= len) {  // padding
+      r.zero();
+      for (int t = t0; t < last; ++t) r.store(out + t * p.so.token, whole, at.n);
+      break;
+    }
     fetch(next, t0 + kRows);
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       const int t = t0 + u;
-      Pack<T, kVec> o;
+      Pack<T, V> o;
 #pragma unroll
       for (int c = 0; c < H; ++c) {
         const float2 xv = pair_of(row[u], c);
@@ -172,19 +178,19 @@ __global__ void __launch_bounds__(kThreads, resident(kForward)) conv_fwd_kernel(
   }
   if (p.state_out && at.first == 0) {
     // the same thread that read state_in, which this may be
-    Pack<T, kVec> keep[K - 1];
+    Pack<T, V> keep[K - 1];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) load_row<T, K>(p, at, len - (K - 1) + j, len, &keep[j]);
+    for (int j = 0; j < K - 1; ++j) load_row<V, T, K>(p, at, len - (K - 1) + j, len, &keep[j]);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j)
       keep[j].store(static_cast<T*>(p.state_out) + ((int64_t)at.b * (K - 1) + j) * p.D + at.ch, false, at.n);
   }
 }
 
-template <typename T, int K>
-__global__ void __launch_bounds__(kThreads, resident(kBackward)) conv_bwd_kernel(const __grid_constant__ ConvArgs p) {
-  constexpr int H = kVec / 2;
-  extern __shared__ float sums[];  // [down][(K + 1) * kVec][across]
+template <typename T, int K, int V>
+__global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T))) conv_bwd_kernel(const __grid_constant__ ConvArgs p) {
+  constexpr int H = V / 2;
+  extern __shared__ float sums[];  // [down][(K + 1) * V][across]
   const Place at(p);
   float2 dw[K + 1][H];
 #pragma unroll
@@ -194,27 +200,27 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward)) conv_bwd_kernel
   if (at.live) {
     const int len = length_of(p, at.b), last = min(at.first + p.seg, p.N), end = last + K - 1;
     float2 w[K][H], bias[H];
-    load_weights<K>(p, at, w, bias);
+    load_weights<V, K>(p, at, w, bias);
     float2 win[K - 1][H], dz[K - 1][H];  // rows t - K + 1 .. t - 1 of x and of dL/dz
-    Pack<T, kVec> r;
+    Pack<T, V> r;
 #pragma unroll
     for (int j = 0; j < K - 1; ++j) {
-      load_row<T, K>(p, at, at.first - (K - 1) + j, len, &r);
+      load_row<V, T, K>(p, at, at.first - (K - 1) + j, len, &r);
 #pragma unroll
       for (int c = 0; c < H; ++c) {
         win[j][c] = pair_of(r, c);
         dz[j][c] = splat(0.f);
       }
     }
-    const bool whole = p.whole && at.n == kVec;
+    const bool whole = p.whole && at.n == V;
     const T* x = static_cast<const T*>(p.x) + at.b * p.sx.batch + at.ch;
     const T* dout = static_cast<const T*>(p.dout) + at.b * p.sdo.batch + at.ch;
     T* dx = static_cast<T*>(p.dx) + at.b * p.sdx.batch + at.ch;
     // Steps inside need no checks: their rows are before the length and the
     // segment's end, and the rows s = t - (K - 1) of dx not before its start.
     auto inside = [&](int t0) { return whole && t0 >= at.first + K - 1 && t0 + kRows <= min(last, len); };
-    Pack<T, kVec> row[kRows], rd[kRows], next[kRows], nextd[kRows];
-    auto fetch = [&](Pack<T, kVec>(&to)[kRows], Pack<T, kVec>(&tod)[kRows], int t0) {
+    Pack<T, V> row[kRows], rd[kRows], next[kRows], nextd[kRows];
+    auto fetch = [&](Pack<T, V>(&to)[kRows], Pack<T, V>(&tod)[kRows], int t0) {
       if (whole && t0 + kRows <= min(end, len)) {
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
@@ -225,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward)) conv_bwd_kernel
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
           const bool in = t0 + u < end;
-          load_row<T, K>(p, at, t0 + u, in ? len : 0, &to[u]);
+          load_row<V, T, K>(p, at, t0 + u, in ? len : 0, &to[u]);
           if (in && t0 + u < len)
             tod[u].load(dout + (t0 + u) * p.sdo.token, whole, at.n);
           else
@@ -237,6 +243,11 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward)) conv_bwd_kernel
     // Rows s < first belong to the segment before, but the first one's are the
     // incoming state's.
     for (int t0 = at.first; t0 < end; t0 += kRows) {
+      if (t0 - (K - 1) >= max(len, at.first)) {  // padding
+        r.zero();
+        for (int s = t0 - (K - 1); s < last; ++s) r.store(dx + s * p.sdx.token, whole, at.n);
+        break;
+      }
       fetch(next, nextd, t0 + kRows);
       const bool fast = inside(t0);
 #pragma unroll
@@ -302,19 +313,19 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward)) conv_bwd_kernel
   }
   if (!p.partial) return;
   const int a = threadIdx.x & (p.across - 1), d = threadIdx.x >> p.across_shift;
-  constexpr int kSums = (K + 1) * kVec;
+  constexpr int kSums = (K + 1) * V;
 #pragma unroll
   for (int j = 0; j <= K; ++j)
 #pragma unroll
-    for (int c = 0; c < kVec; ++c)
-      sums[(d * kSums + j * kVec + c) * p.across + a] = c % 2 ? (dw[j][c / 2]).y : (dw[j][c / 2]).x;
+    for (int c = 0; c < V; ++c)
+      sums[(d * kSums + j * V + c) * p.across + a] = c % 2 ? (dw[j][c / 2]).y : (dw[j][c / 2]).x;
   __syncthreads();
   for (int i = threadIdx.x; i < kSums * p.across; i += kThreads) {
-    const int vec = blockIdx.x * p.across + i % p.across, j = i / p.across / kVec, c = i / p.across % kVec;
-    if (vec * kVec + c >= p.D) continue;
+    const int vec = blockIdx.x * p.across + i % p.across, j = i / p.across / V, c = i / p.across % V;
+    if (vec * V + c >= p.D) continue;
     float s = 0.f;
     for (int v = 0; v < p.down; ++v) s += sums[v * kSums * p.across + i];
-    p.partial[((int64_t)blockIdx.y * (K + 1) + j) * p.D + vec * kVec + c] = s;
+    p.partial[((int64_t)blockIdx.y * (K + 1) + j) * p.D + vec * V + c] = s;
   }
 }
 
@@ -370,8 +381,8 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
 // a segment: those with the least time, counted in rows that one thread takes
 // after another -- a segment's own and about 16 for its weights and borders --
 // over the waves of CTAs that the GPU holds at once.
-void shape(ConvArgs* p, int what) {
-  p->vecs = (p->D + kVec - 1) / kVec;
+void shape(ConvArgs* p, int what, int dtype) {
+  p->vecs = (p->D + p->width - 1) / p->width;
   p->across = 1;
   p->across_shift = 0;
   while (p->across < 32 && p->across < p->vecs) {
@@ -379,7 +390,7 @@ void shape(ConvArgs* p, int what) {
     ++p->across_shift;
   }
   p->down = kThreads / p->across;
-  const int64_t columns = (p->vecs + p->across - 1) / p->across, slots = (int64_t)kOpsSms * resident(what);
+  const int64_t columns = (p->vecs + p->across - 1) / p->across, slots = (int64_t)kOpsSms * resident(what, (int)ops_elem(dtype));
   int64_t best = 0;
   for (int seg = 8; seg <= 256; seg += 4) {
     const int64_t segments = p->N > 0 ? ((int64_t)p->N + seg - 1) / seg : 1;
@@ -404,11 +415,17 @@ mhla_status launch(const ConvArgs& a, int what, cudaStream_t s) {
     return launch_status();
   }
   const dim3 grid((unsigned)((a.vecs + a.across - 1) / a.across), (unsigned)grid_down(a));
-  if (what == kForward) {
-    conv_fwd_kernel<T, K><<<grid, kThreads, 0, s>>>(a);
+  const size_t smem = what == kBackward && a.partial ? sizeof(float) * (K + 1) * a.width * kThreads : 0;
+  if constexpr (sizeof(T) == 4) {  // see choose_width
+    if (what == kForward)
+      conv_fwd_kernel<T, K, 4><<<grid, kThreads, 0, s>>>(a);
+    else
+      conv_bwd_kernel<T, K, 2><<<grid, kThreads, smem, s>>>(a);
   } else {
-    const size_t smem = a.partial ? sizeof(float) * (K + 1) * kVec * kThreads : 0;
-    conv_bwd_kernel<T, K><<<grid, kThreads, smem, s>>>(a);
+    if (what == kForward)
+      (a.width == 4 ? conv_fwd_kernel<T, K, 4> : conv_fwd_kernel<T, K, 2>)<<<grid, kThreads, 0, s>>>(a);
+    else
+      (a.width == 4 ? conv_bwd_kernel<T, K, 4> : conv_bwd_kernel<T, K, 2>)<<<grid, kThreads, smem, s>>>(a);
   }
   return launch_status();
 }
@@ -461,10 +478,20 @@ bool apart(const RowTensor* in, int n_in, const RowTensor* out, int n_out, int s
   return true;
 }
 
-int whole_vectors(const RowTensor* t, int n) {
-  for (int i = 0; i < n; ++i)
-    if (!t[i].empty() && row_alignment(t[i], 16) < kVec * (int)t[i].elem) return 0;
-  return 1;
+// Channels of a thread: four, in one access where rows allow it, but two of
+// float32 in the backward pass, whose registers they fill (4 x 8k x 1024: 79 us,
+// with four 148), and two of bf16 where rows start at pairs only (4 x 4k x 1030
+// backward: 44 us, with four single accesses 97).
+void choose_width(ConvArgs* a, const RowTensor* t, int n, const RowTensor& last, int dtype, bool backward) {
+  int align = row_alignment(last, 16);
+  for (int i = 0; i < n; ++i) {
+    const int x = t[i].empty() ? 16 : row_alignment(t[i], 16);
+    align = x < align ? x : align;
+  }
+  const int elem = (int)ops_elem(dtype);
+  const bool two = dtype == MHLA_DTYPE_F32 ? backward : align == 2 * elem;
+  a->width = two ? 2 : 4;
+  a->whole = align >= a->width * elem;
 }
 
 ConvArgs args_of(const mhla_shortconv_params* p, const void* x, const void* weight, const void* bias,
@@ -506,8 +533,8 @@ mhla_status mhla_shortconv_forward(const void* x, const void* weight, const void
   a.out = out;
   a.so = p->out;
   a.state_out = state_out;
-  a.whole = whole_vectors(in, 1) && whole_vectors(res, 1);
-  shape(&a, kForward);
+  choose_width(&a, in, 1, res[0], p->dtype, false);
+  shape(&a, kForward, p->dtype);
   return dispatch(a, p, kForward, static_cast<cudaStream_t>(stream));
 }
 
@@ -517,8 +544,12 @@ mhla_status mhla_shortconv_backward_workspace_bytes(const mhla_shortconv_params*
   const mhla_status st = check_params(p);
   if (st != MHLA_OK) return st;
   ConvArgs a = args_of(p, nullptr, nullptr, nullptr, nullptr, nullptr);
-  shape(&a, kBackward);
-  *bytes = p->batch && p->width ? sizeof(float) * (size_t)grid_down(a) * (p->taps + 1) * (size_t)p->width : 0;
+  int64_t rows = 0;  // whatever the pointers' alignment
+  for (a.width = 2; a.width <= 4; a.width += 2) {
+    shape(&a, kBackward, p->dtype);
+    rows = grid_down(a) > rows ? grid_down(a) : rows;
+  }
+  *bytes = p->batch && p->width ? sizeof(float) * (size_t)rows * (p->taps + 1) * (size_t)p->width : 0;
   return MHLA_OK;
 }
 
@@ -558,8 +589,8 @@ mhla_status mhla_shortconv_backward(const void* x, const void* weight, const voi
   a.sdx = p->dx;
   a.dstate_in = dstate_in;
   a.partial = sums ? reinterpret_cast<float*>(scratch.ptr()) : nullptr;
-  a.whole = whole_vectors(in, 2) && whole_vectors(res, 1);
-  shape(&a, kBackward);
+  choose_width(&a, in, 2, res[0], p->dtype, true);
+  shape(&a, kBackward, p->dtype);
   st = dispatch(a, p, kBackward, s);
   if (st == MHLA_OK && sums) {
     conv_reduce_kernel<<<dim3((unsigned)((p->width + 31) / 32), (unsigned)(p->taps + 1)), 1024, 0, s>>>(
