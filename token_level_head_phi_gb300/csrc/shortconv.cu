@@ -14,7 +14,12 @@ namespace {
 
 
 constexpr int kThreads = 256;
-constexpr int kRows = 4;      // rows of a step; the next step's are on their way
+// Rows of a step: a multiple of K - 1, so that the windows end it where they began
+// and no register is copied.  Forward the next step's rows are on their way to
+// registers, backward those of kAhead steps to shared memory.
+constexpr int kFwdRows = 6, kAhead = 2;
+template <int K>
+constexpr int kBwdRows = K == 3 ? 2 : 3;
 
 enum { kForward, kBackward, kStep };
 
@@ -132,26 +137,22 @@ __global__ void __launch_bounds__(kThreads, resident(kForward, sizeof(T))) conv_
   T* out = static_cast<T*>(p.out) + at.b * p.so.batch + at.ch;
   const bool whole = p.whole && at.n == V;
   const int inside = whole ? min(last, len) : at.first;  // steps up to here need no checks
-  Pack<T, V> row[kRows], next[kRows];
-  auto fetch = [&](Pack<T, V>(&to)[kRows], int t0) {
+  constexpr int R = kFwdRows;
+  Pack<T, V> rows[2][R];
+  auto fetch = [&](Pack<T, V>(&to)[R], int t0) {
+    if (t0 + R <= inside) {
+      const T* from = x + t0 * p.sx.token;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      if (t0 + kRows <= inside)
-        to[u].load(x + (t0 + u) * p.sx.token, true);
-      else if (t0 < last)
-        load_row<V, T, K>(p, at, t0 + u, len, &to[u]);
+      for (int u = 0; u < R; ++u, from += p.sx.token) to[u].load(from, true);
+    } else if (t0 < last) {
+#pragma unroll
+      for (int u = 0; u < R; ++u) load_row<V, T, K>(p, at, t0 + u, len, &to[u]);
     }
   };
-  fetch(row, at.first);
-  for (int t0 = at.first; t0 < last; t0 += kRows) {
-    if (t0 >= len) {  // padding
-      r.zero();
-      for (int t = t0; t < last; ++t) r.store(out + t * p.so.token, whole, at.n);
-      break;
-    }
-    fetch(next, t0 + kRows);
+  auto step = [&](const Pack<T, V>(&row)[R], int t0) {
+    T* to = out + t0 * p.so.token;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
+    for (int u = 0; u < R; ++u, to += p.so.token) {
       const int t = t0 + u;
       Pack<T, V> o;
 #pragma unroll
@@ -166,15 +167,26 @@ __global__ void __launch_bounds__(kThreads, resident(kForward, sizeof(T))) conv_
         if (p.silu) z = mul2(z, logistic(z));
         put_pair(&o, c, z);
       }
-      if (t0 + kRows <= inside) {
-        o.store(out + t * p.so.token, true);
+      if (t0 + R <= inside) {
+        o.store(to, true);
       } else if (t < last) {
         if (t >= len) o.zero();
-        o.store(out + t * p.so.token, whole, at.n);
+        o.store(to, whole, at.n);
       }
     }
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) row[u] = next[u];
+  };
+  fetch(rows[0], at.first);
+  for (int t0 = at.first; t0 < last; t0 += 2 * R) {
+    if (t0 >= len) {  // padding
+      r.zero();
+      for (int t = t0; t < last; ++t) r.store(out + t * p.so.token, whole, at.n);
+      break;
+    }
+    fetch(rows[1], t0 + R);
+    step(rows[0], t0);
+    if (t0 + R >= last) break;
+    fetch(rows[0], t0 + 2 * R);
+    step(rows[1], t0 + R);
   }
   if (p.state_out && at.first == 0) {
     // the same thread that read state_in, which this may be
@@ -189,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, resident(kForward, sizeof(T))) conv_
 
 template <typename T, int K, int V>
 __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T))) conv_bwd_kernel(const __grid_constant__ ConvArgs p) {
-  constexpr int H = V / 2;
-  extern __shared__ float sums[];  // [down][(K + 1) * V][across]
+  constexpr int H = V / 2, R = kBwdRows<K>;
+  extern __shared__ __align__(16) float sums[];  // rows on their way; then [down][(K + 1) * V][across]
   const Place at(p);
   float2 dw[K + 1][H];
 #pragma unroll
@@ -218,40 +230,53 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T))) conv
     T* dx = static_cast<T*>(p.dx) + at.b * p.sdx.batch + at.ch;
     // Steps inside need no checks: their rows are before the length and the
     // segment's end, and the rows s = t - (K - 1) of dx not before its start.
-    auto inside = [&](int t0) { return whole && t0 >= at.first + K - 1 && t0 + kRows <= min(last, len); };
-    Pack<T, V> row[kRows], rd[kRows], next[kRows], nextd[kRows];
-    auto fetch = [&](Pack<T, V>(&to)[kRows], Pack<T, V>(&tod)[kRows], int t0) {
-      if (whole && t0 + kRows <= min(end, len)) {
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-          to[u].load(x + (t0 + u) * p.sx.token, true);
-          tod[u].load(dout + (t0 + u) * p.sdo.token, true);
-        }
-      } else if (t0 < end) {
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-          const bool in = t0 + u < end;
-          load_row<V, T, K>(p, at, t0 + u, in ? len : 0, &to[u]);
-          if (in && t0 + u < len)
-            tod[u].load(dout + (t0 + u) * p.sdo.token, whole, at.n);
-          else
-            tod[u].zero();
-        }
-      }
+    auto inside = [&](int t0) { return whole && t0 >= at.first + K - 1 && t0 + R <= min(last, len); };
+    // Rows of x and dout go through shared memory of the thread's own.
+    const int copied = whole ? min(end, len) : at.first;
+    auto place = [&](int slot, int u, int which) {
+      return reinterpret_cast<Pack<T, V>*>(sums) + ((slot * R + u) * 2 + which) * kThreads + threadIdx.x;
     };
-    fetch(row, rd, at.first);
+    int put = 0, got = 0;
+    auto fetch = [&](int t0) {
+      const T *from = x + t0 * p.sx.token, *fromd = dout + t0 * p.sdo.token;
+#pragma unroll
+      for (int u = 0; u < R; ++u, from += p.sx.token, fromd += p.sdo.token)
+        if (t0 + u < copied) {
+          copy_async<V * (int)sizeof(T)>(place(put, u, 0), from, V * (int)sizeof(T));
+          copy_async<V * (int)sizeof(T)>(place(put, u, 1), fromd, V * (int)sizeof(T));
+        }
+      copies_commit();
+      put = put < kAhead ? put + 1 : 0;
+    };
+    for (int i = 0; i < kAhead; ++i) fetch(at.first + i * R);
     // Rows s < first belong to the segment before, but the first one's are the
     // incoming state's.
-    for (int t0 = at.first; t0 < end; t0 += kRows) {
+    for (int t0 = at.first; t0 < end; t0 += R) {
       if (t0 - (K - 1) >= max(len, at.first)) {  // padding
         r.zero();
         for (int s = t0 - (K - 1); s < last; ++s) r.store(dx + s * p.sdx.token, whole, at.n);
         break;
       }
-      fetch(next, nextd, t0 + kRows);
-      const bool fast = inside(t0);
+      fetch(t0 + kAhead * R);
+      copies_wait<kAhead>();
+      Pack<T, V> row[R], rd[R];
 #pragma unroll
-      for (int u = 0; u < kRows; ++u) {
+      for (int u = 0; u < R; ++u) {
+        const int t = t0 + u;
+        if (t < copied) {
+          row[u] = *place(got, u, 0);
+          rd[u] = *place(got, u, 1);
+        } else {
+          load_row<V, T, K>(p, at, t, t < end ? len : 0, &row[u]);
+          rd[u].zero();
+          if (t < min(end, len)) rd[u].load(dout + t * p.sdo.token, whole, at.n);
+        }
+      }
+      got = got < kAhead ? got + 1 : 0;
+      const bool fast = inside(t0);
+      T* to = dx + (t0 - (K - 1)) * p.sdx.token;
+#pragma unroll
+      for (int u = 0; u < R; ++u, to += p.sdx.token) {
         const int t = t0 + u, s = t - (K - 1);
         float2 o[H];
 #pragma unroll
@@ -287,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T))) conv
         if (fast) {
 #pragma unroll
           for (int c = 0; c < H; ++c) put_pair(&r, c, o[c]);
-          r.store(dx + s * p.sdx.token, true);
+          r.store(to, true);
           continue;
         }
         const int extra = s - (len - (K - 1));
@@ -304,14 +329,10 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T))) conv
         else if (p.dstate_in)
           r.store(static_cast<T*>(p.dstate_in) + ((int64_t)at.b * (K - 1) + s + K - 1) * p.D + at.ch, false, at.n);
       }
-#pragma unroll
-      for (int u = 0; u < kRows; ++u) {
-        row[u] = next[u];
-        rd[u] = nextd[u];
-      }
     }
   }
   if (!p.partial) return;
+  __syncthreads();  // the rows' places are free
   const int a = threadIdx.x & (p.across - 1), d = threadIdx.x >> p.across_shift;
   constexpr int kSums = (K + 1) * V;
 #pragma unroll
@@ -415,7 +436,9 @@ mhla_status launch(const ConvArgs& a, int what, cudaStream_t s) {
     return launch_status();
   }
   const dim3 grid((unsigned)((a.vecs + a.across - 1) / a.across), (unsigned)grid_down(a));
-  const size_t smem = what == kBackward && a.partial ? sizeof(float) * (K + 1) * a.width * kThreads : 0;
+  // backward: the rows on their way, then the sums; both are at most 48 KB
+  const size_t rows = ops_elem(sizeof(T) == 2 ? MHLA_DTYPE_BF16 : MHLA_DTYPE_F32) * a.width * 2 * kBwdRows<K> * (kAhead + 1) * kThreads;
+  const size_t sums = a.partial ? sizeof(float) * (K + 1) * a.width * kThreads : 0, smem = rows > sums ? rows : sums;
   if constexpr (sizeof(T) == 4) {  // see choose_width
     if (what == kForward)
       conv_fwd_kernel<T, K, 4><<<grid, kThreads, 0, s>>>(a);
