@@ -2,17 +2,27 @@
 #include <algorithm>
 
 #include "gated.cuh"
+#include "tc_host.h"
 
 namespace mhla {
 namespace {
 
-// Adds the units' rows in order.
-__global__ void __launch_bounds__(128) gated_reduce_kernel(const float* partial, int rows, int D, float* out) {
-  const int c = blockIdx.x * 128 + threadIdx.x;
-  if (c >= D) return;
+// Adds the CTAs' rows in order: 32 channels per CTA, 32 threads to one.
+__global__ void __launch_bounds__(1024) gated_reduce_kernel(const float* partial, int rows, int D, float* out) {
+  __shared__ float sh[32][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
   float s = 0.f;
-  for (int i = 0; i < rows; ++i) s += partial[(int64_t)i * D + c];
-  out[c] = s;
+  after_predecessor();
+  if (c < D)
+    for (int r = ty; r < rows; r += 32) s += partial[(int64_t)r * D + c];
+  sh[ty][tx] = s;
+  __syncthreads();
+  if (ty == 0 && c < D) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += sh[i][tx];
+    out[c] = t;
+  }
 }
 
 mhla_status check_params(const mhla_gated_params* p, const float* log_decay) {
@@ -190,9 +200,9 @@ mhla_status mhla_gated_backward(const void* x, const void* gate, const void* inp
   a.dstate_in = dstate_in;
   if (st == MHLA_OK) st = launch_gated_bwd(a, p->dtype, p->kind, s);
   if (st == MHLA_OK && dlog_decay) {
-    gated_reduce_kernel<<<(unsigned)((p->width + 127) / 128), 128, 0, s>>>(a.partial, (int)partial_rows(p), p->width,
-                                                                          dlog_decay);
-    st = launch_status();
+    const int e = launch_pdl(gated_reduce_kernel, dim3((unsigned)((p->width + 31) / 32)), dim3(1024), 0, s,
+                             (const float*)a.partial, (int)partial_rows(p), p->width, dlog_decay);
+    if (e != cudaSuccess) st = record_cuda_error((cudaError_t)e);
   }
   return scratch.give_back(st);
 }

@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   // alone, the first warp has the gradient of the first state
   if (p.dstate_in && rank == 0 && w == 0) ln.put(p.dstate_in + (int64_t)b * p.D, carry);
   if (KIND == MHLA_GATED_DECAY && p.partial) {
+    start_successor();
     __syncthreads();  // the last reads of the mail
     mail[w][l].A = dg;
     __syncthreads();

@@ -66,6 +66,11 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
+// Programmatic launches: a kernel waits here for all of its predecessor's results;
+// its predecessor lets it start early.
+__device__ __forceinline__ void after_predecessor() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void start_successor() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Entry i of a parameter vector that is bf16 or float32.
 __device__ __forceinline__ float param_at(const void* p, int is_f32, int64_t i) {
   return is_f32 ? static_cast<const float*>(p)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);

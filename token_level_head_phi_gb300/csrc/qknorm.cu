@@ -14,6 +14,7 @@
 #include "common.cuh"
 #include "ops.h"
 #include "pack.cuh"
+#include "tc_host.h"
 
 namespace mhla {
 namespace {
@@ -583,6 +584,7 @@ __global__ void __launch_bounds__(256, kResident) qknorm_bwd_kernel(const __grid
     }
   }
   if (!a.partial) return;
+  start_successor();
   // groups of a warp hold the same columns; then the warps in order
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -612,6 +614,7 @@ __global__ void __launch_bounds__(1024) qknorm_reduce_kernel(const float* partia
   const int which = blockIdx.y, tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
   const int first = which ? ctas_q : 0, last = which ? ctas_q + ctas_k : ctas_q;
   float s = 0.f;
+  after_predecessor();
   if (c < dim)
     for (int p = first + ty; p < last; p += 32) s += partial[(int64_t)p * dim + c];
   sh[ty][tx] = s;
@@ -900,9 +903,9 @@ mhla_status mhla_qknorm_backward(const void* dq_out, const void* dk_out, const v
     st = p->dtype == MHLA_DTYPE_BF16 ? dispatch<__nv_bfloat16>(a, p->style, vec, true, s)
                                      : dispatch<float>(a, p->style, vec, true, s);
   if (st == MHLA_OK && sums) {
-    qknorm_reduce_kernel<<<dim3((unsigned)((a.dim + 31) / 32), 2), 1024, 0, s>>>(a.partial, a.ctas[0], a.ctas[1],
-                                                                                 a.dim, dq_weight, dk_weight);
-    st = launch_status();
+    const int e = launch_pdl(qknorm_reduce_kernel, dim3((unsigned)((a.dim + 31) / 32), 2), dim3(1024), 0, s,
+                             (const float*)a.partial, a.ctas[0], a.ctas[1], a.dim, dq_weight, dk_weight);
+    if (e != cudaSuccess) st = record_cuda_error((cudaError_t)e);
   }
   return scratch.give_back(st);
 }

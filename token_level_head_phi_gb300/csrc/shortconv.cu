@@ -8,6 +8,7 @@
 #include "common.cuh"
 #include "ops.h"
 #include "pack.cuh"
+#include "tc_host.h"
 
 namespace mhla {
 namespace {
@@ -332,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T))) conv
     }
   }
   if (!p.partial) return;
+  start_successor();
   __syncthreads();  // the rows' places are free
   const int a = threadIdx.x & (p.across - 1), d = threadIdx.x >> p.across_shift;
   constexpr int kSums = (K + 1) * V;
@@ -356,6 +358,7 @@ __global__ void __launch_bounds__(1024) conv_reduce_kernel(const float* partial,
   __shared__ float sh[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx, j = blockIdx.y;
   float s = 0.f;
+  after_predecessor();
   if (c < D)
     for (int r = ty; r < rows; r += 32) s += partial[((int64_t)r * (K + 1) + j) * D + c];
   sh[ty][tx] = s;
@@ -616,9 +619,9 @@ mhla_status mhla_shortconv_backward(const void* x, const void* weight, const voi
   shape(&a, kBackward, p->dtype);
   st = dispatch(a, p, kBackward, s);
   if (st == MHLA_OK && sums) {
-    conv_reduce_kernel<<<dim3((unsigned)((p->width + 31) / 32), (unsigned)(p->taps + 1)), 1024, 0, s>>>(
-        a.partial, (int)grid_down(a), p->taps, p->width, dweight, dbias);
-    st = launch_status();
+    const int e = launch_pdl(conv_reduce_kernel, dim3((unsigned)((p->width + 31) / 32), (unsigned)(p->taps + 1)), dim3(1024),
+                             0, s, (const float*)a.partial, (int)grid_down(a), p->taps, p->width, dweight, dbias);
+    if (e != cudaSuccess) st = record_cuda_error((cudaError_t)e);
   }
   return scratch.give_back(st);
 }
