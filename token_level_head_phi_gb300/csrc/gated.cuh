@@ -77,18 +77,17 @@ struct Gates {
 template <int KIND, bool IN>
 __device__ __forceinline__ Gates gates_of(float2 r, float2 i, float2 g, float2 g2) {
   Gates o;
-  const float2 f = (mulc(r, kLog2e));
+  const float2 f = mulc(r, kLog2e);
   const float2 e = make_float2(ex2(-f.x), ex2(-f.y)), e1 = addc(e, 1.f);
   if constexpr (IN) {
-    const float2 h = (mulc(i, kLog2e));
+    const float2 h = mulc(i, kLog2e);
     const float2 k1 = addc(make_float2(ex2(-h.x), ex2(-h.y)), 1.f);
-    const float2 d = (mul2(e1, k1));
+    const float2 d = mul2(e1, k1);
     const float2 inv = make_float2(rcp(d.x), rcp(d.y));
     o.s = mul2(inv, k1);
     o.q = mul2(inv, e1);
   } else {
-    const float2 d = (e1);
-    o.s = make_float2(rcp(d.x), rcp(d.y));
+    o.s = make_float2(rcp(e1.x), rcp(e1.y));
   }
   o.less = mul2(e, o.s);
   if constexpr (KIND == MHLA_GATED_DECAY) {
@@ -97,11 +96,10 @@ __device__ __forceinline__ Gates gates_of(float2 r, float2 i, float2 g, float2 g
     t = fmac(x, t, 1.f / 6.f);
     t = fmac(x, t, 0.5f);
     t = fmac(x, t, 1.f);
-    const float2 near = (mul2(x, t)), at = (x), y = (mul2(o.s, g2));
-    o.m = make_float2(at.x > -0.125f ? near.x : ex2(y.x) - 1.f, at.y > -0.125f ? near.y : ex2(y.y) - 1.f);
+    const float2 near = mul2(x, t), y = mul2(o.s, g2);
+    o.m = make_float2(x.x > -0.125f ? near.x : ex2(y.x) - 1.f, x.y > -0.125f ? near.y : ex2(y.y) - 1.f);
   } else {
-    const float2 v = (o.less);
-    o.m = make_float2(-v.x, -v.y);
+    o.m = make_float2(-o.less.x, -o.less.y);
   }
   return o;
 }
@@ -124,17 +122,15 @@ __device__ __forceinline__ float2 wide(const Two<__nv_bfloat16>& x) {
 }
 __device__ __forceinline__ float2 wide(const Two<float>& x) { return make_float2(x.v[0], x.v[1]); }
 __device__ __forceinline__ Two<__nv_bfloat16> narrow(float2 x, __nv_bfloat16) {
-  const float2 f = (x);
-  const __nv_bfloat162 y = __floats2bfloat162_rn(f.x, f.y);
+  const __nv_bfloat162 y = __floats2bfloat162_rn(x.x, x.y);
   Two<__nv_bfloat16> o;
   *reinterpret_cast<uint32_t*>(o.v) = *reinterpret_cast<const uint32_t*>(&y);
   return o;
 }
 __device__ __forceinline__ Two<float> narrow(float2 x, float) {
-  const float2 f = (x);
   Two<float> o;
-  o.v[0] = f.x;
-  o.v[1] = f.y;
+  o.v[0] = x.x;
+  o.v[1] = x.y;
   return o;
 }
 
@@ -161,9 +157,8 @@ struct Lane {
     return make_float2(p && n > 0 ? p[ch] : 0.f, p && n > 1 ? p[ch + 1] : 0.f);
   }
   __device__ __forceinline__ void put(float* p, float2 v) const {
-    const float2 f = (v);
-    if (n > 0) p[ch] = f.x;
-    if (n > 1) p[ch + 1] = f.y;
+    if (n > 0) p[ch] = v.x;
+    if (n > 1) p[ch + 1] = v.y;
   }
 };
 
@@ -227,7 +222,8 @@ struct Walk {
 
   // Writes the rows from `t0` on, as far as there are `rows` and columns.
   template <int TOK>
-  __device__ __forceinline__ void write(const Rows<T, TOK>& from, int t0, bool fast, int rows, int cols, int vec) const {
+  __device__ __forceinline__ void write(const Rows<T, TOK>& from, int t0, bool fast, int rows, int cols,
+                                        int vec) const {
     const int l = threadIdx.x & 31;
     P* to = at + t0 * stride;
     if (vec == 2) {
@@ -265,7 +261,9 @@ __device__ __forceinline__ int cluster_size() {
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return (int)r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // The map h -> A h + H of two channels.
@@ -281,7 +279,9 @@ __device__ __forceinline__ Map load_map(const Map* p) {
   const float4 v = *reinterpret_cast<const float4*>(p);
   return Map{make_float2(v.x, v.y), make_float2(v.z, v.w)};
 }
-__device__ __forceinline__ void store_map(Map* p, Map m) { *reinterpret_cast<float4*>(p) = make_float4(m.A.x, m.A.y, m.H.x, m.H.y); }
+__device__ __forceinline__ void store_map(Map* p, Map m) {
+  *reinterpret_cast<float4*>(p) = make_float4(m.A.x, m.A.y, m.H.x, m.H.y);
+}
 
 // Stores m to the same place of CTA `rank`'s shared memory.
 __device__ __forceinline__ void send(Map* place, int rank, Map m) {
@@ -295,8 +295,12 @@ __device__ __forceinline__ void send(Map* place, int rank, Map m) {
 
 // Barrier `id` (1 .. 15) between two warps of a CTA: one has written, the other
 // reads.
-__device__ __forceinline__ void hand_over(int id) { asm volatile("barrier.cta.arrive.aligned %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ void take_over(int id) { asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void hand_over(int id) {
+  asm volatile("barrier.cta.arrive.aligned %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ void take_over(int id) {
+  asm volatile("barrier.cta.sync.aligned %0, 64;" ::"r"(id) : "memory");
+}
 
 #endif
 

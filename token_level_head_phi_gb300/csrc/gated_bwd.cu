@@ -34,7 +34,8 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   const int len = gated_length(p, b), round = kTile * ranks;
   const float2 lg = ln.get(KIND == MHLA_GATED_DECAY ? p.g : nullptr);
   const float2 g = make_float2(least(lg.x, 0.f), least(lg.y, 0.f)), g2 = mulc(g, kLog2e);
-  const float2 k1 = splat(p.scale == MHLA_GATED_SCALE_MEAN ? -1.f : 0.f), k0 = splat(p.scale == MHLA_GATED_SCALE_MEAN ? 0.f : 1.f);
+  const bool mean = p.scale == MHLA_GATED_SCALE_MEAN;
+  const float2 k1 = splat(mean ? -1.f : 0.f), k0 = splat(mean ? 0.f : 1.f);  // c = k0 + k1 m
   const float2 zero = splat(0.f);
   // the gradient that reaches a token's state from behind it
   float2 carry = ln.get(p.dstate_out ? p.dstate_out + (int64_t)b * p.D : nullptr), dg = zero;

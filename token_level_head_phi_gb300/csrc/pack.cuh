@@ -6,8 +6,8 @@
 
 namespace mhla {
 
-// N consecutive elements, at most 16 bytes; `whole`
-// takes them in one access, otherwise the first `n` one by one.
+// N consecutive elements, at most 16 bytes; `whole` takes them in one access,
+// otherwise the first `n` one by one.
 template <typename T, int N>
 struct Pack {
   static_assert(sizeof(T) * N <= 16, "one access");
@@ -58,7 +58,8 @@ __device__ __forceinline__ void copy_async(void* to, const void* from, int bytes
   if constexpr (BYTES == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at), "l"(from), "r"(bytes) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(BYTES), "r"(bytes) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(at), "l"(from), "n"(BYTES), "r"(bytes)
+                 : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
@@ -132,14 +133,12 @@ __device__ __forceinline__ float2 pair_of(const Pack<float, N>& x, int i) {
 }
 template <int N>
 __device__ __forceinline__ void put_pair(Pack<__nv_bfloat16, N>* x, int i, float2 v) {
-  const float2 f = (v);
-  reinterpret_cast<__nv_bfloat162*>(x->v)[i] = __floats2bfloat162_rn(f.x, f.y);
+  reinterpret_cast<__nv_bfloat162*>(x->v)[i] = __floats2bfloat162_rn(v.x, v.y);
 }
 template <int N>
 __device__ __forceinline__ void put_pair(Pack<float, N>* x, int i, float2 v) {
-  const float2 f = (v);
-  x->v[2 * i] = f.x;
-  x->v[2 * i + 1] = f.y;
+  x->v[2 * i] = v.x;
+  x->v[2 * i + 1] = v.y;
 }
 
 }  // namespace mhla

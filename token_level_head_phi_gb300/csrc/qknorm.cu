@@ -106,7 +106,7 @@ struct Values {
 #pragma unroll
     for (int i = 0; i < 2 * VEC; ++i) {
       if constexpr (kPairs)
-        v[i] = i % 2 ? (p[i / 2]).y : (p[i / 2]).x;
+        v[i] = i % 2 ? p[i / 2].y : p[i / 2].x;
       else
         v[i] = f[i];
     }
@@ -163,8 +163,7 @@ struct Values {
       float2 s = mul2(p[0], x.p[0]);
 #pragma unroll
       for (int i = 1; i < VEC; ++i) s = fma2(p[i], x.p[i], s);
-      const float2 t = (s);
-      return t.x + t.y;
+      return s.x + s.y;
     } else {
       float s = f[0] * x.f[0];
 #pragma unroll
@@ -201,8 +200,8 @@ struct Values {
 // Rows of bf16 take the approximate sine and cosine, off by 2^-21 at most within
 // half a turn (5e-7 of a pair, whose entries are rounded to 2^-9 of themselves).
 template <typename T, int VEC, bool ACROSS>
-__device__ __forceinline__ void turns_of(const QkArgs& a, const uint64_t* turns, int64_t pos, const int (&col)[2], float sign,
-                                         Values<VEC, ACROSS>* c, Values<VEC, ACROSS>* s) {
+__device__ __forceinline__ void turns_of(const QkArgs& a, const uint64_t* turns, int64_t pos, const int (&col)[2],
+                                         float sign, Values<VEC, ACROSS>* c, Values<VEC, ACROSS>* s) {
   float fc[2 * VEC], fs[2 * VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
@@ -339,7 +338,8 @@ __global__ void __launch_bounds__(256, kResident) qknorm_fwd_kernel(const __grid
         const bool exists = ahead.live && ahead.h + r < end;
         const T* from = row_of(ahead, exists ? ahead.h + r : ahead.h);
 #pragma unroll
-        for (int i = 0; i < 2 * E; ++i) ring.start(put, r, i, from + col[i / 2][i % 2], exists && in[i / 2][i % 2], any);
+        for (int i = 0; i < 2 * E; ++i)
+          ring.start(put, r, i, from + col[i / 2][i % 2], exists && in[i / 2][i % 2], any);
       }
       ahead.h = end;
       if (end >= last) locate(ahead, ahead.base + stride);
@@ -505,7 +505,8 @@ __global__ void __launch_bounds__(256, kResident) qknorm_bwd_kernel(const __grid
   for (int64_t base = start; base < all; base += stride) {
     const T *x, *dy;
     const bool live = point(base, &x, &dy);
-    const int64_t token = live ? base + (threadIdx.x >> a.lanes_shift) : 0, b = token / a.tokens, t = token - b * a.tokens;
+    const int64_t token = live ? base + (threadIdx.x >> a.lanes_shift) : 0;
+    const int64_t b = token / a.tokens, t = token - b * a.tokens;
     T* dx = static_cast<T*>(a.y[which]) + b * a.sy[which].batch + t * a.sy[which].token;
     const int64_t pos = position_of(a, b, (int)t);
     V cs[E], sn[E];

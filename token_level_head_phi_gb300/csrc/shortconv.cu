@@ -13,7 +13,6 @@
 namespace mhla {
 namespace {
 
-
 constexpr int kThreads = 256;
 // Rows of a step: a multiple of K - 1, so that the windows end it where they began
 // and no register is copied.  Forward the next step's rows are on their way to
@@ -66,7 +65,8 @@ struct Place {
 
 // Channel pairs of a thread's weights and bias.
 template <int V, typename W, int K>
-__device__ __forceinline__ void load_weights_as(const ConvArgs& p, const Place& at, float (&w)[V][K], float (&bias)[V]) {
+__device__ __forceinline__ void load_weights_as(const ConvArgs& p, const Place& at, float (&w)[V][K],
+                                                float (&bias)[V]) {
   const W *pw = static_cast<const W*>(p.w) + (int64_t)at.ch * K, *pb = static_cast<const W*>(p.bias) + at.ch;
   if (at.n == V) {
 #pragma unroll
@@ -98,8 +98,8 @@ __device__ __forceinline__ void load_weights(const ConvArgs& p, const Place& at,
 
 // 1 / (1 + e^-z)
 __device__ __forceinline__ float2 logistic(float2 z) {
-  const float2 y = (mul2(z, splat(-kLog2e)));
-  const float2 d = (add2(make_float2(ex2(y.x), ex2(y.y)), splat(1.f)));
+  const float2 y = mul2(z, splat(-kLog2e));
+  const float2 d = add2(make_float2(ex2(y.x), ex2(y.y)), splat(1.f));
   return make_float2(rcp(d.x), rcp(d.y));
 }
 
@@ -119,7 +119,8 @@ __device__ __forceinline__ void load_row(const ConvArgs& p, const Place& at, int
 }
 
 template <typename T, int K, int V>
-__global__ void __launch_bounds__(kThreads, resident(kForward, sizeof(T))) conv_fwd_kernel(const __grid_constant__ ConvArgs p) {
+__global__ void __launch_bounds__(kThreads, resident(kForward, sizeof(T)))
+    conv_fwd_kernel(const __grid_constant__ ConvArgs p) {
   constexpr int H = V / 2;
   const Place at(p);
   if (!at.live) return;
@@ -201,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, resident(kForward, sizeof(T))) conv_
 }
 
 template <typename T, int K, int V>
-__global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T))) conv_bwd_kernel(const __grid_constant__ ConvArgs p) {
+__global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
+    conv_bwd_kernel(const __grid_constant__ ConvArgs p) {
   constexpr int H = V / 2, R = kBwdRows<K>;
   extern __shared__ __align__(16) float sums[];  // rows on their way; then [down][(K + 1) * V][across]
   const Place at(p);
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T))) conv
   for (int j = 0; j <= K; ++j)
 #pragma unroll
     for (int c = 0; c < V; ++c)
-      sums[(d * kSums + j * V + c) * p.across + a] = c % 2 ? (dw[j][c / 2]).y : (dw[j][c / 2]).x;
+      sums[(d * kSums + j * V + c) * p.across + a] = c % 2 ? dw[j][c / 2].y : dw[j][c / 2].x;
   __syncthreads();
   for (int i = threadIdx.x; i < kSums * p.across; i += kThreads) {
     const int vec = blockIdx.x * p.across + i % p.across, j = i / p.across / V, c = i / p.across % V;
@@ -389,7 +391,8 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const __grid_constant__ 
     row[j] = p.state_in ? static_cast<const T*>(p.state_in)[(b * (K - 1) + j) * p.D + ch] : from_f32<T>(0.f);
   row[K - 1] = x;
   // the forward kernel's order, so that tokens give the same bits either way
-  float z = fmaf(param_at(p.w, p.w_f32, (int64_t)ch * K + K - 1), to_f32(x), p.bias ? param_at(p.bias, p.w_f32, ch) : 0.f);
+  const float bias = p.bias ? param_at(p.bias, p.w_f32, ch) : 0.f;
+  float z = fmaf(param_at(p.w, p.w_f32, (int64_t)ch * K + K - 1), to_f32(x), bias);
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) z = fmaf(param_at(p.w, p.w_f32, (int64_t)ch * K + j), to_f32(row[j]), z);
   if (p.silu) z = z * rcp(1.f + ex2(-z * kLog2e));
@@ -414,7 +417,8 @@ void shape(ConvArgs* p, int what, int dtype) {
     ++p->across_shift;
   }
   p->down = kThreads / p->across;
-  const int64_t columns = (p->vecs + p->across - 1) / p->across, slots = (int64_t)kOpsSms * resident(what, (int)ops_elem(dtype));
+  const int64_t columns = (p->vecs + p->across - 1) / p->across;
+  const int64_t slots = (int64_t)kOpsSms * resident(what, (int)ops_elem(dtype));
   int64_t best = 0;
   for (int seg = 8; seg <= 256; seg += 4) {
     const int64_t segments = p->N > 0 ? ((int64_t)p->N + seg - 1) / seg : 1;
@@ -440,7 +444,7 @@ mhla_status launch(const ConvArgs& a, int what, cudaStream_t s) {
   }
   const dim3 grid((unsigned)((a.vecs + a.across - 1) / a.across), (unsigned)grid_down(a));
   // backward: the rows on their way, then the sums; both are at most 48 KB
-  const size_t rows = ops_elem(sizeof(T) == 2 ? MHLA_DTYPE_BF16 : MHLA_DTYPE_F32) * a.width * 2 * kBwdRows<K> * (kAhead + 1) * kThreads;
+  const size_t rows = sizeof(T) * a.width * 2 * kBwdRows<K> * (kAhead + 1) * kThreads;
   const size_t sums = a.partial ? sizeof(float) * (K + 1) * a.width * kThreads : 0, smem = rows > sums ? rows : sums;
   if constexpr (sizeof(T) == 4) {  // see choose_width
     if (what == kForward)
@@ -619,8 +623,9 @@ mhla_status mhla_shortconv_backward(const void* x, const void* weight, const voi
   shape(&a, kBackward, p->dtype);
   st = dispatch(a, p, kBackward, s);
   if (st == MHLA_OK && sums) {
-    const int e = launch_pdl(conv_reduce_kernel, dim3((unsigned)((p->width + 31) / 32), (unsigned)(p->taps + 1)), dim3(1024),
-                             0, s, (const float*)a.partial, (int)grid_down(a), p->taps, p->width, dweight, dbias);
+    const dim3 grid((unsigned)((p->width + 31) / 32), (unsigned)(p->taps + 1));
+    const int e = launch_pdl(conv_reduce_kernel, grid, dim3(1024), 0, s, (const float*)a.partial, (int)grid_down(a),
+                             p->taps, p->width, dweight, dbias);
     if (e != cudaSuccess) st = record_cuda_error((cudaError_t)e);
   }
   return scratch.give_back(st);
