@@ -156,6 +156,18 @@ def test_gated_refuses_pointers(lib):
     assert f(p=gated_params(tokens=0x7fffffff)) == UNSUPPORTED
 
 
+def test_gated_refuses_sizes_near_the_end_of_32_bits(lib):
+    # rounds of at most 1024 tokens behind the last one are still counted
+    need = ctypes.c_size_t()
+    for kw in ({"tokens": 0x7ffff001}, {"tokens": 0x7fffff00}, {"width": 0x7ffff001}, {"width": 0x7fffffff}):
+        p = gated_params(**{"batch": 1, "tokens": 1, "width": 1, **kw})
+        assert gated_forward(lib, p) == UNSUPPORTED and gated_step(lib, p) == UNSUPPORTED, kw
+        assert lib.mhla_gated_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == UNSUPPORTED, kw
+    p = gated_params(batch=1, tokens=0x7ffff000, width=1)
+    assert lib.mhla_gated_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(need)) == mb.MHLA_OK
+    assert need.value >= 4 * (0x7ffff000 // mb.GATED_MARK)
+
+
 def test_gated_backward_refuses_pointers(lib):
     p, n = gated_params(), ctypes.c_size_t(0)
     assert lib.mhla_gated_backward_workspace_bytes(ctypes.byref(p), ctypes.byref(n)) == mb.MHLA_OK

@@ -30,7 +30,10 @@ mhla_status check_params(const mhla_gated_params* p, const float* log_decay) {
   if (p->kind != MHLA_GATED_DECAY && p->kind != MHLA_GATED_SIGMOID) return MHLA_ERR_INVALID_ARG;
   if (p->scale < MHLA_GATED_SCALE_NORM || p->scale > MHLA_GATED_SCALE_NONE) return MHLA_ERR_INVALID_ARG;
   if (p->marks != 0 && p->marks != 1) return MHLA_ERR_INVALID_ARG;
-  if (p->tokens > 0x7fffff00) return MHLA_ERR_UNSUPPORTED;  // tokens are rounded up to tiles in 32 bits
+  // tokens and channels are counted in 32 bits, tokens up to three rounds of a
+  // cluster's tiles past the end
+  static_assert(3 * kGatedCluster * kGatedWarps * 16 < 0x1000, "room behind the last token");
+  if (p->tokens > 0x7ffff000 || p->width > 0x7ffff000) return MHLA_ERR_UNSUPPORTED;
   if ((p->kind == MHLA_GATED_DECAY) != (log_decay != nullptr) && p->width > 0) return MHLA_ERR_INVALID_ARG;
   return MHLA_OK;
 }
