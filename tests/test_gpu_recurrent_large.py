@@ -101,3 +101,20 @@ def test_wide_rows():
 
 def test_no_device_error_was_reported():
     assert mb.mhla_device_status() == (0, 0)
+
+
+def test_more_sequences_than_a_grid_is_high():
+    # above 8 x 65535 sequences of one segment, 8 of them a CTA; small whole numbers,
+    # whose sums are exact
+    B, D = 530_000, 128
+    gen = torch.Generator().manual_seed(5)
+    x = torch.randint(-2, 3, (B, 1, D), generator=gen).to(torch.bfloat16).cuda()
+    do = torch.randint(-1, 2, (B, 1, D), generator=gen).to(torch.bfloat16).cuda()
+    w = torch.randint(-2, 3, (D, 4), generator=gen).to(torch.bfloat16).cuda()
+    out, _ = mb.mhla_shortconv_forward(x, w)
+    assert torch.equal(out, x * w[:, 3])
+    db = torch.empty(D, device="cuda")
+    dx, dw, _, _ = mb.mhla_shortconv_backward(x, w, do, dbias=db)
+    assert torch.equal(dx, do * w[:, 3])
+    assert torch.equal(db, do.float().sum((0, 1)))
+    assert torch.equal(dw[:, 3], (do.float() * x.float()).sum((0, 1))) and not dw[:, :3].any()

@@ -38,6 +38,7 @@ struct ConvArgs {
   int vecs;            // of a row
   int across, down;    // of a CTA: vectors and segments, powers of two
   int across_shift;
+  int columns;         // CTAs to the channels of a segment; neighbours in the grid
   int segments, seg;   // segments of a sequence, tokens of one
   int whole;           // vectors in one access
 };
@@ -51,10 +52,13 @@ __device__ __forceinline__ int length_of(const ConvArgs& p, int b) {
 // A thread's channels, sequence and segment.
 struct Place {
   int ch, n, b, first;
+  int down, first_vec;  // of the CTA
   bool live;
   __device__ __forceinline__ Place(const ConvArgs& p) {
-    const int vec = blockIdx.x * p.across + (threadIdx.x & (p.across - 1));
-    const int64_t at = (int64_t)blockIdx.y * p.down + (threadIdx.x >> p.across_shift);
+    down = blockIdx.x / p.columns;
+    first_vec = (blockIdx.x - down * p.columns) * p.across;
+    const int vec = first_vec + (threadIdx.x & (p.across - 1));
+    const int64_t at = (int64_t)down * p.down + (threadIdx.x >> p.across_shift);
     b = (int)(at / p.segments);
     first = (int)(at - (int64_t)b * p.segments) * p.seg;
     ch = vec * p.width;
@@ -346,11 +350,11 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
       sums[(d * kSums + j * V + c) * p.across + a] = c % 2 ? dw[j][c / 2].y : dw[j][c / 2].x;
   __syncthreads();
   for (int i = threadIdx.x; i < kSums * p.across; i += kThreads) {
-    const int vec = blockIdx.x * p.across + i % p.across, j = i / p.across / V, c = i / p.across % V;
+    const int vec = at.first_vec + i % p.across, j = i / p.across / V, c = i / p.across % V;
     if (vec * V + c >= p.D) continue;
     float s = 0.f;
     for (int v = 0; v < p.down; ++v) s += sums[v * kSums * p.across + i];
-    p.partial[((int64_t)blockIdx.y * (K + 1) + j) * p.D + vec * V + c] = s;
+    p.partial[((int64_t)at.down * (K + 1) + j) * p.D + vec * V + c] = s;
   }
 }
 
@@ -417,12 +421,12 @@ void shape(ConvArgs* p, int what, int dtype) {
     ++p->across_shift;
   }
   p->down = kThreads / p->across;
-  const int64_t columns = (p->vecs + p->across - 1) / p->across;
+  p->columns = (p->vecs + p->across - 1) / p->across;
   const int64_t slots = (int64_t)kOpsSms * resident(what, (int)ops_elem(dtype));
   int64_t best = 0;
   for (int seg = 8; seg <= 256; seg += 4) {
     const int64_t segments = p->N > 0 ? ((int64_t)p->N + seg - 1) / seg : 1;
-    const int64_t ctas = columns * (((int64_t)p->B * segments + p->down - 1) / p->down);
+    const int64_t ctas = p->columns * (((int64_t)p->B * segments + p->down - 1) / p->down);
     const int64_t cost = (ctas + slots - 1) / slots * (seg + 16);
     if (seg == 8 || cost < best) {
       best = cost;
@@ -442,7 +446,7 @@ mhla_status launch(const ConvArgs& a, int what, cudaStream_t s) {
     conv_step_kernel<T, K><<<(unsigned)blocks, 128, 0, s>>>(a);
     return launch_status();
   }
-  const dim3 grid((unsigned)((a.vecs + a.across - 1) / a.across), (unsigned)grid_down(a));
+  const unsigned grid = (unsigned)(a.columns * grid_down(a));
   // backward: the rows on their way, then the sums; both are at most 48 KB
   const size_t rows = sizeof(T) * a.width * 2 * kBwdRows<K> * (kAhead + 1) * kThreads;
   const size_t sums = a.partial ? sizeof(float) * (K + 1) * a.width * kThreads : 0, smem = rows > sums ? rows : sums;
@@ -468,7 +472,7 @@ mhla_status with_taps(const ConvArgs& a, int taps, int what, cudaStream_t s) {
 }
 
 mhla_status dispatch(const ConvArgs& a, const mhla_shortconv_params* p, int what, cudaStream_t s) {
-  if (what != kStep && grid_down(a) > 65535) return MHLA_ERR_UNSUPPORTED;
+  if (what != kStep && a.columns * grid_down(a) > 0x7fffffff) return MHLA_ERR_UNSUPPORTED;
   return p->dtype == MHLA_DTYPE_BF16 ? with_taps<__nv_bfloat16>(a, p->taps, what, s)
                                      : with_taps<float>(a, p->taps, what, s);
 }
