@@ -9,6 +9,7 @@
 // are the 64-bit fractions of a turn of mhla_rotary_table.
 // Bound: memory (each row read once and written once; the backward pass reads
 // two rows and writes one).
+#include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
@@ -890,6 +891,8 @@ mhla_status mhla_qknorm_backward(const void* dq_out, const void* dk_out, const v
   shape_rows(&a, vec, p->style);
   share_ctas(&a);
   Scratch scratch;
+  // the launch's own CTAs have the last word on what their sums need
+  need = std::max(need, sizeof(float) * (size_t)(a.ctas[0] + a.ctas[1]) * (size_t)a.dim);
   if (sums && (st = scratch.take(workspace, workspace_bytes, need, s)) != MHLA_OK) return st;
   a.x[0] = q;
   a.x[1] = k;

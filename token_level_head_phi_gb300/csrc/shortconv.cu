@@ -5,6 +5,8 @@
 // A thread takes a few neighbouring channels and walks over a segment of the
 // tokens with the last K rows in registers; the K - 1 rows before a segment
 // (and, backwards, behind it) are read again by its neighbour.  Bound: memory.
+#include <algorithm>
+
 #include "common.cuh"
 #include "ops.h"
 #include "pack.cuh"
@@ -438,6 +440,11 @@ void shape(ConvArgs* p, int what, int dtype) {
 
 int64_t grid_down(const ConvArgs& p) { return ((int64_t)p.B * p.segments + p.down - 1) / p.down; }
 
+// Bytes of the backward pass's partial sums in this shape.
+size_t sums_bytes(const ConvArgs& p, int taps) {
+  return sizeof(float) * (size_t)grid_down(p) * (taps + 1) * (size_t)p.D;
+}
+
 template <typename T, int K>
 mhla_status launch(const ConvArgs& a, int what, cudaStream_t s) {
   if (what == kStep) {
@@ -578,12 +585,11 @@ mhla_status mhla_shortconv_backward_workspace_bytes(const mhla_shortconv_params*
   const mhla_status st = check_params(p);
   if (st != MHLA_OK) return st;
   ConvArgs a = args_of(p, nullptr, nullptr, nullptr, nullptr, nullptr);
-  int64_t rows = 0;  // whatever the pointers' alignment
-  for (a.width = 2; a.width <= 4; a.width += 2) {
+  *bytes = 0;
+  for (a.width = 2; a.width <= 4 && p->batch && p->width; a.width += 2) {  // whatever the pointers' alignment
     shape(&a, kBackward, p->dtype);
-    rows = grid_down(a) > rows ? grid_down(a) : rows;
+    *bytes = std::max(*bytes, sums_bytes(a, p->taps));
   }
-  *bytes = p->batch && p->width ? sizeof(float) * (size_t)rows * (p->taps + 1) * (size_t)p->width : 0;
   return MHLA_OK;
 }
 
@@ -613,9 +619,13 @@ mhla_status mhla_shortconv_backward(const void* x, const void* weight, const voi
     if (e == cudaSuccess && dbias && p->width) e = cudaMemsetAsync(dbias, 0, sizeof(float) * (size_t)p->width, s);
     return e == cudaSuccess ? MHLA_OK : record_cuda_error(e);
   }
-  Scratch scratch;
-  if (sums && (st = scratch.take(workspace, workspace_bytes, need, s)) != MHLA_OK) return st;
   ConvArgs a = args_of(p, x, weight, bias, lengths, state_in);
+  choose_width(&a, in, 2, res[0], p->dtype, true);
+  shape(&a, kBackward, p->dtype);
+  // the launch's own shape has the last word on what its sums need
+  Scratch scratch;
+  if (sums && (st = scratch.take(workspace, workspace_bytes, std::max(need, sums_bytes(a, p->taps)), s)) != MHLA_OK)
+    return st;
   a.dout = dout;
   a.sdo = p->dout;
   a.dstate_out = dstate_out;
@@ -623,8 +633,6 @@ mhla_status mhla_shortconv_backward(const void* x, const void* weight, const voi
   a.sdx = p->dx;
   a.dstate_in = dstate_in;
   a.partial = sums ? reinterpret_cast<float*>(scratch.ptr()) : nullptr;
-  choose_width(&a, in, 2, res[0], p->dtype, true);
-  shape(&a, kBackward, p->dtype);
   st = dispatch(a, p, kBackward, s);
   if (st == MHLA_OK && sums) {
     const dim3 grid((unsigned)((p->width + 31) / 32), (unsigned)(p->taps + 1));
