@@ -115,9 +115,9 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
         }
         map = then(map, Map{a, mul2(a, wide(at.d.v[j][l]))});
       }
-    float2 e;
+    float2 e = carry;
+    Map behind = same();
     if (ranks == 1) {
-      e = carry;
       if (w < kGatedWarps - 1 || base + round < rounds * round) {
         take_over(1 + w);
         e = mail[w][l].H;
@@ -129,7 +129,6 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
         hand_over(1 + to);
       }
     } else {
-      Map behind = same();
       if (w < kGatedWarps - 1) {
         take_over(1 + w);
         behind = load_map(&mail[w][l]);
@@ -141,13 +140,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
       } else {
         for (int v = 0; v < ranks; ++v) send(&tiles[turn][rank][l], v, all);
       }
-      cluster_arrive();
-      cluster_wait();
-      e = carry;
-      for (int v = ranks - 1; v > rank; --v) e = through(load_map(&tiles[turn][v][l]), e);
-      carry = e;
-      for (int v = rank; v >= 0; --v) carry = through(load_map(&tiles[turn][v][l]), carry);
-      e = through(behind, e);
+      cluster_arrive();  // the tokens' states are formed meanwhile
     }
     if (w % 2) {
       take_over(9 + w / 2);
@@ -164,6 +157,13 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
     if (w % 2 == 0) {
       states[w / 2][l] = h;
       hand_over(9 + w / 2);
+    }
+    if (ranks > 1) {
+      cluster_wait();
+      for (int v = ranks - 1; v > rank; --v) e = through(load_map(&tiles[turn][v][l]), e);
+      carry = e;
+      for (int v = rank; v >= 0; --v) carry = through(load_map(&tiles[turn][v][l]), carry);
+      e = through(behind, e);
     }
     if (live)
 #pragma unroll
