@@ -206,16 +206,31 @@ struct Walk {
           *reinterpret_cast<uint4*>(place) = make_uint4(0, 0, 0, 0);
       }
     } else {
-      for (int i = 0; i < TOK; ++i, from += stride) {
-        Two<T>& place = to.v[i][l];
-        if (vec == 1 && i < rows && 2 * l + 1 < cols) {
-          copy_async<2 * sizeof(T)>(&place, from, 2 * (int)sizeof(T));
-        } else {
-          Two<T> v;
-          v.zero();
-          if (i < rows) v.load(from, false, cols - 2 * l);
-          place = v;
+      const T* some = from - 2 * l;  // there, where the lane's channels are not
+      const int n = min(max(cols - 2 * l, 0), 2);
+      if (vec == 1) {
+#pragma unroll
+        for (int i = 0; i < TOK; ++i, from += stride) {
+          const int bytes = i < rows ? n * (int)sizeof(T) : 0;
+          copy_async<2 * sizeof(T)>(&to.v[i][l], bytes ? from : some, bytes);
         }
+      } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < TOK; ++i, from += stride)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const bool there = i < rows && c < n;
+            copy_async<4>(&to.v[i][l].v[c], there ? from + c : some, there ? 4 : 0);
+          }
+      } else {  // no copies of 2 bytes: all rows into registers, then on
+        Two<T> v[TOK];
+#pragma unroll
+        for (int i = 0; i < TOK; ++i, from += stride) {
+          v[i].zero();
+          if (i < rows) v[i].load(from, false, n);
+        }
+#pragma unroll
+        for (int i = 0; i < TOK; ++i) to.v[i][l] = v[i];
       }
     }
   }
