@@ -32,7 +32,7 @@ constexpr int kGatedTok = BACKWARD || F32 ? 8 : 16;
 inline int gated_tile(bool f32, bool backward) { return kGatedWarps * (backward || f32 ? 8 : 16); }
 // CTAs that an SM holds: their registers, and the shared memory of float32's
 // backward pass.
-constexpr int gated_resident(bool f32, bool backward) { return f32 ? 1 : 2; }
+constexpr int gated_resident(bool f32) { return f32 ? 1 : 2; }
 
 struct GatedArgs {
   const void *x, *r, *i, *dout;
@@ -319,19 +319,35 @@ __device__ __forceinline__ void take_over(int id) {
 
 #endif
 
-// CTAs of a cluster: the power of two with the least time, counted in rounds of
-// tiles over the waves of CTAs that the GPU holds at once; of equal ones the
-// smallest.  A round of a cluster, whose warps all wait for the other CTAs,
-// counts twice that of a CTA alone (1.5 times in the longer backward rounds):
-// 64 x 512 tokens of 4096 channels forward take 186 us alone and 257 us in
-// pairs, 2 x 32k of 1024 channels 470 us alone and 139 us in clusters of 8.
+// Clusters of n = 1 .. 8 CTAs that the GPU holds at once, with one or two CTAs to
+// an SM: as cudaOccupancyMaxActiveClusters says, since a cluster stays inside a
+// part of the GPU.
+inline int gated_clusters(int n, int resident) {
+  static constexpr int held[2][kGatedCluster] = {{152, 76, 46, 36, 28, 23, 15, 15}, {304, 152, 97, 74, 58, 46, 38, 36}};
+  return held[resident - 1][n - 1];
+}
+
+// CTAs of a cluster: the number with the least time, counted in rounds of tiles
+// over the waves of clusters that the GPU holds at once; of equal ones the
+// smallest.  A round takes 1.8 us (backward 2.4) of a CTA alone on its SM, 3.2
+// (3.9) of two alone on one SM and 4.1 (4.7) in a cluster, whose warps wait for
+// the maps of all of its tiles.  5 x 1999 tokens of 1024 channels forward take 29
+// us alone, 32 in pairs, 25 in threes and 28 in eights; backward 76, 74, 53 and
+// 59; 16 x 256 tokens forward 8.5 alone and 13 in pairs; 3 x 777 of 321 float32
+// channels 30 alone, 12 in sixes and 16 in eights, of which only 15 fit.
 inline int gated_cluster(int64_t units, int tokens, bool f32, bool backward) {
-  const int tile = gated_tile(f32, backward);
-  const int64_t slots = (int64_t)kOpsSms * gated_resident(f32, backward), tiles = ((int64_t)tokens + tile - 1) / tile;
+  const int tile = gated_tile(f32, backward), resident = gated_resident(f32);
+  const int64_t tiles = ((int64_t)tokens + tile - 1) / tile;
   int64_t best = 0;
   int c = 1;
-  for (int n = 1; n <= kGatedCluster; n *= 2) {
-    const int64_t cost = (units * n + slots - 1) / slots * ((tiles + n - 1) / n) * (n == 1 ? 2 : backward ? 3 : 4);
+  for (int n = 1; n <= kGatedCluster; ++n) {
+    const int held = gated_clusters(n, resident);
+    int round = 8;
+    if (n > 1)
+      round = backward ? 15 : 18;
+    else if (resident > 1 && units > kOpsSms)
+      round = backward ? 13 : 14;
+    const int64_t cost = (units + held - 1) / held * ((tiles + n - 1) / n) * round;
     if (n == 1 || cost < best) {
       best = cost;
       c = n;

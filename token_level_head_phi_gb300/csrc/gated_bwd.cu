@@ -19,7 +19,7 @@ struct Stage {
 static_assert(MHLA_GATED_MARK == 2 * 8, "every second warp starts at a mark");
 
 template <typename T, int KIND, bool IN, bool NORM>
-__global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 4, true))
+__global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 4))
     gated_bwd_kernel(const __grid_constant__ GatedArgs p) {
   constexpr int kTok = kGatedTok<sizeof(T) == 4, true>, kTile = kGatedWarps * kTok;
   extern __shared__ __align__(16) unsigned char dynamic[];

@@ -22,7 +22,7 @@ struct Stage {
 // The warps of a CTA hand their states (alone) or the maps of their tokens (in a
 // cluster) from one to the next, without a barrier for all of them.
 template <typename T, int KIND, bool IN, bool NORM>
-__global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 4, false))
+__global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 4))
     gated_fwd_kernel(const __grid_constant__ GatedArgs p) {
   constexpr int kTok = kGatedTok<sizeof(T) == 4, false>, kTile = kGatedWarps * kTok;
   extern __shared__ __align__(16) unsigned char dynamic[];
