@@ -168,6 +168,8 @@ struct Lane {
 template <typename T, int TOK>
 struct Rows {
   Two<T> v[TOK][32];
+  __device__ __forceinline__ T* single(int row, int i) { return &v[row][i / 2].v[i % 2]; }
+  __device__ __forceinline__ const T* single(int row, int i) const { return &v[row][i / 2].v[i % 2]; }
   static constexpr int kPiece = 16 / sizeof(T), kPieces = kGatedSlab / kPiece;  // of a row
   static constexpr int kAtOnce = 32 / kPieces;                                  // rows of one access of the warp
 };
@@ -175,13 +177,15 @@ struct Rows {
 // A lane's way through the rows of a slab in global memory.
 template <typename T, typename P>
 struct Walk {
-  P* at;  // of the lane: its piece of one of the first rows, or its two channels of the first
+  // of the lane: its piece of one of the first rows (vec 2); of the first row its
+  // two channels (1), or one of two elements that are 32 apart (0)
+  P* at;
   int64_t stride;
   using R1 = Rows<T, 1>;
 
   __device__ __forceinline__ Walk(P* slab, int64_t stride, int vec) : stride(stride) {
     const int l = threadIdx.x & 31;
-    at = slab + (vec == 2 ? l / R1::kPieces * stride + l % R1::kPieces * R1::kPiece : 2 * l);
+    at = slab + (vec == 2 ? l / R1::kPieces * stride + l % R1::kPieces * R1::kPiece : vec == 1 ? 2 * l : l);
   }
 
   // Starts copies of the rows from `t0` on; zeros where they have no `rows` or
@@ -205,32 +209,35 @@ struct Walk {
         else
           *reinterpret_cast<uint4*>(place) = make_uint4(0, 0, 0, 0);
       }
-    } else {
+    } else if (vec == 1) {
       const T* some = from - 2 * l;  // there, where the lane's channels are not
-      const int n = min(max(cols - 2 * l, 0), 2);
-      if (vec == 1) {
+      const int n = min(max(cols - 2 * l, 0), 2) * (int)sizeof(T);
 #pragma unroll
-        for (int i = 0; i < TOK; ++i, from += stride) {
-          const int bytes = i < rows ? n * (int)sizeof(T) : 0;
-          copy_async<2 * sizeof(T)>(&to.v[i][l], bytes ? from : some, bytes);
+      for (int i = 0; i < TOK; ++i, from += stride) {
+        const int bytes = i < rows ? n : 0;
+        copy_async<2 * sizeof(T)>(&to.v[i][l], bytes ? from : some, bytes);
+      }
+    } else if constexpr (sizeof(T) == 4) {
+      const T* some = from - l;
+#pragma unroll
+      for (int i = 0; i < TOK; ++i, from += stride)
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          const bool there = i < rows && c + l < cols;
+          copy_async<4>(to.single(i, c + l), there ? from + c : some, there ? 4 : 0);
         }
-      } else if constexpr (sizeof(T) == 4) {
+    } else {  // no copies of 2 bytes: eight rows into registers, then on
+#pragma unroll 1
+      for (int j = 0; j < TOK; j += 8) {
+        T v[8][2];
 #pragma unroll
-        for (int i = 0; i < TOK; ++i, from += stride)
+        for (int i = 0; i < 8; ++i, from += stride)
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const bool there = i < rows && c < n;
-            copy_async<4>(&to.v[i][l].v[c], there ? from + c : some, there ? 4 : 0);
-          }
-      } else {  // no copies of 2 bytes: all rows into registers, then on
-        Two<T> v[TOK];
+          for (int c = 0; c < 2; ++c) v[i][c] = j + i < rows && 32 * c + l < cols ? from[32 * c] : from_f32<T>(0.f);
 #pragma unroll
-        for (int i = 0; i < TOK; ++i, from += stride) {
-          v[i].zero();
-          if (i < rows) v[i].load(from, false, n);
-        }
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int i = 0; i < TOK; ++i) to.v[i][l] = v[i];
+          for (int c = 0; c < 2; ++c) *to.single(j + i, 32 * c + l) = v[i][c];
       }
     }
   }
@@ -257,9 +264,30 @@ struct Walk {
         }
       }
       __syncwarp();  // before the next copies arrive here
+    } else if (vec == 1) {
+      const bool whole = 2 * l + 1 < cols;
+      Two<T> v[TOK];
+#pragma unroll
+      for (int i = 0; i < TOK; ++i) v[i] = from.v[i][l];
+#pragma unroll
+      for (int i = 0; i < TOK; ++i, to += stride)
+        if (i < rows) v[i].store(to, whole, cols - 2 * l);
     } else {
-      for (int i = 0; i < TOK && i < rows; ++i, to += stride)
-        from.v[i][l].store(to, vec == 1 && 2 * l + 1 < cols, cols - 2 * l);
+      __syncwarp();
+#pragma unroll 1
+      for (int j = 0; j < TOK; j += 8) {
+        T v[8][2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) v[i][c] = *from.single(j + i, 32 * c + l);
+#pragma unroll
+        for (int i = 0; i < 8; ++i, to += stride)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            if (j + i < rows && 32 * c + l < cols) to[32 * c] = v[i][c];
+      }
+      __syncwarp();
     }
   }
 };

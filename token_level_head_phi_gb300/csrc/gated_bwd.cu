@@ -18,7 +18,7 @@ struct Stage {
 };
 static_assert(MHLA_GATED_MARK == 2 * 8, "every second warp starts at a mark");
 
-template <typename T, int KIND, bool IN, bool NORM>
+template <typename T, int KIND, bool IN, bool NORM, bool WIDE>
 __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 4))
     gated_bwd_kernel(const __grid_constant__ GatedArgs p) {
   constexpr int kTok = kGatedTok<sizeof(T) == 4, true>, kTile = kGatedWarps * kTok;
@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   const int b = unit / p.slabs, slab = unit - b * p.slabs, first = slab * kGatedSlab, cols = p.D - first;
   Stage<T, IN>* stage = reinterpret_cast<Stage<T, IN>*>(dynamic) + 2 * w;
   const Lane ln(slab, p.D);
+  const int vec = WIDE ? 2 : p.vec != 0;
   const int len = gated_length(p, b), round = kTile * ranks;
   const float2 lg = ln.get(KIND == MHLA_GATED_DECAY ? p.g : nullptr);
   const float2 g = make_float2(least(lg.x, 0.f), least(lg.y, 0.f)), g2 = mulc(g, kLog2e);
@@ -39,33 +40,33 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   const float2 zero = splat(0.f);
   // the gradient that reaches a token's state from behind it
   float2 carry = ln.get(p.dstate_out ? p.dstate_out + (int64_t)b * p.D : nullptr), dg = zero;
-  const bool whole = p.vec == 2 && cols >= kGatedSlab;
+  const bool whole = WIDE && cols >= kGatedSlab;
   const int rounds = (len + round - 1) / round, mine = rank * kTile + w * kTok;
 
   // The walks are formed anew where they are used: kept, they would take
   // registers that the tokens need.
   auto in = [&](const void* base, const mhla_strides& s) {
-    return Walk<T, const T>(static_cast<const T*>(base) + b * s.batch + first, s.token, p.vec);
+    return Walk<T, const T>(static_cast<const T*>(base) + b * s.batch + first, s.token, vec);
   };
   auto out = [&](void* base, const mhla_strides& s) {
-    return Walk<T, T>(static_cast<T*>(base) + b * s.batch + first, s.token, p.vec);
+    return Walk<T, T>(static_cast<T*>(base) + b * s.batch + first, s.token, vec);
   };
   auto fetch = [&](int slot, int t0) {
     if (t0 >= 0 && t0 < len) {
       const bool fast = whole && t0 + kTok <= len;
-      in(p.x, p.sx).fetch(stage[slot].x, t0, fast, len - t0, cols, p.vec);
-      in(p.dout, p.sdo).fetch(stage[slot].d, t0, fast, len - t0, cols, p.vec);
-      in(p.r, p.sr).fetch(stage[slot].r, t0, fast, len - t0, cols, p.vec);
-      if constexpr (IN) in(p.i, p.si).fetch(stage[slot].i[0], t0, fast, len - t0, cols, p.vec);
+      in(p.x, p.sx).fetch(stage[slot].x, t0, fast, len - t0, cols, vec);
+      in(p.dout, p.sdo).fetch(stage[slot].d, t0, fast, len - t0, cols, vec);
+      in(p.r, p.sr).fetch(stage[slot].r, t0, fast, len - t0, cols, vec);
+      if constexpr (IN) in(p.i, p.si).fetch(stage[slot].i[0], t0, fast, len - t0, cols, vec);
     }
     copies_commit();
   };
   auto write = [&](const Stage<T, IN>& from, int t0) {
     if (t0 >= p.N) return;
     const bool fast = whole && t0 + kTok <= p.N;
-    out(p.dx, p.sdx).write(from.x, t0, fast, p.N - t0, cols, p.vec);
-    out(p.dr, p.sdr).write(from.r, t0, fast, p.N - t0, cols, p.vec);
-    if constexpr (IN) out(p.di, p.sdi).write(from.i[0], t0, fast, p.N - t0, cols, p.vec);
+    out(p.dx, p.sdx).write(from.x, t0, fast, p.N - t0, cols, vec);
+    out(p.dr, p.sdr).write(from.r, t0, fast, p.N - t0, cols, vec);
+    if constexpr (IN) out(p.di, p.sdi).write(from.i[0], t0, fast, p.N - t0, cols, vec);
   };
   auto blank = [&](Stage<T, IN>& to, int j) {
     to.x.v[j][l].zero();
@@ -215,8 +216,8 @@ struct Backward {
   cudaStream_t s;
   template <typename T, int KIND, bool IN, bool NORM>
   mhla_status run() {
-    return launch_gated_clusters(gated_bwd_kernel<T, KIND, IN, NORM>, a, sizeof(T) == 4, true,
-                                 2 * kGatedWarps * sizeof(Stage<T, IN>), s);
+    auto kernel = a.vec == 2 ? gated_bwd_kernel<T, KIND, IN, NORM, true> : gated_bwd_kernel<T, KIND, IN, NORM, false>;
+    return launch_gated_clusters(kernel, a, sizeof(T) == 4, true, 2 * kGatedWarps * sizeof(Stage<T, IN>), s);
   }
   template <typename T, int KIND, bool IN>
   mhla_status go() {

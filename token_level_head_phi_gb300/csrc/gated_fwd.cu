@@ -21,7 +21,7 @@ struct Stage {
 
 // The warps of a CTA hand their states (alone) or the maps of their tokens (in a
 // cluster) from one to the next, without a barrier for all of them.
-template <typename T, int KIND, bool IN, bool NORM>
+template <typename T, int KIND, bool IN, bool NORM, bool WIDE>
 __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 4))
     gated_fwd_kernel(const __grid_constant__ GatedArgs p) {
   constexpr int kTok = kGatedTok<sizeof(T) == 4, false>, kTile = kGatedWarps * kTok;
@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   const int b = unit / p.slabs, slab = unit - b * p.slabs, first = slab * kGatedSlab, cols = p.D - first;
   Stage<T, IN>& my = reinterpret_cast<Stage<T, IN>*>(dynamic)[w];
   const Lane ln(slab, p.D);
+  const int vec = WIDE ? 2 : p.vec != 0;
   const int len = gated_length(p, b), round = kTile * ranks;  // tokens that the cluster takes at once
   const float2 lg = ln.get(KIND == MHLA_GATED_DECAY ? p.g : nullptr);
   const float2 g = make_float2(least(lg.x, 0.f), least(lg.y, 0.f)), g2 = mulc(g, kLog2e);
@@ -40,23 +41,23 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   const float2 k1 = splat(mean ? -1.f : 0.f), k0 = splat(mean ? 0.f : 1.f);  // c = k0 + k1 m
   float2 carry = ln.get(p.state_in ? p.state_in + (int64_t)b * p.D : nullptr);
   using In = Walk<T, const T>;
-  const In x(static_cast<const T*>(p.x) + b * p.sx.batch + first, p.sx.token, p.vec);
-  const In r(static_cast<const T*>(p.r) + b * p.sr.batch + first, p.sr.token, p.vec);
-  const In i(static_cast<const T*>(p.i) + b * p.si.batch + first, p.si.token, p.vec);
-  const Walk<T, T> out(static_cast<T*>(p.out) + b * p.so.batch + first, p.so.token, p.vec);
-  const bool whole = p.vec == 2 && cols >= kGatedSlab;
+  const In x(static_cast<const T*>(p.x) + b * p.sx.batch + first, p.sx.token, vec);
+  const In r(static_cast<const T*>(p.r) + b * p.sr.batch + first, p.sr.token, vec);
+  const In i(static_cast<const T*>(p.i) + b * p.si.batch + first, p.si.token, vec);
+  const Walk<T, T> out(static_cast<T*>(p.out) + b * p.so.batch + first, p.so.token, vec);
+  const bool whole = WIDE && cols >= kGatedSlab;
 
   auto fetch = [&](int slot, int t0) {
     if (t0 < len) {
       const bool fast = whole && t0 + kTok <= len;
-      x.fetch(my.x[slot], t0, fast, len - t0, cols, p.vec);
-      r.fetch(my.r[slot], t0, fast, len - t0, cols, p.vec);
-      if constexpr (IN) i.fetch(my.i[slot], t0, fast, len - t0, cols, p.vec);
+      x.fetch(my.x[slot], t0, fast, len - t0, cols, vec);
+      r.fetch(my.r[slot], t0, fast, len - t0, cols, vec);
+      if constexpr (IN) i.fetch(my.i[slot], t0, fast, len - t0, cols, vec);
     }
     copies_commit();
   };
   auto write = [&](int slot, int t0) {
-    if (p.out && t0 < p.N) out.write(my.x[slot], t0, whole && t0 + kTok <= p.N, p.N - t0, cols, p.vec);
+    if (p.out && t0 < p.N) out.write(my.x[slot], t0, whole && t0 + kTok <= p.N, p.N - t0, cols, vec);
   };
   auto mark = [&](int t0, float2 h) {
     if (p.marks && t0 % MHLA_GATED_MARK == 0 && t0 < p.N)
@@ -183,11 +184,14 @@ __global__ void __launch_bounds__(128) gated_step_kernel(const __grid_constant__
 struct Forward {
   const GatedArgs& a;
   cudaStream_t s;
+  template <typename T, int KIND, bool IN, bool NORM>
+  mhla_status run() {
+    auto kernel = a.vec == 2 ? gated_fwd_kernel<T, KIND, IN, NORM, true> : gated_fwd_kernel<T, KIND, IN, NORM, false>;
+    return launch_gated_clusters(kernel, a, sizeof(T) == 4, false, kGatedWarps * sizeof(Stage<T, IN>), s);
+  }
   template <typename T, int KIND, bool IN>
   mhla_status go() {
-    auto kernel = a.scale == MHLA_GATED_SCALE_NORM ? gated_fwd_kernel<T, KIND, IN, true>
-                                                   : gated_fwd_kernel<T, KIND, IN, false>;
-    return launch_gated_clusters(kernel, a, sizeof(T) == 4, false, kGatedWarps * sizeof(Stage<T, IN>), s);
+    return a.scale == MHLA_GATED_SCALE_NORM ? run<T, KIND, IN, true>() : run<T, KIND, IN, false>();
   }
 };
 
