@@ -248,9 +248,10 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
     int put = 0, got = 0;
     auto fetch = [&](int t0) {
       const T *from = x + t0 * p.sx.token, *fromd = dout + t0 * p.sdo.token;
+      const bool all = t0 + R <= copied;
 #pragma unroll
       for (int u = 0; u < R; ++u, from += p.sx.token, fromd += p.sdo.token)
-        if (t0 + u < copied) {
+        if (all || t0 + u < copied) {
           copy_async<V * (int)sizeof(T)>(place(put, u, 0), from, V * (int)sizeof(T));
           copy_async<V * (int)sizeof(T)>(place(put, u, 1), fromd, V * (int)sizeof(T));
         }
@@ -258,31 +259,9 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
       put = put < kAhead ? put + 1 : 0;
     };
     for (int i = 0; i < kAhead; ++i) fetch(at.first + i * R);
-    // Rows s < first belong to the segment before, but the first one's are the
-    // incoming state's.
-    for (int t0 = at.first; t0 < end; t0 += R) {
-      if (t0 - (K - 1) >= max(len, at.first)) {  // padding
-        r.zero();
-        for (int s = t0 - (K - 1); s < last; ++s) r.store(dx + s * p.sdx.token, whole, at.n);
-        break;
-      }
-      fetch(t0 + kAhead * R);
-      copies_wait<kAhead>();
-      Pack<T, V> row[R], rd[R];
-#pragma unroll
-      for (int u = 0; u < R; ++u) {
-        const int t = t0 + u;
-        if (t < copied) {
-          row[u] = *place(got, u, 0);
-          rd[u] = *place(got, u, 1);
-        } else {
-          load_row<V, T, K>(p, at, t, t < end ? len : 0, &row[u]);
-          rd[u].zero();
-          if (t < min(end, len)) rd[u].load(dout + t * p.sdo.token, whole, at.n);
-        }
-      }
-      got = got < kAhead ? got + 1 : 0;
-      const bool fast = inside(t0);
+    Pack<T, V> row[R], rd[R];
+    // The rows of a step, `fast` (a constant where it is called) inside.
+    auto step = [&](bool fast, int t0) {
       T* to = dx + (t0 - (K - 1)) * p.sdx.token;
 #pragma unroll
       for (int u = 0; u < R; ++u, to += p.sdx.token) {
@@ -322,22 +301,56 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
 #pragma unroll
           for (int c = 0; c < H; ++c) put_pair(&r, c, o[c]);
           r.store(to, true);
-          continue;
-        }
-        const int extra = s - (len - (K - 1));
-        if (t >= end || s < at.first - (at.first == 0 ? K - 1 : 0)) continue;
-        if (p.dstate_out && extra >= 0 && extra < K - 1) {  // the row went into the outgoing state
-          r.load(static_cast<const T*>(p.dstate_out) + ((int64_t)at.b * (K - 1) + extra) * p.D + at.ch, false, at.n);
+        } else {
+          const int extra = s - (len - (K - 1));
+          if (t >= end || s < at.first - (at.first == 0 ? K - 1 : 0)) continue;
+          if (p.dstate_out && extra >= 0 && extra < K - 1) {  // the row went into the outgoing state
+            r.load(static_cast<const T*>(p.dstate_out) + ((int64_t)at.b * (K - 1) + extra) * p.D + at.ch, false, at.n);
 #pragma unroll
-          for (int c = 0; c < H; ++c) o[c] = add2(o[c], pair_of(r, c));
-        }
+            for (int c = 0; c < H; ++c) o[c] = add2(o[c], pair_of(r, c));
+          }
 #pragma unroll
-        for (int c = 0; c < H; ++c) put_pair(&r, c, s < len ? o[c] : splat(0.f));
-        if (s >= 0)
-          r.store(dx + s * p.sdx.token, whole, at.n);
-        else if (p.dstate_in)
-          r.store(static_cast<T*>(p.dstate_in) + ((int64_t)at.b * (K - 1) + s + K - 1) * p.D + at.ch, false, at.n);
+          for (int c = 0; c < H; ++c) put_pair(&r, c, s < len ? o[c] : splat(0.f));
+          if (s >= 0)
+            r.store(dx + s * p.sdx.token, whole, at.n);
+          else if (p.dstate_in)
+            r.store(static_cast<T*>(p.dstate_in) + ((int64_t)at.b * (K - 1) + s + K - 1) * p.D + at.ch, false, at.n);
+        }
       }
+    };
+    // Rows s < first belong to the segment before, but the first one's are the
+    // incoming state's.
+    for (int t0 = at.first; t0 < end; t0 += R) {
+      if (t0 - (K - 1) >= max(len, at.first)) {  // padding
+        r.zero();
+        for (int s = t0 - (K - 1); s < last; ++s) r.store(dx + s * p.sdx.token, whole, at.n);
+        break;
+      }
+      fetch(t0 + kAhead * R);
+      copies_wait<kAhead>();
+      if (inside(t0)) {
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          row[u] = *place(got, u, 0);
+          rd[u] = *place(got, u, 1);
+        }
+        step(true, t0);
+      } else {
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          const int t = t0 + u;
+          if (t < copied) {
+            row[u] = *place(got, u, 0);
+            rd[u] = *place(got, u, 1);
+          } else {
+            load_row<V, T, K>(p, at, t, t < end ? len : 0, &row[u]);
+            rd[u].zero();
+            if (t < min(end, len)) rd[u].load(dout + t * p.sdo.token, whole, at.n);
+          }
+        }
+        step(false, t0);
+      }
+      got = got < kAhead ? got + 1 : 0;
     }
   }
   if (!p.partial) return;
