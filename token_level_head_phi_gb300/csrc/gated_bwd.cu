@@ -102,11 +102,16 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
       if constexpr (!NORM) return fma2(gt[j].m, k1, k0);
       return mul2(minus_v(gt[j].m), inv[j]);
     };
-    if (live)
+    if (live) {
+#pragma unroll
+      for (int j = kTok - 1; j >= 0; --j)
+        gt[j] = gates_of<KIND, IN>(least_gate(at.r.v[j][l]), IN ? least_gate(at.i[0].v[j][l]) : zero, g, g2);
+      if (!fast)
+#pragma unroll
+        for (int j = 0; j < kTok; ++j)
+          if (t0 + j >= len) gt[j].m = gt[j].s = gt[j].less = zero;  // keeps the state
 #pragma unroll
       for (int j = kTok - 1; j >= 0; --j) {
-        gt[j] = gates_of<KIND, IN>(least_gate(at.r.v[j][l]), IN ? least_gate(at.i[0].v[j][l]) : zero, g, g2);
-        if (!fast && t0 + j >= len) gt[j].m = gt[j].s = gt[j].less = zero;  // keeps the state
         const float2 a = addc(gt[j].m, 1.f);
         if constexpr (NORM) {
           // v^(-1/2) as v (max(v, tiny)^(-1/2))^3, which is 0 for v = 0
@@ -116,6 +121,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
         }
         map = then(map, Map{a, mul2(a, wide(at.d.v[j][l]))});
       }
+    }
     float2 e = carry;
     Map behind = same();
     if (ranks == 1) {

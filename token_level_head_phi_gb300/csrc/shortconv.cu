@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
     };
     for (int i = 0; i < kAhead; ++i) fetch(at.first + i * R);
     Pack<T, V> row[R], rd[R];
-    // The rows of a step, `fast` (a constant where it is called) inside.
-    auto step = [&](bool fast, int t0) {
+    // The rows of a step, `fast` (a constant where it is called, as `silu`) inside.
+    auto step = [&](bool fast, bool silu, int t0) {
       T* to = dx + (t0 - (K - 1)) * p.sdx.token;
 #pragma unroll
       for (int u = 0; u < R; ++u, to += p.sdx.token) {
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
         for (int c = 0; c < H; ++c) {
           const float2 xv = pair_of(row[u], c);
           float2 d = pair_of(rd[u], c);
-          if (p.silu) {
+          if (silu) {
             float2 z = fma2(w[K - 1][c], xv, bias[c]);
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) z = fma2(w[j][c], win[j][c], z);
@@ -334,7 +334,10 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
           row[u] = *place(got, u, 0);
           rd[u] = *place(got, u, 1);
         }
-        step(true, t0);
+        if (p.silu)
+          step(true, true, t0);
+        else
+          step(true, false, t0);
       } else {
 #pragma unroll
         for (int u = 0; u < R; ++u) {
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
             if (t < min(end, len)) rd[u].load(dout + t * p.sdo.token, whole, at.n);
           }
         }
-        step(false, t0);
+        step(false, p.silu, t0);
       }
       got = got < kAhead ? got + 1 : 0;
     }
