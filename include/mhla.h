@@ -444,9 +444,10 @@ mhla_status mhla_decay_step(const void* q, const void* k, const void* v, const f
 /* Norm of queries and keys over each head and their rotary positions in one
  * pass: with rstd = 1 / sqrt(mean(x^2) + eps) over a row,
  *   y = R(position) (x rstd * weight),
- * R the map of mhla_rotary (its styles, tables and positions).  Squares and
- * sums in float32: rows whose squares leave its range (entries beyond 1e19)
- * come out as zeros, as their rstd is 0. */
+ * R the map of mhla_rotary (its styles, tables and positions; sines of bf16
+ * rows are off by up to 2^-21).  Squares and sums in float32: rows whose
+ * squares leave its range (entries beyond 1e19) come out as zeros, as their
+ * rstd is 0. */
 typedef struct mhla_qknorm_params {
   int batch, tokens;         /* >= 0                                                     */
   int heads, kv_heads;       /* >= 0, <= 32768: heads of q and of k                      */
@@ -489,7 +490,8 @@ mhla_status mhla_qknorm_backward(const void* dq_out, const void* dk_out, const v
  * h_t and state_out = h_{length-1}; sigma is the logistic function, u_t = x_t
  * without an input gate.  States are float32 [batch, width], contiguous.
  * DECAY: a = exp(log_decay sigma(gate)) with log_decay float32 [width], finite
- * and <= 0; SIGMOID: a = sigma(gate), without log_decay.
+ * and <= 0; SIGMOID: a = sigma(gate), without log_decay.  Gates below -43 are
+ * taken as -43 (sigma 2e-19).
  * NORM: c = sqrt(max(1 - a^2, 0)) (inputs and states of one size), MEAN:
  * c = 1 - a (a running mean), NONE: c = 1.
  * All arithmetic in float32, a result is rounded once. */

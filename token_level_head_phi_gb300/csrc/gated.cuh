@@ -14,7 +14,9 @@
 // asynchronous copies into shared memory of the warp's own, a round ahead.
 // Where sequences and channels are few, a cluster of CTAs takes successive tiles
 // of the same channels at once and exchanges the tiles' maps through distributed
-// shared memory.
+// shared memory.  Rows of whole 16 bytes have kernels of their own, without the
+// code for others (64 x 512 tokens of 4096 channels backward 470 us with it, 389
+// without).
 #pragma once
 
 #include "common.cuh"
@@ -30,7 +32,7 @@ constexpr int kGatedCluster = 8;  // most CTAs of a cluster
 template <bool F32, bool BACKWARD>
 constexpr int kGatedTok = BACKWARD || F32 ? 8 : 16;
 inline int gated_tile(bool f32, bool backward) { return kGatedWarps * (backward || f32 ? 8 : 16); }
-// CTAs that an SM holds: their registers, and the shared memory of float32's
+// CTAs that an SM holds: for their registers, and the shared memory of float32's
 // backward pass.
 constexpr int gated_resident(bool f32) { return f32 ? 1 : 2; }
 

@@ -8,7 +8,10 @@
 // group forms the sines of its token once and walks over the heads.  Phases
 // are the 64-bit fractions of a turn of mhla_rotary_table.
 // Bound: memory (each row read once and written once; the backward pass reads
-// two rows and writes one).
+// two rows and writes one), with the latency of a row's sums where heads are
+// wide: 16 + 4 heads of 64 over 4 x 32k tokens (bf16) take 116 us forward, 5.8 TB/s,
+// and 176 us backward; of 128 over 2 x 8k tokens 33 us (25 at the rate of a copy)
+// and 51 us (37), of which 3 us add the weights' gradients.
 #include <algorithm>
 #include <cmath>
 
