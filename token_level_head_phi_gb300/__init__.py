@@ -7,7 +7,8 @@ inputs.  Importing the package loads nothing: the binding loads the library
 on first use and raises if it is missing.
 
 The binding also holds the operators of a decayed linear-attention layer
-(``mhla_decay_*``, ``mhla_rotary_*``, ``mhla_layernorm_*``).
+(``mhla_decay_*``, ``mhla_rotary_*``, ``mhla_layernorm_*``, ``mhla_qknorm_*``)
+and of a recurrent one (``mhla_gated_*``, ``mhla_shortconv_*``).
 """
 
 __all__ = ["binding", "workloads", "build"]
