@@ -360,8 +360,8 @@ inline int gated_clusters(int n, int resident) {
 // CTAs of a cluster: the number with the least time, counted in rounds of tiles
 // over the waves of clusters that the GPU holds at once; of equal ones the
 // smallest.  A round takes 1.8 us (backward 2.4) of a CTA alone on its SM, 3.2
-// (3.9) of two alone on one SM and 4.1 (4.7) in a cluster, whose warps wait for
-// the maps of all of its tiles.  5 x 1999 tokens of 1024 channels forward take 29
+// (3.9) of two alone on one SM and 4.1 to 5.2 (4.7) in a cluster, whose warps wait
+// for the maps of all of its tiles.  5 x 1999 tokens of 1024 channels forward take 29
 // us alone, 32 in pairs, 25 in threes and 28 in eights; backward 76, 74, 53 and
 // 59; 16 x 256 tokens forward 8.5 alone and 13 in pairs; 3 x 777 of 321 float32
 // channels 30 alone, 12 in sixes and 16 in eights, of which only 15 fit.
@@ -374,7 +374,7 @@ inline int gated_cluster(int64_t units, int tokens, bool f32, bool backward) {
     const int held = gated_clusters(n, resident);
     int round = 8;
     if (n > 1)
-      round = backward ? 15 : 18;
+      round = backward ? 15 : 20;
     else if (resident > 1 && units > kOpsSms)
       round = backward ? 13 : 14;
     const int64_t cost = (units + held - 1) / held * ((tiles + n - 1) / n) * round;
