@@ -25,14 +25,16 @@ struct Stage {
   Rows<T, kTok> x[2], r[2], i[IN ? 2 : 0];
 };
 
-// The warps of a CTA hand their states (alone) or the maps of their tokens (in a
-// cluster) from one to the next, without a barrier for all of them.
+// The warps of a CTA alone hand their states from one to the next, without a
+// barrier for all of them.  In a cluster all wait for the others' tiles anyway:
+// each shows the map of its tokens to the warps behind it (2 x 8k tokens of 1024
+// channels 40 us, handed on from warp to warp 41; backward 80 and 78).
 template <typename T, int KIND, bool IN, bool NORM, bool WIDE>
 __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 4))
     gated_fwd_kernel(const __grid_constant__ GatedArgs p) {
   constexpr int kTok = kGatedTok<sizeof(T) == 4, false>, kTile = kGatedWarps * kTok;
   extern __shared__ __align__(16) unsigned char dynamic[];
-  __shared__ Map mail[kGatedWarps][32];
+  __shared__ Map mail[2][kGatedWarps][32];  // alone the first half, for the states
   __shared__ Map tiles[2][kGatedCluster][32];
   const int rank = cluster_rank(), ranks = cluster_size(), unit = blockIdx.x / ranks;
   const int w = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), l = threadIdx.x & 31;
@@ -102,28 +104,28 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
       h = carry;
       if (w > 0 || base > 0) {
         take_over(1 + w);
-        h = mail[w][l].H;
+        h = mail[0][w][l].H;
       }
       carry = through(map, h);
       if (w < kGatedWarps - 1 || base + round < len) {
         const int to = (w + 1) % kGatedWarps;
-        mail[to][l].H = carry;
+        mail[0][to][l].H = carry;
         hand_over(1 + to);
       }
     } else {
+      store_map(&mail[turn][w][l], map);
+      __syncthreads();
       Map before = same();
-      if (w > 0) {
-        take_over(1 + w);
-        before = load_map(&mail[w][l]);
-      }
-      const Map all = then(before, map);
-      if (w < kGatedWarps - 1) {
-        store_map(&mail[w + 1][l], all);
-        hand_over(2 + w);
-      } else {
+      auto compose = [&] {
+        for (int v = 0; v < w; ++v) before = then(before, load_map(&mail[turn][v][l]));
+      };
+      if (w == kGatedWarps - 1) {
+        compose();
+        const Map all = then(before, map);
         for (int v = 0; v < ranks; ++v) send(&tiles[turn][rank][l], v, all);
       }
       cluster_arrive();
+      if (w < kGatedWarps - 1) compose();
       cluster_wait();
       h = carry;
       for (int v = 0; v < rank; ++v) h = through(load_map(&tiles[turn][v][l]), h);
@@ -147,9 +149,9 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   // alone, the last warp has the final state, and marks past the length need it
   if (ranks == 1 && len > 0 && p.marks) {
     __syncthreads();
-    if (w == kGatedWarps - 1) mail[0][l].H = carry;
+    if (w == kGatedWarps - 1) mail[0][0][l].H = carry;
     __syncthreads();
-    carry = mail[0][l].H;
+    carry = mail[0][0][l].H;
   }
   if (p.state_out && rank == 0 && w == kGatedWarps - 1) ln.put(p.state_out + (int64_t)b * p.D, carry);
   if (t0 >= p.N) return;
