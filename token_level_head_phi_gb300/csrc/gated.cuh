@@ -212,34 +212,42 @@ struct Walk {
           *reinterpret_cast<uint4*>(place) = make_uint4(0, 0, 0, 0);
       }
     } else if (vec == 1) {
-      const T* some = from - 2 * l;  // there, where the lane's channels are not
+      // columns that are not there are lanes of their own, whose values nobody uses
       const int n = min(max(cols - 2 * l, 0), 2) * (int)sizeof(T);
+      if (n && rows >= TOK) {
 #pragma unroll
-      for (int i = 0; i < TOK; ++i, from += stride) {
-        const int bytes = i < rows ? n : 0;
-        copy_async<2 * sizeof(T)>(&to.v[i][l], bytes ? from : some, bytes);
+        for (int i = 0; i < TOK; ++i, from += stride) copy_async<2 * sizeof(T)>(&to.v[i][l], from, n);
+      } else if (n) {
+        const T* some = from;
+#pragma unroll 4
+        for (int i = 0; i < TOK; ++i, from += stride)
+          copy_async<2 * sizeof(T)>(&to.v[i][l], i < rows ? from : some, i < rows ? n : 0);
       }
-    } else if constexpr (sizeof(T) == 4) {
-      const T* some = from - l;
+    } else {
 #pragma unroll
-      for (int i = 0; i < TOK; ++i, from += stride)
+      for (int c = 0; c < 64; c += 32) {
+        const T* at = from + c;
+        if (c + l >= cols) continue;
+        if constexpr (sizeof(T) == 4) {
+          if (rows >= TOK) {
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          const bool there = i < rows && c + l < cols;
-          copy_async<4>(to.single(i, c + l), there ? from + c : some, there ? 4 : 0);
+            for (int i = 0; i < TOK; ++i, at += stride) copy_async<4>(to.single(i, c + l), at, 4);
+          } else {
+            const T* some = at;
+#pragma unroll 4
+            for (int i = 0; i < TOK; ++i, at += stride)
+              copy_async<4>(to.single(i, c + l), i < rows ? at : some, i < rows ? 4 : 0);
+          }
+        } else if (rows >= TOK) {  // no copies of 2 bytes: all rows into registers, then on
+          T v[TOK];
+#pragma unroll
+          for (int i = 0; i < TOK; ++i, at += stride) v[i] = *at;
+#pragma unroll
+          for (int i = 0; i < TOK; ++i) *to.single(i, c + l) = v[i];
+        } else {
+#pragma unroll 4
+          for (int i = 0; i < TOK; ++i, at += stride) *to.single(i, c + l) = i < rows ? *at : from_f32<T>(0.f);
         }
-    } else {  // no copies of 2 bytes: eight rows into registers, then on
-#pragma unroll 1
-      for (int j = 0; j < TOK; j += 8) {
-        T v[8][2];
-#pragma unroll
-        for (int i = 0; i < 8; ++i, from += stride)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) v[i][c] = j + i < rows && 32 * c + l < cols ? from[32 * c] : from_f32<T>(0.f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) *to.single(j + i, 32 * c + l) = v[i][c];
       }
     }
   }
@@ -268,26 +276,35 @@ struct Walk {
       __syncwarp();  // before the next copies arrive here
     } else if (vec == 1) {
       const bool whole = 2 * l + 1 < cols;
+      if (2 * l >= cols) return;
       Two<T> v[TOK];
 #pragma unroll
       for (int i = 0; i < TOK; ++i) v[i] = from.v[i][l];
+      if (rows >= TOK && whole) {
 #pragma unroll
-      for (int i = 0; i < TOK; ++i, to += stride)
-        if (i < rows) v[i].store(to, whole, cols - 2 * l);
+        for (int i = 0; i < TOK; ++i, to += stride) v[i].store(to, true);
+      } else {
+#pragma unroll
+        for (int i = 0; i < TOK; ++i, to += stride)
+          if (i < rows) v[i].store(to, whole, cols - 2 * l);
+      }
     } else {
       __syncwarp();
-#pragma unroll 1
-      for (int j = 0; j < TOK; j += 8) {
-        T v[8][2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+      for (int c = 0; c < 64; c += 32) {
+        P* at = to + c;
+        if (c + l >= cols) continue;
+        T v[TOK];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) v[i][c] = *from.single(j + i, 32 * c + l);
+        for (int i = 0; i < TOK; ++i) v[i] = *from.single(i, c + l);
+        if (rows >= TOK) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i, to += stride)
+          for (int i = 0; i < TOK; ++i, at += stride) *at = v[i];
+        } else {
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            if (j + i < rows && 32 * c + l < cols) to[32 * c] = v[i][c];
+          for (int i = 0; i < TOK; ++i, at += stride)
+            if (i < rows) *at = v[i];
+        }
       }
       __syncwarp();
     }
