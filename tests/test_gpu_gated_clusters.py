@@ -6,6 +6,8 @@ import pytest
 import torch
 from test_gpu_gated import check, problem
 
+from token_level_head_phi_gb300 import binding as mb
+
 pytestmark = pytest.mark.gpu
 
 
@@ -23,3 +25,33 @@ pytestmark = pytest.mark.gpu
 def test_sizes(b, n, d, dtype, ragged):
     lengths = torch.tensor([n // 3, n, 0, 65, n - 1][:b], dtype=torch.int32).cuda() if ragged else None
     check(problem(b, n, d, dtype, "decay", True, ragged), dtype, "norm", lengths, ragged)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("b,n,d", [(3, 333, 65), (2, 200, 130), (40, 70, 321), (1, 1300, 63)])
+def test_row_starts_do_not_change_results(b, n, d, dtype):
+    """The same rows at single elements, at pairs (with a lone last column where d is odd) and at 16
+    bytes, each time with columns behind them that have to stay."""
+    lengths = torch.tensor([n - i % 7 for i in range(b)], dtype=torch.int32).cuda()
+    decay = -torch.rand(d, generator=torch.Generator().manual_seed(3)).cuda()
+    values = [torch.randn(b, n, d, generator=torch.Generator().manual_seed(i)).to(dtype).cuda() for i in range(4)]
+    want = None
+    for width, first in ((d + 16 + d % 2, 1), (d + 18 + d % 2, 2), ((d + 15) // 8 * 8 + 8, 8)):
+        def place(t=None):
+            memory = torch.full((b, n, width + first), 7.0, dtype=dtype, device="cuda")[:, :, :width]
+            view = memory[:, :, first:first + d]
+            if t is not None:
+                view.copy_(t)
+            return memory, view
+
+        x, r, i, do = (place(t)[1] for t in values)
+        (mo, out), (mx, dx), (mr, dr), (mi, di) = (place() for _ in range(4))
+        _, state, marks = mb.mhla_gated_forward(x, r, decay, i, lengths=lengths, out=out, keep=True)
+        grads = mb.mhla_gated_backward(x, r, do, decay, i, marks=marks, lengths=lengths, dx=dx, dgate=dr, dinput_gate=di)
+        got = [t.clone() for t in (out, state, marks, dx, dr, di, grads[3])]
+        for memory, view in ((mo, out), (mx, dx), (mr, dr), (mi, di)):
+            view.fill_(7.0)
+            assert (memory == 7.0).all()
+        if want is None:
+            want = got
+        assert all(torch.equal(a, t) for a, t in zip(got, want)), (width, first)
