@@ -191,3 +191,36 @@ def test_results_do_not_change():
 
 def test_no_device_error_was_reported():
     assert mb.mhla_device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("first", [0, 1, 2, 3])
+@pytest.mark.parametrize("d", [1, 2, 3, 5, 129, 131])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_what_lies_around_single_elements_is_not_used(first, d, dtype):
+    """Rows that start at any element, NaN before the first, behind the last, between them and past the lengths."""
+    b, n, width = 3, 41, d + 3
+    gen = torch.Generator().manual_seed(d)
+    w, bias = torch.randn(d, 4, generator=gen).cuda(), torch.randn(d, generator=gen).cuda()
+    lengths = torch.tensor([41, 17, 0], dtype=torch.int32).cuda()
+
+    def place():
+        t = torch.randn(b, n, d, generator=gen).to(dtype).cuda()
+        for i, k in enumerate((41, 17, 0)):
+            t[i, k:] = 0
+        memory = torch.full((first + b * n * width,), float("nan"), dtype=dtype, device="cuda")
+        view = memory.as_strided((b, n, d), (n * width, width, 1), first)
+        view.copy_(t)
+        for i, k in enumerate((41, 17, 0)):
+            view[i, k:] = float("nan")
+        return t, memory, view
+
+    (x, _, xv), (do, _, dov) = place(), place()
+    out, state = mb.mhla_shortconv_forward(x, w, bias, lengths=lengths, activation="silu")
+    dx, dw, db, _ = mb.mhla_shortconv_backward(x, w, do, bias, lengths=lengths, activation="silu")
+    _, memory, result = place()
+    got = mb.mhla_shortconv_forward(xv, w, bias, lengths=lengths, activation="silu", out=result)
+    assert torch.equal(result, out) and torch.equal(got[1], state)
+    grads = mb.mhla_shortconv_backward(xv, w, dov, bias, lengths=lengths, activation="silu", dx=result)
+    assert torch.equal(result, dx) and torch.equal(grads[1], dw) and torch.equal(grads[2], db)
+    result.fill_(float("nan"))
+    assert memory.isnan().all()  # nothing was written between the rows

@@ -129,10 +129,80 @@ __device__ __forceinline__ void load_row(const ConvArgs& p, const Place& at, int
   }
 }
 
-template <typename T, int K, int V>
+// A thread's V elements of a row, by asynchronous copies into a place of its own.
+// SINGLE: rows start at single elements, and `n` of the V are there.  bf16 then
+// comes in words, the first and last of which may hold a neighbour's element (of
+// the same tensor, which lies between lo and hi), and is shifted when it is used.
+template <typename T, int V, bool SINGLE>
+struct Slot {
+  static constexpr bool kWords = SINGLE && sizeof(T) == 2;
+  static_assert(!kWords || V == 4, "three words");
+  alignas(kWords ? 16 : V * sizeof(T)) unsigned char v[kWords ? 16 : V * sizeof(T)];
+  __device__ __forceinline__ void start(const T* from, int n, const T* lo, const T* hi) {
+    if constexpr (kWords) {
+      const int odd = (int)((uintptr_t)from >> 1) & 1, words = (n + odd + 1) >> 1;
+      const T* first = from - odd;
+      if (first >= lo && first + 2 * words <= hi) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if (i < words) copy_async<4>(v + 4 * i, first + 2 * i, 4);
+      } else {  // the tensor's first or last element
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i < n) reinterpret_cast<T*>(v)[odd + i] = from[i];
+      }
+    } else if constexpr (SINGLE) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < n) copy_async<sizeof(T)>(v + sizeof(T) * i, from + i, sizeof(T));
+    } else {
+      copy_async<V * (int)sizeof(T)>(v, from, V * (int)sizeof(T));
+    }
+  }
+  __device__ __forceinline__ Pack<T, V> take(const T* from) const {
+    if constexpr (kWords) {
+      const uint4 w = *reinterpret_cast<const uint4*>(v);
+      const int shift = (int)((uintptr_t)from >> 1 & 1) * 16;
+      Pack<T, V> r;
+      reinterpret_cast<uint32_t*>(r.v)[0] = __funnelshift_r(w.x, w.y, shift);
+      reinterpret_cast<uint32_t*>(r.v)[1] = __funnelshift_r(w.y, w.z, shift);
+      return r;
+    } else {
+      return *reinterpret_cast<const Pack<T, V>*>(v);
+    }
+  }
+  // Writes a row's elements.
+  __device__ __forceinline__ static void store(T* to, const Pack<T, V>& r, int n) {
+    if (SINGLE && n < V) {
+      r.store(to, false, n);
+    } else if constexpr (kWords) {
+      const uint32_t a = reinterpret_cast<const uint32_t*>(r.v)[0], b = reinterpret_cast<const uint32_t*>(r.v)[1];
+      if ((uintptr_t)to & 2) {
+        to[0] = r.v[0];
+        *reinterpret_cast<uint32_t*>(to + 1) = __funnelshift_r(a, b, 16);
+        to[3] = r.v[3];
+      } else {
+        reinterpret_cast<uint32_t*>(to)[0] = a;
+        reinterpret_cast<uint32_t*>(to)[1] = b;
+      }
+    } else {
+      r.store(to, !SINGLE);
+    }
+  }
+};
+
+// One behind the last element of a tensor.
+template <typename T>
+__device__ __forceinline__ const T* end_of(const ConvArgs& p, const void* t, const mhla_strides& s) {
+  return static_cast<const T*>(t) + (p.B - 1) * s.batch + (p.N - 1) * s.token + p.D;
+}
+
+template <typename T, int K, int V, bool SINGLE>
 __global__ void __launch_bounds__(kThreads, resident(kForward, sizeof(T)))
     conv_fwd_kernel(const __grid_constant__ ConvArgs p) {
   constexpr int H = V / 2;
+  using Row = Slot<T, V, SINGLE>;
+  extern __shared__ __align__(16) unsigned char dynamic[];  // SINGLE: rows on their way
   const Place at(p);
   if (!at.live) return;
   const int len = length_of(p, at.b), last = min(at.first + p.seg, p.N);
@@ -148,10 +218,9 @@ __global__ void __launch_bounds__(kThreads, resident(kForward, sizeof(T)))
   }
   const T* x = static_cast<const T*>(p.x) + at.b * p.sx.batch + at.ch;
   T* out = static_cast<T*>(p.out) + at.b * p.so.batch + at.ch;
-  const bool whole = p.whole && at.n == V;
-  const int inside = whole ? min(last, len) : at.first;  // steps up to here need no checks
-  constexpr int R = kFwdRows;
-  Pack<T, V> rows[2][R];
+  const bool whole = !SINGLE && p.whole && at.n == V;
+  const int inside = SINGLE || whole ? min(last, len) : at.first;  // steps up to here need no checks
+  constexpr int R = SINGLE ? kBwdRows<K> : kFwdRows;
   auto fetch = [&](Pack<T, V>(&to)[R], int t0) {
     if (t0 + R <= inside) {
       const T* from = x + t0 * p.sx.token;
@@ -181,25 +250,60 @@ __global__ void __launch_bounds__(kThreads, resident(kForward, sizeof(T)))
         put_pair(&o, c, z);
       }
       if (t0 + R <= inside) {
-        o.store(to, true);
+        Row::store(to, o, at.n);
       } else if (t < last) {
         if (t >= len) o.zero();
         o.store(to, whole, at.n);
       }
     }
   };
-  fetch(rows[0], at.first);
-  for (int t0 = at.first; t0 < last; t0 += 2 * R) {
-    if (t0 >= len) {  // padding
-      r.zero();
-      for (int t = t0; t < last; ++t) r.store(out + t * p.so.token, whole, at.n);
-      break;
+  auto pad = [&](int t0) {
+    r.zero();
+    for (int t = t0; t < last; ++t) r.store(out + t * p.so.token, whole, at.n);
+  };
+  if constexpr (SINGLE) {
+    const T* x_end = end_of<T>(p, p.x, p.sx);
+    Row* places = reinterpret_cast<Row*>(dynamic) + threadIdx.x;
+    int put = 0, got = 0;
+    auto start = [&](int t0) {
+      const T* from = x + t0 * p.sx.token;
+#pragma unroll
+      for (int u = 0; u < R; ++u, from += p.sx.token)
+        if (t0 + u < inside) places[(put * R + u) * kThreads].start(from, at.n, static_cast<const T*>(p.x), x_end);
+      copies_commit();
+      put = put < kAhead ? put + 1 : 0;
+    };
+    for (int i = 0; i < kAhead; ++i) start(at.first + i * R);
+    for (int t0 = at.first; t0 < last; t0 += R) {
+      if (t0 >= len) {
+        pad(t0);
+        break;
+      }
+      start(t0 + kAhead * R);
+      copies_wait<kAhead>();
+      Pack<T, V> row[R];
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        row[u].zero();
+        if (t0 + u < inside) row[u] = places[(got * R + u) * kThreads].take(x + (t0 + u) * p.sx.token);
+      }
+      got = got < kAhead ? got + 1 : 0;
+      step(row, t0);
     }
-    fetch(rows[1], t0 + R);
-    step(rows[0], t0);
-    if (t0 + R >= last) break;
-    fetch(rows[0], t0 + 2 * R);
-    step(rows[1], t0 + R);
+  } else {
+    Pack<T, V> rows[2][R];
+    fetch(rows[0], at.first);
+    for (int t0 = at.first; t0 < last; t0 += 2 * R) {
+      if (t0 >= len) {
+        pad(t0);
+        break;
+      }
+      fetch(rows[1], t0 + R);
+      step(rows[0], t0);
+      if (t0 + R >= last) break;
+      fetch(rows[0], t0 + 2 * R);
+      step(rows[1], t0 + R);
+    }
   }
   if (p.state_out && at.first == 0) {
     // the same thread that read state_in, which this may be
@@ -212,10 +316,11 @@ __global__ void __launch_bounds__(kThreads, resident(kForward, sizeof(T)))
   }
 }
 
-template <typename T, int K, int V>
+template <typename T, int K, int V, bool SINGLE>
 __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
     conv_bwd_kernel(const __grid_constant__ ConvArgs p) {
   constexpr int H = V / 2, R = kBwdRows<K>;
+  using Row = Slot<T, V, SINGLE>;
   extern __shared__ __align__(16) float sums[];  // rows on their way; then [down][(K + 1) * V][across]
   const Place at(p);
   float2 dw[K + 1][H];
@@ -238,17 +343,19 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
         dz[j][c] = splat(0.f);
       }
     }
-    const bool whole = p.whole && at.n == V;
+    const bool whole = !SINGLE && p.whole && at.n == V;
+    const bool quick = SINGLE || whole;
     const T* x = static_cast<const T*>(p.x) + at.b * p.sx.batch + at.ch;
     const T* dout = static_cast<const T*>(p.dout) + at.b * p.sdo.batch + at.ch;
     T* dx = static_cast<T*>(p.dx) + at.b * p.sdx.batch + at.ch;
+    const T *x_end = end_of<T>(p, p.x, p.sx), *dout_end = end_of<T>(p, p.dout, p.sdo);
     // Steps inside need no checks: their rows are before the length and the
     // segment's end, and the rows s = t - (K - 1) of dx not before its start.
-    auto inside = [&](int t0) { return whole && t0 >= at.first + K - 1 && t0 + R <= min(last, len); };
+    auto inside = [&](int t0) { return quick && t0 >= at.first + K - 1 && t0 + R <= min(last, len); };
     // Rows of x and dout go through shared memory of the thread's own.
-    const int copied = whole ? min(end, len) : at.first;
+    const int copied = quick ? min(end, len) : at.first;
     auto place = [&](int slot, int u, int which) {
-      return reinterpret_cast<Pack<T, V>*>(sums) + ((slot * R + u) * 2 + which) * kThreads + threadIdx.x;
+      return reinterpret_cast<Row*>(sums) + ((slot * R + u) * 2 + which) * kThreads + threadIdx.x;
     };
     int put = 0, got = 0;
     auto fetch = [&](int t0) {
@@ -257,8 +364,8 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
 #pragma unroll
       for (int u = 0; u < R; ++u, from += p.sx.token, fromd += p.sdo.token)
         if (all || t0 + u < copied) {
-          copy_async<V * (int)sizeof(T)>(place(put, u, 0), from, V * (int)sizeof(T));
-          copy_async<V * (int)sizeof(T)>(place(put, u, 1), fromd, V * (int)sizeof(T));
+          place(put, u, 0)->start(from, at.n, static_cast<const T*>(p.x), x_end);
+          place(put, u, 1)->start(fromd, at.n, static_cast<const T*>(p.dout), dout_end);
         }
       copies_commit();
       put = put < kAhead ? put + 1 : 0;
@@ -305,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
         if (fast) {
 #pragma unroll
           for (int c = 0; c < H; ++c) put_pair(&r, c, o[c]);
-          r.store(to, true);
+          Row::store(to, r, at.n);
         } else {
           const int extra = s - (len - (K - 1));
           if (t >= end || s < at.first - (at.first == 0 ? K - 1 : 0)) continue;
@@ -336,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
       if (inside(t0)) {
 #pragma unroll
         for (int u = 0; u < R; ++u) {
-          row[u] = *place(got, u, 0);
-          rd[u] = *place(got, u, 1);
+          row[u] = place(got, u, 0)->take(x + (t0 + u) * p.sx.token);
+          rd[u] = place(got, u, 1)->take(dout + (t0 + u) * p.sdo.token);
         }
         if (p.silu)
           step(true, true, t0);
@@ -348,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, resident(kBackward, sizeof(T)))
         for (int u = 0; u < R; ++u) {
           const int t = t0 + u;
           if (t < copied) {
-            row[u] = *place(got, u, 0);
-            rd[u] = *place(got, u, 1);
+            row[u] = place(got, u, 0)->take(x + t * p.sx.token);
+            rd[u] = place(got, u, 1)->take(dout + t * p.sdo.token);
           } else {
             load_row<V, T, K>(p, at, t, t < end ? len : 0, &row[u]);
             rd[u].zero();
@@ -475,20 +582,26 @@ mhla_status launch(const ConvArgs& a, int what, cudaStream_t s) {
     return launch_status();
   }
   const unsigned grid = (unsigned)(a.columns * grid_down(a));
-  // backward: the rows on their way, then the sums; both are at most 48 KB
-  const size_t rows = sizeof(T) * a.width * 2 * kBwdRows<K> * (kAhead + 1) * kThreads;
-  const size_t sums = a.partial ? sizeof(float) * (K + 1) * a.width * kThreads : 0, smem = rows > sums ? rows : sums;
-  if constexpr (sizeof(T) == 4) {  // see choose_width
-    if (what == kForward)
-      conv_fwd_kernel<T, K, 4><<<grid, kThreads, 0, s>>>(a);
-    else
-      conv_bwd_kernel<T, K, 2><<<grid, kThreads, smem, s>>>(a);
-  } else {
-    if (what == kForward)
-      (a.width == 4 ? conv_fwd_kernel<T, K, 4> : conv_fwd_kernel<T, K, 2>)<<<grid, kThreads, 0, s>>>(a);
-    else
-      (a.width == 4 ? conv_bwd_kernel<T, K, 4> : conv_bwd_kernel<T, K, 2>)<<<grid, kThreads, smem, s>>>(a);
+  constexpr int kBack = sizeof(T) == 4 ? 2 : 4;  // see choose_width
+  if (what == kForward) {
+    auto kernel = a.whole ? conv_fwd_kernel<T, K, 4, false> : conv_fwd_kernel<T, K, 4, true>;
+    if constexpr (sizeof(T) == 2)
+      if (a.width == 2) kernel = conv_fwd_kernel<T, K, 2, false>;
+    // at most 36 KB
+    const size_t smem = a.whole ? 0 : sizeof(Slot<T, 4, true>) * kBwdRows<K> * (kAhead + 1) * kThreads;
+    kernel<<<grid, kThreads, smem, s>>>(a);
+    return launch_status();
   }
+  auto kernel = a.whole ? conv_bwd_kernel<T, K, kBack, false> : conv_bwd_kernel<T, K, kBack, true>;
+  if constexpr (sizeof(T) == 2)
+    if (a.width == 2) kernel = conv_bwd_kernel<T, K, 2, false>;
+  // the rows on their way, then the sums
+  const size_t slot = a.whole ? sizeof(T) * a.width : sizeof(Slot<T, kBack, true>);
+  const size_t rows = slot * 2 * kBwdRows<K> * (kAhead + 1) * kThreads;
+  const size_t sums = a.partial ? sizeof(float) * (K + 1) * a.width * kThreads : 0, smem = rows > sums ? rows : sums;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  kernel<<<grid, kThreads, smem, s>>>(a);
   return launch_status();
 }
 
@@ -543,7 +656,8 @@ bool apart(const RowTensor* in, int n_in, const RowTensor* out, int n_out, int s
 // Channels of a thread: four, in one access where rows allow it, but two of
 // float32 in the backward pass, whose registers they fill (4 x 8k x 1024: 68 us,
 // with four 74), and two of bf16 where rows start at pairs only (4 x 4k x 1030:
-// forward 21 and backward 36 us, with four single accesses 37 and 87).
+// forward 21 and backward 36 us; of 1001, in words of shared memory, 25 and 54,
+// element by element 31 and 88).
 void choose_width(ConvArgs* a, const RowTensor* t, int n, const RowTensor& last, int dtype, bool backward) {
   int align = row_alignment(last, 16);
   for (int i = 0; i < n; ++i) {
