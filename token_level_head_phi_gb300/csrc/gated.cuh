@@ -31,6 +31,10 @@ constexpr int kGatedCluster = 8;  // most CTAs of a cluster
 // tokens of a warp and of a CTA's tile
 template <bool F32, bool BACKWARD>
 constexpr int kGatedTok = BACKWARD || F32 ? 8 : 16;
+// A kernel for rows that start at pairs or at single elements of bf16; of float32
+// each has one of its own (5 x 1999 x 1009 backward 101 us, in one 115; bf16 pairs,
+// 1010 channels, 71 us in one, 85 apart, where registers spill).
+constexpr int kGatedNarrow = -1;
 inline int gated_tile(bool f32, bool backward) { return kGatedWarps * (backward || f32 ? 8 : 16); }
 // CTAs that an SM holds: for their registers, and the shared memory of float32's
 // backward pass.

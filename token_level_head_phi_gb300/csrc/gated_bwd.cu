@@ -24,7 +24,7 @@ struct Stage {
 };
 static_assert(MHLA_GATED_MARK == 2 * 8, "every second warp starts at a mark");
 
-template <typename T, int KIND, bool IN, bool NORM, bool WIDE>
+template <typename T, int KIND, bool IN, bool NORM, int VEC>
 __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 4))
     gated_bwd_kernel(const __grid_constant__ GatedArgs p) {
   constexpr int kTok = kGatedTok<sizeof(T) == 4, true>, kTile = kGatedWarps * kTok;
@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   const int b = unit / p.slabs, slab = unit - b * p.slabs, first = slab * kGatedSlab, cols = p.D - first;
   Stage<T, IN>* stage = reinterpret_cast<Stage<T, IN>*>(dynamic) + 2 * w;
   const Lane ln(slab, p.D);
-  const int vec = WIDE ? 2 : p.vec != 0;
+  const int vec = VEC == kGatedNarrow ? p.vec != 0 : VEC;
   const int len = gated_length(p, b), round = kTile * ranks;
   const float2 lg = ln.get(KIND == MHLA_GATED_DECAY ? p.g : nullptr);
   const float2 g = make_float2(least(lg.x, 0.f), least(lg.y, 0.f)), g2 = mulc(g, kLog2e);
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   const float2 zero = splat(0.f);
   // the gradient that reaches a token's state from behind it
   float2 carry = ln.get(p.dstate_out ? p.dstate_out + (int64_t)b * p.D : nullptr), dg = zero;
-  const bool whole = WIDE && cols >= kGatedSlab;
+  const bool whole = VEC == 2 && cols >= kGatedSlab;
   const int rounds = (len + round - 1) / round, mine = rank * kTile + w * kTok;
 
   // The walks are formed anew where they are used: kept, they would take
@@ -228,7 +228,10 @@ struct Backward {
   cudaStream_t s;
   template <typename T, int KIND, bool IN, bool NORM>
   mhla_status run() {
-    auto kernel = a.vec == 2 ? gated_bwd_kernel<T, KIND, IN, NORM, true> : gated_bwd_kernel<T, KIND, IN, NORM, false>;
+    constexpr bool kApart = sizeof(T) == 4;  // see kGatedNarrow
+    auto kernel = a.vec == 2   ? gated_bwd_kernel<T, KIND, IN, NORM, 2>
+                  : a.vec == 1 ? gated_bwd_kernel<T, KIND, IN, NORM, kApart ? 1 : kGatedNarrow>
+                               : gated_bwd_kernel<T, KIND, IN, NORM, kApart ? 0 : kGatedNarrow>;
     return launch_gated_clusters(kernel, a, sizeof(T) == 4, true, 2 * kGatedWarps * sizeof(Stage<T, IN>), s);
   }
   template <typename T, int KIND, bool IN>

@@ -29,7 +29,7 @@ struct Stage {
 // barrier for all of them.  In a cluster all wait for the others' tiles anyway:
 // each shows the map of its tokens to the warps behind it (2 x 8k tokens of 1024
 // channels 40 us, handed on from warp to warp 41; backward 80 and 78).
-template <typename T, int KIND, bool IN, bool NORM, bool WIDE>
+template <typename T, int KIND, bool IN, bool NORM, int VEC>
 __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 4))
     gated_fwd_kernel(const __grid_constant__ GatedArgs p) {
   constexpr int kTok = kGatedTok<sizeof(T) == 4, false>, kTile = kGatedWarps * kTok;
@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   const int b = unit / p.slabs, slab = unit - b * p.slabs, first = slab * kGatedSlab, cols = p.D - first;
   Stage<T, IN>& my = reinterpret_cast<Stage<T, IN>*>(dynamic)[w];
   const Lane ln(slab, p.D);
-  const int vec = WIDE ? 2 : p.vec != 0;
+  const int vec = VEC == kGatedNarrow ? p.vec != 0 : VEC;
   const int len = gated_length(p, b), round = kTile * ranks;  // tokens that the cluster takes at once
   const float2 lg = ln.get(KIND == MHLA_GATED_DECAY ? p.g : nullptr);
   const float2 g = make_float2(least(lg.x, 0.f), least(lg.y, 0.f)), g2 = mulc(g, kLog2e);
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   const In r(static_cast<const T*>(p.r) + b * p.sr.batch + first, p.sr.token, vec);
   const In i(static_cast<const T*>(p.i) + b * p.si.batch + first, p.si.token, vec);
   const Walk<T, T> out(static_cast<T*>(p.out) + b * p.so.batch + first, p.so.token, vec);
-  const bool whole = WIDE && cols >= kGatedSlab;
+  const bool whole = VEC == 2 && cols >= kGatedSlab;
 
   auto fetch = [&](int slot, int t0) {
     if (t0 < len) {
@@ -194,7 +194,10 @@ struct Forward {
   cudaStream_t s;
   template <typename T, int KIND, bool IN, bool NORM>
   mhla_status run() {
-    auto kernel = a.vec == 2 ? gated_fwd_kernel<T, KIND, IN, NORM, true> : gated_fwd_kernel<T, KIND, IN, NORM, false>;
+    constexpr bool kApart = sizeof(T) == 4;  // see kGatedNarrow
+    auto kernel = a.vec == 2   ? gated_fwd_kernel<T, KIND, IN, NORM, 2>
+                  : a.vec == 1 ? gated_fwd_kernel<T, KIND, IN, NORM, kApart ? 1 : kGatedNarrow>
+                               : gated_fwd_kernel<T, KIND, IN, NORM, kApart ? 0 : kGatedNarrow>;
     return launch_gated_clusters(kernel, a, sizeof(T) == 4, false, kGatedWarps * sizeof(Stage<T, IN>), s);
   }
   template <typename T, int KIND, bool IN>
