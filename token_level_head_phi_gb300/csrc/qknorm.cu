@@ -18,6 +18,7 @@
 #include "common.cuh"
 #include "ops.h"
 #include "pack.cuh"
+#include "qknorm_heads.h"
 #include "tc_host.h"
 
 namespace mhla {
@@ -305,11 +306,8 @@ __global__ void __launch_bounds__(256, kResident) qknorm_fwd_kernel(const __grid
     for (int k = 0; k < 2; ++k) in[e][k] = slot < a.slots && col[e][k] < a.dim;
   }
   const int64_t all = (int64_t)a.batch * a.tokens, stride = (int64_t)gridDim.x * per;
-  const int total = a.heads[0] + a.heads[1];
-  const int first = blockIdx.y * a.heads_per_thread, last = min(first + a.heads_per_thread, total);
-  // q's heads, then k's, in steps that do not mix them
-  const int split = min(max(a.heads[0], first), last);
-  auto next = [&](int h) { return h < split ? min(h + R, split) : h + R; };
+  const HeadShare share(blockIdx.y, a.heads_per_thread, a.heads[0], a.heads[0] + a.heads[1]);
+  const int first = share.first, split = share.split, last = share.last;
 
   // a token's rows: those that are computed, and those that are fetched ahead
   struct Place {
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(256, kResident) qknorm_fwd_kernel(const __grid
   int put = 0, got = 0;
   auto fetch = [&] {
     if (Rows::kAsync && ahead.base < all) {
-      const int end = next(ahead.h);
+      const int end = share.step_end(ahead.h, R);  // rows behind it do not exist
       const T* any = row_of(ahead, ahead.h);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
