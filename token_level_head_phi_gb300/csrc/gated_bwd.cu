@@ -87,6 +87,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
     __syncwarp();
   }
   fetch(0, (rounds - 1) * round + mine);
+  __syncwarp();
   if (ranks > 1) cluster_wait();
   int turn = 0;
   for (int base = (rounds - 1) * round; base >= 0; base -= round, turn ^= 1) {
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
       for (int j = 0; j < kTok; ++j)
         if (t0 + j >= len) blank(at, j);
     write(at, t0);
+    __syncwarp();  // other lanes' copies arrive where this one has read and written
   }
   // alone, the first warp has the gradient of the first state
   if (p.dstate_in && rank == 0 && w == 0) ln.put(p.dstate_in + (int64_t)b * p.D, carry);

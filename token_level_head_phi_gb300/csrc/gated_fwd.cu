@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
     copies_commit();
   };
   auto write = [&](int slot, int t0) {
-    if (p.out && t0 < p.N) out.write(my.x[slot], t0, whole && t0 + kTok <= p.N, p.N - t0, cols, vec);
+    if (t0 < p.N) out.write(my.x[slot], t0, whole && t0 + kTok <= p.N, p.N - t0, cols, vec);
   };
   auto mark = [&](int t0, float2 h) {
     if (p.marks && t0 % MHLA_GATED_MARK == 0 && t0 < p.N)
@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   int t0 = mine, turn = 0;
   if (ranks > 1) cluster_arrive();  // nobody sends before all have begun
   fetch(0, t0);
+  __syncwarp();
   if (ranks > 1) cluster_wait();
   for (int base = 0; base < len; base += round, t0 += round, turn ^= 1) {  // the same turns in all of the cluster
     fetch(turn ^ 1, t0 + round);
@@ -134,17 +135,20 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
       h = through(before, h);
     }
     mark(t0, h);
-    if (t0 < len)
+    if (p.out) {
+      if (t0 < len)
 #pragma unroll
-      for (int j = 0; j < kTok; ++j) {
-        h = fma2(a[j], h, add[j]);
-        my.x[turn].v[j][l] = narrow(h, T());
-      }
-    if (t0 + kTok > len)
+        for (int j = 0; j < kTok; ++j) {
+          h = fma2(a[j], h, add[j]);
+          my.x[turn].v[j][l] = narrow(h, T());
+        }
+      if (t0 + kTok > len)
 #pragma unroll
-      for (int j = 0; j < kTok; ++j)
-        if (t0 + j >= len) my.x[turn].v[j][l].zero();
-    write(turn, t0);
+        for (int j = 0; j < kTok; ++j)
+          if (t0 + j >= len) my.x[turn].v[j][l].zero();
+      write(turn, t0);
+    }
+    __syncwarp();  // other lanes' copies arrive where this one has read
   }
   // alone, the last warp has the final state, and marks past the length need it
   if (ranks == 1 && len > 0 && p.marks) {
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   for (int j = 0; j < kTok; ++j) my.x[0].v[j][l].zero();
   for (; t0 < p.N; t0 += round) {  // padding
     mark(t0, carry);
-    write(0, t0);
+    if (p.out) write(0, t0);
   }
 }
 
