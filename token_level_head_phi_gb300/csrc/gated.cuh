@@ -64,6 +64,7 @@ mhla_status launch_gated_step(const GatedArgs& a, int dtype, int kind, cudaStrea
 
 // What the gates of two channels make, as pairs of float32.
 struct Gates {
+  float2 a;
   float2 m;     // a - 1
   float2 s;     // sigma(r)
   float2 less;  // 1 - sigma(r)
@@ -74,14 +75,17 @@ struct Gates {
 // as at least -43 (least_gate), so the powers' product does not overflow, and
 // sigma as at least 2e-19.
 //
-// a is formed as 1 + expm1(log a): its rounding (2^-25 next to 1) is multiplied
-// with itself over all the tokens that a slow channel remembers, so a float32
-// exponential's last bit, which errs to one side, would show (the final state
-// of 32k tokens 4.5e-6 off instead of 3e-7).  expm1 is its Taylor series above
-// -1/8 (the first term left out is x^6 / 720, 4e-8 of the sum) and 2^(x log2
-// e) - 1 below.  `g`: log_decay, at most 0; `g2`: g log2 e.
+// Next to 1, a is formed as 1 + expm1(log a): its rounding (2^-25 there) is
+// multiplied with itself over all the tokens that a slow channel remembers, so a
+// float32 exponential's last bit, which errs to one side, would show (the final
+// state of 32k tokens 4.5e-6 off instead of 3e-7).  Above log a = -1/8, expm1 is y
+// times a cubic in y = log2 a, fitted for the least largest relative error (2e-8)
+// with ln 2 as its first coefficient.  Below, a is the power itself, so that a small
+// one has all of its digits, and m = a - 1; sigmoids likewise, where 1 - sigma is
+// formed by itself: 1 - (1 - sigma) down to 7/8, sigma below.  `g2`: log_decay log2
+// e, at most 0.
 template <int KIND, bool IN>
-__device__ __forceinline__ Gates gates_of(float2 r, float2 i, float2 g, float2 g2) {
+__device__ __forceinline__ Gates gates_of(float2 r, float2 i, float2 g2) {
   Gates o;
   const float2 f = mulc(r, kLog2e);
   const float2 e = make_float2(ex2(-f.x), ex2(-f.y)), e1 = addc(e, 1.f);
@@ -97,21 +101,30 @@ __device__ __forceinline__ Gates gates_of(float2 r, float2 i, float2 g, float2 g
   }
   o.less = mul2(e, o.s);
   if constexpr (KIND == MHLA_GATED_DECAY) {
-    const float2 x = mul2(g, o.s);
-    float2 t = fma2(x, splat(1.f / 120.f), splat(1.f / 24.f));
-    t = fmac(x, t, 1.f / 6.f);
-    t = fmac(x, t, 0.5f);
-    t = fmac(x, t, 1.f);
-    const float2 near = mul2(x, t), y = mul2(o.s, g2);
-    o.m = make_float2(x.x > -0.125f ? near.x : ex2(y.x) - 1.f, x.y > -0.125f ? near.y : ex2(y.y) - 1.f);
+    const float2 y = mul2(o.s, g2);  // log2 a
+    float2 t = fma2(y, splat(9.17151198e-3f), splat(5.54584153e-2f));
+    t = fmac(y, t, 0.240225211f);
+    t = fmac(y, t, 0.693147182f);
+    const float2 near = mul2(y, t), slow = addc(near, 1.f);
+    const float2 power = make_float2(ex2(y.x), ex2(y.y)), gap = addc(power, -1.f);
+    const bool one = y.x > -0.1803369f, two = y.y > -0.1803369f;
+    o.a = make_float2(one ? slow.x : power.x, two ? slow.y : power.y);
+    o.m = make_float2(one ? near.x : gap.x, two ? near.y : gap.y);
   } else {
+    const float2 slow = add2(splat(1.f), make_float2(-o.less.x, -o.less.y));
+    o.a = make_float2(o.less.x < 0.125f ? slow.x : o.s.x, o.less.y < 0.125f ? slow.y : o.s.y);
     o.m = make_float2(-o.less.x, -o.less.y);
   }
   return o;
 }
 
-// 1 - a^2 with its sign turned.
-__device__ __forceinline__ float2 minus_v(float2 m) { return mul2(m, addc(m, 2.f)); }
+// c of two channels: sqrt(1 - a^2), or k0 + k1 m: 1 or 1 - a.
+template <bool NORM>
+__device__ __forceinline__ float2 factor(float2 m, float2 k1, float2 k0) {
+  if constexpr (!NORM) return fma2(m, k1, k0);
+  const float2 v = mul2(m, addc(m, 2.f));
+  return make_float2(root(-v.x), root(-v.y));
+}
 
 __device__ __forceinline__ int gated_length(const GatedArgs& p, int b) {
   if (!p.lengths) return p.N;

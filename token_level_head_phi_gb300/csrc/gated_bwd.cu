@@ -24,6 +24,13 @@ struct Stage {
 };
 static_assert(MHLA_GATED_MARK == 2 * 8, "every second warp starts at a mark");
 
+// -1 / c, 0 for c = 0, which else is 1e-19 at least (the root of float32's smallest
+// normal number): -c (1 / max(c, tiny))^2.
+__device__ __forceinline__ float2 minus_inverse(float2 c) {
+  const float2 i = make_float2(rcp(fmaxf(c.x, 1e-19f)), rcp(fmaxf(c.y, 1e-19f)));
+  return mul2(mul2(i, make_float2(-i.x, -i.y)), c);
+}
+
 template <typename T, int KIND, bool IN, bool NORM, int VEC>
 __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 4))
     gated_bwd_kernel(const __grid_constant__ GatedArgs p) {
@@ -102,32 +109,21 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
 
     // From the last token: the gates, and what the tokens send to the one before
     // them.
-    Gates gt[kTok];
-    float2 inv[kTok];  // -1 / c for NORM
+    Gates gt[kTok];  // without m, from which c is formed
+    float2 c[kTok];
     Map map = same();
-    auto factor = [&](int j) {
-      if constexpr (!NORM) return fma2(gt[j].m, k1, k0);
-      return mul2(minus_v(gt[j].m), inv[j]);
-    };
     if (live) {
 #pragma unroll
-      for (int j = kTok - 1; j >= 0; --j)
-        gt[j] = gates_of<KIND, IN>(least_gate(at.r.v[j][l]), IN ? least_gate(at.i[0].v[j][l]) : zero, g, g2);
+      for (int j = kTok - 1; j >= 0; --j) {
+        gt[j] = gates_of<KIND, IN>(least_gate(at.r.v[j][l]), IN ? least_gate(at.i[0].v[j][l]) : zero, g2);
+        c[j] = factor<NORM>(gt[j].m, k1, k0);
+      }
       if (!fast)
 #pragma unroll
         for (int j = 0; j < kTok; ++j)
-          if (t0 + j >= len) gt[j].m = gt[j].s = gt[j].less = zero;  // keeps the state
+          if (t0 + j >= len) gt[j].a = splat(1.f), gt[j].s = gt[j].less = c[j] = zero;  // keeps the state
 #pragma unroll
-      for (int j = kTok - 1; j >= 0; --j) {
-        const float2 a = addc(gt[j].m, 1.f);
-        if constexpr (NORM) {
-          // v^(-1/2) as v (max(v, tiny)^(-1/2))^3, which is 0 for v = 0
-          const float2 v = minus_v(gt[j].m);
-          const float2 q = make_float2(rsq(fmaxf(-v.x, 1e-36f)), rsq(fmaxf(-v.y, 1e-36f)));
-          inv[j] = mul2(mul2(v, q), mul2(q, q));
-        }
-        map = then(map, Map{a, mul2(a, wide(at.d.v[j][l]))});
-      }
+      for (int j = kTok - 1; j >= 0; --j) map = then(map, Map{gt[j].a, mul2(gt[j].a, wide(at.d.v[j][l]))});
     }
     float2 e = carry;
     Map behind = same();
@@ -166,7 +162,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
       for (int j = 0; j < kTok; ++j) {
         before[j] = h;
         const float2 xv = wide(at.x.v[j][l]), u = IN ? mul2(xv, gt[j].q) : xv;
-        h = fma2(addc(gt[j].m, 1.f), h, mul2(factor(j), u));
+        h = fma2(gt[j].a, h, mul2(c[j], u));
       }
     if (w % 2 == 0) {
       states[w / 2][l] = h;
@@ -183,19 +179,17 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
 #pragma unroll
       for (int j = kTok - 1; j >= 0; --j) {
         const float2 xv = wide(at.x.v[j][l]), u = IN ? mul2(xv, gt[j].q) : xv;
-        const float2 a = addc(gt[j].m, 1.f), c = factor(j);
-        const float2 G = add2(e, wide(at.d.v[j][l]));
+        const float2 a = gt[j].a, G = add2(e, wide(at.d.v[j][l]));
         // a h + u dc / dlog a = a (h - u a / c), or a (h + u k1)
-        const float2 sum = NORM ? fma2(mul2(u, inv[j]), a, before[j]) : fma2(u, k1, before[j]);
-        // sigma itself where a is one: 1 + m has lost a small one's last bits
-        const float2 dlog = mul2(G, mul2(KIND == MHLA_GATED_DECAY ? a : gt[j].s, sum));
+        const float2 sum = NORM ? fma2(mul2(u, minus_inverse(c[j])), a, before[j]) : fma2(u, k1, before[j]);
+        const float2 dlog = mul2(G, mul2(a, sum));
         float2 o_r = mul2(dlog, gt[j].less);
         if constexpr (KIND == MHLA_GATED_DECAY) {
           const float2 ds = mul2(dlog, gt[j].s);
           dg = add2(dg, ds);
           o_r = mul2(mul2(ds, g), gt[j].less);
         }
-        const float2 du = mul2(G, c), o_x = IN ? mul2(du, gt[j].q) : du;
+        const float2 du = mul2(G, c[j]), o_x = IN ? mul2(du, gt[j].q) : du;
         at.x.v[j][l] = narrow(o_x, T());
         at.r.v[j][l] = narrow(o_r, T());
         if constexpr (IN) {

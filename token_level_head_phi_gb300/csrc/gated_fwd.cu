@@ -10,14 +10,6 @@
 namespace mhla {
 namespace {
 
-// c of two channels: sqrt(1 - a^2), or k0 + k1 m: 1 or 1 - a.
-template <bool NORM>
-__device__ __forceinline__ float2 factor(float2 m, float2 k1, float2 k0) {
-  if constexpr (!NORM) return fma2(m, k1, k0);
-  const float2 v = minus_v(m);
-  return make_float2(root(-v.x), root(-v.y));
-}
-
 // A warp's inputs of two rounds; the results take x's place.
 template <typename T, bool IN>
 struct Stage {
@@ -44,7 +36,7 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
   const int vec = VEC == kGatedNarrow ? p.vec != 0 : VEC;
   const int len = gated_length(p, b), round = kTile * ranks;  // tokens that the cluster takes at once
   const float2 lg = ln.get(KIND == MHLA_GATED_DECAY ? p.g : nullptr);
-  const float2 g = make_float2(least(lg.x, 0.f), least(lg.y, 0.f)), g2 = mulc(g, kLog2e);
+  const float2 g2 = mulc(make_float2(least(lg.x, 0.f), least(lg.y, 0.f)), kLog2e);
   const bool mean = p.scale == MHLA_GATED_SCALE_MEAN;
   const float2 k1 = splat(mean ? -1.f : 0.f), k0 = splat(mean ? 0.f : 1.f);  // c = k0 + k1 m
   float2 carry = ln.get(p.state_in ? p.state_in + (int64_t)b * p.D : nullptr);
@@ -87,9 +79,9 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
 #pragma unroll
       for (int j = 0; j < kTok; ++j) {
         const float2 rv = least_gate(my.r[turn].v[j][l]), iv = IN ? least_gate(my.i[turn].v[j][l]) : splat(0.f);
-        const Gates t = gates_of<KIND, IN>(rv, iv, g, g2);
+        const Gates t = gates_of<KIND, IN>(rv, iv, g2);
         const float2 xv = wide(my.x[turn].v[j][l]), u = IN ? mul2(xv, t.q) : xv;
-        a[j] = addc(t.m, 1.f);
+        a[j] = t.a;
         add[j] = mul2(factor<NORM>(t.m, k1, k0), u);
       }
       if (t0 + kTok > len)
@@ -184,11 +176,11 @@ __global__ void __launch_bounds__(128) gated_step_kernel(const __grid_constant__
   if constexpr (IN) i.load(static_cast<const T*>(p.i) + b * p.si.batch + ln.ch, vec, ln.n);
   const float2 lg = ln.get(KIND == MHLA_GATED_DECAY ? p.g : nullptr);
   float2 h = ln.get(p.state_in ? p.state_in + b * p.D : nullptr);
-  const float2 g = make_float2(least(lg.x, 0.f), least(lg.y, 0.f));
-  const Gates t = gates_of<KIND, IN>(least_gate(r), IN ? least_gate(i) : splat(0.f), g, mulc(g, kLog2e));
+  const float2 g2 = mulc(make_float2(least(lg.x, 0.f), least(lg.y, 0.f)), kLog2e);
+  const Gates t = gates_of<KIND, IN>(least_gate(r), IN ? least_gate(i) : splat(0.f), g2);
   const float2 u = IN ? mul2(wide(x), t.q) : wide(x);
   const float k = p.scale == MHLA_GATED_SCALE_MEAN ? 1.f : 0.f;
-  h = fma2(addc(t.m, 1.f), h, mul2(factor<NORM>(t.m, splat(-k), splat(1.f - k)), u));
+  h = fma2(t.a, h, mul2(factor<NORM>(t.m, splat(-k), splat(1.f - k)), u));
   narrow(h, T()).store(static_cast<T*>(p.out) + b * p.so.batch + ln.ch, vec, ln.n);
   if (p.state_out) ln.put(p.state_out + b * p.D, h);
 }
