@@ -49,6 +49,7 @@ def gated_backward64(x, gate, dout, log_decay=None, input_gate=None, state=None,
     _, states = gated64(x, gate, log_decay, input_gate, state, length, scale)
     n, (a, c, _) = len(states) - 1, gated_factors64(gate, log_decay, scale)
     s, q = sigmoid64(gate), sigmoid64(input_gate) if input_gate is not None else np.ones_like(x)
+    rest = sigmoid64(-np.asarray(input_gate, np.float64)) if input_gate is not None else np.zeros_like(x)
     res = {k: np.zeros_like(x) for k in ("dx", "dgate", "dinput_gate")}
     res["dlog_decay"] = np.zeros(x.shape[1])
     g = np.zeros(x.shape[1]) if dstate_out is None else np.asarray(dstate_out, np.float64)
@@ -66,7 +67,7 @@ def gated_backward64(x, gate, dout, log_decay=None, input_gate=None, state=None,
         else:
             res["dgate"][t] = dlog * sigmoid64(-np.asarray(gate[t], np.float64))
         res["dx"][t] = g * c[t] * q[t]
-        res["dinput_gate"][t] = g * c[t] * x[t] * q[t] * (1.0 - q[t])
+        res["dinput_gate"][t] = g * c[t] * x[t] * q[t] * rest[t]
         g = a[t] * g
     res["dstate"] = g
     return res
