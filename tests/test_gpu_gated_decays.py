@@ -33,7 +33,7 @@ def spread(shape, low, high, seed, dtype="f32"):
 def bounds(x, gate, log_decay, input_gate, state, dout, dstate_out, scale):
     a, c, log_a = ro.gated_factors64(gate, log_decay, scale)
     k = (1.25 * np.abs(gate) + 16) * STEP
-    q = 1.0 if input_gate is None else ro.sigmoid64(input_gate)
+    q, rest_i = (1.0, 1.0) if input_gate is None else (ro.sigmoid64(input_gate), ro.sigmoid64(-input_gate))
     ki = 0.0 if input_gate is None else (1.25 * np.abs(input_gate) + 16) * STEP
     ru, u = ki + STEP, np.abs(x) * q
     with np.errstate(invalid="ignore"):
@@ -46,7 +46,7 @@ def bounds(x, gate, log_decay, input_gate, state, dout, dstate_out, scale):
         keep, add = a[t] * mh[t], c[t] * u[t]
         eh[t + 1] = a[t] * eh[t] + (ra[t] + 6 * STEP) * keep + (rc[t] + (ru + 0 * u)[t] + 7 * STEP) * add
         mh[t + 1] = keep + add
-    res = {name: np.zeros_like(x) for name in ("dx", "dgate")}
+    res = {name: np.zeros_like(x) for name in ("dx", "dgate", "dinput_gate")}
     res["dlog_decay"] = np.zeros(x.shape[1])
     g, e = np.abs(dstate_out), np.zeros(x.shape[1])
     s, rest = ro.sigmoid64(gate), ro.sigmoid64(-gate)
@@ -62,6 +62,7 @@ def bounds(x, gate, log_decay, input_gate, state, dout, dstate_out, scale):
         res["dgate"][t] = slope * (dlog + (2 * k[t] + 4 * STEP) * g * both)
         gc = c[t] * (e + g * (rc[t] + 5 * STEP))
         res["dx"][t] = (q + 0 * u)[t] * (gc + (ki + 0 * u)[t] * c[t] * g)
+        res["dinput_gate"][t] = (u * rest_i)[t] * (gc + 2 * (ki + 0 * u)[t] * c[t] * g)
         res["dlog_decay"] += s[t] * (dlog + (k[t] + (12 + n / 64) * STEP) * g * both)
         e = a[t] * e + (ra[t] + 6 * STEP) * a[t] * g
         g = a[t] * g
@@ -85,7 +86,7 @@ def check(p, dtype, scale):
         near(f64(out[i]), want, eh[1:], dtype, "out")
         near(f64(state[i]), states[-1], eh[-1], "f32", "state")
         ref = ro.gated_backward64(args[0], args[1], f64(dout[i]), *args[2:], f64(ds[i]), None, scale)
-        for name in ("dx", "dgate"):
+        for name in ("dx", "dgate") + (("dinput_gate",) if args[3] is not None else ()):
             near(f64(got[name][i]), ref[name], err[name], dtype, name)
         near(f64(got["dstate"][i]), ref["dstate"], err["dstate"], "f32", "dstate")
         dlog += ref["dlog_decay"]

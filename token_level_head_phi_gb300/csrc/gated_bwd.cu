@@ -193,8 +193,9 @@ __global__ void __launch_bounds__(32 * kGatedWarps, gated_resident(sizeof(T) == 
         at.x.v[j][l] = narrow(o_x, T());
         at.r.v[j][l] = narrow(o_r, T());
         if constexpr (IN) {
-          const float2 o_xx = mul2(o_x, xv);
-          at.i[0].v[j][l] = narrow(fma2(mulc(o_xx, -1.f), gt[j].q, o_xx), T());
+          // 1 - sigma(i) as e^-i sigma(i); the power again, for it has no register
+          const float2 k = mulc(least_gate(at.i[0].v[j][l]), -kLog2e), k1 = make_float2(ex2(k.x), ex2(k.y));
+          at.i[0].v[j][l] = narrow(mul2(mul2(o_x, xv), mul2(gt[j].q, k1)), T());
         }
         e = mul2(a, G);
       }
