@@ -444,10 +444,9 @@ mhla_status mhla_decay_step(const void* q, const void* k, const void* v, const f
 /* Norm of queries and keys over each head and their rotary positions in one
  * pass: with rstd = 1 / sqrt(mean(x^2) + eps) over a row,
  *   y = R(position) (x rstd * weight),
- * R the map of mhla_rotary (its styles, tables and positions; sines of bf16
- * rows are off by up to 2^-21).  Squares and sums in float32: rows whose
- * squares leave its range (entries beyond 1e19) come out as zeros, as their
- * rstd is 0. */
+ * R the map of mhla_rotary (its styles, tables, positions and sines).  Squares
+ * and sums in float32: rows whose squares leave its range (entries beyond 1e19)
+ * come out as zeros, as their rstd is 0. */
 typedef struct mhla_qknorm_params {
   int batch, tokens;         /* >= 0                                                     */
   int heads, kv_heads;       /* >= 0, <= 32768: heads of q and of k                      */

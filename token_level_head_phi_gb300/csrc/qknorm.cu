@@ -200,33 +200,25 @@ struct Values {
 
 // What a slot's values are multiplied with by Values::turn: cosines (in `c`) and
 // sines (in `s`, the second one's with the sign turned, so that turn adds them)
-// times the values' weights; 1 and 0 where nothing is rotated.
-//
-// Rows of bf16 take the approximate sine and cosine, off by 2^-21 at most within
-// half a turn (5e-7 of a pair, whose entries are rounded to 2^-9 of themselves).
-template <typename T, int VEC, bool ACROSS>
+// times the values' weights; 1 and 0 where nothing is rotated, which are those of
+// no turn: taken without a branch (16 + 4 heads of 64, bf16, over 4 x 32k tokens
+// 115 us, with one 125).
+template <int VEC, bool ACROSS>
 __device__ __forceinline__ void turns_of(const QkArgs& a, const uint64_t* turns, int64_t pos, const int (&col)[2],
                                          float sign, Values<VEC, ACROSS>* c, Values<VEC, ACROSS>* s) {
   float fc[2 * VEC], fs[2 * VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
-    float cs = 1.f, sn = 0.f;
     const int j = ACROSS ? i : 2 * i, k = ACROSS ? i + VEC : 2 * i + 1;  // the pair's entries
     const int entry = j < VEC ? col[0] + j : col[1] + j - VEC;           // the first one's column
     const int pair = ACROSS && !a.adjacent ? entry : entry / 2;
-    if (pair < a.half && (!ACROSS || a.adjacent || col[0] < a.half)) {
-      const uint64_t phase = (uint64_t)pos * turns[pair];
-      const float half_turns = (float)(int32_t)(phase >> 32) * 4.656612873077393e-10f;  // in [-1, 1)
-      if constexpr (sizeof(T) == 2)
-        __sincosf(half_turns * 3.14159265f, &sn, &cs);
-      else
-        sincospif(half_turns, &sn, &cs);
-      cs *= a.amp;
-      sn *= a.amp * sign;
-    }
-    fc[j] = fc[k] = cs;
-    fs[j] = sn;
-    fs[k] = -sn;
+    const bool rotated = pair < a.half && (!ACROSS || a.adjacent || col[0] < a.half);
+    const uint64_t phase = rotated ? (uint64_t)pos * turns[pair] : 0;
+    float cs, sn;
+    sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &sn, &cs);  // of half turns in [-1, 1)
+    fc[j] = fc[k] = rotated ? cs * a.amp : 1.f;
+    fs[j] = sn * (a.amp * sign);
+    fs[k] = -fs[j];
   }
   c->set(fc);
   s->set(fs);
@@ -357,7 +349,7 @@ __global__ void __launch_bounds__(256, kResident) qknorm_fwd_kernel(const __grid
   for (int64_t base = (int64_t)blockIdx.x * per; base < all; base += stride) {
     V cs[E], sn[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) turns_of<T, VEC, ACROSS>(a, turns, pos, col[e], 1.f, &cs[e], &sn[e]);
+    for (int e = 0; e < E; ++e) turns_of<VEC, ACROSS>(a, turns, pos, col[e], 1.f, &cs[e], &sn[e]);
     Place then;
     locate(then, base + stride);
     pos = position_of(a, then.b, then.t);  // a token ahead
@@ -513,7 +505,7 @@ __global__ void __launch_bounds__(256, kResident) qknorm_bwd_kernel(const __grid
     const int64_t pos = position_of(a, b, (int)t);
     V cs[E], sn[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) turns_of<T, VEC, ACROSS>(a, turns, pos, col[e], -1.f, &cs[e], &sn[e]);
+    for (int e = 0; e < E; ++e) turns_of<VEC, ACROSS>(a, turns, pos, col[e], -1.f, &cs[e], &sn[e]);
     Pack<T, VEC> nx[Rows::kAsync ? 1 : E][2], nd[Rows::kAsync ? 1 : E][2];
     auto read = [&](int h) {
       if constexpr (!Rows::kAsync) {
