@@ -531,7 +531,8 @@ mhla_status mhla_gated_forward(const void* x, const void* gate, const void* inpu
  * input_gate; dlog_decay float32 [width] (DECAY only) may be NULL, its sums run
  * in a fixed order; dstate_in may be NULL or dstate_out; dstate_out NULL: zeros.
  * Where c = 0 its derivative is taken as 0.  Rows past a length are written as
- * zeros.  workspace as for mhla_layernorm_backward. */
+ * zeros.  workspace as for mhla_layernorm_backward; a DECAY call without
+ * dlog_decay needs as little as one of kind SIGMOID. */
 mhla_status mhla_gated_backward_workspace_bytes(const mhla_gated_params* p, size_t* bytes);
 mhla_status mhla_gated_backward(const void* x, const void* gate, const void* input_gate, const float* log_decay,
                                 const int32_t* lengths, const float* state_in, const float* marks, const void* dout,

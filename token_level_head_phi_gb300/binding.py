@@ -1398,7 +1398,10 @@ def _gated_backward_call(x, gate, dout, log_decay, input_gate, state, dstate_out
     shape = _gated_side(p, x, lengths, state=state, dstate_out=dstate_out, dstate=dstate)
     _flat("marks", marks, x, torch.float32, _marks_shape(p))
     p.marks = int(marks is not None)
-    return _Call("mhla_gated_backward", x, p, mhla_gated_backward_workspace_bytes(p), new_x=_fresh(x), new_r=_fresh(gate),
+    scratch = MhlaGatedParams.from_buffer_copy(p)
+    if not params:
+        scratch.kind = GATED_SIGMOID  # no sums for log_decay's gradient
+    return _Call("mhla_gated_backward", x, p, mhla_gated_backward_workspace_bytes(scratch), new_x=_fresh(x), new_r=_fresh(gate),
                  new_i=None if input_gate is None else _fresh(input_gate), shape=shape, width=p.width)
 
 

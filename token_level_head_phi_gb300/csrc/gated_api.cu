@@ -90,6 +90,12 @@ int64_t partial_rows(const mhla_gated_params* p) {
   return (int64_t)p->batch * gated_cluster(units, p->tokens, p->dtype == MHLA_DTYPE_F32, true);
 }
 
+// Bytes of the backward pass's scratch: those sums, and the marks that it forms.
+size_t scratch_bytes(const mhla_gated_params* p, bool sums) {
+  const size_t state = sizeof(float) * (size_t)p->batch * (size_t)p->width;
+  return (sums ? partial_rows(p) * sizeof(float) * (size_t)p->width : 0) + (p->marks ? 0 : state * (size_t)marks_of(p));
+}
+
 // 2, 1 or 0: rows of all of these start at multiples of 16 bytes, of a pair of
 // elements, or of one.
 int alignment_of(const RowTensor* t, int n) {
@@ -137,9 +143,7 @@ mhla_status mhla_gated_backward_workspace_bytes(const mhla_gated_params* p, size
   if (!bytes || !p) return MHLA_ERR_INVALID_ARG;
   const mhla_status st = check_params(p, p->kind == MHLA_GATED_DECAY ? &some : nullptr);
   if (st != MHLA_OK) return st;
-  const size_t state = sizeof(float) * (size_t)p->batch * (size_t)p->width;
-  const size_t sums = p->kind == MHLA_GATED_DECAY ? partial_rows(p) * sizeof(float) * (size_t)p->width : 0;
-  *bytes = sums + (p->marks ? 0 : state * (size_t)marks_of(p));
+  *bytes = scratch_bytes(p, p->kind == MHLA_GATED_DECAY);
   return MHLA_OK;
 }
 
@@ -157,8 +161,7 @@ mhla_status mhla_gated_backward(const void* x, const void* gate, const void* inp
   if (dlog_decay && p->kind != MHLA_GATED_DECAY) return MHLA_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t state = (int64_t)p->batch * p->width;
-  size_t need = 0;
-  if ((st = mhla_gated_backward_workspace_bytes(p, &need)) != MHLA_OK) return st;
+  const size_t need = scratch_bytes(p, dlog_decay != nullptr);
   const RowTensor none = floats(nullptr, 0);
   const RowTensor in[9] = {rows(x, p, p->x), rows(gate, p, p->gate),
                            input_gate ? rows(input_gate, p, p->input_gate) : none, rows(dout, p, p->dout),
@@ -180,8 +183,8 @@ mhla_status mhla_gated_backward(const void* x, const void* gate, const void* inp
   if ((st = scratch.take(workspace, workspace_bytes, need, s)) != MHLA_OK) return st;
   GatedArgs a = args_of(p, x, gate, input_gate, log_decay, lengths);
   float* at = reinterpret_cast<float*>(scratch.ptr());
-  if (p->kind == MHLA_GATED_DECAY) {
-    if (dlog_decay) a.partial = at;
+  if (dlog_decay) {
+    a.partial = at;
     at += partial_rows(p) * p->width;
   }
   a.state_in = state_in;
