@@ -491,7 +491,8 @@ mhla_status mhla_qknorm_backward(const void* dq_out, const void* dk_out, const v
  * DECAY: a = exp(log_decay sigma(gate)) with log_decay float32 [width], finite
  * and <= 0; SIGMOID: a = sigma(gate), without log_decay.  Gates below -43 are
  * taken as -43 (sigma 2e-19).
- * NORM: c = sqrt(max(1 - a^2, 0)) (inputs and states of one size), MEAN:
+ * NORM: c = sqrt(max(1 - a^2, 0)) (inputs and states of one size; 0 where 1 - a^2
+ * is below 1.2e-38), MEAN:
  * c = 1 - a (a running mean), NONE: c = 1.
  * All arithmetic in float32, a result is rounded once. */
 typedef enum mhla_gated_kind { MHLA_GATED_DECAY = 0, MHLA_GATED_SIGMOID = 1 } mhla_gated_kind;

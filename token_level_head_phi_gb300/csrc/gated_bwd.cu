@@ -8,7 +8,7 @@
 // Bound: instructions and the rounds' latency, not memory (bf16 with an input
 // gate 14 bytes an element): 64 x 512 tokens of 4096 channels take 384 us, 4.9
 // TB/s; 2 x 8k tokens of 1024 channels 78 us in 16 rounds of clusters of 8 (35 us at
-// the rate of a copy), an SM issuing 49 % of the time, 153 instructions to a pair
+// the rate of a copy), an SM issuing 49 % of the time, 155 instructions to a pair
 // of channels.
 #include "gated.cuh"
 

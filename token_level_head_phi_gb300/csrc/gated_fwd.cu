@@ -1,10 +1,10 @@
 // Gated recurrence: prompts, and one token of every sequence.
 //
 // Bound: memory where there are many sequences (bf16 with an input gate 8 bytes
-// an element): 64 x 512 tokens of 4096 channels take 171 us, 6.3 TB/s.  With few
+// an element): 64 x 512 tokens of 4096 channels take 173 us, 6.2 TB/s.  With few
 // it is the latency of the clusters' rounds: 2 x 32k tokens of 1024 channels take
-// 132 us in 32 rounds (79 us at the rate of a copy); an SM issues 45 % of the time,
-// about 70 instructions to a pair of channels, half of them for the gates.
+// 134 us in 32 rounds (79 us at the rate of a copy); an SM issues 46 % of the time,
+// 72 instructions to a pair of channels, half of them for the gates.
 #include "gated.cuh"
 
 namespace mhla {

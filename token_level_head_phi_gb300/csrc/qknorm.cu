@@ -10,8 +10,8 @@
 // Bound: memory (each row read once and written once; the backward pass reads
 // two rows and writes one), with the latency of a row's sums where heads are
 // wide: 16 + 4 heads of 64 over 4 x 32k tokens (bf16) take 116 us forward, 5.8 TB/s,
-// and 176 us backward; of 128 over 2 x 8k tokens 33 us (25 at the rate of a copy)
-// and 51 us (37), of which 3 us add the weights' gradients.
+// and 173 us backward; of 128 over 2 x 8k tokens 32 us (25 at the rate of a copy)
+// and 49 us (37), of which 3 us add the weights' gradients.
 #include <algorithm>
 #include <cmath>
 
